@@ -143,6 +143,20 @@ _SIGS = {
     "vae_decode_causal": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "vae_chain_tiled_workspace_size": (_SZ, [_P, _I, _I, _I, _I, _I, _I]),
     "vae_decode_chain_tiled": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "vae_ckpt_bytes": (_SZ, [_LL, _I]),
+    "vae_ckpt_pack": (_I, [_P, _I, _I, _LL, _I, _P, _P]),
+    "vae_ckpt_unpack": (_I, [_P, _I, _I, _LL, _I, _P, _P]),
+    "vae_groupnorm_silu_ckpt_workspace_size": (_SZ, [_I, _I, _LL, _I, _I]),
+    "vae_groupnorm_silu_ckpt": (_I, [_P, _I, _I, _LL, _I, _I, _F, _P, _P, _I, _P, _P, _P, _P, _P,
+                                     _SZ, _P]),
+    "vae_groupnorm_silu_backward_workspace_size": (_SZ, [_I, _I, _LL, _I, _I]),
+    "vae_groupnorm_silu_backward": (_I, [_P, _P, _P, _I, _I, _LL, _I, _I, _P, _P, _I, _P, _P, _P,
+                                         _P, _P, _SZ, _P]),
+    "vae_conv2d_wgrad_workspace_size": (_SZ, [_I] * 7),
+    "vae_conv2d_wgrad": (_I, [_P, _P] + [_I] * 7 + [_P, _P, _P, _SZ, _P]),
+    "vae_block_norm": (_I, [_P, _P, _I, _LL, _I, _F] + [_P] * 10),
+    "vae_block_norm_backward_workspace_size": (_SZ, [_I, _LL, _I, _I]),
+    "vae_block_norm_backward": (_I, [_P] * 5 + [_I, _LL, _I] + [_P] * 11 + [_SZ, _P]),
     "vae_measure_tf32_mma": (_I, [_I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_float), _P]),
     "vae_debug_set_wait_limit": (_I, [ctypes.c_ulonglong]),
@@ -444,6 +458,283 @@ def vae_causal_stack(x, layers, groups=32, eps=1e-6, layout=VAE_NCHW, out=None, 
         _ptr(x), n, c, t, h, w, layout, L, arr("weight"), arr("bias"), arr("gn_weight"),
         arr("gn_bias"), groups, eps, _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- training operators
+class Checkpoint:
+    """An 8-bit activation checkpoint (vae_ckpt_bytes): ``buf``, the bytes on the
+    device, holding ``rows`` pixels or tokens of ``c`` channels. ``payload``
+    [rows, cp] (float8_e4m3fn, cp = c rounded up to 32) and ``scale``
+    [rows, cp / 32] (float8_e8m0fnu) are views: a value is payload * scale of
+    its block of 32 channels."""
+
+    __slots__ = ("buf", "rows", "c")
+
+    def __init__(self, buf, rows, c):
+        import torch
+        if not (isinstance(buf, torch.Tensor) and buf.is_cuda and buf.dtype == torch.uint8
+                and buf.is_contiguous()):
+            raise TypeError("buf must be a contiguous uint8 CUDA tensor")
+        if rows <= 0 or c <= 0 or buf.numel() < self.nbytes(rows, c):
+            raise ValueError(f"buf holds no checkpoint of {rows} rows of {c} channels")
+        self.buf, self.rows, self.c = buf, rows, c
+
+    @staticmethod
+    def _parts(rows, c):
+        cp = (c + 31) // 32 * 32
+        return cp, (rows * cp + 255) // 256 * 256
+
+    @classmethod
+    def nbytes(cls, rows, c):
+        cp, at = cls._parts(rows, c)
+        return at + rows * (cp // 32)
+
+    @classmethod
+    def empty(cls, rows, c, device):
+        import torch
+        return cls(torch.empty(cls.nbytes(rows, c), dtype=torch.uint8, device=device), rows, c)
+
+    @property
+    def payload(self):
+        import torch
+        cp, _ = self._parts(self.rows, self.c)
+        return self.buf[:self.rows * cp].view(torch.float8_e4m3fn).view(self.rows, cp)
+
+    @property
+    def scale(self):
+        import torch
+        cp, at = self._parts(self.rows, self.c)
+        n = self.rows * (cp // 32)
+        return self.buf[at:at + n].view(torch.float8_e8m0fnu).view(self.rows, cp // 32)
+
+
+def _need_ckpt(k, rows, c, like, name):
+    if not isinstance(k, Checkpoint):
+        raise TypeError(f"{name} must be a Checkpoint")
+    if k.rows != rows or k.c != c:
+        raise ValueError(f"{name} holds {k.rows} rows of {k.c} channels, not {rows} of {c}")
+    if k.buf.device != like.device:
+        raise ValueError(f"{name} is on {k.buf.device}, not {like.device}")
+    return k
+
+
+def _need_shape(t, shape, like, name):
+    _need(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    return t
+
+
+def _opt_shape(t, shape, like, name):
+    return None if t is None else _need_shape(t, shape, like, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dims(x, layout):
+    """(n, c, spatial) of an activation."""
+    if layout not in (VAE_NCHW, VAE_NHWC):
+        raise VaeError("layout", -1)
+    n = x.shape[0]
+    c = x.shape[1] if layout == VAE_NCHW else x.shape[-1]
+    return n, c, x.numel() // (n * c) if n * c else 0
+
+
+def _call(name, like, stream, made, *args):
+    """Calls entry point `name` with `args` and the stream, on the device of the
+    tensor `like`. `made`: tensors that were allocated here; they stay with a
+    caller's stream that is not the current one until it has used them."""
+    import torch
+    fn = getattr(load_library(), name)
+    dev = like.device
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream != current:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        raise VaeError(name, status)
+
+
+def _ws_for(name, device, *args):
+    nbytes = getattr(load_library(), name)(*args)
+    if nbytes == 0:
+        raise VaeError(name, -2)
+    return _ws(nbytes, device)
+
+
+def vae_ckpt_pack(x, layout=VAE_NHWC, stream=None):
+    """A Checkpoint of the activation ``x`` (any number of spatial axes)."""
+    _need(x, "x")
+    n, c, spatial = _dims(x, layout)
+    k = Checkpoint.empty(n * spatial, c, x.device)
+    _call("vae_ckpt_pack", x, stream, (k.buf,), x.data_ptr(), n, c, spatial, layout,
+          k.buf.data_ptr())
+    return k
+
+
+def vae_ckpt_unpack(ckpt, shape, layout=VAE_NHWC, stream=None):
+    """The float32 activation of ``shape`` (in ``layout``) that ``ckpt`` holds."""
+    import torch
+    if not isinstance(ckpt, Checkpoint):
+        raise TypeError("ckpt must be a Checkpoint")
+    out = torch.empty(shape, dtype=torch.float32, device=ckpt.buf.device)
+    n, c, spatial = _dims(out, layout)
+    _need_ckpt(ckpt, n * spatial, c, out, "ckpt")
+    _call("vae_ckpt_unpack", out, stream, (out,), ckpt.buf.data_ptr(), n, c, spatial, layout,
+          out.data_ptr())
+    return out
+
+
+def vae_groupnorm_silu_ckpt(x, gamma, beta, groups=32, eps=1e-6, apply_silu=True,
+                            layout=VAE_NCHW, out=None, keep_x=True, keep_y=True, stream=None):
+    """vae_groupnorm_silu that keeps its backward pass's inputs: returns
+    (y, x_ckpt, y_ckpt, stats), a checkpoint None where keep_x / keep_y is
+    false, stats [n, groups, 2] (mean, 1 / sqrt(var + eps))."""
+    import torch
+    _need(x, "x")
+    n, c, spatial = _dims(x, layout)
+    _need_shape(gamma, (c,), x, "gamma"), _need_shape(beta, (c,), x, "beta")
+    dev = x.device
+    ws = _ws_for("vae_groupnorm_silu_ckpt_workspace_size", dev, n, c, spatial, layout, groups)
+    out = torch.empty_like(x) if out is None else _need_shape(out, x.shape, x, "out")
+    x_ckpt = Checkpoint.empty(n * spatial, c, dev) if keep_x else None
+    y_ckpt = Checkpoint.empty(n * spatial, c, dev) if keep_y else None
+    stats = torch.empty((n, groups, 2), dtype=torch.float32, device=dev)
+    kx, ky = x_ckpt.buf if keep_x else None, y_ckpt.buf if keep_y else None
+    _call("vae_groupnorm_silu_ckpt", x, stream, (ws, out, kx, ky, stats), x.data_ptr(), n, c,
+          spatial, layout, groups, eps, gamma.data_ptr(), beta.data_ptr(), int(apply_silu),
+          out.data_ptr(), _addr(kx), _addr(ky), stats.data_ptr(), ws.data_ptr(), ws.numel())
+    return out, x_ckpt, y_ckpt, stats
+
+
+def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply_silu=True,
+                                layout=VAE_NCHW, dres=None, out=None, stream=None):
+    """(dx, dgamma, dbeta) from dy and what vae_groupnorm_silu_ckpt kept; dres, a
+    further gradient of x (the resnet skip's), is added to dx."""
+    import torch
+    _need(dy, "dy")
+    n, c, spatial = _dims(dy, layout)
+    _need_ckpt(x_ckpt, n * spatial, c, dy, "x_ckpt")
+    _need_shape(stats, (n, groups, 2), dy, "stats")
+    _need_shape(gamma, (c,), dy, "gamma"), _need_shape(beta, (c,), dy, "beta")
+    _opt_shape(dres, dy.shape, dy, "dres")
+    ws = _ws_for("vae_groupnorm_silu_backward_workspace_size", dy.device, n, c, spatial, layout,
+                 groups)
+    out = torch.empty_like(dy) if out is None else _need_shape(out, dy.shape, dy, "out")
+    grads = torch.empty((2, c), dtype=torch.float32, device=dy.device)
+    dgamma, dbeta = grads.unbind()
+    _call("vae_groupnorm_silu_backward", dy, stream, (ws, out, grads), dy.data_ptr(),
+          x_ckpt.buf.data_ptr(), stats.data_ptr(), n, c, spatial, layout, groups,
+          gamma.data_ptr(), beta.data_ptr(), int(apply_silu), _addr(dres), out.data_ptr(),
+          dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel())
+    return out, dgamma, dbeta
+
+
+def vae_conv2d_wgrad(dy, x_ckpt, k, layout=VAE_NCHW, stream=None):
+    """(dw [cout, cin, k, k], dbias [cout]) of vae_conv2d from its output's
+    gradient and the checkpoint of its input."""
+    import torch
+    _need(dy, "dy")
+    if dy.dim() != 4:
+        raise ValueError("dy must have four axes")
+    if layout == VAE_NCHW:
+        n, cout, h, w = dy.shape
+    else:
+        n, h, w, cout = dy.shape
+    if not isinstance(x_ckpt, Checkpoint):
+        raise TypeError("x_ckpt must be a Checkpoint")
+    cin = x_ckpt.c
+    _need_ckpt(x_ckpt, n * h * w, cin, dy, "x_ckpt")
+    ws = _ws_for("vae_conv2d_wgrad_workspace_size", dy.device, n, cin, h, w, layout, cout, k)
+    dw = torch.empty((cout, cin, k, k), dtype=torch.float32, device=dy.device)
+    dbias = torch.empty(cout, dtype=torch.float32, device=dy.device)
+    _call("vae_conv2d_wgrad", dy, stream, (ws, dw, dbias), dy.data_ptr(), x_ckpt.buf.data_ptr(),
+          n, cin, h, w, layout, cout, k, dw.data_ptr(), dbias.data_ptr(), ws.data_ptr(),
+          ws.numel())
+    return dw, dbias
+
+
+def vae_block_norm(u, x, w_post, gate=None, scale=None, w_pre=None, eps=1e-6, keep=True,
+                   out_h=None, out_y=None, stream=None):
+    """The norms around a transformer block on tokens u, x [n, tokens, c]:
+    h = x + gate * scale * w_post * u / rms(u), y = w_pre * h / rms(h). Returns
+    (h, y, u_ckpt, h_ckpt, rstd); y and h_ckpt are None without w_pre, and the
+    last three None with keep=False (serving)."""
+    import torch
+    _need(u, "u")
+    if u.dim() != 3:
+        raise ValueError("u must be [n, tokens, c]")
+    n, tokens, c = u.shape
+    _need_shape(x, u.shape, u, "x"), _need_shape(w_post, (c,), u, "w_post")
+    _opt_shape(gate, (n, c), u, "gate"), _opt_shape(scale, (c,), u, "scale")
+    _opt_shape(w_pre, (c,), u, "w_pre")
+    if out_y is not None and w_pre is None:
+        raise ValueError("out_y without w_pre")
+    dev = u.device
+    h = torch.empty_like(u) if out_h is None else _need_shape(out_h, u.shape, u, "out_h")
+    y = None
+    if w_pre is not None:
+        y = torch.empty_like(u) if out_y is None else _need_shape(out_y, u.shape, u, "out_y")
+    u_ckpt = Checkpoint.empty(n * tokens, c, dev) if keep else None
+    h_ckpt = Checkpoint.empty(n * tokens, c, dev) if keep and w_pre is not None else None
+    rstd = torch.empty((2, n * tokens), dtype=torch.float32, device=dev) if keep else None
+    ku, kh = u_ckpt and u_ckpt.buf, h_ckpt and h_ckpt.buf
+    _call("vae_block_norm", u, stream, (h, y, ku, kh, rstd), u.data_ptr(), x.data_ptr(), n,
+          tokens, c, eps, w_post.data_ptr(), _addr(gate), _addr(scale), _addr(w_pre),
+          h.data_ptr(), _addr(y), _addr(ku), _addr(kh), _addr(rstd))
+    return h, y, u_ckpt, h_ckpt, rstd
+
+
+def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, scale=None,
+                            w_pre=None, stream=None):
+    """The gradients of vae_block_norm, as a dict: du, dx, dw_post, and dgate,
+    dscale, dw_pre (None for an absent input). dy is None without w_pre; dh, the
+    gradient that reaches h by the residual stream, may be None."""
+    import torch
+    like = dh if dy is None else dy
+    if like is None:
+        raise ValueError("dy and dh are both None")
+    _need(like, "dh" if dy is None else "dy")
+    if like.dim() != 3:
+        raise ValueError("gradients must be [n, tokens, c]")
+    n, tokens, c = like.shape
+    _opt_shape(dh, like.shape, like, "dh")
+    if (dy is None) != (w_pre is None) or (h_ckpt is None) != (w_pre is None):
+        raise ValueError("dy and h_ckpt go with w_pre")
+    _need_ckpt(u_ckpt, n * tokens, c, like, "u_ckpt")
+    if h_ckpt is not None:
+        _need_ckpt(h_ckpt, n * tokens, c, like, "h_ckpt")
+    _need_shape(rstd, (2, n * tokens), like, "rstd")
+    _need_shape(w_post, (c,), like, "w_post")
+    _opt_shape(gate, (n, c), like, "gate"), _opt_shape(scale, (c,), like, "scale")
+    _opt_shape(w_pre, (c,), like, "w_pre")
+    dev = like.device
+    ws = _ws_for("vae_block_norm_backward_workspace_size", dev, n, tokens, c,
+                 int(gate is not None))
+    du, dx = torch.empty_like(like), torch.empty_like(like)
+    small = torch.empty((3, c), dtype=torch.float32, device=dev)
+    dw_post, dscale, dw_pre = small.unbind()
+    dscale = None if scale is None else dscale
+    dw_pre = None if w_pre is None else dw_pre
+    dgate = None if gate is None else torch.empty_like(gate)
+    _call("vae_block_norm_backward", like, stream, (ws, du, dx, small, dgate), _addr(dy),
+          _addr(dh), u_ckpt.buf.data_ptr(), None if h_ckpt is None else h_ckpt.buf.data_ptr(),
+          rstd.data_ptr(), n, tokens, c, w_post.data_ptr(), _addr(gate), _addr(scale),
+          _addr(w_pre), du.data_ptr(), dx.data_ptr(), dw_post.data_ptr(), _addr(dgate),
+          _addr(dscale), _addr(dw_pre), ws.data_ptr(), ws.numel())
+    return dict(du=du, dx=dx, dw_post=dw_post, dgate=dgate, dscale=dscale, dw_pre=dw_pre)
 
 
 def vae_measure_tf32_mma(iters, stream=None):

@@ -1,0 +1,634 @@
+// gn_train.cu -- GroupNorm(+SiLU) that keeps 8-bit checkpoints of its input
+// and output, and the backward pass that reads the input's checkpoint.
+//
+// Forward, per (sample, group): mean, biased variance, rstd = 1/sqrt(var +
+// eps); y = act((x - mean) rstd gamma + beta); x_ckpt = Q(x), y_ckpt = Q(y)
+// (ckpt.cuh). Backward, with xh = (x~ - mean) rstd of the checkpoint's x~,
+// z = xh gamma + beta and s = 1 / (1 + e^-z):
+//   dz = dy s (1 + z (1 - s)) (dy without SiLU)
+//   dbeta = sum dz, dgamma = sum dz xh       (samples and pixels)
+//   dx = rstd (gamma dz - mean_g(gamma dz) - xh mean_g(gamma dz xh)) (+ dres)
+//
+// Both need a sum over the whole (sample, group) before the first output
+// element, so both are a reducing pass, a small merge and an elementwise pass
+// over the same slabs of pixels. The slabs are walked forwards by the first
+// pass and backwards by the second, and outputs are stored evict-first, so
+// that the second pass finds in L2 what the first one read last.
+//
+// NHWC: a thread owns four channels; the eight lanes of a 32-channel block
+// share its scale by shuffles. NCHW: a thread owns one pixel and 32 channels,
+// so every load and store of the planes is coalesced over pixels and a
+// checkpoint block is one thread's registers.
+#include "gn_stats.cuh"
+#include "gn_train.cuh"
+
+namespace vae {
+
+namespace {
+
+constexpr int kThreads = 256;      // NHWC kernels
+constexpr int kPixThreads = 128;   // NCHW kernels: one pixel per thread
+constexpr int kBlocks = 4 * 152;   // NHWC: blocks of a launch, about four per SM
+constexpr int kPixBlocks = 8 * 152;
+constexpr int kMergeThreads = 512;
+
+// Blocks (slabs of pixels) per sample.
+int slabs_nhwc(int n, int c, long long spatial) {
+  const int ppi = kThreads / (ckpt_cp(c) / 4);
+  const long long most = std::max(1, kBlocks / n);
+  return static_cast<int>(std::max(1ll, std::min(most, spatial / (4 * ppi))));
+}
+int slabs_nchw(int n, int c, long long spatial) {
+  const long long most = std::max(1, kPixBlocks / (n * (ckpt_cp(c) / 32)));
+  return static_cast<int>(std::min<long long>(most, (spatial + kPixThreads - 1) / kPixThreads));
+}
+int slabs_stats_nchw(int ng, long long seg) {
+  const long long most = std::max(1, kBlocks / ng);
+  return static_cast<int>(std::max(1ll, std::min(most, seg / (kStatThreads * 8))));
+}
+
+// ------------------------------------------------------------- statistics
+__global__ void __launch_bounds__(kStatThreads)
+    ckpt_stats_nhwc(const float *__restrict__ x, int c, long long spatial, int groups,
+                    float *__restrict__ part) {
+  extern __shared__ float sm[];
+  stats_slab_nhwc(x, c, spatial, groups, gridDim.x, blockIdx.y, blockIdx.x, sm, part);
+}
+
+__global__ void __launch_bounds__(kStatThreads)
+    ckpt_stats_nchw(const float *__restrict__ x, int c, long long spatial, int groups,
+                    float *__restrict__ part) {
+  __shared__ float red[kStatThreads][3];
+  stats_segment_nchw(x, c, spatial, groups, gridDim.y, blockIdx.x, blockIdx.y, red, part);
+}
+
+// One block per (sample, group): merges its partials in a fixed order.
+__global__ void __launch_bounds__(kMergeThreads)
+    ckpt_stats_merge(const float *__restrict__ part, int slabs, float eps,
+                     float2 *__restrict__ stats) {
+  __shared__ Triple red[kMergeThreads];
+  const float *e = part + static_cast<size_t>(blockIdx.x) * slabs * 3;
+  Triple acc{0.f, 0.f, 0.f};
+  for (int b = threadIdx.x; b < slabs; b += blockDim.x)
+    acc = merge(acc, Triple{e[3 * b], e[3 * b + 1], e[3 * b + 2]});
+  red[threadIdx.x] = acc;
+  __syncthreads();
+  for (int w = blockDim.x / 2; w > 0; w >>= 1) {
+    if (threadIdx.x < w) red[threadIdx.x] = merge(red[threadIdx.x], red[threadIdx.x + w]);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const double var = red[0].n > 0.f ? static_cast<double>(red[0].m2) / red[0].n : 0.0;
+    stats[blockIdx.x] = make_float2(red[0].mean, static_cast<float>(1.0 / sqrt(var + eps)));
+  }
+}
+
+// ------------------------------------------------------------- forward apply
+// grid (slabs, n).
+__global__ void __launch_bounds__(kThreads)
+    ckpt_apply_nhwc(const float *x, int c, long long spatial, int groups,
+                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                    const float *__restrict__ beta, int silu, float *y, CkptView kx,
+                    CkptView ky) {
+  const int cp = (c + 31) & ~31, quads = cp >> 2, ppi = kThreads / quads;
+  const int q = threadIdx.x % quads, pl = threadIdx.x / quads;
+  if (pl >= ppi) return;
+  const int n = blockIdx.y, ch = 4 * q, cg = c / groups;
+  const bool real = ch < c;  // (c is a multiple of four)
+  float mean[4], rstd[4], ga[4], be[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 st = real ? stats[n * groups + (ch + j) / cg] : make_float2(0.f, 0.f);
+    mean[j] = st.x;
+    rstd[j] = st.y;
+    ga[j] = real ? gamma[ch + j] : 0.f;
+    be[j] = real ? beta[ch + j] : 0.f;
+  }
+  const uint32_t mask = octet_mask();
+  const long long p0 = spatial * blockIdx.x / gridDim.x,
+                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
+  const long long row0 = static_cast<long long>(n) * spatial;
+  auto load = [&](long long p) {
+    return real ? __ldcs(reinterpret_cast<const float4 *>(x + (row0 + p) * c + ch))
+                : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  auto one = [&](long long p, float4 v) {
+    const long long row = row0 + p;
+    float4 o;
+    o.x = act(fmaf((v.x - mean[0]) * rstd[0], ga[0], be[0]), silu);
+    o.y = act(fmaf((v.y - mean[1]) * rstd[1], ga[1], be[1]), silu);
+    o.z = act(fmaf((v.z - mean[2]) * rstd[2], ga[2], be[2]), silu);
+    o.w = act(fmaf((v.w - mean[3]) * rstd[3], ga[3], be[3]), silu);
+    if (real) __stcs(reinterpret_cast<float4 *>(y + row * c + ch), o);
+    uint32_t byte;
+    if (kx.q) {
+      const uint32_t b = octet_quantise(v, mask, &byte);
+      __stcs(reinterpret_cast<uint32_t *>(kx.q + row * cp + ch), b);
+      if ((q & 7) == 0) kx.scale[row * (cp >> 5) + (q >> 3)] = static_cast<uint8_t>(byte);
+    }
+    if (ky.q) {
+      const uint32_t b = octet_quantise(o, mask, &byte);
+      __stcs(reinterpret_cast<uint32_t *>(ky.q + row * cp + ch), b);
+      if ((q & 7) == 0) ky.scale[row * (cp >> 5) + (q >> 3)] = static_cast<uint8_t>(byte);
+    }
+  };
+  // from the slab's end to its start, four loads in flight
+  long long p = p1 - 1 - pl;
+  for (; p - 3 * ppi >= p0; p -= 4 * ppi) {
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = load(p - u * ppi);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) one(p - u * ppi, v[u]);
+  }
+  for (; p >= p0; p -= ppi) one(p, load(p));
+}
+
+// Stores 32 channels of one row: payload and scale byte.
+__device__ __forceinline__ void keep_row32(const float *v, CkptView k, long long row, int cp,
+                                           int cb) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) m = max(m, abs_bits(v[j]));
+  const uint32_t byte = ckpt_scale_byte(m);
+  const float inv = ckpt_inv_scale(byte);
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w[j] = pack_e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv,
+                       v[4 * j + 3] * inv);
+  uint4 *dst = reinterpret_cast<uint4 *>(k.q + row * cp + 32 * cb);
+  __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  k.scale[row * (cp >> 5) + cb] = static_cast<uint8_t>(byte);
+}
+__device__ __forceinline__ void read_row32(float *v, CkptView k, long long row, int cp, int cb) {
+  const uint4 *src = reinterpret_cast<const uint4 *>(k.q + row * cp + 32 * cb);
+  const uint4 a = __ldg(src), b = __ldg(src + 1);
+  const float sc = ckpt_scale(__ldg(k.scale + row * (cp >> 5) + cb));
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 f = unpack_e4m3x4(w[j], sc);
+    v[4 * j] = f.x;
+    v[4 * j + 1] = f.y;
+    v[4 * j + 2] = f.z;
+    v[4 * j + 3] = f.w;
+  }
+}
+
+// Per-channel constants of a 32-channel block, in shared memory: (mean, rstd,
+// gamma, beta), zeros past c.
+__device__ __forceinline__ void load_affine32(float4 *aff, int n, int c, int cb, int groups,
+                                              const float2 *stats, const float *gamma,
+                                              const float *beta) {
+  if (threadIdx.x < 32) {
+    const int ch = 32 * cb + threadIdx.x;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ch < c) {
+      const float2 st = stats[n * groups + ch / (c / groups)];
+      a = make_float4(st.x, st.y, gamma[ch], beta[ch]);
+    }
+    aff[threadIdx.x] = a;
+  }
+  __syncthreads();
+}
+
+// grid (slabs, cp / 32, n): a thread per pixel and 32 channels.
+__global__ void __launch_bounds__(kPixThreads)
+    ckpt_apply_nchw(const float *x, int c, long long spatial, int groups,
+                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                    const float *__restrict__ beta, int silu, float *y, CkptView kx,
+                    CkptView ky) {
+  __shared__ float4 aff[32];
+  const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31;
+  load_affine32(aff, n, c, cb, groups, stats, gamma, beta);
+  const int chans = min(32, c - 32 * cb);
+  const long long p0 = spatial * blockIdx.x / gridDim.x,
+                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
+  const float *xs = x + (static_cast<long long>(n) * c + 32 * cb) * spatial;
+  float *ys = y + (static_cast<long long>(n) * c + 32 * cb) * spatial;
+  for (long long p = p1 - 1 - threadIdx.x; p >= p0; p -= kPixThreads) {
+    const long long row = static_cast<long long>(n) * spatial + p;
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = j < chans ? __ldcs(xs + j * spatial + p) : 0.f;
+    if (kx.q) keep_row32(v, kx, row, cp, cb);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float4 a = aff[j];
+      v[j] = act(fmaf((v[j] - a.x) * a.y, a.z, a.w), silu);
+      if (j < chans) __stcs(ys + j * spatial + p, v[j]);
+    }
+    if (ky.q) keep_row32(v, ky, row, cp, cb);
+  }
+}
+
+// ------------------------------------------------------------- backward
+// dz and xh of one element.
+__device__ __forceinline__ float grad_z(float dy, float xv, float mean, float rstd, float ga,
+                                        float be, int silu, float *xh) {
+  *xh = (xv - mean) * rstd;
+  if (!silu) return dy;
+  const float z = fmaf(*xh, ga, be);
+  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+  return dy * (s * fmaf(z, 1.0f - s, 1.0f));
+}
+
+// Per-(slab, channel) sums of dz and dz xh: part [n][slabs][c] float2. grid (slabs, n).
+__global__ void __launch_bounds__(kThreads)
+    ckpt_sums_nhwc(const float *__restrict__ dy, CkptView k, int c, long long spatial, int groups,
+                   const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                   const float *__restrict__ beta, int silu, float2 *__restrict__ part) {
+  __shared__ float2 red[kThreads * 4];
+  const int cp = (c + 31) & ~31, quads = c >> 2, ppi = kThreads / quads;
+  const int q = threadIdx.x % quads, pl = threadIdx.x / quads;
+  const int n = blockIdx.y, ch = 4 * q, cg = c / groups;
+  float a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  if (pl < ppi) {
+    float mean[4], rstd[4], ga[4], be[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 st = stats[n * groups + (ch + j) / cg];
+      mean[j] = st.x;
+      rstd[j] = st.y;
+      ga[j] = gamma[ch + j];
+      be[j] = beta[ch + j];
+    }
+    const long long p0 = spatial * blockIdx.x / gridDim.x,
+                    p1 = spatial * (blockIdx.x + 1) / gridDim.x;
+    const long long row0 = static_cast<long long>(n) * spatial;
+    auto add = [&](float4 g, uint32_t w, uint32_t byte) {
+      const float4 v = unpack_e4m3x4(w, ckpt_scale(byte));
+      const float gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float xh;
+        const float dz = grad_z(gv[j], xv[j], mean[j], rstd[j], ga[j], be[j], silu, &xh);
+        a[j] += dz;
+        b[j] = fmaf(dz, xh, b[j]);
+      }
+    };
+    auto ld_g = [&](long long p) {
+      return __ldg(reinterpret_cast<const float4 *>(dy + (row0 + p) * c + ch));
+    };
+    auto ld_q = [&](long long p) {
+      return __ldg(reinterpret_cast<const uint32_t *>(k.q + (row0 + p) * cp + ch));
+    };
+    auto ld_s = [&](long long p) {
+      return static_cast<uint32_t>(__ldg(k.scale + (row0 + p) * (cp >> 5) + (q >> 3)));
+    };
+    long long p = p0 + pl;
+    for (; p + 3 * ppi < p1; p += 4 * ppi) {
+      float4 g[4];
+      uint32_t w[4], sb[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        g[u] = ld_g(p + u * ppi);
+        w[u] = ld_q(p + u * ppi);
+        sb[u] = ld_s(p + u * ppi);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add(g[u], w[u], sb[u]);
+    }
+    for (; p < p1; p += ppi) add(ld_g(p), ld_q(p), ld_s(p));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[pl * c + ch + j] = make_float2(a[j], b[j]);
+  }
+  __syncthreads();
+  float2 *o = part + (static_cast<size_t>(n) * gridDim.x + blockIdx.x) * c;
+  for (int i = threadIdx.x; i < c; i += kThreads) {
+    float2 t = red[i];
+    for (int l = 1; l < ppi; ++l) {
+      t.x += red[l * c + i].x;
+      t.y += red[l * c + i].y;
+    }
+    o[i] = t;
+  }
+}
+
+// grid (slabs, cp / 32, n).
+__global__ void __launch_bounds__(kPixThreads)
+    ckpt_sums_nchw(const float *__restrict__ dy, CkptView k, int c, long long spatial, int groups,
+                   const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                   const float *__restrict__ beta, int silu, float2 *__restrict__ part) {
+  __shared__ float4 aff[32];
+  __shared__ float2 red[kPixThreads / 32][32];
+  const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31;
+  load_affine32(aff, n, c, cb, groups, stats, gamma, beta);
+  const int chans = min(32, c - 32 * cb);
+  const long long p0 = spatial * blockIdx.x / gridDim.x,
+                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
+  const float *gs = dy + (static_cast<long long>(n) * c + 32 * cb) * spatial;
+  float a[32], b[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) a[j] = b[j] = 0.f;
+  for (long long p = p0 + threadIdx.x; p < p1; p += kPixThreads) {
+    float v[32];
+    read_row32(v, k, static_cast<long long>(n) * spatial + p, cp, cb);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < chans) {
+        const float4 f = aff[j];
+        float xh;
+        const float dz = grad_z(__ldg(gs + j * spatial + p), v[j], f.x, f.y, f.z, f.w, silu, &xh);
+        a[j] += dz;
+        b[j] = fmaf(dz, xh, b[j]);
+      }
+    }
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
+      b[j] += __shfl_xor_sync(0xffffffffu, b[j], o);
+    }
+    if (lane == j) red[warp][j] = make_float2(a[j], b[j]);
+  }
+  __syncthreads();
+  if (threadIdx.x < chans) {
+    float2 t = red[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kPixThreads / 32; ++w) {
+      t.x += red[w][threadIdx.x].x;
+      t.y += red[w][threadIdx.x].y;
+    }
+    part[(static_cast<size_t>(n) * gridDim.x + blockIdx.x) * c + 32 * cb + threadIdx.x] = t;
+  }
+}
+
+// Block b: channels [32 b, 32 b + 32), every sample. 32 x 32 threads: lanes
+// are channels, warps stride over the slabs; fixed order. Writes the
+// per-(sample, channel) sums and, over the samples, dbeta and dgamma.
+__global__ void __launch_bounds__(1024)
+    ckpt_sums_merge(const float2 *__restrict__ part, int n, int slabs, int c,
+                    float2 *__restrict__ sums, float *__restrict__ dgamma,
+                    float *__restrict__ dbeta) {
+  __shared__ float2 red[32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ch = 32 * blockIdx.x + lane;
+  float tb = 0.f, tg = 0.f;
+  for (int i = 0; i < n; ++i) {
+    float2 t = make_float2(0.f, 0.f);
+    if (ch < c)
+      for (int s = warp; s < slabs; s += 32) {
+        const float2 v = part[(static_cast<size_t>(i) * slabs + s) * c + ch];
+        t.x += v.x;
+        t.y += v.y;
+      }
+    red[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && ch < c) {
+      for (int w = 1; w < 32; ++w) {
+        t.x += red[w][lane].x;
+        t.y += red[w][lane].y;
+      }
+      sums[static_cast<size_t>(i) * c + ch] = t;
+      tb += t.x;
+      tg += t.y;
+    }
+    __syncthreads();
+  }
+  if (warp == 0 && ch < c) {
+    if (dbeta) dbeta[ch] = tb;
+    if (dgamma) dgamma[ch] = tg;
+  }
+}
+
+// k1[g] = rstd mean_g(gamma dz), k2[g] = rstd mean_g(gamma dz xh) of sample n
+// for groups [g0, g1), into shared memory; a warp per group.
+__device__ __forceinline__ void group_means(float2 *km, const float2 *__restrict__ sums, int n,
+                                            int c, int groups, long long spatial,
+                                            const float2 *__restrict__ stats,
+                                            const float *__restrict__ gamma, int g0, int g1) {
+  const int cg = c / groups, lane = threadIdx.x & 31;
+  for (int g = g0 + (threadIdx.x >> 5); g < g1; g += blockDim.x >> 5) {
+    float a = 0.f, b = 0.f;
+    for (int j = lane; j < cg; j += 32) {
+      const float2 t = sums[static_cast<size_t>(n) * c + g * cg + j];
+      const float ga = gamma[g * cg + j];
+      a = fmaf(ga, t.x, a);
+      b = fmaf(ga, t.y, b);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (lane == 0) {
+      const float f = stats[n * groups + g].y / (static_cast<float>(cg) * spatial);
+      km[g - g0] = make_float2(a * f, b * f);
+    }
+  }
+  __syncthreads();
+}
+
+// grid (slabs, n).
+__global__ void __launch_bounds__(kThreads)
+    ckpt_dx_nhwc(const float *dy, CkptView k, int c, long long spatial, int groups,
+                 const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                 const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
+                 const float *dres, float *dx) {
+  __shared__ float2 km[1024];
+  const int cp = (c + 31) & ~31, quads = c >> 2, ppi = kThreads / quads;
+  const int q = threadIdx.x % quads, pl = threadIdx.x / quads;
+  const int n = blockIdx.y, ch = 4 * q, cg = c / groups;
+  group_means(km, sums, n, c, groups, spatial, stats, gamma, 0, groups);
+  if (pl >= ppi) return;
+  float mean[4], rstd[4], ga[4], be[4], k1[4], k2[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int g = (ch + j) / cg;
+    const float2 st = stats[n * groups + g];
+    mean[j] = st.x;
+    rstd[j] = st.y;
+    ga[j] = gamma[ch + j];
+    be[j] = beta[ch + j];
+    k1[j] = km[g].x;
+    k2[j] = km[g].y;
+  }
+  const long long p0 = spatial * blockIdx.x / gridDim.x,
+                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
+  const long long row0 = static_cast<long long>(n) * spatial;
+  auto one = [&](long long p, float4 g, uint32_t w, uint32_t byte, float4 r) {
+    const float4 v = unpack_e4m3x4(w, ckpt_scale(byte));
+    const float gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {v.x, v.y, v.z, v.w};
+    const float rv[4] = {r.x, r.y, r.z, r.w};
+    float o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float xh;
+      const float dz = grad_z(gv[j], xv[j], mean[j], rstd[j], ga[j], be[j], silu, &xh);
+      o[j] = fmaf(rstd[j] * ga[j], dz, -fmaf(xh, k2[j], k1[j])) + rv[j];
+    }
+    __stcs(reinterpret_cast<float4 *>(dx + (row0 + p) * c + ch),
+           make_float4(o[0], o[1], o[2], o[3]));
+  };
+  auto ld_g = [&](long long p) {
+    return __ldcs(reinterpret_cast<const float4 *>(dy + (row0 + p) * c + ch));
+  };
+  auto ld_r = [&](long long p) {
+    return dres ? __ldcs(reinterpret_cast<const float4 *>(dres + (row0 + p) * c + ch))
+                : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  auto ld_q = [&](long long p) {
+    return __ldcs(reinterpret_cast<const uint32_t *>(k.q + (row0 + p) * cp + ch));
+  };
+  auto ld_s = [&](long long p) {
+    return static_cast<uint32_t>(__ldg(k.scale + (row0 + p) * (cp >> 5) + (q >> 3)));
+  };
+  long long p = p1 - 1 - pl;
+  for (; p - 3 * ppi >= p0; p -= 4 * ppi) {
+    float4 g[4], r[4];
+    uint32_t w[4], sb[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      g[u] = ld_g(p - u * ppi);
+      w[u] = ld_q(p - u * ppi);
+      sb[u] = ld_s(p - u * ppi);
+      r[u] = ld_r(p - u * ppi);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) one(p - u * ppi, g[u], w[u], sb[u], r[u]);
+  }
+  for (; p >= p0; p -= ppi) one(p, ld_g(p), ld_q(p), ld_s(p), ld_r(p));
+}
+
+// grid (slabs, cp / 32, n).
+__global__ void __launch_bounds__(kPixThreads)
+    ckpt_dx_nchw(const float *dy, CkptView k, int c, long long spatial, int groups,
+                 const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                 const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
+                 const float *dres, float *dx) {
+  __shared__ float4 aff[32];
+  __shared__ float2 km[32], kch[32];
+  const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31, cg = c / groups;
+  const int chans = min(32, c - 32 * cb);
+  load_affine32(aff, n, c, cb, groups, stats, gamma, beta);
+  const int g0 = 32 * cb / cg, g1 = (32 * cb + chans - 1) / cg + 1;
+  group_means(km, sums, n, c, groups, spatial, stats, gamma, g0, g1);
+  if (threadIdx.x < chans) kch[threadIdx.x] = km[(32 * cb + threadIdx.x) / cg - g0];
+  __syncthreads();
+  const long long p0 = spatial * blockIdx.x / gridDim.x,
+                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
+  const long long base = (static_cast<long long>(n) * c + 32 * cb) * spatial;
+  for (long long p = p1 - 1 - threadIdx.x; p >= p0; p -= kPixThreads) {
+    float v[32], g[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = j < chans ? __ldcs(dy + base + j * spatial + p) : 0.f;
+    read_row32(v, k, static_cast<long long>(n) * spatial + p, cp, cb);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < chans) {
+        const float4 f = aff[j];
+        const float2 m = kch[j];
+        float xh;
+        const float dz = grad_z(g[j], v[j], f.x, f.y, f.z, f.w, silu, &xh);
+        float o = fmaf(f.y * f.z, dz, -fmaf(xh, m.y, m.x));
+        if (dres) o += __ldcs(dres + base + j * spatial + p);
+        __stcs(dx + base + j * spatial + p, o);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- workspaces
+struct CkptWs {
+  float *part;   // statistics partials [n][groups][slabs] x 3, or float2 sums [n][slabs][c]
+  float2 *sums;  // [n][c]
+};
+
+CkptWs carve_forward(Carver &cv, int n, int c, long long spatial, int groups) {
+  CkptWs w{};
+  const long long ng = static_cast<long long>(n) * groups;
+  const size_t a = static_cast<size_t>(ng) * slabs_nhwc(n, c, spatial);
+  const size_t b = static_cast<size_t>(ng) *
+                   slabs_stats_nchw(static_cast<int>(ng), spatial * (c / groups));
+  w.part = cv.take<float>(3 * std::max(a, b));
+  return w;
+}
+CkptWs carve_backward(Carver &cv, int n, int c, long long spatial) {
+  CkptWs w{};
+  const size_t slabs = std::max(slabs_nhwc(n, c, spatial), slabs_nchw(n, c, spatial));
+  w.part = cv.take<float>(2 * static_cast<size_t>(n) * slabs * c);
+  w.sums = cv.take<float2>(static_cast<size_t>(n) * c);
+  return w;
+}
+
+}  // namespace
+
+size_t gn_ckpt_ws_bytes(int n, int c, long long spatial, int groups) {
+  Carver cv(nullptr, 0);
+  carve_forward(cv, n, c, spatial, groups);
+  return cv.used;
+}
+size_t gn_backward_ws_bytes(int n, int c, long long spatial, int groups) {
+  (void)groups;
+  Carver cv(nullptr, 0);
+  carve_backward(cv, n, c, spatial);
+  return cv.used;
+}
+
+int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int groups, float eps,
+            const float *gamma, const float *beta, int silu, float *y, CkptView kx, CkptView ky,
+            float *stats, void *ws, cudaStream_t s) {
+  Carver cv(ws, ~size_t(0));
+  const CkptWs w = carve_forward(cv, n, c, spatial, groups);
+  float2 *st = reinterpret_cast<float2 *>(stats);
+  const int ng = n * groups;
+  int slabs;
+  if (nhwc) {
+    slabs = slabs_nhwc(n, c, spatial);
+    const size_t sm = static_cast<size_t>(kStatThreads / (c / 4)) * c * 3 * sizeof(float);
+    ckpt_stats_nhwc<<<dim3(slabs, n), kStatThreads, sm, s>>>(x, c, spatial, groups, w.part);
+  } else {
+    slabs = slabs_stats_nchw(ng, spatial * (c / groups));
+    ckpt_stats_nchw<<<dim3(ng, slabs), kStatThreads, 0, s>>>(x, c, spatial, groups, w.part);
+  }
+  VAE_LAUNCH_CHECK();
+  ckpt_stats_merge<<<ng, slabs > 128 ? kMergeThreads : 128, 0, s>>>(w.part, slabs, eps, st);
+  VAE_LAUNCH_CHECK();
+  if (nhwc)
+    ckpt_apply_nhwc<<<dim3(slabs, n), kThreads, 0, s>>>(x, c, spatial, groups, st, gamma, beta,
+                                                        silu, y, kx, ky);
+  else
+    ckpt_apply_nchw<<<dim3(slabs_nchw(n, c, spatial), ckpt_cp(c) / 32, n), kPixThreads, 0, s>>>(
+        x, c, spatial, groups, st, gamma, beta, silu, y, kx, ky);
+  VAE_LAUNCH_CHECK();
+  count_launches(3);
+  return VAE_OK;
+}
+
+int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, long long spatial,
+                int nhwc, int groups, const float *gamma, const float *beta, int silu,
+                const float *dres, float *dx, float *dgamma, float *dbeta, void *ws,
+                cudaStream_t s) {
+  Carver cv(ws, ~size_t(0));
+  const CkptWs w = carve_backward(cv, n, c, spatial);
+  const float2 *st = reinterpret_cast<const float2 *>(stats);
+  float2 *part = reinterpret_cast<float2 *>(w.part);
+  const int slabs = nhwc ? slabs_nhwc(n, c, spatial) : slabs_nchw(n, c, spatial);
+  const dim3 grid = nhwc ? dim3(slabs, n) : dim3(slabs, ckpt_cp(c) / 32, n);
+  if (nhwc)
+    ckpt_sums_nhwc<<<grid, kThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
+                                             part);
+  else
+    ckpt_sums_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
+                                                part);
+  VAE_LAUNCH_CHECK();
+  ckpt_sums_merge<<<ckpt_cp(c) / 32, 1024, 0, s>>>(part, n, slabs, c, w.sums, dgamma, dbeta);
+  VAE_LAUNCH_CHECK();
+  if (nhwc)
+    ckpt_dx_nhwc<<<grid, kThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
+                                           w.sums, dres, dx);
+  else
+    ckpt_dx_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
+                                              w.sums, dres, dx);
+  VAE_LAUNCH_CHECK();
+  count_launches(3);
+  return VAE_OK;
+}
+
+}  // namespace vae

@@ -427,6 +427,116 @@ VAE_API int vae_decode_causal(void *handle, const float *z, int n, int t, int h,
                               float *out, void *ws, size_t ws_bytes, vae_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Training operators on 8-bit activation checkpoints: what a backward pass
+ * through the decoder's layers (or a transformer decoder's blocks: RMSNorm,
+ * gated and scaled residuals, vae3d.rs fn rms_norm_into and decode_tile) needs
+ * besides the entry points above. The pages train nothing; the formulas are
+ * the derivatives of the layers as this header defines them.
+ *
+ * A checkpoint keeps `rows` pixels or tokens of c float channels in 8 bits
+ * each: blocks of 32 consecutive channels of a row (the last one filled up
+ * with zeros; cp = 32 * ceil(c / 32)) share the scale 2^e, e the smallest
+ * integer >= -127 with max|v| <= 448 * 2^e, and hold e4m3 numbers
+ * q = v * 2^-e rounded to nearest even; a block holding an infinity or a NaN
+ * reads back as NaN. In memory (16-byte aligned, any layout of the tensor):
+ *   byte 0                          q [rows][cp]
+ *   byte 256 * ceil(rows * cp / 256)  e + 127 [rows][cp / 32] (255: NaN block)
+ * Rows are pixels in (sample, t, y, x) order, or tokens.
+ *   vae_ckpt_bytes   size of a checkpoint; 0 for sizes out of range
+ *   vae_ckpt_pack    x [n,c,spatial] (layout) into a checkpoint of n * spatial rows
+ *   vae_ckpt_unpack  the inverse, x = q * 2^e
+ * Limits: n <= 65535, n * spatial < 2^31, c <= 65536. */
+VAE_API size_t vae_ckpt_bytes(long long rows, int c);
+VAE_API int vae_ckpt_pack(const float *x, int n, int c, long long spatial, int layout, void *ckpt,
+                          vae_stream_t stream);
+VAE_API int vae_ckpt_unpack(const void *ckpt, int n, int c, long long spatial, int layout,
+                            float *x, vae_stream_t stream);
+
+/* vae_groupnorm_silu_ckpt -- vae_groupnorm_silu that also keeps what a
+ * backward pass needs: checkpoints of x (for vae_groupnorm_silu_backward, or a
+ * 1x1 shortcut's weight gradient) and of y (for the weight gradient of the
+ * conv that follows), either NULL when not wanted, and
+ *   stats [n][groups][2]: mean, 1 / sqrt(var + eps)
+ * y == x is allowed. Limits of vae_groupnorm_silu, and n <= 65535,
+ * n * spatial < 2^31. */
+VAE_API size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long spatial, int layout,
+                                                      int groups);
+VAE_API int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,
+                                    int groups, float eps, const float *gamma, const float *beta,
+                                    int apply_silu, float *y, void *x_ckpt, void *y_ckpt,
+                                    float *stats, void *ws, size_t ws_bytes, vae_stream_t stream);
+
+/* vae_groupnorm_silu_backward -- with x~ the checkpoint's values, xh =
+ * (x~ - mean) * rstd (stats as saved), z = xh * gamma + beta, and dz = dy *
+ * silu'(z) (dy itself when apply_silu == 0):
+ *   dbeta = sum dz, dgamma = sum dz * xh over samples and positions,
+ *   dx = rstd * (gamma dz - mean(gamma dz) - xh mean(gamma dz xh)) (+ dres)
+ * with means over each (sample, group).
+ *   dy, dx, dres [n,c,spatial] (layout); dres (a gradient that reaches x by
+ *   another way, the resnet skip) may be NULL; dgamma, dbeta [c] or NULL.
+ *   dx == dy and dx == dres are allowed.
+ * Sums have a fixed order: the same inputs give the same bits. */
+VAE_API size_t vae_groupnorm_silu_backward_workspace_size(int n, int c, long long spatial,
+                                                          int layout, int groups);
+VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, const float *stats,
+                                        int n, int c, long long spatial, int layout, int groups,
+                                        const float *gamma, const float *beta, int apply_silu,
+                                        const float *dres, float *dx, float *dgamma, float *dbeta,
+                                        void *ws, size_t ws_bytes, vae_stream_t stream);
+
+/* vae_conv2d_wgrad -- weight and bias gradient of vae_conv2d (k in {1,3}) from
+ * the output's gradient and a checkpoint of the conv's input:
+ *   dw[o,c,ky,kx] = sum_{n,i,j} dy[n,o,i,j] x~[n,c,i+ky-k/2,j+kx-k/2]
+ *   dbias[o] = sum_{n,i,j} dy[n,o,i,j]
+ * (The gradient of the input is vae_conv2d of dy with the taps flipped and
+ * cin, cout exchanged; the 1x1 shortcut's weight gradient is a call with k = 1.)
+ *   dy [n,cout,h,w] (layout); x_ckpt: n*h*w rows of cin channels;
+ *   dw [cout,cin,k,k]; dbias [cout] or NULL
+ * The products run on the tensor cores with x~ exact and dy in two parts of
+ * 11 significant bits each, scaled per output channel by a power of two, so
+ * that nothing beyond 2^-22 of a value (2^-38 of the channel's largest) is
+ * dropped; FP32 accumulation in a fixed order. A NaN or infinity in dy makes
+ * its output channel's gradients non-finite, one in a checkpoint block the
+ * gradients of that block's 32 input channels.
+ * Limits: cin, cout <= 4096; h, w <= 65535; n * h * (w + 1) < 2^30;
+ * cout % 4 == 0 for NHWC. */
+VAE_API size_t vae_conv2d_wgrad_workspace_size(int n, int cin, int h, int w, int layout, int cout,
+                                               int k);
+VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_ckpt, int n, int cin, int h, int w,
+                             int layout, int cout, int k, float *dw, float *dbias, void *ws,
+                             size_t ws_bytes, vae_stream_t stream);
+
+/* vae_block_norm -- the norms after a transformer block and before the next
+ * one, fused with the block's gate, residual scale and residual sum, on
+ * token-major rows: with rms(v) = sqrt(mean(v^2) + eps) over a row,
+ *   h = x + gate[n] * scale * w_post * u / rms(u),   y = w_pre * h / rms(h)
+ *   u, x, h, y [n][tokens][c]; w_post, scale, w_pre [c]; gate [n][c] (one for
+ *   all tokens of a sample). gate and scale may be NULL (ones); w_pre and y are
+ *   both NULL where no norm follows. h == x and y == u are allowed.
+ * For a backward pass, checkpoints u_ckpt of u and h_ckpt of h (NULL exactly
+ * when w_pre is) and rstd [2][n * tokens]: 1 / rms(u), then 1 / rms(h) (that
+ * half unused without w_pre). All three NULL otherwise (serving).
+ * vae_block_norm_backward -- from dy (NULL exactly when w_pre is) and dh, the
+ * gradient that reaches h by the residual stream (may be NULL): du, dx, and,
+ * each where not NULL, dw_post, dscale, dw_pre [c] and dgate [n][c]. Asking for
+ * the gradient of an absent input is VAE_EINVAL. dx == dh and du == dy are
+ * allowed. Sums have a fixed order: the same inputs give the same bits.
+ * Limits: c % 4 == 0, c <= 4096, n <= 65535, n * tokens < 2^31. */
+VAE_API int vae_block_norm(const float *u, const float *x, int n, long long tokens, int c,
+                           float eps, const float *w_post, const float *gate, const float *scale,
+                           const float *w_pre, float *h, float *y, void *u_ckpt, void *h_ckpt,
+                           float *rstd, vae_stream_t stream);
+VAE_API size_t vae_block_norm_backward_workspace_size(int n, long long tokens, int c,
+                                                      int has_gate);
+VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void *u_ckpt,
+                                    const void *h_ckpt, const float *rstd, int n,
+                                    long long tokens, int c, const float *w_post,
+                                    const float *gate, const float *scale, const float *w_pre,
+                                    float *du, float *dx, float *dw_post, float *dgate,
+                                    float *dscale, float *dw_pre, void *ws, size_t ws_bytes,
+                                    vae_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Step profiler of the chain: when enabled, vae_decode_chain brackets every
  * step (one conv, one GroupNorm+SiLU, the attention block, the latent
  * staging) with CUDA events on the caller's stream and stores the step's

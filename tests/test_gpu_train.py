@@ -1,0 +1,700 @@
+"""The training operators on the GPU against float64 forms (tests/_train_ref.py).
+
+Checkpoints are compared bit by bit: a power-of-two scale makes everything but
+the rounding to e4m3 exact, and the checkpoints of computed tensors (y, h) are
+the quantisation of the float32 output itself. Weight gradients of small
+integers are exact as well. Floating outputs are held to bounds counted in
+half-steps of float32, H = 2^-24, relative to the largest terms that enter:
+each test states its count."""
+import numpy as np
+import pytest
+
+from tests import _train_ref as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+H = 2.0 ** -24
+SENTINEL = -12345.0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import diffusion_vae_decoder_gb300 as p
+    p.load_library()
+    yield
+    assert p.vae_device_error() == 0
+
+
+def pkg():
+    import diffusion_vae_decoder_gb300 as p
+    return p
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda()
+
+
+def host(t):
+    return t.cpu().numpy().astype(np.float64)
+
+
+def to_layout(a, layout):
+    """[n, ..., c] -> the layout the op is called with."""
+    return a if layout == pkg().VAE_NHWC else np.moveaxis(a, -1, 1)
+
+
+def from_layout(a, layout):
+    return a if layout == pkg().VAE_NHWC else np.moveaxis(a, 1, -1)
+
+
+def parts(k):
+    """(codes, scale bytes) of a Checkpoint."""
+    return (k.payload.view(torch.uint8).cpu().numpy(), k.scale.view(torch.uint8).cpu().numpy())
+
+
+def same_codes(k, rows):
+    """The checkpoint holds exactly what float32 rows [r, c] quantise to."""
+    codes, scale = parts(k)
+    want_codes, want_scale = R.quantise(rows)
+    assert (scale == want_scale).all()
+    nan = (want_codes & 127) == 127
+    assert ((codes & 127) == 127)[nan].all()
+    assert (codes[~nan] == want_codes[~nan]).all()
+
+
+LAYOUTS = [0, 1]
+
+
+# ---------------------------------------------------------------- checkpoints
+def awkward_rows(r, c, seed):
+    g = np.random.default_rng(seed)
+    v = (g.normal(size=(r, c)) * 2.0 ** g.integers(-30, 30, size=(r, 1))).astype(np.float32)
+    v[g.random((r, c)) < 0.1] = 0
+    return v
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n,h,w,c", [(1, 1, 1, 1), (2, 3, 5, 31), (1, 7, 1, 32), (3, 2, 2, 33),
+                                     (1, 9, 15, 100), (2, 16, 8, 128), (1, 1, 2, 516)])
+def test_pack_and_unpack_exactly(layout, n, h, w, c):
+    rows = awkward_rows(n * h * w, c, 1)
+    x = dev(to_layout(rows.reshape(n, h, w, c), layout))
+    k = pkg().vae_ckpt_pack(x, layout=layout)
+    same_codes(k, rows)
+    back = pkg().vae_ckpt_unpack(k, x.shape, layout=layout)
+    want = R.dequantise(*parts(k), c).reshape(n, h, w, c)
+    assert (host(back) == to_layout(want, layout)).all()
+
+
+def test_pack_edges_of_the_format():
+    """Zeros, the scale's borders (448 and the next float), ties, the smallest
+    and largest floats, subnormals, -0, infinities and NaN."""
+    tiny, big = 2.0 ** -149, float(np.finfo(np.float32).max)
+    rows = np.zeros((14, 32), dtype=np.float32)
+    rows[1, 0] = 448
+    rows[2, 0] = np.nextafter(np.float32(448), np.float32(500))
+    rows[3] = np.float32(1.0625) * np.where(np.arange(32) % 2, 1, -1)
+    rows[3, 5] = 400
+    rows[4] = tiny * np.arange(32)
+    rows[5, :3] = [big, -big, 1]
+    rows[6, :4] = [np.inf, 1, 2, 3]
+    rows[7, :4] = [1, np.nan, -2, 0]
+    rows[8] = 2.0 ** -126 * np.linspace(-1, 1, 32)
+    rows[9, 0], rows[9, 1] = 448 * 2.0 ** -127, -1e-40
+    rows[10] = -0.0
+    rows[11] = np.linspace(-448, 448, 32)
+    rows[12, 0], rows[12, 1:] = 256, np.arange(31) * 2.0 ** -10
+    rows[13, 0] = -np.inf
+    k = pkg().vae_ckpt_pack(dev(rows[None, None]), layout=pkg().VAE_NHWC)
+    same_codes(k, rows)
+    back = pkg().vae_ckpt_unpack(k, (1, 1, 14, 32), layout=pkg().VAE_NHWC)
+    want = R.dequantise(*parts(k), 32).astype(np.float32)
+    got = back.cpu().numpy()[0, 0]
+    assert (np.isnan(got) == np.isnan(want)).all()
+    assert (got[~np.isnan(want)] == want[~np.isnan(want)]).all()
+
+
+# ---------------------------------------------------------------- GroupNorm + SiLU
+GN = [(1, 8, 8, 128, 32), (2, 5, 7, 32, 32), (1, 1, 1, 64, 32), (3, 3, 11, 96, 32),
+      (1, 37, 29, 48, 8), (2, 16, 33, 512, 32), (1, 4, 9, 1024, 1), (1, 130, 70, 36, 9)]
+
+
+def gn_data(n, h, w, c, seed):
+    g = np.random.default_rng(seed)
+    x = (g.normal(size=(n, h, w, c)) * np.exp(0.5 * g.normal(size=c)) + g.normal(size=c))
+    return (x.astype(np.float32), g.normal(1, 0.1, c).astype(np.float32),
+            g.normal(0, 0.1, c).astype(np.float32))
+
+
+def gn_out_bound(x, rstd, gamma, beta):
+    # mean and rstd: tree sums, under 24 half-steps each of max|x| rstd; the
+    # affine 4; exp, 1 + e and the quotient under 24 for |z| <= 12.
+    return 64 * H * (np.abs(gamma).max() * np.abs(x).max() * rstd.max() + np.abs(beta).max() + 1)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("n,h,w,c,groups", GN)
+def test_groupnorm_ckpt(layout, silu, n, h, w, c, groups):
+    x, gamma, beta = gn_data(n, h, w, c, 2)
+    eps = 1e-3
+    y, kx, ky, stats = pkg().vae_groupnorm_silu_ckpt(
+        dev(to_layout(x, layout)), dev(gamma), dev(beta), groups=groups, eps=eps, apply_silu=silu,
+        layout=layout)
+    x64 = x.reshape(n, h * w, c).astype(np.float64)
+    mean, rstd = R.group_stats(x64, groups, eps)
+    st = host(stats)
+    assert np.abs(st[..., 0] - mean).max() <= 24 * H * np.abs(x).max()
+    # d rstd = rstd^3 / 2 d var, and the variance is off by 48 half-steps of max x^2 at most
+    assert (np.abs(st[..., 1] - rstd) <= 4 * H * rstd + 24 * H * rstd ** 3 *
+            np.abs(x).max() ** 2).all()
+    want = R.gn_forward(x64, groups, eps, gamma, beta, silu)
+    got = from_layout(host(y), layout).reshape(n, h * w, c)
+    # the variance enters z once more, times |x|
+    bound = gn_out_bound(x, rstd, gamma, beta) * (1 + (np.abs(x).max() * rstd.max()) ** 2)
+    assert np.abs(got - want).max() <= bound
+    same_codes(kx, x.reshape(-1, c))
+    same_codes(ky, got.reshape(-1, c))
+
+
+def test_groupnorm_ckpt_keeps_what_is_asked_and_writes_in_place():
+    x, gamma, beta = gn_data(2, 6, 5, 64, 3)
+    for layout in LAYOUTS:
+        xt = dev(to_layout(x, layout))
+        y, kx, ky, st = pkg().vae_groupnorm_silu_ckpt(xt, dev(gamma), dev(beta), layout=layout)
+        z, nx, ny, st2 = pkg().vae_groupnorm_silu_ckpt(xt, dev(gamma), dev(beta), layout=layout,
+                                                       keep_x=False, keep_y=False)
+        assert nx is None and ny is None and torch.equal(y, z) and torch.equal(st, st2)
+        w, kx2, ky2, _ = pkg().vae_groupnorm_silu_ckpt(xt, dev(gamma), dev(beta), layout=layout,
+                                                       out=xt)
+        assert w.data_ptr() == xt.data_ptr() and torch.equal(w, y)
+        for a, b in ((kx, kx2), (ky, ky2)):
+            assert all((p == q).all() for p, q in zip(parts(a), parts(b)))
+
+
+def test_groupnorm_ckpt_agrees_with_vae_groupnorm_silu():
+    x, gamma, beta = gn_data(1, 40, 33, 128, 4)
+    for layout in LAYOUTS:
+        xt = dev(to_layout(x, layout))
+        y = pkg().vae_groupnorm_silu_ckpt(xt, dev(gamma), dev(beta), layout=layout)[0]
+        z = pkg().vae_groupnorm_silu(xt, dev(gamma), dev(beta), layout=layout)
+        # two evaluations, each within the forward's bound
+        _, rstd = R.group_stats(x.reshape(1, -1, 128).astype(np.float64), 32, 1e-6)
+        assert float((y - z).abs().max()) <= 2 * gn_out_bound(x, rstd, gamma, beta) * (
+            1 + (np.abs(x).max() * rstd.max()) ** 2)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("n,h,w,c,groups", GN)
+def test_groupnorm_backward(layout, silu, n, h, w, c, groups):
+    x, gamma, beta = gn_data(n, h, w, c, 5)
+    eps = 1e-3
+    g = np.random.default_rng(6)
+    dy = g.normal(size=x.shape).astype(np.float32)
+    dres = g.normal(size=x.shape).astype(np.float32)
+    kx = pkg().vae_ckpt_pack(dev(to_layout(x, layout)), layout=layout)
+    x64 = x.reshape(n, h * w, c).astype(np.float64)
+    stats = np.stack(R.group_stats(x64, groups, eps), -1).astype(np.float32)
+    xt = R.dequantise(*parts(kx), c).reshape(n, h * w, c)
+    mean, rstd = (stats[..., i].astype(np.float64) for i in range(2))
+    want = R.gn_backward(dy.reshape(n, h * w, c).astype(np.float64), xt, mean, rstd, groups,
+                         gamma, beta, silu)
+    per = np.repeat(rstd, c // groups, 1)[:, None, :]
+    xh = (xt - np.repeat(mean, c // groups, 1)[:, None, :]) * per
+    # xh 3 half-steps, the sigmoid's derivative under 64 (|z| <= 16), sums over
+    # at most 64 values a thread, then trees: 256 half-steps of the largest terms
+    top = 1.1 * np.abs(dy).max() * np.abs(gamma).max()
+    bound = 256 * H * rstd.max() * top * (2 + np.abs(xh).max()) ** 2
+    for res in (None, dres):
+        dx, dgamma, dbeta = pkg().vae_groupnorm_silu_backward(
+            dev(to_layout(dy, layout)), kx, dev(stats), dev(gamma), dev(beta), groups=groups,
+            apply_silu=silu, layout=layout, dres=None if res is None else dev(to_layout(res, layout)))
+        got = from_layout(host(dx), layout).reshape(n, h * w, c)
+        add = 0 if res is None else res.reshape(n, h * w, c)
+        assert np.abs(got - want[0] - add).max() <= bound + H * (0 if res is None else 10)
+        size = 1.1 * np.abs(dy).sum((0, 1, 2))
+        assert (np.abs(host(dgamma) - want[1]) <= 256 * H * size * (1 + np.abs(xh).max())).all()
+        assert (np.abs(host(dbeta) - want[2]) <= 256 * H * size).all()
+
+
+def test_groupnorm_backward_is_the_same_in_place_and_again():
+    x, gamma, beta = gn_data(2, 19, 23, 64, 7)
+    dy = np.random.default_rng(8).normal(size=x.shape)
+    for layout in LAYOUTS:
+        xt, d = dev(to_layout(x, layout)), dev(to_layout(dy, layout))
+        _, kx, _, st = pkg().vae_groupnorm_silu_ckpt(xt, dev(gamma), dev(beta), layout=layout)
+        args = (kx, st, dev(gamma), dev(beta))
+        a = pkg().vae_groupnorm_silu_backward(d, *args, layout=layout)
+        b = pkg().vae_groupnorm_silu_backward(d, *args, layout=layout)
+        r = d.clone()
+        c = pkg().vae_groupnorm_silu_backward(d, *args, layout=layout, dres=r, out=r)
+        e = pkg().vae_groupnorm_silu_backward(d, *args, layout=layout, out=d)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        assert all(torch.equal(p, q) for p, q in zip(a, e)) and e[0].data_ptr() == d.data_ptr()
+        # one rounding of a sum of two values
+        assert float((c[0] - a[0] - dev(to_layout(dy, layout))).abs().max()) <= 4 * H * float(
+            c[0].abs().max() + a[0].abs().max())
+
+
+# ---------------------------------------------------------------- conv weight gradient
+WG = [(1, 1, 1, 32, 32), (1, 1, 1, 1, 4), (2, 3, 5, 16, 12), (1, 8, 8, 64, 64), (1, 7, 33, 96, 20),
+      (2, 13, 129, 40, 132), (1, 64, 1, 130, 64), (1, 1, 300, 33, 8), (3, 20, 17, 160, 72),
+      (1, 40, 90, 128, 128)]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("n,h,w,cin,cout", WG)
+def test_wgrad_exact_integers(layout, k, n, h, w, cin, cout):
+    """Integers of at most four bits are exact in e4m3, and their products' sums
+    in float32: every element is compared for equality."""
+    g = np.random.default_rng(9)
+    x = g.integers(-8, 9, size=(n, h, w, cin)).astype(np.float32)
+    dy = g.integers(-4, 5, size=(n, h, w, cout)).astype(np.float32)
+    kx = pkg().vae_ckpt_pack(dev(x), layout=1)
+    dw, dbias = pkg().vae_conv2d_wgrad(dev(to_layout(dy, layout)), kx, k, layout=layout)
+    want, wb = R.wgrad(dy.astype(np.float64), x.astype(np.float64), k)
+    assert (host(dw) == want).all()
+    assert (host(dbias) == wb).all()
+
+
+def wgrad_bound(dy, xt, k):
+    # dy: two parts, off by 2^-22; a chain of 128 truncating steps in each of two
+    # accumulators, 2^-23 of the running sum at most each; then rounded sums.
+    a, _ = R.wgrad(np.abs(dy), np.abs(xt), k)
+    return (2.0 ** -22 + 2 * 128 * 2.0 ** -23 + 64 * H) * a
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("n,h,w,cin,cout", [(2, 13, 129, 40, 132), (1, 96, 100, 160, 72),
+                                            (1, 5, 6, 64, 300)])
+def test_wgrad_values(layout, k, n, h, w, cin, cout):
+    g = np.random.default_rng(10)
+    x = g.normal(size=(n, h, w, cin)) * np.exp2(g.integers(-6, 6, size=(n, h, w, 1)))
+    dy = (g.normal(size=(n, h, w, cout)) * 10.0 ** g.integers(-20, 20, size=cout)).astype(
+        np.float32)
+    kx = pkg().vae_ckpt_pack(dev(x), layout=1)
+    xt = R.dequantise(*parts(kx), cin).reshape(x.shape)
+    dw, dbias = pkg().vae_conv2d_wgrad(dev(to_layout(dy, layout)), kx, k, layout=layout)
+    want, wb = R.wgrad(dy.astype(np.float64), xt, k)
+    assert (np.abs(host(dw) - want) <= wgrad_bound(dy.astype(np.float64), xt, k)).all()
+    assert (np.abs(host(dbias) - wb) <= 256 * H * np.abs(dy).sum((0, 1, 2))).all()
+
+
+def test_wgrad_zero_tiny_huge_and_non_finite():
+    g = np.random.default_rng(11)
+    x = g.normal(size=(1, 6, 7, 64)).astype(np.float32)
+    x[0, 2, 3, :32] = 0
+    dy = g.normal(size=(1, 6, 7, 16)).astype(np.float32)
+    dy[..., 0] = 0
+    dy[..., 1] *= 2.0 ** -140   # subnormal
+    dy[..., 2] *= 2.0 ** 110
+    dy[0, 3, 3, 3] = np.inf
+    dy[0, 1, 1, 4] = np.nan
+    kx = pkg().vae_ckpt_pack(dev(x), layout=1)
+    xt = R.dequantise(*parts(kx), 64).reshape(x.shape)
+    dw, dbias = (host(t) for t in pkg().vae_conv2d_wgrad(dev(dy), kx, 3, layout=1))
+    fine = [i for i in range(16) if i not in (3, 4)]
+    want, wb = R.wgrad(dy[..., fine].astype(np.float64), xt, 3)
+    # results under the smallest normal number round to its last subnormal place
+    bound = wgrad_bound(dy[..., fine].astype(np.float64), xt, 3) + 2.0 ** -149
+    assert (np.abs(dw[fine] - want) <= bound).all()
+    assert (dw[0] == 0).all() and dbias[0] == 0
+    assert not np.isfinite(dw[3, :, 1, 1]).any() and not np.isfinite(dw[4, :, 1, 1]).any()
+    assert dbias[3] == np.inf and np.isnan(dbias[4])
+    # a block of NaNs reaches its own 32 input channels and no others
+    x[0, 2, 2, 40] = np.nan
+    kx = pkg().vae_ckpt_pack(dev(x), layout=1)
+    dw2 = host(pkg().vae_conv2d_wgrad(dev(dy[..., :3].repeat(2, -1)[..., :4]), kx, 3, layout=1)[0])
+    assert np.isnan(dw2[0, 32:, 1, 1]).all() and np.isfinite(dw2[:, :32]).all()
+
+
+def test_wgrad_of_zeros_is_zero():
+    kx = pkg().vae_ckpt_pack(torch.zeros(1, 9, 9, 32, device="cuda"), layout=1)
+    for d in (torch.zeros(1, 9, 9, 8, device="cuda"), torch.ones(1, 9, 9, 8, device="cuda")):
+        dw, _ = pkg().vae_conv2d_wgrad(d, kx, 3, layout=1)
+        assert (dw == 0).all()
+
+
+def test_wgrad_many_chains_and_pieces():
+    """Pixels for several accumulator chains a piece, against float64 torch."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(1, 512, 640, 32, generator=g, device="cuda")
+    dy = torch.randn(1, 512, 640, 32, generator=g, device="cuda")
+    kx = pkg().vae_ckpt_pack(x, layout=1)
+    xt = pkg().vae_ckpt_unpack(kx, x.shape, layout=1)
+    dw, dbias = pkg().vae_conv2d_wgrad(dy, kx, 3, layout=1)
+    again, _ = pkg().vae_conv2d_wgrad(dy, kx, 3, layout=1)
+    assert torch.equal(dw, again)
+    xp = torch.nn.functional.pad(xt.double(), (0, 0, 1, 1, 1, 1))
+    d = dy.double().reshape(-1, 32)
+    for ky in range(3):
+        for kx_ in range(3):
+            b = xp[:, ky:ky + 512, kx_:kx_ + 640].reshape(-1, 32)
+            want, size = d.t() @ b, d.abs().t() @ b.abs()
+            err = (dw[:, :, ky, kx_].double() - want).abs()
+            assert bool((err <= (2.0 ** -22 + 2 * 128 * 2.0 ** -23 + 64 * H) * size).all())
+
+
+# ---------------------------------------------------------------- block norm
+BN = [(1, 1, 4), (1, 1, 512), (2, 3, 32), (1, 17, 100), (3, 5, 128), (2, 9, 256), (1, 40, 512),
+      (2, 33, 516), (1, 7, 1024), (2, 11, 1536), (1, 19, 2048), (1, 9, 4096), (5, 1, 2052)]
+
+
+def bn_data(n, t, c, gate, scale, pre, seed):
+    g = np.random.default_rng(seed)
+    f = lambda *s, std=1.0, mean=0.0: g.normal(mean, std, s).astype(np.float32)  # noqa: E731
+    return dict(u=f(n, t, c) * np.exp(f(c, std=0.3)), x=f(n, t, c, std=2.0),
+                w_post=f(c, std=0.1, mean=1.0), gate=f(n, c) if gate else None,
+                scale=f(c, std=0.1, mean=0.3) if scale else None,
+                w_pre=f(c, std=0.1, mean=1.0) if pre else None)
+
+
+def bn_call(a, **kw):
+    t = {k: None if v is None else dev(v) for k, v in a.items()}
+    return pkg().vae_block_norm(t["u"], t["x"], t["w_post"], gate=t["gate"], scale=t["scale"],
+                                w_pre=t["w_pre"], **kw)
+
+
+OPTIONS = [(True, True, True), (False, False, False), (True, False, True), (False, True, True),
+           (True, True, False)]
+
+
+@pytest.mark.parametrize("gate,scale,pre", OPTIONS)
+@pytest.mark.parametrize("n,t,c", BN)
+def test_block_norm(n, t, c, gate, scale, pre):
+    a = bn_data(n, t, c, gate, scale, pre, 13)
+    eps = 1e-4
+    h, y, ku, kh, rstd = bn_call(a, eps=eps)
+    b = {k: None if v is None else v.astype(np.float64) for k, v in a.items()}
+    wh, wy, m, r = R.block_norm(b["u"], b["x"], eps, b["w_post"], b["gate"], b["scale"],
+                                b["w_pre"])
+    # a row's sum of squares: 16 values a lane, then a tree, under 32 half-steps;
+    # its root, the factors and the sum another 16
+    hb = 48 * H * (np.abs(wh).max() + np.abs(wh - b["x"]).max())
+    assert np.abs(host(h) - wh).max() <= hb
+    st = host(rstd).reshape(2, n, t)
+    assert (np.abs(st[0] - m) <= 32 * H * m).all()
+    same_codes(ku, a["u"].reshape(-1, c))
+    if pre:
+        top = np.abs(b["w_pre"]).max() * r.max()
+        assert np.abs(host(y) - wy).max() <= 2 * top * hb + 48 * H * np.abs(wy).max() * (
+            1 + r.max() * hb / H / 48)
+        same_codes(kh, h.cpu().numpy().reshape(-1, c))
+    else:
+        assert y is None and kh is None
+    # serving keeps nothing and gives the same
+    h2, y2, *none = bn_call(a, eps=eps, keep=False)
+    assert none == [None, None, None] and torch.equal(h, h2)
+    assert y is None or torch.equal(y, y2)
+
+
+def test_block_norm_in_place():
+    a = bn_data(2, 7, 260, True, True, True, 14)
+    h, y, ku, kh, rstd = bn_call(a)
+    t = {k: dev(v) for k, v in a.items()}
+    h2, y2, ku2, kh2, r2 = pkg().vae_block_norm(
+        t["u"], t["x"], t["w_post"], gate=t["gate"], scale=t["scale"], w_pre=t["w_pre"],
+        out_h=t["x"], out_y=t["u"])
+    assert h2.data_ptr() == t["x"].data_ptr() and y2.data_ptr() == t["u"].data_ptr()
+    assert torch.equal(h, h2) and torch.equal(y, y2) and torch.equal(rstd, r2)
+    assert all((p == q).all() for p, q in zip(parts(ku) + parts(kh), parts(ku2) + parts(kh2)))
+
+
+def test_block_norm_zero_and_nan_rows_stay_apart():
+    a = bn_data(1, 4, 64, True, True, True, 15)
+    a["u"][0, 1] = 0
+    a["u"][0, 2, 5] = np.nan
+    h, y, ku, kh, _ = bn_call(a)
+    assert (host(h)[0, 1] == a["x"][0, 1]).all()
+    assert np.isnan(host(h)[0, 2]).all() and np.isnan(host(y)[0, 2]).all()
+    assert np.isfinite(host(y)[0, [0, 1, 3]]).all()
+    same_codes(ku, a["u"].reshape(-1, 64))
+
+
+@pytest.mark.parametrize("gate,scale,pre", OPTIONS)
+@pytest.mark.parametrize("n,t,c", BN + [(2, 700, 64), (400, 2, 36)])
+def test_block_norm_backward(n, t, c, gate, scale, pre):
+    a = bn_data(n, t, c, gate, scale, pre, 16)
+    _, _, ku, kh, rstd = bn_call(a, eps=1e-4)
+    g = np.random.default_rng(17)
+    dy = g.normal(size=(n, t, c)).astype(np.float32) if pre else None
+    u = R.dequantise(*parts(ku), c).reshape(n, t, c)
+    h = R.dequantise(*parts(kh), c).reshape(n, t, c) if pre else None
+    m, r = host(rstd).reshape(2, n, t)
+    b = {k: None if v is None else v.astype(np.float64) for k, v in a.items()}
+    d = {k: None if v is None else dev(v) for k, v in a.items()}
+    for dh in (g.normal(size=(n, t, c)).astype(np.float32), None):
+        if dh is None and not pre:
+            continue
+        got = pkg().vae_block_norm_backward(
+            None if dy is None else dev(dy), None if dh is None else dev(dh), ku, kh, rstd,
+            d["w_post"], gate=d["gate"], scale=d["scale"], w_pre=d["w_pre"])
+        want = R.block_norm_backward(dy, None if dh is None else dh.astype(np.float64), u, h, m, r,
+                                     b["w_post"], b["gate"], b["scale"], b["w_pre"])
+        uh = np.abs(u * m[..., None]).max()
+        hh = np.abs(h * r[..., None]).max() if pre else 0.0
+        up = (0 if dy is None else np.abs(dy * b["w_pre"]).max() * r.max() * (1 + hh * hh))
+        up += 0 if dh is None else np.abs(dh).max()
+        # two row sums of under 40 half-steps each, a dozen products
+        xb = 64 * H * up
+        assert np.abs(host(got["dx"]) - want["dx"]).max() <= xb
+        f = np.abs(b["w_post"]).max() * (1 if not gate else np.abs(b["gate"]).max()) * (
+            1 if not scale else np.abs(b["scale"]).max())
+        assert np.abs(host(got["du"]) - want["du"]).max() <= 4 * m.max() * f * (1 + uh * uh) * xb
+        # column sums: at most 32 rows a thread, then trees, of terms off by xb
+        cb = (xb + 128 * H * np.abs(want["dx"]).max()) * uh * n * t
+        others = dict(dw_post=f / np.abs(b["w_post"]).max(), dgate=f, dscale=f)
+        if gate:
+            others["dgate"] = f / np.abs(b["gate"]).max()
+        if scale:
+            others["dscale"] = f / np.abs(b["scale"]).max()
+        for name in ("dw_post", "dgate", "dscale"):
+            if name not in want:
+                assert got[name] is None
+                continue
+            assert np.abs(host(got[name]) - want[name]).max() <= cb * others[name]
+        if pre:
+            assert np.abs(host(got["dw_pre"]) - want["dw_pre"]).max() <= (
+                160 * H * np.abs(dy).max() * hh * n * t)
+        else:
+            assert got["dw_pre"] is None
+
+
+# ---------------------------------------------------------------- streams, graphs, memory
+def all_ops():
+    """One call of each operator on fixed inputs; returns its tensors."""
+    p = pkg()
+    g = torch.Generator(device="cuda").manual_seed(18)
+    f = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dy, ga, be = f(2, 24, 20, 64), f(2, 24, 20, 64), f(64), f(64)
+    u, v, wpo, wpr, sc, gate = f(2, 50, 128), f(2, 50, 128), f(128), f(128), f(128), f(2, 128)
+    torch.cuda.synchronize()
+
+    def run(stream=None):
+        y, kx, ky, st = p.vae_groupnorm_silu_ckpt(x, ga, be, layout=1, stream=stream)
+        dx, dga, dbe = p.vae_groupnorm_silu_backward(dy, kx, st, ga, be, layout=1, dres=x,
+                                                     stream=stream)
+        dw, db = p.vae_conv2d_wgrad(dx, ky, 3, layout=1, stream=stream)
+        h, z, ku, kh, rs = p.vae_block_norm(u, v, wpo, gate=gate, scale=sc, w_pre=wpr,
+                                            stream=stream)
+        gr = p.vae_block_norm_backward(z, h, ku, kh, rs, wpo, gate=gate, scale=sc, w_pre=wpr,
+                                       stream=stream)
+        return [y, kx.buf, ky.buf, st, dx, dga, dbe, dw, db, h, z, rs, *gr.values()]
+    return run
+
+
+def same(a, b):
+    # the bytes between a checkpoint's two parts are nobody's
+    return all(torch.equal(p, q) for p, q in zip(a, b) if p.dtype != torch.uint8)
+
+
+def test_ops_on_another_stream():
+    run = all_ops()
+    want = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = run(stream=side)
+    side.synchronize()
+    assert same(want, got)
+    with torch.cuda.stream(side):
+        got = run()
+    side.synchronize()
+    assert same(want, got)
+
+
+def test_two_runs_at_once():
+    run = all_ops()
+    want = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[] for _ in streams]
+    for _ in range(4):
+        for s, g in zip(streams, got):
+            g.append(run(stream=s))
+    torch.cuda.synchronize()
+    assert all(same(want, r) for g in got for r in g)
+
+
+def test_captured_and_replayed():
+    run = all_ops()
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for t in got:
+        t.fill_(0)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert same(want, got)
+
+
+def test_nothing_is_written_behind_the_outputs():
+    """Outputs inside larger buffers, through the C ABI: what lies behind stays."""
+    p, lib = pkg(), pkg().load_library()
+    n, h, w, c, groups, guard = 1, 5, 7, 40, 8, 4096
+    rows = n * h * w
+    g = torch.Generator(device="cuda").manual_seed(19)
+    f = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dy, ga, be = f(n, h, w, c), f(n, h, w, c), f(c), f(c)
+    nb = lib.vae_ckpt_bytes(rows, c)
+
+    def floats(count):
+        return torch.full((count + guard,), SENTINEL, device="cuda")
+
+    def kept():
+        return torch.full((nb + guard,), 77, dtype=torch.uint8, device="cuda")
+
+    def workspace(size):
+        return torch.full((size + guard,), 77, dtype=torch.uint8, device="cuda")
+
+    y, kx, ky, st = floats(rows * c), kept(), kept(), floats(2 * n * groups)
+    size = lib.vae_groupnorm_silu_ckpt_workspace_size(n, c, h * w, 1, groups)
+    ws = workspace(size)
+    assert lib.vae_groupnorm_silu_ckpt(
+        x.data_ptr(), n, c, h * w, 1, groups, 1e-6, ga.data_ptr(), be.data_ptr(), 1, y.data_ptr(),
+        kx.data_ptr(), ky.data_ptr(), st.data_ptr(), ws.data_ptr(), size, None) == 0
+    size_b = lib.vae_groupnorm_silu_backward_workspace_size(n, c, h * w, 1, groups)
+    ws_b, dx, dga, dbe = workspace(size_b), floats(rows * c), floats(c), floats(c)
+    assert lib.vae_groupnorm_silu_backward(
+        dy.data_ptr(), kx.data_ptr(), st.data_ptr(), n, c, h * w, 1, groups, ga.data_ptr(),
+        be.data_ptr(), 1, None, dx.data_ptr(), dga.data_ptr(), dbe.data_ptr(), ws_b.data_ptr(),
+        size_b, None) == 0
+    size_w = lib.vae_conv2d_wgrad_workspace_size(n, c, h, w, 1, c, 3)
+    ws_w, dw, db = workspace(size_w), floats(c * c * 9), floats(c)
+    assert lib.vae_conv2d_wgrad(dy.data_ptr(), ky.data_ptr(), n, c, h, w, 1, c, 3, dw.data_ptr(),
+                                db.data_ptr(), ws_w.data_ptr(), size_w, None) == 0
+    hh, z, ku, kh, rs = floats(rows * c), floats(rows * c), kept(), kept(), floats(2 * rows)
+    assert lib.vae_block_norm(x.data_ptr(), dy.data_ptr(), n, rows, c, 1e-6, ga.data_ptr(), None,
+                              None, be.data_ptr(), hh.data_ptr(), z.data_ptr(), ku.data_ptr(),
+                              kh.data_ptr(), rs.data_ptr(), None) == 0
+    size_n = lib.vae_block_norm_backward_workspace_size(n, rows, c, 0)
+    ws_n, du, dx2, g1, g2 = (workspace(size_n), floats(rows * c), floats(rows * c), floats(c),
+                             floats(c))
+    assert lib.vae_block_norm_backward(
+        dy.data_ptr(), dy.data_ptr(), ku.data_ptr(), kh.data_ptr(), rs.data_ptr(), n, rows, c,
+        ga.data_ptr(), None, None, be.data_ptr(), du.data_ptr(), dx2.data_ptr(), g1.data_ptr(),
+        None, None, g2.data_ptr(), ws_n.data_ptr(), size_n, None) == 0
+    torch.cuda.synchronize()
+    for t in (y, st, dx, dga, dbe, dw, db, hh, z, rs, du, dx2, g1, g2):
+        assert (t[-guard:] == SENTINEL).all() and not (t[:-guard] == SENTINEL).any()
+    for t in (kx, ky, ku, kh, ws, ws_b, ws_w, ws_n):
+        assert (t[-guard:] == 77).all()
+    k = p.Checkpoint(kx, rows, c)
+    same_codes(k, x.cpu().numpy().reshape(rows, c))
+
+
+def test_refusals_of_the_binding():
+    p = pkg()
+    x = torch.randn(2, 4, 4, 64, device="cuda")
+    v = torch.ones(64, device="cuda")
+    k = p.vae_ckpt_pack(x, layout=1)
+    st = torch.zeros(2, 32, 2, device="cuda")
+    with pytest.raises(ValueError):
+        p.vae_groupnorm_silu_ckpt(x, v[:32], v, layout=1)
+    with pytest.raises(ValueError):
+        p.vae_groupnorm_silu_backward(x, p.vae_ckpt_pack(x[:1], layout=1), st, v, v, layout=1)
+    with pytest.raises(ValueError):
+        p.vae_groupnorm_silu_backward(x, k, st[:1], v, v, layout=1)
+    with pytest.raises(TypeError):
+        p.vae_groupnorm_silu_backward(x, k.buf, st, v, v, layout=1)
+    with pytest.raises(TypeError):
+        p.vae_ckpt_pack(x.half(), layout=1)
+    with pytest.raises(TypeError):
+        p.vae_ckpt_pack(x.transpose(1, 2), layout=1)
+    with pytest.raises(ValueError):
+        p.vae_conv2d_wgrad(x[:1].contiguous(), k, 3, layout=1)
+    with pytest.raises(p.VaeError):
+        p.vae_conv2d_wgrad(x, k, 5, layout=1)
+    with pytest.raises(p.VaeError):
+        p.vae_groupnorm_silu_ckpt(x, v, v, groups=24, layout=1)
+    with pytest.raises(ValueError):
+        p.Checkpoint(k.buf[:64].clone(), 32, 64)
+    t = x.view(2, 16, 64)
+    with pytest.raises(ValueError):
+        p.vae_block_norm(t, t[:, :8].contiguous(), v)
+    with pytest.raises(ValueError):
+        p.vae_block_norm(t, t, v, gate=v)
+    with pytest.raises(ValueError):
+        p.vae_block_norm_backward(t, None, k, k, torch.zeros(2, 32, device="cuda"), v)
+    with pytest.raises(ValueError):
+        p.vae_ckpt_unpack(k, (1, 4, 4, 64))
+
+
+# ---------------------------------------------------------------- a step of a resnet
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_resnet_step(layout):
+    """x + conv2(silu(norm2(conv1(silu(norm1(x)))))) through a 1x1 shortcut, forward
+    and backward, as a training step calls it; every gradient against the
+    float64 forms on the same checkpoints and saved values. The convs and the
+    data gradients are TF32 products (per-layer relative L2 1e-3)."""
+    p = pkg()
+    n, h, w, ci, co = 2, 12, 18, 64, 96
+    g = np.random.default_rng(20)
+    f = lambda *s, std=1.0, mean=0.0: g.normal(mean, std, s).astype(np.float32)  # noqa: E731
+    x = dev(to_layout(f(n, h, w, ci), layout))
+    w1, w2, ws = f(co, ci, 3, 3, std=(9 * ci) ** -0.5), f(co, co, 3, 3, std=(9 * co) ** -0.5), f(
+        co, ci, 1, 1, std=ci ** -0.5)
+    ga1, be1, ga2, be2 = f(ci, std=0.1, mean=1), f(ci, std=0.1), f(co, std=0.1, mean=1), f(
+        co, std=0.1)
+    a1, kx, ka1, st1 = p.vae_groupnorm_silu_ckpt(x, dev(ga1), dev(be1), layout=layout)
+    v = p.vae_conv2d(a1, dev(w1), layout=layout)
+    a2, kv, ka2, st2 = p.vae_groupnorm_silu_ckpt(v, dev(ga2), dev(be2), layout=layout)
+    p.vae_conv2d(a2, dev(w2), sc_x=x, sc_w=dev(ws), layout=layout)
+    dy = dev(to_layout(f(n, h, w, co), layout))
+
+    def flipped(t):
+        return dev(np.ascontiguousarray(t[:, :, ::-1, ::-1].transpose(1, 0, 2, 3)))
+
+    dw2, db2 = p.vae_conv2d_wgrad(dy, ka2, 3, layout=layout)
+    dws, _ = p.vae_conv2d_wgrad(dy, kx, 1, layout=layout)
+    da2 = p.vae_conv2d(dy, flipped(w2), layout=layout)
+    dv, dga2, dbe2 = p.vae_groupnorm_silu_backward(da2, kv, st2, dev(ga2), dev(be2),
+                                                   layout=layout)
+    dw1, db1 = p.vae_conv2d_wgrad(dv, ka1, 3, layout=layout)
+    da1 = p.vae_conv2d(dv, flipped(w1), layout=layout)
+    dskip = p.vae_conv2d(dy, flipped(ws), layout=layout)
+    dx, dga1, dbe1 = p.vae_groupnorm_silu_backward(da1, kx, st1, dev(ga1), dev(be1),
+                                                   layout=layout, dres=dskip)
+    torch.cuda.synchronize()
+
+    # the same chain in float64
+    read = lambda k, c: R.dequantise(*parts(k), c)  # noqa: E731
+    dyr = from_layout(host(dy), layout)
+
+    def dgrad(d, wt):
+        k = wt.shape[2]
+        dp = np.pad(d, ((0, 0), (k // 2,) * 2, (k // 2,) * 2, (0, 0)))
+        out = np.zeros(d.shape[:3] + (wt.shape[1],))
+        for ky in range(k):
+            for kx_ in range(k):
+                out += dp[:, ky:ky + h, kx_:kx_ + w] @ wt[:, :, k - 1 - ky, k - 1 - kx_].astype(
+                    np.float64)
+        return out
+
+    def gnb(d, k, st, ga, be, c):
+        s = host(st)
+        o = R.gn_backward(d.reshape(n, h * w, c), read(k, c).reshape(n, h * w, c), s[..., 0],
+                          s[..., 1], 32, ga, be, True)
+        return o[0].reshape(n, h, w, c), o[1], o[2]
+
+    want = {}
+    want["dw2"], want["db2"] = R.wgrad(dyr, read(ka2, co).reshape(n, h, w, co), 3)
+    want["dws"], _ = R.wgrad(dyr, read(kx, ci).reshape(n, h, w, ci), 1)
+    rv, want["dga2"], want["dbe2"] = gnb(dgrad(dyr, w2), kv, st2, ga2, be2, co)
+    want["dw1"], want["db1"] = R.wgrad(rv, read(ka1, ci).reshape(n, h, w, ci), 3)
+    rx, want["dga1"], want["dbe1"] = gnb(dgrad(rv, w1), kx, st1, ga1, be1, ci)
+    want["dx"] = rx + dgrad(dyr, ws)
+    got = dict(dw2=dw2, db2=db2, dws=dws, dga2=dga2, dbe2=dbe2, dw1=dw1, db1=db1, dga1=dga1,
+               dbe1=dbe1, dx=dx)
+    for name, t in got.items():
+        a = from_layout(host(t), layout) if name == "dx" else host(t)
+        rel = np.linalg.norm(a - want[name]) / np.linalg.norm(want[name])
+        assert rel <= (1e-6 if name in ("dw2", "db2", "dws") else 3e-3), (name, rel)
