@@ -29,9 +29,13 @@
 // and a last pass adds a unit's pieces in order and undoes the scaling: the
 // same inputs give the same bits.
 //
-// Eight warps stage (global -> registers -> halves -> shared memory) and drain
-// the accumulators, one thread issues the MMAs.
+// Sixteen warps stage: each thread copies its own 48 bytes of a stage to shared
+// memory three stages ahead (cp.async, no barrier: it reads back only what it
+// copied), converts them and stores the operands; they also drain the
+// accumulators. Three warps turn positions into pixel indexes and block scales
+// ahead of them, one thread issues the MMAs.
 #include "ptx.cuh"
+#include "silu.cuh"
 #include "wgrad.cuh"
 
 namespace vae {
@@ -40,16 +44,19 @@ namespace {
 
 constexpr int kTM = 128;           // input channels of a tile (TMEM lanes)
 constexpr int kTN = 64;            // output channels
-constexpr int kPos = 128;          // positions of a stage
-constexpr int kStages = 3;
-constexpr int kChain = 16;         // stages between two drains: 2048 positions
-constexpr int kProducers = 256;
-constexpr int kMmaThreads = kProducers + 128;  // and a warpgroup of which one thread issues
-// Registers: the launch gives every thread kLaunchRegs (65536 / 384, rounded
-// down to a multiple of 8); the issuing warpgroup hands most of its share to
-// the staging ones, which hold a third of the accumulators and a raw stage.
-constexpr int kLaunchRegs = 168, kStageRegs = 232, kIssueRegs = 40;
-static_assert(2 * kStageRegs + kIssueRegs <= 3 * kLaunchRegs, "the split fits the launch");
+constexpr int kPos = 64;           // positions of a stage
+constexpr int kStages = 3;         // staged operands
+constexpr int kRaw = 4;            // raw stages: three in flight, one being converted
+constexpr int kTables = 8;
+constexpr int kChain = 32;         // stages between two drains: 2048 positions
+constexpr int kProducers = 512;    // staging threads: 16 warps
+constexpr int kTableWarps = 3;     // each makes every third table
+constexpr int kMmaThreads = kProducers + 128;  // one more warpgroup issues and makes tables
+// Registers: the launch gives every thread kLaunchRegs (65536 / 640, rounded
+// down to a multiple of 8); the last warpgroup hands its share to the staging
+// ones, which hold the accumulators.
+constexpr int kLaunchRegs = 96, kStageRegs = 104, kIssueRegs = 64;
+static_assert(4 * kStageRegs + kIssueRegs <= 5 * kLaunchRegs, "the split fits the launch");
 // Positions between two octets, odd so that 16-byte pieces of neighbouring
 // octets fall into different banks.
 constexpr int kSlotsA = kPos + 3, kSlotsB = kPos + 1;
@@ -57,8 +64,19 @@ constexpr uint32_t kSboA = kSlotsA * 16, kSboB = kSlotsB * 16;
 constexpr uint32_t kBytesA = kTM / 8 * kSboA;      // 16 octets
 constexpr uint32_t kBytesB = 2 * kTN / 8 * kSboB;  // hi, then lo
 constexpr uint32_t kStageBytes = (kBytesA + kBytesB + 127) / 128 * 128;
-constexpr size_t kSmem = kStages * kStageBytes + 256;
+// A raw stage: 32 bytes of dy and 16 of x~ per staging thread, and the two
+// further positions of x~ that the taps of a 3x3 conv reach (16 threads).
+constexpr uint32_t kRawX = kProducers * 32, kRawMore = kRawX + kProducers * 16;
+constexpr uint32_t kRawBytes = kRawMore + 16 * 16;
+// A stage's table: per A slot the checkpoint row (-1: a zero) and the scales
+// of the four 32-channel blocks (pairs of halves); per B position the dy pixel
+// (-1: a zero) and its sample.
+constexpr int kTabX = 0, kTabScale = kPos + 4, kTabDy = kTabScale + 4 * (kPos + 2),
+              kTabImg = kTabDy + kPos, kTableInts = kTabImg + kPos;
+constexpr size_t kSmem =
+    kStages * kStageBytes + kRaw * kRawBytes + kTables * kTableInts * 4 + 256;
 static_assert(kSmem <= 227 * 1024, "stages fit an SM");
+static_assert(kRawBytes % 16 == 0 && kStageBytes % 16 == 0 && kTableInts % 4 == 0, "aligned");
 constexpr int kSMs = 152;
 
 struct WgradParams {
@@ -91,6 +109,18 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_shared4(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // The power of two that brings a channel's largest |dy| to [2^14, 2^15), as a
 // float (2^127 at most); 1 for a channel with a non-finite value.
 __device__ __forceinline__ int dy_exponent(unsigned amax_bits) {
@@ -114,114 +144,159 @@ __device__ __forceinline__ Unit unit_at(const WgradParams &p, int u) {
   return t;
 }
 
-// Raw data of one stage in a producer thread's registers.
-struct Raw {
-  float dy[4][8];
-  uint4 x[5];
-  uint32_t xs[5];
+// Walks an SM's (unit, stage) range.
+struct Cursor {
+  int unit, stage;
+  __device__ __forceinline__ bool next(int stages) {  // true on a new unit
+    if (++stage < stages) return false;
+    stage = 0;
+    ++unit;
+    return true;
+  }
 };
+// Ends a chain with its kChain stages, its unit or the range.
+struct Chain {
+  int length = 0;
+  __device__ __forceinline__ bool ends(bool piece_end) {
+    if (!piece_end && ++length < kChain) return false;
+    length = 0;
+    return true;
+  }
+};
+
+// The rows and scales of a stage's positions, by one warp. A slot `slot` is
+// position q0 + slot read at tap kx = 0, so one to the left.
+template <int K>
+__device__ __forceinline__ void make_table(const WgradParams &p, unsigned q0, const Unit &un,
+                                           const uint32_t *etop, int lane, int *table) {
+  constexpr int kPasses = (kPos + K - 1 + 31) / 32;
+  const int nb = p.cp >> 5, b0 = un.ci0 >> 5;
+  int a[kPasses];
+  uint32_t byte[kPasses][4];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int slot = lane + 32 * i;
+    const unsigned pos = q0 + slot;
+    int b = -1, img = 0;
+    a[i] = -1;
+    const unsigned row = fast_div(pos, p.wp_magic, p.wp_shift);
+    const int x = static_cast<int>(pos - row * p.wp);
+    img = static_cast<int>(fast_div(row, p.h_magic, p.h_shift));
+    if (row < static_cast<unsigned>(p.n * p.h)) {
+      if (K == 1) {
+        a[i] = b = static_cast<int>(pos);
+      } else {
+        const int y = static_cast<int>(row) - img * p.h + un.ky - 1;
+        if (x > 0 && y >= 0 && y < p.h)
+          a[i] = (static_cast<int>(row) + un.ky - 1) * p.w + x - 1;
+        if (x < p.w) b = static_cast<int>(row) * p.w + x;
+      }
+    }
+    if (slot < kPos) {
+      table[kTabDy + slot] = b;
+      table[kTabImg + slot] = img;
+    }
+    if (slot < kPos + K - 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        byte[i][k] = a[i] >= 0 && b0 + k < nb
+                         ? __ldg(p.xs + static_cast<size_t>(a[i]) * nb + b0 + k) : 0u;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int slot = lane + 32 * i;
+    if (slot >= kPos + K - 1) continue;
+    table[kTabX + slot] = a[i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // 2^(7 - d), d binades below the largest block, as a half (zero under
+      // 2^-25; whatever a block of NaNs is multiplied by, it stays NaN)
+      const int e = 134 + static_cast<int>(byte[i][k]) - static_cast<int>(etop[k]);
+      const float f = __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 254)) << 23);
+      table[kTabScale + 4 * slot + k] = static_cast<int>(h2_bits(__float2half2_rn(f)));
+    }
+  }
+}
 
 // K: the conv's kernel size. NHWC: the layout of dy.
 template <int K, bool NHWC>
 struct Producer {
   const WgradParams &p;
   const int t;
-  // A: 16 input channels (two octets) at positions slot + 32 j; four threads
-  // cover 64 contiguous bytes, eight lanes store to distinct banks.
+  // A: 16 input channels (two octets) at one position; four threads cover 64
+  // contiguous bytes, eight lanes store to distinct banks.
   const int c16, a_slot;
-  // B: an octet of output channels at positions b_slot + 32 j.
+  // B: an octet of output channels at one position.
   const int co8, b_slot;
 
   __device__ explicit Producer(const WgradParams &params)
-      : p(params), t(threadIdx.x), c16((t & 3) | ((t >> 7) << 2)), a_slot((t >> 2) & 31),
-        co8(NHWC ? t & 7 : t >> 5), b_slot(NHWC ? t >> 3 : t & 31) {}
+      : p(params), t(threadIdx.x), c16((t & 3) | ((t >> 8) << 2)), a_slot((t >> 2) & 63),
+        co8(NHWC ? t & 7 : t >> 6), b_slot(NHWC ? t >> 3 : t & 63) {}
 
-  __device__ void load_x(Raw &r, int j, unsigned pos, const Unit &un) const {
-    const int ch = un.ci0 + 16 * c16;
-    long long pix = -1;
-    if (K == 1) {
-      if (pos < p.positions) pix = pos;
+  // Where this thread's channels start, for the unit whose stages are copied.
+  const uint8_t *x_src;
+  const float *dy_src;
+  bool x_in;
+  int dy_in;  // valid channels of the octet
+  __device__ void set_copy_unit(const Unit &un) {
+    const int ch = un.ci0 + 16 * c16, co = un.co0 + 8 * co8;
+    x_in = ch < p.cp;
+    x_src = p.xq + (x_in ? ch : 0);
+    dy_in = min(8, p.cout - co);
+    dy_src = dy_in > 0 ? p.dy + (NHWC ? static_cast<size_t>(co)
+                                      : static_cast<size_t>(co) * p.h * p.w) : p.dy;
+  }
+
+  __device__ __forceinline__ void copy_x(uint32_t dst, int pix) const {
+    const bool in = pix >= 0 && x_in;
+    const unsigned long long off =
+        static_cast<unsigned long long>(static_cast<unsigned>(in ? pix : 0)) *
+        static_cast<unsigned>(p.cp);
+    cp_async16(dst, x_src + off, in);
+  }
+
+  __device__ __forceinline__ void copy(uint32_t raw, const int *table) const {
+    const int pix = table[kTabDy + b_slot];
+    if (NHWC) {
+      const bool in = pix >= 0 && dy_in > 0;
+      const float *src = dy_src + static_cast<unsigned long long>(
+                                      static_cast<unsigned>(in ? pix : 0)) *
+                                      static_cast<unsigned>(p.cout);
+      cp_async16(raw + t * 16, src, in);
+      const bool in4 = in && dy_in > 4;
+      cp_async16(raw + kProducers * 16 + t * 16, in4 ? src + 4 : src, in4);
     } else {
-      const unsigned row = fast_div(pos, p.wp_magic, p.wp_shift);
-      const int x = static_cast<int>(pos - row * p.wp) - 1;
-      const int y = static_cast<int>(row - fast_div(row, p.h_magic, p.h_shift) * p.h) + un.ky - 1;
-      if (x >= 0 && y >= 0 && y < p.h && row < static_cast<unsigned>(p.n * p.h))
-        pix = (static_cast<long long>(row) + un.ky - 1) * p.w + x;
-    }
-    const bool in = pix >= 0 && ch < p.cp;
-    r.x[j] = in ? __ldg(reinterpret_cast<const uint4 *>(p.xq + pix * p.cp + ch))
-                : make_uint4(0, 0, 0, 0);
-    r.xs[j] = in ? __ldg(p.xs + pix * (p.cp >> 5) + (ch >> 5)) : 0u;
-  }
-
-  __device__ void load(Raw &r, unsigned stage, const Unit &un) const {
-    const unsigned q0 = stage * kPos;
+      const size_t hw = static_cast<size_t>(p.h) * p.w;
+      const int img = table[kTabImg + b_slot];
+      const float *src = dy_src + static_cast<size_t>(img) * (p.cout - 1) * hw + max(pix, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned q = q0 + b_slot + 32 * j;
-      const int co = un.co0 + 8 * co8;
-      long long pix = -1;
-      if (q < p.positions) {
-        if (K == 1) {
-          pix = q;
-        } else {
-          const unsigned row = fast_div(q, p.wp_magic, p.wp_shift);
-          const int x = static_cast<int>(q - row * p.wp);
-          if (x < p.w) pix = static_cast<long long>(row) * p.w + x;
-        }
-      }
-      if (NHWC) {
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float *src = p.dy + pix * p.cout + co;
-        const float4 a =
-            pix >= 0 && co < p.cout ? __ldg(reinterpret_cast<const float4 *>(src)) : zero;
-        const float4 b =
-            pix >= 0 && co + 4 < p.cout ? __ldg(reinterpret_cast<const float4 *>(src) + 1) : zero;
-        r.dy[j][0] = a.x;
-        r.dy[j][1] = a.y;
-        r.dy[j][2] = a.z;
-        r.dy[j][3] = a.w;
-        r.dy[j][4] = b.x;
-        r.dy[j][5] = b.y;
-        r.dy[j][6] = b.z;
-        r.dy[j][7] = b.w;
-      } else {
-        const unsigned hw = static_cast<unsigned>(p.h) * p.w;
-        const unsigned img = pix >= 0 ? static_cast<unsigned>(pix) / hw : 0u;
-        const float *src = p.dy + (static_cast<long long>(img) * p.cout + co) * hw +
-                           (pix - static_cast<long long>(img) * hw);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          r.dy[j][i] = pix >= 0 && co + i < p.cout ? __ldg(src + static_cast<long long>(i) * hw)
-                                                   : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const bool in = pix >= 0 && i < dy_in;
+        cp_async4(raw + i * (kProducers * 4) + t * 4, in ? src + i * hw : p.dy, in);
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) load_x(r, j, q0 + a_slot + 32 * j, un);
-    if (K == 3 && a_slot < 2) load_x(r, 4, q0 + 128 + a_slot, un);
+    copy_x(raw + kRawX + t * 16, table[kTabX + a_slot]);
+    if (K == 3 && a_slot < 2)
+      copy_x(raw + kRawMore + (a_slot * 8 + c16) * 16, table[kTabX + kPos + a_slot]);
   }
 
-  // Scales of the unit whose stages are converted next.
+  // Scales of dy for the unit whose stages are converted.
   float sdy[8];
-  uint32_t etop;
   __device__ void set_unit(const Unit &un) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int co = un.co0 + 8 * co8 + i;
       sdy[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
     }
-    const int ch = un.ci0 + 16 * c16;
-    etop = ch < p.cp ? __ldg(p.emax + (ch >> 5)) : 0u;
   }
 
-  // 16 channels at one position: times 2^(7 - d), d binades below the largest
-  // block, as a half (below 2^-24 zero; a block of NaNs keeps them).
-  __device__ void store_x(uint32_t a, const Raw &r, int j, int slot) const {
-    const uint32_t d = r.xs[j] == 255u ? 7u : etop - r.xs[j];
-    const uint32_t hb = d <= 21 ? (22 - d) << 10 : d <= 31 ? 1u << (31 - d) : 0u;
-    const uint32_t two = hb | (hb << 16);
+  __device__ __forceinline__ void store_x(uint32_t a, uint32_t raw, int slot,
+                                          const int *table) const {
+    const uint4 v = ld_shared16(raw);
+    const uint32_t two = static_cast<uint32_t>(table[kTabScale + 4 * slot + (c16 >> 1)]);
     const __half2 sc = *reinterpret_cast<const __half2 *>(&two);
-    const uint32_t w[4] = {r.x[j].x, r.x[j].y, r.x[j].z, r.x[j].w};
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -233,25 +308,39 @@ struct Producer {
     st_shared16(at + kSboA, make_uint4(o[4], o[5], o[6], o[7]));
   }
 
-  __device__ void store(uint32_t a, uint32_t b, const Raw &r) const {
+  __device__ __forceinline__ void store(uint32_t a, uint32_t b, uint32_t raw,
+                                        const int *table) const {
+    uint64_t v[4];
+    if (NHWC) {
+      const uint4 d0 = ld_shared16(raw + t * 16);
+      const uint4 d1 = ld_shared16(raw + kProducers * 16 + t * 16);
+      v[0] = pk2(__uint_as_float(d0.x), __uint_as_float(d0.y));
+      v[1] = pk2(__uint_as_float(d0.z), __uint_as_float(d0.w));
+      v[2] = pk2(__uint_as_float(d1.x), __uint_as_float(d1.y));
+      v[3] = pk2(__uint_as_float(d1.z), __uint_as_float(d1.w));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v0 = r.dy[j][2 * i] * sdy[2 * i], v1 = r.dy[j][2 * i + 1] * sdy[2 * i + 1];
-        const __half2 h = __floats2half2_rn(v0, v1);
-        const float2 f = __half22float2(h);
-        hi[i] = h2_bits(h);
-        lo[i] = h2_bits(__floats2half2_rn(v0 - f.x, v1 - f.y));
-      }
-      const uint32_t at = b + co8 * kSboB + (b_slot + 32 * j) * 16;
-      st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      st_shared16(at + kTN / 8 * kSboB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      for (int i = 0; i < 4; ++i)
+        v[i] = pk2(ld_shared4(raw + 2 * i * (kProducers * 4) + t * 4),
+                   ld_shared4(raw + (2 * i + 1) * (kProducers * 4) + t * 4));
     }
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store_x(a, r, j, a_slot + 32 * j);
-    if (K == 3 && a_slot < 2) store_x(a, r, 4, 128 + a_slot);
+    for (int i = 0; i < 4; ++i) {
+      // (the scaling is exact, so the difference is what hi dropped)
+      v[i] = mul2(v[i], pk2(sdy[2 * i], sdy[2 * i + 1]));
+      const __half2 h = __floats2half2_rn(lo2(v[i]), hi2(v[i]));
+      const float2 f = __half22float2(h);
+      const uint64_t rest = fma2(pk2(f.x, f.y), pk2(-1.f, -1.f), v[i]);
+      hi[i] = h2_bits(h);
+      lo[i] = h2_bits(__floats2half2_rn(lo2(rest), hi2(rest)));
+    }
+    const uint32_t at = b + co8 * kSboB + b_slot * 16;
+    st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+    st_shared16(at + kTN / 8 * kSboB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    store_x(a, raw + kRawX + t * 16, a_slot, table);
+    if (K == 3 && a_slot < 2)
+      store_x(a, raw + kRawMore + (a_slot * 8 + c16) * 16, kPos + a_slot, table);
   }
 };
 
@@ -264,16 +353,23 @@ template <int K, bool NHWC>
 __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p) {
   constexpr int TAPS = K;  // kx
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
+  uint8_t *raws = smem + kStages * kStageBytes;
+  int *tables = reinterpret_cast<int *>(raws + kRaw * kRawBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(tables + kTables * kTableInts);
   uint64_t *empty = full + kStages;
-  uint64_t *acc_done = empty + kStages, *acc_free = acc_done + 1;
+  uint64_t *tab_full = empty + kStages, *tab_empty = tab_full + kTables;
+  uint64_t *acc_done = tab_empty + kTables, *acc_free = acc_done + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 1);
   volatile uint32_t *abort = tmem_slot + 1;
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(full + i, kProducers / 32);
       mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < kTables; ++i) {
+      mbar_init(tab_full + i, 1);
+      mbar_init(tab_empty + i, kProducers / 32);
     }
     mbar_init(acc_done, 1);
     mbar_init(acc_free, kProducers / 32);
@@ -291,15 +387,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   const uint32_t tmem = *tmem_slot;
   const long long g0 = range_start(p.total, gridDim.x, blockIdx.x);
   const int count = static_cast<int>(range_start(p.total, gridDim.x, blockIdx.x + 1) - g0);
-  const int u0 = static_cast<int>(g0 / p.stages), s0 = static_cast<int>(g0 % p.stages);
-  // Stage i of this SM: unit u0 + (s0 + i) / stages, stage (s0 + i) % stages.
-  // A chain ends with its kChain stages, its unit or the range.
-  auto unit_of = [&](int i) { return u0 + (s0 + i) / p.stages; };
-  auto chain_end = [&](int i, bool *piece_end) {
-    const int first = max(0, (s0 + i) / p.stages * p.stages - s0);  // the piece's first stage
-    *piece_end = i == count - 1 || (s0 + i + 1) % p.stages == 0;
-    return *piece_end || (i - first + 1) % kChain == 0;
-  };
+  const Cursor start{static_cast<int>(g0 / p.stages), static_cast<int>(g0 % p.stages)};
   auto give_up = [&]() {
     *abort = 1u;
     atomicCAS(p.err, 0, static_cast<int>(VAE_EDEVICE_TIMEOUT));
@@ -308,115 +396,168 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   if (warp < kProducers / 32) {
     setmaxnreg_inc<kStageRegs>();
     Producer<K, NHWC> pr(p);
-    const int lane = threadIdx.x & 31;
-    const uint32_t base = smem_u32(smem);
-    // This warp drains TMEM lanes 32 (warp % 4) .., output channels 32 (warp / 4) ..
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21) + (warp >> 2) * 32;
-    float acc[TAPS][32];
+    const uint32_t base = smem_u32(smem), raw0 = smem_u32(raws);
+    bool ok = true;
+    // Waits agree across the warp, so that a timeout leaves it converged.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, p.wait_ns));
+    };
+
+    // This warp drains TMEM lanes 32 (warp % 4) .., output channels 16 (warp / 4) ..
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21) + (warp >> 2) * 16;
+    float acc[TAPS][16];
 #pragma unroll
     for (int k = 0; k < TAPS; ++k)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[k][i] = 0.f;
-    int drained = 0;     // stages whose chain end has been looked at
+      for (int i = 0; i < 16; ++i) acc[k][i] = 0.f;
+    int drained = 0;  // stages whose chain end has been looked at
     uint32_t chains = 0;
-    bool ok = true;
+    Cursor dr = start;
+    Chain dr_chain;
     auto drain_to = [&](int upto) {  // chains that end before stage `upto`
       for (; ok && drained < upto; ++drained) {
-        bool piece_end;
-        if (!chain_end(drained, &piece_end)) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_done, chains & 1, abort, p.wait_ns));
+        const bool piece_end = drained == count - 1 || dr.stage == p.stages - 1;
+        const int unit = dr.unit;
+        dr.next(p.stages);
+        if (!dr_chain.ends(piece_end)) continue;
+        ok = wait(acc_done, chains & 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < TAPS; ++k) {
-          float v[32];
-          tmem_ld_32cols(t_lane + k * 2 * kTN, v);
+          float v[16];
+          tmem_ld_16cols(t_lane + k * 2 * kTN, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[k][i] += v[i];
-          tmem_ld_32cols(t_lane + k * 2 * kTN + kTN, v);
+          for (int i = 0; i < 16; ++i) acc[k][i] += v[i];
+          tmem_ld_16cols(t_lane + k * 2 * kTN + kTN, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[k][i] += v[i];
+          for (int i = 0; i < 16; ++i) acc[k][i] += v[i];
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_free);
         ++chains;
         if (piece_end) {
-          const size_t piece = static_cast<size_t>(unit_of(drained)) + blockIdx.x;
-          float *o = p.part + piece * (TAPS * kTN * kTM) + (warp >> 2) * 32 * kTM +
+          const size_t piece = static_cast<size_t>(unit) + blockIdx.x;
+          float *o = p.part + piece * (TAPS * kTN * kTM) + (warp >> 2) * 16 * kTM +
                      (warp & 3) * 32 + lane;
 #pragma unroll
           for (int k = 0; k < TAPS; ++k)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
               o[(k * kTN + i) * kTM] = acc[k][i];
               acc[k][i] = 0.f;
             }
         }
       }
     };
-    Raw raw;
-    int unit = -1;
-    if (count > 0) pr.load(raw, s0, unit_at(p, u0));
+
+    Cursor cp = start;  // the stage whose copies are issued next
+    pr.set_copy_unit(unit_at(p, cp.unit));
+    auto copy = [&](int i) {
+      if (i < count) {
+        const int s = i % kTables;
+        ok = wait(tab_full + s, (i / kTables) & 1);
+        if (ok) {
+          pr.copy(raw0 + (i % kRaw) * kRawBytes, tables + s * kTableInts);
+          if (cp.next(p.stages) && i + 1 < count) pr.set_copy_unit(unit_at(p, cp.unit));
+        }
+      }
+      cp_async_commit();
+    };
+    Cursor cv = start;  // the stage that is converted
+    pr.set_unit(unit_at(p, cv.unit));
+#pragma unroll 1
+    for (int i = 0; i < kRaw - 1 && ok; ++i) copy(i);
+#pragma unroll 1
     for (int i = 0; i < count && ok; ++i) {
       const int s = i % kStages;
-      if (unit_of(i) != unit) {
-        unit = unit_of(i);
-        pr.set_unit(unit_at(p, unit));
-      }
-      if (i >= kStages)
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(empty + s, (i / kStages - 1) & 1, abort, p.wait_ns));
+      copy(i + kRaw - 1);
+      if (ok && i >= kStages) ok = wait(empty + s, (i / kStages - 1) & 1);
       if (!ok) break;
+      cp_async_wait<kRaw - 1>();
       const uint32_t a = base + s * kStageBytes;
-      pr.store(a, a + kBytesA, raw);
+      pr.store(a, a + kBytesA, raw0 + (i % kRaw) * kRawBytes, tables + (i % kTables) * kTableInts);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + s);
-      if (i + 1 < count)
-        pr.load(raw, (s0 + i + 1) % p.stages, unit_at(p, unit_of(i + 1)));
+      if (lane == 0) {
+        mbar_arrive(full + s);
+        mbar_arrive(tab_empty + i % kTables);
+      }
+      if (cv.next(p.stages) && i + 1 < count) pr.set_unit(unit_at(p, cv.unit));
       // Two stages behind: by then the next chain's first stages are staged.
       drain_to(i - 1);
     }
     if (ok) drain_to(count);
+    cp_async_wait<0>();
     if (!ok) give_up();
   } else {
     setmaxnreg_dec<kIssueRegs>();
     if (threadIdx.x == kProducers) {
-    constexpr uint32_t idesc = idesc_f16_mn(kTM, 2 * kTN);
-    const uint32_t base = smem_u32(smem);
-    uint32_t chains = 0;
-    bool fresh = true, ok = true;
-    for (int i = 0; i < count && ok; ++i) {
-      const int s = i % kStages;
-      if (fresh && chains > 0) ok = mbar_wait(acc_free, (chains - 1) & 1, abort, p.wait_ns);
-      if (ok) ok = mbar_wait(full + s, (i / kStages) & 1, abort, p.wait_ns);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t ad = mn_major_desc(base + s * kStageBytes, 128, kSboA);
-      const uint64_t bd = mn_major_desc(base + s * kStageBytes + kBytesA, 128, kSboB);
+      constexpr uint32_t idesc = idesc_f16_mn(kTM, 2 * kTN);
+      const uint32_t base = smem_u32(smem);
+      uint32_t chains = 0;
+      bool fresh = true, ok = true;
+      Cursor at = start;
+      Chain chain;
+      for (int i = 0; i < count && ok; ++i) {
+        const int s = i % kStages;
+        if (fresh && chains > 0) ok = mbar_wait(acc_free, (chains - 1) & 1, abort, p.wait_ns);
+        if (ok) ok = mbar_wait(full + s, (i / kStages) & 1, abort, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = mn_major_desc(base + s * kStageBytes, 128, kSboA);
+        const uint64_t bd = mn_major_desc(base + s * kStageBytes + kBytesA, 128, kSboB);
 #pragma unroll
-      for (int k = 0; k < kPos / 16; ++k)
+        for (int k = 0; k < kPos / 16; ++k)
 #pragma unroll
-        for (int tap = 0; tap < TAPS; ++tap)
-          umma_f16(tmem + tap * 2 * kTN, ad + 16 * k + tap, bd + 16 * k, idesc,
-                   !fresh || k > 0);
-      fresh = false;
-      umma_commit(empty + s);
-      bool piece_end;
-      if (chain_end(i, &piece_end)) {
-        umma_commit(acc_done);
-        ++chains;
-        fresh = true;
+          for (int tap = 0; tap < TAPS; ++tap)
+            umma_f16(tmem + tap * 2 * kTN, ad + 16 * k + tap, bd + 16 * k, idesc,
+                     !fresh || k > 0);
+        fresh = false;
+        umma_commit(empty + s);
+        const bool piece_end = i == count - 1 || at.stage == p.stages - 1;
+        at.next(p.stages);
+        if (chain.ends(piece_end)) {
+          umma_commit(acc_done);
+          ++chains;
+          fresh = true;
+        }
       }
-    }
-    if (!ok) {
-      give_up();
-      // the MMAs issued so far finish before TMEM is freed
-      umma_commit(acc_done);
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000) {}
-    }
+      if (!ok) {
+        give_up();
+        // the MMAs issued so far finish before TMEM is freed
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000) {}
+      }
+    } else if (warp > kProducers / 32) {
+      const int first = warp - kProducers / 32 - 1;
+      Cursor at = start;
+      for (int i = 0; i < first; ++i) at.next(p.stages);
+      int unit = -1;
+      Unit un{};
+      uint32_t etop[4];
+      bool ok = true;
+      for (int i = first; i < count && ok; i += kTableWarps) {
+        const int s = i % kTables;
+        if (i >= kTables)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(tab_empty + s, (i / kTables - 1) & 1, abort, p.wait_ns));
+        if (!ok) break;
+        if (at.unit != unit) {
+          unit = at.unit;
+          un = unit_at(p, unit);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            etop[k] = (un.ci0 >> 5) + k < p.cp >> 5 ? __ldg(p.emax + (un.ci0 >> 5) + k) : 0u;
+        }
+        make_table<K>(p, static_cast<unsigned>(at.stage) * kPos, un, etop, lane,
+                      tables + s * kTableInts);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tab_full + s);
+        for (int k = 0; k < kTableWarps; ++k) at.next(p.stages);
+      }
+      if (!ok) give_up();
     }
     __syncwarp();
   }
@@ -431,22 +572,41 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
 // ------------------------------------------------------------- before and after
 constexpr int kScanThreads = 256;
 
-// Largest scale byte below 255 of each 32-channel block; a share per block.
+// Largest scale byte below 255 of each 32-channel block; a share per block. A
+// thread steps over the bytes, as words, in strides of nb words, so that byte k
+// of its words always belongs to the same channel block.
 __device__ __forceinline__ void scan_scales(const uint8_t *__restrict__ xs, long long rows,
                                             int nb, unsigned *emax, unsigned *sm, int blk,
                                             int nblk) {
   for (int i = threadIdx.x; i < nb; i += kScanThreads) sm[i] = 0u;
   __syncthreads();
-  const long long r0 = rows * blk / nblk, r1 = rows * (blk + 1) / nblk;
-  const int per = kScanThreads / nb;  // rows at a time (nb <= 128)
-  const int b = threadIdx.x % nb, l = threadIdx.x / nb;
-  unsigned m = 0;
-  if (l < per)
-    for (long long r = r0 + l; r < r1; r += per) {
-      const unsigned v = __ldg(xs + r * nb + b);
-      if (v != 255u) m = max(m, v);
+  const long long bytes = rows * nb, words = bytes / 4;
+  const int per = kScanThreads / nb * nb;  // (nb <= 128)
+  const long long strides = (words + per - 1) / per;
+  const long long w1 = min(words, strides * (blk + 1) / nblk * per);
+  long long w = strides * blk / nblk * per + threadIdx.x;
+  if (threadIdx.x < per && w < w1) {
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(xs);
+    unsigned m = 0;
+    const int first = static_cast<int>(4 * w % nb);
+    auto add = [&](uint32_t v) { m = __vmaxu4(m, v & ~__vcmpeq4(v, 0xffffffffu)); };
+    for (; w + 3 * per < w1; w += 4 * per) {
+      uint32_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = __ldg(src + w + u * per);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add(v[u]);
     }
-  if (m) atomicMax(sm + b, m);
+    for (; w < w1; w += per) add(__ldg(src + w));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (m >> (8 * k) & 255u) atomicMax(sm + (first + k) % nb, m >> (8 * k) & 255u);
+  }
+  if (blk == 0 && threadIdx.x < (bytes & 3)) {
+    const long long i = bytes - 1 - threadIdx.x;
+    const unsigned v = xs[i];
+    if (v != 255u) atomicMax(sm + static_cast<int>(i % nb), v);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < nb; i += kScanThreads)
     if (sm[i]) atomicMax(emax + i, sm[i]);
