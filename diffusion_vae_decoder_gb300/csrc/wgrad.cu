@@ -29,9 +29,9 @@
 // and a last pass adds a unit's pieces in order and undoes the scaling: the
 // same inputs give the same bits.
 //
-// Sixteen warps stage: each thread copies its own 48 bytes of a stage to shared
-// memory three stages ahead (cp.async, no barrier: it reads back only what it
-// copied), converts them and stores the operands; they also drain the
+// Sixteen warps stage: each thread copies its own 48 bytes of a half stage to
+// shared memory three halves ahead (cp.async, no barrier: it reads back only
+// what it copied), converts them and stores the operands; they also drain the
 // accumulators. Three warps turn positions into pixel indexes and block scales
 // ahead of them, one thread issues the MMAs.
 #include "ptx.cuh"
@@ -44,11 +44,12 @@ namespace {
 
 constexpr int kTM = 128;           // input channels of a tile (TMEM lanes)
 constexpr int kTN = 64;            // output channels
-constexpr int kPos = 64;           // positions of a stage
-constexpr int kStages = 3;         // staged operands
-constexpr int kRaw = 4;            // raw stages: three in flight, one being converted
-constexpr int kTables = 8;
-constexpr int kChain = 32;         // stages between two drains: 2048 positions
+constexpr int kPos = 128;          // positions of a stage
+constexpr int kHalf = 64;          // positions that the staging threads take at once
+constexpr int kStages = 2;         // staged operands
+constexpr int kRaw = 3;            // raw halves in flight
+constexpr int kTables = 4;
+constexpr int kChain = 16;         // stages between two drains: 2048 positions
 constexpr int kProducers = 512;    // staging threads: 16 warps
 constexpr int kTableWarps = 3;     // each makes every third table
 constexpr int kMmaThreads = kProducers + 128;  // one more warpgroup issues and makes tables
@@ -64,7 +65,7 @@ constexpr uint32_t kSboA = kSlotsA * 16, kSboB = kSlotsB * 16;
 constexpr uint32_t kBytesA = kTM / 8 * kSboA;      // 16 octets
 constexpr uint32_t kBytesB = 2 * kTN / 8 * kSboB;  // hi, then lo
 constexpr uint32_t kStageBytes = (kBytesA + kBytesB + 127) / 128 * 128;
-// A raw stage: 32 bytes of dy and 16 of x~ per staging thread, and the two
+// A raw half: 32 bytes of dy and 16 of x~ per staging thread, and the two
 // further positions of x~ that the taps of a 3x3 conv reach (16 threads).
 constexpr uint32_t kRawX = kProducers * 32, kRawMore = kRawX + kProducers * 16;
 constexpr uint32_t kRawBytes = kRawMore + 16 * 16;
@@ -256,8 +257,10 @@ struct Producer {
     cp_async16(dst, x_src + off, in);
   }
 
-  __device__ __forceinline__ void copy(uint32_t raw, const int *table) const {
-    const int pix = table[kTabDy + b_slot];
+  // Half `half` of a stage.
+  __device__ __forceinline__ void copy(uint32_t raw, const int *table, int half) const {
+    const int b_at = b_slot + kHalf * half, a_at = a_slot + kHalf * half;
+    const int pix = table[kTabDy + b_at];
     if (NHWC) {
       const bool in = pix >= 0 && dy_in > 0;
       const float *src = dy_src + static_cast<unsigned long long>(
@@ -268,7 +271,7 @@ struct Producer {
       cp_async16(raw + kProducers * 16 + t * 16, in4 ? src + 4 : src, in4);
     } else {
       const size_t hw = static_cast<size_t>(p.h) * p.w;
-      const int img = table[kTabImg + b_slot];
+      const int img = table[kTabImg + b_at];
       const float *src = dy_src + static_cast<size_t>(img) * (p.cout - 1) * hw + max(pix, 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -276,8 +279,8 @@ struct Producer {
         cp_async4(raw + i * (kProducers * 4) + t * 4, in ? src + i * hw : p.dy, in);
       }
     }
-    copy_x(raw + kRawX + t * 16, table[kTabX + a_slot]);
-    if (K == 3 && a_slot < 2)
+    copy_x(raw + kRawX + t * 16, table[kTabX + a_at]);
+    if (K == 3 && half == 1 && a_slot < 2)
       copy_x(raw + kRawMore + (a_slot * 8 + c16) * 16, table[kTabX + kPos + a_slot]);
   }
 
@@ -309,7 +312,7 @@ struct Producer {
   }
 
   __device__ __forceinline__ void store(uint32_t a, uint32_t b, uint32_t raw,
-                                        const int *table) const {
+                                        const int *table, int half) const {
     uint64_t v[4];
     if (NHWC) {
       const uint4 d0 = ld_shared16(raw + t * 16);
@@ -335,11 +338,11 @@ struct Producer {
       hi[i] = h2_bits(h);
       lo[i] = h2_bits(__floats2half2_rn(lo2(rest), hi2(rest)));
     }
-    const uint32_t at = b + co8 * kSboB + b_slot * 16;
+    const uint32_t at = b + co8 * kSboB + (b_slot + kHalf * half) * 16;
     st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
     st_shared16(at + kTN / 8 * kSboB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-    store_x(a, raw + kRawX + t * 16, a_slot, table);
-    if (K == 3 && a_slot < 2)
+    store_x(a, raw + kRawX + t * 16, a_slot + kHalf * half, table);
+    if (K == 3 && half == 1 && a_slot < 2)
       store_x(a, raw + kRawMore + (a_slot * 8 + c16) * 16, kPos + a_slot, table);
   }
 };
@@ -452,32 +455,43 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
       }
     };
 
-    Cursor cp = start;  // the stage whose copies are issued next
+    // Copies run three halves ahead of the conversion: halves `ahead` of stage
+    // `at`, into the raw buffers in turn.
+    Cursor cp = start;
+    int at = 0, ahead = 0;
+    uint32_t raw_in = 0, raw_out = 0;
     pr.set_copy_unit(unit_at(p, cp.unit));
-    auto copy = [&](int i) {
-      if (i < count) {
-        const int s = i % kTables;
-        ok = wait(tab_full + s, (i / kTables) & 1);
-        if (ok) {
-          pr.copy(raw0 + (i % kRaw) * kRawBytes, tables + s * kTableInts);
-          if (cp.next(p.stages) && i + 1 < count) pr.set_copy_unit(unit_at(p, cp.unit));
+    auto copy = [&]() {
+      if (at < count) {
+        const int s = at % kTables;
+        if (!ahead) ok = wait(tab_full + s, (at / kTables) & 1);
+        if (ok) pr.copy(raw0 + raw_in, tables + s * kTableInts, ahead);
+        if (ahead) {
+          ++at;
+          if (cp.next(p.stages) && at < count) pr.set_copy_unit(unit_at(p, cp.unit));
         }
+        ahead ^= 1;
       }
       cp_async_commit();
+      raw_in = raw_in == (kRaw - 1) * kRawBytes ? 0 : raw_in + kRawBytes;
     };
     Cursor cv = start;  // the stage that is converted
     pr.set_unit(unit_at(p, cv.unit));
-#pragma unroll 1
-    for (int i = 0; i < kRaw - 1 && ok; ++i) copy(i);
+    for (int i = 0; i < kRaw && ok; ++i) copy();
 #pragma unroll 1
     for (int i = 0; i < count && ok; ++i) {
       const int s = i % kStages;
-      copy(i + kRaw - 1);
-      if (ok && i >= kStages) ok = wait(empty + s, (i / kStages - 1) & 1);
+      if (i >= kStages) ok = wait(empty + s, (i / kStages - 1) & 1);
       if (!ok) break;
-      cp_async_wait<kRaw - 1>();
       const uint32_t a = base + s * kStageBytes;
-      pr.store(a, a + kBytesA, raw0 + (i % kRaw) * kRawBytes, tables + (i % kTables) * kTableInts);
+      const int *table = tables + (i % kTables) * kTableInts;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        cp_async_wait<kRaw - 1>();
+        pr.store(a, a + kBytesA, raw0 + raw_out, table, half);
+        raw_out = raw_out == (kRaw - 1) * kRawBytes ? 0 : raw_out + kRawBytes;
+        copy();
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -485,8 +499,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
         mbar_arrive(tab_empty + i % kTables);
       }
       if (cv.next(p.stages) && i + 1 < count) pr.set_unit(unit_at(p, cv.unit));
-      // Two stages behind: by then the next chain's first stages are staged.
-      drain_to(i - 1);
+      // One stage behind: the next chain's first stage is staged by then.
+      drain_to(i);
     }
     if (ok) drain_to(count);
     cp_async_wait<0>();
@@ -770,8 +784,13 @@ WgradWs carve_wgrad(Carver &cv, int n, int cin, int h, int w, int cout, int k) {
   const long long positions = static_cast<long long>(n) * h * (w + (k == 3));
   ws.stages = ceil_div(positions, kPos);
   ws.units = ceil_div(cin, kTM) * ceil_div(cout, kTN) * k;
-  ws.grid = static_cast<int>(
-      std::min<long long>(kSMs, static_cast<long long>(ws.units) * ws.stages));
+  // Whole slices of the pixels per SM where that leaves few SMs idle: the units
+  // then walk the same pixels at the same time and share them in L2.
+  const int slices = std::min(kSMs / ws.units, ws.stages);
+  ws.grid = slices * ws.units >= kSMs * 9 / 10
+                ? slices * ws.units
+                : static_cast<int>(std::min<long long>(
+                      kSMs, static_cast<long long>(ws.units) * ws.stages));
   ws.psum = cv.take<float>(static_cast<size_t>(ws.slabs) * cout);
   ws.maxima = cv.take<unsigned>(cout + ckpt_cp(cin) / 32);
   ws.part = cv.take<float>(static_cast<size_t>(ws.units + ws.grid - 1) * k * kTN * kTM);
