@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libvae.so")
 
 SOURCES = ["igemm.cu", "igemm_split.cu", "igemm_xf.cu", "groupnorm.cu", "softmax.cu", "layout.cu", "ops.cu", "chain.cu",
            "runtime.cu", "noalloc.cu", "head.cu", "head_tc.cu", "flash.cu", "splitk.cu", "peak.cu", "tiled.cu",
-           "ckpt.cu", "gn_train.cu", "block_norm.cu", "wgrad.cu", "train.cu"]
+           "ckpt.cu", "gn_train.cu", "gn_resident.cu",
+           "block_norm.cu", "wgrad.cu", "train.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",

@@ -23,6 +23,20 @@ __device__ __forceinline__ Triple merge(Triple a, Triple b) {
   return {n, fmaf(d, wb, a.mean), a.m2 + b.m2 + d * d * a.n * wb};
 }
 
+// Fixed-order merge of the 32 lanes' triples (xor butterfly: at each level a
+// lane merges the lower-lane operand first); every lane returns the total,
+// bit-identical to lane 0's.
+__device__ __forceinline__ Triple warp_merge(Triple acc) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Triple other{__shfl_xor_sync(0xffffffffu, acc.n, o),
+                       __shfl_xor_sync(0xffffffffu, acc.mean, o),
+                       __shfl_xor_sync(0xffffffffu, acc.m2, o)};
+    acc = (threadIdx.x & o) ? merge(other, acc) : merge(acc, other);
+  }
+  return acc;
+}
+
 // NHWC: x[n][spatial][c]. Block `blk` of `nblk` of sample n reduces its slab
 // of pixels into partials [n][groups][nblk] (count, mean, M2); sm holds
 // 3 * kStatThreads * 4 floats.

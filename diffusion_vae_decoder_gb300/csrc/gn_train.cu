@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 // ------------------------------------------------------------- forward apply
 // grid (slabs, n).
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     ckpt_apply_nhwc(const float *x, int c, long long spatial, int groups,
                     const float2 *__restrict__ stats, const float *__restrict__ gamma,
                     const float *__restrict__ beta, int silu, float *y, CkptView kx,
@@ -144,39 +144,6 @@ __global__ void __launch_bounds__(kThreads)
   for (; p >= p0; p -= ppi) one(p, load(p));
 }
 
-// Stores 32 channels of one row: payload and scale byte.
-__device__ __forceinline__ void keep_row32(const float *v, CkptView k, long long row, int cp,
-                                           int cb) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) m = max(m, abs_bits(v[j]));
-  const uint32_t byte = ckpt_scale_byte(m);
-  const float inv = ckpt_inv_scale(byte);
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j] = pack_e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv,
-                       v[4 * j + 3] * inv);
-  uint4 *dst = reinterpret_cast<uint4 *>(k.q + row * cp + 32 * cb);
-  __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
-  __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
-  k.scale[row * (cp >> 5) + cb] = static_cast<uint8_t>(byte);
-}
-__device__ __forceinline__ void read_row32(float *v, CkptView k, long long row, int cp, int cb) {
-  const uint4 *src = reinterpret_cast<const uint4 *>(k.q + row * cp + 32 * cb);
-  const uint4 a = __ldg(src), b = __ldg(src + 1);
-  const float sc = ckpt_scale(__ldg(k.scale + row * (cp >> 5) + cb));
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 f = unpack_e4m3x4(w[j], sc);
-    v[4 * j] = f.x;
-    v[4 * j + 1] = f.y;
-    v[4 * j + 2] = f.z;
-    v[4 * j + 3] = f.w;
-  }
-}
-
 // Per-channel constants of a 32-channel block, in shared memory: (mean, rstd,
 // gamma, beta), zeros past c.
 __device__ __forceinline__ void load_affine32(float4 *aff, int n, int c, int cb, int groups,
@@ -225,18 +192,8 @@ __global__ void __launch_bounds__(kPixThreads)
 }
 
 // ------------------------------------------------------------- backward
-// dz and xh of one element.
-__device__ __forceinline__ float grad_z(float dy, float xv, float mean, float rstd, float ga,
-                                        float be, int silu, float *xh) {
-  *xh = (xv - mean) * rstd;
-  if (!silu) return dy;
-  const float z = fmaf(*xh, ga, be);
-  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-  return dy * (s * fmaf(z, 1.0f - s, 1.0f));
-}
-
 // Per-(slab, channel) sums of dz and dz xh: part [n][slabs][c] float2. grid (slabs, n).
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     ckpt_sums_nhwc(const float *__restrict__ dy, CkptView k, int c, long long spatial, int groups,
                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
                    const float *__restrict__ beta, int silu, float2 *__restrict__ part) {
@@ -320,33 +277,29 @@ __global__ void __launch_bounds__(kPixThreads)
   const long long p0 = spatial * blockIdx.x / gridDim.x,
                   p1 = spatial * (blockIdx.x + 1) / gridDim.x;
   const float *gs = dy + (static_cast<long long>(n) * c + 32 * cb) * spatial;
-  float a[32], b[32];
-#pragma unroll
-  for (int j = 0; j < 32; ++j) a[j] = b[j] = 0.f;
-  for (long long p = p0 + threadIdx.x; p < p1; p += kPixThreads) {
-    float v[32];
-    read_row32(v, k, static_cast<long long>(n) * spatial + p, cp, cb);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float2 sum = make_float2(0.f, 0.f);  // of channel `lane`
+  for (long long pw = p0 + 32 * warp; pw < p1; pw += kPixThreads) {
+    const long long p = pw + lane;
+    const bool here = p < p1;
+    float v[32], g[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      if (j < chans) {
-        const float4 f = aff[j];
-        float xh;
-        const float dz = grad_z(__ldg(gs + j * spatial + p), v[j], f.x, f.y, f.z, f.w, silu, &xh);
-        a[j] += dz;
-        b[j] = fmaf(dz, xh, b[j]);
-      }
+      g[j] = j < chans && here ? __ldg(gs + j * spatial + p) : 0.f;
+      v[j] = 0.f;
     }
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (here) read_row32(v, k, static_cast<long long>(n) * spatial + p, cp, cb);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
-      b[j] += __shfl_xor_sync(0xffffffffu, b[j], o);
+    for (int j = 0; j < 32; ++j) {
+      const float4 f = aff[j];
+      float xh;
+      g[j] = grad_z(g[j], v[j], f.x, f.y, f.z, f.w, silu, &xh);
+      v[j] = g[j] * xh;
     }
-    if (lane == j) red[warp][j] = make_float2(a[j], b[j]);
+    sum.x += reduce_scatter32(g, lane);
+    sum.y += reduce_scatter32(v, lane);
   }
+  red[warp][lane] = sum;
   __syncthreads();
   if (threadIdx.x < chans) {
     float2 t = red[0][threadIdx.x];
@@ -426,7 +379,7 @@ __device__ __forceinline__ void group_means(float2 *km, const float2 *__restrict
 }
 
 // grid (slabs, n).
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     ckpt_dx_nhwc(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
                  const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
@@ -480,18 +433,18 @@ __global__ void __launch_bounds__(kThreads)
     return static_cast<uint32_t>(__ldg(k.scale + (row0 + p) * (cp >> 5) + (q >> 3)));
   };
   long long p = p1 - 1 - pl;
-  for (; p - 3 * ppi >= p0; p -= 4 * ppi) {
-    float4 g[4], r[4];
-    uint32_t w[4], sb[4];
+  for (; p - ppi >= p0; p -= 2 * ppi) {
+    float4 g[2], r[2];
+    uint32_t w[2], sb[2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       g[u] = ld_g(p - u * ppi);
       w[u] = ld_q(p - u * ppi);
       sb[u] = ld_s(p - u * ppi);
       r[u] = ld_r(p - u * ppi);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) one(p - u * ppi, g[u], w[u], sb[u], r[u]);
+    for (int u = 0; u < 2; ++u) one(p - u * ppi, g[u], w[u], sb[u], r[u]);
   }
   for (; p >= p0; p -= ppi) one(p, ld_g(p), ld_q(p), ld_s(p), ld_r(p));
 }
@@ -574,6 +527,9 @@ size_t gn_backward_ws_bytes(int n, int c, long long spatial, int groups) {
 int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int groups, float eps,
             const float *gamma, const float *beta, int silu, float *y, CkptView kx, CkptView ky,
             float *stats, void *ws, cudaStream_t s) {
+  const int rc = gn_ckpt_resident(x, n, c, spatial, nhwc, groups, eps, gamma, beta, silu, y, kx,
+                                  ky, stats, s);
+  if (rc != VAE_EUNSUPPORTED) return rc;
   Carver cv(ws, ~size_t(0));
   const CkptWs w = carve_forward(cv, n, c, spatial, groups);
   float2 *st = reinterpret_cast<float2 *>(stats);
@@ -609,6 +565,14 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   const CkptWs w = carve_backward(cv, n, c, spatial);
   const float2 *st = reinterpret_cast<const float2 *>(stats);
   float2 *part = reinterpret_cast<float2 *>(w.part);
+  const int rc = gn_backward_resident(dy, k, stats, n, c, spatial, nhwc, groups, gamma, beta,
+                                      silu, dres, dx, dgamma, dbeta, w.sums, s);
+  if (rc == VAE_OK && n > 1 && (dgamma || dbeta)) {
+    ckpt_sums_merge<<<ckpt_cp(c) / 32, 1024, 0, s>>>(w.sums, 1, n, c, part, dgamma, dbeta);
+    VAE_LAUNCH_CHECK();
+    count_launches(1);
+  }
+  if (rc != VAE_EUNSUPPORTED) return rc;
   const int slabs = nhwc ? slabs_nhwc(n, c, spatial) : slabs_nchw(n, c, spatial);
   const dim3 grid = nhwc ? dim3(slabs, n) : dim3(slabs, ckpt_cp(c) / 32, n);
   if (nhwc)

@@ -2,6 +2,7 @@
 // backward pass (gn_train.cu).
 #pragma once
 #include "ckpt.cuh"
+#include "gn_stats.cuh"
 
 namespace vae {
 
@@ -19,5 +20,79 @@ int gn_backward(const float *dy, CkptView x_ckpt, const float *stats, int n, int
                 long long spatial, int nhwc, int groups, const float *gamma, const float *beta,
                 int silu, const float *dres, float *dx, float *dgamma, float *dbeta, void *ws,
                 cudaStream_t s);
+
+// The same in one launch of thread-block clusters that hold a (sample, channel
+// slab) on chip between the reduction and the elementwise pass
+// (gn_resident.cu); VAE_EUNSUPPORTED, with nothing launched, for slabs that do
+// not fit.
+int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, int groups,
+                     float eps, const float *gamma, const float *beta, int silu, float *y,
+                     CkptView x_ckpt, CkptView y_ckpt, float *stats, cudaStream_t s);
+// sums: [n][c] float2 for (sum dz, sum dz xh), written when n > 1 (dgamma and
+// dbeta are written here for n == 1).
+int gn_backward_resident(const float *dy, CkptView x_ckpt, const float *stats, int n, int c,
+                         long long spatial, int nhwc, int groups, const float *gamma,
+                         const float *beta, int silu, const float *dres, float *dx,
+                         float *dgamma, float *dbeta, float2 *sums, cudaStream_t s);
+
+// ------------------------------------------------------------- device pieces
+// Stores 32 channels of one row: payload and scale byte.
+__device__ __forceinline__ void keep_row32(const float *v, CkptView k, long long row, int cp,
+                                           int cb) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) m = max(m, abs_bits(v[j]));
+  const uint32_t byte = ckpt_scale_byte(m);
+  const float inv = ckpt_inv_scale(byte);
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w[j] = pack_e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv,
+                       v[4 * j + 3] * inv);
+  uint4 *dst = reinterpret_cast<uint4 *>(k.q + row * cp + 32 * cb);
+  __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  k.scale[row * (cp >> 5) + cb] = static_cast<uint8_t>(byte);
+}
+__device__ __forceinline__ void read_row32(float *v, CkptView k, long long row, int cp, int cb) {
+  const uint4 *src = reinterpret_cast<const uint4 *>(k.q + row * cp + 32 * cb);
+  const uint4 a = __ldg(src), b = __ldg(src + 1);
+  const float sc = ckpt_scale(__ldg(k.scale + row * (cp >> 5) + cb));
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 f = unpack_e4m3x4(w[j], sc);
+    v[4 * j] = f.x;
+    v[4 * j + 1] = f.y;
+    v[4 * j + 2] = f.z;
+    v[4 * j + 3] = f.w;
+  }
+}
+
+// dz and xh of one element.
+__device__ __forceinline__ float grad_z(float dy, float xv, float mean, float rstd, float ga,
+                                        float be, int silu, float *xh) {
+  *xh = (xv - mean) * rstd;
+  if (!silu) return dy;
+  const float z = fmaf(*xh, ga, be);
+  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+  return dy * (s * fmaf(z, 1.0f - s, 1.0f));
+}
+
+// Sums of 32 values over a warp, value j to lane j: 31 shuffles; each step
+// halves the values a lane still carries. The order is fixed.
+__device__ __forceinline__ float reduce_scatter32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < o) {
+        const float keep = up ? v[j + o] : v[j], send = up ? v[j] : v[j + o];
+        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+  }
+  return v[0];
+}
 
 }  // namespace vae

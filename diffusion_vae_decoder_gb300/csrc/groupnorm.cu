@@ -166,20 +166,6 @@ __global__ void gn_apply_nchw(const float *__restrict__ x, long long total, int 
 constexpr int kFusedMaxSlots = 64;
 constexpr int kCompactThreads = 256;
 
-// Fixed-order merge of the 32 lanes' triples (xor butterfly: at each level a
-// lane merges the lower-lane operand first); every lane returns the total,
-// bit-identical to lane 0's.
-__device__ __forceinline__ Triple warp_merge(Triple acc) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Triple other{__shfl_xor_sync(0xffffffffu, acc.n, o),
-                       __shfl_xor_sync(0xffffffffu, acc.mean, o),
-                       __shfl_xor_sync(0xffffffffu, acc.m2, o)};
-    acc = (threadIdx.x & o) ? merge(other, acc) : merge(acc, other);
-  }
-  return acc;
-}
-
 // Compacted slots per (sample, group) in gn_compact_finalize: one block each,
 // so a 32-group sample takes 512 blocks, a single wave on the SMs.
 constexpr int kCompactSlots = 16;

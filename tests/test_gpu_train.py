@@ -120,6 +120,8 @@ def test_pack_edges_of_the_format():
 # ---------------------------------------------------------------- GroupNorm + SiLU
 GN = [(1, 8, 8, 128, 32), (2, 5, 7, 32, 32), (1, 1, 1, 64, 32), (3, 3, 11, 96, 32),
       (1, 37, 29, 48, 8), (2, 16, 33, 512, 32), (1, 4, 9, 1024, 1), (1, 130, 70, 36, 9)]
+# one launch with clusters of 8 and 16 blocks, and the passes over larger tensors
+GN_LARGE = [(1, 96, 100, 64, 32), (1, 150, 160, 64, 32), (2, 190, 180, 32, 8)]
 
 
 def gn_data(n, h, w, c, seed):
@@ -185,6 +187,58 @@ def test_groupnorm_ckpt_agrees_with_vae_groupnorm_silu():
         _, rstd = R.group_stats(x.reshape(1, -1, 128).astype(np.float64), 32, 1e-6)
         assert float((y - z).abs().max()) <= 2 * gn_out_bound(x, rstd, gamma, beta) * (
             1 + (np.abs(x).max() * rstd.max()) ** 2)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n,h,w,c,groups", GN_LARGE)
+def test_groupnorm_pair_on_larger_tensors(layout, n, h, w, c, groups):
+    """Against float64 torch on the GPU; the same bounds as below."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    f = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    rows, dyr = f(n, h * w, c) * 2 + 1, f(n, h * w, c)
+    gamma, beta, eps = 1 + 0.1 * f(c), 0.1 * f(c), 1e-4
+
+    def lay(t):
+        t = t.view(n, h, w, c)
+        return t if layout == 1 else t.permute(0, 3, 1, 2).contiguous()
+
+    def unlay(t):
+        return (t if layout == 1 else t.permute(0, 2, 3, 1)).reshape(n, h * w, c).double()
+
+    y, kx, ky, st = pkg().vae_groupnorm_silu_ckpt(lay(rows), gamma, beta, groups=groups, eps=eps,
+                                                  layout=layout)
+    ga, be, per = gamma.double(), beta.double(), lambda a: a.repeat_interleave(  # noqa: E731
+        c // groups, 1)[:, None]
+    x = rows.double().view(n, h * w, groups, -1)
+    mean, var = x.mean((1, 3)), x.var((1, 3), unbiased=False)
+    rstd = (var + eps).rsqrt()
+    z = (rows.double() - per(mean)) * per(rstd) * ga + be
+    top = float(rows.abs().max() * rstd.max())
+    bound = 64 * H * (1.5 * top + 2) * (1 + top ** 2)
+    assert float((unlay(y) - z * z.sigmoid()).abs().max()) <= bound
+    assert float((st[..., 1].double() - rstd).abs().max()) <= bound
+    # the checkpoints are those of a separate pack of x and y
+    for kept, t in ((kx, lay(rows)), (ky, y)):
+        again = pkg().vae_ckpt_pack(t, layout=layout)
+        assert (parts(kept)[0] == parts(again)[0]).all() and (
+            parts(kept)[1] == parts(again)[1]).all()
+    dx, dgamma, dbeta = pkg().vae_groupnorm_silu_backward(lay(dyr), kx, st, gamma, beta,
+                                                          groups=groups, layout=layout)
+    xt = unlay(pkg().vae_ckpt_unpack(kx, y.shape, layout=layout))
+    xh = (xt - per(st[..., 0].double())) * per(st[..., 1].double())
+    z = xh * ga + be
+    s = z.sigmoid()
+    dz = dyr.double() * s * (1 + z * (1 - s))
+    t = (dz * ga).view(n, h * w, groups, -1)
+    m = lambda a: a.reshape(n, h * w, groups, -1).mean((1, 3))  # noqa: E731
+    want = per(st[..., 1].double()) * (dz * ga - per(m(t)) - xh * per(m(t * xh.view_as(t))))
+    limit = 256 * H * float(rstd.max()) * 1.1 * float(dyr.abs().max()) * 1.5 * (
+        2 + float(xh.abs().max())) ** 2
+    assert float((unlay(dx) - want).abs().max()) <= limit
+    size = 1.1 * dyr.double().abs().sum((0, 1))
+    assert bool(((dgamma.double() - (dz * xh).sum((0, 1))).abs() <=
+                 256 * H * size * (1 + float(xh.abs().max()))).all())
+    assert bool(((dbeta.double() - dz.sum((0, 1))).abs() <= 256 * H * size).all())
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
