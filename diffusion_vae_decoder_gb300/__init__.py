@@ -10,6 +10,7 @@ an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -461,6 +462,8 @@ def vae_causal_stack(x, layers, groups=32, eps=1e-6, layout=VAE_NCHW, out=None, 
 
 
 # ---------------------------------------------------------------- training operators
+# These are called many times a step on tensors whose kernels take a few
+# microseconds, so the checks are one short call per tensor.
 class Checkpoint:
     """An 8-bit activation checkpoint (vae_ckpt_bytes): ``buf``, the bytes on the
     device, holding ``rows`` pixels or tokens of ``c`` channels. ``payload``
@@ -480,120 +483,151 @@ class Checkpoint:
         self.buf, self.rows, self.c = buf, rows, c
 
     @staticmethod
-    def _parts(rows, c):
+    def nbytes(rows, c):
         cp = (c + 31) // 32 * 32
-        return cp, (rows * cp + 255) // 256 * 256
+        return (rows * cp + 255) // 256 * 256 + rows * (cp // 32)
 
     @classmethod
-    def nbytes(cls, rows, c):
-        cp, at = cls._parts(rows, c)
-        return at + rows * (cp // 32)
-
-    @classmethod
-    def empty(cls, rows, c, device):
+    def _make(cls, rows, c, device):
         import torch
-        return cls(torch.empty(cls.nbytes(rows, c), dtype=torch.uint8, device=device), rows, c)
+        self = cls.__new__(cls)
+        self.buf = torch.empty(cls.nbytes(rows, c), dtype=torch.uint8, device=device)
+        self.rows, self.c = rows, c
+        return self
 
     @property
     def payload(self):
         import torch
-        cp, _ = self._parts(self.rows, self.c)
-        return self.buf[:self.rows * cp].view(torch.float8_e4m3fn).view(self.rows, cp)
+        cp = (self.c + 31) // 32 * 32
+        return self.buf.view(torch.float8_e4m3fn).as_strided((self.rows, cp), (cp, 1))
 
     @property
     def scale(self):
         import torch
-        cp, at = self._parts(self.rows, self.c)
-        n = self.rows * (cp // 32)
-        return self.buf[at:at + n].view(torch.float8_e8m0fnu).view(self.rows, cp // 32)
+        cp = (self.c + 31) // 32 * 32
+        # (as_strided's offset counts from the storage's start)
+        at = self.buf.storage_offset() + (self.rows * cp + 255) // 256 * 256
+        return self.buf.view(torch.float8_e8m0fnu).as_strided((self.rows, cp // 32),
+                                                              (cp // 32, 1), at)
 
 
-def _need_ckpt(k, rows, c, like, name):
+def _refuse(t, shape, device, name):
+    """Why `_at` does not take `t`."""
+    _need(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _at(t, shape, device, name):
+    """The address of a contiguous float32 tensor of `shape` on `device`."""
+    import torch
+    try:
+        if (t.dtype is torch.float32 and t.shape == shape and t.device == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, shape, device, name)
+
+
+def _at_opt(t, shape, device, name):
+    return None if t is None else _at(t, shape, device, name)
+
+
+def _ckpt_at(k, rows, c, device, name):
     if not isinstance(k, Checkpoint):
         raise TypeError(f"{name} must be a Checkpoint")
     if k.rows != rows or k.c != c:
         raise ValueError(f"{name} holds {k.rows} rows of {k.c} channels, not {rows} of {c}")
-    if k.buf.device != like.device:
-        raise ValueError(f"{name} is on {k.buf.device}, not {like.device}")
-    return k
+    if k.buf.device != device:
+        raise ValueError(f"{name} is on {k.buf.device}, not {device}")
+    return k.buf.data_ptr()
 
 
-def _need_shape(t, shape, like, name):
-    _need(t, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    return t
-
-
-def _opt_shape(t, shape, like, name):
-    return None if t is None else _need_shape(t, shape, like, name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _dims(x, layout):
-    """(n, c, spatial) of an activation."""
-    if layout not in (VAE_NCHW, VAE_NHWC):
-        raise VaeError("layout", -1)
-    n = x.shape[0]
-    c = x.shape[1] if layout == VAE_NCHW else x.shape[-1]
-    return n, c, x.numel() // (n * c) if n * c else 0
-
-
-def _call(name, like, stream, made, *args):
-    """Calls entry point `name` with `args` and the stream, on the device of the
-    tensor `like`. `made`: tensors that were allocated here; they stay with a
-    caller's stream that is not the current one until it has used them."""
+def _first(x, name):
+    """(shape, device) of the tensor the others are compared with."""
     import torch
-    fn = getattr(load_library(), name)
-    dev = like.device
-    current = torch.cuda.current_stream(dev)
-    if stream is None:
-        stream = current
-    elif stream != current:
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        _need(x, name)
+    return x.shape, x.device
+
+
+def _dims(shape, layout):
+    """(n, c, spatial) of an activation."""
+    if len(shape) < 3:
+        raise ValueError("an activation has at least three axes")
+    if layout == VAE_NCHW:
+        n, c, *rest = shape
+    elif layout == VAE_NHWC:
+        n, *rest, c = shape
+    else:
+        raise VaeError("layout", -1)
+    spatial = 1
+    for v in rest:
+        spatial *= v
+    return n, c, spatial
+
+
+def _call(name, device, stream, made, *args):
+    """Calls entry point `name` with `args` and the stream, on `device`. `made`:
+    tensors that were allocated here; they stay with a caller's stream that is
+    not the current one until it has used them."""
+    import torch
+    fn = getattr(_lib, name)
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None and stream.cuda_stream != raw:
+        raw = stream.cuda_stream
         for t in made:
             if t is not None:
                 t.record_stream(stream)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, stream.cuda_stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream.cuda_stream)
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
     if status != 0:
         raise VaeError(name, status)
 
 
-def _ws_for(name, device, *args):
-    nbytes = getattr(load_library(), name)(*args)
-    if nbytes == 0:
-        raise VaeError(name, -2)
-    return _ws(nbytes, device)
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(name, *args):
+    return getattr(load_library(), name)(*args)
+
+
+def _workspace(device, name, *args):
+    """(tensor, address, bytes) of an operator's workspace; Nones when it takes none."""
+    import torch
+    nbytes = _ws_bytes(name, *args)
+    if not nbytes:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), nbytes
 
 
 def vae_ckpt_pack(x, layout=VAE_NHWC, stream=None):
     """A Checkpoint of the activation ``x`` (any number of spatial axes)."""
-    _need(x, "x")
-    n, c, spatial = _dims(x, layout)
-    k = Checkpoint.empty(n * spatial, c, x.device)
-    _call("vae_ckpt_pack", x, stream, (k.buf,), x.data_ptr(), n, c, spatial, layout,
-          k.buf.data_ptr())
+    load_library()
+    shape, dev = _first(x, "x")
+    n, c, spatial = _dims(shape, layout)
+    at = _at(x, shape, dev, "x")
+    k = Checkpoint._make(n * spatial, c, dev)
+    _call("vae_ckpt_pack", dev, stream, (k.buf,), at, n, c, spatial, layout, k.buf.data_ptr())
     return k
 
 
 def vae_ckpt_unpack(ckpt, shape, layout=VAE_NHWC, stream=None):
     """The float32 activation of ``shape`` (in ``layout``) that ``ckpt`` holds."""
     import torch
+    load_library()
     if not isinstance(ckpt, Checkpoint):
         raise TypeError("ckpt must be a Checkpoint")
-    out = torch.empty(shape, dtype=torch.float32, device=ckpt.buf.device)
-    n, c, spatial = _dims(out, layout)
-    _need_ckpt(ckpt, n * spatial, c, out, "ckpt")
-    _call("vae_ckpt_unpack", out, stream, (out,), ckpt.buf.data_ptr(), n, c, spatial, layout,
-          out.data_ptr())
+    n, c, spatial = _dims(shape, layout)
+    dev = ckpt.buf.device
+    at = _ckpt_at(ckpt, n * spatial, c, dev, "ckpt")
+    out = torch.empty(shape, dtype=torch.float32, device=dev)
+    _call("vae_ckpt_unpack", dev, stream, (out,), at, n, c, spatial, layout, out.data_ptr())
     return out
 
 
@@ -603,20 +637,28 @@ def vae_groupnorm_silu_ckpt(x, gamma, beta, groups=32, eps=1e-6, apply_silu=True
     (y, x_ckpt, y_ckpt, stats), a checkpoint None where keep_x / keep_y is
     false, stats [n, groups, 2] (mean, 1 / sqrt(var + eps))."""
     import torch
-    _need(x, "x")
-    n, c, spatial = _dims(x, layout)
-    _need_shape(gamma, (c,), x, "gamma"), _need_shape(beta, (c,), x, "beta")
-    dev = x.device
-    ws = _ws_for("vae_groupnorm_silu_ckpt_workspace_size", dev, n, c, spatial, layout, groups)
-    out = torch.empty_like(x) if out is None else _need_shape(out, x.shape, x, "out")
-    x_ckpt = Checkpoint.empty(n * spatial, c, dev) if keep_x else None
-    y_ckpt = Checkpoint.empty(n * spatial, c, dev) if keep_y else None
-    stats = torch.empty((n, groups, 2), dtype=torch.float32, device=dev)
-    kx, ky = x_ckpt.buf if keep_x else None, y_ckpt.buf if keep_y else None
-    _call("vae_groupnorm_silu_ckpt", x, stream, (ws, out, kx, ky, stats), x.data_ptr(), n, c,
-          spatial, layout, groups, eps, gamma.data_ptr(), beta.data_ptr(), int(apply_silu),
-          out.data_ptr(), _addr(kx), _addr(ky), stats.data_ptr(), ws.data_ptr(), ws.numel())
-    return out, x_ckpt, y_ckpt, stats
+    load_library()
+    shape, dev = _first(x, "x")
+    n, c, spatial = _dims(shape, layout)
+    px = _at(x, shape, dev, "x")
+    pg, pb = _at(gamma, (c,), dev, "gamma"), _at(beta, (c,), dev, "beta")
+    y = torch.empty_like(x) if out is None else out
+    py = y.data_ptr() if out is None else _at(out, shape, dev, "out")
+    ws, pw, nw = _workspace(dev, "vae_groupnorm_silu_ckpt_workspace_size", n, c, spatial, layout,
+                            groups)
+    x_ckpt = y_ckpt = kx = ky = pkx = pky = None
+    if keep_x:
+        x_ckpt = Checkpoint._make(n * spatial, c, dev)
+        kx = x_ckpt.buf
+        pkx = kx.data_ptr()
+    if keep_y:
+        y_ckpt = Checkpoint._make(n * spatial, c, dev)
+        ky = y_ckpt.buf
+        pky = ky.data_ptr()
+    stats = torch.empty((n, max(groups, 1), 2), dtype=torch.float32, device=dev)
+    _call("vae_groupnorm_silu_ckpt", dev, stream, (ws, y, kx, ky, stats), px, n, c, spatial,
+          layout, groups, eps, pg, pb, bool(apply_silu), py, pkx, pky, stats.data_ptr(), pw, nw)
+    return y, x_ckpt, y_ckpt, stats
 
 
 def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply_silu=True,
@@ -624,45 +666,46 @@ def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply
     """(dx, dgamma, dbeta) from dy and what vae_groupnorm_silu_ckpt kept; dres, a
     further gradient of x (the resnet skip's), is added to dx."""
     import torch
-    _need(dy, "dy")
-    n, c, spatial = _dims(dy, layout)
-    _need_ckpt(x_ckpt, n * spatial, c, dy, "x_ckpt")
-    _need_shape(stats, (n, groups, 2), dy, "stats")
-    _need_shape(gamma, (c,), dy, "gamma"), _need_shape(beta, (c,), dy, "beta")
-    _opt_shape(dres, dy.shape, dy, "dres")
-    ws = _ws_for("vae_groupnorm_silu_backward_workspace_size", dy.device, n, c, spatial, layout,
-                 groups)
-    out = torch.empty_like(dy) if out is None else _need_shape(out, dy.shape, dy, "out")
-    grads = torch.empty((2, c), dtype=torch.float32, device=dy.device)
-    dgamma, dbeta = grads.unbind()
-    _call("vae_groupnorm_silu_backward", dy, stream, (ws, out, grads), dy.data_ptr(),
-          x_ckpt.buf.data_ptr(), stats.data_ptr(), n, c, spatial, layout, groups,
-          gamma.data_ptr(), beta.data_ptr(), int(apply_silu), _addr(dres), out.data_ptr(),
-          dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel())
-    return out, dgamma, dbeta
+    load_library()
+    shape, dev = _first(dy, "dy")
+    n, c, spatial = _dims(shape, layout)
+    pd = _at(dy, shape, dev, "dy")
+    pk = _ckpt_at(x_ckpt, n * spatial, c, dev, "x_ckpt")
+    ps = _at(stats, (n, groups, 2), dev, "stats")
+    pg, pb = _at(gamma, (c,), dev, "gamma"), _at(beta, (c,), dev, "beta")
+    pr = _at_opt(dres, shape, dev, "dres")
+    dx = torch.empty_like(dy) if out is None else out
+    px = dx.data_ptr() if out is None else _at(out, shape, dev, "out")
+    ws, pw, nw = _workspace(dev, "vae_groupnorm_silu_backward_workspace_size", n, c, spatial,
+                            layout, groups)
+    dgamma = torch.empty_like(gamma)
+    dbeta = torch.empty_like(beta)
+    _call("vae_groupnorm_silu_backward", dev, stream, (ws, dx, dgamma, dbeta), pd, pk, ps, n, c,
+          spatial, layout, groups, pg, pb, bool(apply_silu), pr, px, dgamma.data_ptr(),
+          dbeta.data_ptr(), pw, nw)
+    return dx, dgamma, dbeta
 
 
 def vae_conv2d_wgrad(dy, x_ckpt, k, layout=VAE_NCHW, stream=None):
     """(dw [cout, cin, k, k], dbias [cout]) of vae_conv2d from its output's
     gradient and the checkpoint of its input."""
     import torch
-    _need(dy, "dy")
-    if dy.dim() != 4:
+    load_library()
+    shape, dev = _first(dy, "dy")
+    if len(shape) != 4:
         raise ValueError("dy must have four axes")
     if layout == VAE_NCHW:
-        n, cout, h, w = dy.shape
+        n, cout, h, w = shape
     else:
-        n, h, w, cout = dy.shape
-    if not isinstance(x_ckpt, Checkpoint):
-        raise TypeError("x_ckpt must be a Checkpoint")
-    cin = x_ckpt.c
-    _need_ckpt(x_ckpt, n * h * w, cin, dy, "x_ckpt")
-    ws = _ws_for("vae_conv2d_wgrad_workspace_size", dy.device, n, cin, h, w, layout, cout, k)
-    dw = torch.empty((cout, cin, k, k), dtype=torch.float32, device=dy.device)
-    dbias = torch.empty(cout, dtype=torch.float32, device=dy.device)
-    _call("vae_conv2d_wgrad", dy, stream, (ws, dw, dbias), dy.data_ptr(), x_ckpt.buf.data_ptr(),
-          n, cin, h, w, layout, cout, k, dw.data_ptr(), dbias.data_ptr(), ws.data_ptr(),
-          ws.numel())
+        n, h, w, cout = shape
+    pd = _at(dy, shape, dev, "dy")
+    cin = getattr(x_ckpt, "c", 0)
+    pk = _ckpt_at(x_ckpt, n * h * w, cin, dev, "x_ckpt")
+    ws, pw, nw = _workspace(dev, "vae_conv2d_wgrad_workspace_size", n, cin, h, w, layout, cout, k)
+    dw = torch.empty((cout, cin, k, k), dtype=torch.float32, device=dev)
+    dbias = torch.empty(cout, dtype=torch.float32, device=dev)
+    _call("vae_conv2d_wgrad", dev, stream, (ws, dw, dbias), pd, pk, n, cin, h, w, layout, cout, k,
+          dw.data_ptr(), dbias.data_ptr(), pw, nw)
     return dw, dbias
 
 
@@ -673,27 +716,35 @@ def vae_block_norm(u, x, w_post, gate=None, scale=None, w_pre=None, eps=1e-6, ke
     (h, y, u_ckpt, h_ckpt, rstd); y and h_ckpt are None without w_pre, and the
     last three None with keep=False (serving)."""
     import torch
-    _need(u, "u")
-    if u.dim() != 3:
+    load_library()
+    shape, dev = _first(u, "u")
+    if len(shape) != 3:
         raise ValueError("u must be [n, tokens, c]")
-    n, tokens, c = u.shape
-    _need_shape(x, u.shape, u, "x"), _need_shape(w_post, (c,), u, "w_post")
-    _opt_shape(gate, (n, c), u, "gate"), _opt_shape(scale, (c,), u, "scale")
-    _opt_shape(w_pre, (c,), u, "w_pre")
-    if out_y is not None and w_pre is None:
-        raise ValueError("out_y without w_pre")
-    dev = u.device
-    h = torch.empty_like(u) if out_h is None else _need_shape(out_h, u.shape, u, "out_h")
-    y = None
+    n, tokens, c = shape
+    pu, px = _at(u, shape, dev, "u"), _at(x, shape, dev, "x")
+    po, pg = _at(w_post, (c,), dev, "w_post"), _at_opt(gate, (n, c), dev, "gate")
+    ps, pp = _at_opt(scale, (c,), dev, "scale"), _at_opt(w_pre, (c,), dev, "w_pre")
+    h = torch.empty_like(u) if out_h is None else out_h
+    ph = h.data_ptr() if out_h is None else _at(out_h, shape, dev, "out_h")
+    y = py = None
     if w_pre is not None:
-        y = torch.empty_like(u) if out_y is None else _need_shape(out_y, u.shape, u, "out_y")
-    u_ckpt = Checkpoint.empty(n * tokens, c, dev) if keep else None
-    h_ckpt = Checkpoint.empty(n * tokens, c, dev) if keep and w_pre is not None else None
-    rstd = torch.empty((2, n * tokens), dtype=torch.float32, device=dev) if keep else None
-    ku, kh = u_ckpt and u_ckpt.buf, h_ckpt and h_ckpt.buf
-    _call("vae_block_norm", u, stream, (h, y, ku, kh, rstd), u.data_ptr(), x.data_ptr(), n,
-          tokens, c, eps, w_post.data_ptr(), _addr(gate), _addr(scale), _addr(w_pre),
-          h.data_ptr(), _addr(y), _addr(ku), _addr(kh), _addr(rstd))
+        y = torch.empty_like(u) if out_y is None else out_y
+        py = y.data_ptr() if out_y is None else _at(out_y, shape, dev, "out_y")
+    elif out_y is not None:
+        raise ValueError("out_y without w_pre")
+    u_ckpt = h_ckpt = rstd = ku = kh = pku = pkh = pr = None
+    if keep:
+        u_ckpt = Checkpoint._make(n * tokens, c, dev)
+        ku = u_ckpt.buf
+        pku = ku.data_ptr()
+        if w_pre is not None:
+            h_ckpt = Checkpoint._make(n * tokens, c, dev)
+            kh = h_ckpt.buf
+            pkh = kh.data_ptr()
+        rstd = torch.empty((2, n * tokens), dtype=torch.float32, device=dev)
+        pr = rstd.data_ptr()
+    _call("vae_block_norm", dev, stream, (h, y, ku, kh, rstd), pu, px, n, tokens, c, eps, po, pg,
+          ps, pp, ph, py, pku, pkh, pr)
     return h, y, u_ckpt, h_ckpt, rstd
 
 
@@ -703,37 +754,31 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
     dscale, dw_pre (None for an absent input). dy is None without w_pre; dh, the
     gradient that reaches h by the residual stream, may be None."""
     import torch
-    like = dh if dy is None else dy
+    load_library()
+    like, name = (dh, "dh") if dy is None else (dy, "dy")
     if like is None:
         raise ValueError("dy and dh are both None")
-    _need(like, "dh" if dy is None else "dy")
-    if like.dim() != 3:
+    shape, dev = _first(like, name)
+    if len(shape) != 3:
         raise ValueError("gradients must be [n, tokens, c]")
-    n, tokens, c = like.shape
-    _opt_shape(dh, like.shape, like, "dh")
     if (dy is None) != (w_pre is None) or (h_ckpt is None) != (w_pre is None):
         raise ValueError("dy and h_ckpt go with w_pre")
-    _need_ckpt(u_ckpt, n * tokens, c, like, "u_ckpt")
-    if h_ckpt is not None:
-        _need_ckpt(h_ckpt, n * tokens, c, like, "h_ckpt")
-    _need_shape(rstd, (2, n * tokens), like, "rstd")
-    _need_shape(w_post, (c,), like, "w_post")
-    _opt_shape(gate, (n, c), like, "gate"), _opt_shape(scale, (c,), like, "scale")
-    _opt_shape(w_pre, (c,), like, "w_pre")
-    dev = like.device
-    ws = _ws_for("vae_block_norm_backward_workspace_size", dev, n, tokens, c,
-                 int(gate is not None))
-    du, dx = torch.empty_like(like), torch.empty_like(like)
-    small = torch.empty((3, c), dtype=torch.float32, device=dev)
-    dw_post, dscale, dw_pre = small.unbind()
-    dscale = None if scale is None else dscale
-    dw_pre = None if w_pre is None else dw_pre
+    n, tokens, c = shape
+    pdy, pdh = _at_opt(dy, shape, dev, "dy"), _at_opt(dh, shape, dev, "dh")
+    pu = _ckpt_at(u_ckpt, n * tokens, c, dev, "u_ckpt")
+    ph = None if h_ckpt is None else _ckpt_at(h_ckpt, n * tokens, c, dev, "h_ckpt")
+    pr, po = _at(rstd, (2, n * tokens), dev, "rstd"), _at(w_post, (c,), dev, "w_post")
+    pg, ps = _at_opt(gate, (n, c), dev, "gate"), _at_opt(scale, (c,), dev, "scale")
+    pp = _at_opt(w_pre, (c,), dev, "w_pre")
+    ws, pw, nw = _workspace(dev, "vae_block_norm_backward_workspace_size", n, tokens, c,
+                            int(gate is not None))
+    du, dx, dw_post = torch.empty_like(like), torch.empty_like(like), torch.empty_like(w_post)
     dgate = None if gate is None else torch.empty_like(gate)
-    _call("vae_block_norm_backward", like, stream, (ws, du, dx, small, dgate), _addr(dy),
-          _addr(dh), u_ckpt.buf.data_ptr(), None if h_ckpt is None else h_ckpt.buf.data_ptr(),
-          rstd.data_ptr(), n, tokens, c, w_post.data_ptr(), _addr(gate), _addr(scale),
-          _addr(w_pre), du.data_ptr(), dx.data_ptr(), dw_post.data_ptr(), _addr(dgate),
-          _addr(dscale), _addr(dw_pre), ws.data_ptr(), ws.numel())
+    dscale = None if scale is None else torch.empty_like(scale)
+    dw_pre = None if w_pre is None else torch.empty_like(w_pre)
+    _call("vae_block_norm_backward", dev, stream, (ws, du, dx, dw_post, dgate, dscale, dw_pre),
+          pdy, pdh, pu, ph, pr, n, tokens, c, po, pg, ps, pp, du.data_ptr(), dx.data_ptr(),
+          dw_post.data_ptr(), _ptr(dgate), _ptr(dscale), _ptr(dw_pre), pw, nw)
     return dict(du=du, dx=dx, dw_post=dw_post, dgate=dgate, dscale=dscale, dw_pre=dw_pre)
 
 

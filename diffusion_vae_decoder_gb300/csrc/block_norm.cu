@@ -103,12 +103,15 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ch = 4 * (i * T + tid);
-      if (KEEP && live && ch < cp) {
+      if (KEEP) {
         uint32_t byte;
-        const uint32_t b = octet_quantise(v[i], octet_mask(), &byte);
-        __stcs(reinterpret_cast<uint32_t *>(ku.q + static_cast<size_t>(row) * cp + ch), b);
-        if ((tid & 7) == 0)
-          ku.scale[static_cast<size_t>(row) * (cp >> 5) + (ch >> 5)] = static_cast<uint8_t>(byte);
+        const uint32_t b = octet_quantise(v[i], &byte);
+        if (live && ch < cp) {
+          __stcs(reinterpret_cast<uint32_t *>(ku.q + static_cast<size_t>(row) * cp + ch), b);
+          if ((tid & 7) == 0)
+            ku.scale[static_cast<size_t>(row) * (cp >> 5) + (ch >> 5)] =
+                static_cast<uint8_t>(byte);
+        }
       }
       const float4 gf = mul4(f[i], g && ch < c ? ld4(g + ch) : one);
       v[i] = fma4(gf, mul4s(v[i], m), xv[i]);
@@ -124,12 +127,15 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ch = 4 * (i * T + tid);
-      if (KEEP && live && ch < cp) {
+      if (KEEP) {
         uint32_t byte;
-        const uint32_t b = octet_quantise(v[i], octet_mask(), &byte);
-        __stcs(reinterpret_cast<uint32_t *>(kh.q + static_cast<size_t>(row) * cp + ch), b);
-        if ((tid & 7) == 0)
-          kh.scale[static_cast<size_t>(row) * (cp >> 5) + (ch >> 5)] = static_cast<uint8_t>(byte);
+        const uint32_t b = octet_quantise(v[i], &byte);
+        if (live && ch < cp) {
+          __stcs(reinterpret_cast<uint32_t *>(kh.q + static_cast<size_t>(row) * cp + ch), b);
+          if ((tid & 7) == 0)
+            kh.scale[static_cast<size_t>(row) * (cp >> 5) + (ch >> 5)] =
+                static_cast<uint8_t>(byte);
+        }
       }
       if (live && ch < c)
         __stcs(reinterpret_cast<float4 *>(y + at + ch), mul4(mul4s(v[i], r), wp[i]));

@@ -14,22 +14,23 @@ __global__ void __launch_bounds__(kThreads)
     pack_rows(const float *__restrict__ x, long long rows, int c, CkptView k) {
   const int cp = (c + 31) & ~31, quads = cp >> 2;
   const long long total = rows * quads;  // a multiple of 8: octets stay whole
-  const uint32_t mask = octet_mask();
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long row = i / quads;
+  for (long long i0 = blockIdx.x * static_cast<long long>(kThreads); i0 < total;
+       i0 += static_cast<long long>(gridDim.x) * kThreads) {
+    const long long i = i0 + threadIdx.x, row = i / quads;
     const int q = static_cast<int>(i - row * quads), ch = 4 * q;
+    const bool in = i < total;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ch + 4 <= c && (c & 3) == 0) {
+    if (in && ch + 4 <= c && (c & 3) == 0) {
       v = __ldcs(reinterpret_cast<const float4 *>(x + row * c + ch));
-    } else {
+    } else if (in) {
       if (ch < c) v.x = x[row * c + ch];
       if (ch + 1 < c) v.y = x[row * c + ch + 1];
       if (ch + 2 < c) v.z = x[row * c + ch + 2];
       if (ch + 3 < c) v.w = x[row * c + ch + 3];
     }
     uint32_t byte;
-    const uint32_t b = octet_quantise(v, mask, &byte);
+    const uint32_t b = octet_quantise(v, &byte);
+    if (!in) continue;
     *reinterpret_cast<uint32_t *>(k.q + row * cp + ch) = b;
     if ((q & 7) == 0) k.scale[row * (cp >> 5) + (q >> 3)] = static_cast<uint8_t>(byte);
   }

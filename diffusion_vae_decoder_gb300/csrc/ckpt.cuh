@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "silu.cuh"
 
 namespace vae {
 
@@ -54,6 +55,12 @@ __device__ __forceinline__ float ckpt_scale(uint32_t byte) {
   return __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// max(|a|, |b|, |c|), NaN when one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // Four values (already times 2^-e) -> four e4m3 bytes, the first lowest.
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
@@ -76,19 +83,62 @@ __device__ __forceinline__ float4 unpack_e4m3x4(uint32_t q, float scale) {
 
 // A block spread over the eight lanes of an aligned octet, four values each:
 // quantises them, returns this lane's four bytes and the block's scale byte.
-// `mask` names the octet's lanes (octet_mask), all of which have to call.
-__device__ __forceinline__ uint32_t octet_mask() { return 0xffu << (threadIdx.x & 24); }
-__device__ __forceinline__ uint32_t octet_max(uint32_t m, uint32_t mask) {
+// Every lane of the warp calls.
+__device__ __forceinline__ uint32_t octet_quantise(float4 v, uint32_t *byte) {
+  float m = max_abs3(max_abs3(v.x, v.y, v.z), v.w, v.w);
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-  return m;
-}
-__device__ __forceinline__ uint32_t octet_quantise(float4 v, uint32_t mask, uint32_t *byte) {
-  const uint32_t m =
-      max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
-  *byte = ckpt_scale_byte(octet_max(m, mask));
+  for (int o = 4; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, m, o);
+    m = max_abs3(m, w, w);
+  }
+  *byte = ckpt_scale_byte(__float_as_uint(m));
   const float inv = ckpt_inv_scale(*byte);
   return pack_e4m3x4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+}
+
+// Eight consecutive channels as packed pairs, for the two-wide FP32 pipe.
+struct Oct {
+  uint64_t v[4];
+};
+__device__ __forceinline__ Oct oct_of(float4 a, float4 b) {
+  return {{pk2(a.x, a.y), pk2(a.z, a.w), pk2(b.x, b.y), pk2(b.z, b.w)}};
+}
+__device__ __forceinline__ float4 oct_lo(const Oct &o) {
+  return make_float4(lo2(o.v[0]), hi2(o.v[0]), lo2(o.v[1]), hi2(o.v[1]));
+}
+__device__ __forceinline__ float4 oct_hi(const Oct &o) {
+  return make_float4(lo2(o.v[2]), hi2(o.v[2]), lo2(o.v[3]), hi2(o.v[3]));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The same for a block spread over four aligned lanes, eight values each.
+__device__ __forceinline__ uint2 quad_quantise(const Oct &x, uint32_t *byte) {
+  float m = max_abs3(lo2(x.v[0]), hi2(x.v[0]), lo2(x.v[1]));
+  m = max_abs3(m, hi2(x.v[1]), lo2(x.v[2]));
+  m = max_abs3(m, hi2(x.v[2]), lo2(x.v[3]));
+  m = max_abs3(m, hi2(x.v[3]), __shfl_xor_sync(0xffffffffu, max_abs3(m, hi2(x.v[3]), m), 1));
+  m = max_abs3(m, m, __shfl_xor_sync(0xffffffffu, m, 2));
+  *byte = ckpt_scale_byte(__float_as_uint(m));
+  const float inv = ckpt_inv_scale(*byte);
+  const uint64_t i2 = pk2(inv, inv);
+  uint64_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q[j] = mul2(x.v[j], i2);
+  return make_uint2(pack_e4m3x4(lo2(q[0]), hi2(q[0]), lo2(q[1]), hi2(q[1])),
+                    pack_e4m3x4(lo2(q[2]), hi2(q[2]), lo2(q[3]), hi2(q[3])));
+}
+__device__ __forceinline__ Oct unpack_oct(uint2 q, float scale) {
+  const uint64_t s2 = pk2(scale, scale);
+  const float2 a = __half22float2(e4m3x2_half2(q.x & 0xffffu));
+  const float2 b = __half22float2(e4m3x2_half2(q.x >> 16));
+  const float2 c = __half22float2(e4m3x2_half2(q.y & 0xffffu));
+  const float2 d = __half22float2(e4m3x2_half2(q.y >> 16));
+  return {{mul2(pk2(a.x, a.y), s2), mul2(pk2(b.x, b.y), s2), mul2(pk2(c.x, c.y), s2),
+           mul2(pk2(d.x, d.y), s2)}};
 }
 
 // Pack / unpack a float tensor (ckpt.cu); x in either layout.

@@ -50,7 +50,7 @@ __host__ __device__ constexpr size_t head_floats(int slab) {
   return static_cast<size_t>(slab) * 9;
 }
 // Scratch of the block's channel sums: a pair per (pixel lane, channel).
-constexpr size_t kRedFloats = kThreads * 4 * 2;
+constexpr size_t kRedFloats = kThreads * 8 * 2;
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t v;
@@ -73,27 +73,30 @@ __device__ __forceinline__ void load_gamma(const ResArgs &a, float4 *aff, int ch
   }
 }
 
-// Channel sums of a block whose threads hold four channels each (quad q of the
+// Channel sums of a block whose threads hold eight channels each (oct o of the
 // slab, pixel lane pl of ppi): out[channel] = (sum s, sum t). Lanes of a warp
-// that share a quad first, then the rows of `red` in order.
-__device__ __forceinline__ void channel_sums(float (&s)[4], float (&t)[4], int slab, int q,
+// that share an oct first, then the rows of `red` in order.
+__device__ __forceinline__ void channel_sums(uint64_t (&s)[4], uint64_t (&t)[4], int slab, int o,
                                              int pl, int ppi, float2 *red, float2 *out) {
-  const int quads = slab >> 2;
-  const bool folds = 32 % quads == 0;
+  const int octs = slab >> 3;
+  const bool folds = 32 % octs == 0;
   int rows = ppi, row = pl;
   if (folds) {
-    for (int o = quads; o < 32; o <<= 1)
+    for (int d = octs; d < 32; d <<= 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-        t[j] += __shfl_xor_sync(0xffffffffu, t[j], o);
+        s[j] = add2(s[j], __shfl_xor_sync(0xffffffffu, s[j], d));
+        t[j] = add2(t[j], __shfl_xor_sync(0xffffffffu, t[j], d));
       }
     rows = kWarps;
     row = threadIdx.x >> 5;
   }
-  if (folds ? (threadIdx.x & 31) < quads : pl < ppi)
+  if (folds ? (threadIdx.x & 31) < octs : pl < ppi)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[row * slab + 4 * q + j] = make_float2(s[j], t[j]);
+    for (int j = 0; j < 4; ++j) {
+      red[row * slab + 8 * o + 2 * j] = make_float2(lo2(s[j]), lo2(t[j]));
+      red[row * slab + 8 * o + 2 * j + 1] = make_float2(hi2(s[j]), hi2(t[j]));
+    }
   __syncthreads();
   for (int ch = threadIdx.x; ch < slab; ch += kThreads) {
     float2 v = red[ch];
@@ -106,6 +109,37 @@ __device__ __forceinline__ void channel_sums(float (&s)[4], float (&t)[4], int s
   }
   __syncthreads();
 }
+
+// The packed affine of eight channels.
+__device__ __forceinline__ Affine8 affine8(const float4 *aff) {
+  Affine8 f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 a = aff[2 * j], b = aff[2 * j + 1];
+    f.nmean[j] = pk2(-a.x, -b.x);
+    f.rstd[j] = pk2(a.y, b.y);
+    f.gamma[j] = pk2(a.z, b.z);
+    f.beta[j] = pk2(a.w, b.w);
+  }
+  return f;
+}
+
+// Where a thread stands in a block's piece of an NHWC tensor.
+struct Piece {
+  int o, pl, ppi, ch, left, count;
+  long long row0;
+  __device__ Piece(const ResArgs &a) {
+    const int octs = a.slab >> 3, ch0 = blockIdx.y * a.slab;
+    ppi = kThreads / octs;
+    o = threadIdx.x % octs;
+    pl = threadIdx.x / octs;
+    ch = ch0 + 8 * o;
+    left = pl < ppi ? a.c - ch : 0;
+    const long long p0 = static_cast<long long>(blockIdx.x) * a.per;
+    count = static_cast<int>(max(0ll, min(static_cast<long long>(a.per), a.spatial - p0)));
+    row0 = blockIdx.z * a.spatial + p0;
+  }
+};
 
 // Merges the group triples of the cluster's blocks (lane r reads rank r's),
 // writes stats and completes the slab's affines. tri: this block's [groups of
@@ -147,6 +181,7 @@ __device__ __forceinline__ void finish_stats(const ResArgs &a, float *tri, float
 }
 
 // grid (cluster, slabs, n).
+template <bool SILU>
 __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
@@ -154,54 +189,39 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
   float2 *sums = reinterpret_cast<float2 *>(sm + 7 * a.slab);
   float2 *red = reinterpret_cast<float2 *>(sm + head_floats(a.slab));
   float4 *data = reinterpret_cast<float4 *>(sm + head_floats(a.slab) + kRedFloats);
+  const Piece pc(a);
   const int n = blockIdx.z, ch0 = blockIdx.y * a.slab, cp = (a.c + 31) & ~31;
-  const int quads = a.slab >> 2, ppi = kThreads / quads;
-  const int q = threadIdx.x % quads, pl = threadIdx.x / quads, ch = ch0 + 4 * q;
-  const bool real = ch < a.c, live = pl < ppi;
-  const long long p0 = static_cast<long long>(blockIdx.x) * a.per;
-  const int count = static_cast<int>(max(0ll, min(static_cast<long long>(a.per), a.spatial - p0)));
-  const long long row0 = n * a.spatial + p0;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   load_gamma(a, aff, ch0);
-  const float *src = a.x + row0 * a.c + ch;
+  const float *src = a.x + pc.row0 * a.c + pc.ch;
   // Sums of deviations from the piece's first pixel (the block's pixel lanes
   // share it, so that they add up).
-  const float4 first =
-      real && count ? __ldg(reinterpret_cast<const float4 *>(src)) : zero;
-  const float k[4] = {first.x, first.y, first.z, first.w};
-  float s[4] = {0, 0, 0, 0}, ss[4] = {0, 0, 0, 0};
-  if (live) {
-    auto add = [&](float4 v) {
-      const float e[4] = {v.x, v.y, v.z, v.w};
+  Oct k = load_oct(src, pc.count ? pc.left : 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float d = e[j] - k[j];
-        s[j] += d;
-        ss[j] = fmaf(d, d, ss[j]);
+  for (int j = 0; j < 4; ++j) k.v[j] = mul2(k.v[j], pk2(-1.f, -1.f));
+  uint64_t s[4] = {0, 0, 0, 0}, ss[4] = {0, 0, 0, 0};
+  if (pc.pl < pc.ppi) {
+    constexpr int U = 4;
+    for (int p = pc.pl, i = threadIdx.x; p < pc.count; p += U * pc.ppi, i += 2 * U * kThreads) {
+      Oct v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[u] = load_oct(src + static_cast<long long>(p + u * pc.ppi) * a.c,
+                        p + u * pc.ppi < pc.count ? pc.left : 0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p + u * pc.ppi >= pc.count) break;
+        data[i + 2 * u * kThreads] = oct_lo(v[u]);
+        data[i + (2 * u + 1) * kThreads] = oct_hi(v[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = add2(v[u].v[j], k.v[j]);
+          s[j] = add2(s[j], d);
+          ss[j] = fma2(d, d, ss[j]);
+        }
       }
-    };
-    int p = pl, i = threadIdx.x;
-    for (; p + 7 * ppi < count; p += 8 * ppi, i += 8 * kThreads) {
-      float4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = real ? __ldcs(reinterpret_cast<const float4 *>(
-                          src + static_cast<long long>(p + u * ppi) * a.c)) : zero;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        data[i + u * kThreads] = v[u];
-        add(v[u]);
-      }
-    }
-    for (; p < count; p += ppi, i += kThreads) {
-      const float4 v =
-          real ? __ldcs(reinterpret_cast<const float4 *>(src + static_cast<long long>(p) * a.c))
-               : zero;
-      data[i] = v;
-      add(v);
     }
   }
-  channel_sums(s, ss, a.slab, q, pl, ppi, red, sums);
+  channel_sums(s, ss, a.slab, pc.o, pc.pl, pc.ppi, red, sums);
   const int cg = a.c / a.groups, g0 = ch0 / cg;
   const int ng = min(a.slab, a.c - ch0) / cg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -209,9 +229,9 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
     Triple t{0.f, 0.f, 0.f};
     for (int i = lane; i < cg; i += 32) {
       const float2 v = sums[g * cg + i];
-      const float m = count ? v.x / count : 0.f;
-      const float shift = count ? __ldg(a.x + row0 * a.c + ch0 + g * cg + i) : 0.f;
-      t = merge(t, Triple{static_cast<float>(count), shift + m, fmaxf(v.y - v.x * m, 0.f)});
+      const float m = pc.count ? v.x / pc.count : 0.f;
+      const float shift = pc.count ? a.x[pc.row0 * a.c + ch0 + g * cg + i] : 0.f;
+      t = merge(t, Triple{static_cast<float>(pc.count), shift + m, fmaxf(v.y - v.x * m, 0.f)});
     }
     t = warp_merge(t);
     if (lane == 0) {
@@ -221,31 +241,30 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
     }
   }
   finish_stats(a, tri, sums, aff, g0, ng, n);
-  if (live) {
-    float4 f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = real ? aff[4 * q + j] : zero;
-    const uint32_t mask = octet_mask();
+  const Affine8 f = affine8(aff + 8 * pc.o);
 #pragma unroll 2
-    for (int p = pl, i = threadIdx.x; p < count; p += ppi, i += kThreads) {
-      const long long row = row0 + p;
-      const float4 v = data[i];
-      float4 o;
-      o.x = act(fmaf((v.x - f[0].x) * f[0].y, f[0].z, f[0].w), a.silu);
-      o.y = act(fmaf((v.y - f[1].x) * f[1].y, f[1].z, f[1].w), a.silu);
-      o.z = act(fmaf((v.z - f[2].x) * f[2].y, f[2].z, f[2].w), a.silu);
-      o.w = act(fmaf((v.w - f[3].x) * f[3].y, f[3].z, f[3].w), a.silu);
-      if (real) __stcs(reinterpret_cast<float4 *>(a.y + row * a.c + ch), o);
-      uint32_t byte;
-      if (a.kx.q) {
-        const uint32_t b = octet_quantise(v, mask, &byte);
-        __stcs(reinterpret_cast<uint32_t *>(a.kx.q + row * cp + ch), b);
-        if ((q & 7) == 0) a.kx.scale[row * (cp >> 5) + (ch >> 5)] = static_cast<uint8_t>(byte);
+  for (int p0 = 0, i = threadIdx.x; p0 < pc.count; p0 += pc.ppi, i += 2 * kThreads) {
+    const long long row = pc.row0 + p0 + pc.pl;
+    const bool in = p0 + pc.pl < pc.count && pc.pl < pc.ppi;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const Oct v = oct_of(in ? data[i] : zero, in ? data[i + kThreads] : zero);
+    const Oct o = forward8<SILU>(v, f);
+    store_oct(a.y + row * a.c + pc.ch, in ? pc.left : 0, o);
+    uint32_t byte;
+    if (a.kx.q) {
+      const uint2 q = quad_quantise(v, &byte);
+      if (in) {
+        __stcs(reinterpret_cast<uint2 *>(a.kx.q + row * cp + pc.ch), q);
+        if ((pc.o & 3) == 0)
+          a.kx.scale[row * (cp >> 5) + (pc.ch >> 5)] = static_cast<uint8_t>(byte);
       }
-      if (a.ky.q) {
-        const uint32_t b = octet_quantise(o, mask, &byte);
-        __stcs(reinterpret_cast<uint32_t *>(a.ky.q + row * cp + ch), b);
-        if ((q & 7) == 0) a.ky.scale[row * (cp >> 5) + (ch >> 5)] = static_cast<uint8_t>(byte);
+    }
+    if (a.ky.q) {
+      const uint2 q = quad_quantise(o, &byte);
+      if (in) {
+        __stcs(reinterpret_cast<uint2 *>(a.ky.q + row * cp + pc.ch), q);
+        if ((pc.o & 3) == 0)
+          a.ky.scale[row * (cp >> 5) + (pc.ch >> 5)] = static_cast<uint8_t>(byte);
       }
     }
   }
@@ -426,6 +445,7 @@ __device__ __forceinline__ void finish_sums(const ResArgs &a, const float2 *mine
   __syncthreads();
 }
 
+template <bool SILU>
 __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
@@ -433,79 +453,74 @@ __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
   float2 *km = reinterpret_cast<float2 *>(sm + 7 * a.slab);
   float2 *red = reinterpret_cast<float2 *>(sm + head_floats(a.slab));
   float4 *data = reinterpret_cast<float4 *>(sm + head_floats(a.slab) + kRedFloats);
+  const Piece pc(a);
   const int n = blockIdx.z, ch0 = blockIdx.y * a.slab, cp = (a.c + 31) & ~31;
-  const int quads = a.slab >> 2, ppi = kThreads / quads;
-  const int q = threadIdx.x % quads, pl = threadIdx.x / quads, ch = ch0 + 4 * q;
-  const bool live = pl < ppi && ch < a.c;
-  const long long p0 = static_cast<long long>(blockIdx.x) * a.per;
-  const int count = static_cast<int>(max(0ll, min(static_cast<long long>(a.per), a.spatial - p0)));
-  const long long row0 = n * a.spatial + p0;
   load_affine(a, aff, n, ch0);
   __syncthreads();
-  float4 f[4];
+  const Affine8 f = affine8(aff + 8 * pc.o);
+  const uint8_t *qs = a.kx.q + pc.row0 * cp + pc.ch,
+                *bs = a.kx.scale + pc.row0 * (cp >> 5) + (pc.ch >> 5);
+  uint64_t s[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
+  if (pc.pl < pc.ppi) {
+    const float *src = a.x + pc.row0 * a.c + pc.ch;
+    constexpr int U = 2;
+    for (int p = pc.pl, i = threadIdx.x; p < pc.count; p += U * pc.ppi, i += 2 * U * kThreads) {
+      Oct g[U];
+      uint2 q[U];
+      uint32_t sb[U];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = aff[4 * q + j];
-  const uint8_t *qs = a.kx.q + row0 * cp + ch, *bs = a.kx.scale + row0 * (cp >> 5) + (ch >> 5);
-  auto value = [&](int p) {
-    return unpack_e4m3x4(
-        __ldg(reinterpret_cast<const uint32_t *>(qs + static_cast<long long>(p) * cp)),
-        ckpt_scale(__ldg(bs + static_cast<long long>(p) * (cp >> 5))));
-  };
-  float s[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
-  if (live) {
-    const float *src = a.x + row0 * a.c + ch;
-    auto add = [&](float4 g, float4 v, int i) {
-      const float gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {v.x, v.y, v.z, v.w};
-      float dz[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float xh;
-        dz[j] = grad_z(gv[j], xv[j], f[j].x, f[j].y, f[j].z, f[j].w, a.silu, &xh);
-        s[j] += dz[j];
-        t[j] = fmaf(dz[j], xh, t[j]);
-      }
-      data[i] = make_float4(dz[0], dz[1], dz[2], dz[3]);
-    };
-    int p = pl, i = threadIdx.x;
-    for (; p + 3 * ppi < count; p += 4 * ppi, i += 4 * kThreads) {
-      float4 g[4], v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        g[u] = __ldcs(reinterpret_cast<const float4 *>(src + static_cast<long long>(p + u * ppi) *
-                                                                 a.c));
-        v[u] = value(p + u * ppi);
+      for (int u = 0; u < U; ++u) {
+        const long long pp = p + u * pc.ppi;
+        const bool in = pp < pc.count;
+        g[u] = load_oct(src + pp * a.c, in ? pc.left : 0);
+        q[u] = in ? __ldg(reinterpret_cast<const uint2 *>(qs + pp * cp)) : make_uint2(0, 0);
+        sb[u] = in ? __ldg(bs + pp * (cp >> 5)) : 0u;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) add(g[u], v[u], i + u * kThreads);
+      for (int u = 0; u < U; ++u) {
+        if (p + u * pc.ppi >= pc.count) break;
+        Oct xh;
+        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+        data[i + 2 * u * kThreads] = oct_lo(dz);
+        data[i + (2 * u + 1) * kThreads] = oct_hi(dz);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[j] = add2(s[j], dz.v[j]);
+          t[j] = fma2(dz.v[j], xh.v[j], t[j]);
+        }
+      }
     }
-    for (; p < count; p += ppi, i += kThreads)
-      add(__ldcs(reinterpret_cast<const float4 *>(src + static_cast<long long>(p) * a.c)),
-          value(p), i);
   }
-  channel_sums(s, t, a.slab, q, pl, ppi, red, mine);
+  channel_sums(s, t, a.slab, pc.o, pc.pl, pc.ppi, red, mine);
   finish_sums(a, mine, km, aff, n, ch0);
-  if (live) {
-    float2 kk[4];
+  if (pc.left > 0) {
+    uint64_t rg[4], k1[4], k2[4];  // dx = rg dz + (k1 + xh k2), both means negated
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kk[j] = km[4 * q + j];
-#pragma unroll 4
-    for (int p = pl, i = threadIdx.x; p < count; p += ppi, i += kThreads) {
-      const float4 v = value(p), z = data[i];
-      const size_t at = (row0 + p) * a.c + ch;
-      const float dz[4] = {z.x, z.y, z.z, z.w}, xv[4] = {v.x, v.y, v.z, v.w};
-      float o[4];
+    for (int j = 0; j < 4; ++j) {
+      const float2 u = km[8 * pc.o + 2 * j], v = km[8 * pc.o + 2 * j + 1];
+      const bool in = 2 * j < pc.left;  // (left is a multiple of four)
+      rg[j] = mul2(f.rstd[j], f.gamma[j]);
+      k1[j] = in ? pk2(-u.x, -v.x) : 0;
+      k2[j] = in ? pk2(-u.y, -v.y) : 0;
+    }
+#pragma unroll 2
+    for (int p = pc.pl, i = threadIdx.x; p < pc.count; p += pc.ppi, i += 2 * kThreads) {
+      const Oct x = unpack_oct(
+          __ldg(reinterpret_cast<const uint2 *>(qs + static_cast<long long>(p) * cp)),
+          ckpt_scale(__ldg(bs + static_cast<long long>(p) * (cp >> 5))));
+      const Oct dz = oct_of(data[i], data[i + kThreads]);
+      const size_t at = (pc.row0 + p) * a.c + pc.ch;
+      Oct o;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o[j] = fmaf(f[j].y * f[j].z, dz[j],
-                    -fmaf((xv[j] - f[j].x) * f[j].y, kk[j].y, kk[j].x));
+        o.v[j] = fma2(rg[j], dz.v[j],
+                      fma2(mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]), k2[j], k1[j]));
       if (a.dres) {
-        const float4 r = __ldcs(reinterpret_cast<const float4 *>(a.dres + at));
-        o[0] += r.x;
-        o[1] += r.y;
-        o[2] += r.z;
-        o[3] += r.w;
+        const Oct r = load_oct(a.dres + at, pc.left);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.v[j] = add2(o.v[j], r.v[j]);
       }
-      __stcs(reinterpret_cast<float4 *>(a.dx + at), make_float4(o[0], o[1], o[2], o[3]));
+      store_oct(a.dx + at, pc.left, o);
     }
   }
   leave();
@@ -517,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) gn_res_bwd_nchw(const ResArgs a) 
   float2 *mine = reinterpret_cast<float2 *>(sm + 4 * a.slab);
   float2 *km = reinterpret_cast<float2 *>(sm + 7 * a.slab);
   float2 *red = reinterpret_cast<float2 *>(sm + head_floats(a.slab));  // [warps][32]
-  float *data = sm + head_floats(a.slab) + kRedFloats;
+  float *data = sm + head_floats(a.slab) + kWarps * 32 * 2;
   const int n = blockIdx.z, ch0 = blockIdx.y * a.slab, cp = (a.c + 31) & ~31;
   const int chans = min(a.slab, a.c - ch0), ld = (a.per + 31) & ~31;
   const long long p0 = static_cast<long long>(blockIdx.x) * a.per;
@@ -602,17 +617,23 @@ int slab_channels(int c, int groups) {
   return l;  // divides c
 }
 
+// Shared memory besides the pixels.
+size_t fixed_bytes(int slab, bool nhwc, bool backward) {
+  const size_t red = nhwc ? kRedFloats : backward ? kWarps * 32 * 2 : 0;
+  return (head_floats(slab) + red) * sizeof(float);
+}
+
 // Blocks of a cluster: as few as fit, up to 8 until the launch has a block per
 // SM or a block under 256 pixels; 16 (not portable) only to fit. 0: no fit.
 int cluster_blocks(int n, int c, long long spatial, int slab, size_t fixed, int *per,
                    size_t *smem, bool nhwc) {
   const int pieces = n * ((c + slab - 1) / slab);
-  const int quads = slab / 4, ppi = kThreads / quads;
+  const int ppi = kThreads / (slab / 8);
   for (int cl = 1; cl <= 16; cl *= 2) {
     const long long pp = (spatial + cl - 1) / cl;
     if (pp > 65536) continue;
     // NHWC: slots of one pixel per pixel lane; NCHW: rows of pixels rounded up to 32
-    const size_t bytes = nhwc ? static_cast<size_t>((pp + ppi - 1) / ppi) * kThreads * 16
+    const size_t bytes = nhwc ? static_cast<size_t>((pp + ppi - 1) / ppi) * kThreads * 32
                               : static_cast<size_t>((pp + 31) / 32 * 32) * slab * 4;
     const size_t total = fixed + bytes;
     if (total > kMaxSmem) continue;
@@ -626,8 +647,9 @@ int cluster_blocks(int n, int c, long long spatial, int slab, size_t fixed, int 
 
 template <class Kernel>
 int launch(Kernel kernel, const ResArgs &a, int cl, int n, size_t smem, cudaStream_t s) {
-  VAE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kMaxSmem)));
+  if (smem > 48 * 1024)
+    VAE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(kMaxSmem)));
   if (cl > 8)
     VAE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   cudaLaunchConfig_t cfg{};
@@ -656,12 +678,21 @@ int launch(Kernel kernel, const ResArgs &a, int cl, int n, size_t smem, cudaStre
 
 }  // namespace
 
+bool gn_resident_surely(int n, int c, long long spatial, int nhwc, int groups, bool backward) {
+  const int slab = slab_channels(c, groups);
+  int per = 0;
+  size_t smem = 0;
+  const int cl = cluster_blocks(n, c, spatial, slab, fixed_bytes(slab, nhwc, backward), &per,
+                                &smem, nhwc);
+  return cl > 0 && cl <= 8;
+}
+
 int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, int groups,
                      float eps, const float *gamma, const float *beta, int silu, float *y,
                      CkptView kx, CkptView ky, float *stats, cudaStream_t s) {
   ResArgs a{};
   a.slab = slab_channels(c, groups);
-  const size_t fixed = (head_floats(a.slab) + (nhwc ? kRedFloats : 0)) * sizeof(float);
+  const size_t fixed = fixed_bytes(a.slab, nhwc, false);
   size_t smem = 0;
   const int cl = cluster_blocks(n, c, spatial, a.slab, fixed, &a.per, &smem, nhwc);
   if (!cl) return VAE_EUNSUPPORTED;
@@ -677,7 +708,7 @@ int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, 
   a.eps = eps;
   a.y = y;
   a.stats = reinterpret_cast<float2 *>(stats);
-  return nhwc ? launch(gn_res_fwd_nhwc, a, cl, n, smem, s)
+  return nhwc ? launch(silu ? gn_res_fwd_nhwc<true> : gn_res_fwd_nhwc<false>, a, cl, n, smem, s)
               : launch(gn_res_fwd_nchw, a, cl, n, smem, s);
 }
 
@@ -687,7 +718,7 @@ int gn_backward_resident(const float *dy, CkptView kx, const float *stats, int n
                          float *dgamma, float *dbeta, float2 *sums, cudaStream_t s) {
   ResArgs a{};
   a.slab = slab_channels(c, groups);
-  const size_t fixed = (head_floats(a.slab) + kRedFloats) * sizeof(float);
+  const size_t fixed = fixed_bytes(a.slab, nhwc, true);
   size_t smem = 0;
   const int cl = cluster_blocks(n, c, spatial, a.slab, fixed, &a.per, &smem, nhwc);
   if (!cl) return VAE_EUNSUPPORTED;
@@ -705,7 +736,7 @@ int gn_backward_resident(const float *dy, CkptView kx, const float *stats, int n
   a.dgamma = dgamma;
   a.dbeta = dbeta;
   a.sums = n > 1 ? sums : nullptr;
-  return nhwc ? launch(gn_res_bwd_nhwc, a, cl, n, smem, s)
+  return nhwc ? launch(silu ? gn_res_bwd_nhwc<true> : gn_res_bwd_nhwc<false>, a, cl, n, smem, s)
               : launch(gn_res_bwd_nchw, a, cl, n, smem, s);
 }
 

@@ -15,12 +15,14 @@
 // pass and backwards by the second, and outputs are stored evict-first, so
 // that the second pass finds in L2 what the first one read last.
 //
-// NHWC: a thread owns four channels; the eight lanes of a 32-channel block
-// share its scale by shuffles. NCHW: a thread owns one pixel and 32 channels,
+// NHWC: a thread owns eight channels, in packed pairs (these sweeps are bound
+// by issued instructions before HBM); the four lanes of a 32-channel block share
+// its scale by shuffles. NCHW: a thread owns one pixel and 32 channels,
 // so every load and store of the planes is coalesced over pixels and a
 // checkpoint block is one thread's registers.
 #include "gn_stats.cuh"
 #include "gn_train.cuh"
+#include "ptx.cuh"
 
 namespace vae {
 
@@ -34,7 +36,7 @@ constexpr int kMergeThreads = 512;
 
 // Blocks (slabs of pixels) per sample.
 int slabs_nhwc(int n, int c, long long spatial) {
-  const int ppi = kThreads / (ckpt_cp(c) / 4);
+  const int ppi = kThreads / (ckpt_cp(c) / 8);
   const long long most = std::max(1, kBlocks / n);
   return static_cast<int>(std::max(1ll, std::min(most, spatial / (4 * ppi))));
 }
@@ -83,65 +85,123 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
 }
 
-// ------------------------------------------------------------- forward apply
-// grid (slabs, n).
-__global__ void __launch_bounds__(kThreads, 4)
-    ckpt_apply_nhwc(const float *x, int c, long long spatial, int groups,
-                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
-                    const float *__restrict__ beta, int silu, float *y, CkptView kx,
-                    CkptView ky) {
-  const int cp = (c + 31) & ~31, quads = cp >> 2, ppi = kThreads / quads;
-  const int q = threadIdx.x % quads, pl = threadIdx.x / quads;
-  if (pl >= ppi) return;
-  const int n = blockIdx.y, ch = 4 * q, cg = c / groups;
-  const bool real = ch < c;  // (c is a multiple of four)
-  float mean[4], rstd[4], ga[4], be[4];
+// ------------------------------------------------------------- NHWC pieces
+// A thread owns channels 8 o .. 8 o + 7 of every ppi-th pixel of its block's
+// slab. Its 32-byte loads run kDepth - 1 pixels ahead into shared memory slots
+// that it alone uses (no barriers; registers hold no loads in flight). Offsets
+// count from the slab's first pixel and fit 32 bits. Blocks are walked by whole
+// iterations, so that every lane takes part in the shuffles of a checkpoint
+// block.
+constexpr int kDepth = 4;
+constexpr uint32_t kSlotBytes = kThreads * 32;
+
+struct Slab {
+  int o, pl, ppi, ch, left, len, iters;
+  long long row0;  // the slab's first pixel
+  __device__ Slab(int c, long long spatial) {
+    const int octs = ((c + 31) & ~31) >> 3;
+    ppi = kThreads / octs;
+    o = threadIdx.x % octs;
+    pl = threadIdx.x / octs;
+    ch = 8 * o;
+    left = pl < ppi ? c - ch : 0;
+    const long long p0 = spatial * blockIdx.x / gridDim.x;
+    len = static_cast<int>(spatial * (blockIdx.x + 1) / gridDim.x - p0);
+    row0 = static_cast<long long>(blockIdx.y) * spatial + p0;
+    iters = (len + ppi - 1) / ppi;
+  }
+};
+
+// Copies eight channels (those below `left`, else zeros) at `src`.
+__device__ __forceinline__ void fetch_oct(uint32_t slot, const float *base, uint32_t off,
+                                          int left) {
+  const float *src = base + (left > 0 ? off : 0u);
+  cp_async16(slot + threadIdx.x * 16, src, left > 0);
+  cp_async16(slot + kThreads * 16 + threadIdx.x * 16, left > 4 ? src + 4 : base, left > 4);
+}
+__device__ __forceinline__ Oct slot_oct(const float4 *slot) {
+  return oct_of(slot[threadIdx.x], slot[kThreads + threadIdx.x]);
+}
+
+__device__ __forceinline__ Affine8 load_affine8(const Slab &sl, int c, int groups,
+                                                const float2 *__restrict__ stats,
+                                                const float *__restrict__ gamma,
+                                                const float *__restrict__ beta) {
+  const int cg = c / groups;
+  float m[8], r[8], ga[8], be[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool in = j < sl.left;
+    const float2 st = in ? stats[blockIdx.y * groups + (sl.ch + j) / cg] : make_float2(0.f, 0.f);
+    m[j] = -st.x;
+    r[j] = st.y;
+    ga[j] = in ? gamma[sl.ch + j] : 0.f;
+    be[j] = in ? beta[sl.ch + j] : 0.f;
+  }
+  Affine8 f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 st = real ? stats[n * groups + (ch + j) / cg] : make_float2(0.f, 0.f);
-    mean[j] = st.x;
-    rstd[j] = st.y;
-    ga[j] = real ? gamma[ch + j] : 0.f;
-    be[j] = real ? beta[ch + j] : 0.f;
+    f.nmean[j] = pk2(m[2 * j], m[2 * j + 1]);
+    f.rstd[j] = pk2(r[2 * j], r[2 * j + 1]);
+    f.gamma[j] = pk2(ga[2 * j], ga[2 * j + 1]);
+    f.beta[j] = pk2(be[2 * j], be[2 * j + 1]);
   }
-  const uint32_t mask = octet_mask();
-  const long long p0 = spatial * blockIdx.x / gridDim.x,
-                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
-  const long long row0 = static_cast<long long>(n) * spatial;
-  auto load = [&](long long p) {
-    return real ? __ldcs(reinterpret_cast<const float4 *>(x + (row0 + p) * c + ch))
-                : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  auto one = [&](long long p, float4 v) {
-    const long long row = row0 + p;
-    float4 o;
-    o.x = act(fmaf((v.x - mean[0]) * rstd[0], ga[0], be[0]), silu);
-    o.y = act(fmaf((v.y - mean[1]) * rstd[1], ga[1], be[1]), silu);
-    o.z = act(fmaf((v.z - mean[2]) * rstd[2], ga[2], be[2]), silu);
-    o.w = act(fmaf((v.w - mean[3]) * rstd[3], ga[3], be[3]), silu);
-    if (real) __stcs(reinterpret_cast<float4 *>(y + row * c + ch), o);
-    uint32_t byte;
-    if (kx.q) {
-      const uint32_t b = octet_quantise(v, mask, &byte);
-      __stcs(reinterpret_cast<uint32_t *>(kx.q + row * cp + ch), b);
-      if ((q & 7) == 0) kx.scale[row * (cp >> 5) + (q >> 3)] = static_cast<uint8_t>(byte);
-    }
-    if (ky.q) {
-      const uint32_t b = octet_quantise(o, mask, &byte);
-      __stcs(reinterpret_cast<uint32_t *>(ky.q + row * cp + ch), b);
-      if ((q & 7) == 0) ky.scale[row * (cp >> 5) + (q >> 3)] = static_cast<uint8_t>(byte);
-    }
-  };
-  // from the slab's end to its start, four loads in flight
-  long long p = p1 - 1 - pl;
-  for (; p - 3 * ppi >= p0; p -= 4 * ppi) {
-    float4 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = load(p - u * ppi);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) one(p - u * ppi, v[u]);
+  return f;
+}
+
+// k: the checkpoint from the slab's first row on.
+__device__ __forceinline__ void keep_oct(CkptView k, uint32_t pix, int cp, int ch, bool in,
+                                         const Oct &v) {
+  uint32_t byte;
+  const uint2 q = quad_quantise(v, &byte);
+  if (!in) return;
+  __stcs(reinterpret_cast<uint2 *>(k.q + (pix * cp + ch)), q);
+  if ((ch & 31) == 0) k.scale[pix * (cp >> 5) + (ch >> 5)] = static_cast<uint8_t>(byte);
+}
+__device__ __forceinline__ CkptView from_row(CkptView k, long long row, int cp) {
+  if (k.q) {
+    k.q += row * cp;
+    k.scale += row * (cp >> 5);
   }
-  for (; p >= p0; p -= ppi) one(p, load(p));
+  return k;
+}
+
+// ------------------------------------------------------------- forward apply
+// grid (slabs, n). From the slab's end to its start.
+template <bool SILU>
+__global__ void __launch_bounds__(kThreads, 2)
+    ckpt_apply_nhwc(const float *x, int c, long long spatial, int groups,
+                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                    const float *__restrict__ beta, float *y, CkptView kx, CkptView ky) {
+  extern __shared__ __align__(16) float4 slots[];
+  const Slab sl(c, spatial);
+  const int cp = (c + 31) & ~31;
+  const Affine8 f = load_affine8(sl, c, groups, stats, gamma, beta);
+  const uint32_t slot0 = smem_u32(slots);
+  x += sl.row0 * c;
+  y += sl.row0 * c;
+  kx = from_row(kx, sl.row0, cp);
+  ky = from_row(ky, sl.row0, cp);
+  auto fetch = [&](int i) {
+    const int p = sl.len - 1 - sl.pl - i * sl.ppi;
+    fetch_oct(slot0 + (i % kDepth) * kSlotBytes, x, static_cast<uint32_t>(p) * c + sl.ch,
+              i < sl.iters && p >= 0 ? sl.left : 0);
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+#pragma unroll 1
+  for (int i = 0; i < sl.iters; ++i) {
+    fetch(i + kDepth - 1);
+    cp_async_wait<kDepth - 1>();
+    const Oct v = slot_oct(slots + (i % kDepth) * (kSlotBytes / 16));
+    const int p = sl.len - 1 - sl.pl - i * sl.ppi;
+    const bool in = p >= 0 && sl.pl < sl.ppi;
+    const Oct o = forward8<SILU>(v, f);
+    store_oct(y + (static_cast<uint32_t>(p) * c + sl.ch), in ? sl.left : 0, o);
+    if (kx.q) keep_oct(kx, p, cp, sl.ch, in, v);
+    if (ky.q) keep_oct(ky, p, cp, sl.ch, in, o);
+  }
 }
 
 // Per-channel constants of a 32-channel block, in shared memory: (mean, rstd,
@@ -193,72 +253,72 @@ __global__ void __launch_bounds__(kPixThreads)
 
 // ------------------------------------------------------------- backward
 // Per-(slab, channel) sums of dz and dz xh: part [n][slabs][c] float2. grid (slabs, n).
-__global__ void __launch_bounds__(kThreads, 4)
+template <bool SILU>
+__global__ void __launch_bounds__(kThreads, 2)
     ckpt_sums_nhwc(const float *__restrict__ dy, CkptView k, int c, long long spatial, int groups,
                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
-                   const float *__restrict__ beta, int silu, float2 *__restrict__ part) {
-  __shared__ float2 red[kThreads * 4];
-  const int cp = (c + 31) & ~31, quads = c >> 2, ppi = kThreads / quads;
-  const int q = threadIdx.x % quads, pl = threadIdx.x / quads;
-  const int n = blockIdx.y, ch = 4 * q, cg = c / groups;
-  float a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
-  if (pl < ppi) {
-    float mean[4], rstd[4], ga[4], be[4];
+                   const float *__restrict__ beta, float2 *__restrict__ part) {
+  extern __shared__ __align__(16) float4 slots[];
+  float2 *red = reinterpret_cast<float2 *>(slots);  // after the sweep
+  const Slab sl(c, spatial);
+  const int cp = (c + 31) & ~31;
+  uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  if (sl.pl < sl.ppi) {
+    const Affine8 f = load_affine8(sl, c, groups, stats, gamma, beta);
+    const float *src = dy + sl.row0 * c;
+    const CkptView kv = from_row(k, sl.row0, cp);
+    const uint32_t slot0 = smem_u32(slots);
+    uint2 q[kDepth];
+    uint32_t sb[kDepth];
+    auto fetch = [&](int i, int u) {
+      const int p = sl.pl + i * sl.ppi;
+      const bool in = p < sl.len;
+      fetch_oct(slot0 + u * kSlotBytes, src, static_cast<uint32_t>(p) * c + sl.ch,
+                in ? sl.left : 0);
+      cp_async_commit();
+      q[u] = make_uint2(0, 0);
+      sb[u] = 0;
+      if (in) {
+        q[u] = __ldg(reinterpret_cast<const uint2 *>(
+            kv.q + (static_cast<uint32_t>(p) * cp + sl.ch)));
+        sb[u] = __ldg(kv.scale + (static_cast<uint32_t>(p) * (cp >> 5) + (sl.ch >> 5)));
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kDepth - 1; ++u) fetch(u, u);
+#pragma unroll 1
+    for (int i = 0; i < sl.iters; i += kDepth)
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) {  // (a pixel outside has dy = 0 and adds nothing)
+        fetch(i + u + kDepth - 1, (u + kDepth - 1) % kDepth);
+        cp_async_wait<kDepth - 1>();
+        Oct xh;
+        const Oct dz = grad8<SILU>(slot_oct(slots + u * (kSlotBytes / 16)),
+                                   unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j] = add2(a[j], dz.v[j]);
+          b[j] = fma2(dz.v[j], xh.v[j], b[j]);
+        }
+      }
+    cp_async_wait<0>();
+  }
+  __syncthreads();  // every slot has been read
+  if (sl.pl < sl.ppi) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 st = stats[n * groups + (ch + j) / cg];
-      mean[j] = st.x;
-      rstd[j] = st.y;
-      ga[j] = gamma[ch + j];
-      be[j] = beta[ch + j];
+      red[sl.pl * cp + sl.ch + 2 * j] = make_float2(lo2(a[j]), lo2(b[j]));
+      red[sl.pl * cp + sl.ch + 2 * j + 1] = make_float2(hi2(a[j]), hi2(b[j]));
     }
-    const long long p0 = spatial * blockIdx.x / gridDim.x,
-                    p1 = spatial * (blockIdx.x + 1) / gridDim.x;
-    const long long row0 = static_cast<long long>(n) * spatial;
-    auto add = [&](float4 g, uint32_t w, uint32_t byte) {
-      const float4 v = unpack_e4m3x4(w, ckpt_scale(byte));
-      const float gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float xh;
-        const float dz = grad_z(gv[j], xv[j], mean[j], rstd[j], ga[j], be[j], silu, &xh);
-        a[j] += dz;
-        b[j] = fmaf(dz, xh, b[j]);
-      }
-    };
-    auto ld_g = [&](long long p) {
-      return __ldg(reinterpret_cast<const float4 *>(dy + (row0 + p) * c + ch));
-    };
-    auto ld_q = [&](long long p) {
-      return __ldg(reinterpret_cast<const uint32_t *>(k.q + (row0 + p) * cp + ch));
-    };
-    auto ld_s = [&](long long p) {
-      return static_cast<uint32_t>(__ldg(k.scale + (row0 + p) * (cp >> 5) + (q >> 3)));
-    };
-    long long p = p0 + pl;
-    for (; p + 3 * ppi < p1; p += 4 * ppi) {
-      float4 g[4];
-      uint32_t w[4], sb[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        g[u] = ld_g(p + u * ppi);
-        w[u] = ld_q(p + u * ppi);
-        sb[u] = ld_s(p + u * ppi);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) add(g[u], w[u], sb[u]);
-    }
-    for (; p < p1; p += ppi) add(ld_g(p), ld_q(p), ld_s(p));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) red[pl * c + ch + j] = make_float2(a[j], b[j]);
   }
   __syncthreads();
-  float2 *o = part + (static_cast<size_t>(n) * gridDim.x + blockIdx.x) * c;
+  float2 *o = part + (static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * c;
   for (int i = threadIdx.x; i < c; i += kThreads) {
     float2 t = red[i];
-    for (int l = 1; l < ppi; ++l) {
-      t.x += red[l * c + i].x;
-      t.y += red[l * c + i].y;
+#pragma unroll 8
+    for (int l = 1; l < sl.ppi; ++l) {
+      t.x += red[l * cp + i].x;
+      t.y += red[l * cp + i].y;
     }
     o[i] = t;
   }
@@ -379,74 +439,72 @@ __device__ __forceinline__ void group_means(float2 *km, const float2 *__restrict
 }
 
 // grid (slabs, n).
-__global__ void __launch_bounds__(kThreads, 4)
+template <bool SILU>
+__global__ void __launch_bounds__(kThreads, 2)
     ckpt_dx_nhwc(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
-                 const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
+                 const float *__restrict__ beta, const float2 *__restrict__ sums,
                  const float *dres, float *dx) {
+  extern __shared__ __align__(16) float4 slots[];
   __shared__ float2 km[1024];
-  const int cp = (c + 31) & ~31, quads = c >> 2, ppi = kThreads / quads;
-  const int q = threadIdx.x % quads, pl = threadIdx.x / quads;
-  const int n = blockIdx.y, ch = 4 * q, cg = c / groups;
-  group_means(km, sums, n, c, groups, spatial, stats, gamma, 0, groups);
-  if (pl >= ppi) return;
-  float mean[4], rstd[4], ga[4], be[4], k1[4], k2[4];
+  const Slab sl(c, spatial);
+  const int cp = (c + 31) & ~31, cg = c / groups;
+  group_means(km, sums, blockIdx.y, c, groups, spatial, stats, gamma, 0, groups);
+  if (sl.pl >= sl.ppi) return;
+  const Affine8 f = load_affine8(sl, c, groups, stats, gamma, beta);
+  // dx = rg dz + (k1 + xh k2), rg = rstd gamma, with both means negated
+  uint64_t rg[4], k1[4], k2[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int g = (ch + j) / cg;
-    const float2 st = stats[n * groups + g];
-    mean[j] = st.x;
-    rstd[j] = st.y;
-    ga[j] = gamma[ch + j];
-    be[j] = beta[ch + j];
-    k1[j] = km[g].x;
-    k2[j] = km[g].y;
+    const float2 u = 2 * j < sl.left ? km[(sl.ch + 2 * j) / cg] : make_float2(0.f, 0.f);
+    const float2 v = 2 * j + 1 < sl.left ? km[(sl.ch + 2 * j + 1) / cg] : make_float2(0.f, 0.f);
+    rg[j] = mul2(f.rstd[j], f.gamma[j]);
+    k1[j] = pk2(-u.x, -v.x);
+    k2[j] = pk2(-u.y, -v.y);
   }
-  const long long p0 = spatial * blockIdx.x / gridDim.x,
-                  p1 = spatial * (blockIdx.x + 1) / gridDim.x;
-  const long long row0 = static_cast<long long>(n) * spatial;
-  auto one = [&](long long p, float4 g, uint32_t w, uint32_t byte, float4 r) {
-    const float4 v = unpack_e4m3x4(w, ckpt_scale(byte));
-    const float gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {v.x, v.y, v.z, v.w};
-    const float rv[4] = {r.x, r.y, r.z, r.w};
-    float o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float xh;
-      const float dz = grad_z(gv[j], xv[j], mean[j], rstd[j], ga[j], be[j], silu, &xh);
-      o[j] = fmaf(rstd[j] * ga[j], dz, -fmaf(xh, k2[j], k1[j])) + rv[j];
+  dy += sl.row0 * c;
+  dx += sl.row0 * c;
+  if (dres) dres += sl.row0 * c;
+  const CkptView kv = from_row(k, sl.row0, cp);
+  const uint32_t slot0 = smem_u32(slots);
+  uint2 q[kDepth];
+  uint32_t sb[kDepth];
+  auto fetch = [&](int i, int u) {
+    const int p = sl.len - 1 - sl.pl - i * sl.ppi;
+    const bool in = p >= 0;
+    fetch_oct(slot0 + u * kSlotBytes, dy, static_cast<uint32_t>(p) * c + sl.ch,
+              in ? sl.left : 0);
+    cp_async_commit();
+    q[u] = make_uint2(0, 0);
+    sb[u] = 0;
+    if (in) {
+      q[u] = __ldcs(reinterpret_cast<const uint2 *>(
+          kv.q + (static_cast<uint32_t>(p) * cp + sl.ch)));
+      sb[u] = __ldg(kv.scale + (static_cast<uint32_t>(p) * (cp >> 5) + (sl.ch >> 5)));
     }
-    __stcs(reinterpret_cast<float4 *>(dx + (row0 + p) * c + ch),
-           make_float4(o[0], o[1], o[2], o[3]));
   };
-  auto ld_g = [&](long long p) {
-    return __ldcs(reinterpret_cast<const float4 *>(dy + (row0 + p) * c + ch));
-  };
-  auto ld_r = [&](long long p) {
-    return dres ? __ldcs(reinterpret_cast<const float4 *>(dres + (row0 + p) * c + ch))
-                : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  auto ld_q = [&](long long p) {
-    return __ldcs(reinterpret_cast<const uint32_t *>(k.q + (row0 + p) * cp + ch));
-  };
-  auto ld_s = [&](long long p) {
-    return static_cast<uint32_t>(__ldg(k.scale + (row0 + p) * (cp >> 5) + (q >> 3)));
-  };
-  long long p = p1 - 1 - pl;
-  for (; p - ppi >= p0; p -= 2 * ppi) {
-    float4 g[2], r[2];
-    uint32_t w[2], sb[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      g[u] = ld_g(p - u * ppi);
-      w[u] = ld_q(p - u * ppi);
-      sb[u] = ld_s(p - u * ppi);
-      r[u] = ld_r(p - u * ppi);
+  for (int u = 0; u < kDepth - 1; ++u) fetch(u, u);
+#pragma unroll 1
+  for (int i = 0; i < sl.iters; i += kDepth)
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      const int p = sl.len - 1 - sl.pl - (i + u) * sl.ppi;
+      const uint32_t at = static_cast<uint32_t>(p) * c + sl.ch;
+      Oct xh, o, r;
+      if (dres) r = load_oct(dres + (p >= 0 ? at : 0u), p >= 0 ? sl.left : 0);
+      fetch(i + u + kDepth - 1, (u + kDepth - 1) % kDepth);
+      cp_async_wait<kDepth - 1>();
+      const Oct dz = grad8<SILU>(slot_oct(slots + u * (kSlotBytes / 16)),
+                                 unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o.v[j] = fma2(rg[j], dz.v[j], fma2(xh.v[j], k2[j], k1[j]));
+        if (dres) o.v[j] = add2(o.v[j], r.v[j]);
+      }
+      store_oct(dx + at, p >= 0 ? sl.left : 0, o);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) one(p - u * ppi, g[u], w[u], sb[u], r[u]);
-  }
-  for (; p >= p0; p -= ppi) one(p, ld_g(p), ld_q(p), ld_s(p), ld_r(p));
+  cp_async_wait<0>();
 }
 
 // grid (slabs, cp / 32, n).
@@ -512,13 +570,14 @@ CkptWs carve_backward(Carver &cv, int n, int c, long long spatial) {
 
 }  // namespace
 
-size_t gn_ckpt_ws_bytes(int n, int c, long long spatial, int groups) {
+size_t gn_ckpt_ws_bytes(int n, int c, long long spatial, int nhwc, int groups) {
+  if (gn_resident_surely(n, c, spatial, nhwc, groups, false)) return 0;
   Carver cv(nullptr, 0);
   carve_forward(cv, n, c, spatial, groups);
   return cv.used;
 }
-size_t gn_backward_ws_bytes(int n, int c, long long spatial, int groups) {
-  (void)groups;
+size_t gn_backward_ws_bytes(int n, int c, long long spatial, int nhwc, int groups) {
+  if (n == 1 && gn_resident_surely(n, c, spatial, nhwc, groups, true)) return 0;
   Carver cv(nullptr, 0);
   carve_backward(cv, n, c, spatial);
   return cv.used;
@@ -547,8 +606,9 @@ int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int group
   ckpt_stats_merge<<<ng, slabs > 128 ? kMergeThreads : 128, 0, s>>>(w.part, slabs, eps, st);
   VAE_LAUNCH_CHECK();
   if (nhwc)
-    ckpt_apply_nhwc<<<dim3(slabs, n), kThreads, 0, s>>>(x, c, spatial, groups, st, gamma, beta,
-                                                        silu, y, kx, ky);
+    (silu ? ckpt_apply_nhwc<true> : ckpt_apply_nhwc<false>)<<<dim3(slabs, n), kThreads, kDepth * kSlotBytes,
+                                                                s>>>(
+        x, c, spatial, groups, st, gamma, beta, y, kx, ky);
   else
     ckpt_apply_nchw<<<dim3(slabs_nchw(n, c, spatial), ckpt_cp(c) / 32, n), kPixThreads, 0, s>>>(
         x, c, spatial, groups, st, gamma, beta, silu, y, kx, ky);
@@ -576,8 +636,8 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   const int slabs = nhwc ? slabs_nhwc(n, c, spatial) : slabs_nchw(n, c, spatial);
   const dim3 grid = nhwc ? dim3(slabs, n) : dim3(slabs, ckpt_cp(c) / 32, n);
   if (nhwc)
-    ckpt_sums_nhwc<<<grid, kThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
-                                             part);
+    (silu ? ckpt_sums_nhwc<true> : ckpt_sums_nhwc<false>)<<<grid, kThreads, kDepth * kSlotBytes, s>>>(
+        dy, k, c, spatial, groups, st, gamma, beta, part);
   else
     ckpt_sums_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
                                                 part);
@@ -585,8 +645,8 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   ckpt_sums_merge<<<ckpt_cp(c) / 32, 1024, 0, s>>>(part, n, slabs, c, w.sums, dgamma, dbeta);
   VAE_LAUNCH_CHECK();
   if (nhwc)
-    ckpt_dx_nhwc<<<grid, kThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
-                                           w.sums, dres, dx);
+    (silu ? ckpt_dx_nhwc<true> : ckpt_dx_nhwc<false>)<<<grid, kThreads, kDepth * kSlotBytes, s>>>(
+        dy, k, c, spatial, groups, st, gamma, beta, w.sums, dres, dx);
   else
     ckpt_dx_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
                                               w.sums, dres, dx);

@@ -6,9 +6,10 @@
 
 namespace vae {
 
-// Room for the statistics, their partials and the per-channel sums.
-size_t gn_ckpt_ws_bytes(int n, int c, long long spatial, int groups);
-size_t gn_backward_ws_bytes(int n, int c, long long spatial, int groups);
+// Room for the partial statistics and the per-channel sums; 0 where one launch
+// of clusters needs none.
+size_t gn_ckpt_ws_bytes(int n, int c, long long spatial, int nhwc, int groups);
+size_t gn_backward_ws_bytes(int n, int c, long long spatial, int nhwc, int groups);
 
 // y = act(GroupNorm(x)); stats [n][groups] (mean, 1 / sqrt(var + eps));
 // x_ckpt / y_ckpt: views with q == nullptr are not written.
@@ -25,6 +26,8 @@ int gn_backward(const float *dy, CkptView x_ckpt, const float *stats, int n, int
 // slab) on chip between the reduction and the elementwise pass
 // (gn_resident.cu); VAE_EUNSUPPORTED, with nothing launched, for slabs that do
 // not fit.
+// Whether that is certain for these sizes (clusters of at most 8 blocks).
+bool gn_resident_surely(int n, int c, long long spatial, int nhwc, int groups, bool backward);
 int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, int groups,
                      float eps, const float *gamma, const float *beta, int silu, float *y,
                      CkptView x_ckpt, CkptView y_ckpt, float *stats, cudaStream_t s);
@@ -77,6 +80,61 @@ __device__ __forceinline__ float grad_z(float dy, float xv, float mean, float rs
   const float z = fmaf(*xh, ga, be);
   const float s = __fdividef(1.0f, 1.0f + __expf(-z));
   return dy * (s * fmaf(z, 1.0f - s, 1.0f));
+}
+
+// Eight channels of a pixel, packed. negated means and logarithms' constants
+// are folded so that each step is one two-wide operation.
+struct Affine8 {
+  uint64_t nmean[4], rstd[4], gamma[4], beta[4];
+};
+__device__ __forceinline__ uint64_t rcp2(uint64_t a) {
+  float x, y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(lo2(a)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(hi2(a)));
+  return pk2(x, y);
+}
+// 1 / (1 + e^-z), from the exp2 and reciprocal units (a few units in the last
+// place; e^-z overflows to infinity for z < -88, whose reciprocal is 0).
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+  const uint64_t t = mul2(z, pk2(-1.4426950408889634f, -1.4426950408889634f));
+  return rcp2(add2(pk2(ex2_approx(lo2(t)), ex2_approx(hi2(t))), pk2(1.f, 1.f)));
+}
+template <bool SILU>
+__device__ __forceinline__ Oct forward8(const Oct &x, const Affine8 &f) {
+  Oct o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t z = fma2(mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]), f.gamma[j], f.beta[j]);
+    o.v[j] = SILU ? mul2(z, sigmoid2(z)) : z;
+  }
+  return o;
+}
+// dz of eight elements; xh receives the normalised inputs.
+template <bool SILU>
+__device__ __forceinline__ Oct grad8(const Oct &dy, const Oct &x, const Affine8 &f, Oct *xh) {
+  Oct o;
+  const uint64_t one = pk2(1.f, 1.f), minus = pk2(-1.f, -1.f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    xh->v[j] = mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]);
+    o.v[j] = dy.v[j];
+    if (SILU) {
+      const uint64_t z = fma2(xh->v[j], f.gamma[j], f.beta[j]);
+      const uint64_t s = sigmoid2(z);
+      o.v[j] = mul2(dy.v[j], mul2(s, fma2(z, fma2(s, minus, one), one)));
+    }
+  }
+  return o;
+}
+// Loads eight channels; those past c (a multiple of four) are zeros.
+__device__ __forceinline__ Oct load_oct(const float *p, int left) {
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  return oct_of(left > 0 ? __ldcs(reinterpret_cast<const float4 *>(p)) : zero,
+                left > 4 ? __ldcs(reinterpret_cast<const float4 *>(p) + 1) : zero);
+}
+__device__ __forceinline__ void store_oct(float *p, int left, const Oct &o) {
+  if (left > 0) __stcs(reinterpret_cast<float4 *>(p), oct_lo(o));
+  if (left > 4) __stcs(reinterpret_cast<float4 *>(p) + 1, oct_hi(o));
 }
 
 // Sums of 32 values over a warp, value j to lane j: 31 shuffles; each step

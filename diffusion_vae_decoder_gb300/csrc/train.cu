@@ -18,6 +18,13 @@ bool all_aligned(T... p) {
 constexpr long long kMaxRows = 0x7fffffffll;  // pixels or tokens of one call
 constexpr int kMaxSamples = 65535;            // a grid dimension
 
+// A workspace of `need` bytes (none: ws may be NULL).
+int workspace_ok(const void *ws, size_t ws_bytes, size_t need) {
+  if (!need) return VAE_OK;
+  if (!ws) return VAE_EINVAL;
+  return ws_bytes < need ? VAE_EWORKSPACE : VAE_OK;
+}
+
 int act_args_ok(int n, int c, long long spatial, int layout) {
   if (n <= 0 || c <= 0 || spatial <= 0) return VAE_EINVAL;
   if (layout != VAE_NCHW && layout != VAE_NHWC) return VAE_EINVAL;
@@ -84,17 +91,17 @@ int vae_ckpt_unpack(const void *ckpt, int n, int c, long long spatial, int layou
 size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long spatial, int layout,
                                               int groups) {
   return gn_args_ok(n, c, spatial, layout, groups) == VAE_OK
-             ? gn_ckpt_ws_bytes(n, c, spatial, groups) : 0;
+             ? gn_ckpt_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups) : 0;
 }
 
 int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,
                             int groups, float eps, const float *gamma, const float *beta,
                             int apply_silu, float *y, void *x_ckpt, void *y_ckpt, float *stats,
                             void *ws, size_t ws_bytes, vae_stream_t stream) {
-  if (!x || !gamma || !beta || !y || !stats || !ws) return VAE_EINVAL;
+  if (!x || !gamma || !beta || !y || !stats) return VAE_EINVAL;
   VAE_TRY(gn_args_ok(n, c, spatial, layout, groups));
   if (!all_aligned(x, y, x_ckpt, y_ckpt, stats, ws)) return VAE_EINVAL;
-  if (ws_bytes < gn_ckpt_ws_bytes(n, c, spatial, groups)) return VAE_EWORKSPACE;
+  VAE_TRY(workspace_ok(ws, ws_bytes, gn_ckpt_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups)));
   const long long rows = n * spatial;
   return gn_ckpt(x, n, c, spatial, layout == VAE_NHWC, groups, eps, gamma, beta, apply_silu != 0,
                  y, ckpt_view(x_ckpt, rows, c), ckpt_view(y_ckpt, rows, c), stats, ws,
@@ -104,7 +111,7 @@ int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int
 size_t vae_groupnorm_silu_backward_workspace_size(int n, int c, long long spatial, int layout,
                                                   int groups) {
   return gn_args_ok(n, c, spatial, layout, groups) == VAE_OK
-             ? gn_backward_ws_bytes(n, c, spatial, groups) : 0;
+             ? gn_backward_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups) : 0;
 }
 
 int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, const float *stats, int n,
@@ -112,10 +119,11 @@ int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, const float
                                 const float *gamma, const float *beta, int apply_silu,
                                 const float *dres, float *dx, float *dgamma, float *dbeta,
                                 void *ws, size_t ws_bytes, vae_stream_t stream) {
-  if (!dy || !x_ckpt || !stats || !gamma || !beta || !dx || !ws) return VAE_EINVAL;
+  if (!dy || !x_ckpt || !stats || !gamma || !beta || !dx) return VAE_EINVAL;
   VAE_TRY(gn_args_ok(n, c, spatial, layout, groups));
   if (!all_aligned(dy, x_ckpt, stats, dres, dx, ws)) return VAE_EINVAL;
-  if (ws_bytes < gn_backward_ws_bytes(n, c, spatial, groups)) return VAE_EWORKSPACE;
+  VAE_TRY(workspace_ok(ws, ws_bytes,
+                       gn_backward_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups)));
   return gn_backward(dy, ckpt_view(x_ckpt, n * spatial, c), stats, n, c, spatial,
                      layout == VAE_NHWC, groups, gamma, beta, apply_silu != 0, dres, dx, dgamma,
                      dbeta, ws, reinterpret_cast<cudaStream_t>(stream));

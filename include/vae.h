@@ -457,8 +457,9 @@ VAE_API int vae_ckpt_unpack(const void *ckpt, int n, int c, long long spatial, i
  * 1x1 shortcut's weight gradient) and of y (for the weight gradient of the
  * conv that follows), either NULL when not wanted, and
  *   stats [n][groups][2]: mean, 1 / sqrt(var + eps)
- * y == x is allowed. Limits of vae_groupnorm_silu, and n <= 65535,
- * n * spatial < 2^31. */
+ * y == x is allowed. A workspace size of 0 for valid sizes (here and in the
+ * backward pass: small tensors) means that ws is not used and may be NULL.
+ * Limits of vae_groupnorm_silu, and n <= 65535, n * spatial < 2^31. */
 VAE_API size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long spatial, int layout,
                                                       int groups);
 VAE_API int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,

@@ -611,6 +611,7 @@ def test_nothing_is_written_behind_the_outputs():
 
     y, kx, ky, st = floats(rows * c), kept(), kept(), floats(2 * n * groups)
     size = lib.vae_groupnorm_silu_ckpt_workspace_size(n, c, h * w, 1, groups)
+    assert size == 0  # the guard then has to stay untouched from its first byte
     ws = workspace(size)
     assert lib.vae_groupnorm_silu_ckpt(
         x.data_ptr(), n, c, h * w, 1, groups, 1e-6, ga.data_ptr(), be.data_ptr(), 1, y.data_ptr(),

@@ -46,13 +46,13 @@ def test_pack_and_unpack_refuse(lib, fn, args, status):
     assert getattr(lib, fn)(*args, None) == status
 
 
-def gn_fwd(lib, x=P, n=1, c=64, sp=64, lay=1, g=32, ga=P, be=P, y=P, kx=P, ky=P, st=P, ws=P,
+def gn_fwd(lib, x=P, n=1, c=64, sp=1 << 20, lay=1, g=32, ga=P, be=P, y=P, kx=P, ky=P, st=P, ws=P,
            nb=BIG):
     return lib.vae_groupnorm_silu_ckpt(x, n, c, sp, lay, g, 1e-6, ga, be, 1, y, kx, ky, st, ws,
                                        nb, None)
 
 
-def gn_bwd(lib, dy=P, kx=P, st=P, n=1, c=64, sp=64, lay=1, g=32, ga=P, be=P, res=None, dx=P,
+def gn_bwd(lib, dy=P, kx=P, st=P, n=1, c=64, sp=1 << 20, lay=1, g=32, ga=P, be=P, res=None, dx=P,
            ws=P, nb=BIG):
     return lib.vae_groupnorm_silu_backward(dy, kx, st, n, c, sp, lay, g, ga, be, 1, res, dx, P, P,
                                            ws, nb, None)
@@ -136,9 +136,11 @@ def test_block_norm_backward_refuses(lib, kw, status):
 def test_workspace_sizes(lib):
     assert lib.vae_conv2d_wgrad_workspace_size(1, 128, 64, 64, 1, 128, 3) > 0
     assert lib.vae_conv2d_wgrad_workspace_size(1, 128, 64, 64, 1, 128, 2) == 0
-    assert lib.vae_groupnorm_silu_ckpt_workspace_size(1, 64, 64, 1, 32) > 0
+    assert lib.vae_groupnorm_silu_ckpt_workspace_size(1, 64, 1 << 20, 1, 32) > 0
+    assert lib.vae_groupnorm_silu_ckpt_workspace_size(1, 64, 64, 1, 32) == 0  # none is used
     assert lib.vae_groupnorm_silu_ckpt_workspace_size(1, 64, 64, 1, 24) == 0
-    assert lib.vae_groupnorm_silu_backward_workspace_size(1, 64, 64, 0, 32) > 0
+    assert lib.vae_groupnorm_silu_backward_workspace_size(1, 64, 1 << 20, 0, 32) > 0
+    assert lib.vae_groupnorm_silu_backward_workspace_size(2, 64, 64, 0, 32) > 0
     assert lib.vae_groupnorm_silu_backward_workspace_size(1, 64, 0, 0, 32) == 0
     one = lib.vae_block_norm_backward_workspace_size(1, 4096, 512, 0)
     assert 0 < one and lib.vae_block_norm_backward_workspace_size(0, 4096, 512, 0) == 0
