@@ -181,7 +181,7 @@ __device__ __forceinline__ void finish_stats(const ResArgs &a, float *tri, float
 }
 
 // grid (cluster, slabs, n).
-template <bool SILU>
+template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
   const float *src = a.x + pc.row0 * a.c + pc.ch;
   // Sums of deviations from the piece's first pixel (the block's pixel lanes
   // share it, so that they add up).
-  Oct k = load_oct(src, pc.count ? pc.left : 0);
+  Oct k = load_oct<WIDE, true>(src, pc.count ? pc.left : 0);
 #pragma unroll
   for (int j = 0; j < 4; ++j) k.v[j] = mul2(k.v[j], pk2(-1.f, -1.f));
   uint64_t s[4] = {0, 0, 0, 0}, ss[4] = {0, 0, 0, 0};
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
       Oct v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = load_oct(src + static_cast<long long>(p + u * pc.ppi) * a.c,
+        v[u] = load_oct<WIDE, true>(src + static_cast<long long>(p + u * pc.ppi) * a.c,
                         p + u * pc.ppi < pc.count ? pc.left : 0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     const Oct v = oct_of(in ? data[i] : zero, in ? data[i + kThreads] : zero);
     const Oct o = forward8<SILU>(v, f);
-    store_oct(a.y + row * a.c + pc.ch, in ? pc.left : 0, o);
+    store_oct<WIDE>(a.y + row * a.c + pc.ch, in ? pc.left : 0, o);
     uint32_t byte;
     if (a.kx.q) {
       const uint2 q = quad_quantise(v, &byte);
@@ -445,7 +445,7 @@ __device__ __forceinline__ void finish_sums(const ResArgs &a, const float2 *mine
   __syncthreads();
 }
 
-template <bool SILU>
+template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
       for (int u = 0; u < U; ++u) {
         const long long pp = p + u * pc.ppi;
         const bool in = pp < pc.count;
-        g[u] = load_oct(src + pp * a.c, in ? pc.left : 0);
+        g[u] = load_oct<WIDE, true>(src + pp * a.c, in ? pc.left : 0);
         q[u] = in ? __ldg(reinterpret_cast<const uint2 *>(qs + pp * cp)) : make_uint2(0, 0);
         sb[u] = in ? __ldg(bs + pp * (cp >> 5)) : 0u;
       }
@@ -516,11 +516,11 @@ __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
         o.v[j] = fma2(rg[j], dz.v[j],
                       fma2(mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]), k2[j], k1[j]));
       if (a.dres) {
-        const Oct r = load_oct(a.dres + at, pc.left);
+        const Oct r = load_oct<WIDE, true>(a.dres + at, pc.left);
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.v[j] = add2(o.v[j], r.v[j]);
       }
-      store_oct(a.dx + at, pc.left, o);
+      store_oct<WIDE>(a.dx + at, pc.left, o);
     }
   }
   leave();
@@ -708,8 +708,11 @@ int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, 
   a.eps = eps;
   a.y = y;
   a.stats = reinterpret_cast<float2 *>(stats);
-  return nhwc ? launch(silu ? gn_res_fwd_nhwc<true> : gn_res_fwd_nhwc<false>, a, cl, n, smem, s)
-              : launch(gn_res_fwd_nchw, a, cl, n, smem, s);
+  if (!nhwc) return launch(gn_res_fwd_nchw, a, cl, n, smem, s);
+  return launch(wide_ok(c, x, y) ? (silu ? gn_res_fwd_nhwc<true, true> : gn_res_fwd_nhwc<false, true>)
+                                 : (silu ? gn_res_fwd_nhwc<true, false>
+                                         : gn_res_fwd_nhwc<false, false>),
+                a, cl, n, smem, s);
 }
 
 int gn_backward_resident(const float *dy, CkptView kx, const float *stats, int n, int c,
@@ -736,8 +739,11 @@ int gn_backward_resident(const float *dy, CkptView kx, const float *stats, int n
   a.dgamma = dgamma;
   a.dbeta = dbeta;
   a.sums = n > 1 ? sums : nullptr;
-  return nhwc ? launch(silu ? gn_res_bwd_nhwc<true> : gn_res_bwd_nhwc<false>, a, cl, n, smem, s)
-              : launch(gn_res_bwd_nchw, a, cl, n, smem, s);
+  if (!nhwc) return launch(gn_res_bwd_nchw, a, cl, n, smem, s);
+  const bool wide = dres ? wide_ok(c, dy, dx, dres) : wide_ok(c, dy, dx);
+  return launch(wide ? (silu ? gn_res_bwd_nhwc<true, true> : gn_res_bwd_nhwc<false, true>)
+                     : (silu ? gn_res_bwd_nhwc<true, false> : gn_res_bwd_nhwc<false, false>),
+                a, cl, n, smem, s);
 }
 
 }  // namespace vae

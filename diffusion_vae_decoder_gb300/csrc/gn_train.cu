@@ -10,10 +10,10 @@
 //   dx = rstd (gamma dz - mean_g(gamma dz) - xh mean_g(gamma dz xh)) (+ dres)
 //
 // Both need a sum over the whole (sample, group) before the first output
-// element, so both are a reducing pass, a small merge and an elementwise pass
-// over the same slabs of pixels. The slabs are walked forwards by the first
-// pass and backwards by the second, and outputs are stored evict-first, so
-// that the second pass finds in L2 what the first one read last.
+// element, so both are a reducing pass, a small merge and an elementwise pass.
+// The first walks the pixels forwards, the second backwards, and outputs are
+// stored evict-first, so that the second pass finds in L2 what the first one
+// read last.
 //
 // NHWC: a thread owns eight channels, in packed pairs (these sweeps are bound
 // by issued instructions before HBM); the four lanes of a 32-channel block share
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;      // NHWC kernels
 constexpr int kPixThreads = 128;   // NCHW kernels: one pixel per thread
-constexpr int kBlocks = 4 * 152;   // NHWC: blocks of a launch, about four per SM
+constexpr int kBlocks = 2 * 152;   // NHWC: the resident blocks, two per SM
 constexpr int kPixBlocks = 8 * 152;
 constexpr int kMergeThreads = 512;
 
@@ -50,13 +50,6 @@ int slabs_stats_nchw(int ng, long long seg) {
 }
 
 // ------------------------------------------------------------- statistics
-__global__ void __launch_bounds__(kStatThreads)
-    ckpt_stats_nhwc(const float *__restrict__ x, int c, long long spatial, int groups,
-                    float *__restrict__ part) {
-  extern __shared__ float sm[];
-  stats_slab_nhwc(x, c, spatial, groups, gridDim.x, blockIdx.y, blockIdx.x, sm, part);
-}
-
 __global__ void __launch_bounds__(kStatThreads)
     ckpt_stats_nchw(const float *__restrict__ x, int c, long long spatial, int groups,
                     float *__restrict__ part) {
@@ -86,44 +79,117 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 // ------------------------------------------------------------- NHWC pieces
-// A thread owns channels 8 o .. 8 o + 7 of every ppi-th pixel of its block's
-// slab. Its 32-byte loads run kDepth - 1 pixels ahead into shared memory slots
-// that it alone uses (no barriers; registers hold no loads in flight). Offsets
-// count from the slab's first pixel and fit 32 bits. Blocks are walked by whole
-// iterations, so that every lane takes part in the shuffles of a checkpoint
-// block.
-constexpr int kDepth = 4;
-constexpr uint32_t kSlotBytes = kThreads * 32;
+// A thread owns channels 8 o .. 8 o + 7 of its pixels; at any time the grid
+// works on one contiguous run of pixels. Blocks are walked by whole iterations,
+// so that every lane takes part in the shuffles of a checkpoint block.
 
-struct Slab {
-  int o, pl, ppi, ch, left, len, iters;
-  long long row0;  // the slab's first pixel
-  __device__ Slab(int c, long long spatial) {
+struct Sweep {
+  int o, pl, ppi, ch, left, iters;
+  unsigned first, step, spatial;
+  long long row0;  // the sample's first pixel
+  __device__ Sweep(int c, long long pixels) {
     const int octs = ((c + 31) & ~31) >> 3;
     ppi = kThreads / octs;
     o = threadIdx.x % octs;
     pl = threadIdx.x / octs;
     ch = 8 * o;
     left = pl < ppi ? c - ch : 0;
-    const long long p0 = spatial * blockIdx.x / gridDim.x;
-    len = static_cast<int>(spatial * (blockIdx.x + 1) / gridDim.x - p0);
-    row0 = static_cast<long long>(blockIdx.y) * spatial + p0;
-    iters = (len + ppi - 1) / ppi;
+    spatial = static_cast<unsigned>(pixels);  // (below 2^31)
+    first = blockIdx.x * ppi + pl;
+    step = gridDim.x * ppi;
+    iters = static_cast<int>((spatial + step - 1) / step);
+    row0 = static_cast<long long>(blockIdx.y) * pixels;
   }
+  __device__ unsigned pixel(int i) const { return first + static_cast<unsigned>(i) * step; }
+  __device__ bool in(int i, unsigned p) const { return i >= 0 && i < iters && p < spatial; }
 };
 
-// Copies eight channels (those below `left`, else zeros) at `src`.
-__device__ __forceinline__ void fetch_oct(uint32_t slot, const float *base, uint32_t off,
-                                          int left) {
-  const float *src = base + (left > 0 ? off : 0u);
-  cp_async16(slot + threadIdx.x * 16, src, left > 0);
-  cp_async16(slot + kThreads * 16 + threadIdx.x * 16, left > 4 ? src + 4 : base, left > 4);
-}
-__device__ __forceinline__ Oct slot_oct(const float4 *slot) {
-  return oct_of(slot[threadIdx.x], slot[kThreads + threadIdx.x]);
+// base + p * stride, one 32 x 32 -> 64 bit multiply-add.
+template <class T>
+__device__ __forceinline__ T *row_at(T *base, unsigned p, unsigned stride) {
+  return base + static_cast<unsigned long long>(p) * stride;
 }
 
-__device__ __forceinline__ Affine8 load_affine8(const Slab &sl, int c, int groups,
+// Statistics: part [n][groups][gridDim.x] triples. Sums of deviations from the
+// block's first pixel, which its pixel lanes share.
+template <bool WIDE>
+__global__ void __launch_bounds__(kThreads, 2)
+    ckpt_stats_nhwc(const float *__restrict__ x, int c, long long spatial, int groups,
+                    float *__restrict__ part) {
+  __shared__ float2 red[kThreads * 8];
+  const Sweep sw(c, spatial);
+  const int cp = (c + 31) & ~31;
+  x += sw.row0 * c;
+  const unsigned origin = blockIdx.x * sw.ppi;  // (every block has a pixel)
+  const float *src = x + sw.ch;
+  Oct k = load_oct<WIDE, false>(row_at(src, origin, c), sw.left);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k.v[j] = mul2(k.v[j], pk2(-1.f, -1.f));
+  uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  if (sw.pl < sw.ppi) {
+    constexpr int U = 6;
+#pragma unroll 1
+    for (int i = 0; i < sw.iters; i += U) {
+      Oct v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const unsigned p = sw.pixel(i + u);
+        v[u] = load_oct<WIDE, false>(row_at(src, p, c), sw.in(i + u, p) ? sw.left : 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (sw.in(i + u, sw.pixel(i + u))) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t d = add2(v[u].v[j], k.v[j]);
+            a[j] = add2(a[j], d);
+            b[j] = fma2(d, d, b[j]);
+          }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      red[sw.pl * cp + sw.ch + 2 * j] = make_float2(lo2(a[j]), lo2(b[j]));
+      red[sw.pl * cp + sw.ch + 2 * j + 1] = make_float2(hi2(a[j]), hi2(b[j]));
+    }
+  }
+  __syncthreads();
+  // pixels of the block: a full ppi per iteration but for the last
+  const unsigned last = (sw.iters - 1) * sw.step + origin;
+  const float total = static_cast<float>(
+      static_cast<long long>(sw.iters - 1) * sw.ppi +
+      (last < sw.spatial ? min(static_cast<unsigned>(sw.ppi), sw.spatial - last) : 0u));
+  for (int i = threadIdx.x; i < c; i += kThreads) {
+    float2 t = red[i];
+#pragma unroll 8
+    for (int l = 1; l < sw.ppi; ++l) {
+      t.x += red[l * cp + i].x;
+      t.y += red[l * cp + i].y;
+    }
+    red[i] = t;  // (column i is this thread's)
+  }
+  __syncthreads();
+  const int cg = c / groups, lane = threadIdx.x & 31;
+  for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
+    Triple t{0.f, 0.f, 0.f};
+    for (int i = lane; i < cg; i += 32) {
+      const float2 v = red[g * cg + i];
+      const float m = v.x / total;
+      t = merge(t, Triple{total, row_at(x, origin, c)[g * cg + i] + m,
+                          fmaxf(v.y - v.x * m, 0.f)});
+    }
+    t = warp_merge(t);
+    if (lane == 0) {
+      float *o =
+          part + ((static_cast<size_t>(blockIdx.y) * groups + g) * gridDim.x + blockIdx.x) * 3;
+      o[0] = t.n;
+      o[1] = t.mean;
+      o[2] = t.m2;
+    }
+  }
+}
+
+__device__ __forceinline__ Affine8 load_affine8(const Sweep &sw, int c, int groups,
                                                 const float2 *__restrict__ stats,
                                                 const float *__restrict__ gamma,
                                                 const float *__restrict__ beta) {
@@ -131,12 +197,12 @@ __device__ __forceinline__ Affine8 load_affine8(const Slab &sl, int c, int group
   float m[8], r[8], ga[8], be[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const bool in = j < sl.left;
-    const float2 st = in ? stats[blockIdx.y * groups + (sl.ch + j) / cg] : make_float2(0.f, 0.f);
+    const bool in = j < sw.left;
+    const float2 st = in ? stats[blockIdx.y * groups + (sw.ch + j) / cg] : make_float2(0.f, 0.f);
     m[j] = -st.x;
     r[j] = st.y;
-    ga[j] = in ? gamma[sl.ch + j] : 0.f;
-    be[j] = in ? beta[sl.ch + j] : 0.f;
+    ga[j] = in ? gamma[sw.ch + j] : 0.f;
+    be[j] = in ? beta[sw.ch + j] : 0.f;
   }
   Affine8 f;
 #pragma unroll
@@ -149,14 +215,14 @@ __device__ __forceinline__ Affine8 load_affine8(const Slab &sl, int c, int group
   return f;
 }
 
-// k: the checkpoint from the slab's first row on.
-__device__ __forceinline__ void keep_oct(CkptView k, uint32_t pix, int cp, int ch, bool in,
+// k: the checkpoint from the sample's first row on.
+__device__ __forceinline__ void keep_oct(CkptView k, unsigned p, int cp, int ch, bool in,
                                          const Oct &v) {
   uint32_t byte;
   const uint2 q = quad_quantise(v, &byte);
   if (!in) return;
-  __stcs(reinterpret_cast<uint2 *>(k.q + (pix * cp + ch)), q);
-  if ((ch & 31) == 0) k.scale[pix * (cp >> 5) + (ch >> 5)] = static_cast<uint8_t>(byte);
+  __stcs(reinterpret_cast<uint2 *>(row_at(k.q + ch, p, cp)), q);
+  if ((ch & 31) == 0) *row_at(k.scale + (ch >> 5), p, cp >> 5) = static_cast<uint8_t>(byte);
 }
 __device__ __forceinline__ CkptView from_row(CkptView k, long long row, int cp) {
   if (k.q) {
@@ -167,40 +233,37 @@ __device__ __forceinline__ CkptView from_row(CkptView k, long long row, int cp) 
 }
 
 // ------------------------------------------------------------- forward apply
-// grid (slabs, n). From the slab's end to its start.
-template <bool SILU>
+// grid (blocks, n). From the end to the start.
+template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
     ckpt_apply_nhwc(const float *x, int c, long long spatial, int groups,
                     const float2 *__restrict__ stats, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float *y, CkptView kx, CkptView ky) {
-  extern __shared__ __align__(16) float4 slots[];
-  const Slab sl(c, spatial);
+  const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
-  const Affine8 f = load_affine8(sl, c, groups, stats, gamma, beta);
-  const uint32_t slot0 = smem_u32(slots);
-  x += sl.row0 * c;
-  y += sl.row0 * c;
-  kx = from_row(kx, sl.row0, cp);
-  ky = from_row(ky, sl.row0, cp);
-  auto fetch = [&](int i) {
-    const int p = sl.len - 1 - sl.pl - i * sl.ppi;
-    fetch_oct(slot0 + (i % kDepth) * kSlotBytes, x, static_cast<uint32_t>(p) * c + sl.ch,
-              i < sl.iters && p >= 0 ? sl.left : 0);
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+  const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
+  const float *src = x + sw.row0 * c + sw.ch;
+  float *dst = y + sw.row0 * c + sw.ch;
+  kx = from_row(kx, sw.row0, cp);
+  ky = from_row(ky, sw.row0, cp);
+  constexpr int U = 4;
 #pragma unroll 1
-  for (int i = 0; i < sl.iters; ++i) {
-    fetch(i + kDepth - 1);
-    cp_async_wait<kDepth - 1>();
-    const Oct v = slot_oct(slots + (i % kDepth) * (kSlotBytes / 16));
-    const int p = sl.len - 1 - sl.pl - i * sl.ppi;
-    const bool in = p >= 0 && sl.pl < sl.ppi;
-    const Oct o = forward8<SILU>(v, f);
-    store_oct(y + (static_cast<uint32_t>(p) * c + sl.ch), in ? sl.left : 0, o);
-    if (kx.q) keep_oct(kx, p, cp, sl.ch, in, v);
-    if (ky.q) keep_oct(ky, p, cp, sl.ch, in, o);
+  for (int top = sw.iters - 1; top >= 0; top -= U) {
+    Oct v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned p = sw.pixel(top - u);
+      v[u] = load_oct<WIDE, true>(row_at(src, p, c), sw.in(top - u, p) ? sw.left : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned p = sw.pixel(top - u);
+      const bool in = sw.in(top - u, p) && sw.pl < sw.ppi;
+      if (kx.q) keep_oct(kx, p, cp, sw.ch, in, v[u]);
+      const Oct o = forward8<SILU>(v[u], f);
+      store_oct<WIDE>(row_at(dst, p, c), in ? sw.left : 0, o);
+      if (ky.q) keep_oct(ky, p, cp, sw.ch, in, o);
+    }
   }
 }
 
@@ -253,62 +316,52 @@ __global__ void __launch_bounds__(kPixThreads)
 
 // ------------------------------------------------------------- backward
 // Per-(slab, channel) sums of dz and dz xh: part [n][slabs][c] float2. grid (slabs, n).
-template <bool SILU>
+template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
     ckpt_sums_nhwc(const float *__restrict__ dy, CkptView k, int c, long long spatial, int groups,
                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
                    const float *__restrict__ beta, float2 *__restrict__ part) {
-  extern __shared__ __align__(16) float4 slots[];
-  float2 *red = reinterpret_cast<float2 *>(slots);  // after the sweep
-  const Slab sl(c, spatial);
+  __shared__ float2 red[kThreads * 8];
+  const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
   uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
-  if (sl.pl < sl.ppi) {
-    const Affine8 f = load_affine8(sl, c, groups, stats, gamma, beta);
-    const float *src = dy + sl.row0 * c;
-    const CkptView kv = from_row(k, sl.row0, cp);
-    const uint32_t slot0 = smem_u32(slots);
-    uint2 q[kDepth];
-    uint32_t sb[kDepth];
-    auto fetch = [&](int i, int u) {
-      const int p = sl.pl + i * sl.ppi;
-      const bool in = p < sl.len;
-      fetch_oct(slot0 + u * kSlotBytes, src, static_cast<uint32_t>(p) * c + sl.ch,
-                in ? sl.left : 0);
-      cp_async_commit();
-      q[u] = make_uint2(0, 0);
-      sb[u] = 0;
-      if (in) {
-        q[u] = __ldg(reinterpret_cast<const uint2 *>(
-            kv.q + (static_cast<uint32_t>(p) * cp + sl.ch)));
-        sb[u] = __ldg(kv.scale + (static_cast<uint32_t>(p) * (cp >> 5) + (sl.ch >> 5)));
-      }
-    };
-#pragma unroll
-    for (int u = 0; u < kDepth - 1; ++u) fetch(u, u);
+  if (sw.pl < sw.ppi) {
+    const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
+    const float *src = dy + sw.row0 * c + sw.ch;
+    const CkptView kv = from_row(k, sw.row0, cp);
+    constexpr int U = 3;
 #pragma unroll 1
-    for (int i = 0; i < sl.iters; i += kDepth)
+    for (int i = 0; i < sw.iters; i += U) {
+      Oct g[U];
+      uint2 q[U];
+      uint32_t sb[U];
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u) {  // (a pixel outside has dy = 0 and adds nothing)
-        fetch(i + u + kDepth - 1, (u + kDepth - 1) % kDepth);
-        cp_async_wait<kDepth - 1>();
+      for (int u = 0; u < U; ++u) {
+        const unsigned p = sw.pixel(i + u);
+        const bool in = sw.in(i + u, p);
+        g[u] = load_oct<WIDE, false>(row_at(src, p, c), in ? sw.left : 0);
+        q[u] = make_uint2(0, 0);
+        sb[u] = 0;
+        if (in) {
+          q[u] = __ldg(reinterpret_cast<const uint2 *>(row_at(kv.q + sw.ch, p, cp)));
+          sb[u] = __ldg(row_at(kv.scale + (sw.ch >> 5), p, cp >> 5));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {  // (a pixel outside has dy = 0 and adds nothing)
         Oct xh;
-        const Oct dz = grad8<SILU>(slot_oct(slots + u * (kSlotBytes / 16)),
-                                   unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           a[j] = add2(a[j], dz.v[j]);
           b[j] = fma2(dz.v[j], xh.v[j], b[j]);
         }
       }
-    cp_async_wait<0>();
-  }
-  __syncthreads();  // every slot has been read
-  if (sl.pl < sl.ppi) {
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      red[sl.pl * cp + sl.ch + 2 * j] = make_float2(lo2(a[j]), lo2(b[j]));
-      red[sl.pl * cp + sl.ch + 2 * j + 1] = make_float2(hi2(a[j]), hi2(b[j]));
+      red[sw.pl * cp + sw.ch + 2 * j] = make_float2(lo2(a[j]), lo2(b[j]));
+      red[sw.pl * cp + sw.ch + 2 * j + 1] = make_float2(hi2(a[j]), hi2(b[j]));
     }
   }
   __syncthreads();
@@ -316,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = threadIdx.x; i < c; i += kThreads) {
     float2 t = red[i];
 #pragma unroll 8
-    for (int l = 1; l < sl.ppi; ++l) {
+    for (int l = 1; l < sw.ppi; ++l) {
       t.x += red[l * cp + i].x;
       t.y += red[l * cp + i].y;
     }
@@ -439,72 +492,63 @@ __device__ __forceinline__ void group_means(float2 *km, const float2 *__restrict
 }
 
 // grid (slabs, n).
-template <bool SILU>
+template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
     ckpt_dx_nhwc(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
                  const float *__restrict__ beta, const float2 *__restrict__ sums,
                  const float *dres, float *dx) {
-  extern __shared__ __align__(16) float4 slots[];
   __shared__ float2 km[1024];
-  const Slab sl(c, spatial);
+  const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31, cg = c / groups;
   group_means(km, sums, blockIdx.y, c, groups, spatial, stats, gamma, 0, groups);
-  if (sl.pl >= sl.ppi) return;
-  const Affine8 f = load_affine8(sl, c, groups, stats, gamma, beta);
+  if (sw.pl >= sw.ppi) return;
+  const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
   // dx = rg dz + (k1 + xh k2), rg = rstd gamma, with both means negated
   uint64_t rg[4], k1[4], k2[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 u = 2 * j < sl.left ? km[(sl.ch + 2 * j) / cg] : make_float2(0.f, 0.f);
-    const float2 v = 2 * j + 1 < sl.left ? km[(sl.ch + 2 * j + 1) / cg] : make_float2(0.f, 0.f);
+    const float2 u = 2 * j < sw.left ? km[(sw.ch + 2 * j) / cg] : make_float2(0.f, 0.f);
+    const float2 v = 2 * j + 1 < sw.left ? km[(sw.ch + 2 * j + 1) / cg] : make_float2(0.f, 0.f);
     rg[j] = mul2(f.rstd[j], f.gamma[j]);
     k1[j] = pk2(-u.x, -v.x);
     k2[j] = pk2(-u.y, -v.y);
   }
-  dy += sl.row0 * c;
-  dx += sl.row0 * c;
-  if (dres) dres += sl.row0 * c;
-  const CkptView kv = from_row(k, sl.row0, cp);
-  const uint32_t slot0 = smem_u32(slots);
-  uint2 q[kDepth];
-  uint32_t sb[kDepth];
-  auto fetch = [&](int i, int u) {
-    const int p = sl.len - 1 - sl.pl - i * sl.ppi;
-    const bool in = p >= 0;
-    fetch_oct(slot0 + u * kSlotBytes, dy, static_cast<uint32_t>(p) * c + sl.ch,
-              in ? sl.left : 0);
-    cp_async_commit();
-    q[u] = make_uint2(0, 0);
-    sb[u] = 0;
-    if (in) {
-      q[u] = __ldcs(reinterpret_cast<const uint2 *>(
-          kv.q + (static_cast<uint32_t>(p) * cp + sl.ch)));
-      sb[u] = __ldg(kv.scale + (static_cast<uint32_t>(p) * (cp >> 5) + (sl.ch >> 5)));
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < kDepth - 1; ++u) fetch(u, u);
+  const float *src = dy + sw.row0 * c + sw.ch, *res = dres ? dres + sw.row0 * c + sw.ch : nullptr;
+  float *dst = dx + sw.row0 * c + sw.ch;
+  const CkptView kv = from_row(k, sw.row0, cp);
+  constexpr int U = 2;
 #pragma unroll 1
-  for (int i = 0; i < sl.iters; i += kDepth)
+  for (int top = sw.iters - 1; top >= 0; top -= U) {
+    Oct g[U], r[U];
+    uint2 q[U];
+    uint32_t sb[U];
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int p = sl.len - 1 - sl.pl - (i + u) * sl.ppi;
-      const uint32_t at = static_cast<uint32_t>(p) * c + sl.ch;
-      Oct xh, o, r;
-      if (dres) r = load_oct(dres + (p >= 0 ? at : 0u), p >= 0 ? sl.left : 0);
-      fetch(i + u + kDepth - 1, (u + kDepth - 1) % kDepth);
-      cp_async_wait<kDepth - 1>();
-      const Oct dz = grad8<SILU>(slot_oct(slots + u * (kSlotBytes / 16)),
-                                 unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+    for (int u = 0; u < U; ++u) {
+      const unsigned p = sw.pixel(top - u);
+      const bool in = sw.in(top - u, p);
+      g[u] = load_oct<WIDE, true>(row_at(src, p, c), in ? sw.left : 0);
+      if (res) r[u] = load_oct<WIDE, true>(row_at(res, p, c), in ? sw.left : 0);
+      q[u] = make_uint2(0, 0);
+      sb[u] = 0;
+      if (in) {
+        q[u] = __ldcs(reinterpret_cast<const uint2 *>(row_at(kv.q + sw.ch, p, cp)));
+        sb[u] = __ldg(row_at(kv.scale + (sw.ch >> 5), p, cp >> 5));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned p = sw.pixel(top - u);
+      Oct xh, o;
+      const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         o.v[j] = fma2(rg[j], dz.v[j], fma2(xh.v[j], k2[j], k1[j]));
-        if (dres) o.v[j] = add2(o.v[j], r.v[j]);
+        if (res) o.v[j] = add2(o.v[j], r[u].v[j]);
       }
-      store_oct(dx + at, p >= 0 ? sl.left : 0, o);
+      store_oct<WIDE>(row_at(dst, p, c), sw.in(top - u, p) ? sw.left : 0, o);
     }
-  cp_async_wait<0>();
+  }
 }
 
 // grid (slabs, cp / 32, n).
@@ -593,11 +637,12 @@ int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int group
   const CkptWs w = carve_forward(cv, n, c, spatial, groups);
   float2 *st = reinterpret_cast<float2 *>(stats);
   const int ng = n * groups;
+  const bool wide = wide_ok(c, x, y);
   int slabs;
   if (nhwc) {
     slabs = slabs_nhwc(n, c, spatial);
-    const size_t sm = static_cast<size_t>(kStatThreads / (c / 4)) * c * 3 * sizeof(float);
-    ckpt_stats_nhwc<<<dim3(slabs, n), kStatThreads, sm, s>>>(x, c, spatial, groups, w.part);
+    (wide ? ckpt_stats_nhwc<true> : ckpt_stats_nhwc<false>)<<<dim3(slabs, n), kThreads, 0, s>>>(
+        x, c, spatial, groups, w.part);
   } else {
     slabs = slabs_stats_nchw(ng, spatial * (c / groups));
     ckpt_stats_nchw<<<dim3(ng, slabs), kStatThreads, 0, s>>>(x, c, spatial, groups, w.part);
@@ -606,8 +651,9 @@ int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int group
   ckpt_stats_merge<<<ng, slabs > 128 ? kMergeThreads : 128, 0, s>>>(w.part, slabs, eps, st);
   VAE_LAUNCH_CHECK();
   if (nhwc)
-    (silu ? ckpt_apply_nhwc<true> : ckpt_apply_nhwc<false>)<<<dim3(slabs, n), kThreads, kDepth * kSlotBytes,
-                                                                s>>>(
+    (wide ? (silu ? ckpt_apply_nhwc<true, true> : ckpt_apply_nhwc<false, true>)
+          : (silu ? ckpt_apply_nhwc<true, false> : ckpt_apply_nhwc<false, false>))<<<
+        dim3(slabs, n), kThreads, 0, s>>>(
         x, c, spatial, groups, st, gamma, beta, y, kx, ky);
   else
     ckpt_apply_nchw<<<dim3(slabs_nchw(n, c, spatial), ckpt_cp(c) / 32, n), kPixThreads, 0, s>>>(
@@ -625,6 +671,7 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   const CkptWs w = carve_backward(cv, n, c, spatial);
   const float2 *st = reinterpret_cast<const float2 *>(stats);
   float2 *part = reinterpret_cast<float2 *>(w.part);
+  const bool wide = dres ? wide_ok(c, dy, dx, dres) : wide_ok(c, dy, dx);
   const int rc = gn_backward_resident(dy, k, stats, n, c, spatial, nhwc, groups, gamma, beta,
                                       silu, dres, dx, dgamma, dbeta, w.sums, s);
   if (rc == VAE_OK && n > 1 && (dgamma || dbeta)) {
@@ -636,7 +683,9 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   const int slabs = nhwc ? slabs_nhwc(n, c, spatial) : slabs_nchw(n, c, spatial);
   const dim3 grid = nhwc ? dim3(slabs, n) : dim3(slabs, ckpt_cp(c) / 32, n);
   if (nhwc)
-    (silu ? ckpt_sums_nhwc<true> : ckpt_sums_nhwc<false>)<<<grid, kThreads, kDepth * kSlotBytes, s>>>(
+    (wide ? (silu ? ckpt_sums_nhwc<true, true> : ckpt_sums_nhwc<false, true>)
+          : (silu ? ckpt_sums_nhwc<true, false> : ckpt_sums_nhwc<false, false>))<<<grid, kThreads, 0,
+                                                                          s>>>(
         dy, k, c, spatial, groups, st, gamma, beta, part);
   else
     ckpt_sums_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
@@ -645,7 +694,9 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   ckpt_sums_merge<<<ckpt_cp(c) / 32, 1024, 0, s>>>(part, n, slabs, c, w.sums, dgamma, dbeta);
   VAE_LAUNCH_CHECK();
   if (nhwc)
-    (silu ? ckpt_dx_nhwc<true> : ckpt_dx_nhwc<false>)<<<grid, kThreads, kDepth * kSlotBytes, s>>>(
+    (wide ? (silu ? ckpt_dx_nhwc<true, true> : ckpt_dx_nhwc<false, true>)
+          : (silu ? ckpt_dx_nhwc<true, false> : ckpt_dx_nhwc<false, false>))<<<grid, kThreads, 0,
+                                                                          s>>>(
         dy, k, c, spatial, groups, st, gamma, beta, w.sums, dres, dx);
   else
     ckpt_dx_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
