@@ -40,11 +40,10 @@ inline CkptView ckpt_view(const void *p, long long rows, int c) {
 // Scale byte of a block from the largest bit pattern of its |v| (unsigned
 // order is the order of magnitudes, with infinity and NaN on top).
 // 448 = 1.75 * 2^8, so e = exponent - 8, one more when the significand is
-// above 1.75.
+// above 1.75: when adding 0x1fffff to its 23 bits carries.
 __device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t amax_bits) {
-  if (amax_bits >= 0x7f800000u) return 255u;
-  const int b = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u);
-  return b > 0 ? static_cast<uint32_t>(b) : 0u;
+  const int b = max(static_cast<int>((amax_bits + 0x1fffffu) >> 23) - 8, 0);
+  return amax_bits >= 0x7f800000u ? 255u : static_cast<uint32_t>(b);
 }
 // 2^-e as a float (a normal number for every byte below 255); NaN for 255.
 __device__ __forceinline__ float ckpt_inv_scale(uint32_t byte) {

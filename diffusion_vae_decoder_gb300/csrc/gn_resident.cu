@@ -18,7 +18,7 @@ namespace vae {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
 
@@ -112,16 +112,16 @@ __device__ __forceinline__ void channel_sums(uint64_t (&s)[4], uint64_t (&t)[4],
 
 // The packed affine of eight channels.
 __device__ __forceinline__ Affine8 affine8(const float4 *aff) {
-  Affine8 f;
+  float m[8], r[8], ga[8], be[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 a = aff[2 * j], b = aff[2 * j + 1];
-    f.nmean[j] = pk2(-a.x, -b.x);
-    f.rstd[j] = pk2(a.y, b.y);
-    f.gamma[j] = pk2(a.z, b.z);
-    f.beta[j] = pk2(a.w, b.w);
+  for (int j = 0; j < 8; ++j) {
+    const float4 a = aff[j];
+    m[j] = a.x;
+    r[j] = a.y;
+    ga[j] = a.z;
+    be[j] = a.w;
   }
-  return f;
+  return affine_of(m, r, ga, be);
 }
 
 // Where a thread stands in a block's piece of an NHWC tensor.
@@ -182,7 +182,7 @@ __device__ __forceinline__ void finish_stats(const ResArgs &a, float *tri, float
 
 // grid (cluster, slabs, n).
 template <bool SILU, bool WIDE>
-__global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gn_res_fwd_nhwc(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
   float *tri = sm + 4 * a.slab;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nhwc(const ResArgs a) {
 }
 
 // Pixels of a channel row in shared memory: a.per rounded up to 32.
-__global__ void __launch_bounds__(kThreads) gn_res_fwd_nchw(const ResArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gn_res_fwd_nchw(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
   float *tri = sm + 4 * a.slab, *chs = tri;  // channel triples first, group triples over them
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_fwd_nchw(const ResArgs a) {
   const int cg = a.c / a.groups, g0 = ch0 / cg, ng = chans / cg;
   // (group g's triple replaces that of channel g <= g cg: merged by one thread
   // in order, after every thread has read its channels)
-  Triple t[2];
+  Triple t[1024 / kThreads];
   int at = 0;
   for (int g = threadIdx.x; g < ng; g += kThreads, ++at) {
     t[at] = Triple{0.f, 0.f, 0.f};
@@ -446,7 +446,7 @@ __device__ __forceinline__ void finish_sums(const ResArgs &a, const float2 *mine
 }
 
 template <bool SILU, bool WIDE>
-__global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gn_res_bwd_nhwc(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
   float2 *mine = reinterpret_cast<float2 *>(sm + 4 * a.slab);
@@ -479,29 +479,33 @@ __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (p + u * pc.ppi >= pc.count) break;
-        Oct xh;
-        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+        Oct dev;
+        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &dev);
         data[i + 2 * u * kThreads] = oct_lo(dz);
         data[i + (2 * u + 1) * kThreads] = oct_hi(dz);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           s[j] = add2(s[j], dz.v[j]);
-          t[j] = fma2(dz.v[j], xh.v[j], t[j]);
+          t[j] = fma2(dz.v[j], dev.v[j], t[j]);
         }
       }
     }
   }
+  float rstd[8];  // dev rstd = xh
+#pragma unroll
+  for (int j = 0; j < 8; ++j) rstd[j] = aff[8 * pc.o + j].y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t[j] = mul2(t[j], pk2(rstd[2 * j], rstd[2 * j + 1]));
   channel_sums(s, t, a.slab, pc.o, pc.pl, pc.ppi, red, mine);
   finish_sums(a, mine, km, aff, n, ch0);
   if (pc.left > 0) {
-    uint64_t rg[4], k1[4], k2[4];  // dx = rg dz + (k1 + xh k2), both means negated
+    uint64_t k1[4], k2[4];  // dx = scale dz + (k1 + dev k2), both means negated
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 u = km[8 * pc.o + 2 * j], v = km[8 * pc.o + 2 * j + 1];
       const bool in = 2 * j < pc.left;  // (left is a multiple of four)
-      rg[j] = mul2(f.rstd[j], f.gamma[j]);
       k1[j] = in ? pk2(-u.x, -v.x) : 0;
-      k2[j] = in ? pk2(-u.y, -v.y) : 0;
+      k2[j] = in ? pk2(-u.y * rstd[2 * j], -v.y * rstd[2 * j + 1]) : 0;
     }
 #pragma unroll 2
     for (int p = pc.pl, i = threadIdx.x; p < pc.count; p += pc.ppi, i += 2 * kThreads) {
@@ -513,8 +517,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
       Oct o;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o.v[j] = fma2(rg[j], dz.v[j],
-                      fma2(mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]), k2[j], k1[j]));
+        o.v[j] = fma2(f.scale[j], dz.v[j], fma2(add2(x.v[j], f.nmean[j]), k2[j], k1[j]));
       if (a.dres) {
         const Oct r = load_oct<WIDE, true>(a.dres + at, pc.left);
 #pragma unroll
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(kThreads) gn_res_bwd_nhwc(const ResArgs a) {
   leave();
 }
 
-__global__ void __launch_bounds__(kThreads, 1) gn_res_bwd_nchw(const ResArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gn_res_bwd_nchw(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
   float2 *mine = reinterpret_cast<float2 *>(sm + 4 * a.slab);

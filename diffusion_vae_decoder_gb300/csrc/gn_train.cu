@@ -199,20 +199,12 @@ __device__ __forceinline__ Affine8 load_affine8(const Sweep &sw, int c, int grou
   for (int j = 0; j < 8; ++j) {
     const bool in = j < sw.left;
     const float2 st = in ? stats[blockIdx.y * groups + (sw.ch + j) / cg] : make_float2(0.f, 0.f);
-    m[j] = -st.x;
+    m[j] = st.x;
     r[j] = st.y;
     ga[j] = in ? gamma[sw.ch + j] : 0.f;
     be[j] = in ? beta[sw.ch + j] : 0.f;
   }
-  Affine8 f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f.nmean[j] = pk2(m[2 * j], m[2 * j + 1]);
-    f.rstd[j] = pk2(r[2 * j], r[2 * j + 1]);
-    f.gamma[j] = pk2(ga[2 * j], ga[2 * j + 1]);
-    f.beta[j] = pk2(be[2 * j], be[2 * j + 1]);
-  }
-  return f;
+  return affine_of(m, r, ga, be);
 }
 
 // k: the checkpoint from the sample's first row on.
@@ -329,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
     const float *src = dy + sw.row0 * c + sw.ch;
     const CkptView kv = from_row(k, sw.row0, cp);
-    constexpr int U = 3;
+    constexpr int U = 4;
 #pragma unroll 1
     for (int i = 0; i < sw.iters; i += U) {
       Oct g[U];
@@ -349,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {  // (a pixel outside has dy = 0 and adds nothing)
-        Oct xh;
-        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+        Oct dev;
+        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &dev);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           a[j] = add2(a[j], dz.v[j]);
-          b[j] = fma2(dz.v[j], xh.v[j], b[j]);
+          b[j] = fma2(dz.v[j], dev.v[j], b[j]);
         }
       }
     }
@@ -373,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       t.x += red[l * cp + i].x;
       t.y += red[l * cp + i].y;
     }
+    t.y *= stats[blockIdx.y * groups + i / (c / groups)].y;  // dev rstd = xh
     o[i] = t;
   }
 }
@@ -504,20 +497,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   group_means(km, sums, blockIdx.y, c, groups, spatial, stats, gamma, 0, groups);
   if (sw.pl >= sw.ppi) return;
   const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
-  // dx = rg dz + (k1 + xh k2), rg = rstd gamma, with both means negated
-  uint64_t rg[4], k1[4], k2[4];
+  // dx = scale dz + (k1 + dev k2): both means negated, k2 with the rstd of xh
+  uint64_t k1[4], k2[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 u = 2 * j < sw.left ? km[(sw.ch + 2 * j) / cg] : make_float2(0.f, 0.f);
-    const float2 v = 2 * j + 1 < sw.left ? km[(sw.ch + 2 * j + 1) / cg] : make_float2(0.f, 0.f);
-    rg[j] = mul2(f.rstd[j], f.gamma[j]);
-    k1[j] = pk2(-u.x, -v.x);
-    k2[j] = pk2(-u.y, -v.y);
+    float2 m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m[h] = make_float2(0.f, 0.f);
+      if (2 * j + h < sw.left) {
+        const int g = (sw.ch + 2 * j + h) / cg;
+        m[h] = make_float2(-km[g].x, -km[g].y * stats[blockIdx.y * groups + g].y);
+      }
+    }
+    k1[j] = pk2(m[0].x, m[1].x);
+    k2[j] = pk2(m[0].y, m[1].y);
   }
   const float *src = dy + sw.row0 * c + sw.ch, *res = dres ? dres + sw.row0 * c + sw.ch : nullptr;
   float *dst = dx + sw.row0 * c + sw.ch;
   const CkptView kv = from_row(k, sw.row0, cp);
-  constexpr int U = 2;
+  constexpr int U = 3;
 #pragma unroll 1
   for (int top = sw.iters - 1; top >= 0; top -= U) {
     Oct g[U], r[U];
@@ -539,11 +538,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const unsigned p = sw.pixel(top - u);
-      Oct xh, o;
-      const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &xh);
+      Oct dev, o;
+      const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &dev);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        o.v[j] = fma2(rg[j], dz.v[j], fma2(xh.v[j], k2[j], k1[j]));
+        o.v[j] = fma2(f.scale[j], dz.v[j], fma2(dev.v[j], k2[j], k1[j]));
         if (res) o.v[j] = add2(o.v[j], r[u].v[j]);
       }
       store_oct<WIDE>(row_at(dst, p, c), sw.in(top - u, p) ? sw.left : 0, o);

@@ -82,11 +82,22 @@ __device__ __forceinline__ float grad_z(float dy, float xv, float mean, float rs
   return dy * (s * fmaf(z, 1.0f - s, 1.0f));
 }
 
-// Eight channels of a pixel, packed. negated means and logarithms' constants
-// are folded so that each step is one two-wide operation.
+// Eight channels of a pixel, in packed pairs: z = (x - mean) scale + beta with
+// scale = rstd gamma.
 struct Affine8 {
-  uint64_t nmean[4], rstd[4], gamma[4], beta[4];
+  uint64_t nmean[4], scale[4], beta[4];
 };
+__device__ __forceinline__ Affine8 affine_of(const float (&mean)[8], const float (&rstd)[8],
+                                             const float (&gamma)[8], const float (&beta)[8]) {
+  Affine8 f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f.nmean[j] = pk2(-mean[2 * j], -mean[2 * j + 1]);
+    f.scale[j] = pk2(rstd[2 * j] * gamma[2 * j], rstd[2 * j + 1] * gamma[2 * j + 1]);
+    f.beta[j] = pk2(beta[2 * j], beta[2 * j + 1]);
+  }
+  return f;
+}
 __device__ __forceinline__ uint64_t rcp2(uint64_t a) {
   float x, y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(lo2(a)));
@@ -104,22 +115,22 @@ __device__ __forceinline__ Oct forward8(const Oct &x, const Affine8 &f) {
   Oct o;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t z = fma2(mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]), f.gamma[j], f.beta[j]);
+    const uint64_t z = fma2(add2(x.v[j], f.nmean[j]), f.scale[j], f.beta[j]);
     o.v[j] = SILU ? mul2(z, sigmoid2(z)) : z;
   }
   return o;
 }
-// dz of eight elements; xh receives the normalised inputs.
+// dz of eight elements; dev receives x - mean.
 template <bool SILU>
-__device__ __forceinline__ Oct grad8(const Oct &dy, const Oct &x, const Affine8 &f, Oct *xh) {
+__device__ __forceinline__ Oct grad8(const Oct &dy, const Oct &x, const Affine8 &f, Oct *dev) {
   Oct o;
   const uint64_t one = pk2(1.f, 1.f), minus = pk2(-1.f, -1.f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    xh->v[j] = mul2(add2(x.v[j], f.nmean[j]), f.rstd[j]);
+    dev->v[j] = add2(x.v[j], f.nmean[j]);
     o.v[j] = dy.v[j];
     if (SILU) {
-      const uint64_t z = fma2(xh->v[j], f.gamma[j], f.beta[j]);
+      const uint64_t z = fma2(dev->v[j], f.scale[j], f.beta[j]);
       const uint64_t s = sigmoid2(z);
       o.v[j] = mul2(dy.v[j], mul2(s, fma2(z, fma2(s, minus, one), one)));
     }
