@@ -124,6 +124,27 @@ __device__ __forceinline__ Affine8 affine8(const float4 *aff) {
   return affine_of(m, r, ga, be);
 }
 
+// NCHW: room for the slab's channel pairs, or before them for a triple per warp
+// and lane.
+__host__ __device__ constexpr size_t pair_floats(int slab) {
+  const size_t a = static_cast<size_t>(slab) / 2 * (sizeof(PairAffine) / 4);
+  const size_t b = kWarps * 32 * 3;
+  return a > b ? a : b;
+}
+__device__ __forceinline__ void pair_up(const ResArgs &a, const float4 *aff, PairAffine *pairs,
+                                        int chans) {
+  for (int t = threadIdx.x; t < a.slab / 2; t += kThreads) {
+    float4 f[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      f[h] = 2 * t + h < chans ? aff[2 * t + h] : make_float4(0.f, 0.f, 0.f, 0.f);
+    pairs[t].nmean = pk2(-f[0].x, -f[1].x);
+    pairs[t].scale = pk2(f[0].y * f[0].z, f[1].y * f[1].z);
+    pairs[t].beta = pk2(f[0].w, f[1].w);
+  }
+  __syncthreads();
+}
+
 // Where a thread stands in a block's piece of an NHWC tensor.
 struct Piece {
   int o, pl, ppi, ch, left, count;
@@ -271,63 +292,63 @@ __global__ void __launch_bounds__(kThreads, 2) gn_res_fwd_nhwc(const ResArgs a) 
   leave();
 }
 
-// Pixels of a channel row in shared memory: a.per rounded up to 32.
+// Warps of an NCHW block take a 32-channel block of the slab and every
+// `stride`th run of 32 pixels of it; more blocks than warps go in rounds.
+struct Runs {
+  int blocks, width, stride, first;
+  __device__ Runs(int chans) {
+    const int warp = threadIdx.x >> 5;
+    blocks = (chans + 31) / 32;
+    width = min(blocks, kWarps);
+    stride = kWarps / width;
+    first = warp / width;  // `stride` and above: idle
+  }
+  __device__ int block(int round) const { return round + (threadIdx.x >> 5) % width; }
+};
+
+// Shared memory of a block: per run of 32 pixels the channels of the slab, 32
+// pixels each ([run][channel][32]).
 __global__ void __launch_bounds__(kThreads, 2) gn_res_fwd_nchw(const ResArgs a) {
   extern __shared__ __align__(16) float sm[];
   float4 *aff = reinterpret_cast<float4 *>(sm);
-  float *tri = sm + 4 * a.slab, *chs = tri;  // channel triples first, group triples over them
-  float *data = sm + head_floats(a.slab);
+  float *tri = sm + 4 * a.slab, *chs = tri;  // channel triples, then group triples over them
+  PairAffine *pairs = reinterpret_cast<PairAffine *>(sm + head_floats(a.slab));
+  Triple *red = reinterpret_cast<Triple *>(pairs);  // [warps][32], before the pairs
+  float *data = sm + head_floats(a.slab) + pair_floats(a.slab);
   const int n = blockIdx.z, ch0 = blockIdx.y * a.slab, cp = (a.c + 31) & ~31;
-  const int chans = min(a.slab, a.c - ch0), ld = (a.per + 31) & ~31;
+  const int chans = min(a.slab, a.c - ch0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long p0 = static_cast<long long>(blockIdx.x) * a.per;
   const int count = static_cast<int>(max(0ll, min(static_cast<long long>(a.per), a.spatial - p0)));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float *src = a.x + (static_cast<long long>(n) * a.c + ch0) * a.spatial + p0;
+  const long long base = (static_cast<long long>(n) * a.c + ch0) * a.spatial + p0;
   load_gamma(a, aff, ch0);
-  // a warp per channel: load it, then its triple from shared memory, two passes
-  for (int ch = warp; ch < chans; ch += kWarps) {
-    const float *s = src + ch * a.spatial;
-    float *d = data + ch * ld;
-    float sum = 0.f;
-    int p = lane;
-    for (; p + 480 < count; p += 512) {
-      float v[16];
+  const Runs rn(chans);
+  for (int round = 0; round < rn.blocks; round += rn.width) {
+    const int cb = rn.block(round);
+    Triple t{0.f, 0.f, 0.f};
+    if (cb < rn.blocks && rn.first < rn.stride)
+      for (int r = rn.first; 32 * r < count; r += rn.stride) {
+        const int p = 32 * r + lane, left = chans - 32 * cb;
+        const Row32 v = load_planes(a.x + base + static_cast<long long>(32 * cb) * a.spatial + p,
+                                    a.spatial, p < count ? left : 0);
+        float *d = data + (static_cast<size_t>(r) * a.slab + 32 * cb) * 32 + lane;
 #pragma unroll
-      for (int u = 0; u < 16; ++u) v[u] = __ldcs(s + p + 32 * u);
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        d[p + 32 * u] = v[u];
-        sum += v[u];
+        for (int j = 0; j < 16; ++j) {
+          d[64 * j] = lo2(v.v[j]);
+          d[64 * j + 32] = hi2(v.v[j]);
+        }
+        t = merge(t, run_triple(v, min(32, count - 32 * r), lane));
       }
+    red[warp * 32 + lane] = t;
+    __syncthreads();
+    if (rn.first == 0 && cb < rn.blocks) {
+      for (int r = 1; r < rn.stride; ++r) t = merge(t, red[(warp + r * rn.width) * 32 + lane]);
+      float *e = chs + 3 * (32 * cb + lane);
+      e[0] = t.n;
+      e[1] = t.mean;
+      e[2] = t.m2;
     }
-#pragma unroll 4
-    for (; p < count; p += 32) {
-      const float v = __ldcs(s + p);
-      d[p] = v;
-      sum += v;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float mean = count ? sum / count : 0.f;
-    float m2 = 0.f, rest = 0.f;  // the mean's own rounding is corrected by the rest
-    for (int i = lane; i < count; i += 32) {
-      const float e = d[i] - mean;
-      rest += e;
-      m2 = fmaf(e, e, m2);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-      rest += __shfl_xor_sync(0xffffffffu, rest, o);
-    }
-    if (lane == 0) {
-      const float fix = count ? rest / count : 0.f;
-      chs[3 * ch] = static_cast<float>(count);
-      chs[3 * ch + 1] = mean + fix;
-      chs[3 * ch + 2] = count ? fmaxf(m2 - rest * fix, 0.f) : 0.f;
-    }
+    __syncthreads();
   }
-  __syncthreads();
   const int cg = a.c / a.groups, g0 = ch0 / cg, ng = chans / cg;
   // (group g's triple replaces that of channel g <= g cg: merged by one thread
   // in order, after every thread has read its channels)
@@ -348,25 +369,25 @@ __global__ void __launch_bounds__(kThreads, 2) gn_res_fwd_nchw(const ResArgs a) 
     tri[3 * g + 2] = t[at].m2;
   }
   finish_stats(a, tri, reinterpret_cast<float2 *>(sm + 7 * a.slab), aff, g0, ng, n);
-  float *ys = a.y + (static_cast<long long>(n) * a.c + ch0) * a.spatial + p0;
-  const int blocks = (chans + 31) / 32;
-  for (int item = threadIdx.x; item < blocks * ld; item += kThreads) {
-    const int cb = item / ld, p = item - cb * ld;
-    if (p >= count) continue;
-    const long long row = n * a.spatial + p0 + p;
-    const int in = min(32, chans - 32 * cb);
-    float v[32];
+  pair_up(a, aff, pairs, chans);
+  for (int round = 0; round < rn.blocks; round += rn.width) {
+    const int cb = rn.block(round);
+    if (cb >= rn.blocks || rn.first >= rn.stride) continue;
+    const int left = chans - 32 * cb;
+    for (int r = rn.first; 32 * r < count; r += rn.stride) {
+      const int p = 32 * r + lane;
+      if (p >= count) continue;
+      const float *d = data + (static_cast<size_t>(r) * a.slab + 32 * cb) * 32 + lane;
+      Row32 v;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = j < in ? data[(32 * cb + j) * ld + p] : 0.f;
-    if (a.kx.q) keep_row32(v, a.kx, row, cp, ch0 / 32 + cb);
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < in) {
-        const float4 f = aff[32 * cb + j];
-        v[j] = act(fmaf((v[j] - f.x) * f.y, f.z, f.w), a.silu);
-        __stcs(ys + static_cast<long long>(32 * cb + j) * a.spatial + p, v[j]);
-      }
-    if (a.ky.q) keep_row32(v, a.ky, row, cp, ch0 / 32 + cb);
+      for (int j = 0; j < 16; ++j) v.v[j] = pk2(d[64 * j], d[64 * j + 32]);
+      const long long row = n * a.spatial + p0 + p;
+      if (a.kx.q) keep_row32(v, a.kx, row, cp, ch0 / 32 + cb);
+      const Row32 o = forward32(v, pairs + 16 * cb, a.silu);
+      store_planes(a.y + base + static_cast<long long>(32 * cb) * a.spatial + p, a.spatial, left,
+                   o);
+      if (a.ky.q) keep_row32(o, a.ky, row, cp, ch0 / 32 + cb);
+    }
   }
   leave();
 }
@@ -534,79 +555,90 @@ __global__ void __launch_bounds__(kThreads, 2) gn_res_bwd_nchw(const ResArgs a) 
   float4 *aff = reinterpret_cast<float4 *>(sm);
   float2 *mine = reinterpret_cast<float2 *>(sm + 4 * a.slab);
   float2 *km = reinterpret_cast<float2 *>(sm + 7 * a.slab);
-  float2 *red = reinterpret_cast<float2 *>(sm + head_floats(a.slab));  // [warps][32]
-  float *data = sm + head_floats(a.slab) + kWarps * 32 * 2;
+  PairAffine *pairs = reinterpret_cast<PairAffine *>(sm + head_floats(a.slab));
+  float2 *red = reinterpret_cast<float2 *>(sm + head_floats(a.slab) + pair_floats(a.slab));
+  float *data = sm + head_floats(a.slab) + pair_floats(a.slab) + kWarps * 32 * 2;
   const int n = blockIdx.z, ch0 = blockIdx.y * a.slab, cp = (a.c + 31) & ~31;
-  const int chans = min(a.slab, a.c - ch0), ld = (a.per + 31) & ~31;
+  const int chans = min(a.slab, a.c - ch0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long p0 = static_cast<long long>(blockIdx.x) * a.per;
   const int count = static_cast<int>(max(0ll, min(static_cast<long long>(a.per), a.spatial - p0)));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long base = (static_cast<long long>(n) * a.c + ch0) * a.spatial + p0;
   load_affine(a, aff, n, ch0);
   __syncthreads();
-  // Warps take a 32-channel block and every `stride`th run of 32 pixels of it;
-  // a run's channel sums go to the lanes right away.
-  const int blocks = (chans + 31) / 32;
-  const int stride = blocks < kWarps ? kWarps / blocks : 1;
-  for (int cb0 = 0; cb0 < blocks; cb0 += kWarps) {
-    const int cb = cb0 + warp % min(blocks, kWarps), run0 = warp / min(blocks, kWarps);
+  pair_up(a, aff, pairs, chans);
+  const Runs rn(chans);
+  for (int round = 0; round < rn.blocks; round += rn.width) {
+    const int cb = rn.block(round);
     float2 sum = make_float2(0.f, 0.f);
-    if (cb < blocks && run0 < stride) {
-      const int in = min(32, chans - 32 * cb);
-      const float *src = a.x + base + static_cast<long long>(32 * cb) * a.spatial;
-      for (int p0w = 32 * run0; p0w < count; p0w += 32 * stride) {
-        const int p = p0w + lane;
-        const bool here = p < count;
-        float v[32], g[32];
+    if (cb < rn.blocks && rn.first < rn.stride)
+      for (int r = rn.first; 32 * r < count; r += rn.stride) {
+        const int p = 32 * r + lane;
+        const bool here = p < count;  // (elsewhere dy = 0, which adds nothing)
+        const Row32 g =
+            load_planes(a.x + base + static_cast<long long>(32 * cb) * a.spatial + p, a.spatial,
+                        here ? chans - 32 * cb : 0);
+        const Row32 v =
+            read_row32(a.kx, n * a.spatial + p0 + (here ? p : 0), cp, ch0 / 32 + cb);
+        Row32 dev;
+        const Row32 dz = grad32(g, v, pairs + 16 * cb, a.silu, &dev);
+        float *d = data + (static_cast<size_t>(r) * a.slab + 32 * cb) * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          g[j] = j < in && here ? __ldcs(src + j * a.spatial + p) : 0.f;
-          v[j] = 0.f;
+        for (int j = 0; j < 16; ++j) {
+          d[64 * j] = lo2(dz.v[j]);
+          d[64 * j + 32] = hi2(dz.v[j]);
         }
-        if (here) read_row32(v, a.kx, n * a.spatial + p0 + p, cp, ch0 / 32 + cb);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float4 f = aff[32 * cb + j];
-          float xh;
-          g[j] = grad_z(g[j], v[j], f.x, f.y, f.z, f.w, a.silu, &xh);
-          if (j < in && here) data[(32 * cb + j) * ld + p] = g[j];
-          v[j] = g[j] * xh;
-        }
-        sum.x += reduce_scatter32(g, lane);
-        sum.y += reduce_scatter32(v, lane);
+        const float2 t = run_sums(dz, dev, lane);
+        sum.x += t.x;
+        sum.y += t.y;
       }
-    }
     red[warp * 32 + lane] = sum;
     __syncthreads();
-    if (run0 == 0 && cb < blocks) {  // one warp per block adds its runs in order
-      float2 v = sum;
-      for (int r = 1; r < stride; ++r) {
-        const float2 w = red[(warp + r * blocks) * 32 + lane];
-        v.x += w.x;
-        v.y += w.y;
+    if (rn.first == 0 && cb < rn.blocks) {  // one warp per block adds its runs in order
+      for (int r = 1; r < rn.stride; ++r) {
+        const float2 w = red[(warp + r * rn.width) * 32 + lane];
+        sum.x += w.x;
+        sum.y += w.y;
       }
-      mine[32 * cb + lane] = v;
+      sum.y *= aff[32 * cb + lane].y;  // dev rstd = xh
+      mine[32 * cb + lane] = sum;
     }
     __syncthreads();
   }
   finish_sums(a, mine, km, aff, n, ch0);
-  for (int item = threadIdx.x; item < blocks * ld; item += kThreads) {
-    const int cb = item / ld, p = item - cb * ld;
-    if (p >= count) continue;
-    const int in = min(32, chans - 32 * cb);
-    float v[32];
-    read_row32(v, a.kx, n * a.spatial + p0 + p, cp, ch0 / 32 + cb);
+  for (int t = threadIdx.x; t < a.slab / 2; t += kThreads) {
+    float2 m[2];
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < in) {
-        const int ch = 32 * cb + j;
-        const float4 f = aff[ch];
-        const float2 m = km[ch];
-        const long long at = base + static_cast<long long>(ch) * a.spatial + p;
-        float o = fmaf(f.y * f.z, data[ch * ld + p], -fmaf((v[j] - f.x) * f.y, m.y, m.x));
-        if (a.dres) o += __ldcs(a.dres + at);
-        __stcs(a.dx + at, o);
+    for (int h = 0; h < 2; ++h) {
+      const int ch = 2 * t + h;
+      m[h] = ch < chans ? make_float2(-km[ch].x, -km[ch].y * aff[ch].y) : make_float2(0.f, 0.f);
+    }
+    pairs[t].k1 = pk2(m[0].x, m[1].x);
+    pairs[t].k2 = pk2(m[0].y, m[1].y);
+  }
+  __syncthreads();
+  for (int round = 0; round < rn.blocks; round += rn.width) {
+    const int cb = rn.block(round);
+    if (cb >= rn.blocks || rn.first >= rn.stride) continue;
+    const int left = chans - 32 * cb;
+    for (int r = rn.first; 32 * r < count; r += rn.stride) {
+      const int p = 32 * r + lane;
+      if (p >= count) continue;
+      const float *d = data + (static_cast<size_t>(r) * a.slab + 32 * cb) * 32 + lane;
+      Row32 dz, dev = read_row32(a.kx, n * a.spatial + p0 + p, cp, ch0 / 32 + cb);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        dz.v[j] = pk2(d[64 * j], d[64 * j + 32]);
+        dev.v[j] = add2(dev.v[j], pairs[16 * cb + j].nmean);
       }
+      Row32 o = dx32(dz, dev, pairs + 16 * cb);
+      const long long at = base + static_cast<long long>(32 * cb) * a.spatial + p;
+      if (a.dres) {
+        const Row32 res = load_planes(a.dres + at, a.spatial, left);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o.v[j] = add2(o.v[j], res.v[j]);
+      }
+      store_planes(a.dx + at, a.spatial, left, o);
+    }
   }
   leave();
 }
@@ -622,12 +654,13 @@ int slab_channels(int c, int groups) {
 
 // Shared memory besides the pixels.
 size_t fixed_bytes(int slab, bool nhwc, bool backward) {
-  const size_t red = nhwc ? kRedFloats : backward ? kWarps * 32 * 2 : 0;
+  const size_t red = nhwc ? kRedFloats
+                          : pair_floats(slab) + (backward ? kWarps * 32 * 2 : 0);
   return (head_floats(slab) + red) * sizeof(float);
 }
 
 // Blocks of a cluster: as few as fit, up to 8 until the launch has a block per
-// SM or a block under 256 pixels; 16 (not portable) only to fit. 0: no fit.
+// SM or a block under 256 (NHWC) or 128 pixels; 16 (not portable) only to fit. 0: no fit.
 int cluster_blocks(int n, int c, long long spatial, int slab, size_t fixed, int *per,
                    size_t *smem, bool nhwc) {
   const int pieces = n * ((c + slab - 1) / slab);
@@ -640,7 +673,7 @@ int cluster_blocks(int n, int c, long long spatial, int slab, size_t fixed, int 
                               : static_cast<size_t>((pp + 31) / 32 * 32) * slab * 4;
     const size_t total = fixed + bytes;
     if (total > kMaxSmem) continue;
-    if (cl < 8 && static_cast<long long>(pieces) * cl < 152 && pp >= 256) continue;
+    if (cl < 8 && static_cast<long long>(pieces) * cl < 152 && pp >= (nhwc ? 256 : 128)) continue;
     *per = static_cast<int>(pp);
     *smem = total;
     return cl;

@@ -259,50 +259,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Per-channel constants of a 32-channel block, in shared memory: (mean, rstd,
-// gamma, beta), zeros past c.
-__device__ __forceinline__ void load_affine32(float4 *aff, int n, int c, int cb, int groups,
-                                              const float2 *stats, const float *gamma,
-                                              const float *beta) {
-  if (threadIdx.x < 32) {
-    const int ch = 32 * cb + threadIdx.x;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ch < c) {
-      const float2 st = stats[n * groups + ch / (c / groups)];
-      a = make_float4(st.x, st.y, gamma[ch], beta[ch]);
-    }
-    aff[threadIdx.x] = a;
-  }
-  __syncthreads();
-}
-
 // grid (slabs, cp / 32, n): a thread per pixel and 32 channels.
 __global__ void __launch_bounds__(kPixThreads)
     ckpt_apply_nchw(const float *x, int c, long long spatial, int groups,
                     const float2 *__restrict__ stats, const float *__restrict__ gamma,
                     const float *__restrict__ beta, int silu, float *y, CkptView kx,
                     CkptView ky) {
-  __shared__ float4 aff[32];
+  __shared__ PairAffine aff[16];
   const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31;
-  load_affine32(aff, n, c, cb, groups, stats, gamma, beta);
-  const int chans = min(32, c - 32 * cb);
+  if (threadIdx.x < 16)
+    load_pairs(aff, stats + n * groups, gamma, beta, 32 * cb, c, c / groups, threadIdx.x);
+  __syncthreads();
   const long long p0 = spatial * blockIdx.x / gridDim.x,
                   p1 = spatial * (blockIdx.x + 1) / gridDim.x;
-  const float *xs = x + (static_cast<long long>(n) * c + 32 * cb) * spatial;
-  float *ys = y + (static_cast<long long>(n) * c + 32 * cb) * spatial;
+  const long long base = (static_cast<long long>(n) * c + 32 * cb) * spatial;
   for (long long p = p1 - 1 - threadIdx.x; p >= p0; p -= kPixThreads) {
     const long long row = static_cast<long long>(n) * spatial + p;
-    float v[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = j < chans ? __ldcs(xs + j * spatial + p) : 0.f;
+    const Row32 v = load_planes(x + base + p, spatial, c - 32 * cb);
     if (kx.q) keep_row32(v, kx, row, cp, cb);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float4 a = aff[j];
-      v[j] = act(fmaf((v[j] - a.x) * a.y, a.z, a.w), silu);
-      if (j < chans) __stcs(ys + j * spatial + p, v[j]);
-    }
-    if (ky.q) keep_row32(v, ky, row, cp, cb);
+    const Row32 o = forward32(v, aff, silu);
+    store_planes(y + base + p, spatial, c - 32 * cb, o);
+    if (ky.q) keep_row32(o, ky, row, cp, cb);
   }
 }
 
@@ -375,46 +352,40 @@ __global__ void __launch_bounds__(kPixThreads)
     ckpt_sums_nchw(const float *__restrict__ dy, CkptView k, int c, long long spatial, int groups,
                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
                    const float *__restrict__ beta, int silu, float2 *__restrict__ part) {
-  __shared__ float4 aff[32];
+  __shared__ PairAffine aff[16];
   __shared__ float2 red[kPixThreads / 32][32];
-  const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31;
-  load_affine32(aff, n, c, cb, groups, stats, gamma, beta);
-  const int chans = min(32, c - 32 * cb);
+  const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31, cg = c / groups;
+  if (threadIdx.x < 16)
+    load_pairs(aff, stats + n * groups, gamma, beta, 32 * cb, c, cg, threadIdx.x);
+  __syncthreads();
+  const int left = c - 32 * cb, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long p0 = spatial * blockIdx.x / gridDim.x,
                   p1 = spatial * (blockIdx.x + 1) / gridDim.x;
-  const float *gs = dy + (static_cast<long long>(n) * c + 32 * cb) * spatial;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float *src = dy + (static_cast<long long>(n) * c + 32 * cb) * spatial;
   float2 sum = make_float2(0.f, 0.f);  // of channel `lane`
   for (long long pw = p0 + 32 * warp; pw < p1; pw += kPixThreads) {
     const long long p = pw + lane;
-    const bool here = p < p1;
-    float v[32], g[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      g[j] = j < chans && here ? __ldg(gs + j * spatial + p) : 0.f;
-      v[j] = 0.f;
-    }
-    if (here) read_row32(v, k, static_cast<long long>(n) * spatial + p, cp, cb);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float4 f = aff[j];
-      float xh;
-      g[j] = grad_z(g[j], v[j], f.x, f.y, f.z, f.w, silu, &xh);
-      v[j] = g[j] * xh;
-    }
-    sum.x += reduce_scatter32(g, lane);
-    sum.y += reduce_scatter32(v, lane);
+    const bool here = p < p1;  // (elsewhere dy = 0, which adds nothing)
+    const Row32 g = load_planes(src + p, spatial, here ? left : 0);
+    const Row32 v = read_row32(k, static_cast<long long>(n) * spatial + (here ? p : p0), cp, cb);
+    Row32 dev;
+    const Row32 dz = grad32(g, v, aff, silu, &dev);
+    const float2 t = run_sums(dz, dev, lane);
+    sum.x += t.x;
+    sum.y += t.y;
   }
   red[warp][lane] = sum;
   __syncthreads();
-  if (threadIdx.x < chans) {
+  if (threadIdx.x < 32 && threadIdx.x < left) {
     float2 t = red[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < kPixThreads / 32; ++w) {
       t.x += red[w][threadIdx.x].x;
       t.y += red[w][threadIdx.x].y;
     }
-    part[(static_cast<size_t>(n) * gridDim.x + blockIdx.x) * c + 32 * cb + threadIdx.x] = t;
+    const int ch = 32 * cb + threadIdx.x;
+    t.y *= stats[n * groups + ch / cg].y;  // dev rstd = xh
+    part[(static_cast<size_t>(n) * gridDim.x + blockIdx.x) * c + ch] = t;
   }
 }
 
@@ -556,35 +527,41 @@ __global__ void __launch_bounds__(kPixThreads)
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
                  const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
                  const float *dres, float *dx) {
-  __shared__ float4 aff[32];
-  __shared__ float2 km[32], kch[32];
+  __shared__ PairAffine aff[16];
+  __shared__ float2 km[32];
   const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31, cg = c / groups;
-  const int chans = min(32, c - 32 * cb);
-  load_affine32(aff, n, c, cb, groups, stats, gamma, beta);
+  const int left = c - 32 * cb, chans = min(32, left);
+  if (threadIdx.x < 16)
+    load_pairs(aff, stats + n * groups, gamma, beta, 32 * cb, c, cg, threadIdx.x);
   const int g0 = 32 * cb / cg, g1 = (32 * cb + chans - 1) / cg + 1;
   group_means(km, sums, n, c, groups, spatial, stats, gamma, g0, g1);
-  if (threadIdx.x < chans) kch[threadIdx.x] = km[(32 * cb + threadIdx.x) / cg - g0];
+  if (threadIdx.x < 16) {
+    float2 m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int ch = 2 * threadIdx.x + h, g = (32 * cb + ch) / cg;
+      m[h] = ch < chans ? make_float2(-km[g - g0].x, -km[g - g0].y * stats[n * groups + g].y)
+                        : make_float2(0.f, 0.f);
+    }
+    aff[threadIdx.x].k1 = pk2(m[0].x, m[1].x);
+    aff[threadIdx.x].k2 = pk2(m[0].y, m[1].y);
+  }
   __syncthreads();
   const long long p0 = spatial * blockIdx.x / gridDim.x,
                   p1 = spatial * (blockIdx.x + 1) / gridDim.x;
   const long long base = (static_cast<long long>(n) * c + 32 * cb) * spatial;
   for (long long p = p1 - 1 - threadIdx.x; p >= p0; p -= kPixThreads) {
-    float v[32], g[32];
+    const Row32 g = load_planes(dy + base + p, spatial, left);
+    const Row32 v = read_row32(k, static_cast<long long>(n) * spatial + p, cp, cb);
+    Row32 dev;
+    const Row32 dz = grad32(g, v, aff, silu, &dev);
+    Row32 o = dx32(dz, dev, aff);
+    if (dres) {
+      const Row32 r = load_planes(dres + base + p, spatial, left);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] = j < chans ? __ldcs(dy + base + j * spatial + p) : 0.f;
-    read_row32(v, k, static_cast<long long>(n) * spatial + p, cp, cb);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j < chans) {
-        const float4 f = aff[j];
-        const float2 m = kch[j];
-        float xh;
-        const float dz = grad_z(g[j], v[j], f.x, f.y, f.z, f.w, silu, &xh);
-        float o = fmaf(f.y * f.z, dz, -fmaf(xh, m.y, m.x));
-        if (dres) o += __ldcs(dres + base + j * spatial + p);
-        __stcs(dx + base + j * spatial + p, o);
-      }
+      for (int j = 0; j < 16; ++j) o.v[j] = add2(o.v[j], r.v[j]);
     }
+    store_planes(dx + base + p, spatial, left, o);
   }
 }
 

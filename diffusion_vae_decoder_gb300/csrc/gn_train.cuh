@@ -39,49 +39,6 @@ int gn_backward_resident(const float *dy, CkptView x_ckpt, const float *stats, i
                          float *dgamma, float *dbeta, float2 *sums, cudaStream_t s);
 
 // ------------------------------------------------------------- device pieces
-// Stores 32 channels of one row: payload and scale byte.
-__device__ __forceinline__ void keep_row32(const float *v, CkptView k, long long row, int cp,
-                                           int cb) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) m = max(m, abs_bits(v[j]));
-  const uint32_t byte = ckpt_scale_byte(m);
-  const float inv = ckpt_inv_scale(byte);
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j] = pack_e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv,
-                       v[4 * j + 3] * inv);
-  uint4 *dst = reinterpret_cast<uint4 *>(k.q + row * cp + 32 * cb);
-  __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
-  __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
-  k.scale[row * (cp >> 5) + cb] = static_cast<uint8_t>(byte);
-}
-__device__ __forceinline__ void read_row32(float *v, CkptView k, long long row, int cp, int cb) {
-  const uint4 *src = reinterpret_cast<const uint4 *>(k.q + row * cp + 32 * cb);
-  const uint4 a = __ldg(src), b = __ldg(src + 1);
-  const float sc = ckpt_scale(__ldg(k.scale + row * (cp >> 5) + cb));
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 f = unpack_e4m3x4(w[j], sc);
-    v[4 * j] = f.x;
-    v[4 * j + 1] = f.y;
-    v[4 * j + 2] = f.z;
-    v[4 * j + 3] = f.w;
-  }
-}
-
-// dz and xh of one element.
-__device__ __forceinline__ float grad_z(float dy, float xv, float mean, float rstd, float ga,
-                                        float be, int silu, float *xh) {
-  *xh = (xv - mean) * rstd;
-  if (!silu) return dy;
-  const float z = fmaf(*xh, ga, be);
-  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-  return dy * (s * fmaf(z, 1.0f - s, 1.0f));
-}
-
 // Eight channels of a pixel, in packed pairs: z = (x - mean) scale + beta with
 // scale = rstd gamma.
 struct Affine8 {
@@ -182,6 +139,119 @@ inline bool wide_ok(int c, const T *...p) {
   return c % 8 == 0 && (((reinterpret_cast<uintptr_t>(p) & 31) == 0) && ...);
 }
 
+// ------------------------------------------------------------- NCHW pieces
+// 32 channels of one pixel in a thread's registers, packed pairs; a warp's lanes
+// are 32 neighbouring pixels (a "run"), so that the planes are read and written
+// coalesced and a checkpoint block is one thread's.
+struct Row32 {
+  uint64_t v[16];
+};
+// Per pair of channels: the affine of Affine8, and for the backward pass the
+// group means of dx = scale dz + (k1 + dev k2).
+struct PairAffine {
+  uint64_t nmean, scale, beta, k1, k2;
+};
+__device__ __forceinline__ Row32 load_planes(const float *p, long long plane, int left) {
+  Row32 r;
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = j < left ? __ldcs(p + j * plane) : 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) r.v[j] = pk2(v[2 * j], v[2 * j + 1]);
+  return r;
+}
+__device__ __forceinline__ void store_planes(float *p, long long plane, int left,
+                                             const Row32 &r) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (2 * j < left) __stcs(p + (2 * j) * plane, lo2(r.v[j]));
+    if (2 * j + 1 < left) __stcs(p + (2 * j + 1) * plane, hi2(r.v[j]));
+  }
+}
+__device__ __forceinline__ void keep_row32(const Row32 &r, CkptView k, long long row, int cp,
+                                           int cb) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) m = max_abs3(m, lo2(r.v[j]), hi2(r.v[j]));
+  const uint32_t byte = ckpt_scale_byte(__float_as_uint(m));
+  const float inv = ckpt_inv_scale(byte);
+  const uint64_t i2 = pk2(inv, inv);
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint64_t a = mul2(r.v[2 * j], i2), b = mul2(r.v[2 * j + 1], i2);
+    w[j] = pack_e4m3x4(lo2(a), hi2(a), lo2(b), hi2(b));
+  }
+  uint4 *dst = reinterpret_cast<uint4 *>(k.q + row * cp + 32 * cb);
+  __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  k.scale[row * (cp >> 5) + cb] = static_cast<uint8_t>(byte);
+}
+__device__ __forceinline__ Row32 read_row32(CkptView k, long long row, int cp, int cb) {
+  const uint4 *src = reinterpret_cast<const uint4 *>(k.q + row * cp + 32 * cb);
+  const uint4 a = __ldg(src), b = __ldg(src + 1);
+  const float sc = ckpt_scale(__ldg(k.scale + row * (cp >> 5) + cb));
+  const Oct o[4] = {unpack_oct(make_uint2(a.x, a.y), sc), unpack_oct(make_uint2(a.z, a.w), sc),
+                    unpack_oct(make_uint2(b.x, b.y), sc), unpack_oct(make_uint2(b.z, b.w), sc)};
+  Row32 r;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) r.v[j] = o[j / 4].v[j % 4];
+  return r;
+}
+// The affines of the 32-channel block that starts at channel ch0, zeros past c,
+// by the block's first 16 threads.
+__device__ __forceinline__ void load_pairs(PairAffine *out, const float2 *stats,
+                                           const float *gamma, const float *beta, int ch0, int c,
+                                           int cg, int t) {
+  float m[2], s[2], b[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int ch = ch0 + 2 * t + h;
+    const bool in = ch < c;
+    const float2 st = in ? stats[ch / cg] : make_float2(0.f, 0.f);
+    m[h] = -st.x;
+    s[h] = in ? st.y * gamma[ch] : 0.f;
+    b[h] = in ? beta[ch] : 0.f;
+  }
+  out[t].nmean = pk2(m[0], m[1]);
+  out[t].scale = pk2(s[0], s[1]);
+  out[t].beta = pk2(b[0], b[1]);
+}
+__device__ __forceinline__ Row32 forward32(const Row32 &x, const PairAffine *f, int silu) {
+  Row32 o;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint64_t z = fma2(add2(x.v[j], f[j].nmean), f[j].scale, f[j].beta);
+    o.v[j] = silu ? mul2(z, sigmoid2(z)) : z;
+  }
+  return o;
+}
+// dz of 32 elements; dev receives x - mean.
+__device__ __forceinline__ Row32 grad32(const Row32 &dy, const Row32 &x, const PairAffine *f,
+                                        int silu, Row32 *dev) {
+  Row32 o;
+  const uint64_t one = pk2(1.f, 1.f), minus = pk2(-1.f, -1.f);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    dev->v[j] = add2(x.v[j], f[j].nmean);
+    o.v[j] = dy.v[j];
+    if (silu) {
+      const uint64_t z = fma2(dev->v[j], f[j].scale, f[j].beta);
+      const uint64_t s = sigmoid2(z);
+      o.v[j] = mul2(dy.v[j], mul2(s, fma2(z, fma2(s, minus, one), one)));
+    }
+  }
+  return o;
+}
+// dx of 32 elements from dz, in place of dz.
+__device__ __forceinline__ Row32 dx32(const Row32 &dz, const Row32 &dev, const PairAffine *f) {
+  Row32 o;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    o.v[j] = fma2(f[j].scale, dz.v[j], fma2(dev.v[j], f[j].k2, f[j].k1));
+  return o;
+}
+
 // Sums of 32 values over a warp, value j to lane j: 31 shuffles; each step
 // halves the values a lane still carries. The order is fixed.
 __device__ __forceinline__ float reduce_scatter32(float (&v)[32], int lane) {
@@ -196,6 +266,42 @@ __device__ __forceinline__ float reduce_scatter32(float (&v)[32], int lane) {
       }
   }
   return v[0];
+}
+__device__ __forceinline__ float sum_to_lane(const Row32 &r, int lane) {
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    v[2 * j] = lo2(r.v[j]);
+    v[2 * j + 1] = hi2(r.v[j]);
+  }
+  return reduce_scatter32(v, lane);
+}
+// (sum dz, sum dz dev) of a run, channel j to lane j.
+__device__ __forceinline__ float2 run_sums(const Row32 &dz, const Row32 &dev, int lane) {
+  Row32 t;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) t.v[j] = mul2(dz.v[j], dev.v[j]);
+  const float a = sum_to_lane(dz, lane);
+  return make_float2(a, sum_to_lane(t, lane));
+}
+// The triple of a run's `count` leading lanes, channel j to lane j: deviations
+// from lane 0's values.
+__device__ __forceinline__ Triple run_triple(const Row32 &x, int count, int lane) {
+  Row32 d, q;
+  float first = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float a = __shfl_sync(0xffffffffu, lo2(x.v[j]), 0);
+    const float b = __shfl_sync(0xffffffffu, hi2(x.v[j]), 0);
+    if (lane == 2 * j) first = a;
+    if (lane == 2 * j + 1) first = b;
+    d.v[j] = lane < count ? add2(x.v[j], pk2(-a, -b)) : 0;
+    q.v[j] = mul2(d.v[j], d.v[j]);
+  }
+  const float s = sum_to_lane(d, lane), ss = sum_to_lane(q, lane);
+  if (count <= 0) return {0.f, 0.f, 0.f};
+  const float m = s / count;
+  return {static_cast<float>(count), first + m, fmaxf(ss - s * m, 0.f)};
 }
 
 }  // namespace vae
