@@ -471,7 +471,7 @@ class Checkpoint:
     [rows, cp / 32] (float8_e8m0fnu) are views: a value is payload * scale of
     its block of 32 channels."""
 
-    __slots__ = ("buf", "rows", "c")
+    __slots__ = ("rows", "c", "_cp", "_at", "_bytes")
 
     def __init__(self, buf, rows, c):
         import torch
@@ -480,7 +480,13 @@ class Checkpoint:
             raise TypeError("buf must be a contiguous uint8 CUDA tensor")
         if rows <= 0 or c <= 0 or buf.numel() < self.nbytes(rows, c):
             raise ValueError(f"buf holds no checkpoint of {rows} rows of {c} channels")
-        self.buf, self.rows, self.c = buf, rows, c
+        self._sizes(rows, c)
+        self._bytes = buf
+
+    def _sizes(self, rows, c):
+        self.rows, self.c = rows, c
+        self._cp = (c + 31) // 32 * 32
+        self._at = (rows * self._cp + 255) // 256 * 256  # of the scales
 
     @staticmethod
     def nbytes(rows, c):
@@ -491,24 +497,31 @@ class Checkpoint:
     def _make(cls, rows, c, device):
         import torch
         self = cls.__new__(cls)
-        self.buf = torch.empty(cls.nbytes(rows, c), dtype=torch.uint8, device=device)
-        self.rows, self.c = rows, c
+        self._sizes(rows, c)
+        self._bytes = torch.empty(self._at + rows * (self._cp // 32), dtype=torch.float8_e4m3fn,
+                                  device=device)
         return self
 
     @property
-    def payload(self):
+    def buf(self):
         import torch
-        cp = (self.c + 31) // 32 * 32
-        return self.buf.view(torch.float8_e4m3fn).as_strided((self.rows, cp), (cp, 1))
+        return self._bytes.view(torch.uint8)
+
+    @property
+    def payload(self):
+        # (as_strided's offset counts from the storage's start)
+        import torch
+        k = self._bytes
+        if k.dtype is not torch.float8_e4m3fn:
+            k = k.view(torch.float8_e4m3fn)
+        return k.as_strided((self.rows, self._cp), (self._cp, 1), k.storage_offset())
 
     @property
     def scale(self):
         import torch
-        cp = (self.c + 31) // 32 * 32
-        # (as_strided's offset counts from the storage's start)
-        at = self.buf.storage_offset() + (self.rows * cp + 255) // 256 * 256
-        return self.buf.view(torch.float8_e8m0fnu).as_strided((self.rows, cp // 32),
-                                                              (cp // 32, 1), at)
+        k, n = self._bytes, self._cp // 32
+        return k.view(torch.float8_e8m0fnu).as_strided((self.rows, n), (n, 1),
+                                                       k.storage_offset() + self._at)
 
 
 def _refuse(t, shape, device, name):
@@ -521,9 +534,8 @@ def _refuse(t, shape, device, name):
 
 def _at(t, shape, device, name):
     """The address of a contiguous float32 tensor of `shape` on `device`."""
-    import torch
     try:
-        if (t.dtype is torch.float32 and t.shape == shape and t.device == device
+        if (t.dtype is _F32 and t.shape == shape and t.device == device
                 and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
@@ -540,14 +552,19 @@ def _ckpt_at(k, rows, c, device, name):
         raise TypeError(f"{name} must be a Checkpoint")
     if k.rows != rows or k.c != c:
         raise ValueError(f"{name} holds {k.rows} rows of {k.c} channels, not {rows} of {c}")
-    if k.buf.device != device:
-        raise ValueError(f"{name} is on {k.buf.device}, not {device}")
-    return k.buf.data_ptr()
+    if k._bytes.device != device:
+        raise ValueError(f"{name} is on {k._bytes.device}, not {device}")
+    return k._bytes.data_ptr()
+
+
+_F32 = None  # torch.float32, once torch is loaded
 
 
 def _first(x, name):
     """(shape, device) of the tensor the others are compared with."""
     import torch
+    global _F32
+    _F32 = torch.float32
     if not (isinstance(x, torch.Tensor) and x.is_cuda):
         _need(x, name)
     return x.shape, x.device
@@ -582,7 +599,7 @@ def _call(name, device, stream, made, *args):
         for t in made:
             if t is not None:
                 t.record_stream(stream)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -613,7 +630,8 @@ def vae_ckpt_pack(x, layout=VAE_NHWC, stream=None):
     n, c, spatial = _dims(shape, layout)
     at = _at(x, shape, dev, "x")
     k = Checkpoint._make(n * spatial, c, dev)
-    _call("vae_ckpt_pack", dev, stream, (k.buf,), at, n, c, spatial, layout, k.buf.data_ptr())
+    _call("vae_ckpt_pack", dev, stream, (k._bytes,), at, n, c, spatial, layout,
+          k._bytes.data_ptr())
     return k
 
 
@@ -624,7 +642,7 @@ def vae_ckpt_unpack(ckpt, shape, layout=VAE_NHWC, stream=None):
     if not isinstance(ckpt, Checkpoint):
         raise TypeError("ckpt must be a Checkpoint")
     n, c, spatial = _dims(shape, layout)
-    dev = ckpt.buf.device
+    dev = ckpt._bytes.device
     at = _ckpt_at(ckpt, n * spatial, c, dev, "ckpt")
     out = torch.empty(shape, dtype=torch.float32, device=dev)
     _call("vae_ckpt_unpack", dev, stream, (out,), at, n, c, spatial, layout, out.data_ptr())
@@ -649,11 +667,11 @@ def vae_groupnorm_silu_ckpt(x, gamma, beta, groups=32, eps=1e-6, apply_silu=True
     x_ckpt = y_ckpt = kx = ky = pkx = pky = None
     if keep_x:
         x_ckpt = Checkpoint._make(n * spatial, c, dev)
-        kx = x_ckpt.buf
+        kx = x_ckpt._bytes
         pkx = kx.data_ptr()
     if keep_y:
         y_ckpt = Checkpoint._make(n * spatial, c, dev)
-        ky = y_ckpt.buf
+        ky = y_ckpt._bytes
         pky = ky.data_ptr()
     stats = torch.empty((n, max(groups, 1), 2), dtype=torch.float32, device=dev)
     _call("vae_groupnorm_silu_ckpt", dev, stream, (ws, y, kx, ky, stats), px, n, c, spatial,
@@ -735,11 +753,11 @@ def vae_block_norm(u, x, w_post, gate=None, scale=None, w_pre=None, eps=1e-6, ke
     u_ckpt = h_ckpt = rstd = ku = kh = pku = pkh = pr = None
     if keep:
         u_ckpt = Checkpoint._make(n * tokens, c, dev)
-        ku = u_ckpt.buf
+        ku = u_ckpt._bytes
         pku = ku.data_ptr()
         if w_pre is not None:
             h_ckpt = Checkpoint._make(n * tokens, c, dev)
-            kh = h_ckpt.buf
+            kh = h_ckpt._bytes
             pkh = kh.data_ptr()
         rstd = torch.empty((2, n * tokens), dtype=torch.float32, device=dev)
         pr = rstd.data_ptr()

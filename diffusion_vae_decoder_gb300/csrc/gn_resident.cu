@@ -688,6 +688,12 @@ int launch(Kernel kernel, const ResArgs &a, int cl, int n, size_t smem, cudaStre
                                       static_cast<int>(kMaxSmem)));
   if (cl > 8)
     VAE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  if (cl == 1) {  // (a launch with a cluster attribute costs the host more)
+    kernel<<<dim3(1, (a.c + a.slab - 1) / a.slab, n), kThreads, smem, s>>>(a);
+    VAE_LAUNCH_CHECK();
+    count_launches(1);
+    return VAE_OK;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cl, (a.c + a.slab - 1) / a.slab, n);
   cfg.blockDim = dim3(kThreads);

@@ -127,26 +127,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int j = 0; j < 4; ++j) k.v[j] = mul2(k.v[j], pk2(-1.f, -1.f));
   uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
   if (sw.pl < sw.ppi) {
-    constexpr int U = 6;
+    constexpr int D = 6;  // loads in flight
+    Oct v[D];
+    auto fetch = [&](int i) {
+      const unsigned p = sw.pixel(i);
+      return load_oct<WIDE, false>(row_at(src, p, c), sw.in(i, p) ? sw.left : 0);
+    };
+#pragma unroll
+    for (int u = 0; u < D; ++u) v[u] = fetch(u);
 #pragma unroll 1
-    for (int i = 0; i < sw.iters; i += U) {
-      Oct v[U];
+    for (int i = 0; i < sw.iters; i += D)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const unsigned p = sw.pixel(i + u);
-        v[u] = load_oct<WIDE, false>(row_at(src, p, c), sw.in(i + u, p) ? sw.left : 0);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < D; ++u) {
+        const Oct x8 = v[u];
+        v[u] = fetch(i + u + D);
         if (sw.in(i + u, sw.pixel(i + u))) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint64_t d = add2(v[u].v[j], k.v[j]);
+            const uint64_t d = add2(x8.v[j], k.v[j]);
             a[j] = add2(a[j], d);
             b[j] = fma2(d, d, b[j]);
           }
         }
-    }
+      }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       red[sw.pl * cp + sw.ch + 2 * j] = make_float2(lo2(a[j]), lo2(b[j]));
@@ -238,25 +241,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   float *dst = y + sw.row0 * c + sw.ch;
   kx = from_row(kx, sw.row0, cp);
   ky = from_row(ky, sw.row0, cp);
-  constexpr int U = 4;
+  constexpr int D = 4;  // loads in flight
+  Oct v[D];
+  auto fetch = [&](int i) {
+    const unsigned p = sw.pixel(i);
+    return load_oct<WIDE, true>(row_at(src, p, c), sw.in(i, p) ? sw.left : 0);
+  };
+#pragma unroll
+  for (int u = 0; u < D; ++u) v[u] = fetch(sw.iters - 1 - u);
 #pragma unroll 1
-  for (int top = sw.iters - 1; top >= 0; top -= U) {
-    Oct v[U];
+  for (int top = sw.iters - 1; top >= 0; top -= D)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned p = sw.pixel(top - u);
-      v[u] = load_oct<WIDE, true>(row_at(src, p, c), sw.in(top - u, p) ? sw.left : 0);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned p = sw.pixel(top - u);
-      const bool in = sw.in(top - u, p) && sw.pl < sw.ppi;
-      if (kx.q) keep_oct(kx, p, cp, sw.ch, in, v[u]);
-      const Oct o = forward8<SILU>(v[u], f);
+    for (int u = 0; u < D; ++u) {
+      const int i = top - u;
+      const unsigned p = sw.pixel(i);
+      const bool in = sw.in(i, p) && sw.pl < sw.ppi;
+      const Oct x8 = v[u];
+      v[u] = fetch(i - D);
+      if (kx.q) keep_oct(kx, p, cp, sw.ch, in, x8);
+      const Oct o = forward8<SILU>(x8, f);
       store_oct<WIDE>(row_at(dst, p, c), in ? sw.left : 0, o);
       if (ky.q) keep_oct(ky, p, cp, sw.ch, in, o);
     }
-  }
 }
 
 // grid (slabs, cp / 32, n): a thread per pixel and 32 channels.
@@ -298,35 +304,37 @@ __global__ void __launch_bounds__(kThreads, 2)
     const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
     const float *src = dy + sw.row0 * c + sw.ch;
     const CkptView kv = from_row(k, sw.row0, cp);
-    constexpr int U = 4;
-#pragma unroll 1
-    for (int i = 0; i < sw.iters; i += U) {
-      Oct g[U];
-      uint2 q[U];
-      uint32_t sb[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const unsigned p = sw.pixel(i + u);
-        const bool in = sw.in(i + u, p);
-        g[u] = load_oct<WIDE, false>(row_at(src, p, c), in ? sw.left : 0);
-        q[u] = make_uint2(0, 0);
-        sb[u] = 0;
-        if (in) {
-          q[u] = __ldg(reinterpret_cast<const uint2 *>(row_at(kv.q + sw.ch, p, cp)));
-          sb[u] = __ldg(row_at(kv.scale + (sw.ch >> 5), p, cp >> 5));
-        }
+    constexpr int D = 3;  // pixels in flight
+    Oct g[D];
+    uint2 q[D];
+    uint32_t sb[D];
+    auto fetch = [&](int i, int u) {
+      const unsigned p = sw.pixel(i);
+      const bool in = sw.in(i, p);
+      g[u] = load_oct<WIDE, false>(row_at(src, p, c), in ? sw.left : 0);
+      q[u] = make_uint2(0, 0);
+      sb[u] = 0;
+      if (in) {
+        q[u] = __ldg(reinterpret_cast<const uint2 *>(row_at(kv.q + sw.ch, p, cp)));
+        sb[u] = __ldg(row_at(kv.scale + (sw.ch >> 5), p, cp >> 5));
       }
+    };
 #pragma unroll
-      for (int u = 0; u < U; ++u) {  // (a pixel outside has dy = 0 and adds nothing)
+    for (int u = 0; u < D; ++u) fetch(u, u);
+#pragma unroll 1
+    for (int i = 0; i < sw.iters; i += D)
+#pragma unroll
+      for (int u = 0; u < D; ++u) {  // (a pixel outside has dy = 0 and adds nothing)
+        const Oct dy8 = g[u], x8 = unpack_oct(q[u], ckpt_scale(sb[u]));
+        fetch(i + u + D, u);
         Oct dev;
-        const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &dev);
+        const Oct dz = grad8<SILU>(dy8, x8, f, &dev);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           a[j] = add2(a[j], dz.v[j]);
           b[j] = fma2(dz.v[j], dev.v[j], b[j]);
         }
       }
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       red[sw.pl * cp + sw.ch + 2 * j] = make_float2(lo2(a[j]), lo2(b[j]));
@@ -487,38 +495,42 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float *src = dy + sw.row0 * c + sw.ch, *res = dres ? dres + sw.row0 * c + sw.ch : nullptr;
   float *dst = dx + sw.row0 * c + sw.ch;
   const CkptView kv = from_row(k, sw.row0, cp);
-  constexpr int U = 3;
-#pragma unroll 1
-  for (int top = sw.iters - 1; top >= 0; top -= U) {
-    Oct g[U], r[U];
-    uint2 q[U];
-    uint32_t sb[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned p = sw.pixel(top - u);
-      const bool in = sw.in(top - u, p);
-      g[u] = load_oct<WIDE, true>(row_at(src, p, c), in ? sw.left : 0);
-      if (res) r[u] = load_oct<WIDE, true>(row_at(res, p, c), in ? sw.left : 0);
-      q[u] = make_uint2(0, 0);
-      sb[u] = 0;
-      if (in) {
-        q[u] = __ldcs(reinterpret_cast<const uint2 *>(row_at(kv.q + sw.ch, p, cp)));
-        sb[u] = __ldg(row_at(kv.scale + (sw.ch >> 5), p, cp >> 5));
-      }
+  constexpr int D = 3;  // pixels in flight
+  Oct g[D];
+  uint2 q[D];
+  uint32_t sb[D];
+  auto fetch = [&](int i, int u) {
+    const unsigned p = sw.pixel(i);
+    const bool in = sw.in(i, p);
+    g[u] = load_oct<WIDE, true>(row_at(src, p, c), in ? sw.left : 0);
+    q[u] = make_uint2(0, 0);
+    sb[u] = 0;
+    if (in) {
+      q[u] = __ldcs(reinterpret_cast<const uint2 *>(row_at(kv.q + sw.ch, p, cp)));
+      sb[u] = __ldg(row_at(kv.scale + (sw.ch >> 5), p, cp >> 5));
     }
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned p = sw.pixel(top - u);
-      Oct dev, o;
-      const Oct dz = grad8<SILU>(g[u], unpack_oct(q[u], ckpt_scale(sb[u])), f, &dev);
+  for (int u = 0; u < D; ++u) fetch(sw.iters - 1 - u, u);
+#pragma unroll 1
+  for (int top = sw.iters - 1; top >= 0; top -= D)
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      const int i = top - u;
+      const unsigned p = sw.pixel(i);
+      const int left = sw.in(i, p) ? sw.left : 0;
+      const Oct dy8 = g[u], x8 = unpack_oct(q[u], ckpt_scale(sb[u]));
+      Oct dev, o, r = {{0, 0, 0, 0}};
+      if (res) r = load_oct<WIDE, true>(row_at(res, p, c), left);
+      fetch(i - D, u);
+      const Oct dz = grad8<SILU>(dy8, x8, f, &dev);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         o.v[j] = fma2(f.scale[j], dz.v[j], fma2(dev.v[j], k2[j], k1[j]));
-        if (res) o.v[j] = add2(o.v[j], r[u].v[j]);
+        o.v[j] = add2(o.v[j], r.v[j]);
       }
-      store_oct<WIDE>(row_at(dst, p, c), sw.in(top - u, p) ? sw.left : 0, o);
+      store_oct<WIDE>(row_at(dst, p, c), left, o);
     }
-  }
 }
 
 // grid (slabs, cp / 32, n).
