@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 2 : 1)
   }
 }
 
-// Block b: channels [32 b, 32 b + 32); lanes are channels, warps stride over
-// the slabs, samples in order.
+// Block b: channels [32 b, 32 b + 32); lanes are channels. The 32 warps split
+// the samples (up to 32 at a time) and their slabs; fixed order.
 __global__ void __launch_bounds__(1024)
     block_norm_merge(const float2 *__restrict__ part, int n, int slabs, int c,
                      const float *__restrict__ w_post, const float *__restrict__ gate,
@@ -315,26 +315,45 @@ __global__ void __launch_bounds__(1024)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = 32 * blockIdx.x + lane;
   const float wpo = ch < c ? w_post[ch] : 0.f, sc = scale && ch < c ? scale[ch] : 1.f;
-  float sum_s = 0.f, sum_p = 0.f;  // sum of gate S; sum of dy hh
-  for (int i = 0; i < n; ++i) {
+  const int per = 32 / min(n, 32);  // warps of a sample
+  float sum_s = 0.f, sum_p = 0.f;   // sum of gate S; sum of dy hh
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + warp / per;
     float2 t = make_float2(0.f, 0.f);
-    if (ch < c)
-      for (int s = warp; s < slabs; s += 32) {
-        const float2 v = part[(static_cast<size_t>(i) * slabs + s) * c + ch];
+    if (ch < c && i < min(n, i0 + 32)) {
+      const float2 *e = part + static_cast<size_t>(i) * slabs * c + ch;
+#pragma unroll 4
+      for (int s = warp % per; s < slabs; s += per) {
+        const float2 v = __ldg(e + static_cast<size_t>(s) * c);
         t.x += v.x;
         t.y += v.y;
       }
+    }
     red[warp][lane] = t;
     __syncthreads();
-    if (warp == 0 && ch < c) {
-      for (int w = 1; w < 32; ++w) {
-        t.x += red[w][lane].x;
-        t.y += red[w][lane].y;
+    const int j = i0 + warp;  // one warp per sample adds its warps' sums
+    const bool mine = ch < c && j < min(n, i0 + 32);
+    if (mine) {
+      t = red[warp * per][lane];
+#pragma unroll 4
+      for (int w = 1; w < per; ++w) {
+        t.x += red[warp * per + w][lane].x;
+        t.y += red[warp * per + w][lane].y;
       }
-      if (dgate) dgate[static_cast<size_t>(i) * c + ch] = sc * wpo * t.x;
-      sum_s = fmaf(gate ? gate[static_cast<size_t>(i) * c + ch] : 1.f, t.x, sum_s);
-      sum_p += t.y;
+      const size_t at = static_cast<size_t>(j) * c + ch;
+      if (dgate) dgate[at] = sc * wpo * t.x;
+      if (gate) t.x *= gate[at];
     }
+    __syncthreads();
+    red[warp][lane] = mine ? t : make_float2(0.f, 0.f);
+    __syncthreads();
+    if (warp == 0)
+#pragma unroll 4
+      for (int w = 0; w < min(32, n - i0); ++w) {
+        sum_s += red[w][lane].x;
+        sum_p += red[w][lane].y;
+      }
     __syncthreads();
   }
   if (warp == 0 && ch < c) {

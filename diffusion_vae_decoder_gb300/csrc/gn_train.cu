@@ -32,7 +32,7 @@ constexpr int kThreads = 256;      // NHWC kernels
 constexpr int kPixThreads = 128;   // NCHW kernels: one pixel per thread
 constexpr int kBlocks = 2 * 152;   // NHWC: the resident blocks, two per SM
 constexpr int kPixBlocks = 8 * 152;
-constexpr int kMergeThreads = 512;
+constexpr int kMergeThreads = 320;  // a block's slabs in one round
 
 // Blocks (slabs of pixels) per sample.
 int slabs_nhwc(int n, int c, long long spatial) {
@@ -57,24 +57,25 @@ __global__ void __launch_bounds__(kStatThreads)
   stats_segment_nchw(x, c, spatial, groups, gridDim.y, blockIdx.x, blockIdx.y, red, part);
 }
 
-// One block per (sample, group): merges its partials in a fixed order.
+// One block per (sample, group): merges its partials in a fixed order. (Little
+// code: a kernel this short is bound by fetching its instructions.)
 __global__ void __launch_bounds__(kMergeThreads)
     ckpt_stats_merge(const float *__restrict__ part, int slabs, float eps,
                      float2 *__restrict__ stats) {
-  __shared__ Triple red[kMergeThreads];
+  __shared__ Triple red[kMergeThreads / 32];
   const float *e = part + static_cast<size_t>(blockIdx.x) * slabs * 3;
   Triple acc{0.f, 0.f, 0.f};
-  for (int b = threadIdx.x; b < slabs; b += blockDim.x)
+#pragma unroll 1
+  for (int b = threadIdx.x; b < slabs; b += kMergeThreads)
     acc = merge(acc, Triple{e[3 * b], e[3 * b + 1], e[3 * b + 2]});
-  red[threadIdx.x] = acc;
+  acc = warp_merge(acc);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
   __syncthreads();
-  for (int w = blockDim.x / 2; w > 0; w >>= 1) {
-    if (threadIdx.x < w) red[threadIdx.x] = merge(red[threadIdx.x], red[threadIdx.x + w]);
-    __syncthreads();
-  }
   if (threadIdx.x == 0) {
-    const double var = red[0].n > 0.f ? static_cast<double>(red[0].m2) / red[0].n : 0.0;
-    stats[blockIdx.x] = make_float2(red[0].mean, static_cast<float>(1.0 / sqrt(var + eps)));
+#pragma unroll 1
+    for (int w = 1; w < kMergeThreads / 32; ++w) acc = merge(acc, red[w]);
+    const float var = acc.n > 0.f ? acc.m2 / acc.n : 0.f;
+    stats[blockIdx.x] = make_float2(acc.mean, 1.0f / sqrtf(var + eps));
   }
 }
 
@@ -117,24 +118,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     ckpt_stats_nhwc(const float *__restrict__ x, int c, long long spatial, int groups,
                     float *__restrict__ part) {
   __shared__ float2 red[kThreads * 8];
+  __shared__ float shift[1024];
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
   x += sw.row0 * c;
   const unsigned origin = blockIdx.x * sw.ppi;  // (every block has a pixel)
   const float *src = x + sw.ch;
-  Oct k = load_oct<WIDE, false>(row_at(src, origin, c), sw.left);
+  constexpr int D = 6;  // loads in flight
+  Oct k = load_oct<WIDE, false>(row_at(src, origin, c), sw.left), v[D];
+  auto fetch = [&](int i) {
+    const unsigned p = sw.pixel(i);
+    return load_oct<WIDE, false>(row_at(src, p, c), sw.in(i, p) ? sw.left : 0);
+  };
+#pragma unroll
+  for (int u = 0; u < D; ++u) v[u] = fetch(u);
+  if (sw.pl == 0)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (2 * j < sw.left) {
+        shift[sw.ch + 2 * j] = lo2(k.v[j]);
+        shift[sw.ch + 2 * j + 1] = hi2(k.v[j]);
+      }
 #pragma unroll
   for (int j = 0; j < 4; ++j) k.v[j] = mul2(k.v[j], pk2(-1.f, -1.f));
   uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
   if (sw.pl < sw.ppi) {
-    constexpr int D = 6;  // loads in flight
-    Oct v[D];
-    auto fetch = [&](int i) {
-      const unsigned p = sw.pixel(i);
-      return load_oct<WIDE, false>(row_at(src, p, c), sw.in(i, p) ? sw.left : 0);
-    };
-#pragma unroll
-    for (int u = 0; u < D; ++u) v[u] = fetch(u);
 #pragma unroll 1
     for (int i = 0; i < sw.iters; i += D)
 #pragma unroll
@@ -178,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = lane; i < cg; i += 32) {
       const float2 v = red[g * cg + i];
       const float m = v.x / total;
-      t = merge(t, Triple{total, row_at(x, origin, c)[g * cg + i] + m,
-                          fmaxf(v.y - v.x * m, 0.f)});
+      t = merge(t, Triple{total, shift[g * cg + i] + m, fmaxf(v.y - v.x * m, 0.f)});
     }
     t = warp_merge(t);
     if (lane == 0) {
@@ -236,7 +243,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float *__restrict__ beta, float *y, CkptView kx, CkptView ky) {
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
-  const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
   const float *src = x + sw.row0 * c + sw.ch;
   float *dst = y + sw.row0 * c + sw.ch;
   kx = from_row(kx, sw.row0, cp);
@@ -249,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) v[u] = fetch(sw.iters - 1 - u);
+  const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
 #pragma unroll 1
   for (int top = sw.iters - 1; top >= 0; top -= D)
 #pragma unroll
@@ -301,7 +308,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cp = (c + 31) & ~31;
   uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
   if (sw.pl < sw.ppi) {
-    const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
     const float *src = dy + sw.row0 * c + sw.ch;
     const CkptView kv = from_row(k, sw.row0, cp);
     constexpr int D = 3;  // pixels in flight
@@ -321,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
 #pragma unroll
     for (int u = 0; u < D; ++u) fetch(u, u);
+    const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
 #pragma unroll 1
     for (int i = 0; i < sw.iters; i += D)
 #pragma unroll
@@ -397,42 +404,56 @@ __global__ void __launch_bounds__(kPixThreads)
   }
 }
 
-// Block b: channels [32 b, 32 b + 32), every sample. 32 x 32 threads: lanes
-// are channels, warps stride over the slabs; fixed order. Writes the
-// per-(sample, channel) sums and, over the samples, dbeta and dgamma.
+// Block (b, i): channels [32 b, 32 b + 32) of sample i; lanes are channels, warps
+// stride over the slabs; fixed order.
 __global__ void __launch_bounds__(1024)
-    ckpt_sums_merge(const float2 *__restrict__ part, int n, int slabs, int c,
-                    float2 *__restrict__ sums, float *__restrict__ dgamma,
-                    float *__restrict__ dbeta) {
+    ckpt_sums_merge(const float2 *__restrict__ part, int slabs, int c,
+                    float2 *__restrict__ sums) {
   __shared__ float2 red[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = 32 * blockIdx.x + lane;
-  float tb = 0.f, tg = 0.f;
-  for (int i = 0; i < n; ++i) {
-    float2 t = make_float2(0.f, 0.f);
-    if (ch < c)
-      for (int s = warp; s < slabs; s += 32) {
-        const float2 v = part[(static_cast<size_t>(i) * slabs + s) * c + ch];
-        t.x += v.x;
-        t.y += v.y;
-      }
-    red[warp][lane] = t;
-    __syncthreads();
-    if (warp == 0 && ch < c) {
-      for (int w = 1; w < 32; ++w) {
-        t.x += red[w][lane].x;
-        t.y += red[w][lane].y;
-      }
-      sums[static_cast<size_t>(i) * c + ch] = t;
-      tb += t.x;
-      tg += t.y;
+  const float2 *e = part + static_cast<size_t>(blockIdx.y) * slabs * c + ch;
+  float2 t = make_float2(0.f, 0.f);
+  if (ch < c)
+#pragma unroll 4
+    for (int s = warp; s < slabs; s += 32) {
+      const float2 v = __ldg(e + static_cast<size_t>(s) * c);
+      t.x += v.x;
+      t.y += v.y;
     }
-    __syncthreads();
-  }
+  red[warp][lane] = t;
+  __syncthreads();
   if (warp == 0 && ch < c) {
-    if (dbeta) dbeta[ch] = tb;
-    if (dgamma) dgamma[ch] = tg;
+#pragma unroll 4
+    for (int w = 1; w < 32; ++w) {
+      t.x += red[w][lane].x;
+      t.y += red[w][lane].y;
+    }
+    sums[static_cast<size_t>(blockIdx.y) * c + ch] = t;
   }
+}
+
+// dbeta and dgamma of channels [first, last): sums over the samples, in order.
+__device__ __forceinline__ void param_grads(const float2 *__restrict__ sums, int n, int c,
+                                            int first, int last, float *__restrict__ dgamma,
+                                            float *__restrict__ dbeta) {
+  for (int ch = first + threadIdx.x; ch < last; ch += blockDim.x) {
+    float2 t = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float2 v = sums[static_cast<size_t>(i) * c + ch];
+      t.x += v.x;
+      t.y += v.y;
+    }
+    if (dbeta) dbeta[ch] = t.x;
+    if (dgamma) dgamma[ch] = t.y;
+  }
+}
+__global__ void __launch_bounds__(128)
+    ckpt_param_grads(const float2 *__restrict__ sums, int n, int c, float *__restrict__ dgamma,
+                     float *__restrict__ dbeta) {
+  const int first = blockIdx.x * blockDim.x;
+  param_grads(sums, n, c, first, min(c, first + static_cast<int>(blockDim.x)), dgamma, dbeta);
 }
 
 // k1[g] = rstd mean_g(gamma dz), k2[g] = rstd mean_g(gamma dz xh) of sample n
@@ -469,29 +490,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     ckpt_dx_nhwc(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
                  const float *__restrict__ beta, const float2 *__restrict__ sums,
-                 const float *dres, float *dx) {
+                 const float *dres, float *dx, float *__restrict__ dgamma,
+                 float *__restrict__ dbeta) {
   __shared__ float2 km[1024];
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31, cg = c / groups;
-  group_means(km, sums, blockIdx.y, c, groups, spatial, stats, gamma, 0, groups);
-  if (sw.pl >= sw.ppi) return;
-  const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
-  // dx = scale dz + (k1 + dev k2): both means negated, k2 with the rstd of xh
-  uint64_t k1[4], k2[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float2 m[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      m[h] = make_float2(0.f, 0.f);
-      if (2 * j + h < sw.left) {
-        const int g = (sw.ch + 2 * j + h) / cg;
-        m[h] = make_float2(-km[g].x, -km[g].y * stats[blockIdx.y * groups + g].y);
-      }
-    }
-    k1[j] = pk2(m[0].x, m[1].x);
-    k2[j] = pk2(m[0].y, m[1].y);
-  }
   const float *src = dy + sw.row0 * c + sw.ch, *res = dres ? dres + sw.row0 * c + sw.ch : nullptr;
   float *dst = dx + sw.row0 * c + sw.ch;
   const CkptView kv = from_row(k, sw.row0, cp);
@@ -512,6 +515,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) fetch(sw.iters - 1 - u, u);
+  group_means(km, sums, blockIdx.y, c, groups, spatial, stats, gamma, 0, groups);
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
+    param_grads(sums, gridDim.y, c, 0, c, dgamma, dbeta);
+  if (sw.pl >= sw.ppi) return;
+  const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
+  // dx = scale dz + (k1 + dev k2): both means negated, k2 with the rstd of xh
+  uint64_t k1[4], k2[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m[h] = make_float2(0.f, 0.f);
+      if (2 * j + h < sw.left) {
+        const int g = (sw.ch + 2 * j + h) / cg;
+        m[h] = make_float2(-km[g].x, -km[g].y * stats[blockIdx.y * groups + g].y);
+      }
+    }
+    k1[j] = pk2(m[0].x, m[1].x);
+    k2[j] = pk2(m[0].y, m[1].y);
+  }
 #pragma unroll 1
   for (int top = sw.iters - 1; top >= 0; top -= D)
 #pragma unroll
@@ -538,7 +562,8 @@ __global__ void __launch_bounds__(kPixThreads)
     ckpt_dx_nchw(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
                  const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
-                 const float *dres, float *dx) {
+                 const float *dres, float *dx, float *__restrict__ dgamma,
+                 float *__restrict__ dbeta) {
   __shared__ PairAffine aff[16];
   __shared__ float2 km[32];
   const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31, cg = c / groups;
@@ -575,6 +600,8 @@ __global__ void __launch_bounds__(kPixThreads)
     }
     store_planes(dx + base + p, spatial, left, o);
   }
+  if (blockIdx.x == 0 && n == 0)
+    param_grads(sums, gridDim.z, c, 32 * cb, 32 * cb + chans, dgamma, dbeta);
 }
 
 // ------------------------------------------------------------- workspaces
@@ -636,7 +663,7 @@ int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int group
     ckpt_stats_nchw<<<dim3(ng, slabs), kStatThreads, 0, s>>>(x, c, spatial, groups, w.part);
   }
   VAE_LAUNCH_CHECK();
-  ckpt_stats_merge<<<ng, slabs > 128 ? kMergeThreads : 128, 0, s>>>(w.part, slabs, eps, st);
+  ckpt_stats_merge<<<ng, kMergeThreads, 0, s>>>(w.part, slabs, eps, st);
   VAE_LAUNCH_CHECK();
   if (nhwc)
     (wide ? (silu ? ckpt_apply_nhwc<true, true> : ckpt_apply_nhwc<false, true>)
@@ -663,7 +690,7 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   const int rc = gn_backward_resident(dy, k, stats, n, c, spatial, nhwc, groups, gamma, beta,
                                       silu, dres, dx, dgamma, dbeta, w.sums, s);
   if (rc == VAE_OK && n > 1 && (dgamma || dbeta)) {
-    ckpt_sums_merge<<<ckpt_cp(c) / 32, 1024, 0, s>>>(w.sums, 1, n, c, part, dgamma, dbeta);
+    ckpt_param_grads<<<ceil_div(c, 128), 128, 0, s>>>(w.sums, n, c, dgamma, dbeta);
     VAE_LAUNCH_CHECK();
     count_launches(1);
   }
@@ -679,16 +706,17 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
     ckpt_sums_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
                                                 part);
   VAE_LAUNCH_CHECK();
-  ckpt_sums_merge<<<ckpt_cp(c) / 32, 1024, 0, s>>>(part, n, slabs, c, w.sums, dgamma, dbeta);
+  ckpt_sums_merge<<<dim3(ckpt_cp(c) / 32, n), 1024, 0, s>>>(part, slabs, c, w.sums);
   VAE_LAUNCH_CHECK();
   if (nhwc)
     (wide ? (silu ? ckpt_dx_nhwc<true, true> : ckpt_dx_nhwc<false, true>)
           : (silu ? ckpt_dx_nhwc<true, false> : ckpt_dx_nhwc<false, false>))<<<grid, kThreads, 0,
                                                                           s>>>(
-        dy, k, c, spatial, groups, st, gamma, beta, w.sums, dres, dx);
+        dy, k, c, spatial, groups, st, gamma, beta, w.sums, dres, dx, dgamma,
+        dbeta);
   else
     ckpt_dx_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
-                                              w.sums, dres, dx);
+                                              w.sums, dres, dx, dgamma, dbeta);
   VAE_LAUNCH_CHECK();
   count_launches(3);
   return VAE_OK;
