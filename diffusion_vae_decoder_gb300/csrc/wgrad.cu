@@ -4,14 +4,17 @@
 //   dw[o][c][ky][kx] = sum_p dy[p][o] x~[p + (ky, kx) - k/2][c]
 //
 // A GEMM per tap whose reduction runs over the pixels: M = 128 input channels,
-// N = 64 output channels. Both operands arrive pixel by pixel with channels
-// next to each other, so both are M/N-major. An octet of channels takes a run
-// of 16-byte pieces, one per pixel; the tap kx is the same tile read 16 kx
-// bytes further on, so one staged tile serves three taps (TMEM holds three
-// accumulators). Pixels are flattened over rows of w + 1 positions: the extra
-// one, zero in both operands, is the padding on the right of its row and on
-// the left of the next, so any 128 consecutive positions make a tile whatever
-// w is. ky moves the input row: it is one of the grid's units.
+// N = 64 output channels in two parts. Pixels are flattened over rows of w + 1
+// positions: the extra one, zero in both operands, is the padding on the right of
+// its row and on the left of the next, so any 128 consecutive positions make a
+// tile whatever w is. x~ goes to tensor memory (lane = channel, two positions a
+// column). dy goes to shared memory as it comes, pixel by pixel with channels next
+// to each other (M/N-major): an octet of channels is a run of 16-byte pieces, one
+// per position, and the tap kx is the same tile read 16 kx bytes apart, so that
+// one staged tile serves three taps (three accumulators in TMEM). ky moves dy's
+// row: it is one of the grid's units. With both operands in shared memory its
+// bandwidth would bound the kernel: at N = 128 the MMA alone reads 128 bytes a
+// clock (measured: 64.2 clocks a step, N = 64 no less than 53.6).
 //
 // Precision. x~ is e4m3 times a power of two: a half holds it exactly once the
 // block scales are taken relative to the largest of their 32 channels (blocks
@@ -19,9 +22,9 @@
 // channel by a power of two to below 2^15 and split into two halves, hi + lo,
 // 22 significant bits. The MMA reads [hi | lo] as 128 columns next to one A
 // operand, so the two parts have accumulators of their own. The tensor core's
-// accumulator truncates: measured on GB300, the sum of K/8 steps is off by
-// about 5e-9 of its value per step. So a chain of MMAs ends after kChain
-// stages; its sums move to FP32 registers, rounded to nearest.
+// accumulator truncates: measured on GB300, a sum is off by about 1e-8 of its
+// value per step. So a chain of MMAs ends after kChain stages; its sums move to
+// FP32 registers, rounded to nearest.
 //
 // Schedule. (unit, stage) pairs, unit = (input-channel tile, output-channel
 // tile, ky), are cut into equal contiguous ranges, one per SM, so that work
@@ -29,9 +32,9 @@
 // and a last pass adds a unit's pieces in order and undoes the scaling: the
 // same inputs give the same bits.
 //
-// Sixteen warps stage: each thread copies its own 48 bytes of a half stage to
-// shared memory three halves ahead (cp.async, no barrier: it reads back only
-// what it copied), converts them and stores the operands; they also drain the
+// Eight warps bring x~ (global -> registers -> halves -> TMEM), eight bring dy
+// (global -> registers -> halves -> shared memory), each thread loading the next
+// stage's piece where it has just converted this one's; all sixteen drain the
 // accumulators. Three warps turn positions into pixel indexes and block scales
 // ahead of them, one thread issues the MMAs.
 #include "ptx.cuh"
@@ -45,39 +48,33 @@ namespace {
 constexpr int kTM = 128;           // input channels of a tile (TMEM lanes)
 constexpr int kTN = 64;            // output channels
 constexpr int kPos = 128;          // positions of a stage
-constexpr int kHalf = 64;          // positions that the staging threads take at once
-constexpr int kStages = 2;         // staged operands
-constexpr int kRaw = 3;            // raw halves in flight
+constexpr int kStagesA = 2;        // x~ in TMEM, 64 columns each
+constexpr int kStagesB = 4;        // dy in shared memory
 constexpr int kTables = 4;
 constexpr int kChain = 16;         // stages between two drains: 2048 positions
-constexpr int kProducers = 512;    // staging threads: 16 warps
+constexpr int kStagers = 512;      // staging threads: eight warps for x~, eight for dy
+constexpr int kDyThreads = 256;
 constexpr int kTableWarps = 3;     // each makes every third table
-constexpr int kMmaThreads = kProducers + 128;  // one more warpgroup issues and makes tables
+constexpr int kMmaThreads = kStagers + 128;  // one more warpgroup issues and makes tables
 // Registers: the launch gives every thread kLaunchRegs (65536 / 640, rounded
 // down to a multiple of 8); the last warpgroup hands its share to the staging
-// ones, which hold the accumulators.
+// ones, which hold the accumulators and a raw stage.
 constexpr int kLaunchRegs = 96, kStageRegs = 104, kIssueRegs = 64;
 static_assert(4 * kStageRegs + kIssueRegs <= 5 * kLaunchRegs, "the split fits the launch");
-// Positions between two octets, odd so that 16-byte pieces of neighbouring
+// Positions between two octets of dy: odd, so that 16-byte pieces of neighbouring
 // octets fall into different banks.
-constexpr int kSlotsA = kPos + 3, kSlotsB = kPos + 1;
-constexpr uint32_t kSboA = kSlotsA * 16, kSboB = kSlotsB * 16;
-constexpr uint32_t kBytesA = kTM / 8 * kSboA;      // 16 octets
-constexpr uint32_t kBytesB = 2 * kTN / 8 * kSboB;  // hi, then lo
-constexpr uint32_t kStageBytes = (kBytesA + kBytesB + 127) / 128 * 128;
-// A raw half: 32 bytes of dy and 16 of x~ per staging thread, and the two
-// further positions of x~ that the taps of a 3x3 conv reach (16 threads).
-constexpr uint32_t kRawX = kProducers * 32, kRawMore = kRawX + kProducers * 16;
-constexpr uint32_t kRawBytes = kRawMore + 16 * 16;
-// A stage's table: per A slot the checkpoint row (-1: a zero) and the scales
-// of the four 32-channel blocks (pairs of halves); per B position the dy pixel
-// (-1: a zero) and its sample.
-constexpr int kTabX = 0, kTabScale = kPos + 4, kTabDy = kTabScale + 4 * (kPos + 2),
-              kTabImg = kTabDy + kPos, kTableInts = kTabImg + kPos;
-constexpr size_t kSmem =
-    kStages * kStageBytes + kRaw * kRawBytes + kTables * kTableInts * 4 + 256;
+constexpr int kSlots = kPos + 3;
+constexpr uint32_t kSbo = kSlots * 16;
+constexpr uint32_t kLo = kTN / 8 * kSbo;               // from an octet's hi to its lo
+constexpr uint32_t kStageBytes = 2 * kTN / 8 * kSbo;
+// A stage's table: the x~ pixel of each position (-1: a zero), the scales of the
+// four 32-channel blocks (a pair of halves per two positions), the dy pixel of
+// each slot (-1: a zero) and its sample.
+constexpr int kTabX = 0, kTabScale = kPos, kTabDy = kTabScale + 4 * (kPos / 2),
+              kTabImg = kTabDy + kPos + 4, kTableInts = kTabImg + kPos + 4;
+constexpr size_t kSmem = kStagesB * kStageBytes + kTables * kTableInts * 4 + 256;
 static_assert(kSmem <= 227 * 1024, "stages fit an SM");
-static_assert(kRawBytes % 16 == 0 && kStageBytes % 16 == 0 && kTableInts % 4 == 0, "aligned");
+static_assert(kStageBytes % 16 == 0 && kTableInts % 4 == 0, "aligned");
 constexpr int kSMs = 152;
 
 struct WgradParams {
@@ -116,12 +113,6 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ float ld_shared4(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // The power of two that brings a channel's largest |dy| to [2^14, 2^15), as a
 // float (2^127 at most); 1 for a channel with a non-finite value.
 __device__ __forceinline__ int dy_exponent(unsigned amax_bits) {
@@ -165,185 +156,193 @@ struct Chain {
   }
 };
 
-// The rows and scales of a stage's positions, by one warp. A slot `slot` is
-// position q0 + slot read at tap kx = 0, so one to the left.
+// One warp makes a stage's table. dy slot j is position q0 - 1 + j for a 3x3
+// conv (tap kx pairs x~'s position k with slot k + 2 - kx), q0 + j for a 1x1.
 template <int K>
 __device__ __forceinline__ void make_table(const WgradParams &p, unsigned q0, const Unit &un,
                                            const uint32_t *etop, int lane, int *table) {
-  constexpr int kPasses = (kPos + K - 1 + 31) / 32;
   const int nb = p.cp >> 5, b0 = un.ci0 >> 5;
-  int a[kPasses];
-  uint32_t byte[kPasses][4];
+  const bool words = (nb & 3) == 0;  // four blocks' scale bytes in one load
+  const unsigned rows = static_cast<unsigned>(p.n) * p.h;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int slot = lane + 32 * i;
-    const unsigned pos = q0 + slot;
-    int b = -1, img = 0;
-    a[i] = -1;
-    const unsigned row = fast_div(pos, p.wp_magic, p.wp_shift);
-    const int x = static_cast<int>(pos - row * p.wp);
-    img = static_cast<int>(fast_div(row, p.h_magic, p.h_shift));
-    if (row < static_cast<unsigned>(p.n * p.h)) {
-      if (K == 1) {
-        a[i] = b = static_cast<int>(pos);
-      } else {
-        const int y = static_cast<int>(row) - img * p.h + un.ky - 1;
-        if (x > 0 && y >= 0 && y < p.h)
-          a[i] = (static_cast<int>(row) + un.ky - 1) * p.w + x - 1;
-        if (x < p.w) b = static_cast<int>(row) * p.w + x;
+  for (int i = 0; i < 2; ++i) {
+    const int pair = lane + 32 * i;
+    uint32_t four[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned pos = q0 + 2 * pair + h;
+      const unsigned row = fast_div(pos, p.wp_magic, p.wp_shift);
+      const int x = static_cast<int>(pos - row * p.wp);
+      const int pix = row < rows && x < p.w ? static_cast<int>(row) * p.w + x : -1;
+      table[kTabX + 2 * pair + h] = pix;
+      four[h] = 0;
+      if (pix >= 0) {
+        const uint8_t *src = p.xs + static_cast<size_t>(pix) * nb + b0;
+        if (words) {
+          four[h] = __ldg(reinterpret_cast<const uint32_t *>(src));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (b0 + k < nb) four[h] |= static_cast<uint32_t>(__ldg(src + k)) << (8 * k);
+        }
       }
     }
-    if (slot < kPos) {
-      table[kTabDy + slot] = b;
-      table[kTabImg + slot] = img;
-    }
-    if (slot < kPos + K - 1) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        byte[i][k] = a[i] >= 0 && b0 + k < nb
-                         ? __ldg(p.xs + static_cast<size_t>(a[i]) * nb + b0 + k) : 0u;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int slot = lane + 32 * i;
-    if (slot >= kPos + K - 1) continue;
-    table[kTabX + slot] = a[i];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // 2^(7 - d), d binades below the largest block, as a half (zero under
+      // 2^(7 - d), d binades below the largest block, as halves (zero under
       // 2^-25; whatever a block of NaNs is multiplied by, it stays NaN)
-      const int e = 134 + static_cast<int>(byte[i][k]) - static_cast<int>(etop[k]);
-      const float f = __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 254)) << 23);
-      table[kTabScale + 4 * slot + k] = static_cast<int>(h2_bits(__float2half2_rn(f)));
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = 134 + static_cast<int>(four[h] >> (8 * k) & 255u) - static_cast<int>(etop[k]);
+        f[h] = __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 254)) << 23);
+      }
+      table[kTabScale + k * (kPos / 2) + pair] =
+          static_cast<int>(h2_bits(__floats2half2_rn(f[0], f[1])));
     }
+  }
+  for (int slot = lane; slot < kPos + K - 1; slot += 32) {
+    const unsigned pos = q0 + slot - (K == 3);  // (wraps below the first position)
+    const unsigned row = fast_div(pos & 0x3fffffffu, p.wp_magic, p.wp_shift);
+    const int x = static_cast<int>(pos - row * p.wp);
+    const int img = static_cast<int>(fast_div(row, p.h_magic, p.h_shift));
+    const int y = static_cast<int>(row) - img * p.h + (K == 3 ? 1 - un.ky : 0);
+    const bool in = pos < p.positions && x < p.w && y >= 0 && y < p.h;
+    table[kTabDy + slot] =
+        in ? (static_cast<int>(row) + (K == 3 ? 1 - un.ky : 0)) * p.w + x : -1;
+    table[kTabImg + slot] = img;
   }
 }
 
-// K: the conv's kernel size. NHWC: the layout of dy.
-template <int K, bool NHWC>
-struct Producer {
+// One of the 256 threads that bring x~. Warp w fills TMEM lanes 32 (w % 4) ..,
+// one 32-channel block, for positions 64 (w / 4) ..; thread t of it takes four
+// channels 4 (t / 4) + j, which land in lanes t / 4 + 8 j of the quadrant, at
+// two positions in eight.
+struct XStager {
   const WgradParams &p;
-  const int t;
-  // A: 16 input channels (two octets) at one position; four threads cover 64
-  // contiguous bytes, eight lanes store to distinct banks.
-  const int c16, a_slot;
-  // B: an octet of output channels at one position.
-  const int co8, b_slot;
+  const int quad, pair0;  // of the first of its pairs; eight of them, 4 apart
+  const uint8_t *src = nullptr;
+  uint32_t raw[16];
 
-  __device__ explicit Producer(const WgradParams &params)
-      : p(params), t(threadIdx.x), c16((t & 3) | ((t >> 8) << 2)), a_slot((t >> 2) & 63),
-        co8(NHWC ? t & 7 : t >> 6), b_slot(NHWC ? t >> 3 : t & 63) {}
-
-  // Where this thread's channels start, for the unit whose stages are copied.
-  const uint8_t *x_src;
-  const float *dy_src;
-  bool x_in;
-  int dy_in;  // valid channels of the octet
-  __device__ void set_copy_unit(const Unit &un) {
-    const int ch = un.ci0 + 16 * c16, co = un.co0 + 8 * co8;
-    x_in = ch < p.cp;
-    x_src = p.xq + (x_in ? ch : 0);
-    dy_in = min(8, p.cout - co);
-    dy_src = dy_in > 0 ? p.dy + (NHWC ? static_cast<size_t>(co)
-                                      : static_cast<size_t>(co) * p.h * p.w) : p.dy;
+  __device__ explicit XStager(const WgradParams &params)
+      : p(params), quad(threadIdx.x >> 5 & 3),
+        pair0(32 * (threadIdx.x >> 7) + (threadIdx.x & 3)) {}
+  __device__ void set_load_unit(const Unit &un) {
+    const int ch = un.ci0 + 32 * quad + (threadIdx.x >> 2 & 7) * 4;
+    src = ch < p.cp ? p.xq + ch : nullptr;
   }
-
-  __device__ __forceinline__ void copy_x(uint32_t dst, int pix) const {
-    const bool in = pix >= 0 && x_in;
-    const unsigned long long off =
-        static_cast<unsigned long long>(static_cast<unsigned>(in ? pix : 0)) *
-        static_cast<unsigned>(p.cp);
-    cp_async16(dst, x_src + off, in);
-  }
-
-  // Half `half` of a stage.
-  __device__ __forceinline__ void copy(uint32_t raw, const int *table, int half) const {
-    const int b_at = b_slot + kHalf * half, a_at = a_slot + kHalf * half;
-    const int pix = table[kTabDy + b_at];
-    if (NHWC) {
-      const bool in = pix >= 0 && dy_in > 0;
-      const float *src = dy_src + static_cast<unsigned long long>(
-                                      static_cast<unsigned>(in ? pix : 0)) *
-                                      static_cast<unsigned>(p.cout);
-      cp_async16(raw + t * 16, src, in);
-      const bool in4 = in && dy_in > 4;
-      cp_async16(raw + kProducers * 16 + t * 16, in4 ? src + 4 : src, in4);
-    } else {
-      const size_t hw = static_cast<size_t>(p.h) * p.w;
-      const int img = table[kTabImg + b_at];
-      const float *src = dy_src + static_cast<size_t>(img) * (p.cout - 1) * hw + max(pix, 0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = pix >= 0 && i < dy_in;
-        cp_async4(raw + i * (kProducers * 4) + t * 4, in ? src + i * hw : p.dy, in);
-      }
+  __device__ __forceinline__ void load(int i, const int *table) {
+    const int2 pix = *reinterpret_cast<const int2 *>(table + kTabX + 2 * (pair0 + 4 * i));
+    raw[2 * i] = raw[2 * i + 1] = 0;
+    if (src) {
+      if (pix.x >= 0)
+        raw[2 * i] = __ldg(reinterpret_cast<const uint32_t *>(
+            src + static_cast<unsigned long long>(static_cast<unsigned>(pix.x)) *
+                      static_cast<unsigned>(p.cp)));
+      if (pix.y >= 0)
+        raw[2 * i + 1] = __ldg(reinterpret_cast<const uint32_t *>(
+            src + static_cast<unsigned long long>(static_cast<unsigned>(pix.y)) *
+                      static_cast<unsigned>(p.cp)));
     }
-    copy_x(raw + kRawX + t * 16, table[kTabX + a_at]);
-    if (K == 3 && half == 1 && a_slot < 2)
-      copy_x(raw + kRawMore + (a_slot * 8 + c16) * 16, table[kTabX + kPos + a_slot]);
   }
+  // Pair i as halves: channel j of the two positions in out[j].
+  __device__ __forceinline__ void convert(int i, const int *table, uint32_t *out) const {
+    const uint32_t two =
+        static_cast<uint32_t>(table[kTabScale + quad * (kPos / 2) + pair0 + 4 * i]);
+    const __half2 sc = *reinterpret_cast<const __half2 *>(&two);
+    const uint32_t a = __byte_perm(raw[2 * i], raw[2 * i + 1], 0x5140);
+    const uint32_t b = __byte_perm(raw[2 * i], raw[2 * i + 1], 0x7362);
+    out[0] = h2_bits(__hmul2(e4m3x2_half2(a & 0xffffu), sc));
+    out[1] = h2_bits(__hmul2(e4m3x2_half2(a >> 16), sc));
+    out[2] = h2_bits(__hmul2(e4m3x2_half2(b & 0xffffu), sc));
+    out[3] = h2_bits(__hmul2(e4m3x2_half2(b >> 16), sc));
+  }
+};
 
-  // Scales of dy for the unit whose stages are converted.
-  float sdy[8];
+// One of the 256 threads that bring dy: an octet of output channels at slots
+// first + 32 j. A 3x3 conv's stage has 130 slots, whose first two are the last
+// two of the stage before; the threads of the last two carry them over.
+template <int K, bool NHWC>
+struct DyStager {
+  const WgradParams &p;
+  const int co8, first;
+  const float *src = nullptr;
+  int valid = 0;  // channels of the octet
+  float4 raw[4][2];
+  float scale[8];
+
+  __device__ explicit DyStager(const WgradParams &params)
+      : p(params), co8(NHWC ? threadIdx.x & 7 : (threadIdx.x & 255) >> 5),
+        first((NHWC ? (threadIdx.x & 255) >> 3 : threadIdx.x & 31) + (K - 1)) {}
+  __device__ void set_load_unit(const Unit &un) {
+    const int co = un.co0 + 8 * co8;
+    valid = p.cout - co;
+    src = p.dy + (NHWC ? static_cast<size_t>(co) : static_cast<size_t>(co) * p.h * p.w);
+  }
   __device__ void set_unit(const Unit &un) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int co = un.co0 + 8 * co8 + i;
-      sdy[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
+      scale[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
     }
   }
-
-  __device__ __forceinline__ void store_x(uint32_t a, uint32_t raw, int slot,
-                                          const int *table) const {
-    const uint4 v = ld_shared16(raw);
-    const uint32_t two = static_cast<uint32_t>(table[kTabScale + 4 * slot + (c16 >> 1)]);
-    const __half2 sc = *reinterpret_cast<const __half2 *>(&two);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = h2_bits(__hmul2(e4m3x2_half2(w[i] & 0xffffu), sc));
-      o[2 * i + 1] = h2_bits(__hmul2(e4m3x2_half2(w[i] >> 16), sc));
-    }
-    const uint32_t at = a + 2 * c16 * kSboA + slot * 16;
-    st_shared16(at, make_uint4(o[0], o[1], o[2], o[3]));
-    st_shared16(at + kSboA, make_uint4(o[4], o[5], o[6], o[7]));
-  }
-
-  __device__ __forceinline__ void store(uint32_t a, uint32_t b, uint32_t raw,
-                                        const int *table, int half) const {
-    uint64_t v[4];
+  __device__ __forceinline__ void load_slot(float4 (&r)[2], int slot, const int *table) const {
+    const int pix = table[kTabDy + slot];
+    r[0] = r[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pix < 0) return;
     if (NHWC) {
-      const uint4 d0 = ld_shared16(raw + t * 16);
-      const uint4 d1 = ld_shared16(raw + kProducers * 16 + t * 16);
-      v[0] = pk2(__uint_as_float(d0.x), __uint_as_float(d0.y));
-      v[1] = pk2(__uint_as_float(d0.z), __uint_as_float(d0.w));
-      v[2] = pk2(__uint_as_float(d1.x), __uint_as_float(d1.y));
-      v[3] = pk2(__uint_as_float(d1.z), __uint_as_float(d1.w));
+      const float4 *q = reinterpret_cast<const float4 *>(
+          src + static_cast<unsigned long long>(static_cast<unsigned>(pix)) *
+                    static_cast<unsigned>(p.cout));
+      if (valid > 0) r[0] = __ldg(q);
+      if (valid > 4) r[1] = __ldg(q + 1);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = pk2(ld_shared4(raw + 2 * i * (kProducers * 4) + t * 4),
-                   ld_shared4(raw + (2 * i + 1) * (kProducers * 4) + t * 4));
+      const size_t hw = static_cast<size_t>(p.h) * p.w;
+      const float *q = src + static_cast<size_t>(table[kTabImg + slot]) * (p.cout - 1) * hw + pix;
+      if (valid > 0) r[0].x = __ldg(q);
+      if (valid > 1) r[0].y = __ldg(q + hw);
+      if (valid > 2) r[0].z = __ldg(q + 2 * hw);
+      if (valid > 3) r[0].w = __ldg(q + 3 * hw);
+      if (valid > 4) r[1].x = __ldg(q + 4 * hw);
+      if (valid > 5) r[1].y = __ldg(q + 5 * hw);
+      if (valid > 6) r[1].z = __ldg(q + 6 * hw);
+      if (valid > 7) r[1].w = __ldg(q + 7 * hw);
     }
+  }
+  __device__ __forceinline__ uint32_t at(uint32_t stage, int slot) const {
+    return stage + co8 * kSbo + slot * 16;
+  }
+  __device__ __forceinline__ void store_slot(uint32_t stage, int slot,
+                                             const float4 (&r)[2]) const {
+    const uint64_t v[4] = {pk2(r[0].x, r[0].y), pk2(r[0].z, r[0].w), pk2(r[1].x, r[1].y),
+                           pk2(r[1].z, r[1].w)};
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (the scaling is exact, so the difference is what hi dropped)
-      v[i] = mul2(v[i], pk2(sdy[2 * i], sdy[2 * i + 1]));
-      const __half2 h = __floats2half2_rn(lo2(v[i]), hi2(v[i]));
+      const uint64_t s = mul2(v[i], pk2(scale[2 * i], scale[2 * i + 1]));
+      const __half2 h = __floats2half2_rn(lo2(s), hi2(s));
       const float2 f = __half22float2(h);
-      const uint64_t rest = fma2(pk2(f.x, f.y), pk2(-1.f, -1.f), v[i]);
+      const uint64_t rest = fma2(pk2(f.x, f.y), pk2(-1.f, -1.f), s);
       hi[i] = h2_bits(h);
       lo[i] = h2_bits(__floats2half2_rn(lo2(rest), hi2(rest)));
     }
-    const uint32_t at = b + co8 * kSboB + (b_slot + kHalf * half) * 16;
-    st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-    st_shared16(at + kTN / 8 * kSboB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-    store_x(a, raw + kRawX + t * 16, a_slot + kHalf * half, table);
-    if (K == 3 && half == 1 && a_slot < 2)
-      store_x(a, raw + kRawMore + (a_slot * 8 + c16) * 16, kPos + a_slot, table);
+    st_shared16(at(stage, slot), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+    st_shared16(at(stage, slot) + kLo, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+  }
+  // Slots 0 and 1 of a 3x3 stage, by the threads of slots 128 and 129.
+  __device__ __forceinline__ void carry(uint32_t stage, uint32_t before, bool contiguous,
+                                        const int *table) const {
+    if (K == 1 || first + 96 < kPos) return;
+    const int slot = first + 96 - kPos;
+    if (contiguous) {
+      st_shared16(at(stage, slot), ld_shared16(at(before, kPos + slot)));
+      st_shared16(at(stage, slot) + kLo, ld_shared16(at(before, kPos + slot) + kLo));
+    } else {
+      float4 r[2];
+      load_slot(r, slot, table);
+      store_slot(stage, slot, r);
+    }
   }
 };
 
@@ -355,32 +354,38 @@ __host__ __device__ __forceinline__ long long range_start(long long total, int g
 template <int K, bool NHWC>
 __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p) {
   constexpr int TAPS = K;  // kx
+  constexpr uint32_t kAcc = TAPS * 2 * kTN;  // TMEM columns of the accumulators
+  constexpr uint32_t kCols = TAPS == 1 ? 256 : 512;
+  static_assert(kAcc + kStagesA * (kPos / 2) <= kCols, "TMEM holds both");
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *raws = smem + kStages * kStageBytes;
-  int *tables = reinterpret_cast<int *>(raws + kRaw * kRawBytes);
-  uint64_t *full = reinterpret_cast<uint64_t *>(tables + kTables * kTableInts);
-  uint64_t *empty = full + kStages;
-  uint64_t *tab_full = empty + kStages, *tab_empty = tab_full + kTables;
-  uint64_t *acc_done = tab_empty + kTables, *acc_free = acc_done + 1;
+  int *tables = reinterpret_cast<int *>(smem + kStagesB * kStageBytes);
+  uint64_t *a_full = reinterpret_cast<uint64_t *>(tables + kTables * kTableInts);
+  uint64_t *a_empty = a_full + kStagesA, *b_full = a_empty + kStagesA;
+  uint64_t *b_empty = b_full + kStagesB, *tab_full = b_empty + kStagesB;
+  uint64_t *tab_empty = tab_full + kTables, *acc_done = tab_empty + kTables;
+  uint64_t *acc_free = acc_done + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 1);
   volatile uint32_t *abort = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(full + i, kProducers / 32);
-      mbar_init(empty + i, 1);
+    for (int i = 0; i < kStagesA; ++i) {
+      mbar_init(a_full + i, (kStagers - kDyThreads) / 32);
+      mbar_init(a_empty + i, 1);
+    }
+    for (int i = 0; i < kStagesB; ++i) {
+      mbar_init(b_full + i, kDyThreads / 32);
+      mbar_init(b_empty + i, 1);
     }
     for (int i = 0; i < kTables; ++i) {
       mbar_init(tab_full + i, 1);
-      mbar_init(tab_empty + i, kProducers / 32);
+      mbar_init(tab_empty + i, kStagers / 32);
     }
     mbar_init(acc_done, 1);
-    mbar_init(acc_free, kProducers / 32);
+    mbar_init(acc_free, kStagers / 32);
     *abort = 0u;
     fence_mbarrier_init();
   }
-  constexpr uint32_t kCols = TAPS == 1 ? 128 : 512;
-  if (warp == kProducers / 32) {
+  if (warp == kStagers / 32) {
     tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
   }
@@ -396,10 +401,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
     atomicCAS(p.err, 0, static_cast<int>(VAE_EDEVICE_TIMEOUT));
   };
 
-  if (warp < kProducers / 32) {
+  if (warp < kStagers / 32) {
     setmaxnreg_inc<kStageRegs>();
-    Producer<K, NHWC> pr(p);
-    const uint32_t base = smem_u32(smem), raw0 = smem_u32(raws);
     bool ok = true;
     // Waits agree across the warp, so that a timeout leaves it converged.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -407,129 +410,167 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
     };
 
     // This warp drains TMEM lanes 32 (warp % 4) .., output channels 16 (warp / 4) ..
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21) + (warp >> 2) * 16;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     float acc[TAPS][16];
 #pragma unroll
     for (int k = 0; k < TAPS; ++k)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[k][i] = 0.f;
-    int drained = 0;  // stages whose chain end has been looked at
     uint32_t chains = 0;
-    Cursor dr = start;
+    Cursor dr = start;  // the stage whose chain end is looked at next
     Chain dr_chain;
-    auto drain_to = [&](int upto) {  // chains that end before stage `upto`
-      for (; ok && drained < upto; ++drained) {
-        const bool piece_end = drained == count - 1 || dr.stage == p.stages - 1;
-        const int unit = dr.unit;
-        dr.next(p.stages);
-        if (!dr_chain.ends(piece_end)) continue;
-        ok = wait(acc_done, chains & 1);
-        if (!ok) break;
-        tc_fence_after();
+    // Looks at stage `i`; called one stage behind, when the next chain's first
+    // stage is on its way.
+    auto drain = [&](int i) {
+      const bool piece_end = i == count - 1 || dr.stage == p.stages - 1;
+      const int unit = dr.unit;
+      dr.next(p.stages);
+      if (!dr_chain.ends(piece_end)) return;
+      ok = wait(acc_done, chains & 1);
+      if (!ok) return;
+      tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < TAPS; ++k) {
-          float v[16];
-          tmem_ld_16cols(t_lane + k * 2 * kTN, v);
+      for (int k = 0; k < TAPS; ++k) {
+        float v[16];
+        tmem_ld_16cols(t_lane + (warp >> 2) * 16 + k * 2 * kTN, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[k][i] += v[i];
-          tmem_ld_16cols(t_lane + k * 2 * kTN + kTN, v);
+        for (int j = 0; j < 16; ++j) acc[k][j] += v[j];
+        tmem_ld_16cols(t_lane + (warp >> 2) * 16 + k * 2 * kTN + kTN, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[k][i] += v[i];
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_free);
-        ++chains;
-        if (piece_end) {
-          const size_t piece = static_cast<size_t>(unit) + blockIdx.x;
-          float *o = p.part + piece * (TAPS * kTN * kTM) + (warp >> 2) * 16 * kTM +
-                     (warp & 3) * 32 + lane;
+        for (int j = 0; j < 16; ++j) acc[k][j] += v[j];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_free);
+      ++chains;
+      if (piece_end) {
+        // TMEM lane r of a quadrant is channel 4 (r % 8) + r / 8
+        const size_t piece = static_cast<size_t>(unit) + blockIdx.x;
+        float *o = p.part + piece * (TAPS * kTN * kTM) + (warp >> 2) * 16 * kTM +
+                   (warp & 3) * 32 + 4 * (lane & 7) + (lane >> 3);
 #pragma unroll
-          for (int k = 0; k < TAPS; ++k)
+        for (int k = 0; k < TAPS; ++k)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              o[(k * kTN + i) * kTM] = acc[k][i];
-              acc[k][i] = 0.f;
-            }
-        }
+          for (int j = 0; j < 16; ++j) {
+            o[(k * kTN + j) * kTM] = acc[k][j];
+            acc[k][j] = 0.f;
+          }
       }
     };
 
-    // Copies run three halves ahead of the conversion: halves `ahead` of stage
-    // `at`, into the raw buffers in turn.
-    Cursor cp = start;
-    int at = 0, ahead = 0;
-    uint32_t raw_in = 0, raw_out = 0;
-    pr.set_copy_unit(unit_at(p, cp.unit));
-    auto copy = [&]() {
-      if (at < count) {
-        const int s = at % kTables;
-        if (!ahead) ok = wait(tab_full + s, (at / kTables) & 1);
-        if (ok) pr.copy(raw0 + raw_in, tables + s * kTableInts, ahead);
-        if (ahead) {
-          ++at;
-          if (cp.next(p.stages) && at < count) pr.set_copy_unit(unit_at(p, cp.unit));
-        }
-        ahead ^= 1;
-      }
-      cp_async_commit();
-      raw_in = raw_in == (kRaw - 1) * kRawBytes ? 0 : raw_in + kRawBytes;
-    };
-    Cursor cv = start;  // the stage that is converted
-    pr.set_unit(unit_at(p, cv.unit));
-    for (int i = 0; i < kRaw && ok; ++i) copy();
-#pragma unroll 1
-    for (int i = 0; i < count && ok; ++i) {
-      const int s = i % kStages;
-      if (i >= kStages) ok = wait(empty + s, (i / kStages - 1) & 1);
-      if (!ok) break;
-      const uint32_t a = base + s * kStageBytes;
-      const int *table = tables + (i % kTables) * kTableInts;
+    Cursor ld = start;  // the stage that is loaded next
+    if (warp < (kStagers - kDyThreads) / 32) {
+      XStager st(p);
+      st.set_load_unit(unit_at(p, ld.unit));
+      ok = wait(tab_full, 0);
+      if (ok)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        cp_async_wait<kRaw - 1>();
-        pr.store(a, a + kBytesA, raw0 + raw_out, table, half);
-        raw_out = raw_out == (kRaw - 1) * kRawBytes ? 0 : raw_out + kRawBytes;
-        copy();
+        for (int k = 0; k < 8; ++k) st.load(k, tables);
+#pragma unroll 1
+      for (int i = 0; i < count && ok; ++i) {
+        const int *table = tables + (i % kTables) * kTableInts;
+        const bool more = i + 1 < count;
+        const int *ahead = tables + ((i + 1) % kTables) * kTableInts;
+        if (ld.next(p.stages) && more) st.set_load_unit(unit_at(p, ld.unit));
+        if (more) ok = wait(tab_full + (i + 1) % kTables, ((i + 1) / kTables) & 1);
+        if (ok && i >= kStagesA)
+          ok = wait(a_empty + i % kStagesA, (i / kStagesA - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dst = t_lane + kAcc + (i % kStagesA) * (kPos / 2) + (warp >> 2) * 32;
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+          uint32_t low[8], high[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+            st.convert(k + j, table, o);
+            low[2 * j] = o[0];
+            low[2 * j + 1] = o[1];
+            high[2 * j] = o[2];
+            high[2 * j + 1] = o[3];
+            if (more) st.load(k + j, ahead);
+          }
+          tmem_st_16x16(dst + 4 * k, low);
+          tmem_st_16x16(dst + 4 * k + (16u << 16), high);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(a_full + i % kStagesA);
+          mbar_arrive(tab_empty + i % kTables);
+        }
+        if (i > 0) drain(i - 1);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(full + s);
-        mbar_arrive(tab_empty + i % kTables);
+    } else {
+      DyStager<K, NHWC> st(p);
+      const uint32_t base = smem_u32(smem);
+      st.set_load_unit(unit_at(p, ld.unit));
+      st.set_unit(unit_at(p, ld.unit));
+      Cursor cv = start;  // the stage that is converted
+      bool contiguous = false;
+      ok = wait(tab_full, 0);
+      if (ok)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.load_slot(st.raw[j], st.first + 32 * j, tables);
+#pragma unroll 1
+      for (int i = 0; i < count && ok; ++i) {
+        const int *table = tables + (i % kTables) * kTableInts;
+        const bool more = i + 1 < count;
+        const int *ahead = tables + ((i + 1) % kTables) * kTableInts;
+        const uint32_t stage = base + (i % kStagesB) * kStageBytes;
+        const uint32_t before = base + ((i + kStagesB - 1) % kStagesB) * kStageBytes;
+        if (i >= kStagesB) ok = wait(b_empty + i % kStagesB, (i / kStagesB - 1) & 1);
+        if (ok && more) ok = wait(tab_full + (i + 1) % kTables, ((i + 1) / kTables) & 1);
+        if (!ok) break;
+        st.carry(stage, before, contiguous, table);
+        if (ld.next(p.stages) && more) st.set_load_unit(unit_at(p, ld.unit));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          st.store_slot(stage, st.first + 32 * j, st.raw[j]);
+          if (more) st.load_slot(st.raw[j], st.first + 32 * j, ahead);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_full + i % kStagesB);
+          mbar_arrive(tab_empty + i % kTables);
+        }
+        contiguous = !cv.next(p.stages);
+        if (!contiguous && more) st.set_unit(unit_at(p, cv.unit));
+        if (i > 0) drain(i - 1);
       }
-      if (cv.next(p.stages) && i + 1 < count) pr.set_unit(unit_at(p, cv.unit));
-      // One stage behind: the next chain's first stage is staged by then.
-      drain_to(i);
     }
-    if (ok) drain_to(count);
-    cp_async_wait<0>();
+    if (ok) drain(count - 1);
     if (!ok) give_up();
   } else {
     setmaxnreg_dec<kIssueRegs>();
-    if (threadIdx.x == kProducers) {
-      constexpr uint32_t idesc = idesc_f16_mn(kTM, 2 * kTN);
+    if (threadIdx.x == kStagers) {
+      constexpr uint32_t idesc = idesc_f16_tmem_a(kTM, 2 * kTN);
       const uint32_t base = smem_u32(smem);
       uint32_t chains = 0;
       bool fresh = true, ok = true;
       Cursor at = start;
       Chain chain;
       for (int i = 0; i < count && ok; ++i) {
-        const int s = i % kStages;
+        const int sa = i % kStagesA, sb = i % kStagesB;
         if (fresh && chains > 0) ok = mbar_wait(acc_free, (chains - 1) & 1, abort, p.wait_ns);
-        if (ok) ok = mbar_wait(full + s, (i / kStages) & 1, abort, p.wait_ns);
+        if (ok) ok = mbar_wait(a_full + sa, (i / kStagesA) & 1, abort, p.wait_ns);
+        if (ok) ok = mbar_wait(b_full + sb, (i / kStagesB) & 1, abort, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ad = mn_major_desc(base + s * kStageBytes, 128, kSboA);
-        const uint64_t bd = mn_major_desc(base + s * kStageBytes + kBytesA, 128, kSboB);
+        const uint32_t a = tmem + kAcc + sa * (kPos / 2);
+        const uint64_t b = mn_major_desc(base + sb * kStageBytes, 128, kSbo);
 #pragma unroll
         for (int k = 0; k < kPos / 16; ++k)
 #pragma unroll
           for (int tap = 0; tap < TAPS; ++tap)
-            umma_f16(tmem + tap * 2 * kTN, ad + 16 * k + tap, bd + 16 * k, idesc,
-                     !fresh || k > 0);
+            umma_f16_tmem_a(tmem + tap * 2 * kTN, a + 8 * k, b + 16 * k + (TAPS - 1 - tap), idesc,
+                            !fresh || k > 0);
         fresh = false;
-        umma_commit(empty + s);
+        umma_commit(a_empty + sa);
+        umma_commit(b_empty + sb);
         const bool piece_end = i == count - 1 || at.stage == p.stages - 1;
         at.next(p.stages);
         if (chain.ends(piece_end)) {
@@ -544,8 +585,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000) {}
       }
-    } else if (warp > kProducers / 32) {
-      const int first = warp - kProducers / 32 - 1;
+    } else if (warp > kStagers / 32) {
+      const int first = warp - kStagers / 32 - 1;
       Cursor at = start;
       for (int i = 0; i < first; ++i) at.next(p.stages);
       int unit = -1;
@@ -577,7 +618,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kProducers / 32) {
+  if (warp == kStagers / 32) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
@@ -726,43 +767,52 @@ __global__ void __launch_bounds__(kScanThreads)
                 min(kSMs, static_cast<int>(gridDim.x * gridDim.y)));
 }
 
-// Blocks (128 threads: input channels) x output channel x (ky, and one more
-// for dbias): adds a unit's pieces in order and undoes the scaling.
+// grid (input-channel tiles + 1, cout): adds a unit's pieces in order, undoes
+// the scaling and writes the taps of 128 input channels, contiguous in dw, through
+// shared memory; the last column of blocks adds up dbias.
 template <int K>
 __global__ void __launch_bounds__(kTM)
     wgrad_reduce(const WgradParams p, int grid, const float *__restrict__ psum, int slabs,
                  float *__restrict__ dw, float *__restrict__ dbias) {
+  __shared__ float out[kTM * K * K];
   const int co = blockIdx.y;
-  if (blockIdx.z == K) {
-    if (blockIdx.x > 0 || !dbias || threadIdx.x >= 32) return;
+  if (blockIdx.x == gridDim.x - 1) {
+    if (!dbias || threadIdx.x >= 32) return;
     float s = 0.f;
+#pragma unroll 4
     for (int i = threadIdx.x; i < slabs; i += 32) s += psum[static_cast<size_t>(i) * p.cout + co];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (threadIdx.x == 0) dbias[co] = s;
     return;
   }
-  const int ci = blockIdx.x * kTM + threadIdx.x, ky = blockIdx.z;
-  const int u = (static_cast<int>(blockIdx.x) * p.co_tiles + co / kTN) * K + ky;
-  // the SM ranges that hold the unit's first and last stage
-  const long long a = static_cast<long long>(u) * p.stages, b = a + p.stages - 1;
-  const int c0 = static_cast<int>(((a + 1) * grid - 1) / p.total);
-  const int c1 = static_cast<int>(((b + 1) * grid - 1) / p.total);
-  float v[K];
+  const int ci0 = blockIdx.x * kTM, ci = ci0 + threadIdx.x;
+  const int e = ci < p.cin ? static_cast<int>(p.emax[ci >> 5]) - 127 - 7 - dy_exponent(p.amax[co])
+                           : 0;
+#pragma unroll 1
+  for (int ky = 0; ky < K; ++ky) {
+    const int u = (static_cast<int>(blockIdx.x) * p.co_tiles + co / kTN) * K + ky;
+    // the SM ranges that hold the unit's first and last stage
+    const long long a = static_cast<long long>(u) * p.stages, b = a + p.stages - 1;
+    const int c0 = static_cast<int>(((a + 1) * grid - 1) / p.total);
+    const int c1 = static_cast<int>(((b + 1) * grid - 1) / p.total);
+    float v[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.f;
+    for (int k = 0; k < K; ++k) v[k] = 0.f;
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float *src = p.part + static_cast<size_t>(u + c) * (K * kTN * kTM) +
-                       (co % kTN) * kTM + threadIdx.x;
+    for (int c = c0; c <= c1; ++c) {
+      const float *src = p.part + static_cast<size_t>(u + c) * (K * kTN * kTM) +
+                         (co % kTN) * kTM + threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += src[k * kTN * kTM];
+      for (int k = 0; k < K; ++k) v[k] += src[k * kTN * kTM];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) out[threadIdx.x * (K * K) + ky * K + k] = scalbnf(v[k], e);
   }
-  if (ci >= p.cin) return;
-  const int e = static_cast<int>(p.emax[ci >> 5]) - 127 - 7 - dy_exponent(p.amax[co]);
-  float *o = dw + (static_cast<size_t>(co) * p.cin + ci) * (K * K) + ky * K;
-#pragma unroll
-  for (int k = 0; k < K; ++k) o[k] = scalbnf(v[k], e);
+  __syncthreads();
+  const int count = min(kTM, p.cin - ci0) * K * K;
+  float *o = dw + (static_cast<size_t>(co) * p.cin + ci0) * (K * K);
+  for (int i = threadIdx.x; i < count; i += kTM) o[i] = out[i];
 }
 
 int floor_log2(unsigned d) {
@@ -780,7 +830,7 @@ struct WgradWs {
 WgradWs carve_wgrad(Carver &cv, int n, int cin, int h, int w, int cout, int k) {
   WgradWs ws{};
   const long long rows = static_cast<long long>(n) * h * w;
-  ws.slabs = static_cast<int>(std::max(1ll, std::min<long long>(4 * kSMs, rows / 64)));
+  ws.slabs = static_cast<int>(std::max(1ll, std::min<long long>(4 * kSMs, rows / 16)));
   const long long positions = static_cast<long long>(n) * h * (w + (k == 3));
   ws.stages = ceil_div(positions, kPos);
   ws.units = ceil_div(cin, kTM) * ceil_div(cout, kTN) * k;
@@ -868,7 +918,7 @@ int wgrad(const float *dy, CkptView x, int n, int cin, int h, int w, int nhwc, i
     VAE_TRY((nhwc ? launch_mma<3, true> : launch_mma<3, false>)(p, ws.grid, s));
   else
     VAE_TRY((nhwc ? launch_mma<1, true> : launch_mma<1, false>)(p, ws.grid, s));
-  const dim3 rg(ceil_div(cin, kTM), cout, k + 1);
+  const dim3 rg(ceil_div(cin, kTM) + 1, cout);
   if (k == 3)
     wgrad_reduce<3><<<rg, kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
   else
