@@ -145,19 +145,19 @@ _SIGS = {
     "vae_chain_tiled_workspace_size": (_SZ, [_P, _I, _I, _I, _I, _I, _I]),
     "vae_decode_chain_tiled": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "vae_ckpt_bytes": (_SZ, [_LL, _I]),
-    "vae_ckpt_pack": (_I, [_P, _I, _I, _LL, _I, _P, _P]),
-    "vae_ckpt_unpack": (_I, [_P, _I, _I, _LL, _I, _P, _P]),
+    "vae_ckpt_pack": (_I, [_P, _I, _I, _LL, _I, _P, _P, _P]),
+    "vae_ckpt_unpack": (_I, [_P, _P, _I, _I, _LL, _I, _P, _P]),
     "vae_groupnorm_silu_ckpt_workspace_size": (_SZ, [_I, _I, _LL, _I, _I]),
-    "vae_groupnorm_silu_ckpt": (_I, [_P, _I, _I, _LL, _I, _I, _F, _P, _P, _I, _P, _P, _P, _P, _P,
-                                     _SZ, _P]),
+    "vae_groupnorm_silu_ckpt": (_I, [_P, _I, _I, _LL, _I, _I, _F, _P, _P, _I] + [_P] * 7 +
+                                [_SZ, _P]),
     "vae_groupnorm_silu_backward_workspace_size": (_SZ, [_I, _I, _LL, _I, _I]),
-    "vae_groupnorm_silu_backward": (_I, [_P, _P, _P, _I, _I, _LL, _I, _I, _P, _P, _I, _P, _P, _P,
-                                         _P, _P, _SZ, _P]),
+    "vae_groupnorm_silu_backward": (_I, [_P] * 4 + [_I, _I, _LL, _I, _I, _P, _P, _I] + [_P] * 5 +
+                                    [_SZ, _P]),
     "vae_conv2d_wgrad_workspace_size": (_SZ, [_I] * 7),
-    "vae_conv2d_wgrad": (_I, [_P, _P] + [_I] * 7 + [_P, _P, _P, _SZ, _P]),
-    "vae_block_norm": (_I, [_P, _P, _I, _LL, _I, _F] + [_P] * 10),
+    "vae_conv2d_wgrad": (_I, [_P, _P, _P] + [_I] * 7 + [_P, _P, _P, _SZ, _P]),
+    "vae_block_norm": (_I, [_P, _P, _I, _LL, _I, _F] + [_P] * 12),
     "vae_block_norm_backward_workspace_size": (_SZ, [_I, _LL, _I, _I]),
-    "vae_block_norm_backward": (_I, [_P] * 5 + [_I, _LL, _I] + [_P] * 11 + [_SZ, _P]),
+    "vae_block_norm_backward": (_I, [_P] * 7 + [_I, _LL, _I] + [_P] * 11 + [_SZ, _P]),
     "vae_measure_tf32_mma": (_I, [_I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_float), _P]),
     "vae_debug_set_wait_limit": (_I, [ctypes.c_ulonglong]),
@@ -465,13 +465,14 @@ def vae_causal_stack(x, layers, groups=32, eps=1e-6, layout=VAE_NCHW, out=None, 
 # These are called many times a step on tensors whose kernels take a few
 # microseconds, so the checks are one short call per tensor.
 class Checkpoint:
-    """An 8-bit activation checkpoint (vae_ckpt_bytes): ``buf``, the bytes on the
-    device, holding ``rows`` pixels or tokens of ``c`` channels. ``payload``
-    [rows, cp] (float8_e4m3fn, cp = c rounded up to 32) and ``scale``
-    [rows, cp / 32] (float8_e8m0fnu) are views: a value is payload * scale of
-    its block of 32 channels."""
+    """An 8-bit activation checkpoint of ``rows`` pixels or tokens of ``c``
+    channels: ``payload`` [rows, cp] (float8_e4m3fn, cp = c rounded up to 32) and
+    ``scale`` [rows, cp / 32] (float8_e8m0fnu); a value is payload * scale of its
+    block of 32 channels. Made by the operators that keep one, or around the
+    bytes of one (payload first, scales at the next multiple of 256 bytes;
+    vae_ckpt_bytes long, 16-byte aligned)."""
 
-    __slots__ = ("rows", "c", "_cp", "_at", "_bytes")
+    __slots__ = ("rows", "c", "_bytes", "_payload", "_scale")
 
     def __init__(self, buf, rows, c):
         import torch
@@ -480,13 +481,8 @@ class Checkpoint:
             raise TypeError("buf must be a contiguous uint8 CUDA tensor")
         if rows <= 0 or c <= 0 or buf.numel() < self.nbytes(rows, c):
             raise ValueError(f"buf holds no checkpoint of {rows} rows of {c} channels")
-        self._sizes(rows, c)
-        self._bytes = buf
-
-    def _sizes(self, rows, c):
         self.rows, self.c = rows, c
-        self._cp = (c + 31) // 32 * 32
-        self._at = (rows * self._cp + 255) // 256 * 256  # of the scales
+        self._bytes, self._payload, self._scale = buf, None, None
 
     @staticmethod
     def nbytes(rows, c):
@@ -497,31 +493,40 @@ class Checkpoint:
     def _make(cls, rows, c, device):
         import torch
         self = cls.__new__(cls)
-        self._sizes(rows, c)
-        self._bytes = torch.empty(self._at + rows * (self._cp // 32), dtype=torch.float8_e4m3fn,
-                                  device=device)
+        self.rows, self.c, self._bytes = rows, c, None
+        cp = (c + 31) // 32 * 32
+        self._payload = torch.empty((rows, cp), dtype=torch.float8_e4m3fn, device=device)
+        self._scale = torch.empty((rows, cp // 32), dtype=torch.float8_e8m0fnu, device=device)
         return self
 
-    @property
-    def buf(self):
+    def _split(self):
         import torch
-        return self._bytes.view(torch.uint8)
+        cp = (self.c + 31) // 32 * 32
+        at, n = (self.rows * cp + 255) // 256 * 256, self.rows * (cp // 32)
+        self._payload = self._bytes[:self.rows * cp].view(torch.float8_e4m3fn).view(self.rows, cp)
+        self._scale = self._bytes[at:at + n].view(torch.float8_e8m0fnu).view(self.rows, cp // 32)
 
     @property
     def payload(self):
-        # (as_strided's offset counts from the storage's start)
-        import torch
-        k = self._bytes
-        if k.dtype is not torch.float8_e4m3fn:
-            k = k.view(torch.float8_e4m3fn)
-        return k.as_strided((self.rows, self._cp), (self._cp, 1), k.storage_offset())
+        if self._payload is None:
+            self._split()
+        return self._payload
 
     @property
     def scale(self):
-        import torch
-        k, n = self._bytes, self._cp // 32
-        return k.view(torch.float8_e8m0fnu).as_strided((self.rows, n), (n, 1),
-                                                       k.storage_offset() + self._at)
+        if self._scale is None:
+            self._split()
+        return self._scale
+
+    @property
+    def device(self):
+        return (self._payload if self._bytes is None else self._bytes).device
+
+    def _addresses(self):
+        if self._bytes is None:
+            return self._payload.data_ptr(), self._scale.data_ptr()
+        at = self._bytes.data_ptr()
+        return at, at + (self.rows * ((self.c + 31) // 32 * 32) + 255) // 256 * 256
 
 
 def _refuse(t, shape, device, name):
@@ -548,13 +553,14 @@ def _at_opt(t, shape, device, name):
 
 
 def _ckpt_at(k, rows, c, device, name):
+    """The addresses of a checkpoint's payload and scales."""
     if not isinstance(k, Checkpoint):
         raise TypeError(f"{name} must be a Checkpoint")
     if k.rows != rows or k.c != c:
         raise ValueError(f"{name} holds {k.rows} rows of {k.c} channels, not {rows} of {c}")
-    if k._bytes.device != device:
-        raise ValueError(f"{name} is on {k._bytes.device}, not {device}")
-    return k._bytes.data_ptr()
+    if k.device != device:
+        raise ValueError(f"{name} is on {k.device}, not {device}")
+    return k._addresses()
 
 
 _F32 = None  # torch.float32, once torch is loaded
@@ -630,8 +636,8 @@ def vae_ckpt_pack(x, layout=VAE_NHWC, stream=None):
     n, c, spatial = _dims(shape, layout)
     at = _at(x, shape, dev, "x")
     k = Checkpoint._make(n * spatial, c, dev)
-    _call("vae_ckpt_pack", dev, stream, (k._bytes,), at, n, c, spatial, layout,
-          k._bytes.data_ptr())
+    _call("vae_ckpt_pack", dev, stream, (k._payload, k._scale), at, n, c, spatial, layout,
+          *k._addresses())
     return k
 
 
@@ -642,10 +648,10 @@ def vae_ckpt_unpack(ckpt, shape, layout=VAE_NHWC, stream=None):
     if not isinstance(ckpt, Checkpoint):
         raise TypeError("ckpt must be a Checkpoint")
     n, c, spatial = _dims(shape, layout)
-    dev = ckpt._bytes.device
-    at = _ckpt_at(ckpt, n * spatial, c, dev, "ckpt")
+    dev = ckpt.device
+    pq, ps = _ckpt_at(ckpt, n * spatial, c, dev, "ckpt")
     out = torch.empty(shape, dtype=torch.float32, device=dev)
-    _call("vae_ckpt_unpack", dev, stream, (out,), at, n, c, spatial, layout, out.data_ptr())
+    _call("vae_ckpt_unpack", dev, stream, (out,), pq, ps, n, c, spatial, layout, out.data_ptr())
     return out
 
 
@@ -664,18 +670,20 @@ def vae_groupnorm_silu_ckpt(x, gamma, beta, groups=32, eps=1e-6, apply_silu=True
     py = y.data_ptr() if out is None else _at(out, shape, dev, "out")
     ws, pw, nw = _workspace(dev, "vae_groupnorm_silu_ckpt_workspace_size", n, c, spatial, layout,
                             groups)
-    x_ckpt = y_ckpt = kx = ky = pkx = pky = None
+    x_ckpt = y_ckpt = pxq = pxs = pyq = pys = None
+    made = [ws, y]
     if keep_x:
         x_ckpt = Checkpoint._make(n * spatial, c, dev)
-        kx = x_ckpt._bytes
-        pkx = kx.data_ptr()
+        pxq, pxs = x_ckpt._addresses()
+        made += (x_ckpt._payload, x_ckpt._scale)
     if keep_y:
         y_ckpt = Checkpoint._make(n * spatial, c, dev)
-        ky = y_ckpt._bytes
-        pky = ky.data_ptr()
+        pyq, pys = y_ckpt._addresses()
+        made += (y_ckpt._payload, y_ckpt._scale)
     stats = torch.empty((n, max(groups, 1), 2), dtype=torch.float32, device=dev)
-    _call("vae_groupnorm_silu_ckpt", dev, stream, (ws, y, kx, ky, stats), px, n, c, spatial,
-          layout, groups, eps, pg, pb, bool(apply_silu), py, pkx, pky, stats.data_ptr(), pw, nw)
+    made.append(stats)
+    _call("vae_groupnorm_silu_ckpt", dev, stream, made, px, n, c, spatial, layout, groups, eps,
+          pg, pb, bool(apply_silu), py, pxq, pxs, pyq, pys, stats.data_ptr(), pw, nw)
     return y, x_ckpt, y_ckpt, stats
 
 
@@ -688,7 +696,7 @@ def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply
     shape, dev = _first(dy, "dy")
     n, c, spatial = _dims(shape, layout)
     pd = _at(dy, shape, dev, "dy")
-    pk = _ckpt_at(x_ckpt, n * spatial, c, dev, "x_ckpt")
+    pq, pk = _ckpt_at(x_ckpt, n * spatial, c, dev, "x_ckpt")
     ps = _at(stats, (n, groups, 2), dev, "stats")
     pg, pb = _at(gamma, (c,), dev, "gamma"), _at(beta, (c,), dev, "beta")
     pr = _at_opt(dres, shape, dev, "dres")
@@ -698,7 +706,7 @@ def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply
                             layout, groups)
     dgamma = torch.empty_like(gamma)
     dbeta = torch.empty_like(beta)
-    _call("vae_groupnorm_silu_backward", dev, stream, (ws, dx, dgamma, dbeta), pd, pk, ps, n, c,
+    _call("vae_groupnorm_silu_backward", dev, stream, (ws, dx, dgamma, dbeta), pd, pq, pk, ps, n, c,
           spatial, layout, groups, pg, pb, bool(apply_silu), pr, px, dgamma.data_ptr(),
           dbeta.data_ptr(), pw, nw)
     return dx, dgamma, dbeta
@@ -718,12 +726,12 @@ def vae_conv2d_wgrad(dy, x_ckpt, k, layout=VAE_NCHW, stream=None):
         n, h, w, cout = shape
     pd = _at(dy, shape, dev, "dy")
     cin = getattr(x_ckpt, "c", 0)
-    pk = _ckpt_at(x_ckpt, n * h * w, cin, dev, "x_ckpt")
+    pq, pk = _ckpt_at(x_ckpt, n * h * w, cin, dev, "x_ckpt")
     ws, pw, nw = _workspace(dev, "vae_conv2d_wgrad_workspace_size", n, cin, h, w, layout, cout, k)
     dw = torch.empty((cout, cin, k, k), dtype=torch.float32, device=dev)
     dbias = torch.empty(cout, dtype=torch.float32, device=dev)
-    _call("vae_conv2d_wgrad", dev, stream, (ws, dw, dbias), pd, pk, n, cin, h, w, layout, cout, k,
-          dw.data_ptr(), dbias.data_ptr(), pw, nw)
+    _call("vae_conv2d_wgrad", dev, stream, (ws, dw, dbias), pd, pq, pk, n, cin, h, w, layout, cout,
+          k, dw.data_ptr(), dbias.data_ptr(), pw, nw)
     return dw, dbias
 
 
@@ -750,19 +758,20 @@ def vae_block_norm(u, x, w_post, gate=None, scale=None, w_pre=None, eps=1e-6, ke
         py = y.data_ptr() if out_y is None else _at(out_y, shape, dev, "out_y")
     elif out_y is not None:
         raise ValueError("out_y without w_pre")
-    u_ckpt = h_ckpt = rstd = ku = kh = pku = pkh = pr = None
+    u_ckpt = h_ckpt = rstd = puq = pus = phq = phs = pr = None
+    made = [h, y]
     if keep:
         u_ckpt = Checkpoint._make(n * tokens, c, dev)
-        ku = u_ckpt._bytes
-        pku = ku.data_ptr()
-        if w_pre is not None:
-            h_ckpt = Checkpoint._make(n * tokens, c, dev)
-            kh = h_ckpt._bytes
-            pkh = kh.data_ptr()
+        puq, pus = u_ckpt._addresses()
         rstd = torch.empty((2, n * tokens), dtype=torch.float32, device=dev)
         pr = rstd.data_ptr()
-    _call("vae_block_norm", dev, stream, (h, y, ku, kh, rstd), pu, px, n, tokens, c, eps, po, pg,
-          ps, pp, ph, py, pku, pkh, pr)
+        made += (u_ckpt._payload, u_ckpt._scale, rstd)
+        if w_pre is not None:
+            h_ckpt = Checkpoint._make(n * tokens, c, dev)
+            phq, phs = h_ckpt._addresses()
+            made += (h_ckpt._payload, h_ckpt._scale)
+    _call("vae_block_norm", dev, stream, made, pu, px, n, tokens, c, eps, po, pg, ps, pp, ph, py,
+          puq, pus, phq, phs, pr)
     return h, y, u_ckpt, h_ckpt, rstd
 
 
@@ -783,8 +792,8 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
         raise ValueError("dy and h_ckpt go with w_pre")
     n, tokens, c = shape
     pdy, pdh = _at_opt(dy, shape, dev, "dy"), _at_opt(dh, shape, dev, "dh")
-    pu = _ckpt_at(u_ckpt, n * tokens, c, dev, "u_ckpt")
-    ph = None if h_ckpt is None else _ckpt_at(h_ckpt, n * tokens, c, dev, "h_ckpt")
+    puq, pus = _ckpt_at(u_ckpt, n * tokens, c, dev, "u_ckpt")
+    phq, phs = (None, None) if h_ckpt is None else _ckpt_at(h_ckpt, n * tokens, c, dev, "h_ckpt")
     pr, po = _at(rstd, (2, n * tokens), dev, "rstd"), _at(w_post, (c,), dev, "w_post")
     pg, ps = _at_opt(gate, (n, c), dev, "gate"), _at_opt(scale, (c,), dev, "scale")
     pp = _at_opt(w_pre, (c,), dev, "w_pre")
@@ -795,8 +804,8 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
     dscale = None if scale is None else torch.empty_like(scale)
     dw_pre = None if w_pre is None else torch.empty_like(w_pre)
     _call("vae_block_norm_backward", dev, stream, (ws, du, dx, dw_post, dgate, dscale, dw_pre),
-          pdy, pdh, pu, ph, pr, n, tokens, c, po, pg, ps, pp, du.data_ptr(), dx.data_ptr(),
-          dw_post.data_ptr(), _ptr(dgate), _ptr(dscale), _ptr(dw_pre), pw, nw)
+          pdy, pdh, puq, pus, phq, phs, pr, n, tokens, c, po, pg, ps, pp, du.data_ptr(),
+          dx.data_ptr(), dw_post.data_ptr(), _ptr(dgate), _ptr(dscale), _ptr(dw_pre), pw, nw)
     return dict(du=du, dx=dx, dw_post=dw_post, dgate=dgate, dscale=dscale, dw_pre=dw_pre)
 
 

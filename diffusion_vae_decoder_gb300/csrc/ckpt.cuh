@@ -29,11 +29,10 @@ inline size_t ckpt_scale_offset(long long rows, int c) {
 inline size_t ckpt_bytes(long long rows, int c) {
   return ckpt_scale_offset(rows, c) + static_cast<size_t>(rows) * (ckpt_cp(c) / 32);
 }
-inline CkptView ckpt_view(const void *p, long long rows, int c) {
+inline CkptView ckpt_view(const void *q, const void *scale) {
   CkptView v;
-  if (!p) return v;
-  v.q = static_cast<uint8_t *>(const_cast<void *>(p));
-  v.scale = v.q + ckpt_scale_offset(rows, c);
+  v.q = static_cast<uint8_t *>(const_cast<void *>(q));
+  v.scale = static_cast<uint8_t *>(const_cast<void *>(scale));
   return v;
 }
 

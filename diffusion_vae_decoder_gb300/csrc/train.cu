@@ -18,6 +18,9 @@ bool all_aligned(T... p) {
 constexpr long long kMaxRows = 0x7fffffffll;  // pixels or tokens of one call
 constexpr int kMaxSamples = 65535;            // a grid dimension
 
+// An optional checkpoint's two arrays: both or none.
+bool pair(const void *q, const void *scale) { return (q != nullptr) == (scale != nullptr); }
+
 // A workspace of `need` bytes (none: ws may be NULL).
 int workspace_ok(const void *ws, size_t ws_bytes, size_t need) {
   if (!need) return VAE_OK;
@@ -67,23 +70,23 @@ size_t vae_ckpt_bytes(long long rows, int c) {
   return ckpt_bytes(rows, c);
 }
 
-int vae_ckpt_pack(const float *x, int n, int c, long long spatial, int layout, void *ckpt,
-                  vae_stream_t stream) {
-  if (!x || !ckpt) return VAE_EINVAL;
+int vae_ckpt_pack(const float *x, int n, int c, long long spatial, int layout, void *q,
+                  void *scale, vae_stream_t stream) {
+  if (!x || !q || !scale) return VAE_EINVAL;
   VAE_TRY(act_args_ok(n, c, spatial, layout));
   if (c > 65536) return VAE_EUNSUPPORTED;
-  if (!all_aligned(x, ckpt)) return VAE_EINVAL;
-  return ckpt_pack(x, n, c, spatial, layout == VAE_NHWC, ckpt_view(ckpt, n * spatial, c),
+  if (!all_aligned(x, q, scale)) return VAE_EINVAL;
+  return ckpt_pack(x, n, c, spatial, layout == VAE_NHWC, ckpt_view(q, scale),
                    reinterpret_cast<cudaStream_t>(stream));
 }
 
-int vae_ckpt_unpack(const void *ckpt, int n, int c, long long spatial, int layout, float *x,
-                    vae_stream_t stream) {
-  if (!x || !ckpt) return VAE_EINVAL;
+int vae_ckpt_unpack(const void *q, const void *scale, int n, int c, long long spatial, int layout,
+                    float *x, vae_stream_t stream) {
+  if (!x || !q || !scale) return VAE_EINVAL;
   VAE_TRY(act_args_ok(n, c, spatial, layout));
   if (c > 65536) return VAE_EUNSUPPORTED;
-  if (!all_aligned(x, ckpt)) return VAE_EINVAL;
-  return ckpt_unpack(ckpt_view(ckpt, n * spatial, c), n, c, spatial, layout == VAE_NHWC, x,
+  if (!all_aligned(x, q, scale)) return VAE_EINVAL;
+  return ckpt_unpack(ckpt_view(q, scale), n, c, spatial, layout == VAE_NHWC, x,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -96,15 +99,15 @@ size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long spatial, i
 
 int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,
                             int groups, float eps, const float *gamma, const float *beta,
-                            int apply_silu, float *y, void *x_ckpt, void *y_ckpt, float *stats,
-                            void *ws, size_t ws_bytes, vae_stream_t stream) {
-  if (!x || !gamma || !beta || !y || !stats) return VAE_EINVAL;
+                            int apply_silu, float *y, void *x_q, void *x_scale, void *y_q,
+                            void *y_scale, float *stats, void *ws, size_t ws_bytes, vae_stream_t stream) {
+  if (!x || !gamma || !beta || !y || !stats || !pair(x_q, x_scale) || !pair(y_q, y_scale))
+    return VAE_EINVAL;
   VAE_TRY(gn_args_ok(n, c, spatial, layout, groups));
-  if (!all_aligned(x, y, x_ckpt, y_ckpt, stats, ws)) return VAE_EINVAL;
+  if (!all_aligned(x, y, x_q, x_scale, y_q, y_scale, stats, ws)) return VAE_EINVAL;
   VAE_TRY(workspace_ok(ws, ws_bytes, gn_ckpt_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups)));
-  const long long rows = n * spatial;
   return gn_ckpt(x, n, c, spatial, layout == VAE_NHWC, groups, eps, gamma, beta, apply_silu != 0,
-                 y, ckpt_view(x_ckpt, rows, c), ckpt_view(y_ckpt, rows, c), stats, ws,
+                 y, ckpt_view(x_q, x_scale), ckpt_view(y_q, y_scale), stats, ws,
                  reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -114,17 +117,17 @@ size_t vae_groupnorm_silu_backward_workspace_size(int n, int c, long long spatia
              ? gn_backward_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups) : 0;
 }
 
-int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, const float *stats, int n,
-                                int c, long long spatial, int layout, int groups,
+int vae_groupnorm_silu_backward(const float *dy, const void *x_q, const void *x_scale,
+                                const float *stats, int n, int c, long long spatial, int layout, int groups,
                                 const float *gamma, const float *beta, int apply_silu,
                                 const float *dres, float *dx, float *dgamma, float *dbeta,
                                 void *ws, size_t ws_bytes, vae_stream_t stream) {
-  if (!dy || !x_ckpt || !stats || !gamma || !beta || !dx) return VAE_EINVAL;
+  if (!dy || !x_q || !x_scale || !stats || !gamma || !beta || !dx) return VAE_EINVAL;
   VAE_TRY(gn_args_ok(n, c, spatial, layout, groups));
-  if (!all_aligned(dy, x_ckpt, stats, dres, dx, ws)) return VAE_EINVAL;
+  if (!all_aligned(dy, x_q, x_scale, stats, dres, dx, ws)) return VAE_EINVAL;
   VAE_TRY(workspace_ok(ws, ws_bytes,
                        gn_backward_ws_bytes(n, c, spatial, layout == VAE_NHWC, groups)));
-  return gn_backward(dy, ckpt_view(x_ckpt, n * spatial, c), stats, n, c, spatial,
+  return gn_backward(dy, ckpt_view(x_q, x_scale), stats, n, c, spatial,
                      layout == VAE_NHWC, groups, gamma, beta, apply_silu != 0, dres, dx, dgamma,
                      dbeta, ws, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -136,33 +139,33 @@ size_t vae_conv2d_wgrad_workspace_size(int n, int cin, int h, int w, int layout,
              ? wgrad_ws_bytes(n, cin, h, w, cout, k) : 0;
 }
 
-int vae_conv2d_wgrad(const float *dy, const void *x_ckpt, int n, int cin, int h, int w,
-                     int layout, int cout, int k, float *dw, float *dbias, void *ws,
+int vae_conv2d_wgrad(const float *dy, const void *x_q, const void *x_scale, int n, int cin, int h,
+                     int w, int layout, int cout, int k, float *dw, float *dbias, void *ws,
                      size_t ws_bytes, vae_stream_t stream) {
-  if (!dy || !x_ckpt || !dw || !ws) return VAE_EINVAL;
+  if (!dy || !x_q || !x_scale || !dw || !ws) return VAE_EINVAL;
   VAE_TRY(wgrad_args_ok(n, cin, h, w, layout, cout, k));
-  if (!all_aligned(dy, x_ckpt, ws)) return VAE_EINVAL;
+  if (!all_aligned(dy, x_q, x_scale, ws)) return VAE_EINVAL;
   if (ws_bytes < wgrad_ws_bytes(n, cin, h, w, cout, k)) return VAE_EWORKSPACE;
-  const long long rows = static_cast<long long>(n) * h * w;
-  return wgrad(dy, ckpt_view(x_ckpt, rows, cin), n, cin, h, w, layout == VAE_NHWC, cout, k, dw,
+  return wgrad(dy, ckpt_view(x_q, x_scale), n, cin, h, w, layout == VAE_NHWC, cout, k, dw,
                dbias, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ block norm
 int vae_block_norm(const float *u, const float *x, int n, long long tokens, int c, float eps,
                    const float *w_post, const float *gate, const float *scale,
-                   const float *w_pre, float *h, float *y, void *u_ckpt, void *h_ckpt,
-                   float *rstd, vae_stream_t stream) {
+                   const float *w_pre, float *h, float *y, void *u_q, void *u_scale, void *h_q,
+                   void *h_scale, float *rstd, vae_stream_t stream) {
   if (!u || !x || !w_post || !h) return VAE_EINVAL;
   if ((w_pre != nullptr) != (y != nullptr)) return VAE_EINVAL;
-  // keeping: u_ckpt and rstd, and h_ckpt exactly where there is a norm of h
-  if ((u_ckpt != nullptr) != (rstd != nullptr)) return VAE_EINVAL;
-  if ((h_ckpt != nullptr) != (u_ckpt && w_pre)) return VAE_EINVAL;
+  // keeping: u's checkpoint and rstd, and h's exactly where there is a norm of h
+  if (!pair(u_q, u_scale) || !pair(h_q, h_scale) || (u_q != nullptr) != (rstd != nullptr))
+    return VAE_EINVAL;
+  if ((h_q != nullptr) != (u_q && w_pre)) return VAE_EINVAL;
   VAE_TRY(block_norm_args_ok(n, tokens, c));
-  if (!all_aligned(u, x, w_post, gate, scale, w_pre, h, y, u_ckpt, h_ckpt)) return VAE_EINVAL;
+  if (!all_aligned(u, x, w_post, gate, scale, w_pre, h, y, u_q, u_scale, h_q, h_scale))
+    return VAE_EINVAL;
   const BlockNormArgs a{n, tokens, c, w_post, gate, scale, w_pre};
-  return block_norm(a, u, x, eps, h, y, ckpt_view(u_ckpt, n * tokens, c),
-                    ckpt_view(h_ckpt, n * tokens, c), rstd,
+  return block_norm(a, u, x, eps, h, y, ckpt_view(u_q, u_scale), ckpt_view(h_q, h_scale), rstd,
                     reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -174,24 +177,26 @@ size_t vae_block_norm_backward_workspace_size(int n, long long tokens, int c, in
   return block_norm_backward_ws_bytes(a);
 }
 
-int vae_block_norm_backward(const float *dy, const float *dh, const void *u_ckpt,
-                            const void *h_ckpt, const float *rstd, int n, long long tokens, int c,
+int vae_block_norm_backward(const float *dy, const float *dh, const void *u_q,
+                            const void *u_scale, const void *h_q, const void *h_scale,
+                            const float *rstd, int n, long long tokens, int c,
                             const float *w_post, const float *gate, const float *scale,
                             const float *w_pre, float *du, float *dx, float *dw_post,
                             float *dgate, float *dscale, float *dw_pre, void *ws, size_t ws_bytes,
                             vae_stream_t stream) {
-  if (!u_ckpt || !rstd || !w_post || !du || !dx || !ws) return VAE_EINVAL;
-  if ((w_pre != nullptr) != (dy != nullptr) || (w_pre != nullptr) != (h_ckpt != nullptr))
+  if (!u_q || !u_scale || !rstd || !w_post || !du || !dx || !ws || !pair(h_q, h_scale))
+    return VAE_EINVAL;
+  if ((w_pre != nullptr) != (dy != nullptr) || (w_pre != nullptr) != (h_q != nullptr))
     return VAE_EINVAL;
   if (!dy && !dh) return VAE_EINVAL;
   if ((dgate && !gate) || (dscale && !scale) || (dw_pre && !w_pre)) return VAE_EINVAL;
   VAE_TRY(block_norm_args_ok(n, tokens, c));
-  if (!all_aligned(dy, dh, u_ckpt, h_ckpt, w_post, gate, scale, w_pre, du, dx, ws))
+  if (!all_aligned(dy, dh, u_q, u_scale, h_q, h_scale, w_post, gate, scale, w_pre, du, dx, ws))
     return VAE_EINVAL;
   const BlockNormArgs a{n, tokens, c, w_post, gate, scale, w_pre};
   if (ws_bytes < block_norm_backward_ws_bytes(a)) return VAE_EWORKSPACE;
-  return block_norm_backward(a, dy, dh, ckpt_view(u_ckpt, n * tokens, c),
-                             ckpt_view(h_ckpt, n * tokens, c), rstd, du, dx, dw_post, dgate,
+  return block_norm_backward(a, dy, dh, ckpt_view(u_q, u_scale),
+                             ckpt_view(h_q, h_scale), rstd, du, dx, dw_post, dgate,
                              dscale, dw_pre, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 

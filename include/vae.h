@@ -438,19 +438,22 @@ VAE_API int vae_decode_causal(void *handle, const float *z, int n, int t, int h,
  * with zeros; cp = 32 * ceil(c / 32)) share the scale 2^e, e the smallest
  * integer >= -127 with max|v| <= 448 * 2^e, and hold e4m3 numbers
  * q = v * 2^-e rounded to nearest even; a block holding an infinity or a NaN
- * reads back as NaN. In memory (16-byte aligned, any layout of the tensor):
- *   byte 0                          q [rows][cp]
- *   byte 256 * ceil(rows * cp / 256)  e + 127 [rows][cp / 32] (255: NaN block)
- * Rows are pixels in (sample, t, y, x) order, or tokens.
- *   vae_ckpt_bytes   size of a checkpoint; 0 for sizes out of range
+ * reads back as NaN. It is two arrays, whatever the tensor's layout, each
+ * 16-byte aligned:
+ *   q     [rows][cp]       e4m3
+ *   scale [rows][cp / 32]  bytes e + 127 (255: a block of NaNs)
+ * passed as a pair of pointers (both NULL where a checkpoint is optional and
+ * not wanted). Rows are pixels in (sample, t, y, x) order, or tokens.
+ *   vae_ckpt_bytes   room for both in one buffer: q at 0, scale at the next
+ *                    multiple of 256 bytes; 0 for sizes out of range
  *   vae_ckpt_pack    x [n,c,spatial] (layout) into a checkpoint of n * spatial rows
  *   vae_ckpt_unpack  the inverse, x = q * 2^e
  * Limits: n <= 65535, n * spatial < 2^31, c <= 65536. */
 VAE_API size_t vae_ckpt_bytes(long long rows, int c);
-VAE_API int vae_ckpt_pack(const float *x, int n, int c, long long spatial, int layout, void *ckpt,
-                          vae_stream_t stream);
-VAE_API int vae_ckpt_unpack(const void *ckpt, int n, int c, long long spatial, int layout,
-                            float *x, vae_stream_t stream);
+VAE_API int vae_ckpt_pack(const float *x, int n, int c, long long spatial, int layout, void *q,
+                          void *scale, vae_stream_t stream);
+VAE_API int vae_ckpt_unpack(const void *q, const void *scale, int n, int c, long long spatial,
+                            int layout, float *x, vae_stream_t stream);
 
 /* vae_groupnorm_silu_ckpt -- vae_groupnorm_silu that also keeps what a
  * backward pass needs: checkpoints of x (for vae_groupnorm_silu_backward, or a
@@ -464,8 +467,8 @@ VAE_API size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long sp
                                                       int groups);
 VAE_API int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,
                                     int groups, float eps, const float *gamma, const float *beta,
-                                    int apply_silu, float *y, void *x_ckpt, void *y_ckpt,
-                                    float *stats, void *ws, size_t ws_bytes, vae_stream_t stream);
+                                    int apply_silu, float *y, void *x_q, void *x_scale,
+                                    void *y_q, void *y_scale, float *stats, void *ws, size_t ws_bytes, vae_stream_t stream);
 
 /* vae_groupnorm_silu_backward -- with x~ the checkpoint's values, xh =
  * (x~ - mean) * rstd (stats as saved), z = xh * gamma + beta, and dz = dy *
@@ -479,7 +482,8 @@ VAE_API int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spat
  * Sums have a fixed order: the same inputs give the same bits. */
 VAE_API size_t vae_groupnorm_silu_backward_workspace_size(int n, int c, long long spatial,
                                                           int layout, int groups);
-VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, const float *stats,
+VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_q,
+                                        const void *x_scale, const float *stats,
                                         int n, int c, long long spatial, int layout, int groups,
                                         const float *gamma, const float *beta, int apply_silu,
                                         const float *dres, float *dx, float *dgamma, float *dbeta,
@@ -491,7 +495,7 @@ VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, con
  *   dbias[o] = sum_{n,i,j} dy[n,o,i,j]
  * (The gradient of the input is vae_conv2d of dy with the taps flipped and
  * cin, cout exchanged; the 1x1 shortcut's weight gradient is a call with k = 1.)
- *   dy [n,cout,h,w] (layout); x_ckpt: n*h*w rows of cin channels;
+ *   dy [n,cout,h,w] (layout); x_q, x_scale: n*h*w rows of cin channels;
  *   dw [cout,cin,k,k]; dbias [cout] or NULL
  * The products run on the tensor cores with x~ exact and dy in two parts of
  * 11 significant bits each, scaled per output channel by a power of two, so
@@ -503,8 +507,8 @@ VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_ckpt, con
  * cout % 4 == 0 for NHWC. */
 VAE_API size_t vae_conv2d_wgrad_workspace_size(int n, int cin, int h, int w, int layout, int cout,
                                                int k);
-VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_ckpt, int n, int cin, int h, int w,
-                             int layout, int cout, int k, float *dw, float *dbias, void *ws,
+VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_q, const void *x_scale, int n,
+                             int cin, int h, int w, int layout, int cout, int k, float *dw, float *dbias, void *ws,
                              size_t ws_bytes, vae_stream_t stream);
 
 /* vae_block_norm -- the norms after a transformer block and before the next
@@ -514,9 +518,9 @@ VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_ckpt, int n, int cin
  *   u, x, h, y [n][tokens][c]; w_post, scale, w_pre [c]; gate [n][c] (one for
  *   all tokens of a sample). gate and scale may be NULL (ones); w_pre and y are
  *   both NULL where no norm follows. h == x and y == u are allowed.
- * For a backward pass, checkpoints u_ckpt of u and h_ckpt of h (NULL exactly
- * when w_pre is) and rstd [2][n * tokens]: 1 / rms(u), then 1 / rms(h) (that
- * half unused without w_pre). All three NULL otherwise (serving).
+ * For a backward pass, checkpoints of u and of h (h_q NULL exactly when w_pre
+ * is) and rstd [2][n * tokens]: 1 / rms(u), then 1 / rms(h) (that
+ * half unused without w_pre). All NULL otherwise (serving).
  * vae_block_norm_backward -- from dy (NULL exactly when w_pre is) and dh, the
  * gradient that reaches h by the residual stream (may be NULL): du, dx, and,
  * each where not NULL, dw_post, dscale, dw_pre [c] and dgate [n][c]. Asking for
@@ -525,12 +529,13 @@ VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_ckpt, int n, int cin
  * Limits: c % 4 == 0, c <= 4096, n <= 65535, n * tokens < 2^31. */
 VAE_API int vae_block_norm(const float *u, const float *x, int n, long long tokens, int c,
                            float eps, const float *w_post, const float *gate, const float *scale,
-                           const float *w_pre, float *h, float *y, void *u_ckpt, void *h_ckpt,
-                           float *rstd, vae_stream_t stream);
+                           const float *w_pre, float *h, float *y, void *u_q, void *u_scale,
+                           void *h_q, void *h_scale, float *rstd, vae_stream_t stream);
 VAE_API size_t vae_block_norm_backward_workspace_size(int n, long long tokens, int c,
                                                       int has_gate);
-VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void *u_ckpt,
-                                    const void *h_ckpt, const float *rstd, int n,
+VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void *u_q,
+                                    const void *u_scale, const void *h_q, const void *h_scale,
+                                    const float *rstd, int n,
                                     long long tokens, int c, const float *w_post,
                                     const float *gate, const float *scale, const float *w_pre,
                                     float *du, float *dx, float *dw_post, float *dgate,

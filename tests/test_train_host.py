@@ -37,25 +37,29 @@ def test_ckpt_bytes(lib):
 
 @pytest.mark.parametrize("fn", ["vae_ckpt_pack", "vae_ckpt_unpack"])
 @pytest.mark.parametrize("args,status", [
-    ((None, 1, 32, 4, 0, P), EINVAL), ((P, 1, 32, 4, 0, None), EINVAL),
-    ((P, 0, 32, 4, 0, P), EINVAL), ((P, 1, 0, 4, 0, P), EINVAL), ((P, 1, 32, 0, 0, P), EINVAL),
-    ((P, 1, 32, 4, 2, P), EINVAL), ((ODD, 1, 32, 4, 0, P), EINVAL),
-    ((P, 1, 32, 4, 0, ODD), EINVAL), ((P, 65536, 32, 4, 0, P), EUNSUPPORTED),
-    ((P, 2, 32, 1 << 30, 0, P), EUNSUPPORTED), ((P, 1, 65537, 4, 0, P), EUNSUPPORTED)])
+    (dict(x=None), EINVAL), (dict(q=None), EINVAL), (dict(s=None), EINVAL), (dict(n=0), EINVAL),
+    (dict(c=0), EINVAL), (dict(sp=0), EINVAL), (dict(lay=2), EINVAL), (dict(x=ODD), EINVAL),
+    (dict(q=ODD), EINVAL), (dict(s=ODD), EINVAL), (dict(n=65536), EUNSUPPORTED),
+    (dict(n=2, sp=1 << 30), EUNSUPPORTED), (dict(c=65537), EUNSUPPORTED)])
 def test_pack_and_unpack_refuse(lib, fn, args, status):
-    assert getattr(lib, fn)(*args, None) == status
+    a = dict(x=P, q=P, s=P, n=1, c=32, sp=4, lay=0) | args
+    size = (a["n"], a["c"], a["sp"], a["lay"])
+    if fn == "vae_ckpt_pack":
+        assert lib.vae_ckpt_pack(a["x"], *size, a["q"], a["s"], None) == status
+    else:
+        assert lib.vae_ckpt_unpack(a["q"], a["s"], *size, a["x"], None) == status
 
 
-def gn_fwd(lib, x=P, n=1, c=64, sp=1 << 20, lay=1, g=32, ga=P, be=P, y=P, kx=P, ky=P, st=P, ws=P,
-           nb=BIG):
-    return lib.vae_groupnorm_silu_ckpt(x, n, c, sp, lay, g, 1e-6, ga, be, 1, y, kx, ky, st, ws,
-                                       nb, None)
+def gn_fwd(lib, x=P, n=1, c=64, sp=1 << 20, lay=1, g=32, ga=P, be=P, y=P, kx=P, sx=P, ky=P, sy=P,
+           st=P, ws=P, nb=BIG):
+    return lib.vae_groupnorm_silu_ckpt(x, n, c, sp, lay, g, 1e-6, ga, be, 1, y, kx, sx, ky, sy, st,
+                                       ws, nb, None)
 
 
-def gn_bwd(lib, dy=P, kx=P, st=P, n=1, c=64, sp=1 << 20, lay=1, g=32, ga=P, be=P, res=None, dx=P,
-           ws=P, nb=BIG):
-    return lib.vae_groupnorm_silu_backward(dy, kx, st, n, c, sp, lay, g, ga, be, 1, res, dx, P, P,
-                                           ws, nb, None)
+def gn_bwd(lib, dy=P, kx=P, sx=P, st=P, n=1, c=64, sp=1 << 20, lay=1, g=32, ga=P, be=P, res=None,
+           dx=P, ws=P, nb=BIG):
+    return lib.vae_groupnorm_silu_backward(dy, kx, sx, st, n, c, sp, lay, g, ga, be, 1, res, dx, P,
+                                           P, ws, nb, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -71,23 +75,24 @@ def test_groupnorm_pair_refuses(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(y=None), dict(x=ODD), dict(y=ODD),
-                                dict(kx=ODD), dict(ky=ODD)])
+                                dict(kx=ODD), dict(ky=ODD), dict(kx=None), dict(sx=None),
+                                dict(ky=None), dict(sy=None), dict(sx=ODD), dict(sy=ODD)])
 def test_groupnorm_forward_refuses_pointers(lib, kw):
     assert gn_fwd(lib, **kw) == EINVAL
 
 
-@pytest.mark.parametrize("kw", [dict(dy=None), dict(kx=None), dict(dx=None), dict(dy=ODD),
+@pytest.mark.parametrize("kw", [dict(dy=None), dict(kx=None), dict(sx=None), dict(dx=None), dict(dy=ODD),
                                 dict(kx=ODD), dict(res=ODD), dict(dx=ODD)])
 def test_groupnorm_backward_refuses_pointers(lib, kw):
     assert gn_bwd(lib, **kw) == EINVAL
 
 
-def wgrad(lib, dy=P, k8=P, n=1, cin=32, h=8, w=8, lay=1, cout=32, k=3, dw=P, ws=P, nb=BIG):
-    return lib.vae_conv2d_wgrad(dy, k8, n, cin, h, w, lay, cout, k, dw, None, ws, nb, None)
+def wgrad(lib, dy=P, k8=P, s8=P, n=1, cin=32, h=8, w=8, lay=1, cout=32, k=3, dw=P, ws=P, nb=BIG):
+    return lib.vae_conv2d_wgrad(dy, k8, s8, n, cin, h, w, lay, cout, k, dw, None, ws, nb, None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(dy=None), EINVAL), (dict(k8=None), EINVAL), (dict(dw=None), EINVAL),
+    (dict(dy=None), EINVAL), (dict(k8=None), EINVAL), (dict(s8=None), EINVAL), (dict(s8=ODD), EINVAL), (dict(dw=None), EINVAL),
     (dict(ws=None), EINVAL), (dict(n=0), EINVAL), (dict(cin=0), EINVAL), (dict(h=0), EINVAL),
     (dict(w=-1), EINVAL), (dict(cout=0), EINVAL), (dict(lay=3), EINVAL), (dict(dy=ODD), EINVAL),
     (dict(k8=ODD), EINVAL), (dict(ws=ODD), EINVAL), (dict(k=2), EUNSUPPORTED),
@@ -99,16 +104,18 @@ def test_wgrad_refuses(lib, kw, status):
     assert wgrad(lib, **kw) == status
 
 
-def bn_fwd(lib, u=P, x=P, n=1, t=4, c=64, wpo=P, gate=None, sc=None, wpr=P, h=P, y=P, ku=P, kh=P,
-           rs=P):
-    return lib.vae_block_norm(u, x, n, t, c, 1e-6, wpo, gate, sc, wpr, h, y, ku, kh, rs, None)
+def bn_fwd(lib, u=P, x=P, n=1, t=4, c=64, wpo=P, gate=None, sc=None, wpr=P, h=P, y=P, ku=P, su=P,
+           kh=P, sh=P, rs=P):
+    return lib.vae_block_norm(u, x, n, t, c, 1e-6, wpo, gate, sc, wpr, h, y, ku, su, kh, sh, rs,
+                              None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(u=None), EINVAL), (dict(x=None), EINVAL), (dict(wpo=None), EINVAL),
     (dict(h=None), EINVAL), (dict(y=None), EINVAL), (dict(wpr=None), EINVAL),
     (dict(ku=None), EINVAL), (dict(kh=None), EINVAL), (dict(rs=None), EINVAL),
-    (dict(wpr=None, y=None), EINVAL), (dict(n=0), EINVAL), (dict(t=0), EINVAL),
+    (dict(su=None), EINVAL), (dict(sh=None), EINVAL), (dict(kh=None, sh=None), EINVAL),
+    (dict(ku=None, su=None), EINVAL), (dict(wpr=None, y=None), EINVAL), (dict(n=0), EINVAL), (dict(t=0), EINVAL),
     (dict(c=0), EINVAL), (dict(u=ODD), EINVAL), (dict(gate=ODD), EINVAL), (dict(kh=ODD), EINVAL),
     (dict(c=66), EUNSUPPORTED), (dict(c=4100), EUNSUPPORTED), (dict(n=65536), EUNSUPPORTED),
     (dict(n=4, t=1 << 29), EUNSUPPORTED)])
@@ -116,18 +123,19 @@ def test_block_norm_refuses(lib, kw, status):
     assert bn_fwd(lib, **kw) == status
 
 
-def bn_bwd(lib, dy=P, dh=P, ku=P, kh=P, rs=P, n=1, t=4, c=64, wpo=P, gate=P, sc=P, wpr=P, du=P,
+def bn_bwd(lib, dy=P, dh=P, ku=P, su=P, kh=P, sh=P, rs=P, n=1, t=4, c=64, wpo=P, gate=P, sc=P, wpr=P, du=P,
            dx=P, dwpo=P, dgate=P, dsc=P, dwpr=P, ws=P, nb=BIG):
-    return lib.vae_block_norm_backward(dy, dh, ku, kh, rs, n, t, c, wpo, gate, sc, wpr, du, dx,
+    return lib.vae_block_norm_backward(dy, dh, ku, su, kh, sh, rs, n, t, c, wpo, gate, sc, wpr, du, dx,
                                        dwpo, dgate, dsc, dwpr, ws, nb, None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dy=None), EINVAL), (dict(kh=None), EINVAL), (dict(wpr=None), EINVAL),
-    (dict(dy=None, dh=None, kh=None, wpr=None, dwpr=None), EINVAL), (dict(ku=None), EINVAL),
+    (dict(dy=None, dh=None, kh=None, sh=None, wpr=None, dwpr=None), EINVAL), (dict(ku=None), EINVAL),
     (dict(rs=None), EINVAL), (dict(wpo=None), EINVAL), (dict(du=None), EINVAL),
     (dict(dx=None), EINVAL), (dict(ws=None), EINVAL), (dict(gate=None), EINVAL),
-    (dict(sc=None), EINVAL), (dict(dy=None, kh=None, wpr=None), EINVAL), (dict(dh=ODD), EINVAL),
+    (dict(sc=None), EINVAL), (dict(dy=None, kh=None, sh=None, wpr=None), EINVAL),
+    (dict(su=None), EINVAL), (dict(sh=None), EINVAL), (dict(dh=ODD), EINVAL),
     (dict(n=0), EINVAL), (dict(c=2), EUNSUPPORTED), (dict(nb=4), EWORKSPACE)])
 def test_block_norm_backward_refuses(lib, kw, status):
     assert bn_bwd(lib, **kw) == status
