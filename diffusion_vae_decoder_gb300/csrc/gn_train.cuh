@@ -94,50 +94,6 @@ __device__ __forceinline__ Oct grad8(const Oct &dy, const Oct &x, const Affine8 
   }
   return o;
 }
-// Eight channels in one 256-bit access where rows and pointers are 32-byte
-// aligned (WIDE: c a multiple of eight), else in two of 128 bits: with 32 bytes
-// between lanes the halves of a sector would pass L2 twice. Those past c (a
-// multiple of four), from `left` on, are zeros. LAST: the data is not needed in
-// L2 any more (evict first), and stores never are.
-template <bool WIDE, bool LAST>
-__device__ __forceinline__ Oct load_oct(const float *p, int left) {
-  if (WIDE) {
-    Oct o = {{0, 0, 0, 0}};
-    if (left > 0) {
-      if (LAST)
-        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v4.b64 {%0, %1, %2, %3}, [%4];"
-                     : "=l"(o.v[0]), "=l"(o.v[1]), "=l"(o.v[2]), "=l"(o.v[3])
-                     : "l"(p)
-                     : "memory");
-      else
-        asm volatile("ld.global.L1::no_allocate.v4.b64 {%0, %1, %2, %3}, [%4];"
-                     : "=l"(o.v[0]), "=l"(o.v[1]), "=l"(o.v[2]), "=l"(o.v[3])
-                     : "l"(p)
-                     : "memory");
-    }
-    return o;
-  }
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  return oct_of(left > 0 ? *reinterpret_cast<const float4 *>(p) : zero,
-                left > 4 ? *(reinterpret_cast<const float4 *>(p) + 1) : zero);
-}
-template <bool WIDE>
-__device__ __forceinline__ void store_oct(float *p, int left, const Oct &o) {
-  if (WIDE) {
-    if (left > 0)
-      asm volatile("st.global.L2::evict_first.v4.b64 [%4], {%0, %1, %2, %3};" ::"l"(o.v[0]),
-                   "l"(o.v[1]), "l"(o.v[2]), "l"(o.v[3]), "l"(p)
-                   : "memory");
-    return;
-  }
-  if (left > 0) __stcs(reinterpret_cast<float4 *>(p), oct_lo(o));
-  if (left > 4) __stcs(reinterpret_cast<float4 *>(p) + 1, oct_hi(o));
-}
-// Whether all of these tensors of c channels a pixel take 256-bit accesses.
-template <class... T>
-inline bool wide_ok(int c, const T *...p) {
-  return c % 8 == 0 && (((reinterpret_cast<uintptr_t>(p) & 31) == 0) && ...);
-}
 
 // ------------------------------------------------------------- NCHW pieces
 // 32 channels of one pixel in a thread's registers, packed pairs; a warp's lanes

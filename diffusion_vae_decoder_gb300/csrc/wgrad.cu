@@ -262,13 +262,13 @@ struct XStager {
 // One of the 256 threads that bring dy: an octet of output channels at slots
 // first + 32 j. A 3x3 conv's stage has 130 slots, whose first two are the last
 // two of the stage before; the threads of the last two carry them over.
-template <int K, bool NHWC>
+template <int K, bool NHWC, bool WIDE>
 struct DyStager {
   const WgradParams &p;
   const int co8, first;
   const float *src = nullptr;
   int valid = 0;  // channels of the octet
-  float4 raw[4][2];
+  Oct raw[4];
   float scale[8];
 
   __device__ explicit DyStager(const WgradParams &params)
@@ -286,41 +286,34 @@ struct DyStager {
       scale[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
     }
   }
-  __device__ __forceinline__ void load_slot(float4 (&r)[2], int slot, const int *table) const {
+  __device__ __forceinline__ void load_slot(Oct &r, int slot, const int *table) const {
     const int pix = table[kTabDy + slot];
-    r[0] = r[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (pix < 0) return;
     if (NHWC) {
-      const float4 *q = reinterpret_cast<const float4 *>(
-          src + static_cast<unsigned long long>(static_cast<unsigned>(pix)) *
-                    static_cast<unsigned>(p.cout));
-      if (valid > 0) r[0] = __ldg(q);
-      if (valid > 4) r[1] = __ldg(q + 1);
-    } else {
+      r = load_oct<WIDE, false>(src + static_cast<unsigned long long>(static_cast<unsigned>(pix)) *
+                                          static_cast<unsigned>(p.cout),
+                                pix < 0 ? 0 : valid);
+      return;
+    }
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (pix >= 0) {
       const size_t hw = static_cast<size_t>(p.h) * p.w;
       const float *q = src + static_cast<size_t>(table[kTabImg + slot]) * (p.cout - 1) * hw + pix;
-      if (valid > 0) r[0].x = __ldg(q);
-      if (valid > 1) r[0].y = __ldg(q + hw);
-      if (valid > 2) r[0].z = __ldg(q + 2 * hw);
-      if (valid > 3) r[0].w = __ldg(q + 3 * hw);
-      if (valid > 4) r[1].x = __ldg(q + 4 * hw);
-      if (valid > 5) r[1].y = __ldg(q + 5 * hw);
-      if (valid > 6) r[1].z = __ldg(q + 6 * hw);
-      if (valid > 7) r[1].w = __ldg(q + 7 * hw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (valid > i) v[i] = __ldg(q + i * hw);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = pk2(v[2 * i], v[2 * i + 1]);
   }
   __device__ __forceinline__ uint32_t at(uint32_t stage, int slot) const {
     return stage + co8 * kSbo + slot * 16;
   }
-  __device__ __forceinline__ void store_slot(uint32_t stage, int slot,
-                                             const float4 (&r)[2]) const {
-    const uint64_t v[4] = {pk2(r[0].x, r[0].y), pk2(r[0].z, r[0].w), pk2(r[1].x, r[1].y),
-                           pk2(r[1].z, r[1].w)};
+  __device__ __forceinline__ void store_slot(uint32_t stage, int slot, const Oct &r) const {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (the scaling is exact, so the difference is what hi dropped)
-      const uint64_t s = mul2(v[i], pk2(scale[2 * i], scale[2 * i + 1]));
+      const uint64_t s = mul2(r.v[i], pk2(scale[2 * i], scale[2 * i + 1]));
       const __half2 h = __floats2half2_rn(lo2(s), hi2(s));
       const float2 f = __half22float2(h);
       const uint64_t rest = fma2(pk2(f.x, f.y), pk2(-1.f, -1.f), s);
@@ -339,7 +332,7 @@ struct DyStager {
       st_shared16(at(stage, slot), ld_shared16(at(before, kPos + slot)));
       st_shared16(at(stage, slot) + kLo, ld_shared16(at(before, kPos + slot) + kLo));
     } else {
-      float4 r[2];
+      Oct r;
       load_slot(r, slot, table);
       store_slot(stage, slot, r);
     }
@@ -351,7 +344,7 @@ __host__ __device__ __forceinline__ long long range_start(long long total, int g
   return total * c / grid;
 }
 
-template <int K, bool NHWC>
+template <int K, bool NHWC, bool WIDE>
 __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p) {
   constexpr int TAPS = K;  // kx
   constexpr uint32_t kAcc = TAPS * 2 * kTN;  // TMEM columns of the accumulators
@@ -504,7 +497,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
         if (i > 0) drain(i - 1);
       }
     } else {
-      DyStager<K, NHWC> st(p);
+      DyStager<K, NHWC, WIDE> st(p);
       const uint32_t base = smem_u32(smem);
       st.set_load_unit(unit_at(p, ld.unit));
       st.set_unit(unit_at(p, ld.unit));
@@ -668,57 +661,55 @@ __device__ __forceinline__ void scan_scales(const uint8_t *__restrict__ xs, long
 }
 
 // grid (slabs, ceil(cout / 1024)): sums [slab][cout] and the largest |dy| of
-// each output channel. The maxima do not depend on the order of the atomics.
-__global__ void __launch_bounds__(kScanThreads)
+// each output channel. The blocks are those resident at a time and sweep the
+// rows side by side. The maxima do not depend on the order of the atomics.
+template <bool WIDE>
+__global__ void __launch_bounds__(kScanThreads, 2)
     wgrad_scan_nhwc(const float *__restrict__ dy, long long rows, int cout,
                     const uint8_t *__restrict__ xs, int nb, float *__restrict__ psum,
                     unsigned *__restrict__ amax, unsigned *__restrict__ emax) {
+  constexpr int kDepth = 4;  // rows in flight
   __shared__ unsigned sm[128];
-  __shared__ float4 rs[kScanThreads], rm[kScanThreads];
-  const int c0 = blockIdx.y * 1024, quads = min(1024, cout - c0) / 4;
-  const int per = kScanThreads / quads, q = threadIdx.x % quads, l = threadIdx.x / quads;
-  const long long r0 = rows * blockIdx.x / gridDim.x, r1 = rows * (blockIdx.x + 1) / gridDim.x;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  uint4 m = make_uint4(0, 0, 0, 0);
-  if (l < per) {
-    const float *src = dy + c0 + 4 * q;
-    auto add = [&](float4 v) {
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-      m.x = max(m.x, abs_bits(v.x));
-      m.y = max(m.y, abs_bits(v.y));
-      m.z = max(m.z, abs_bits(v.z));
-      m.w = max(m.w, abs_bits(v.w));
-    };
-    long long r = r0 + l;
-    for (; r + 3 * per < r1; r += 4 * per) {
-      float4 v[4];
+  __shared__ float4 rs[2 * kScanThreads], rm[2 * kScanThreads];  // [row of a sweep][channel]
+  const int c0 = blockIdx.y * 1024, cols = min(1024, cout - c0), octs = (cols + 7) / 8;
+  const int per = kScanThreads / octs, q = threadIdx.x % octs, l = threadIdx.x / octs;
+  const int left = l < per ? cols - 8 * q : 0;
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  Oct s = {{0, 0, 0, 0}};
+  float m[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float *src = dy + c0 + 8 * q;
+  for (long long r = static_cast<long long>(blockIdx.x) * per + l; r < rows; r += kDepth * step) {
+    Oct v[kDepth];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        v[u] = __ldg(reinterpret_cast<const float4 *>(src + (r + u * per) * cout));
+    for (int u = 0; u < kDepth; ++u)
+      v[u] = load_oct<WIDE, false>(src + (r + u * step) * cout, r + u * step < rows ? left : 0);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) add(v[u]);
-    }
-    for (; r < r1; r += per) add(__ldg(reinterpret_cast<const float4 *>(src + r * cout)));
+    for (int u = 0; u < kDepth; u += 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s.v[i] = add2(s.v[i], add2(v[u].v[i], v[u + 1].v[i]));
+        m[2 * i] = max_abs3(m[2 * i], lo2(v[u].v[i]), lo2(v[u + 1].v[i]));
+        m[2 * i + 1] = max_abs3(m[2 * i + 1], hi2(v[u].v[i]), hi2(v[u + 1].v[i]));
+      }
   }
-  rs[threadIdx.x] = s;
-  rm[threadIdx.x] = make_float4(__uint_as_float(m.x), __uint_as_float(m.y),
-                                __uint_as_float(m.z), __uint_as_float(m.w));
+  if (l < per) {
+    const int at = 2 * (l * octs + q);
+    rs[at] = oct_lo(s);
+    rs[at + 1] = oct_hi(s);
+    rm[at] = make_float4(m[0], m[1], m[2], m[3]);
+    rm[at + 1] = make_float4(m[4], m[5], m[6], m[7]);
+  }
   __syncthreads();
-  if (threadIdx.x < quads) {
-    for (int k = 1; k < per; ++k) {
-      const float4 a = rs[k * quads + q], b = rm[k * quads + q];
-      s = make_float4(s.x + a.x, s.y + a.y, s.z + a.z, s.w + a.w);
-      m = make_uint4(max(m.x, __float_as_uint(b.x)), max(m.y, __float_as_uint(b.y)),
-                     max(m.z, __float_as_uint(b.z)), max(m.w, __float_as_uint(b.w)));
+  for (int c = threadIdx.x; c < cols; c += kScanThreads) {
+    float sum = 0.f, top = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < per; ++k) {
+      sum += reinterpret_cast<const float *>(rs)[k * octs * 8 + c];
+      const float t = reinterpret_cast<const float *>(rm)[k * octs * 8 + c];
+      top = max_abs3(top, t, t);
     }
-    *reinterpret_cast<float4 *>(psum + static_cast<size_t>(blockIdx.x) * cout + c0 + 4 * q) = s;
-    atomicMax(amax + c0 + 4 * q, m.x);
-    atomicMax(amax + c0 + 4 * q + 1, m.y);
-    atomicMax(amax + c0 + 4 * q + 2, m.z);
-    atomicMax(amax + c0 + 4 * q + 3, m.w);
+    psum[static_cast<size_t>(blockIdx.x) * cout + c0 + c] = sum;
+    atomicMax(amax + c0 + c, __float_as_uint(top));
   }
   if (blockIdx.y == 0) scan_scales(xs, rows, nb, emax, sm, blockIdx.x, gridDim.x);
 }
@@ -824,13 +815,13 @@ int floor_log2(unsigned d) {
 struct WgradWs {
   float *psum, *part;
   unsigned *maxima;  // amax [cout], emax [cp / 32]
-  int slabs, grid, units, stages;
+  int slabs, grid, units, stages;  // slabs: at most, of the scan
 };
 
 WgradWs carve_wgrad(Carver &cv, int n, int cin, int h, int w, int cout, int k) {
   WgradWs ws{};
   const long long rows = static_cast<long long>(n) * h * w;
-  ws.slabs = static_cast<int>(std::max(1ll, std::min<long long>(4 * kSMs, rows / 16)));
+  ws.slabs = static_cast<int>(std::max(1ll, std::min<long long>(2 * kSMs, rows / 8)));
   const long long positions = static_cast<long long>(n) * h * (w + (k == 3));
   ws.stages = ceil_div(positions, kPos);
   ws.units = ceil_div(cin, kTM) * ceil_div(cout, kTN) * k;
@@ -847,20 +838,26 @@ WgradWs carve_wgrad(Carver &cv, int n, int cin, int h, int w, int cout, int k) {
   return ws;
 }
 
-template <int K, bool NHWC>
+template <int K, bool NHWC, bool WIDE>
 int launch_mma(const WgradParams &p, int grid, cudaStream_t s) {
   // (the register split waits for what the launch did not bring)
   static const int regs = [] {
     cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, wgrad_mma<K, NHWC>) == cudaSuccess ? a.numRegs : 0;
+    return cudaFuncGetAttributes(&a, wgrad_mma<K, NHWC, WIDE>) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs != kLaunchRegs) return VAE_ECUDA;
-  VAE_CUDA_TRY(cudaFuncSetAttribute(wgrad_mma<K, NHWC>,
+  VAE_CUDA_TRY(cudaFuncSetAttribute(wgrad_mma<K, NHWC, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem)));
-  wgrad_mma<K, NHWC><<<grid, kMmaThreads, kSmem, s>>>(p);
+  wgrad_mma<K, NHWC, WIDE><<<grid, kMmaThreads, kSmem, s>>>(p);
   VAE_LAUNCH_CHECK();
   return VAE_OK;
+}
+
+template <int K>
+int launch_mma(const WgradParams &p, int nhwc, bool wide, int grid, cudaStream_t s) {
+  if (!nhwc) return launch_mma<K, false, false>(p, grid, s);
+  return wide ? launch_mma<K, true, true>(p, grid, s) : launch_mma<K, true, false>(p, grid, s);
 }
 
 }  // namespace
@@ -904,20 +901,21 @@ int wgrad(const float *dy, CkptView x, int n, int cin, int h, int w, int nhwc, i
   if (!p.err) return VAE_ECUDA;
   p.wait_ns = wait_limit_ns();
   VAE_CUDA_TRY(cudaMemsetAsync(ws.maxima, 0, (cout + nb) * sizeof(unsigned), s));
+  const bool wide = wide_ok(cout, dy);
+  int slabs;
   if (nhwc) {
-    wgrad_scan_nhwc<<<dim3(ws.slabs, ceil_div(cout, 1024)), kScanThreads, 0, s>>>(
+    const int per = kScanThreads / std::min(128, ceil_div(cout, 8));  // rows of a block's sweep
+    slabs = static_cast<int>(std::max(1ll, std::min<long long>(ws.slabs, rows / (4 * per))));
+    (wide ? wgrad_scan_nhwc<true> : wgrad_scan_nhwc<false>)<<<
+        dim3(slabs, ceil_div(cout, 1024)), kScanThreads, 0, s>>>(
         dy, rows, cout, x.scale, nb, ws.psum, ws.maxima, ws.maxima + cout);
   } else {
-    const int slabs = std::max(1, std::min(ws.slabs, 8 * kSMs / cout));
+    slabs = std::max(1, std::min(ws.slabs, 8 * kSMs / cout));
     wgrad_scan_nchw<<<dim3(slabs, cout), kScanThreads, 0, s>>>(
         dy, n, hw, cout, x.scale, nb, ws.psum, ws.maxima, ws.maxima + cout);
   }
   VAE_LAUNCH_CHECK();
-  const int slabs = nhwc ? ws.slabs : std::max(1, std::min(ws.slabs, 8 * kSMs / cout));
-  if (k == 3)
-    VAE_TRY((nhwc ? launch_mma<3, true> : launch_mma<3, false>)(p, ws.grid, s));
-  else
-    VAE_TRY((nhwc ? launch_mma<1, true> : launch_mma<1, false>)(p, ws.grid, s));
+  VAE_TRY((k == 3 ? launch_mma<3> : launch_mma<1>)(p, nhwc, wide, ws.grid, s));
   const dim3 rg(ceil_div(cin, kTM) + 1, cout);
   if (k == 3)
     wgrad_reduce<3><<<rg, kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
