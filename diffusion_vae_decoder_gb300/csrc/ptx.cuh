@@ -71,6 +71,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
   }
 }
 
+// The same with one try in the code, for kernels of many roles and waits, whose
+// instruction fetch counts.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity,
+                                                volatile uint32_t *abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  uint32_t tries = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (++tries & 31) continue;
+    if (*abort) return false;
+    const uint64_t now = global_timer_ns();
+    if (tries == 32) t0 = now;
+    if (now - t0 > limit_ns) return false;
+  }
+  return true;
+}
+
 // Flag exchange between CTAs of one launch (gpu scope).
 __device__ __forceinline__ int ld_acquire_gpu(const int *p) {
   int v;
@@ -352,16 +369,25 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const float *v) {
       : "memory");
 }
 
-// Registers per thread of this warpgroup (all four warps call), within what the
-// block was launched with.
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+// 8 columns at each of two places, one wait for both.
+__device__ __forceinline__ void tmem_ld_8cols_pair(uint32_t t0, uint32_t t1, float *a, float *b) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]),
+        "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]),
+        "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15])
+      : "r"(t0), "r"(t1)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = __uint_as_float(r[i]);
+    b[i] = __uint_as_float(r[8 + i]);
+  }
 }
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
+
 
 // Registers -> TMEM, 16 lanes x 16 columns from the address's lane on: register
 // 2 i + h of thread t goes to lane t / 4 + 8 h, column 4 i + t % 4. Not waited for.

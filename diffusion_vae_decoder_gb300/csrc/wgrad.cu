@@ -23,8 +23,9 @@
 // 22 significant bits. The MMA reads [hi | lo] as 128 columns next to one A
 // operand, so the two parts have accumulators of their own. The tensor core's
 // accumulator truncates: measured on GB300, a sum is off by about 1e-8 of its
-// value per step. So a chain of MMAs ends after kChain stages; its sums move to
-// FP32 registers, rounded to nearest.
+// value per step. So a chain of MMAs ends after kChain stages; its sums are added
+// to the piece's FP32 numbers in global memory, rounded to nearest. Each of those
+// belongs to one thread, whose additions keep their order.
 //
 // Schedule. (unit, stage) pairs, unit = (input-channel tile, output-channel
 // tile, ky), are cut into equal contiguous ranges, one per SM, so that work
@@ -36,7 +37,16 @@
 // (global -> registers -> halves -> shared memory), each thread loading the next
 // stage's piece where it has just converted this one's; all sixteen drain the
 // accumulators. Three warps turn positions into pixel indexes and block scales
-// ahead of them, one thread issues the MMAs.
+// ahead of them. Three threads issue the MMAs, one per tap: a thread takes 80
+// clocks to issue one, the tensor core 64 to run it.
+//
+// Bound: the tensor core (24 MMAs of 64 clocks a stage), then what the staging
+// warps and barriers add. 128 to 128 channels at 512^2: 114 us, 12300 stages of
+// 128 positions on 150 SMs, 65 us of them the MMAs' (154 GFLOP; 1.36 PFLOP/s).
+// Measured on the way at this size: one issuing thread 142 us, sums in registers
+// with the spills of prefetched data that they bring 187 us, 128-bit loads of dy
+// (each sector twice) 40 us more; sixteen warps for x~ at 64 registers 179 us,
+// sixteen for dy 115 us.
 #include "ptx.cuh"
 #include "silu.cuh"
 #include "wgrad.cuh"
@@ -52,26 +62,29 @@ constexpr int kStagesA = 2;        // x~ in TMEM, 64 columns each
 constexpr int kStagesB = 4;        // dy in shared memory
 constexpr int kTables = 4;
 constexpr int kChain = 16;         // stages between two drains: 2048 positions
-constexpr int kStagers = 512;      // staging threads: eight warps for x~, eight for dy
-constexpr int kDyThreads = 256;
+constexpr int kXGroups = 2;        // of four warps each, for a share of the positions
+constexpr int kXWarps = 4 * kXGroups, kDyWarps = 8;
+constexpr int kStageWarps = kXWarps + kDyWarps;
 constexpr int kTableWarps = 3;     // each makes every third table
-constexpr int kMmaThreads = kStagers + 128;  // one more warpgroup issues and makes tables
-// Registers: the launch gives every thread kLaunchRegs (65536 / 640, rounded
-// down to a multiple of 8); the last warpgroup hands its share to the staging
-// ones, which hold the accumulators and a raw stage.
-constexpr int kLaunchRegs = 96, kStageRegs = 104, kIssueRegs = 64;
-static_assert(4 * kStageRegs + kIssueRegs <= 5 * kLaunchRegs, "the split fits the launch");
+constexpr int kIssueWarp = kStageWarps, kTableWarp = kStageWarps + 3;  // one issuer per tap
+constexpr int kMmaThreads = 32 * (kTableWarp + kTableWarps);
 // Positions between two octets of dy: odd, so that 16-byte pieces of neighbouring
 // octets fall into different banks.
 constexpr int kSlots = kPos + 3;
 constexpr uint32_t kSbo = kSlots * 16;
 constexpr uint32_t kLo = kTN / 8 * kSbo;               // from an octet's hi to its lo
 constexpr uint32_t kStageBytes = 2 * kTN / 8 * kSbo;
-// A stage's table: the x~ pixel of each position (-1: a zero), the scales of the
-// four 32-channel blocks (a pair of halves per two positions), the dy pixel of
-// each slot (-1: a zero) and its sample.
-constexpr int kTabX = 0, kTabScale = kPos, kTabDy = kTabScale + 4 * (kPos / 2),
-              kTabImg = kTabDy + kPos + 4, kTableInts = kTabImg + kPos + 4;
+// A stage's table: its unit and flags, the x~ pixel of each position (-1: a
+// zero), the scales of the four 32-channel blocks (a pair of halves per two
+// positions), the dy pixel of each slot (-1: a zero) and, NCHW, its sample.
+constexpr int kTabUnit = 0, kTabFlags = 1, kTabX = 4, kTabScale = kTabX + kPos,
+              kTabDy = kTabScale + 4 * (kPos / 2), kTabImg = kTabDy + kPos + 4,
+              kTableInts = kTabImg + kPos + 4;
+enum : int {
+  kNewUnit = 1,     // the stage before is another unit's
+  kChainEnd = 2,    // its MMAs end a chain
+  kFirstChain = 4,  // which is the first of its (unit, SM) piece
+};
 constexpr size_t kSmem = kStagesB * kStageBytes + kTables * kTableInts * 4 + 256;
 static_assert(kSmem <= 227 * 1024, "stages fit an SM");
 static_assert(kStageBytes % 16 == 0 && kTableInts % 4 == 0, "aligned");
@@ -112,6 +125,27 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+// Loads where `at` is not negative, else zeros: predicated, where a branch around
+// each would cost the staging warps more than the loads.
+__device__ __forceinline__ uint32_t load4_if(int at, const uint8_t *p) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ge.s32 q, %1, 0;\n\tmov.b32 %0, 0;\n\t"
+      "@q ld.global.nc.b32 %0, [%2];\n\t}"
+      : "=r"(v)
+      : "r"(at), "l"(p));
+  return v;
+}
+__device__ __forceinline__ Oct load32_if(int at, const float *p) {
+  Oct o;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ge.s32 q, %4, 0;\n\t"
+      "mov.b64 %0, 0;\n\tmov.b64 %1, 0;\n\tmov.b64 %2, 0;\n\tmov.b64 %3, 0;\n\t"
+      "@q ld.global.L1::no_allocate.v4.b64 {%0, %1, %2, %3}, [%5];\n\t}"
+      : "=&l"(o.v[0]), "=&l"(o.v[1]), "=&l"(o.v[2]), "=&l"(o.v[3])
+      : "r"(at), "l"(p));
+  return o;
 }
 // The power of two that brings a channel's largest |dy| to [2^14, 2^15), as a
 // float (2^127 at most); 1 for a channel with a non-finite value.
@@ -158,22 +192,30 @@ struct Chain {
 
 // One warp makes a stage's table. dy slot j is position q0 - 1 + j for a 3x3
 // conv (tap kx pairs x~'s position k with slot k + 2 - kx), q0 + j for a 1x1.
-template <int K>
+template <int K, bool NHWC>
 __device__ __forceinline__ void make_table(const WgradParams &p, unsigned q0, const Unit &un,
                                            const uint32_t *etop, int lane, int *table) {
   const int nb = p.cp >> 5, b0 = un.ci0 >> 5;
   const bool words = (nb & 3) == 0;  // four blocks' scale bytes in one load
-  const unsigned rows = static_cast<unsigned>(p.n) * p.h;
+  const int up = K == 3 ? 1 - un.ky : 0;
+  // x~'s pixel at a position (-1: none), and dy's in its slot
+  auto place = [&](unsigned pos, int slot) {
+    const unsigned row = fast_div(pos & 0x3fffffffu, p.wp_magic, p.wp_shift);
+    const int x = static_cast<int>(pos - row * p.wp);
+    const int img = static_cast<int>(fast_div(row, p.h_magic, p.h_shift));
+    const int y = static_cast<int>(row) - img * p.h + up;
+    const int pix = pos < p.positions && x < p.w ? static_cast<int>(row) * p.w + x : -1;
+    table[kTabDy + slot] = pix >= 0 && y >= 0 && y < p.h ? pix + up * p.w : -1;
+    if (!NHWC) table[kTabImg + slot] = img;
+    return pix;
+  };
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int pair = lane + 32 * i;
     uint32_t four[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const unsigned pos = q0 + 2 * pair + h;
-      const unsigned row = fast_div(pos, p.wp_magic, p.wp_shift);
-      const int x = static_cast<int>(pos - row * p.wp);
-      const int pix = row < rows && x < p.w ? static_cast<int>(row) * p.w + x : -1;
+      const int pix = place(q0 + 2 * pair + h, 2 * pair + h + (K == 3));
       table[kTabX + 2 * pair + h] = pix;
       four[h] = 0;
       if (pix >= 0) {
@@ -201,49 +243,36 @@ __device__ __forceinline__ void make_table(const WgradParams &p, unsigned q0, co
           static_cast<int>(h2_bits(__floats2half2_rn(f[0], f[1])));
     }
   }
-  for (int slot = lane; slot < kPos + K - 1; slot += 32) {
-    const unsigned pos = q0 + slot - (K == 3);  // (wraps below the first position)
-    const unsigned row = fast_div(pos & 0x3fffffffu, p.wp_magic, p.wp_shift);
-    const int x = static_cast<int>(pos - row * p.wp);
-    const int img = static_cast<int>(fast_div(row, p.h_magic, p.h_shift));
-    const int y = static_cast<int>(row) - img * p.h + (K == 3 ? 1 - un.ky : 0);
-    const bool in = pos < p.positions && x < p.w && y >= 0 && y < p.h;
-    table[kTabDy + slot] =
-        in ? (static_cast<int>(row) + (K == 3 ? 1 - un.ky : 0)) * p.w + x : -1;
-    table[kTabImg + slot] = img;
-  }
+  if (K == 3 && lane < 2) place(lane ? q0 + kPos : q0 - 1, lane * (kPos + 1));
 }
 
-// One of the 256 threads that bring x~. Warp w fills TMEM lanes 32 (w % 4) ..,
-// one 32-channel block, for positions 64 (w / 4) ..; thread t of it takes four
-// channels 4 (t / 4) + j, which land in lanes t / 4 + 8 j of the quadrant, at
+// One of the threads that bring x~. Warp w fills TMEM lanes 32 (w % 4) .., one
+// 32-channel block, for a group's share of the positions; thread t of it takes
+// four channels 4 (t / 4) + j, which land in lanes t / 4 + 8 j of the quadrant, at
 // two positions in eight.
 struct XStager {
   const WgradParams &p;
-  const int quad, pair0;  // of the first of its pairs; eight of them, 4 apart
+  static constexpr int kPairs = kPos / 8 / kXGroups;  // a thread's, four apart
+  const int quad, pair0;  // of the first
   const uint8_t *src = nullptr;
-  uint32_t raw[16];
+  int none = 0;  // -1 behind the last channel
+  uint32_t raw[2 * kPairs];
 
   __device__ explicit XStager(const WgradParams &params)
       : p(params), quad(threadIdx.x >> 5 & 3),
-        pair0(32 * (threadIdx.x >> 7) + (threadIdx.x & 3)) {}
+        pair0(4 * kPairs * (threadIdx.x >> 7) + (threadIdx.x & 3)) {}
   __device__ void set_load_unit(const Unit &un) {
     const int ch = un.ci0 + 32 * quad + (threadIdx.x >> 2 & 7) * 4;
-    src = ch < p.cp ? p.xq + ch : nullptr;
+    none = ch < p.cp ? 0 : -1;
+    src = p.xq + ch;
   }
-  __device__ __forceinline__ void load(int i, const int *table) {
+  __device__ __forceinline__ void load(int i, const int *table, int skip) {
     const int2 pix = *reinterpret_cast<const int2 *>(table + kTabX + 2 * (pair0 + 4 * i));
-    raw[2 * i] = raw[2 * i + 1] = 0;
-    if (src) {
-      if (pix.x >= 0)
-        raw[2 * i] = __ldg(reinterpret_cast<const uint32_t *>(
-            src + static_cast<unsigned long long>(static_cast<unsigned>(pix.x)) *
-                      static_cast<unsigned>(p.cp)));
-      if (pix.y >= 0)
-        raw[2 * i + 1] = __ldg(reinterpret_cast<const uint32_t *>(
-            src + static_cast<unsigned long long>(static_cast<unsigned>(pix.y)) *
-                      static_cast<unsigned>(p.cp)));
-    }
+    const unsigned cp = static_cast<unsigned>(p.cp);
+    raw[2 * i] = load4_if(pix.x | skip, src + static_cast<unsigned long long>(
+                                                  static_cast<unsigned>(pix.x)) * cp);
+    raw[2 * i + 1] = load4_if(pix.y | skip, src + static_cast<unsigned long long>(
+                                                      static_cast<unsigned>(pix.y)) * cp);
   }
   // Pair i as halves: channel j of the two positions in out[j].
   __device__ __forceinline__ void convert(int i, const int *table, uint32_t *out) const {
@@ -259,39 +288,50 @@ struct XStager {
   }
 };
 
-// One of the 256 threads that bring dy: an octet of output channels at slots
-// first + 32 j. A 3x3 conv's stage has 130 slots, whose first two are the last
+// One of the threads that bring dy: an octet of output channels at slots
+// first + kStep j. A 3x3 conv's stage has 130 slots, whose first two are the last
 // two of the stage before; the threads of the last two carry them over.
 template <int K, bool NHWC, bool WIDE>
 struct DyStager {
   const WgradParams &p;
+  static constexpr int kStep = 4 * kDyWarps, kCount = kPos / kStep;
   const int co8, first;
   const float *src = nullptr;
   int valid = 0;  // channels of the octet
-  Oct raw[4];
-  float scale[8];
+  Oct raw[kCount];
+  uint64_t scale[4];
 
-  __device__ explicit DyStager(const WgradParams &params)
-      : p(params), co8(NHWC ? threadIdx.x & 7 : (threadIdx.x & 255) >> 5),
-        first((NHWC ? (threadIdx.x & 255) >> 3 : threadIdx.x & 31) + (K - 1)) {}
+  __device__ DyStager(const WgradParams &params, int t)
+      : p(params), co8(NHWC ? t & 7 : t >> 5 & 7),
+        first((NHWC ? t >> 3 : (t & 31) + (t >> 8) * 32) + (K - 1)) {}
   __device__ void set_load_unit(const Unit &un) {
     const int co = un.co0 + 8 * co8;
     valid = p.cout - co;
     src = p.dy + (NHWC ? static_cast<size_t>(co) : static_cast<size_t>(co) * p.h * p.w);
   }
   __device__ void set_unit(const Unit &un) {
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int co = un.co0 + 8 * co8 + i;
-      scale[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
+      f[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scale[i] = pk2(f[2 * i], f[2 * i + 1]);
   }
-  __device__ __forceinline__ void load_slot(Oct &r, int slot, const int *table) const {
-    const int pix = table[kTabDy + slot];
+  // skip: -1 to load nothing (zeros)
+  __device__ __forceinline__ void load_slot(Oct &r, int slot, const int *table, int skip) const {
+    const int pix = table[kTabDy + slot] | skip;
+    if (WIDE) {
+      r = load32_if(valid > 0 ? pix : -1,
+                    src + static_cast<unsigned long long>(static_cast<unsigned>(pix)) *
+                              static_cast<unsigned>(p.cout));
+      return;
+    }
     if (NHWC) {
-      r = load_oct<WIDE, false>(src + static_cast<unsigned long long>(static_cast<unsigned>(pix)) *
-                                          static_cast<unsigned>(p.cout),
-                                pix < 0 ? 0 : valid);
+      r = load_oct<false, false>(src + static_cast<unsigned long long>(static_cast<unsigned>(pix)) *
+                                           static_cast<unsigned>(p.cout),
+                                 pix < 0 ? 0 : valid);
       return;
     }
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -313,7 +353,7 @@ struct DyStager {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (the scaling is exact, so the difference is what hi dropped)
-      const uint64_t s = mul2(r.v[i], pk2(scale[2 * i], scale[2 * i + 1]));
+      const uint64_t s = mul2(r.v[i], scale[i]);
       const __half2 h = __floats2half2_rn(lo2(s), hi2(s));
       const float2 f = __half22float2(h);
       const uint64_t rest = fma2(pk2(f.x, f.y), pk2(-1.f, -1.f), s);
@@ -326,14 +366,14 @@ struct DyStager {
   // Slots 0 and 1 of a 3x3 stage, by the threads of slots 128 and 129.
   __device__ __forceinline__ void carry(uint32_t stage, uint32_t before, bool contiguous,
                                         const int *table) const {
-    if (K == 1 || first + 96 < kPos) return;
-    const int slot = first + 96 - kPos;
+    const int slot = first - kStep;
+    if (K == 1 || slot < 0) return;
     if (contiguous) {
       st_shared16(at(stage, slot), ld_shared16(at(before, kPos + slot)));
       st_shared16(at(stage, slot) + kLo, ld_shared16(at(before, kPos + slot) + kLo));
     } else {
       Oct r;
-      load_slot(r, slot, table);
+      load_slot(r, slot, table, 0);
       store_slot(stage, slot, r);
     }
   }
@@ -342,6 +382,21 @@ struct DyStager {
 // First (unit, stage) of SM range c.
 __host__ __device__ __forceinline__ long long range_start(long long total, int grid, int c) {
   return total * c / grid;
+}
+
+// The SM range that holds stage g, the largest c with total * c < (g + 1) * grid:
+// guessed in FP32 (c < 152, so at most one off) and put right.
+__device__ __forceinline__ int range_of(long long total, int grid, long long g) {
+  const long long bound = (g + 1) * grid;
+  int c = static_cast<int>(__fdividef(static_cast<float>(bound), static_cast<float>(total)));
+  while (total * c >= bound) --c;
+  while (total * (c + 1) < bound) ++c;
+  return c;
+}
+
+// Adds to a value that only this thread writes, in its order.
+__device__ __forceinline__ void red_add(float *p, float v) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
 
 template <int K, bool NHWC, bool WIDE>
@@ -362,23 +417,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStagesA; ++i) {
-      mbar_init(a_full + i, (kStagers - kDyThreads) / 32);
-      mbar_init(a_empty + i, 1);
+      mbar_init(a_full + i, kXWarps);
+      mbar_init(a_empty + i, TAPS);
     }
     for (int i = 0; i < kStagesB; ++i) {
-      mbar_init(b_full + i, kDyThreads / 32);
-      mbar_init(b_empty + i, 1);
+      mbar_init(b_full + i, kDyWarps);
+      mbar_init(b_empty + i, TAPS);
     }
     for (int i = 0; i < kTables; ++i) {
       mbar_init(tab_full + i, 1);
-      mbar_init(tab_empty + i, kStagers / 32);
+      mbar_init(tab_empty + i, kStageWarps);
     }
-    mbar_init(acc_done, 1);
-    mbar_init(acc_free, kStagers / 32);
+    mbar_init(acc_done, TAPS);
+    mbar_init(acc_free, kStageWarps);
     *abort = 0u;
     fence_mbarrier_init();
   }
-  if (warp == kStagers / 32) {
+  if (warp == kIssueWarp) {
     tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
   }
@@ -389,90 +444,76 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   const long long g0 = range_start(p.total, gridDim.x, blockIdx.x);
   const int count = static_cast<int>(range_start(p.total, gridDim.x, blockIdx.x + 1) - g0);
   const Cursor start{static_cast<int>(g0 / p.stages), static_cast<int>(g0 % p.stages)};
-  auto give_up = [&]() {
-    *abort = 1u;
-    atomicCAS(p.err, 0, static_cast<int>(VAE_EDEVICE_TIMEOUT));
-  };
+  bool ok = true;
 
-  if (warp < kStagers / 32) {
-    setmaxnreg_inc<kStageRegs>();
-    bool ok = true;
+  if (warp < kStageWarps) {
     // Waits agree across the warp, so that a timeout leaves it converged.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, p.wait_ns));
+      return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, abort, p.wait_ns));
     };
-
-    // This warp drains TMEM lanes 32 (warp % 4) .., output channels 16 (warp / 4) ..
+    // Two at once: a wait that finds its phase complete still takes some 300 clocks.
+    auto wait_both = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) {
+      const bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+      return __all_sync(0xffffffffu, r0 && r1) || (wait(b0, p0) && wait(b1, p1));
+    };
+    // TMEM lanes 32 (warp % 4) ..
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-    float acc[TAPS][16];
-#pragma unroll
-    for (int k = 0; k < TAPS; ++k)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[k][i] = 0.f;
     uint32_t chains = 0;
-    Cursor dr = start;  // the stage whose chain end is looked at next
-    Chain dr_chain;
-    // Looks at stage `i`; called one stage behind, when the next chain's first
-    // stage is on its way.
-    auto drain = [&](int i) {
-      const bool piece_end = i == count - 1 || dr.stage == p.stages - 1;
-      const int unit = dr.unit;
-      dr.next(p.stages);
-      if (!dr_chain.ends(piece_end)) return;
+    // Brings a finished chain's sums to the piece; called one stage behind its
+    // last, when the next chain's first stage is on its way.
+    auto drain = [&](int flags, int unit) {
+      if (!ok || !(flags & kChainEnd)) return;
       ok = wait(acc_done, chains & 1);
       if (!ok) return;
+      ++chains;
       tc_fence_after();
+      // TMEM lane r of a quadrant is channel 4 (r % 8) + r / 8
+      const size_t piece = static_cast<size_t>(unit) + blockIdx.x;
+      float *o = p.part + piece * (TAPS * kTN * kTM) + (warp & 3) * 32 + 4 * (lane & 7) +
+                 (lane >> 3);
+#pragma unroll 1
+      for (int c = warp >> 2; c < TAPS * kTN / 8; c += kStageWarps / 4) {
+        const uint32_t at = t_lane + (c / (kTN / 8)) * 2 * kTN + c % (kTN / 8) * 8;
+        float v[8], low[8];
+        tmem_ld_8cols_pair(at, at + kTN, v, low);
+        float *dst = o + c * 8 * kTM;
+        if (flags & kFirstChain) {
 #pragma unroll
-      for (int k = 0; k < TAPS; ++k) {
-        float v[16];
-        tmem_ld_16cols(t_lane + (warp >> 2) * 16 + k * 2 * kTN, v);
+          for (int j = 0; j < 8; ++j) dst[j * kTM] = v[j] + low[j];
+        } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[k][j] += v[j];
-        tmem_ld_16cols(t_lane + (warp >> 2) * 16 + k * 2 * kTN + kTN, v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) acc[k][j] += v[j];
+          for (int j = 0; j < 8; ++j) red_add(dst + j * kTM, v[j] + low[j]);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_free);
-      ++chains;
-      if (piece_end) {
-        // TMEM lane r of a quadrant is channel 4 (r % 8) + r / 8
-        const size_t piece = static_cast<size_t>(unit) + blockIdx.x;
-        float *o = p.part + piece * (TAPS * kTN * kTM) + (warp >> 2) * 16 * kTM +
-                   (warp & 3) * 32 + 4 * (lane & 7) + (lane >> 3);
-#pragma unroll
-        for (int k = 0; k < TAPS; ++k)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            o[(k * kTN + j) * kTM] = acc[k][j];
-            acc[k][j] = 0.f;
-          }
-      }
     };
+    int flags = 0, unit = start.unit;  // of the stage before
 
-    Cursor ld = start;  // the stage that is loaded next
-    if (warp < (kStagers - kDyThreads) / 32) {
+    if (warp < kXWarps) {
       XStager st(p);
-      st.set_load_unit(unit_at(p, ld.unit));
+      st.set_load_unit(unit_at(p, start.unit));
       ok = wait(tab_full, 0);
       if (ok)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) st.load(k, tables);
+        for (int k = 0; k < st.kPairs; ++k) st.load(k, tables, st.none);
 #pragma unroll 1
       for (int i = 0; i < count && ok; ++i) {
         const int *table = tables + (i % kTables) * kTableInts;
-        const bool more = i + 1 < count;
         const int *ahead = tables + ((i + 1) % kTables) * kTableInts;
-        if (ld.next(p.stages) && more) st.set_load_unit(unit_at(p, ld.unit));
-        if (more) ok = wait(tab_full + (i + 1) % kTables, ((i + 1) / kTables) & 1);
-        if (ok && i >= kStagesA)
-          ok = wait(a_empty + i % kStagesA, (i / kStagesA - 1) & 1);
+        const bool more = i + 1 < count;
+        const int next = more ? i + 1 : i;
+        ok = wait_both(tab_full + next % kTables, (next / kTables) & 1, a_empty + i % kStagesA,
+                       (i / kStagesA + 1) & 1);
         if (!ok) break;
+        if (more && (ahead[kTabFlags] & kNewUnit)) st.set_load_unit(unit_at(p, ahead[kTabUnit]));
         tc_fence_after();
-        const uint32_t dst = t_lane + kAcc + (i % kStagesA) * (kPos / 2) + (warp >> 2) * 32;
+        const int skip = more ? st.none : -1;
+        const uint32_t dst = t_lane + kAcc + (i % kStagesA) * (kPos / 2) +
+                             (warp >> 2) * (4 * st.kPairs);
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
+        for (int k = 0; k < st.kPairs; k += 4) {
           uint32_t low[8], high[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -482,11 +523,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
             low[2 * j + 1] = o[1];
             high[2 * j] = o[2];
             high[2 * j + 1] = o[3];
-            if (more) st.load(k + j, ahead);
+            st.load(k + j, ahead, skip);
           }
           tmem_st_16x16(dst + 4 * k, low);
           tmem_st_16x16(dst + 4 * k + (16u << 16), high);
         }
+        const int2 head = *reinterpret_cast<const int2 *>(table);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -494,35 +536,39 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
           mbar_arrive(a_full + i % kStagesA);
           mbar_arrive(tab_empty + i % kTables);
         }
-        if (i > 0) drain(i - 1);
+        drain(flags, unit);
+        unit = head.x;
+        flags = head.y;
       }
     } else {
-      DyStager<K, NHWC, WIDE> st(p);
+      DyStager<K, NHWC, WIDE> st(p, threadIdx.x - 32 * kXWarps);
       const uint32_t base = smem_u32(smem);
-      st.set_load_unit(unit_at(p, ld.unit));
-      st.set_unit(unit_at(p, ld.unit));
-      Cursor cv = start;  // the stage that is converted
-      bool contiguous = false;
+      st.set_load_unit(unit_at(p, start.unit));
       ok = wait(tab_full, 0);
       if (ok)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) st.load_slot(st.raw[j], st.first + 32 * j, tables);
+        for (int j = 0; j < st.kCount; ++j) 
+          st.load_slot(st.raw[j], st.first + st.kStep * j, tables, 0);
+      st.set_unit(unit_at(p, start.unit));
 #pragma unroll 1
       for (int i = 0; i < count && ok; ++i) {
         const int *table = tables + (i % kTables) * kTableInts;
-        const bool more = i + 1 < count;
         const int *ahead = tables + ((i + 1) % kTables) * kTableInts;
+        const bool more = i + 1 < count;
         const uint32_t stage = base + (i % kStagesB) * kStageBytes;
         const uint32_t before = base + ((i + kStagesB - 1) % kStagesB) * kStageBytes;
-        if (i >= kStagesB) ok = wait(b_empty + i % kStagesB, (i / kStagesB - 1) & 1);
-        if (ok && more) ok = wait(tab_full + (i + 1) % kTables, ((i + 1) / kTables) & 1);
+        const int next = more ? i + 1 : i;
+        ok = wait_both(tab_full + next % kTables, (next / kTables) & 1, b_empty + i % kStagesB,
+                       (i / kStagesB + 1) & 1);
         if (!ok) break;
-        st.carry(stage, before, contiguous, table);
-        if (ld.next(p.stages) && more) st.set_load_unit(unit_at(p, ld.unit));
+        const int2 head = *reinterpret_cast<const int2 *>(table);
+        if (i > 0 && (head.y & kNewUnit)) st.set_unit(unit_at(p, head.x));
+        st.carry(stage, before, !(head.y & kNewUnit), table);
+        if (more && (ahead[kTabFlags] & kNewUnit)) st.set_load_unit(unit_at(p, ahead[kTabUnit]));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          st.store_slot(stage, st.first + 32 * j, st.raw[j]);
-          if (more) st.load_slot(st.raw[j], st.first + 32 * j, ahead);
+        for (int j = 0; j < st.kCount; ++j) {
+          st.store_slot(stage, st.first + st.kStep * j, st.raw[j]);
+          st.load_slot(st.raw[j], st.first + st.kStep * j, ahead, more ? 0 : -1);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -530,67 +576,75 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
           mbar_arrive(b_full + i % kStagesB);
           mbar_arrive(tab_empty + i % kTables);
         }
-        contiguous = !cv.next(p.stages);
-        if (!contiguous && more) st.set_unit(unit_at(p, cv.unit));
-        if (i > 0) drain(i - 1);
+        drain(flags, unit);
+        unit = head.x;
+        flags = head.y;
       }
     }
-    if (ok) drain(count - 1);
-    if (!ok) give_up();
-  } else {
-    setmaxnreg_dec<kIssueRegs>();
-    if (threadIdx.x == kStagers) {
+    if (count > 0) drain(flags, unit);
+  } else if (warp < kTableWarp) {
+    const int tap = warp - kIssueWarp;
+    if (tap < TAPS && lane == 0) {
       constexpr uint32_t idesc = idesc_f16_tmem_a(kTM, 2 * kTN);
+      const uint32_t acc = tmem + tap * 2 * kTN;
       const uint32_t base = smem_u32(smem);
       uint32_t chains = 0;
-      bool fresh = true, ok = true;
+      bool fresh = true;
+      // What the next stage needs is asked for before this one's MMAs are done.
+      bool a_ready = false, b_ready = false;
       Cursor at = start;
       Chain chain;
       for (int i = 0; i < count && ok; ++i) {
         const int sa = i % kStagesA, sb = i % kStagesB;
-        if (fresh && chains > 0) ok = mbar_wait(acc_free, (chains - 1) & 1, abort, p.wait_ns);
-        if (ok) ok = mbar_wait(a_full + sa, (i / kStagesA) & 1, abort, p.wait_ns);
-        if (ok) ok = mbar_wait(b_full + sb, (i / kStagesB) & 1, abort, p.wait_ns);
+        if (!a_ready) ok = mbar_wait_short(a_full + sa, (i / kStagesA) & 1, abort, p.wait_ns);
+        if (ok && !b_ready) ok = mbar_wait_short(b_full + sb, (i / kStagesB) & 1, abort, p.wait_ns);
+        if (ok && fresh && chains > 0)
+          ok = mbar_wait_short(acc_free, (chains - 1) & 1, abort, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = tmem + kAcc + sa * (kPos / 2);
-        const uint64_t b = mn_major_desc(base + sb * kStageBytes, 128, kSbo);
+        const uint64_t b = mn_major_desc(base + sb * kStageBytes, 128, kSbo) + (TAPS - 1 - tap);
 #pragma unroll
         for (int k = 0; k < kPos / 16; ++k)
-#pragma unroll
-          for (int tap = 0; tap < TAPS; ++tap)
-            umma_f16_tmem_a(tmem + tap * 2 * kTN, a + 8 * k, b + 16 * k + (TAPS - 1 - tap), idesc,
-                            !fresh || k > 0);
-        fresh = false;
+          umma_f16_tmem_a(acc, a + 8 * k, b + 16 * k, idesc, !fresh || k > 0);
+        a_ready = mbar_try_wait(a_full + (i + 1) % kStagesA, ((i + 1) / kStagesA) & 1);
+        b_ready = mbar_try_wait(b_full + (i + 1) % kStagesB, ((i + 1) / kStagesB) & 1);
         umma_commit(a_empty + sa);
         umma_commit(b_empty + sb);
         const bool piece_end = i == count - 1 || at.stage == p.stages - 1;
         at.next(p.stages);
-        if (chain.ends(piece_end)) {
+        fresh = chain.ends(piece_end);
+        if (fresh) {
           umma_commit(acc_done);
           ++chains;
-          fresh = true;
         }
       }
       if (!ok) {
-        give_up();
         // the MMAs issued so far finish before TMEM is freed
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000) {}
       }
-    } else if (warp > kStagers / 32) {
-      const int first = warp - kStagers / 32 - 1;
-      Cursor at = start;
-      for (int i = 0; i < first; ++i) at.next(p.stages);
-      int unit = -1;
-      Unit un{};
-      uint32_t etop[4];
-      bool ok = true;
-      for (int i = first; i < count && ok; i += kTableWarps) {
+    }
+    __syncwarp();
+  } else {
+    const int first = warp - kTableWarp;
+    Cursor at = start;
+    Chain chain;
+    int unit = -1;
+    bool new_chain = true;  // the stage's chain is its piece's first
+    Unit un{};
+    uint32_t etop[4];
+    for (int i = 0; i < count && ok; ++i) {
+      const bool piece_end = i == count - 1 || at.stage == p.stages - 1;
+      const bool chain_end = chain.ends(piece_end);
+      const int flags = (i == 0 || at.stage == 0 ? kNewUnit : 0) | (chain_end ? kChainEnd : 0) |
+                        (new_chain ? kFirstChain : 0);
+      if (i % kTableWarps == first) {
         const int s = i % kTables;
+        int *table = tables + s * kTableInts;
         if (i >= kTables)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(tab_empty + s, (i / kTables - 1) & 1, abort, p.wait_ns));
+          ok = __all_sync(0xffffffffu, mbar_wait_short(tab_empty + s, (i / kTables - 1) & 1, abort,
+                                                       p.wait_ns));
         if (!ok) break;
         if (at.unit != unit) {
           unit = at.unit;
@@ -599,19 +653,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
           for (int k = 0; k < 4; ++k)
             etop[k] = (un.ci0 >> 5) + k < p.cp >> 5 ? __ldg(p.emax + (un.ci0 >> 5) + k) : 0u;
         }
-        make_table<K>(p, static_cast<unsigned>(at.stage) * kPos, un, etop, lane,
-                      tables + s * kTableInts);
+        if (lane == 0) *reinterpret_cast<int2 *>(table) = make_int2(unit, flags);
+        make_table<K, NHWC>(p, static_cast<unsigned>(at.stage) * kPos, un, etop, lane, table);
         __syncwarp();
         if (lane == 0) mbar_arrive(tab_full + s);
-        for (int k = 0; k < kTableWarps; ++k) at.next(p.stages);
       }
-      if (!ok) give_up();
+      at.next(p.stages);
+      if (chain_end) new_chain = piece_end;
     }
-    __syncwarp();
   }
+  if (!ok) {
+    *abort = 1u;
+    atomicCAS(p.err, 0, static_cast<int>(VAE_EDEVICE_TIMEOUT));
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kStagers / 32) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
@@ -758,11 +816,12 @@ __global__ void __launch_bounds__(kScanThreads)
                 min(kSMs, static_cast<int>(gridDim.x * gridDim.y)));
 }
 
-// grid (input-channel tiles + 1, cout): adds a unit's pieces in order, undoes
-// the scaling and writes the taps of 128 input channels, contiguous in dw, through
-// shared memory; the last column of blocks adds up dbias.
+// grid (input-channel tiles + 1, cout), a group of kTM threads per ky: adds a
+// unit's pieces in order, undoes the scaling and writes the taps of 128 input
+// channels, contiguous in dw, through shared memory; the last column of blocks
+// adds up dbias.
 template <int K>
-__global__ void __launch_bounds__(kTM)
+__global__ void __launch_bounds__(K *kTM)
     wgrad_reduce(const WgradParams p, int grid, const float *__restrict__ psum, int slabs,
                  float *__restrict__ dw, float *__restrict__ dbias) {
   __shared__ float out[kTM * K * K];
@@ -777,33 +836,27 @@ __global__ void __launch_bounds__(kTM)
     if (threadIdx.x == 0) dbias[co] = s;
     return;
   }
-  const int ci0 = blockIdx.x * kTM, ci = ci0 + threadIdx.x;
+  const int ky = threadIdx.x / kTM, c = threadIdx.x % kTM;
+  const int ci0 = blockIdx.x * kTM, ci = ci0 + c;
   const int e = ci < p.cin ? static_cast<int>(p.emax[ci >> 5]) - 127 - 7 - dy_exponent(p.amax[co])
                            : 0;
-#pragma unroll 1
-  for (int ky = 0; ky < K; ++ky) {
-    const int u = (static_cast<int>(blockIdx.x) * p.co_tiles + co / kTN) * K + ky;
-    // the SM ranges that hold the unit's first and last stage
-    const long long a = static_cast<long long>(u) * p.stages, b = a + p.stages - 1;
-    const int c0 = static_cast<int>(((a + 1) * grid - 1) / p.total);
-    const int c1 = static_cast<int>(((b + 1) * grid - 1) / p.total);
-    float v[K];
+  const int u = (static_cast<int>(blockIdx.x) * p.co_tiles + co / kTN) * K + ky;
+  const long long a = static_cast<long long>(u) * p.stages;
+  const int c0 = range_of(p.total, grid, a), c1 = range_of(p.total, grid, a + p.stages - 1);
+  const float *src = p.part + static_cast<size_t>(u + c0) * (K * kTN * kTM) + (co % kTN) * kTM + c;
+  float v[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float *src = p.part + static_cast<size_t>(u + c) * (K * kTN * kTM) +
-                         (co % kTN) * kTM + threadIdx.x;
+  for (int k = 0; k < K; ++k) v[k] = 0.f;
+#pragma unroll 8
+  for (int i = c0; i <= c1; ++i, src += K * kTN * kTM)
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += src[k * kTN * kTM];
-    }
+    for (int k = 0; k < K; ++k) v[k] += __ldg(src + k * kTN * kTM);
 #pragma unroll
-    for (int k = 0; k < K; ++k) out[threadIdx.x * (K * K) + ky * K + k] = scalbnf(v[k], e);
-  }
+  for (int k = 0; k < K; ++k) out[c * (K * K) + ky * K + k] = scalbnf(v[k], e);
   __syncthreads();
   const int count = min(kTM, p.cin - ci0) * K * K;
   float *o = dw + (static_cast<size_t>(co) * p.cin + ci0) * (K * K);
-  for (int i = threadIdx.x; i < count; i += kTM) o[i] = out[i];
+  for (int i = threadIdx.x; i < count; i += K * kTM) o[i] = out[i];
 }
 
 int floor_log2(unsigned d) {
@@ -840,12 +893,6 @@ WgradWs carve_wgrad(Carver &cv, int n, int cin, int h, int w, int cout, int k) {
 
 template <int K, bool NHWC, bool WIDE>
 int launch_mma(const WgradParams &p, int grid, cudaStream_t s) {
-  // (the register split waits for what the launch did not bring)
-  static const int regs = [] {
-    cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, wgrad_mma<K, NHWC, WIDE>) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs != kLaunchRegs) return VAE_ECUDA;
   VAE_CUDA_TRY(cudaFuncSetAttribute(wgrad_mma<K, NHWC, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem)));
@@ -918,7 +965,7 @@ int wgrad(const float *dy, CkptView x, int n, int cin, int h, int w, int nhwc, i
   VAE_TRY((k == 3 ? launch_mma<3> : launch_mma<1>)(p, nhwc, wide, ws.grid, s));
   const dim3 rg(ceil_div(cin, kTM) + 1, cout);
   if (k == 3)
-    wgrad_reduce<3><<<rg, kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
+    wgrad_reduce<3><<<rg, 3 * kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
   else
     wgrad_reduce<1><<<rg, kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
   VAE_LAUNCH_CHECK();
