@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 2 : 1)
   constexpr int R = kThreads / T;
   __shared__ float buf[2][kWarps];
   __shared__ float4 red[R > 1 ? kThreads * NV : 1][4];
+  grid_release();
   const int tid = threadIdx.x % T, grp = threadIdx.x / T, cp = (c + 31) & ~31;
   const unsigned row0 = blockIdx.y * tokens, step = gridDim.x * R;
   Oct gn[NV], bn[NV];
@@ -306,17 +307,17 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 2 : 1)
 // Block b: channels [32 b, 32 b + 32); lanes are channels. The 32 warps split
 // the samples (up to 32 at a time) and their slabs; fixed order.
 __global__ void __launch_bounds__(1024)
-    block_norm_merge(const float2 *__restrict__ part, int n, int slabs, int c,
+    block_norm_merge(const float2 *part, int n, int slabs, int c,
                      const float *__restrict__ w_post, const float *__restrict__ gate,
-                     const float *__restrict__ scale, float *__restrict__ dw_post,
-                     float *__restrict__ dgate, float *__restrict__ dscale,
-                     float *__restrict__ dw_pre) {
+                     const float *__restrict__ scale, float *dw_post, float *dgate, float *dscale,
+                     float *dw_pre) {
   __shared__ float2 red[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = 32 * blockIdx.x + lane;
   const float wpo = ch < c ? w_post[ch] : 0.f, sc = scale && ch < c ? scale[ch] : 1.f;
   const int per = 32 / min(n, 32);  // warps of a sample
   float sum_s = 0.f, sum_p = 0.f;   // sum of gate S; sum of dy hh
+  grid_wait();
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + warp / per;
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(1024)
       const float2 *e = part + static_cast<size_t>(i) * slabs * c + ch;
 #pragma unroll 4
       for (int s = warp % per; s < slabs; s += per) {
-        const float2 v = __ldg(e + static_cast<size_t>(s) * c);
+        const float2 v = e[static_cast<size_t>(s) * c];
         t.x += v.x;
         t.y += v.y;
       }
@@ -439,9 +440,8 @@ int block_norm_backward(const BlockNormArgs &a, const float *dy, const float *dh
     VAE_LAUNCH_CHECK();
     return VAE_OK;
   }));
-  block_norm_merge<<<ceil_div(a.c, 32), 1024, 0, s>>>(part, sh.n, slabs, a.c, a.w_post, a.gate,
-                                                      a.scale, dw_post, dgate, dscale, dw_pre);
-  VAE_LAUNCH_CHECK();
+  VAE_CUDA_TRY(launch_after(block_norm_merge, ceil_div(a.c, 32), 1024, 0, s, part, sh.n, slabs,
+                            a.c, a.w_post, a.gate, a.scale, dw_post, dgate, dscale, dw_pre));
   count_launches(2);
   return VAE_OK;
 }

@@ -21,6 +21,33 @@ bool cuda_failed(cudaError_t e, const char *file, int line);
 // After a kernel launch: the launch's own error (configuration, resources).
 #define VAE_LAUNCH_CHECK() VAE_CUDA_TRY(cudaGetLastError())
 
+// Kernels of one operator that follow each other: the later one may start while
+// the earlier runs (launch_after; the earlier one calls grid_release when its
+// blocks may share the SMs, which is at once), and waits in grid_wait for all of
+// it before it reads or writes what the earlier one touches. Pointers to what the
+// earlier one wrote are not __restrict__, or loads could move above the wait.
+// The first kernel of an operator is launched as usual, so the operator's inputs
+// may be read before grid_wait. Saves 1 to 2 us a launch.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         A &&...args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 #define VAE_TRY(expr)                                   \
   do {                                                  \
     int s__ = (expr);                                   \

@@ -54,15 +54,17 @@ __global__ void __launch_bounds__(kStatThreads)
     ckpt_stats_nchw(const float *__restrict__ x, int c, long long spatial, int groups,
                     float *__restrict__ part) {
   __shared__ float red[kStatThreads][3];
+  grid_release();
   stats_segment_nchw(x, c, spatial, groups, gridDim.y, blockIdx.x, blockIdx.y, red, part);
 }
 
 // One block per (sample, group): merges its partials in a fixed order. (Little
 // code: a kernel this short is bound by fetching its instructions.)
 __global__ void __launch_bounds__(kMergeThreads)
-    ckpt_stats_merge(const float *__restrict__ part, int slabs, float eps,
-                     float2 *__restrict__ stats) {
+    ckpt_stats_merge(const float *part, int slabs, float eps, float2 *stats) {
   __shared__ Triple red[kMergeThreads / 32];
+  grid_release();
+  grid_wait();
   const float *e = part + static_cast<size_t>(blockIdx.x) * slabs * 3;
   Triple acc{0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -119,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float *__restrict__ part) {
   __shared__ float2 red[kThreads * 8];
   __shared__ float shift[1024];
+  grid_release();
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
   x += sw.row0 * c;
@@ -239,7 +242,7 @@ __device__ __forceinline__ CkptView from_row(CkptView k, long long row, int cp) 
 template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
     ckpt_apply_nhwc(const float *x, int c, long long spatial, int groups,
-                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                    const float2 *stats, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float *y, CkptView kx, CkptView ky) {
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
@@ -255,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) v[u] = fetch(sw.iters - 1 - u);
+  grid_wait();
   const Affine8 f = load_affine8(sw, c, groups, stats, gamma, beta);
 #pragma unroll 1
   for (int top = sw.iters - 1; top >= 0; top -= D)
@@ -275,10 +279,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 // grid (slabs, cp / 32, n): a thread per pixel and 32 channels.
 __global__ void __launch_bounds__(kPixThreads)
     ckpt_apply_nchw(const float *x, int c, long long spatial, int groups,
-                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
+                    const float2 *stats, const float *__restrict__ gamma,
                     const float *__restrict__ beta, int silu, float *y, CkptView kx,
                     CkptView ky) {
   __shared__ PairAffine aff[16];
+  grid_wait();
   const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31;
   if (threadIdx.x < 16)
     load_pairs(aff, stats + n * groups, gamma, beta, 32 * cb, c, c / groups, threadIdx.x);
@@ -304,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                    const float2 *__restrict__ stats, const float *__restrict__ gamma,
                    const float *__restrict__ beta, float2 *__restrict__ part) {
   __shared__ float2 red[kThreads * 8];
+  grid_release();
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31;
   uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
@@ -369,6 +375,7 @@ __global__ void __launch_bounds__(kPixThreads)
                    const float *__restrict__ beta, int silu, float2 *__restrict__ part) {
   __shared__ PairAffine aff[16];
   __shared__ float2 red[kPixThreads / 32][32];
+  grid_release();
   const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31, cg = c / groups;
   if (threadIdx.x < 16)
     load_pairs(aff, stats + n * groups, gamma, beta, 32 * cb, c, cg, threadIdx.x);
@@ -407,9 +414,10 @@ __global__ void __launch_bounds__(kPixThreads)
 // Block (b, i): channels [32 b, 32 b + 32) of sample i; lanes are channels, warps
 // stride over the slabs; fixed order.
 __global__ void __launch_bounds__(1024)
-    ckpt_sums_merge(const float2 *__restrict__ part, int slabs, int c,
-                    float2 *__restrict__ sums) {
+    ckpt_sums_merge(const float2 *part, int slabs, int c, float2 *sums) {
   __shared__ float2 red[32][32];
+  grid_release();
+  grid_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = 32 * blockIdx.x + lane;
   const float2 *e = part + static_cast<size_t>(blockIdx.y) * slabs * c + ch;
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(1024)
   if (ch < c)
 #pragma unroll 4
     for (int s = warp; s < slabs; s += 32) {
-      const float2 v = __ldg(e + static_cast<size_t>(s) * c);
+      const float2 v = e[static_cast<size_t>(s) * c];
       t.x += v.x;
       t.y += v.y;
     }
@@ -434,9 +442,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 // dbeta and dgamma of channels [first, last): sums over the samples, in order.
-__device__ __forceinline__ void param_grads(const float2 *__restrict__ sums, int n, int c,
-                                            int first, int last, float *__restrict__ dgamma,
-                                            float *__restrict__ dbeta) {
+__device__ __forceinline__ void param_grads(const float2 *sums, int n, int c, int first, int last,
+                                            float *dgamma, float *dbeta) {
   for (int ch = first + threadIdx.x; ch < last; ch += blockDim.x) {
     float2 t = make_float2(0.f, 0.f);
 #pragma unroll 4
@@ -450,16 +457,16 @@ __device__ __forceinline__ void param_grads(const float2 *__restrict__ sums, int
   }
 }
 __global__ void __launch_bounds__(128)
-    ckpt_param_grads(const float2 *__restrict__ sums, int n, int c, float *__restrict__ dgamma,
-                     float *__restrict__ dbeta) {
+    ckpt_param_grads(const float2 *sums, int n, int c, float *dgamma, float *dbeta) {
+  grid_wait();
   const int first = blockIdx.x * blockDim.x;
   param_grads(sums, n, c, first, min(c, first + static_cast<int>(blockDim.x)), dgamma, dbeta);
 }
 
 // k1[g] = rstd mean_g(gamma dz), k2[g] = rstd mean_g(gamma dz xh) of sample n
 // for groups [g0, g1), into shared memory; a warp per group.
-__device__ __forceinline__ void group_means(float2 *km, const float2 *__restrict__ sums, int n,
-                                            int c, int groups, long long spatial,
+__device__ __forceinline__ void group_means(float2 *km, const float2 *sums, int n, int c,
+                                            int groups, long long spatial,
                                             const float2 *__restrict__ stats,
                                             const float *__restrict__ gamma, int g0, int g1) {
   const int cg = c / groups, lane = threadIdx.x & 31;
@@ -489,9 +496,8 @@ template <bool SILU, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
     ckpt_dx_nhwc(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
-                 const float *__restrict__ beta, const float2 *__restrict__ sums,
-                 const float *dres, float *dx, float *__restrict__ dgamma,
-                 float *__restrict__ dbeta) {
+                 const float *__restrict__ beta, const float2 *sums, const float *dres, float *dx,
+                 float *dgamma, float *dbeta) {
   __shared__ float2 km[1024];
   const Sweep sw(c, spatial);
   const int cp = (c + 31) & ~31, cg = c / groups;
@@ -515,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) fetch(sw.iters - 1 - u, u);
+  grid_wait();
   group_means(km, sums, blockIdx.y, c, groups, spatial, stats, gamma, 0, groups);
   if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
     param_grads(sums, gridDim.y, c, 0, c, dgamma, dbeta);
@@ -561,9 +568,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 __global__ void __launch_bounds__(kPixThreads)
     ckpt_dx_nchw(const float *dy, CkptView k, int c, long long spatial, int groups,
                  const float2 *__restrict__ stats, const float *__restrict__ gamma,
-                 const float *__restrict__ beta, int silu, const float2 *__restrict__ sums,
-                 const float *dres, float *dx, float *__restrict__ dgamma,
-                 float *__restrict__ dbeta) {
+                 const float *__restrict__ beta, int silu, const float2 *sums, const float *dres,
+                 float *dx, float *dgamma, float *dbeta) {
   __shared__ PairAffine aff[16];
   __shared__ float2 km[32];
   const int n = blockIdx.z, cb = blockIdx.y, cp = (c + 31) & ~31, cg = c / groups;
@@ -571,6 +577,7 @@ __global__ void __launch_bounds__(kPixThreads)
   if (threadIdx.x < 16)
     load_pairs(aff, stats + n * groups, gamma, beta, 32 * cb, c, cg, threadIdx.x);
   const int g0 = 32 * cb / cg, g1 = (32 * cb + chans - 1) / cg + 1;
+  grid_wait();
   group_means(km, sums, n, c, groups, spatial, stats, gamma, g0, g1);
   if (threadIdx.x < 16) {
     float2 m[2];
@@ -663,17 +670,16 @@ int gn_ckpt(const float *x, int n, int c, long long spatial, int nhwc, int group
     ckpt_stats_nchw<<<dim3(ng, slabs), kStatThreads, 0, s>>>(x, c, spatial, groups, w.part);
   }
   VAE_LAUNCH_CHECK();
-  ckpt_stats_merge<<<ng, kMergeThreads, 0, s>>>(w.part, slabs, eps, st);
-  VAE_LAUNCH_CHECK();
+  VAE_CUDA_TRY(launch_after(ckpt_stats_merge, ng, kMergeThreads, 0, s, w.part, slabs, eps, st));
   if (nhwc)
-    (wide ? (silu ? ckpt_apply_nhwc<true, true> : ckpt_apply_nhwc<false, true>)
-          : (silu ? ckpt_apply_nhwc<true, false> : ckpt_apply_nhwc<false, false>))<<<
-        dim3(slabs, n), kThreads, 0, s>>>(
-        x, c, spatial, groups, st, gamma, beta, y, kx, ky);
+    VAE_CUDA_TRY(launch_after(
+        wide ? (silu ? ckpt_apply_nhwc<true, true> : ckpt_apply_nhwc<false, true>)
+             : (silu ? ckpt_apply_nhwc<true, false> : ckpt_apply_nhwc<false, false>),
+        dim3(slabs, n), kThreads, 0, s, x, c, spatial, groups, st, gamma, beta, y, kx, ky));
   else
-    ckpt_apply_nchw<<<dim3(slabs_nchw(n, c, spatial), ckpt_cp(c) / 32, n), kPixThreads, 0, s>>>(
-        x, c, spatial, groups, st, gamma, beta, silu, y, kx, ky);
-  VAE_LAUNCH_CHECK();
+    VAE_CUDA_TRY(launch_after(ckpt_apply_nchw,
+                              dim3(slabs_nchw(n, c, spatial), ckpt_cp(c) / 32, n), kPixThreads, 0,
+                              s, x, c, spatial, groups, st, gamma, beta, silu, y, kx, ky));
   count_launches(3);
   return VAE_OK;
 }
@@ -690,8 +696,8 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
   const int rc = gn_backward_resident(dy, k, stats, n, c, spatial, nhwc, groups, gamma, beta,
                                       silu, dres, dx, dgamma, dbeta, w.sums, s);
   if (rc == VAE_OK && n > 1 && (dgamma || dbeta)) {
-    ckpt_param_grads<<<ceil_div(c, 128), 128, 0, s>>>(w.sums, n, c, dgamma, dbeta);
-    VAE_LAUNCH_CHECK();
+    VAE_CUDA_TRY(
+        launch_after(ckpt_param_grads, ceil_div(c, 128), 128, 0, s, w.sums, n, c, dgamma, dbeta));
     count_launches(1);
   }
   if (rc != VAE_EUNSUPPORTED) return rc;
@@ -706,18 +712,17 @@ int gn_backward(const float *dy, CkptView k, const float *stats, int n, int c, l
     ckpt_sums_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
                                                 part);
   VAE_LAUNCH_CHECK();
-  ckpt_sums_merge<<<dim3(ckpt_cp(c) / 32, n), 1024, 0, s>>>(part, slabs, c, w.sums);
-  VAE_LAUNCH_CHECK();
+  VAE_CUDA_TRY(launch_after(ckpt_sums_merge, dim3(ckpt_cp(c) / 32, n), 1024, 0, s, part, slabs, c,
+                            w.sums));
   if (nhwc)
-    (wide ? (silu ? ckpt_dx_nhwc<true, true> : ckpt_dx_nhwc<false, true>)
-          : (silu ? ckpt_dx_nhwc<true, false> : ckpt_dx_nhwc<false, false>))<<<grid, kThreads, 0,
-                                                                          s>>>(
-        dy, k, c, spatial, groups, st, gamma, beta, w.sums, dres, dx, dgamma,
-        dbeta);
+    VAE_CUDA_TRY(launch_after(
+        wide ? (silu ? ckpt_dx_nhwc<true, true> : ckpt_dx_nhwc<false, true>)
+             : (silu ? ckpt_dx_nhwc<true, false> : ckpt_dx_nhwc<false, false>),
+        grid, kThreads, 0, s, dy, k, c, spatial, groups, st, gamma, beta, w.sums, dres, dx, dgamma,
+        dbeta));
   else
-    ckpt_dx_nchw<<<grid, kPixThreads, 0, s>>>(dy, k, c, spatial, groups, st, gamma, beta, silu,
-                                              w.sums, dres, dx, dgamma, dbeta);
-  VAE_LAUNCH_CHECK();
+    VAE_CUDA_TRY(launch_after(ckpt_dx_nchw, grid, kPixThreads, 0, s, dy, k, c, spatial, groups, st,
+                              gamma, beta, silu, w.sums, dres, dx, dgamma, dbeta));
   count_launches(3);
   return VAE_OK;
 }

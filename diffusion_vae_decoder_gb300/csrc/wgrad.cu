@@ -314,7 +314,7 @@ struct DyStager {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int co = un.co0 + 8 * co8 + i;
-      f[i] = co < p.cout ? exp2i(dy_exponent(__ldg(p.amax + co))) : 0.f;
+      f[i] = co < p.cout ? exp2i(dy_exponent(p.amax[co])) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) scale[i] = pk2(f[2 * i], f[2 * i + 1]);
@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 1);
   volatile uint32_t *abort = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_release();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStagesA; ++i) {
       mbar_init(a_full + i, kXWarps);
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
   const long long g0 = range_start(p.total, gridDim.x, blockIdx.x);
   const int count = static_cast<int>(range_start(p.total, gridDim.x, blockIdx.x + 1) - g0);
   const Cursor start{static_cast<int>(g0 / p.stages), static_cast<int>(g0 % p.stages)};
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
           un = unit_at(p, unit);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            etop[k] = (un.ci0 >> 5) + k < p.cp >> 5 ? __ldg(p.emax + (un.ci0 >> 5) + k) : 0u;
+            etop[k] = (un.ci0 >> 5) + k < p.cp >> 5 ? p.emax[(un.ci0 >> 5) + k] : 0u;
         }
         if (lane == 0) *reinterpret_cast<int2 *>(table) = make_int2(unit, flags);
         make_table<K, NHWC>(p, static_cast<unsigned>(at.stage) * kPos, un, etop, lane, table);
@@ -677,6 +679,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
 
 // ------------------------------------------------------------- before and after
 constexpr int kScanThreads = 256;
+
+// (Launched before the scan, which may start, and read, while this runs.)
+__global__ void __launch_bounds__(1024) wgrad_zero(unsigned *maxima, int count) {
+  grid_release();
+  for (int i = threadIdx.x; i < count; i += 1024) maxima[i] = 0u;
+}
 
 // Largest scale byte below 255 of each 32-channel block; a share per block. A
 // thread steps over the bytes, as words, in strides of nb words, so that byte k
@@ -724,8 +732,9 @@ __device__ __forceinline__ void scan_scales(const uint8_t *__restrict__ xs, long
 template <bool WIDE>
 __global__ void __launch_bounds__(kScanThreads, 2)
     wgrad_scan_nhwc(const float *__restrict__ dy, long long rows, int cout,
-                    const uint8_t *__restrict__ xs, int nb, float *__restrict__ psum,
-                    unsigned *__restrict__ amax, unsigned *__restrict__ emax) {
+                    const uint8_t *__restrict__ xs, int nb, float *psum, unsigned *amax,
+                    unsigned *emax) {
+  grid_release();
   constexpr int kDepth = 4;  // rows in flight
   __shared__ unsigned sm[128];
   __shared__ float4 rs[2 * kScanThreads], rm[2 * kScanThreads];  // [row of a sweep][channel]
@@ -758,6 +767,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     rm[at + 1] = make_float4(m[4], m[5], m[6], m[7]);
   }
   __syncthreads();
+  grid_wait();
   for (int c = threadIdx.x; c < cols; c += kScanThreads) {
     float sum = 0.f, top = 0.f;
 #pragma unroll 4
@@ -775,11 +785,12 @@ __global__ void __launch_bounds__(kScanThreads, 2)
 // grid (slabs, cout): slab of the n planes of one channel.
 __global__ void __launch_bounds__(kScanThreads)
     wgrad_scan_nchw(const float *__restrict__ dy, int n, long long hw, int cout,
-                    const uint8_t *__restrict__ xs, int nb, float *__restrict__ psum,
-                    unsigned *__restrict__ amax, unsigned *__restrict__ emax) {
+                    const uint8_t *__restrict__ xs, int nb, float *psum, unsigned *amax,
+                    unsigned *emax) {
   __shared__ unsigned sm[128];
   __shared__ float rs[kScanThreads / 32];
   __shared__ unsigned rm[kScanThreads / 32];
+  grid_release();
   const int co = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long p0 = hw * blockIdx.x / gridDim.x, p1 = hw * (blockIdx.x + 1) / gridDim.x;
   float s = 0.f;
@@ -802,6 +813,7 @@ __global__ void __launch_bounds__(kScanThreads)
     rm[warp] = m;
   }
   __syncthreads();
+  grid_wait();
   if (threadIdx.x == 0) {
     for (int k = 1; k < kScanThreads / 32; ++k) {
       s += rs[k];
@@ -822,9 +834,10 @@ __global__ void __launch_bounds__(kScanThreads)
 // adds up dbias.
 template <int K>
 __global__ void __launch_bounds__(K *kTM)
-    wgrad_reduce(const WgradParams p, int grid, const float *__restrict__ psum, int slabs,
-                 float *__restrict__ dw, float *__restrict__ dbias) {
+    wgrad_reduce(const WgradParams p, int grid, const float *psum, int slabs, float *dw,
+                 float *dbias) {
   __shared__ float out[kTM * K * K];
+  grid_wait();
   const int co = blockIdx.y;
   if (blockIdx.x == gridDim.x - 1) {
     if (!dbias || threadIdx.x >= 32) return;
@@ -850,7 +863,7 @@ __global__ void __launch_bounds__(K *kTM)
 #pragma unroll 8
   for (int i = c0; i <= c1; ++i, src += K * kTN * kTM)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __ldg(src + k * kTN * kTM);
+    for (int k = 0; k < K; ++k) v[k] += src[k * kTN * kTM];
 #pragma unroll
   for (int k = 0; k < K; ++k) out[c * (K * K) + ky * K + k] = scalbnf(v[k], e);
   __syncthreads();
@@ -896,8 +909,7 @@ int launch_mma(const WgradParams &p, int grid, cudaStream_t s) {
   VAE_CUDA_TRY(cudaFuncSetAttribute(wgrad_mma<K, NHWC, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem)));
-  wgrad_mma<K, NHWC, WIDE><<<grid, kMmaThreads, kSmem, s>>>(p);
-  VAE_LAUNCH_CHECK();
+  VAE_CUDA_TRY(launch_after(wgrad_mma<K, NHWC, WIDE>, grid, kMmaThreads, kSmem, s, p));
   return VAE_OK;
 }
 
@@ -947,29 +959,26 @@ int wgrad(const float *dy, CkptView x, int n, int cin, int h, int w, int nhwc, i
   p.err = device_error_word();
   if (!p.err) return VAE_ECUDA;
   p.wait_ns = wait_limit_ns();
-  VAE_CUDA_TRY(cudaMemsetAsync(ws.maxima, 0, (cout + nb) * sizeof(unsigned), s));
+  wgrad_zero<<<1, 1024, 0, s>>>(ws.maxima, cout + nb);
+  VAE_LAUNCH_CHECK();
   const bool wide = wide_ok(cout, dy);
   int slabs;
   if (nhwc) {
     const int per = kScanThreads / std::min(128, ceil_div(cout, 8));  // rows of a block's sweep
     slabs = static_cast<int>(std::max(1ll, std::min<long long>(ws.slabs, rows / (4 * per))));
-    (wide ? wgrad_scan_nhwc<true> : wgrad_scan_nhwc<false>)<<<
-        dim3(slabs, ceil_div(cout, 1024)), kScanThreads, 0, s>>>(
-        dy, rows, cout, x.scale, nb, ws.psum, ws.maxima, ws.maxima + cout);
+    VAE_CUDA_TRY(launch_after(wide ? wgrad_scan_nhwc<true> : wgrad_scan_nhwc<false>,
+                              dim3(slabs, ceil_div(cout, 1024)), kScanThreads, 0, s, dy, rows,
+                              cout, x.scale, nb, ws.psum, ws.maxima, ws.maxima + cout));
   } else {
     slabs = std::max(1, std::min(ws.slabs, 8 * kSMs / cout));
-    wgrad_scan_nchw<<<dim3(slabs, cout), kScanThreads, 0, s>>>(
-        dy, n, hw, cout, x.scale, nb, ws.psum, ws.maxima, ws.maxima + cout);
+    VAE_CUDA_TRY(launch_after(wgrad_scan_nchw, dim3(slabs, cout), kScanThreads, 0, s, dy, n, hw,
+                              cout, x.scale, nb, ws.psum, ws.maxima, ws.maxima + cout));
   }
-  VAE_LAUNCH_CHECK();
   VAE_TRY((k == 3 ? launch_mma<3> : launch_mma<1>)(p, nhwc, wide, ws.grid, s));
-  const dim3 rg(ceil_div(cin, kTM) + 1, cout);
-  if (k == 3)
-    wgrad_reduce<3><<<rg, 3 * kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
-  else
-    wgrad_reduce<1><<<rg, kTM, 0, s>>>(p, ws.grid, ws.psum, slabs, dw, dbias);
-  VAE_LAUNCH_CHECK();
-  count_launches(3);
+  VAE_CUDA_TRY(launch_after(k == 3 ? wgrad_reduce<3> : wgrad_reduce<1>,
+                            dim3(ceil_div(cin, kTM) + 1, cout), k * kTM, 0, s, p, ws.grid, ws.psum,
+                            slabs, dw, dbias));
+  count_launches(4);
   return VAE_OK;
 }
 
