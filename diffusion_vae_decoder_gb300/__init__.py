@@ -592,19 +592,12 @@ def _dims(shape, layout):
     return n, c, spatial
 
 
-def _call(name, device, stream, made, *args):
-    """Calls entry point `name` with `args` and the stream, on `device`. `made`:
-    tensors that were allocated here; they stay with a caller's stream that is
-    not the current one until it has used them."""
+def _call(name, device, *args):
+    """Calls entry point `name` with `args` and the current stream of `device`."""
     import torch
     fn = getattr(_lib, name)
     index = device.index
     raw = torch._C._cuda_getCurrentRawStream(index)
-    if stream is not None and stream.cuda_stream != raw:
-        raw = stream.cuda_stream
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, raw)
     else:
@@ -612,6 +605,30 @@ def _call(name, device, stream, made, *args):
             status = fn(*args, raw)
     if status != 0:
         raise VaeError(name, status)
+
+
+def _on(stream, fn, *args):
+    """fn(*args) with `stream` current. The memory it allocates is the stream's, so
+    nothing pending on the caller's current stream still uses it; what it returns
+    is not reused before that stream's work has passed it."""
+    import torch
+    device = next((a.device for a in args if hasattr(a, "device")), stream.device)
+    if device != stream.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    if stream != here:
+        todo = [out]
+        while todo:
+            t = todo.pop()
+            if isinstance(t, (tuple, dict)):
+                todo += t.values() if isinstance(t, dict) else t
+            elif isinstance(t, Checkpoint):
+                todo += (t.payload, t.scale)
+            elif t is not None:
+                t.record_stream(here)
+    return out
 
 
 @functools.lru_cache(maxsize=4096)
@@ -631,19 +648,22 @@ def _workspace(device, name, *args):
 
 def vae_ckpt_pack(x, layout=VAE_NHWC, stream=None):
     """A Checkpoint of the activation ``x`` (any number of spatial axes)."""
+    if stream is not None:
+        return _on(stream, vae_ckpt_pack, x, layout)
     load_library()
     shape, dev = _first(x, "x")
     n, c, spatial = _dims(shape, layout)
     at = _at(x, shape, dev, "x")
     k = Checkpoint._make(n * spatial, c, dev)
-    _call("vae_ckpt_pack", dev, stream, (k._payload, k._scale), at, n, c, spatial, layout,
-          *k._addresses())
+    _call("vae_ckpt_pack", dev, at, n, c, spatial, layout, *k._addresses())
     return k
 
 
 def vae_ckpt_unpack(ckpt, shape, layout=VAE_NHWC, stream=None):
     """The float32 activation of ``shape`` (in ``layout``) that ``ckpt`` holds."""
     import torch
+    if stream is not None:
+        return _on(stream, vae_ckpt_unpack, ckpt, shape, layout)
     load_library()
     if not isinstance(ckpt, Checkpoint):
         raise TypeError("ckpt must be a Checkpoint")
@@ -651,7 +671,7 @@ def vae_ckpt_unpack(ckpt, shape, layout=VAE_NHWC, stream=None):
     dev = ckpt.device
     pq, ps = _ckpt_at(ckpt, n * spatial, c, dev, "ckpt")
     out = torch.empty(shape, dtype=torch.float32, device=dev)
-    _call("vae_ckpt_unpack", dev, stream, (out,), pq, ps, n, c, spatial, layout, out.data_ptr())
+    _call("vae_ckpt_unpack", dev, pq, ps, n, c, spatial, layout, out.data_ptr())
     return out
 
 
@@ -661,6 +681,9 @@ def vae_groupnorm_silu_ckpt(x, gamma, beta, groups=32, eps=1e-6, apply_silu=True
     (y, x_ckpt, y_ckpt, stats), a checkpoint None where keep_x / keep_y is
     false, stats [n, groups, 2] (mean, 1 / sqrt(var + eps))."""
     import torch
+    if stream is not None:
+        return _on(stream, vae_groupnorm_silu_ckpt, x, gamma, beta, groups, eps, apply_silu, layout,
+                   out, keep_x, keep_y)
     load_library()
     shape, dev = _first(x, "x")
     n, c, spatial = _dims(shape, layout)
@@ -671,19 +694,15 @@ def vae_groupnorm_silu_ckpt(x, gamma, beta, groups=32, eps=1e-6, apply_silu=True
     ws, pw, nw = _workspace(dev, "vae_groupnorm_silu_ckpt_workspace_size", n, c, spatial, layout,
                             groups)
     x_ckpt = y_ckpt = pxq = pxs = pyq = pys = None
-    made = [ws, y]
     if keep_x:
         x_ckpt = Checkpoint._make(n * spatial, c, dev)
         pxq, pxs = x_ckpt._addresses()
-        made += (x_ckpt._payload, x_ckpt._scale)
     if keep_y:
         y_ckpt = Checkpoint._make(n * spatial, c, dev)
         pyq, pys = y_ckpt._addresses()
-        made += (y_ckpt._payload, y_ckpt._scale)
     stats = torch.empty((n, max(groups, 1), 2), dtype=torch.float32, device=dev)
-    made.append(stats)
-    _call("vae_groupnorm_silu_ckpt", dev, stream, made, px, n, c, spatial, layout, groups, eps,
-          pg, pb, bool(apply_silu), py, pxq, pxs, pyq, pys, stats.data_ptr(), pw, nw)
+    _call("vae_groupnorm_silu_ckpt", dev, px, n, c, spatial, layout, groups, eps, pg, pb,
+          bool(apply_silu), py, pxq, pxs, pyq, pys, stats.data_ptr(), pw, nw)
     return y, x_ckpt, y_ckpt, stats
 
 
@@ -692,6 +711,9 @@ def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply
     """(dx, dgamma, dbeta) from dy and what vae_groupnorm_silu_ckpt kept; dres, a
     further gradient of x (the resnet skip's), is added to dx."""
     import torch
+    if stream is not None:
+        return _on(stream, vae_groupnorm_silu_backward, dy, x_ckpt, stats, gamma, beta, groups,
+                   apply_silu, layout, dres, out)
     load_library()
     shape, dev = _first(dy, "dy")
     n, c, spatial = _dims(shape, layout)
@@ -706,9 +728,8 @@ def vae_groupnorm_silu_backward(dy, x_ckpt, stats, gamma, beta, groups=32, apply
                             layout, groups)
     dgamma = torch.empty_like(gamma)
     dbeta = torch.empty_like(beta)
-    _call("vae_groupnorm_silu_backward", dev, stream, (ws, dx, dgamma, dbeta), pd, pq, pk, ps, n, c,
-          spatial, layout, groups, pg, pb, bool(apply_silu), pr, px, dgamma.data_ptr(),
-          dbeta.data_ptr(), pw, nw)
+    _call("vae_groupnorm_silu_backward", dev, pd, pq, pk, ps, n, c, spatial, layout, groups, pg,
+          pb, bool(apply_silu), pr, px, dgamma.data_ptr(), dbeta.data_ptr(), pw, nw)
     return dx, dgamma, dbeta
 
 
@@ -716,6 +737,8 @@ def vae_conv2d_wgrad(dy, x_ckpt, k, layout=VAE_NCHW, stream=None):
     """(dw [cout, cin, k, k], dbias [cout]) of vae_conv2d from its output's
     gradient and the checkpoint of its input."""
     import torch
+    if stream is not None:
+        return _on(stream, vae_conv2d_wgrad, dy, x_ckpt, k, layout)
     load_library()
     shape, dev = _first(dy, "dy")
     if len(shape) != 4:
@@ -730,8 +753,8 @@ def vae_conv2d_wgrad(dy, x_ckpt, k, layout=VAE_NCHW, stream=None):
     ws, pw, nw = _workspace(dev, "vae_conv2d_wgrad_workspace_size", n, cin, h, w, layout, cout, k)
     dw = torch.empty((cout, cin, k, k), dtype=torch.float32, device=dev)
     dbias = torch.empty(cout, dtype=torch.float32, device=dev)
-    _call("vae_conv2d_wgrad", dev, stream, (ws, dw, dbias), pd, pq, pk, n, cin, h, w, layout, cout,
-          k, dw.data_ptr(), dbias.data_ptr(), pw, nw)
+    _call("vae_conv2d_wgrad", dev, pd, pq, pk, n, cin, h, w, layout, cout, k, dw.data_ptr(),
+          dbias.data_ptr(), pw, nw)
     return dw, dbias
 
 
@@ -742,6 +765,9 @@ def vae_block_norm(u, x, w_post, gate=None, scale=None, w_pre=None, eps=1e-6, ke
     (h, y, u_ckpt, h_ckpt, rstd); y and h_ckpt are None without w_pre, and the
     last three None with keep=False (serving)."""
     import torch
+    if stream is not None:
+        return _on(stream, vae_block_norm, u, x, w_post, gate, scale, w_pre, eps, keep, out_h,
+                   out_y)
     load_library()
     shape, dev = _first(u, "u")
     if len(shape) != 3:
@@ -759,19 +785,16 @@ def vae_block_norm(u, x, w_post, gate=None, scale=None, w_pre=None, eps=1e-6, ke
     elif out_y is not None:
         raise ValueError("out_y without w_pre")
     u_ckpt = h_ckpt = rstd = puq = pus = phq = phs = pr = None
-    made = [h, y]
     if keep:
         u_ckpt = Checkpoint._make(n * tokens, c, dev)
         puq, pus = u_ckpt._addresses()
         rstd = torch.empty((2, n * tokens), dtype=torch.float32, device=dev)
         pr = rstd.data_ptr()
-        made += (u_ckpt._payload, u_ckpt._scale, rstd)
         if w_pre is not None:
             h_ckpt = Checkpoint._make(n * tokens, c, dev)
             phq, phs = h_ckpt._addresses()
-            made += (h_ckpt._payload, h_ckpt._scale)
-    _call("vae_block_norm", dev, stream, made, pu, px, n, tokens, c, eps, po, pg, ps, pp, ph, py,
-          puq, pus, phq, phs, pr)
+    _call("vae_block_norm", dev, pu, px, n, tokens, c, eps, po, pg, ps, pp, ph, py, puq, pus, phq,
+          phs, pr)
     return h, y, u_ckpt, h_ckpt, rstd
 
 
@@ -781,6 +804,9 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
     dscale, dw_pre (None for an absent input). dy is None without w_pre; dh, the
     gradient that reaches h by the residual stream, may be None."""
     import torch
+    if stream is not None:
+        return _on(stream, vae_block_norm_backward, dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate,
+                   scale, w_pre)
     load_library()
     like, name = (dh, "dh") if dy is None else (dy, "dy")
     if like is None:
@@ -803,9 +829,9 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
     dgate = None if gate is None else torch.empty_like(gate)
     dscale = None if scale is None else torch.empty_like(scale)
     dw_pre = None if w_pre is None else torch.empty_like(w_pre)
-    _call("vae_block_norm_backward", dev, stream, (ws, du, dx, dw_post, dgate, dscale, dw_pre),
-          pdy, pdh, puq, pus, phq, phs, pr, n, tokens, c, po, pg, ps, pp, du.data_ptr(),
-          dx.data_ptr(), dw_post.data_ptr(), _ptr(dgate), _ptr(dscale), _ptr(dw_pre), pw, nw)
+    _call("vae_block_norm_backward", dev, pdy, pdh, puq, pus, phq, phs, pr, n, tokens, c, po, pg,
+          ps, pp, du.data_ptr(), dx.data_ptr(), dw_post.data_ptr(), _ptr(dgate), _ptr(dscale),
+          _ptr(dw_pre), pw, nw)
     return dict(du=du, dx=dx, dw_post=dw_post, dgate=dgate, dscale=dscale, dw_pre=dw_pre)
 
 

@@ -100,7 +100,8 @@ size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long spatial, i
 int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,
                             int groups, float eps, const float *gamma, const float *beta,
                             int apply_silu, float *y, void *x_q, void *x_scale, void *y_q,
-                            void *y_scale, float *stats, void *ws, size_t ws_bytes, vae_stream_t stream) {
+                            void *y_scale, float *stats, void *ws, size_t ws_bytes,
+                            vae_stream_t stream) {
   if (!x || !gamma || !beta || !y || !stats || !pair(x_q, x_scale) || !pair(y_q, y_scale))
     return VAE_EINVAL;
   VAE_TRY(gn_args_ok(n, c, spatial, layout, groups));
@@ -118,9 +119,9 @@ size_t vae_groupnorm_silu_backward_workspace_size(int n, int c, long long spatia
 }
 
 int vae_groupnorm_silu_backward(const float *dy, const void *x_q, const void *x_scale,
-                                const float *stats, int n, int c, long long spatial, int layout, int groups,
-                                const float *gamma, const float *beta, int apply_silu,
-                                const float *dres, float *dx, float *dgamma, float *dbeta,
+                                const float *stats, int n, int c, long long spatial, int layout,
+                                int groups, const float *gamma, const float *beta,
+                                int apply_silu, const float *dres, float *dx, float *dgamma, float *dbeta,
                                 void *ws, size_t ws_bytes, vae_stream_t stream) {
   if (!dy || !x_q || !x_scale || !stats || !gamma || !beta || !dx) return VAE_EINVAL;
   VAE_TRY(gn_args_ok(n, c, spatial, layout, groups));
@@ -142,10 +143,10 @@ size_t vae_conv2d_wgrad_workspace_size(int n, int cin, int h, int w, int layout,
 int vae_conv2d_wgrad(const float *dy, const void *x_q, const void *x_scale, int n, int cin, int h,
                      int w, int layout, int cout, int k, float *dw, float *dbias, void *ws,
                      size_t ws_bytes, vae_stream_t stream) {
-  if (!dy || !x_q || !x_scale || !dw || !ws) return VAE_EINVAL;
+  if (!dy || !x_q || !x_scale || !dw) return VAE_EINVAL;
   VAE_TRY(wgrad_args_ok(n, cin, h, w, layout, cout, k));
   if (!all_aligned(dy, x_q, x_scale, ws)) return VAE_EINVAL;
-  if (ws_bytes < wgrad_ws_bytes(n, cin, h, w, cout, k)) return VAE_EWORKSPACE;
+  VAE_TRY(workspace_ok(ws, ws_bytes, wgrad_ws_bytes(n, cin, h, w, cout, k)));
   return wgrad(dy, ckpt_view(x_q, x_scale), n, cin, h, w, layout == VAE_NHWC, cout, k, dw,
                dbias, ws, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -184,7 +185,7 @@ int vae_block_norm_backward(const float *dy, const float *dh, const void *u_q,
                             const float *w_pre, float *du, float *dx, float *dw_post,
                             float *dgate, float *dscale, float *dw_pre, void *ws, size_t ws_bytes,
                             vae_stream_t stream) {
-  if (!u_q || !u_scale || !rstd || !w_post || !du || !dx || !ws || !pair(h_q, h_scale))
+  if (!u_q || !u_scale || !rstd || !w_post || !du || !dx || !pair(h_q, h_scale))
     return VAE_EINVAL;
   if ((w_pre != nullptr) != (dy != nullptr) || (w_pre != nullptr) != (h_q != nullptr))
     return VAE_EINVAL;
@@ -194,7 +195,7 @@ int vae_block_norm_backward(const float *dy, const float *dh, const void *u_q,
   if (!all_aligned(dy, dh, u_q, u_scale, h_q, h_scale, w_post, gate, scale, w_pre, du, dx, ws))
     return VAE_EINVAL;
   const BlockNormArgs a{n, tokens, c, w_post, gate, scale, w_pre};
-  if (ws_bytes < block_norm_backward_ws_bytes(a)) return VAE_EWORKSPACE;
+  VAE_TRY(workspace_ok(ws, ws_bytes, block_norm_backward_ws_bytes(a)));
   return block_norm_backward(a, dy, dh, ckpt_view(u_q, u_scale),
                              ckpt_view(h_q, h_scale), rstd, du, dx, dw_post, dgate,
                              dscale, dw_pre, ws, reinterpret_cast<cudaStream_t>(stream));

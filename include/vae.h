@@ -468,7 +468,8 @@ VAE_API size_t vae_groupnorm_silu_ckpt_workspace_size(int n, int c, long long sp
 VAE_API int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spatial, int layout,
                                     int groups, float eps, const float *gamma, const float *beta,
                                     int apply_silu, float *y, void *x_q, void *x_scale,
-                                    void *y_q, void *y_scale, float *stats, void *ws, size_t ws_bytes, vae_stream_t stream);
+                                    void *y_q, void *y_scale, float *stats, void *ws,
+                                    size_t ws_bytes, vae_stream_t stream);
 
 /* vae_groupnorm_silu_backward -- with x~ the checkpoint's values, xh =
  * (x~ - mean) * rstd (stats as saved), z = xh * gamma + beta, and dz = dy *
@@ -479,7 +480,8 @@ VAE_API int vae_groupnorm_silu_ckpt(const float *x, int n, int c, long long spat
  *   dy, dx, dres [n,c,spatial] (layout); dres (a gradient that reaches x by
  *   another way, the resnet skip) may be NULL; dgamma, dbeta [c] or NULL.
  *   dx == dy and dx == dres are allowed.
- * Sums have a fixed order: the same inputs give the same bits. */
+ * Limits of vae_groupnorm_silu_ckpt. Sums have a fixed order: the same inputs
+ * give the same bits. */
 VAE_API size_t vae_groupnorm_silu_backward_workspace_size(int n, int c, long long spatial,
                                                           int layout, int groups);
 VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_q,
@@ -508,8 +510,8 @@ VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_q,
 VAE_API size_t vae_conv2d_wgrad_workspace_size(int n, int cin, int h, int w, int layout, int cout,
                                                int k);
 VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_q, const void *x_scale, int n,
-                             int cin, int h, int w, int layout, int cout, int k, float *dw, float *dbias, void *ws,
-                             size_t ws_bytes, vae_stream_t stream);
+                             int cin, int h, int w, int layout, int cout, int k, float *dw,
+                             float *dbias, void *ws, size_t ws_bytes, vae_stream_t stream);
 
 /* vae_block_norm -- the norms after a transformer block and before the next
  * one, fused with the block's gate, residual scale and residual sum, on
@@ -519,8 +521,8 @@ VAE_API int vae_conv2d_wgrad(const float *dy, const void *x_q, const void *x_sca
  *   all tokens of a sample). gate and scale may be NULL (ones); w_pre and y are
  *   both NULL where no norm follows. h == x and y == u are allowed.
  * For a backward pass, checkpoints of u and of h (h_q NULL exactly when w_pre
- * is) and rstd [2][n * tokens]: 1 / rms(u), then 1 / rms(h) (that
- * half unused without w_pre). All NULL otherwise (serving).
+ * is) and rstd [2][n * tokens]: 1 / rms(u), then 1 / rms(h) (that half unused
+ * without w_pre). All NULL otherwise (serving).
  * vae_block_norm_backward -- from dy (NULL exactly when w_pre is) and dh, the
  * gradient that reaches h by the residual stream (may be NULL): du, dx, and,
  * each where not NULL, dw_post, dscale, dw_pre [c] and dgate [n][c]. Asking for

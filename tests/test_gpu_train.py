@@ -521,12 +521,13 @@ def test_block_norm_backward(n, t, c, gate, scale, pre):
 
 
 # ---------------------------------------------------------------- streams, graphs, memory
-def all_ops():
-    """One call of each operator on fixed inputs; returns its tensors."""
+def all_ops(n=2, h=24, w=20, c=64):
+    """One call of each operator on fixed inputs; returns its tensors. The default
+    GroupNorms are one launch each, those of the second of `SIZES` three."""
     p = pkg()
     g = torch.Generator(device="cuda").manual_seed(18)
     f = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
-    x, dy, ga, be = f(2, 24, 20, 64), f(2, 24, 20, 64), f(64), f(64)
+    x, dy, ga, be = f(n, h, w, c), f(n, h, w, c), f(c), f(c)
     u, v, wpo, wpr, sc, gate = f(2, 50, 128), f(2, 50, 128), f(128), f(128), f(128), f(2, 128)
     torch.cuda.synchronize()
 
@@ -545,12 +546,16 @@ def all_ops():
     return run
 
 
+SIZES = [(2, 24, 20, 64), (1, 150, 160, 64)]
+
+
 def same(a, b):
     return all(torch.equal(p, q) for p, q in zip(a, b))
 
 
-def test_ops_on_another_stream():
-    run = all_ops()
+@pytest.mark.parametrize("size", SIZES)
+def test_ops_on_another_stream(size):
+    run = all_ops(*size)
     want = run()
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
@@ -561,6 +566,80 @@ def test_ops_on_another_stream():
         got = run()
     side.synchronize()
     assert same(want, got)
+
+
+def test_a_streams_results_are_not_in_memory_that_another_stream_still_writes():
+    p = pkg()
+    u = torch.randn(1, 4096, 512, device="cuda")
+    w, side = torch.ones(512, device="cuda"), torch.cuda.Stream()
+    want = p.vae_block_norm(u, u, w, keep=False)[0]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        late = torch.empty_like(u)
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+        late.fill_(SENTINEL)
+        del late  # free for the current stream, which has yet to write it
+        got = p.vae_block_norm(u, u, w, keep=False, stream=side)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del got
+
+
+def test_a_result_freed_early_stays_until_the_callers_stream_has_read_it():
+    p = pkg()
+    u = torch.randn(1, 4096, 512, device="cuda")
+    w, side = torch.ones(512, device="cuda"), torch.cuda.Stream()
+    want = p.vae_block_norm(u, u, w, keep=False)[0]
+    torch.cuda.synchronize()
+    got = p.vae_block_norm(u, u, w, keep=False, stream=side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    read = got.clone()
+    del got
+    for _ in range(3):
+        p.vae_block_norm(u, 2 * u, w, keep=False, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(read, want)
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_calls_of_two_threads_on_one_stream(size):
+    import threading
+    runs = [all_ops(*size), all_ops(1, 9, 7, 32)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(6):
+            got[i].append(runs[i]())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(len(g) == 6 and all(same(w, r) for r in g) for w, g in zip(want, got))
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_two_graphs_replayed_at_once(size):
+    run = all_ops(*size)
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(run())
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(same(want, o) for o in outs)
 
 
 def test_two_runs_at_once():
@@ -576,8 +655,9 @@ def test_two_runs_at_once():
     assert all(same(want, r) for g in got for r in g)
 
 
-def test_captured_and_replayed():
-    run = all_ops()
+@pytest.mark.parametrize("size", SIZES)
+def test_captured_and_replayed(size):
+    run = all_ops(*size)
     want = [t.clone() for t in run()]
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -591,6 +671,117 @@ def test_captured_and_replayed():
     assert same(want, got)
 
 
+def shifted(t):
+    """A copy that starts 16 bytes behind a 32-byte boundary."""
+    buf = torch.empty(t.numel() + 16, device="cuda")
+    first = (4 - buf.data_ptr() // 4) % 8
+    out = buf[first:first + t.numel()].view(t.shape)
+    assert out.data_ptr() % 32 == 16
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_tensors_on_16_byte_boundaries(size):
+    """256-bit accesses are taken on 32-byte boundaries only; elsewhere two of 128
+    bits bring the same numbers in the same order."""
+    p = pkg()
+    n, h, w, c = size
+    g = torch.Generator(device="cuda").manual_seed(23)
+    f = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dy, ga, be = f(n, h, w, c), f(n, h, w, c), f(c), f(c)
+    a = p.vae_groupnorm_silu_ckpt(x, ga, be, layout=1)
+    b = p.vae_groupnorm_silu_ckpt(shifted(x), shifted(ga), shifted(be), layout=1,
+                                  out=shifted(x))
+    bits = lambda k: [k.payload.view(torch.uint8), k.scale.view(torch.uint8)]  # noqa: E731
+    assert same([a[0], a[3], *bits(a[1]), *bits(a[2])], [b[0], b[3], *bits(b[1]), *bits(b[2])])
+    a2 = p.vae_groupnorm_silu_backward(dy, a[1], a[3], ga, be, layout=1, dres=x)
+    b2 = p.vae_groupnorm_silu_backward(shifted(dy), b[1], shifted(b[3]), ga, be, layout=1,
+                                       dres=shifted(x), out=shifted(dy))
+    assert same(a2, b2)
+    for k in (1, 3):
+        assert same(p.vae_conv2d_wgrad(dy, a[2], k, layout=1),
+                    p.vae_conv2d_wgrad(shifted(dy), b[2], k, layout=1))
+    u, v = x.view(n, h * w, c), dy.view(n, h * w, c)
+    a = p.vae_block_norm(u, v, ga, w_pre=be)
+    b = p.vae_block_norm(shifted(u), shifted(v), shifted(ga), w_pre=shifted(be),
+                         out_h=shifted(u), out_y=shifted(u))
+    assert same([a[0], a[1], a[4], *bits(a[2]), *bits(a[3])],
+                [b[0], b[1], b[4], *bits(b[2]), *bits(b[3])])
+    a2 = p.vae_block_norm_backward(v, u, a[2], a[3], a[4], ga, w_pre=be)
+    b2 = p.vae_block_norm_backward(shifted(v), shifted(u), b[2], b[3], b[4], ga, w_pre=be)
+    assert all(a2[k] is b2[k] or torch.equal(a2[k], b2[k]) for k in a2)
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+def test_block_norm_and_checkpoints_past_2_to_32_elements():
+    """Rows are independent: the last ones are what a call on them alone gives."""
+    p = pkg()
+    t, c, tail = (1 << 20) + 37, 4096, 64
+    u = torch.empty(1, t, c, device="cuda").uniform_(-1, 1)
+    w, wp = torch.full((c,), 0.5, device="cuda"), torch.full((c,), 2.0, device="cuda")
+    end = u[:, -tail:].contiguous()
+    want = p.vae_block_norm(end, end, w, w_pre=wp)
+    got = p.vae_block_norm(u, u, w, w_pre=wp)
+    bits = lambda k: [k.payload.view(torch.uint8), k.scale.view(torch.uint8)]  # noqa: E731
+    last = lambda ts, axis: [v.narrow(axis, v.shape[axis] - tail, tail) for v in ts]  # noqa: E731
+    assert same(want[:2], last(got[:2], 1))
+    assert same([*bits(want[2]), *bits(want[3])], last([*bits(got[2]), *bits(got[3])], 0))
+    grads = p.vae_block_norm_backward(u, u, *got[2:], w, w_pre=wp)
+    alone = p.vae_block_norm_backward(end, end, *want[2:], w, w_pre=wp)
+    assert same([alone["du"], alone["dx"]], last([grads["du"], grads["dx"]], 1))
+    del got, grads
+    k = p.vae_ckpt_pack(u, layout=1)
+    assert same(bits(p.vae_ckpt_pack(end, layout=1)), last(bits(k), 0))
+    back = p.vae_ckpt_unpack(k, u.shape, layout=1)
+    assert same([p.vae_ckpt_unpack(p.vae_ckpt_pack(end, layout=1), end.shape, layout=1)],
+                last([back], 1))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_groupnorm_pair_past_2_to_32_elements(layout):
+    """Two samples of over 2^31 numbers; the second's results against the call on it
+    alone, which cuts its sums differently. A thread adds up under 2^13 numbers in a
+    row, so sums are off by 2^-11 of their terms' sizes: deviations up to 2 and
+    squares up to 4 (mean 2^-10, variance 2^-7, rstd = 1.73 2^-6, y 2^-5; both calls:
+    twice that). dx, of size up to 3, has four such terms. A wrong offset gives
+    differences of the order of the values."""
+    p = pkg()
+    c, spatial = 256, (1 << 23) + 40
+    shape = (2, spatial, c) if layout == 1 else (2, c, spatial)
+    x = torch.empty(shape, device="cuda").uniform_(-1, 1)
+    ga, be = torch.full((c,), 1.5, device="cuda"), torch.full((c,), 0.5, device="cuda")
+    y, kx, ky, st = p.vae_groupnorm_silu_ckpt(x, ga, be, layout=layout)
+    one = x[1:].contiguous()
+    y1, kx1, ky1, st1 = p.vae_groupnorm_silu_ckpt(one, ga, be, layout=layout)
+    bits = lambda k: [k.payload.view(torch.uint8), k.scale.view(torch.uint8)]  # noqa: E731
+    assert all(torch.equal(a[spatial:], b) for a, b in zip(bits(kx), bits(kx1)))
+    assert float((st[1] - st1[0]).abs().max()) <= 2.0 ** -5
+    assert float((y[1] - y1[0]).abs().max()) <= 2.0 ** -4
+    del y, y1, ky, ky1, one
+    dx, dga, dbe = p.vae_groupnorm_silu_backward(x, kx, st, ga, be, layout=layout)
+    dx1, _, _ = p.vae_groupnorm_silu_backward(x[1:].contiguous(), kx1, st1, ga, be, layout=layout)
+    assert float((dx[1] - dx1[0]).abs().max()) <= 2.0 ** -2
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_wgrad_past_2_to_32_elements(layout):
+    """Small integers, whose sums stay below 2^24, are exact whatever their order:
+    the whole is the sum of its samples."""
+    p = pkg()
+    n, h, w, cin, cout = 2, 2048, 2056, 512, 512  # 2^32 + bytes of payload, numbers of dy
+    g = torch.Generator(device="cuda").manual_seed(24)
+    shape = (n, h, w, cout) if layout == 1 else (n, cout, h, w)
+    dy = torch.randint(-1, 2, shape, generator=g, device="cuda", dtype=torch.int8).float()
+    x = torch.randint(-1, 2, (n, h * w, cin), generator=g, device="cuda", dtype=torch.int8).float()
+    dw, db = p.vae_conv2d_wgrad(dy, p.vae_ckpt_pack(x, layout=1), 1, layout=layout)
+    parts_ = [p.vae_conv2d_wgrad(dy[i:i + 1].contiguous(),
+                                 p.vae_ckpt_pack(x[i:i + 1].contiguous(), layout=1), 1,
+                                 layout=layout) for i in range(n)]
+    assert torch.equal(dw, parts_[0][0] + parts_[1][0])
+    assert torch.equal(db, parts_[0][1] + parts_[1][1])
+
+
+# ---------------------------------------------------------------- memory
 def test_nothing_is_written_behind_the_outputs():
     """Outputs inside larger buffers, through the C ABI: what lies behind stays."""
     p, lib = pkg(), pkg().load_library()
