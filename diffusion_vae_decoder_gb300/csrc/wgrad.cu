@@ -546,12 +546,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) wgrad_mma(const WgradParams p)
       DyStager<K, NHWC, WIDE> st(p, threadIdx.x - 32 * kXWarps);
       const uint32_t base = smem_u32(smem);
       st.set_load_unit(unit_at(p, start.unit));
+      st.set_unit(unit_at(p, start.unit));
       ok = wait(tab_full, 0);
       if (ok)
 #pragma unroll
-        for (int j = 0; j < st.kCount; ++j) 
+        for (int j = 0; j < st.kCount; ++j)
           st.load_slot(st.raw[j], st.first + st.kStep * j, tables, 0);
-      st.set_unit(unit_at(p, start.unit));
 #pragma unroll 1
       for (int i = 0; i < count && ok; ++i) {
         const int *table = tables + (i % kTables) * kTableInts;
