@@ -4,13 +4,15 @@
 //
 // A slab is the smallest run of channels made of whole groups and whole
 // 32-channel checkpoint blocks (lcm(32, c / groups); every channel when c is
-// not a multiple of 32). A cluster of up to 16 blocks splits its pixels, keeps
+// not a multiple of 32). A cluster of up to 8 blocks splits its pixels, keeps
 // them in shared memory, reduces, exchanges the partial sums of the blocks
 // through distributed shared memory (every block adds them in rank order, so
 // all get the same bits) and writes the results: each tensor moves once, and
 // the three launches with two passes over HBM of gn_train.cu become one. These
-// are the launch-bound sizes: at [1, 512, 64, 64] NHWC the forward takes one
-// launch instead of 9.1 + 5.1 + 10.9 us of kernels.
+// are the launch-bound sizes: at [1, 512, 64, 64] NHWC the forward takes 13.0 us
+// instead of 14.9, the backward 11.8 instead of 18.1, and a call in a loop 23
+// and 16 instead of 32 and 26; what bounds it is one block's chain of launch,
+// load, two cluster barriers and store.
 #include "gn_train.cuh"
 #include "ptx.cuh"
 
@@ -20,7 +22,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr size_t kMaxSmem = 227 * 1024 - 1024;
+constexpr size_t kMaxHeld = 64 * 1024;  // of a block's pixels
+constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
@@ -420,15 +423,15 @@ __device__ __forceinline__ void finish_sums(const ResArgs &a, const float2 *mine
   for (int ch = threadIdx.x; ch < chans; ch += kThreads) {
     float2 t = make_float2(0.f, 0.f);
     if (nctas > 1) {
-      float2 part[16];
+      float2 part[kMaxCluster];
 #pragma unroll
-      for (uint32_t r = 0; r < 16; ++r)
+      for (uint32_t r = 0; r < kMaxCluster; ++r)
         if (r < nctas) {
           const uint32_t src = mapa_rank(mine + ch, r);
           part[r] = make_float2(ld_cluster(src), ld_cluster(src + 4));
         }
 #pragma unroll
-      for (uint32_t r = 0; r < 16; ++r)
+      for (uint32_t r = 0; r < kMaxCluster; ++r)
         if (r < nctas) {
           t.x += part[r].x;
           t.y += part[r].y;
@@ -659,23 +662,40 @@ size_t fixed_bytes(int slab, bool nhwc, bool backward) {
   return (head_floats(slab) + red) * sizeof(float);
 }
 
-// Blocks of a cluster: as few as fit, up to 8 until the launch has a block per
-// SM or a block under 256 (NHWC) or 128 pixels; 16 (not portable) only to fit. 0: no fit.
-int cluster_blocks(int n, int c, long long spatial, int slab, size_t fixed, int *per,
-                   size_t *smem, bool nhwc) {
+constexpr size_t kMaxSmem =
+    kMaxHeld + (head_floats(1024) + std::max(kRedFloats, pair_floats(1024) + kWarps * 32 * 2)) * 4;
+static_assert(kMaxSmem <= 227 * 1024, "the widest slab (c <= 1024) fits an SM");
+
+// Blocks of a cluster; 0: the three launches of gn_train.cu. As few blocks as
+// hold the pixels, up to 8 until the launch has a block per SM or a block under 256
+// (NHWC) or 128 pixels.
+//
+// A block takes about 8 us and 0.7 (forward; backward 0.5) per 1024 numbers that it
+// holds, three launches 8 to 14 us in all, but 10 us more of the host's time when
+// they are called one by one. Measured, GPU (calls in a loop), us:
+//   numbers a block          one launch           three launches
+//   4096  (1, 64, 1024)      10.3 (23)  7.6 (16)  8.2 (33)  12.1 (26)  NCHW
+//   16384 (1, 256, 4096)     10.2 (24)  9.4 (17)  11.7 (34) 14.4 (27)  NHWC
+//   16384 (1, 256, 4096)     15.3 (23)  12.6 (17) 10.3 (33) 12.5 (27)  NCHW
+//   23500 (2, 96, 1961)                 21.0 (27)           12.2 (26)  NCHW
+//   49152 (1, 96, 4096)      41.3 (43)  33.3 (35) 8.7 (33)  12.5 (26)  NCHW
+//   twice 16384 (4, 512, 4096) 72 (73)  58 (60)   30 (33)   54 (58)    NCHW
+// so one launch up to 16384 numbers, counting the rounds that the SMs take.
+int cluster_blocks(int n, int c, long long spatial, int slab, int *per, size_t *bytes,
+                   bool nhwc) {
   const int pieces = n * ((c + slab - 1) / slab);
   const int ppi = kThreads / (slab / 8);
-  for (int cl = 1; cl <= 16; cl *= 2) {
+  for (int cl = 1; cl <= kMaxCluster; cl *= 2) {
     const long long pp = (spatial + cl - 1) / cl;
     if (pp > 65536) continue;
     // NHWC: slots of one pixel per pixel lane; NCHW: rows of pixels rounded up to 32
-    const size_t bytes = nhwc ? static_cast<size_t>((pp + ppi - 1) / ppi) * kThreads * 32
-                              : static_cast<size_t>((pp + 31) / 32 * 32) * slab * 4;
-    const size_t total = fixed + bytes;
-    if (total > kMaxSmem) continue;
-    if (cl < 8 && static_cast<long long>(pieces) * cl < 152 && pp >= (nhwc ? 256 : 128)) continue;
+    const size_t held = nhwc ? static_cast<size_t>((pp + ppi - 1) / ppi) * kThreads * 32
+                             : static_cast<size_t>((pp + 31) / 32 * 32) * slab * 4;
+    const long long blocks = static_cast<long long>(pieces) * cl, rounds = (blocks + 255) / 256;
+    if (held * rounds > kMaxHeld) continue;
+    if (cl < kMaxCluster && blocks < 152 && pp >= (nhwc ? 256 : 128)) continue;
     *per = static_cast<int>(pp);
-    *smem = total;
+    *bytes = held;
     return cl;
   }
   return 0;
@@ -686,8 +706,6 @@ int launch(Kernel kernel, const ResArgs &a, int cl, int n, size_t smem, cudaStre
   if (smem > 48 * 1024)
     VAE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(kMaxSmem)));
-  if (cl > 8)
-    VAE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   if (cl == 1) {  // (a launch with a cluster attribute costs the host more)
     kernel<<<dim3(1, (a.c + a.slab - 1) / a.slab, n), kThreads, smem, s>>>(a);
     VAE_LAUNCH_CHECK();
@@ -705,13 +723,6 @@ int launch(Kernel kernel, const ResArgs &a, int cl, int n, size_t smem, cudaStre
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cl > 8) {  // a cluster of 16 needs 16 SMs of one partition
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
-      (void)cudaGetLastError();
-      return VAE_EUNSUPPORTED;
-    }
-  }
   VAE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a));
   VAE_LAUNCH_CHECK();
   count_launches(1);
@@ -720,13 +731,10 @@ int launch(Kernel kernel, const ResArgs &a, int cl, int n, size_t smem, cudaStre
 
 }  // namespace
 
-bool gn_resident_surely(int n, int c, long long spatial, int nhwc, int groups, bool backward) {
-  const int slab = slab_channels(c, groups);
+bool gn_resident(int n, int c, long long spatial, int nhwc, int groups) {
   int per = 0;
-  size_t smem = 0;
-  const int cl = cluster_blocks(n, c, spatial, slab, fixed_bytes(slab, nhwc, backward), &per,
-                                &smem, nhwc);
-  return cl > 0 && cl <= 8;
+  size_t held = 0;
+  return cluster_blocks(n, c, spatial, slab_channels(c, groups), &per, &held, nhwc) > 0;
 }
 
 int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, int groups,
@@ -734,10 +742,10 @@ int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, 
                      CkptView kx, CkptView ky, float *stats, cudaStream_t s) {
   ResArgs a{};
   a.slab = slab_channels(c, groups);
-  const size_t fixed = fixed_bytes(a.slab, nhwc, false);
-  size_t smem = 0;
-  const int cl = cluster_blocks(n, c, spatial, a.slab, fixed, &a.per, &smem, nhwc);
+  size_t held = 0;
+  const int cl = cluster_blocks(n, c, spatial, a.slab, &a.per, &held, nhwc);
   if (!cl) return VAE_EUNSUPPORTED;
+  const size_t smem = fixed_bytes(a.slab, nhwc, false) + held;
   a.x = x;
   a.kx = kx;
   a.ky = ky;
@@ -763,10 +771,10 @@ int gn_backward_resident(const float *dy, CkptView kx, const float *stats, int n
                          float *dgamma, float *dbeta, float2 *sums, cudaStream_t s) {
   ResArgs a{};
   a.slab = slab_channels(c, groups);
-  const size_t fixed = fixed_bytes(a.slab, nhwc, true);
-  size_t smem = 0;
-  const int cl = cluster_blocks(n, c, spatial, a.slab, fixed, &a.per, &smem, nhwc);
+  size_t held = 0;
+  const int cl = cluster_blocks(n, c, spatial, a.slab, &a.per, &held, nhwc);
   if (!cl) return VAE_EUNSUPPORTED;
+  const size_t smem = fixed_bytes(a.slab, nhwc, true) + held;
   a.x = dy;
   a.kx = kx;
   a.c = c;

@@ -24,10 +24,9 @@ int gn_backward(const float *dy, CkptView x_ckpt, const float *stats, int n, int
 
 // The same in one launch of thread-block clusters that hold a (sample, channel
 // slab) on chip between the reduction and the elementwise pass
-// (gn_resident.cu); VAE_EUNSUPPORTED, with nothing launched, for slabs that do
-// not fit.
-// Whether that is certain for these sizes (clusters of at most 8 blocks).
-bool gn_resident_surely(int n, int c, long long spatial, int nhwc, int groups, bool backward);
+// (gn_resident.cu); VAE_EUNSUPPORTED, with nothing launched, for sizes that
+// gn_resident does not take.
+bool gn_resident(int n, int c, long long spatial, int nhwc, int groups);
 int gn_ckpt_resident(const float *x, int n, int c, long long spatial, int nhwc, int groups,
                      float eps, const float *gamma, const float *beta, int silu, float *y,
                      CkptView x_ckpt, CkptView y_ckpt, float *stats, cudaStream_t s);

@@ -41,8 +41,10 @@
 // clocks to issue one, the tensor core 64 to run it.
 //
 // Bound: the tensor core (24 MMAs of 64 clocks a stage), then what the staging
-// warps and barriers add. 128 to 128 channels at 512^2: 114 us, 12300 stages of
-// 128 positions on 150 SMs, 65 us of them the MMAs' (154 GFLOP; 1.36 PFLOP/s).
+// warps and barriers add (dy's loop takes 2300 clocks a stage; a chain's end 3700,
+// for 768 reductions of 128 bytes). 128 to 128 channels at 512^2: 113 us, 12300
+// stages of 128 positions on 150 SMs, 65 us of them the MMAs' (154 GFLOP; 1.36
+// PFLOP/s); with the scan (25 us) and the reduction 145 us.
 // Measured on the way at this size: one issuing thread 142 us, sums in registers
 // with the spills of prefetched data that they bring 187 us, 128-bit loads of dy
 // (each sector twice) 40 us more; sixteen warps for x~ at 64 registers 179 us,
