@@ -20,7 +20,7 @@
 // 18.06 backward. HBM bounds both, launch latency a single token. Column sums run
 // in registers over the rows of a block and meet in a fixed order. Measured:
 // forward 16384 x 512 with checkpoints 25.9 us (5.9 TB/s), one token 2.7 us;
-// backward 4 x 4096 x 1024 54 us, 45 of it the rows (6.6 TB/s), 1024 x 512 8.1 us.
+// backward 4 x 4096 x 1024 53 us, 45 of it the rows (6.7 TB/s), 1024 x 512 8.0 us.
 #include <type_traits>
 
 #include "block_norm.cuh"
@@ -307,7 +307,9 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 2 : 1)
 }
 
 // Block b: channels [32 b, 32 b + 32); lanes are channels. The 32 warps split
-// the samples (up to 32 at a time) and their slabs; fixed order.
+// the samples (up to 32 at a time) and their slabs; fixed order. (Eight loads in
+// flight: four take 1.3 us longer for 4 x 76 slabs, ten and more keep fetching
+// instructions, 2.7 us longer.)
 __global__ void __launch_bounds__(1024)
     block_norm_merge(const float2 *part, int n, int slabs, int c,
                      const float *__restrict__ w_post, const float *__restrict__ gate,
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(1024)
     float2 t = make_float2(0.f, 0.f);
     if (ch < c && i < min(n, i0 + 32)) {
       const float2 *e = part + static_cast<size_t>(i) * slabs * c + ch;
-#pragma unroll 4
+#pragma unroll 8
       for (int s = warp % per; s < slabs; s += per) {
         const float2 v = e[static_cast<size_t>(s) * c];
         t.x += v.x;

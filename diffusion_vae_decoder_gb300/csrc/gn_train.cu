@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(1024)
   const float2 *e = part + static_cast<size_t>(blockIdx.y) * slabs * c + ch;
   float2 t = make_float2(0.f, 0.f);
   if (ch < c)
-#pragma unroll 4
+#pragma unroll 8
     for (int s = warp; s < slabs; s += 32) {
       const float2 v = e[static_cast<size_t>(s) * c];
       t.x += v.x;
