@@ -9,9 +9,9 @@
 // through distributed shared memory (every block adds them in rank order, so
 // all get the same bits) and writes the results: each tensor moves once, and
 // the three launches with two passes over HBM of gn_train.cu become one. These
-// are the launch-bound sizes: at [1, 512, 64, 64] NHWC the forward takes 13.0 us
-// instead of 14.9, the backward 11.8 instead of 18.1, and a call in a loop 23
-// and 16 instead of 32 and 26; what bounds it is one block's chain of launch,
+// are the launch-bound sizes: at [1, 512, 64, 64] NHWC the forward takes 13 to 14
+// us instead of 15, the backward 12 instead of 18, and a call in a loop 23 and 16
+// instead of 32 and 26; what bounds it is one block's chain of launch,
 // load, two cluster barriers and store.
 #include "gn_train.cuh"
 #include "ptx.cuh"
@@ -144,6 +144,7 @@ __device__ __forceinline__ void pair_up(const ResArgs &a, const float4 *aff, Pai
     pairs[t].nmean = pk2(-f[0].x, -f[1].x);
     pairs[t].scale = pk2(f[0].y * f[0].z, f[1].y * f[1].z);
     pairs[t].beta = pk2(f[0].w, f[1].w);
+    pairs[t].k1 = pk2(dropped(f[0].y, f[0].z), dropped(f[1].y, f[1].z));
   }
   __syncthreads();
 }
@@ -189,8 +190,7 @@ __device__ __forceinline__ void finish_stats(const ResArgs &a, float *tri, float
       t = Triple{tri[3 * g], tri[3 * g + 1], tri[3 * g + 2]};
     }
     if (lane == 0) {
-      const float var = t.n > 0.f ? t.m2 / t.n : 0.f;
-      const float2 st = make_float2(t.mean, 1.0f / sqrtf(var + a.eps));
+      const float2 st = make_float2(t.mean, precise_rstd(t.m2, 0.f, t.n, a.eps));
       gst[g] = st;
       if (rank == 0) a.stats[n * a.groups + g0 + g] = st;
     }

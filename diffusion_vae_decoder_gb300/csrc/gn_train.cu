@@ -21,8 +21,9 @@
 // so every load and store of the planes is coalesced over pixels and a
 // checkpoint block is one thread's registers.
 //
-// Measured: forward [1, 512, 512, 128] NHWC 81 us, statistics 25 (134 MB, 5.4
-// TB/s), merge 3, apply 51 (336 MB, 6.6 TB/s); backward [1, 256, 256, 256] 49 us,
+// Measured: forward [1, 512, 512, 128] NHWC 82 us, statistics 25 (134 MB, 5.4
+// TB/s), merge 3, apply 52 (336 MB, 6.5 TB/s; 1 us of it for the low part of the
+// scale, without which y is off by 1.0e-7 rms instead of 0.7e-7); backward [1, 256, 256, 256] 49 us,
 // sums 21 (84 MB), merge 4, dx 25 (151 MB, some of it from L2). The sums' pass is
 // short: coefficients before it, exp and reciprocal in it and the reduction
 // behind it are a third of its time; 2 to 4 pixels in flight measure the same,
@@ -65,26 +66,57 @@ __global__ void __launch_bounds__(kStatThreads)
   stats_segment_nchw(x, c, spatial, groups, gridDim.y, blockIdx.x, blockIdx.y, red, part);
 }
 
+// A Triple whose mean and M2 carry what rounding dropped of them (Knuth's two-sum):
+// a (sample, group) merges 300 of them, and the error of the total is every
+// output's. (Before: rstd off by 6e-8 rms, the mean by 3e-8 of the deviation.)
+struct Wide {
+  float n, mean, m2, mean_low, m2_low;
+};
+__device__ __forceinline__ float two_sum(float a, float b, float *low) {
+  const float s = a + b, c = s - a;
+  *low += (a - (s - c)) + (b - c);
+  return s;
+}
+__device__ __forceinline__ Wide merge(const Wide &a, const Wide &b) {
+  if (a.n == 0.f) return b;
+  if (b.n == 0.f) return a;
+  Wide r{a.n + b.n, 0.f, 0.f, a.mean_low, a.m2_low + b.m2_low};
+  const float w = b.n / r.n, d = (b.mean - a.mean) + (b.mean_low - a.mean_low);
+  r.mean = two_sum(a.mean, d * w, &r.mean_low);
+  r.m2 = two_sum(a.m2, b.m2, &r.m2_low);
+  r.m2 = two_sum(r.m2, d * d * a.n * w, &r.m2_low);
+  return r;
+}
+
 // One block per (sample, group): merges its partials in a fixed order. (Little
 // code: a kernel this short is bound by fetching its instructions.)
 __global__ void __launch_bounds__(kMergeThreads)
     ckpt_stats_merge(const float *part, int slabs, float eps, float2 *stats) {
-  __shared__ Triple red[kMergeThreads / 32];
+  __shared__ Wide red[kMergeThreads / 32];
   grid_release();
   grid_wait();
   const float *e = part + static_cast<size_t>(blockIdx.x) * slabs * 3;
-  Triple acc{0.f, 0.f, 0.f};
+  Wide acc{0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int b = threadIdx.x; b < slabs; b += kMergeThreads)
-    acc = merge(acc, Triple{e[3 * b], e[3 * b + 1], e[3 * b + 2]});
-  acc = warp_merge(acc);
+    acc = merge(acc, Wide{e[3 * b], e[3 * b + 1], e[3 * b + 2], 0.f, 0.f});
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {  // (a lane merges the lower lane's first)
+    const Wide other{__shfl_xor_sync(0xffffffffu, acc.n, o),
+                     __shfl_xor_sync(0xffffffffu, acc.mean, o),
+                     __shfl_xor_sync(0xffffffffu, acc.m2, o),
+                     __shfl_xor_sync(0xffffffffu, acc.mean_low, o),
+                     __shfl_xor_sync(0xffffffffu, acc.m2_low, o)};
+    const bool upper = threadIdx.x & o;
+    acc = merge(upper ? other : acc, upper ? acc : other);
+  }
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll 1
     for (int w = 1; w < kMergeThreads / 32; ++w) acc = merge(acc, red[w]);
-    const float var = acc.n > 0.f ? acc.m2 / acc.n : 0.f;
-    stats[blockIdx.x] = make_float2(acc.mean, 1.0f / sqrtf(var + eps));
+    stats[blockIdx.x] = make_float2(acc.mean + acc.mean_low,
+                                    precise_rstd(acc.m2, acc.m2_low, acc.n, eps));
   }
 }
 

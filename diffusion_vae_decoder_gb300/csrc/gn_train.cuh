@@ -42,7 +42,13 @@ int gn_backward_resident(const float *dy, CkptView x_ckpt, const float *stats, i
 // scale = rstd gamma.
 struct Affine8 {
   uint64_t nmean[4], scale[4], beta[4];
+  uint64_t low[4];  // what rounding dropped of scale; forward only
 };
+// What rounding dropped of a b (nothing where that is not finite).
+__device__ __forceinline__ float dropped(float a, float b) {
+  const float p = a * b;
+  return isfinite(p) ? fmaf(a, b, -p) : 0.f;
+}
 __device__ __forceinline__ Affine8 affine_of(const float (&mean)[8], const float (&rstd)[8],
                                              const float (&gamma)[8], const float (&beta)[8]) {
   Affine8 f;
@@ -51,8 +57,20 @@ __device__ __forceinline__ Affine8 affine_of(const float (&mean)[8], const float
     f.nmean[j] = pk2(-mean[2 * j], -mean[2 * j + 1]);
     f.scale[j] = pk2(rstd[2 * j] * gamma[2 * j], rstd[2 * j + 1] * gamma[2 * j + 1]);
     f.beta[j] = pk2(beta[2 * j], beta[2 * j + 1]);
+    f.low[j] = pk2(dropped(rstd[2 * j], gamma[2 * j]), dropped(rstd[2 * j + 1], gamma[2 * j + 1]));
   }
   return f;
+}
+// 1 / sqrt(v + eps) of v = m2 / n, rounded once: the error of a group's rstd is
+// every output's. One Newton step from r = 1 / sqrtf, its residual 1 - v r^2 with
+// the parts that rounding drops.
+__device__ __forceinline__ float precise_rstd(float m2, float m2_low, float n, float eps) {
+  if (!(n > 0.f)) return 1.0f / sqrtf(eps);
+  const float q = m2 / n, q_low = (fmaf(-q, n, m2) + m2_low) / n;
+  const float v = q + eps, v_low = (eps - (v - q)) + (q - (v - (v - q))) + q_low;
+  const float r = 1.0f / sqrtf(v), t = v * r;
+  const float e = fmaf(-t, r, 1.f) - (fmaf(v, r, -t) + v_low * r) * r;
+  return isfinite(e) ? fmaf(0.5f * r, e, r) : r;
 }
 __device__ __forceinline__ uint64_t rcp2(uint64_t a) {
   float x, y;
@@ -71,7 +89,8 @@ __device__ __forceinline__ Oct forward8(const Oct &x, const Affine8 &f) {
   Oct o;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t z = fma2(add2(x.v[j], f.nmean[j]), f.scale[j], f.beta[j]);
+    const uint64_t d = add2(x.v[j], f.nmean[j]);
+    const uint64_t z = fma2(d, f.scale[j], fma2(d, f.low[j], f.beta[j]));
     o.v[j] = SILU ? mul2(z, sigmoid2(z)) : z;
   }
   return o;
@@ -102,7 +121,7 @@ struct Row32 {
   uint64_t v[16];
 };
 // Per pair of channels: the affine of Affine8, and for the backward pass the
-// group means of dx = scale dz + (k1 + dev k2).
+// group means of dx = scale dz + (k1 + dev k2); forward, k1 is Affine8's low.
 struct PairAffine {
   uint64_t nmean, scale, beta, k1, k2;
 };
@@ -158,7 +177,7 @@ __device__ __forceinline__ Row32 read_row32(CkptView k, long long row, int cp, i
 __device__ __forceinline__ void load_pairs(PairAffine *out, const float2 *stats,
                                            const float *gamma, const float *beta, int ch0, int c,
                                            int cg, int t) {
-  float m[2], s[2], b[2];
+  float m[2], s[2], b[2], low[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int ch = ch0 + 2 * t + h;
@@ -166,17 +185,20 @@ __device__ __forceinline__ void load_pairs(PairAffine *out, const float2 *stats,
     const float2 st = in ? stats[ch / cg] : make_float2(0.f, 0.f);
     m[h] = -st.x;
     s[h] = in ? st.y * gamma[ch] : 0.f;
+    low[h] = in ? dropped(st.y, gamma[ch]) : 0.f;
     b[h] = in ? beta[ch] : 0.f;
   }
   out[t].nmean = pk2(m[0], m[1]);
   out[t].scale = pk2(s[0], s[1]);
   out[t].beta = pk2(b[0], b[1]);
+  out[t].k1 = pk2(low[0], low[1]);
 }
 __device__ __forceinline__ Row32 forward32(const Row32 &x, const PairAffine *f, int silu) {
   Row32 o;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const uint64_t z = fma2(add2(x.v[j], f[j].nmean), f[j].scale, f[j].beta);
+    const uint64_t d = add2(x.v[j], f[j].nmean);
+    const uint64_t z = fma2(d, f[j].scale, fma2(d, f[j].k1, f[j].beta));
     o.v[j] = silu ? mul2(z, sigmoid2(z)) : z;
   }
   return o;
