@@ -143,7 +143,8 @@ struct Sweep {
     row0 = static_cast<long long>(blockIdx.y) * pixels;
   }
   __device__ unsigned pixel(int i) const { return first + static_cast<unsigned>(i) * step; }
-  __device__ bool in(int i, unsigned p) const { return i >= 0 && i < iters && p < spatial; }
+  // (pixels past the last sweep are outside; those before the first wrap round)
+  __device__ bool in(unsigned p) const { return p < spatial; }
 };
 
 // base + p * stride, one 32 x 32 -> 64 bit multiply-add.
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   Oct k = load_oct<WIDE, false>(row_at(src, origin, c), sw.left), v[D];
   auto fetch = [&](int i) {
     const unsigned p = sw.pixel(i);
-    return load_oct<WIDE, false>(row_at(src, p, c), sw.in(i, p) ? sw.left : 0);
+    return load_oct<WIDE, false>(row_at(src, p, c), sw.in(p) ? sw.left : 0);
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) v[u] = fetch(u);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int u = 0; u < D; ++u) {
         const Oct x8 = v[u];
         v[u] = fetch(i + u + D);
-        if (sw.in(i + u, sw.pixel(i + u))) {
+        if (sw.in(sw.pixel(i + u))) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint64_t d = add2(x8.v[j], k.v[j]);
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   Oct v[D];
   auto fetch = [&](int i) {
     const unsigned p = sw.pixel(i);
-    return load_oct<WIDE, true>(row_at(src, p, c), sw.in(i, p) ? sw.left : 0);
+    return load_oct<WIDE, true>(row_at(src, p, c), sw.in(p) ? sw.left : 0);
   };
 #pragma unroll
   for (int u = 0; u < D; ++u) v[u] = fetch(sw.iters - 1 - u);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int u = 0; u < D; ++u) {
       const int i = top - u;
       const unsigned p = sw.pixel(i);
-      const bool in = sw.in(i, p) && sw.pl < sw.ppi;
+      const bool in = sw.in(p) && sw.pl < sw.ppi;
       const Oct x8 = v[u];
       v[u] = fetch(i - D);
       if (kx.q) keep_oct(kx, p, cp, sw.ch, in, x8);
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t sb[D];
     auto fetch = [&](int i, int u) {
       const unsigned p = sw.pixel(i);
-      const bool in = sw.in(i, p);
+      const bool in = sw.in(p);
       g[u] = load_oct<WIDE, false>(row_at(src, p, c), in ? sw.left : 0);
       q[u] = make_uint2(0, 0);
       sb[u] = 0;
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t sb[D];
   auto fetch = [&](int i, int u) {
     const unsigned p = sw.pixel(i);
-    const bool in = sw.in(i, p);
+    const bool in = sw.in(p);
     g[u] = load_oct<WIDE, true>(row_at(src, p, c), in ? sw.left : 0);
     q[u] = make_uint2(0, 0);
     sb[u] = 0;
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int u = 0; u < D; ++u) {
       const int i = top - u;
       const unsigned p = sw.pixel(i);
-      const int left = sw.in(i, p) ? sw.left : 0;
+      const int left = sw.in(p) ? sw.left : 0;
       const Oct dy8 = g[u], x8 = unpack_oct(q[u], ckpt_scale(sb[u]));
       Oct dev, o, r = {{0, 0, 0, 0}};
       if (res) r = load_oct<WIDE, true>(row_at(res, p, c), left);
