@@ -67,12 +67,13 @@ __device__ __forceinline__ void leave() {
 }
 
 // gamma and beta of the slab's channels into the affines (loaded while the
-// pixels are on their way).
+// pixels are on their way). Behind channel c everything is zero: finish_stats
+// completes real channels only, and the padding's share of a checkpoint block
+// must not come from what an earlier kernel left here.
 __device__ __forceinline__ void load_gamma(const ResArgs &a, float4 *aff, int ch0) {
   for (int ch = threadIdx.x; ch < a.slab; ch += kThreads) {
     const bool in = ch0 + ch < a.c;
-    aff[ch].z = in ? a.gamma[ch0 + ch] : 0.f;
-    aff[ch].w = in ? a.beta[ch0 + ch] : 0.f;
+    aff[ch] = make_float4(0.f, 0.f, in ? a.gamma[ch0 + ch] : 0.f, in ? a.beta[ch0 + ch] : 0.f);
   }
 }
 

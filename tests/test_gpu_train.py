@@ -297,6 +297,30 @@ def test_groupnorm_backward_is_the_same_in_place_and_again():
             c[0].abs().max() + a[0].abs().max())
 
 
+def leave_nan_in_shared_memory():
+    """An ordinary call after which the start of every SM's shared memory holds NaN:
+    1024 one-block samples of NaN, whose channels' affines lie there."""
+    x = torch.full((1024, 1, 1, 1024), float("nan"), device="cuda")
+    v = torch.ones(1024, device="cuda")
+    pkg().vae_groupnorm_silu_ckpt(x, v, v, groups=1, layout=pkg().VAE_NHWC, keep_x=False,
+                                  keep_y=False)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("n,h,w,c,groups", [(1, 8, 8, 36, 9), (2, 5, 7, 40, 8), (1, 16, 16, 100, 25),
+                                            (3, 1, 1, 48, 8), (1, 3, 5, 1020, 5), (1, 2, 2, 4, 1)])
+def test_padding_channels_do_not_depend_on_what_ran_before(layout, silu, n, h, w, c, groups):
+    """c is no multiple of 32: the last block of y's checkpoint ends in padding."""
+    x, gamma, beta = gn_data(n, h, w, c, 30)
+    args = dev(to_layout(x, layout)), dev(gamma), dev(beta)
+    leave_nan_in_shared_memory()
+    y, kx, ky, _ = pkg().vae_groupnorm_silu_ckpt(*args, groups=groups, apply_silu=silu,
+                                                 layout=layout)
+    same_codes(kx, x.reshape(-1, c))
+    same_codes(ky, from_layout(y.cpu().numpy(), layout).reshape(-1, c))
+
+
 # ---------------------------------------------------------------- conv weight gradient
 WG = [(1, 1, 1, 32, 32), (1, 1, 1, 1, 4), (2, 3, 5, 16, 12), (1, 8, 8, 64, 64), (1, 7, 33, 96, 20),
       (2, 13, 129, 40, 132), (1, 64, 1, 130, 64), (1, 1, 300, 33, 8), (3, 20, 17, 160, 72),
