@@ -607,27 +607,39 @@ def _call(name, device, *args):
         raise VaeError(name, status)
 
 
+def _memory(*values):
+    """The tensors that hold `values`: tensors, checkpoints, and tuples and dicts of
+    them; other values hold none."""
+    todo = list(values)
+    while todo:
+        v = todo.pop()
+        if isinstance(v, (tuple, dict)):
+            todo += v.values() if isinstance(v, dict) else v
+        elif isinstance(v, Checkpoint):
+            todo += (v._payload, v._scale) if v._bytes is None else (v._bytes,)
+        elif hasattr(v, "record_stream"):
+            yield v
+
+
 def _on(stream, fn, *args):
     """fn(*args) with `stream` current. The memory it allocates is the stream's, so
     nothing pending on the caller's current stream still uses it; what it returns
-    is not reused before that stream's work has passed it."""
+    is not reused before that stream's work has passed it, and neither is what it was
+    given before `stream` has, so that temporaries may be passed."""
     import torch
     device = next((a.device for a in args if hasattr(a, "device")), stream.device)
     if device != stream.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     here = torch.cuda.current_stream(device)
+    if stream != here:
+        for t in _memory(*args):
+            if t.device == device:  # (fn refuses the others)
+                t.record_stream(stream)
     with torch.cuda.stream(stream):
         out = fn(*args)
     if stream != here:
-        todo = [out]
-        while todo:
-            t = todo.pop()
-            if isinstance(t, (tuple, dict)):
-                todo += t.values() if isinstance(t, dict) else t
-            elif isinstance(t, Checkpoint):
-                todo += (t.payload, t.scale)
-            elif t is not None:
-                t.record_stream(here)
+        for t in _memory(out):
+            t.record_stream(here)
     return out
 
 

@@ -629,6 +629,62 @@ def test_a_result_freed_early_stays_until_the_callers_stream_has_read_it():
     assert torch.equal(read, want)
 
 
+def test_a_temporary_stays_until_the_other_stream_has_read_it():
+    """Inputs whose last reference goes with the call, behind a delay on the call's
+    stream; the caller's stream then allocates and fills as much."""
+    p = pkg()
+    n, h, w, c = 1, 64, 64, 128
+    x = torch.randn(n, h, w, c, device="cuda")
+    t, v, side = x.view(n, h * w, c), torch.randn(c, device="cuda"), torch.cuda.Stream()
+    _, kx, _, st = p.vae_groupnorm_silu_ckpt(x, v, v, layout=1)
+    _, _, ku, kh, rs = p.vae_block_norm(t, t, v, w_pre=v)
+
+    def again(k):
+        """A checkpoint of its own around copied bytes."""
+        buf = torch.zeros(p.Checkpoint.nbytes(k.rows, k.c), dtype=torch.uint8, device="cuda")
+        out = p.Checkpoint(buf, k.rows, k.c)
+        out.payload.view(torch.uint8).copy_(k.payload.view(torch.uint8))
+        out.scale.view(torch.uint8).copy_(k.scale.view(torch.uint8))
+        return out
+
+    calls = [
+        (lambda **kw: lambda a: p.vae_groupnorm_silu_ckpt(a, v, v, layout=1, **kw),
+         lambda: (2 * x,)),
+        (lambda **kw: lambda a, k: p.vae_groupnorm_silu_backward(a, k, st, v, v, layout=1, **kw),
+         lambda: (2 * x, again(kx))),
+        (lambda **kw: lambda a, k: p.vae_conv2d_wgrad(a, k, 3, layout=1, **kw),
+         lambda: (2 * x, again(kx))),
+        (lambda **kw: lambda a, b: p.vae_block_norm(a, b, v, w_pre=v, **kw),
+         lambda: (2 * t, 3 * t)),
+        (lambda **kw: lambda a, b, k, m: p.vae_block_norm_backward(a, b, k, m, rs, v, w_pre=v, **kw),
+         lambda: (2 * t, 3 * t, again(ku), again(kh))),
+        (lambda **kw: lambda a: p.vae_ckpt_pack(a, layout=1, **kw), lambda: (2 * x,)),
+        (lambda **kw: lambda k: p.vae_ckpt_unpack(k, x.shape, layout=1, **kw), lambda: (again(kx),)),
+    ]
+
+    def flat(r):
+        if isinstance(r, p.Checkpoint):
+            return [r.payload.view(torch.uint8), r.scale.view(torch.uint8)]
+        if isinstance(r, (tuple, dict)):
+            return [f for e in (r.values() if isinstance(r, dict) else r) for f in flat(e)]
+        return [] if r is None else [r]
+
+    for call, inputs in calls:
+        want = flat(call()(*inputs()))
+        args = inputs()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        got = call(stream=side)(*args)
+        del args
+        junk = [torch.full_like(x, float("nan")) for _ in range(8)]
+        junk += [torch.full((p.Checkpoint.nbytes(h * w, c),), 255, dtype=torch.uint8,
+                            device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert same(want, flat(got))
+        del junk, got
+
+
 @pytest.mark.parametrize("size", SIZES)
 def test_calls_of_two_threads_on_one_stream(size):
     import threading

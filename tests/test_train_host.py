@@ -172,6 +172,58 @@ def test_python_refuses_what_is_not_on_the_gpu():
         pkg.vae_block_norm_backward(None, None, None, None, None, t[0, 0])
 
 
+def test_a_call_on_another_stream_records_what_it_reads_and_returns(monkeypatch):
+    """Inputs, buffers for results and checkpoints belong to the caller's stream: the
+    allocator has to be told that the other stream uses them, or a temporary's
+    memory is given away while the kernel still reads it."""
+    import contextlib
+    torch = pytest.importorskip("torch")
+    import diffusion_vae_decoder_gb300 as pkg
+
+    class Stream:
+        device = "cuda:0"
+
+    here, side = Stream(), Stream()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    seen = []
+
+    class Fake:
+        device = "cuda:0"
+
+        def __init__(self, name):
+            self.name = name
+
+        def record_stream(self, stream):
+            seen.append((self.name, "side" if stream is side else "here"))
+
+    def checkpoint(name, packed):
+        k = pkg.Checkpoint.__new__(pkg.Checkpoint)
+        k.rows, k.c = 1, 32
+        k._bytes = Fake(name) if packed else None
+        k._payload, k._scale = (None, None) if packed else (Fake(name + ".q"), Fake(name + ".s"))
+        return k
+
+    result = (Fake("y"), None, checkpoint("kept", False), dict(g=Fake("g"), none=None))
+    call = lambda *args: result  # noqa: E731
+    args = (Fake("x"), None, 32, 1e-6, True, (1, 2, 3), checkpoint("a", True),
+            checkpoint("b", False), Fake("out"))
+    assert pkg._on(side, call, *args) is result
+    assert sorted(seen) == sorted(
+        [(n, "side") for n in ("x", "a", "b.q", "b.s", "out")] +
+        [(n, "here") for n in ("y", "kept.q", "kept.s", "g")])
+    seen.clear()
+    pkg._on(here, call, *args)  # the caller's own stream: nothing to tell
+    assert not seen
+
+    def failing(*args):
+        raise pkg.VaeError("op", -5)  # perhaps behind its first kernel
+
+    with pytest.raises(pkg.VaeError):
+        pkg._on(side, failing, *args)
+    assert sorted(seen) == [(n, "side") for n in ("a", "b.q", "b.s", "out", "x")]
+
+
 # ---------------------------------------------------------------- the float64 forms
 def _difference(f, a, d, step=1e-5):
     """Central difference of f along d at a."""
