@@ -422,6 +422,36 @@ def test_wgrad_many_chains_and_pieces():
             assert bool((err <= (2.0 ** -22 + 2 * 128 * 2.0 ** -23 + 64 * H) * size).all())
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_wgrad_both_parts_of_dy_in_every_chain(layout):
+    """Integers of 13 bits need both halves of dy, and x~ is 0 or +-1 in so few pixels
+    that every sum of magnitudes stays below 2^24: exact in any order, over several
+    chains a piece. Without the second half, in any chain, the sums differ."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    h, w, c = 512, 640, 32
+    r = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device="cuda")  # noqa: E731
+    dy = (r(4096, 8192, 1, h, w, c) * (2 * r(0, 2, 1, h, w, c) - 1)).float()
+    x = (r(0, 200, 1, h, w, c) == 0).float() * (2 * r(0, 2, 1, h, w, c) - 1)
+    kx = pkg().vae_ckpt_pack(x, layout=1)
+    d_in = dy if layout == 1 else dy.permute(0, 3, 1, 2).contiguous()
+    dw, dbias = pkg().vae_conv2d_wgrad(d_in, kx, 3, layout=layout)
+    xp = torch.nn.functional.pad(x.double(), (0, 0, 1, 1, 1, 1))
+    d = dy.double().reshape(-1, c)
+    first = d.to(torch.float16).double()  # 11 significant bits
+    for ky in range(3):
+        for kx_ in range(3):
+            b = xp[:, ky:ky + h, kx_:kx_ + w].reshape(-1, c)
+            assert float((d.abs().t() @ b.abs()).max()) < 2 ** 24
+            want = d.t() @ b
+            assert torch.equal(dw[:, :, ky, kx_].double(), want)
+            # what a chain of 2048 positions would lose: it shows
+            rows = slice(200 * 640, 203 * 640)
+            lost = (d - first)[rows].t() @ b[rows]
+            assert float((lost != 0).double().mean()) > 0.5
+    # a value passes 34 additions in a thread, 64 in a block, 10 + 5 behind it at most
+    assert float((dbias.double() - d.sum(0)).abs().max()) <= 113 * H * float(d.abs().sum(0).max())
+
+
 # ---------------------------------------------------------------- block norm
 BN = [(1, 1, 4), (1, 1, 512), (2, 3, 32), (1, 17, 100), (3, 5, 128), (2, 9, 256), (1, 40, 512),
       (2, 33, 516), (1, 7, 1024), (2, 11, 1536), (1, 19, 2048), (1, 9, 4096), (5, 1, 2052)]
