@@ -17,8 +17,13 @@
 // clock (measured: 64.2 clocks a step, N = 64 no less than 53.6).
 //
 // Precision. x~ is e4m3 times a power of two: a half holds it exactly once the
-// block scales are taken relative to the largest of their 32 channels (blocks
-// 2^22 below it round at 2^-24 of the largest). dy is scaled per output
+// block scales are taken relative to the largest of their 32 channels, which is
+// put at 2^7 (its largest numbers are 224 to 448 times that). A block whose scale is
+// d binades lower holds multiples of 2^(-2 - d): exact to d = 22, rounded to
+// multiples of 2^-24 to d = 31 (2^-39 of the largest number), zero from d = 32 on
+// (2^-31 of it at most). It shows only where dy is next to nothing wherever the
+// activations are large; bf16 operands would hold any range, but take dy in three
+// parts, half as many MMAs again. dy is scaled per output
 // channel by a power of two to below 2^15 and split into two halves, hi + lo,
 // 22 significant bits. The MMA reads [hi | lo] as 128 columns next to one A
 // operand, so the two parts have accumulators of their own. The tensor core's

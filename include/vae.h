@@ -499,10 +499,14 @@ VAE_API int vae_groupnorm_silu_backward(const float *dy, const void *x_q,
  * cin, cout exchanged; the 1x1 shortcut's weight gradient is a call with k = 1.)
  *   dy [n,cout,h,w] (layout); x_q, x_scale: n*h*w rows of cin channels;
  *   dw [cout,cin,k,k]; dbias [cout] or NULL
- * The products run on the tensor cores with x~ exact and dy in two parts of
- * 11 significant bits each, scaled per output channel by a power of two, so
- * that nothing beyond 2^-22 of a value (2^-38 of the channel's largest) is
- * dropped; FP32 accumulation in a fixed order. A NaN or infinity in dy makes
+ * The products run on the tensor cores in half precision. dy goes in as two
+ * parts of 11 significant bits each, scaled per output channel by a power of
+ * two, so that nothing beyond 2^-22 of a value (2^-38 of the channel's largest)
+ * is dropped. x~ is scaled by a power of two per 32 channels (one for all
+ * pixels): it is exact where the block's scale is at most 2^22 below the
+ * largest scale of its 32 channels, off by at most 2^-39 of their largest value
+ * below that, and taken for zero (2^-31 of that value at most) from 2^32 on.
+ * FP32 accumulation in a fixed order. A NaN or infinity in dy makes
  * its output channel's gradients non-finite, one in a checkpoint block the
  * gradients of that block's 32 input channels.
  * Limits: cin, cout <= 4096; h, w <= 65535; n * h * (w + 1) < 2^30;

@@ -423,6 +423,33 @@ def test_wgrad_many_chains_and_pieces():
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("below,off", [(21, 0.0), (30, 2.0 ** -39), (60, 2.0 ** -31)])
+def test_wgrad_of_activations_far_below_the_largest(layout, k, below, off):
+    """One pixel of ones, where dy is 0, and activations 2^below under it everywhere
+    else, so that nothing hides what they lose. The scales of blocks are d = below - 2
+    to below + 1 binades under the largest; with that at 2^7 in half precision, e4m3
+    times 2^(7 - d) is a multiple of 2^(-2 - d): exact for d <= 22, rounded to a multiple
+    of 2^-24 for d <= 31 (2^-25 of the scaled largest, at least 224 * 2^7: 2^-39), and
+    nothing, 448 * 2^-25 at most, from d = 32 on (2^-31)."""
+    g = np.random.default_rng(32)
+    n, h, w, cin, cout = 1, 24, 37, 40, 12
+    down = np.exp2(g.integers(0, 3, size=(n, h, w, 1)) - float(below))
+    x = g.uniform(0.5, 1, size=(n, h, w, cin)) * g.choice([-1, 1], size=(n, h, w, cin)) * down
+    x = x.astype(np.float32)
+    x[0, 11, 17] = np.where(np.arange(cin) % 2, 1, -1)
+    dy = g.normal(size=(n, h, w, cout)).astype(np.float32)
+    dy[0, 10:13, 16:19] = 0
+    kx = pkg().vae_ckpt_pack(dev(x), layout=1)
+    xt = R.dequantise(*parts(kx), cin).reshape(x.shape)
+    dw, _ = pkg().vae_conv2d_wgrad(dev(to_layout(dy, layout)), kx, k, layout=layout)
+    d64 = dy.astype(np.float64)
+    want, _ = R.wgrad(d64, xt, k)
+    per, _ = R.wgrad(np.abs(d64), np.full_like(xt, np.abs(xt).max()), k)
+    assert (np.abs(host(dw) - want) <= wgrad_bound(d64, xt, k) + off * per).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
 def test_wgrad_both_parts_of_dy_in_every_chain(layout):
     """Integers of 13 bits need both halves of dy, and x~ is 0 or +-1 in so few pixels
     that every sum of magnitudes stays below 2^24: exact in any order, over several
