@@ -903,6 +903,54 @@ def test_groupnorm_pair_past_2_to_32_elements(layout):
     assert float((dx[1] - dx1[0]).abs().max()) <= 2.0 ** -2
 
 
+def test_groupnorm_statistics_of_long_planes_nchw():
+    """A plane of one value behind 256 zeros, which are the first numbers of its first
+    256 threads: their sums of deviations lose the same amount at every step. A thread
+    adds up at most 2^12 numbers, step i off by i H of the value: half of 2^12 H of the
+    mean, and 64 H for the division and the merges behind it."""
+    n, c, side = 5, 32, 1 << 23
+    value = 1 + 2.0 ** -10 - 2.0 ** -14
+    x = torch.full((n, c, side), value, device="cuda")
+    x[:, :, :256] = 0
+    v = torch.ones(c, device="cuda")
+    _, _, _, st = pkg().vae_groupnorm_silu_ckpt(x, v, v, groups=c, layout=pkg().VAE_NCHW, out=x,
+                                                keep_x=False, keep_y=False)
+    want = value * (1 - 256 / side)
+    assert float((st[..., 0].double() - want).abs().max()) <= (2048 + 64) * H * value
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_groupnorm_backward_sums_past_2_to_32_elements(layout):
+    """Values of -1, 0 and 1, mean 0, rstd 1 and no SiLU: every sum is a whole number
+    below 2^24, exact in any order. The parameters' gradients are the sums of the
+    samples', and a sample's dx is that of a call on it alone."""
+    p = pkg()
+    g = torch.Generator(device="cuda").manual_seed(33)
+    n, c, spatial = 2, 256, (1 << 23) - 40
+    shape = (n, spatial, c) if layout == 1 else (n, c, spatial)
+    draw = lambda *s: torch.randint(  # noqa: E731
+        -1, 2, s, generator=g, device="cuda", dtype=torch.int8).float()
+    kx = [p.vae_ckpt_pack(draw(1, spatial, c), layout=1) for _ in range(n)]
+    both = p.Checkpoint(torch.empty(p.Checkpoint.nbytes(n * spatial, c), dtype=torch.uint8,
+                                    device="cuda"), n * spatial, c)
+    for part in ("payload", "scale"):
+        torch.cat([getattr(k, part).view(torch.uint8) for k in kx],
+                  out=getattr(both, part).view(torch.uint8))
+    dy = draw(*shape)
+    st = torch.tensor([0.0, 1.0], device="cuda").expand(n, 32, 2).contiguous()
+    ga, be = torch.full((c,), 1.5, device="cuda"), torch.full((c,), 0.5, device="cuda")
+    dx, dga, dbe = p.vae_groupnorm_silu_backward(dy, both, st, ga, be, apply_silu=False,
+                                                 layout=layout)
+    sums = torch.zeros(2, c, device="cuda")
+    for i in range(n):
+        dx1, dga1, dbe1 = p.vae_groupnorm_silu_backward(dy[i:i + 1], kx[i], st[i:i + 1], ga, be,
+                                                        apply_silu=False, layout=layout)
+        assert torch.equal(dx[i], dx1[0])
+        sums += torch.stack([dga1, dbe1])
+    assert torch.equal(torch.stack([dga, dbe]), sums)
+    assert torch.equal(dbe.double(), dy.sum((0, 1) if layout == 1 else (0, 2), dtype=torch.float64))
+
+
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_wgrad_past_2_to_32_elements(layout):
     """Small integers, whose sums stay below 2^24, are exact whatever their order:
