@@ -297,6 +297,45 @@ def test_groupnorm_backward_is_the_same_in_place_and_again():
             c[0].abs().max() + a[0].abs().max())
 
 
+def silu_of(betas, layout, pixels):
+    """vae_groupnorm_silu_ckpt of a constant: z is beta to the bit, every pixel alike."""
+    x = torch.zeros((1, pixels, 1, 64) if layout == 1 else (1, 64, pixels, 1), device="cuda")
+    rows = []
+    for b in betas.split(64):
+        y, _, _, _ = pkg().vae_groupnorm_silu_ckpt(x, torch.ones_like(b), b, groups=2,
+                                                   layout=layout)
+        y = y.reshape(pixels, 64) if layout == 1 else y.reshape(64, pixels).t()
+        assert bool(((y == y[0]) | (y != y)).all())
+        rows.append(y[0])
+    return torch.cat(rows)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("pixels", [1, 24000])  # one launch, three
+def test_silu_is_as_precise_where_it_is_small(layout, pixels):
+    """Half-steps of y for |z| <= 12: the exp2 unit 4, its correction 1 and ln 2's
+    rounding 0.6, the sum with 1 one, the reciprocal 2, the product 1."""
+    z = torch.linspace(-12, 12, 64 * 60, device="cuda")
+    want = z.double() * torch.sigmoid(z.double())
+    got = silu_of(z, layout, pixels).double()
+    assert float(((got - want).abs() / want.abs().clamp(min=1e-30)).max()) <= 10 * H
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("pixels", [1, 24000])
+def test_silu_of_the_largest_and_of_non_finite_values(layout, pixels):
+    big = [88.0, 104.0, 200.0, 1e6, 2.0 ** 24, 1e9, 1e30, 2.4e38, 3.4e38, float("inf")]
+    z = torch.zeros(64, device="cuda")
+    z[:10], z[10:20], z[20] = torch.tensor(big), -torch.tensor(big), float("nan")
+    got = silu_of(z, layout, pixels)
+    want = z / (1 + torch.exp(-z))
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan) and int(nan.sum()) == 2  # -infinity and NaN
+    # e^-88 is a small normal number's reciprocal, which may be taken for 0
+    assert bool((got[~nan] - want[~nan]).abs().le(2.0 ** -119 + 10 * H * want[~nan].abs())
+                .logical_or(got[~nan] == want[~nan]).all())
+
+
 def leave_nan_in_shared_memory():
     """An ordinary call after which the start of every SM's shared memory holds NaN:
     1024 one-block samples of NaN, whose channels' affines lie there."""
