@@ -360,6 +360,42 @@ def test_padding_channels_do_not_depend_on_what_ran_before(layout, silu, n, h, w
     same_codes(ky, from_layout(y.cpu().numpy(), layout).reshape(-1, c))
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("h,w,c,groups", [(5, 7, 64, 16), (5, 7, 48, 12), (150, 100, 64, 16),
+                                          (130, 120, 48, 12)])  # one launch; three
+def test_groupnorm_pair_keeps_non_finite_values_apart(layout, value, h, w, c, groups):
+    """One value of sample 1, group 3: its group of outputs is lost, and in the backward
+    pass the sample's groups that share the checkpoint block. Every other number is, to
+    the bit, what it is without it."""
+    x, gamma, beta = gn_data(2, h, w, c, 34)
+    dy = dev(to_layout(np.random.default_rng(35).normal(size=x.shape), layout))
+    args = dev(gamma), dev(beta)
+    out = []
+    for bad in (False, True):
+        x[1, h // 2, w // 3, 13] = value if bad else 0.5
+        xt = dev(to_layout(x, layout))
+        y, kx, ky, st = pkg().vae_groupnorm_silu_ckpt(xt, *args, groups=groups, layout=layout)
+        for kept, t in ((kx, xt), (ky, y)):
+            again = pkg().vae_ckpt_pack(t, layout=layout)
+            assert all((a == b).all() for a, b in zip(parts(kept), parts(again)))
+        dx, dga, dbe = pkg().vae_groupnorm_silu_backward(dy, kx, st, *args, groups=groups,
+                                                         layout=layout)
+        flat = lambda t: from_layout(t.cpu().numpy(), layout).reshape(2, h * w, c)  # noqa: E731
+        out.append([flat(y), st.cpu().numpy(), flat(dx), dga.cpu().numpy(), dbe.cpu().numpy()])
+    (y, st, dx, dga, dbe), (yb, stb, dxb, dgab, dbeb) = out
+    lost = np.zeros((2, c), dtype=bool)
+    lost[1, 12:16] = True
+    assert np.isnan(yb[1, :, 12:16]).all() and np.isnan(stb[1, 3, 1])
+    assert (yb == y)[:, :, ~lost[1]].all() and (yb[0] == y[0]).all()
+    ok = ~lost.reshape(2, groups, -1).any(2)
+    assert (stb == st)[ok].all()
+    block = np.arange(c) < 32
+    assert np.isnan(dxb[1][:, block]).all() and np.isnan(dgab[block]).all()
+    assert (dxb[0] == dx[0]).all() and (dxb[1] == dx[1])[:, ~block].all()
+    assert (dgab == dga)[~block].all() and (dbeb == dbe)[~block].all()
+
+
 # ---------------------------------------------------------------- conv weight gradient
 WG = [(1, 1, 1, 32, 32), (1, 1, 1, 1, 4), (2, 3, 5, 16, 12), (1, 8, 8, 64, 64), (1, 7, 33, 96, 20),
       (2, 13, 129, 40, 132), (1, 64, 1, 130, 64), (1, 1, 300, 33, 8), (3, 20, 17, 160, 72),
