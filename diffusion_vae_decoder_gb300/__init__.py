@@ -463,7 +463,9 @@ def vae_causal_stack(x, layers, groups=32, eps=1e-6, layout=VAE_NCHW, out=None, 
 
 # ---------------------------------------------------------------- training operators
 # These are called many times a step on tensors whose kernels take a few
-# microseconds, so the checks are one short call per tensor.
+# microseconds, so the checks are one short call per tensor. Like the other entry
+# points they are outside autograd: results carry no graph, and a training step calls
+# the forward and the backward operators itself (or from an autograd.Function).
 class Checkpoint:
     """An 8-bit activation checkpoint of ``rows`` pixels or tokens of ``c``
     channels: ``payload`` [rows, cp] (float8_e4m3fn, cp = c rounded up to 32) and

@@ -158,8 +158,7 @@ inline bool wide_ok(int c, const T *...p) {
   return c % 8 == 0 && (((reinterpret_cast<uintptr_t>(p) & 31) == 0) && ...);
 }
 
-
-// The same for a block spread over four aligned lanes, eight values each.
+// octet_quantise for a block spread over four aligned lanes, eight values each.
 __device__ __forceinline__ uint2 quad_quantise(const Oct &x, uint32_t *byte) {
   float m = max_abs3(lo2(x.v[0]), hi2(x.v[0]), lo2(x.v[1]));
   m = max_abs3(m, hi2(x.v[1]), lo2(x.v[2]));

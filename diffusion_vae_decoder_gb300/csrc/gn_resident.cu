@@ -9,10 +9,11 @@
 // through distributed shared memory (every block adds them in rank order, so
 // all get the same bits) and writes the results: each tensor moves once, and
 // the three launches with two passes over HBM of gn_train.cu become one. These
-// are the launch-bound sizes: at [1, 512, 64, 64] NHWC the forward takes 13 to 14
-// us instead of 15, the backward 12 instead of 18, and a call in a loop 23 and 16
-// instead of 32 and 26; what bounds it is one block's chain of launch,
-// load, two cluster barriers and store.
+// are the launch-bound sizes: at [1, 512, 64, 64] NHWC the forward takes 13 us of the
+// GPU instead of 15, the backward 12 instead of 18, and a call of the binding in a
+// bare loop on the same tensors, which the host bounds, 24 and 17 instead of 31 and
+// 25. On the GPU it is one block's chain of launch, load, two cluster barriers and
+// store.
 #include "gn_train.cuh"
 #include "ptx.cuh"
 
@@ -675,9 +676,9 @@ static_assert(kMaxSmem <= 227 * 1024, "the widest slab (c <= 1024) fits an SM");
 // holds, three launches 8 to 14 us in all, but 10 us more of the host's time when
 // they are called one by one. Measured, GPU (calls in a loop), us:
 //   numbers a block          one launch           three launches
-//   4096  (1, 64, 1024)      10.3 (23)  7.6 (16)  8.2 (33)  12.1 (26)  NCHW
-//   16384 (1, 256, 4096)     10.2 (24)  9.4 (17)  11.7 (34) 14.4 (27)  NHWC
-//   16384 (1, 256, 4096)     15.3 (23)  12.6 (17) 10.3 (33) 12.5 (27)  NCHW
+//   4096  (1, 64, 1024)      10.5 (23)  7.8 (17)  8.8 (31)  12.5 (25)  NCHW
+//   16384 (1, 256, 4096)     11.1 (24)  9.4 (18)  12.3 (31) 15.0 (25)  NHWC
+//   16384 (1, 256, 4096)     16.0 (23)  12.7 (17) 10.9 (31) 13.1 (25)  NCHW
 //   23500 (2, 96, 1961)                 21.0 (27)           12.2 (26)  NCHW
 //   49152 (1, 96, 4096)      41.3 (43)  33.3 (35) 8.7 (33)  12.5 (26)  NCHW
 //   twice 16384 (4, 512, 4096) 72 (73)  58 (60)   30 (33)   54 (58)    NCHW

@@ -120,7 +120,6 @@ def test_pack_edges_of_the_format():
 # ---------------------------------------------------------------- GroupNorm + SiLU
 GN = [(1, 8, 8, 128, 32), (2, 5, 7, 32, 32), (1, 1, 1, 64, 32), (3, 3, 11, 96, 32),
       (1, 37, 29, 48, 8), (2, 16, 33, 512, 32), (1, 4, 9, 1024, 1), (1, 130, 70, 36, 9)]
-# one launch with clusters of 8 and 16 blocks, and the passes over larger tensors
 # one launch at its largest, several rounds of blocks, a slab of all channels, many
 # samples; then three launches
 GN_LARGE = [(1, 64, 64, 512, 32), (4, 64, 64, 512, 32), (1, 64, 64, 96, 32), (300, 4, 4, 64, 32),
