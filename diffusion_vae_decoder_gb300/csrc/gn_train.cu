@@ -46,24 +46,25 @@ constexpr long long kMostInARow = 4096;
 
 // Blocks (slabs of pixels) per sample. A thread adds up kMostInARow numbers in a row
 // at most: step i of a sum of like numbers is off by up to i half-steps of one, and a
-// plane of 2^23 pixels in sums of 32768 had its mean off by 4e-4. (More blocks than
-// are resident, then; tensors of some 10 GB and above.)
+// plane of 2^23 pixels in sums of 32768 had its mean off by 4e-4. More blocks than
+// are resident are whole rounds of them: from 5 GB on NHWC, and the NCHW statistics of
+// many samples from 0.6.
 int slabs_nhwc(int n, int c, long long spatial) {
   const int ppi = kThreads / (ckpt_cp(c) / 8);
   const long long most = std::max(1, kBlocks / n);
-  return static_cast<int>(std::max({1ll, std::min(most, spatial / (4 * ppi)),
-                                    (spatial - 1) / (kMostInARow * ppi) + 1}));
+  const long long rounds = (spatial - 1) / (kMostInARow * ppi * most) + 1;
+  return static_cast<int>(std::max(1ll, std::min(rounds * most, spatial / (4 * ppi))));
 }
 int slabs_nchw(int n, int c, long long spatial) {
   const long long most = std::max(1, kPixBlocks / (n * (ckpt_cp(c) / 32)));
-  return static_cast<int>(std::max(std::min(most, (spatial + kPixThreads - 1) / kPixThreads),
-                                   (spatial - 1) / (kMostInARow * kPixThreads) + 1));
+  const long long rounds = (spatial - 1) / (kMostInARow * kPixThreads * most) + 1;
+  return static_cast<int>(std::min(rounds * most, (spatial + kPixThreads - 1) / kPixThreads));
 }
 int slabs_stats_nchw(int ng, long long seg) {  // (a grid's y)
   const long long most = std::max(1, kBlocks / ng);
+  const long long rounds = (seg - 1) / (kMostInARow * kStatThreads * most) + 1;
   return static_cast<int>(
-      std::min(65535ll, std::max({1ll, std::min(most, seg / (kStatThreads * 8)),
-                                  (seg - 1) / (kMostInARow * kStatThreads) + 1})));
+      std::max(1ll, std::min({65535ll, rounds * most, seg / (kStatThreads * 8)})));
 }
 
 // ------------------------------------------------------------- statistics
