@@ -20,6 +20,8 @@ HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "vae.h")
 
 VAE_NCHW = 0
 VAE_NHWC = 1
+VAE_F32, VAE_BF16, VAE_F16 = 0, 1, 2
+VAE_ACT_NONE, VAE_ACT_SILU, VAE_ACT_GELU = 0, 1, 2
 STATUS = {0: "VAE_OK", -1: "VAE_EINVAL", -2: "VAE_EUNSUPPORTED", -3: "VAE_EWORKSPACE",
           -4: "VAE_ECUDA", -5: "VAE_ENOTPREPARED", -6: "VAE_EDEVICE_TIMEOUT", -7: "VAE_ENOMEM"}
 
@@ -101,6 +103,7 @@ TRACE_KINDS = {0: "latent", 1: "conv", 2: "groupnorm", 3: "resnet", 4: "attentio
 INJECT_WITHHOLD_STREAMK_FLAG = 1
 
 _I, _LL, _F, _SZ = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+_ULL = ctypes.c_ulonglong
 _SIGS = {
     "vae_conv2d_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "vae_conv2d": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _I, _P, _P, _SZ,
@@ -158,6 +161,16 @@ _SIGS = {
     "vae_block_norm": (_I, [_P, _P, _I, _LL, _I, _F] + [_P] * 12),
     "vae_block_norm_backward_workspace_size": (_SZ, [_I, _LL, _I, _I]),
     "vae_block_norm_backward": (_I, [_P] * 7 + [_I, _LL, _I] + [_P] * 11 + [_SZ, _P]),
+    "vae_layer_norm": (_I, [_P, _I, _LL, _I, _F] + [_P] * 5),
+    "vae_layer_norm_backward_workspace_size": (_SZ, [_LL, _I]),
+    "vae_layer_norm_backward": (_I, [_P, _P, _I, _P, _LL, _I] + [_P] * 6 + [_SZ, _P]),
+    "vae_dropout": (_I, [_P, _I, _LL, ctypes.c_double, _ULL, _ULL] + [_P] * 4),
+    "vae_linear_workspace_size": (_SZ, [_I, _LL, _I, _I]),
+    "vae_linear": (_I, [_P, _I, _LL, _I, _P, _P, _I, _I] + [_P] * 4 + [_SZ, _P]),
+    "vae_linear_dgrad_workspace_size": (_SZ, [_I, _LL, _I, _I]),
+    "vae_linear_dgrad": (_I, [_P, _I, _LL, _I, _P, _I, _I] + [_P] * 3 + [_SZ, _P]),
+    "vae_linear_wgrad_workspace_size": (_SZ, [_I, _LL, _I, _I]),
+    "vae_linear_wgrad": (_I, [_P, _P, _I, _LL, _I, _I] + [_P] * 3 + [_SZ, _P]),
     "vae_measure_tf32_mma": (_I, [_I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_float), _P]),
     "vae_debug_set_wait_limit": (_I, [ctypes.c_ulonglong]),
@@ -847,6 +860,206 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
           ps, pp, du.data_ptr(), dx.data_ptr(), dw_post.data_ptr(), _ptr(dgate), _ptr(dscale),
           _ptr(dw_pre), pw, nw)
     return dict(du=du, dx=dx, dw_post=dw_post, dgate=dgate, dscale=dscale, dw_pre=dw_pre)
+
+
+# ---------------------------------------------------------------- a transformer block's MLP
+@functools.lru_cache(maxsize=None)
+def _dtypes():
+    import torch
+    return {torch.float32: VAE_F32, torch.bfloat16: VAE_BF16, torch.float16: VAE_F16}
+
+
+def _tokens(x, name):
+    """(vae_dtype, dtype, shape, rows, c, device) of token rows x [..., c]."""
+    global _F32
+    try:
+        dtype = x.dtype
+        code = _dtypes()[dtype]
+        if not (x.is_cuda and x.is_contiguous()):
+            raise KeyError
+    except (AttributeError, KeyError):
+        raise TypeError(f"{name} must be a contiguous float32, bfloat16 or float16 CUDA "
+                        "tensor") from None
+    if _F32 is None:
+        import torch
+        _F32 = torch.float32
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError(f"{name} must be [..., c]")
+    c = shape[-1]
+    if c > 65536:  # (beyond every operator's limit, and C's int)
+        raise VaeError(name, -2)
+    return code, dtype, shape, x.numel() // c if c else 0, c, x.device
+
+
+def _like(t, dtype, shape, device, name):
+    """The address of a contiguous tensor of `dtype` and `shape` on `device`."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if dtype is _F32:
+        _refuse(t, shape, device, name)
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
+            and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _like_opt(t, dtype, shape, device, name):
+    return None if t is None else _like(t, dtype, shape, device, name)
+
+
+def vae_layer_norm(x, gamma, beta=None, eps=1e-6, keep=True, out=None, stream=None):
+    """Layer norm of token rows x [..., c]: (y, stats), stats [..., 2] (mean,
+    1 / sqrt(var + eps)) for the backward pass, None with keep=False (serving)."""
+    import torch
+    if stream is not None:
+        return _on(stream, vae_layer_norm, x, gamma, beta, eps, keep, out)
+    load_library()
+    code, dtype, shape, rows, c, dev = _tokens(x, "x")
+    pg, pb = _like(gamma, _F32, (c,), dev, "gamma"), _like_opt(beta, _F32, (c,), dev, "beta")
+    y = torch.empty_like(x) if out is None else out
+    py = y.data_ptr() if out is None else _like(out, dtype, shape, dev, "out")
+    stats = pst = None
+    if keep:
+        stats = torch.empty((*shape[:-1], 2), dtype=_F32, device=dev)
+        pst = stats.data_ptr()
+    _call("vae_layer_norm", dev, x.data_ptr(), code, rows, c, eps, pg, pb, py, pst)
+    return y, stats
+
+
+def vae_layer_norm_backward(dy, x, stats, gamma, dres=None, out=None, stream=None):
+    """(dx, dgamma, dbeta) of vae_layer_norm from its input and the statistics it
+    kept; dres, a further gradient of x (the residual stream's), is added to dx."""
+    import torch
+    if stream is not None:
+        return _on(stream, vae_layer_norm_backward, dy, x, stats, gamma, dres, out)
+    load_library()
+    code, dtype, shape, rows, c, dev = _tokens(dy, "dy")
+    px = _like(x, dtype, shape, dev, "x")
+    pst = _like(stats, _F32, (*shape[:-1], 2), dev, "stats")
+    pg = _like(gamma, _F32, (c,), dev, "gamma")
+    pr = _like_opt(dres, dtype, shape, dev, "dres")
+    dx = torch.empty_like(dy) if out is None else out
+    pdx = dx.data_ptr() if out is None else _like(out, dtype, shape, dev, "out")
+    ws, pw, nw = _workspace(dev, "vae_layer_norm_backward_workspace_size", rows, c)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
+    _call("vae_layer_norm_backward", dev, dy.data_ptr(), px, code, pst, rows, c, pg, pr, pdx,
+          dgamma.data_ptr(), dbeta.data_ptr(), pw, nw)
+    return dx, dgamma, dbeta
+
+
+def vae_dropout(x, p, seed=None, offset=0, state=None, residual=None, out=None, stream=None):
+    """Dropout of any contiguous tensor, with a mask that (seed, offset) determine
+    and nothing stores: y = x / (1 - p) where kept, 0 elsewhere (+ residual). The
+    gradient of x is the same call on the gradient of y, without the residual. In
+    the place of `seed`, `state` (int64 CUDA tensor [2]: seed, a number added to
+    offset) may change between the replays of a captured graph. A call takes
+    ceil(x.numel() / 8) counters from `offset` on."""
+    import torch
+    if stream is not None:
+        return _on(stream, vae_dropout, x, p, seed, offset, state, residual, out)
+    load_library()
+    code = _dtypes().get(getattr(x, "dtype", None))
+    if code is None or not (x.is_cuda and x.is_contiguous()):
+        raise TypeError("x must be a contiguous float32, bfloat16 or float16 CUDA tensor")
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    if (seed is None) == (state is None):
+        raise ValueError("one of seed and state must be given")
+    for v, name in ((seed or 0, "seed"), (offset, "offset")):
+        if not 0 <= v < 2 ** 64:
+            raise ValueError(f"{name} must lie in [0, 2^64)")
+    if not 0 <= p <= 1:
+        raise ValueError("p must lie in [0, 1]")
+    ps = None if state is None else _like(state, torch.int64, (2,), dev, "state")
+    pr = _like_opt(residual, dtype, shape, dev, "residual")
+    y = torch.empty_like(x) if out is None else out
+    py = y.data_ptr() if out is None else _like(out, dtype, shape, dev, "out")
+    _call("vae_dropout", dev, x.data_ptr(), code, x.numel(), p, seed or 0, offset, ps, pr, py)
+    return y
+
+
+def _weights(w, dtype, c, axis, device):
+    """(address, n, k) of a linear layer's weights [n, k] with c along `axis`."""
+    if getattr(w, "ndim", None) != 2:
+        raise ValueError("w must be [n, k]")
+    n, k = w.shape
+    if n > 65536 or k > 65536:
+        raise VaeError("w", -2)
+    return _like(w, dtype, (n, c) if axis else (c, k), device, "w"), n, k
+
+
+def vae_linear(x, w, bias=None, act=VAE_ACT_NONE, residual=None, keep=False, out=None,
+               stream=None):
+    """(y, z) of a linear layer on token rows x [..., k] with weights w [n, k]:
+    z = x w^T + bias, y = act(z) + residual. z is None with keep=False; act's
+    gradient (vae_linear_dgrad of the layer that follows) needs it."""
+    import torch
+    if stream is not None:
+        return _on(stream, vae_linear, x, w, bias, act, residual, keep, out)
+    load_library()
+    code, dtype, shape, rows, k, dev = _tokens(x, "x")
+    pw, n, _ = _weights(w, dtype, k, 1, dev)
+    pb = _like_opt(bias, _F32, (n,), dev, "bias")
+    to = (*shape[:-1], n)
+    pr = _like_opt(residual, dtype, to, dev, "residual")
+    y = torch.empty(to, dtype=dtype, device=dev) if out is None else out
+    py = y.data_ptr() if out is None else _like(out, dtype, to, dev, "out")
+    z = pz = None
+    if keep:
+        z = torch.empty(to, dtype=dtype, device=dev)
+        pz = z.data_ptr()
+    ws, pws, nws = _workspace(dev, "vae_linear_workspace_size", code, rows, n, k)
+    _call("vae_linear", dev, x.data_ptr(), code, rows, k, pw, pb, n, act, pr, py, pz, pws, nws)
+    return y, z
+
+
+def vae_linear_dgrad(dy, w, z=None, act=VAE_ACT_NONE, out=None, stream=None):
+    """dx = (dy w) act'(z) for dy [..., n] and w [n, k]: the gradient of the layer's
+    input, carried through the activation that made it out of z [..., k] (None
+    without one)."""
+    import torch
+    if stream is not None:
+        return _on(stream, vae_linear_dgrad, dy, w, z, act, out)
+    load_library()
+    code, dtype, shape, rows, n, dev = _tokens(dy, "dy")
+    pw, _, k = _weights(w, dtype, n, 0, dev)
+    to = (*shape[:-1], k)
+    if (z is None) != (act == VAE_ACT_NONE):
+        raise ValueError("z goes with an activation")
+    pz = _like_opt(z, dtype, to, dev, "z")
+    dx = torch.empty(to, dtype=dtype, device=dev) if out is None else out
+    pdx = dx.data_ptr() if out is None else _like(out, dtype, to, dev, "out")
+    ws, pws, nws = _workspace(dev, "vae_linear_dgrad_workspace_size", code, rows, n, k)
+    _call("vae_linear_dgrad", dev, dy.data_ptr(), code, rows, n, pw, k, act, pz, pdx, pws, nws)
+    return dx
+
+
+def vae_linear_wgrad(dy, x, bias=True, stream=None):
+    """(dw [n, k], dbias [n]), float32, of a linear layer from its output's gradient
+    dy [..., n] and its input x [..., k]; dbias is None with bias=False."""
+    import torch
+    if stream is not None:
+        return _on(stream, vae_linear_wgrad, dy, x, bias)
+    load_library()
+    code, dtype, shape, rows, n, dev = _tokens(dy, "dy")
+    _, _, _, _, k, _ = _tokens(x, "x")
+    px = _like(x, dtype, (*shape[:-1], k), dev, "x")
+    ws, pws, nws = _workspace(dev, "vae_linear_wgrad_workspace_size", code, rows, n, k)
+    dw = torch.empty((n, k), dtype=_F32, device=dev)
+    dbias = pb = None
+    if bias:
+        dbias = torch.empty(n, dtype=_F32, device=dev)
+        pb = dbias.data_ptr()
+    _call("vae_linear_wgrad", dev, dy.data_ptr(), px, code, rows, n, k, dw.data_ptr(), pb, pws,
+          nws)
+    return dw, dbias
 
 
 def vae_measure_tf32_mma(iters, stream=None):

@@ -95,7 +95,8 @@ long long launch_count();
 // swizzle128 = false: plain row-major boxes in shared memory.
 int encode_tiled(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
                  const uint64_t *strides_bytes /* rank-1 entries */, const uint32_t *box,
-                 bool swizzle128 = true);
+                 bool swizzle128 = true,
+                 CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 
 // ------------------------------------------------------------------ kernels
 // Implicit-GEMM convolution / GEMM on tcgen05 (igemm.cu).

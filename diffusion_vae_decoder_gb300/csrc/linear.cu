@@ -1,0 +1,215 @@
+// linear.cu -- a linear layer on token rows, and its gradients.
+//
+//   z = x w^T + b, y = act(z) + residual       x [rows][k], w [n][k]
+//   dx = (dy w) act'(z)                        z [rows][k] of the layer that made x
+//   dw = dy^T x, db = sum over rows of dy
+// The products run on the tensor cores (gemm.cu); floats go in as three bf16 parts,
+// which a pass of its own writes (6 bytes a number).
+#include "linear.cuh"
+#include "tokens.cuh"
+
+namespace vae {
+
+namespace {
+
+// x = h + m + l exactly, each the nearest bf16 of what is left: 8 significant bits
+// and a sign, so that |m| <= 2^-8 |x| and |l| <= 2^-17 |x| (what lies below the
+// smallest bf16 is dropped). An infinite or NaN x is h; a finite one that would round
+// to infinity is cut.
+__device__ __forceinline__ uint32_t nearest_bf16(float x) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+__device__ __forceinline__ void split3(float x, uint32_t *h, uint32_t *m, uint32_t *l) {
+  const uint32_t bits = __float_as_uint(x), mag = bits & 0x7fffffffu;
+  *h = mag >= 0x7f7f8000u && mag < 0x7f800000u ? bits >> 16 : nearest_bf16(x);
+  if (mag >= 0x7f800000u) {
+    *m = *l = 0;
+    return;
+  }
+  const float r = x - __uint_as_float(*h << 16);
+  *m = nearest_bf16(r);
+  *l = nearest_bf16(r - __uint_as_float(*m << 16));
+}
+
+// Two tensors at once: parts of a [na] behind one another at da, of b [nb] at db.
+__global__ void __launch_bounds__(256)
+    split_kernel(const float *__restrict__ a, long long na, uint16_t *da,
+                 const float *__restrict__ b, long long nb, uint16_t *db) {
+  grid_release();
+  const long long step = 8ll * gridDim.x * 256;
+  for (long long at = 8ll * (blockIdx.x * 256ll + threadIdx.x); at < na + nb; at += step) {
+    const bool second = at >= na;
+    const long long i = second ? at - na : at, n = second ? nb : na;
+    const float *src = (second ? b : a) + i;
+    uint16_t *dst = (second ? db : da) + i;
+    const Raw<float> r = load_raw<float, false>(src, 8);
+    const uint32_t *v = reinterpret_cast<const uint32_t *>(r.v);
+    uint32_t w[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h0, m0, l0, h1, m1, l1;
+      split3(__uint_as_float(v[2 * j]), &h0, &m0, &l0);
+      split3(__uint_as_float(v[2 * j + 1]), &h1, &m1, &l1);
+      w[0][j] = h0 | h1 << 16;
+      w[1][j] = m0 | m1 << 16;
+      w[2][j] = l0 | l1 << 16;
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<uint4 *>(dst + q * n) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+  }
+}
+
+// Operands a [na], b [nb] of type `dtype`: as they are, or floats' parts in `ws`.
+size_t parts_bytes(int dtype, long long na, long long nb) {
+  return dtype == VAE_F32 ? 6 * static_cast<size_t>(na + nb) : 0;
+}
+int operands(GemmDesc *d, int dtype, const void *a, long long na, const void *b, long long nb,
+             void *ws, cudaStream_t s) {
+  d->a.p = a;
+  d->b.p = b;
+  d->dtype = dtype;
+  d->f16 = dtype == VAE_F16;
+  if (dtype != VAE_F32) return VAE_OK;
+  uint16_t *pa = static_cast<uint16_t *>(ws), *pb = pa + 3 * na;
+  const unsigned grid = static_cast<unsigned>(
+      std::min<long long>((na + nb + 2047) / 2048, 8ll * num_sms()));
+  split_kernel<<<grid, 256, 0, s>>>(static_cast<const float *>(a), na, pa,
+                                    static_cast<const float *>(b), nb, pb);
+  VAE_LAUNCH_CHECK();
+  count_launches(1);
+  d->a.p = pa;
+  d->b.p = pb;
+  d->parts = 3;
+  d->wait = true;
+  return VAE_OK;
+}
+
+// ------------------------------------------------------------------ column sums
+// part [slabs][n]: sums of dy's columns over a slab's rows. A block has 256 columns,
+// eight to a thread, and eight rows at a time.
+template <class D, bool WIDE>
+__global__ void __launch_bounds__(256)
+    column_sums(const D *__restrict__ dy, long long rows, int n, float *part) {
+  __shared__ float4 red[8][32][2];
+  grid_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ch = 256 * blockIdx.x + 8 * lane;
+  Oct sum = {{0, 0, 0, 0}};
+#pragma unroll 4
+  for (long long r = 8ll * blockIdx.y + warp; r < rows; r += 8ll * gridDim.y) {
+    const Oct v = oct_of(load_raw<D, WIDE>(dy + r * n + ch, n - ch));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum.v[j] = add2(sum.v[j], v.v[j]);
+  }
+  red[warp][lane][0] = oct_lo(sum);
+  red[warp][lane][1] = oct_hi(sum);
+  __syncthreads();
+  if (warp == 0 && ch < n) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const Oct o = oct_of(red[w][lane][0], red[w][lane][1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum.v[j] = add2(sum.v[j], o.v[j]);
+    }
+    store_raw<float, false>(part + static_cast<size_t>(blockIdx.y) * n + ch, n - ch,
+                            raw_of<float>(sum));
+  }
+}
+__global__ void __launch_bounds__(256)
+    merge_sums(const float *part, int slabs, int n, float *__restrict__ out) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = 32 * blockIdx.x + lane;
+  float t = 0.f;
+  grid_wait();
+  if (ch < n)
+#pragma unroll 8
+    for (int s = warp; s < slabs; s += 8) t += part[static_cast<size_t>(s) * n + ch];
+  red[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && ch < n) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t += red[w][lane];
+    out[ch] = t;
+  }
+}
+int sum_slabs(long long rows, int n) {
+  const int cols = ceil_div(n, 256);
+  return static_cast<int>(
+      std::max<long long>(1, std::min<long long>((rows + 31) / 32, 608 / cols)));
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ operators
+size_t linear_ws_bytes(int dtype, long long rows, int n, int k) {
+  return parts_bytes(dtype, rows * k, static_cast<long long>(n) * k);
+}
+
+int linear(const void *x, int dtype, long long rows, int k, const void *w, const float *bias,
+           int n, int act, const void *residual, void *y, void *z, void *ws, cudaStream_t s) {
+  GemmDesc d;
+  VAE_TRY(operands(&d, dtype, x, rows * k, w, static_cast<long long>(n) * k, ws, s));
+  d.m = rows;
+  d.n = n;
+  d.k = k;
+  d.epi = {bias, residual, y, z, act, false};
+  return gemm(d, s);
+}
+
+size_t linear_dgrad_ws_bytes(int dtype, long long rows, int n, int k) {
+  return parts_bytes(dtype, rows * n, static_cast<long long>(n) * k);
+}
+
+int linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w, int k, int act,
+                 const void *z, void *dx, void *ws, cudaStream_t s) {
+  GemmDesc d;
+  VAE_TRY(operands(&d, dtype, dy, rows * n, w, static_cast<long long>(n) * k, ws, s));
+  d.b.k_major = false;
+  d.m = rows;
+  d.n = k;
+  d.k = n;
+  d.epi = {nullptr, z, dx, nullptr, act, true};
+  return gemm(d, s);
+}
+
+size_t linear_wgrad_ws_bytes(int dtype, long long rows, int n, int k) {
+  Carver cv(nullptr, 0);
+  cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
+  cv.take<float>(static_cast<size_t>(sum_slabs(rows, n)) * n);
+  return cv.used;
+}
+
+int linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n, int k, float *dw,
+                 float *dbias, void *ws, cudaStream_t s) {
+  Carver cv(ws, ~size_t(0));
+  void *parts = cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
+  const int slabs = sum_slabs(rows, n);
+  float *part = cv.take<float>(static_cast<size_t>(slabs) * n);
+  if (dbias) {
+    VAE_TRY(by_dtype(dtype, [&](auto t) -> int {
+      using D = decltype(t);
+      auto kernel = raw_wide<D>(n, dy) ? column_sums<D, true> : column_sums<D, false>;
+      kernel<<<dim3(ceil_div(n, 256), slabs), 256, 0, s>>>(static_cast<const D *>(dy), rows, n,
+                                                          slabs > 1 ? part : dbias);
+      VAE_LAUNCH_CHECK();
+      return VAE_OK;
+    }));
+    count_launches(1);
+    if (slabs > 1) {
+      VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, slabs, n, dbias));
+      count_launches(1);
+    }
+  }
+  GemmDesc d;
+  VAE_TRY(operands(&d, dtype, dy, rows * n, x, rows * k, parts, s));
+  d.dtype = VAE_F32;
+  d.a.k_major = d.b.k_major = false;
+  d.m = n;
+  d.n = k;
+  d.k = rows;
+  d.epi = {nullptr, nullptr, dw, nullptr, VAE_ACT_NONE, true};
+  return gemm(d, s);
+}
+
+}  // namespace vae

@@ -119,7 +119,8 @@ void count_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed);
 long long launch_count() { return g_launches.load(std::memory_order_relaxed); }
 
 int encode_tiled(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
-                 const uint64_t *strides_bytes, const uint32_t *box, bool swizzle128) {
+                 const uint64_t *strides_bytes, const uint32_t *box, bool swizzle128,
+                 CUtensorMapDataType type) {
   auto fn = encode_fn();
   if (!fn) return VAE_ECUDA;
   cuuint64_t gd[5], gs[4];
@@ -131,7 +132,7 @@ int encode_tiled(CUtensorMap *map, const void *base, int rank, const uint64_t *d
   }
   for (int i = 0; i + 1 < rank; ++i) gs[i] = strides_bytes[i];
   const CUresult r =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, static_cast<cuuint32_t>(rank),
+      fn(map, type, static_cast<cuuint32_t>(rank),
          const_cast<void *>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
          swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -549,6 +549,82 @@ VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void
                                     vae_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * A transformer block's MLP on token rows, forward and backward: layer norm, the
+ * matrix products with what follows them, dropout. Tokens, weights of the products
+ * and kept activations are of one vae_dtype a call; norm weights, biases and the
+ * gradients of every parameter are float32. Everything is computed in FP32 and
+ * rounded once, when it is stored. Sums have a fixed order: the same inputs give
+ * the same bits. Limits: rows <= 2^31 - 256. */
+typedef enum { VAE_F32 = 0, VAE_BF16 = 1, VAE_F16 = 2 } vae_dtype;
+/* z; z / (1 + e^-z); and z / (1 + e^-v), v = sqrt(8 / pi) (z + 0.044715 z^3), which
+ * is GELU in its tanh form */
+typedef enum { VAE_ACT_NONE = 0, VAE_ACT_SILU = 1, VAE_ACT_GELU = 2 } vae_act;
+
+/* vae_layer_norm -- per row of c: y = gamma (x - mean) rstd + beta with
+ * rstd = 1 / sqrt(var + eps), var biased.
+ *   x, y [rows][c]; gamma, beta [c], beta may be NULL (zeros); stats [rows][2]:
+ *   mean, rstd, or NULL (serving). y == x is allowed.
+ * vae_layer_norm_backward -- with xh = (x - mean) rstd (stats as saved) and
+ * t = gamma dy: dx = rstd (t - mean(t) - xh mean(t xh)) (+ dres),
+ * dgamma = sum dy xh, dbeta = sum dy over the rows.
+ *   dres, a gradient that reaches x by another way (the residual stream), may be
+ *   NULL, and so may dgamma and dbeta. dx may be dy, x or dres.
+ * Limits: c % 4 == 0, c <= 8192. */
+VAE_API int vae_layer_norm(const void *x, int dtype, long long rows, int c, float eps,
+                           const float *gamma, const float *beta, void *y, float *stats,
+                           vae_stream_t stream);
+VAE_API size_t vae_layer_norm_backward_workspace_size(long long rows, int c);
+VAE_API int vae_layer_norm_backward(const void *dy, const void *x, int dtype, const float *stats,
+                                    long long rows, int c, const float *gamma, const void *dres,
+                                    void *dx, float *dgamma, float *dbeta, void *ws,
+                                    size_t ws_bytes, vae_stream_t stream);
+
+/* vae_dropout -- y = x / q where an element is kept, 0 where it is dropped (+
+ * residual). The mask is not stored: the backward pass is the same call on the
+ * gradient of y, with the same p, seed and offset and no residual.
+ * Element i (of `count`, in memory order) takes 16 bits of a Philox 4x32-10 block
+ * (Salmon, Moraes, Dror, Shaw, 2011) with key `seed` (low word first) and the 64-bit
+ * counter offset + i / 8 (low word first, two words of zeros behind it): of the
+ * block's four words, word (i % 8) / 2, its low half for even i. It is dropped where
+ * those bits are below T = floor(65536 p + 1/2), and q = 1 - T / 65536. A call takes
+ * ceil(count / 8) counters; calls that should not share random numbers take
+ * offsets at least so far apart.
+ *   state: NULL, or two integers on the device (8-byte aligned): the seed, in the
+ *   place of `seed`, and a number that is added to `offset`, so that a captured
+ *   graph draws anew at every replay. 0 <= p <= 1. y may be x or residual. */
+VAE_API int vae_dropout(const void *x, int dtype, long long count, double p,
+                        unsigned long long seed, unsigned long long offset,
+                        const long long *state, const void *residual, void *y,
+                        vae_stream_t stream);
+
+/* vae_linear -- z = x w^T + bias, y = act(z) + residual.
+ *   x [rows][k], w [n][k], bias [n] or NULL, residual [rows][n] or NULL, y [rows][n];
+ *   z [rows][n] or NULL: what the gradient of act needs. y == residual is allowed.
+ * vae_linear_dgrad -- dx = (dy w) act'(z): the gradient of a layer's input x,
+ * carried through the activation that made x out of z.
+ *   dy [rows][n], w [n][k], dx [rows][k]; z [rows][k], NULL exactly when act is
+ *   VAE_ACT_NONE (dx = dy w). At an infinite z the derivative is its limit.
+ * vae_linear_wgrad -- dw[o][c] = sum over rows of dy[o] x[c], dbias[o] = sum of dy[o].
+ *   dy [rows][n], x [rows][k], dw [n][k] float32, dbias [n] float32 or NULL.
+ * 16-bit products are exact, their sums FP32. Floats enter the tensor cores as three
+ * bf16 parts each (all 24 bits), of whose products those below 2^-24 are left out;
+ * an infinity or a NaN among them makes the sums it enters NaN. A workspace size of
+ * 0 for valid sizes means that ws is not used and may be NULL.
+ * Limits: n % 8 == 0, k % 8 == 0, n, k <= 65536. */
+VAE_API size_t vae_linear_workspace_size(int dtype, long long rows, int n, int k);
+VAE_API int vae_linear(const void *x, int dtype, long long rows, int k, const void *w,
+                       const float *bias, int n, int act, const void *residual, void *y, void *z,
+                       void *ws, size_t ws_bytes, vae_stream_t stream);
+VAE_API size_t vae_linear_dgrad_workspace_size(int dtype, long long rows, int n, int k);
+VAE_API int vae_linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w,
+                             int k, int act, const void *z, void *dx, void *ws, size_t ws_bytes,
+                             vae_stream_t stream);
+VAE_API size_t vae_linear_wgrad_workspace_size(int dtype, long long rows, int n, int k);
+VAE_API int vae_linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n,
+                             int k, float *dw, float *dbias, void *ws, size_t ws_bytes,
+                             vae_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Step profiler of the chain: when enabled, vae_decode_chain brackets every
  * step (one conv, one GroupNorm+SiLU, the attention block, the latent
  * staging) with CUDA events on the caller's stream and stores the step's
