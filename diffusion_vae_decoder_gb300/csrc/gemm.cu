@@ -367,6 +367,323 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (splits > 1) cluster_sync();  // the others read this block's sums until here
 }
 
+// ------------------------------------------------------------------ large tiles
+// Two blocks on paired SMs share a 256 x 256 tile: each stages 128 rows of either
+// operand and holds 128 rows of sums, so that a stage brings 32 KB into an SM for 512
+// clocks of its tensor core (a tile of one SM's own would bring 48 KB for 128 x 256).
+// Persistent: a pair takes every (grid / 2)-th tile, and while eight warps of either
+// block finish a tile from one half of tensor memory, the next one's products go to
+// the other half.
+constexpr int kPairTile = 256;
+constexpr int kPairStages = 5;
+constexpr int kPairThreads = 320;
+constexpr int kPairStageBytes = 2 * 128 * kBK * 2;
+constexpr int kPairWarps = 8;
+constexpr int kStaging = 2 * 32 * 128;  // a warp's two buffers of 32 rows of 128 bytes
+constexpr size_t kPairSmem =
+    kPairStages * kPairStageBytes + kPairWarps * kStaging + 1024 + 256;
+static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
+
+// 16-byte piece `c` of row `r` of a staging buffer: rows shift by a piece, so that
+// neither a thread's walk along its row nor a warp's along rows meets in a bank.
+__device__ __forceinline__ uint4 *piece(uint8_t *buf, int r, int c) {
+  return reinterpret_cast<uint4 *>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+}
+// Numbers in 16 bytes, as pairs of floats.
+template <class T>
+struct Piece {
+  uint64_t v[8 / sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ Piece<T> piece_of(uint4 u) {
+  if constexpr (sizeof(T) == 4)
+    return {{u.x | static_cast<uint64_t>(u.y) << 32, u.z | static_cast<uint64_t>(u.w) << 32}};
+  else
+    return {{unpack2(u.x, T{}), unpack2(u.y, T{}), unpack2(u.z, T{}), unpack2(u.w, T{})}};
+}
+template <class T>
+__device__ __forceinline__ uint4 bits_of(const Piece<T> &p) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(static_cast<uint32_t>(p.v[0]), static_cast<uint32_t>(p.v[0] >> 32),
+                      static_cast<uint32_t>(p.v[1]), static_cast<uint32_t>(p.v[1] >> 32));
+  else
+    return make_uint4(pack2(lo2(p.v[0]), hi2(p.v[0]), T{}), pack2(lo2(p.v[1]), hi2(p.v[1]), T{}),
+                      pack2(lo2(p.v[2]), hi2(p.v[2]), T{}), pack2(lo2(p.v[3]), hi2(p.v[3]), T{}));
+}
+
+// A warp's 32 rows x (128 / sizeof(T)) columns of sums at (row, col), a row a thread,
+// finished and stored. Global memory is read and written in whole 128-byte rows.
+template <class T>
+struct Emitter {
+  static constexpr int kCols = 128 / sizeof(T), kPer = 16 / sizeof(T);  // of a row, of a piece
+  const Params &p;
+  uint8_t *buf;  // kStaging bytes: out (aux before it) and z
+  int lane;
+
+  // The piece of a row-major array that this lane carries in step i; NULL outside.
+  template <class P>
+  __device__ __forceinline__ P *at(P *base, long long row, int col, int i) const {
+    const long long r = row + 4 * i + (lane >> 3);
+    const int c = col + (lane & 7) * kPer;
+    return r < p.m && c < p.n ? base + r * p.n + c : nullptr;
+  }
+  __device__ __forceinline__ uint4 *mine(uint8_t *b, int i) const {
+    return piece(b, 4 * i + (lane >> 3), lane & 7);
+  }
+  __device__ __forceinline__ uint4 fetch(long long row, int col, int i) const {
+    const T *a = at(static_cast<const T *>(p.e.aux), row, col, i);
+    return a ? *reinterpret_cast<const uint4 *>(a) : make_uint4(0, 0, 0, 0);
+  }
+  // 16-bit numbers: pieces c0 .. c0 + N - 1 of the thread's row, of sums v.
+  template <int N>
+  __device__ __forceinline__ void finish(const float *v, int col, int c0) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i;
+      Piece<T> a, o, z;
+      if (p.e.aux) a = piece_of<T>(*piece(buf, lane, c));
+#pragma unroll
+      for (int j = 0; j < kPer / 2; ++j) {
+        const int ch = col + c * kPer + 2 * j;
+        uint64_t bias = 0;
+        if (p.e.bias && ch < p.n) bias = __ldg(reinterpret_cast<const unsigned long long *>(p.e.bias + ch));
+        z.v[j] = 0;
+        o.v[j] = finish2<false>(p.e, pk2(v[i * kPer + 2 * j], v[i * kPer + 2 * j + 1]),
+                                         bias, p.e.aux ? a.v[j] : 0, &z.v[j]);
+      }
+      *piece(buf, lane, c) = bits_of<T>(o);
+      if (p.e.keep) *piece(buf + kStaging / 2, lane, c) = bits_of<T>(z);
+    }
+  }
+  // Floats whose sums lie in the buffer.
+  __device__ __forceinline__ void finish_rows(long long row, int col) const {
+    const int ch = col + (lane & 7) * 4;
+    Quad bias = {{0, 0}};
+    if (p.e.bias && ch < p.n) bias = load_quad(p.e.bias + ch);
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      float *o = at(static_cast<float *>(p.e.out), row, col, i);
+      if (!o) continue;
+      const size_t off = o - static_cast<float *>(p.e.out);
+      const Piece<float> sum = piece_of<float>(*mine(buf, i));
+      Quad a = {{0, 0}}, z = {{0, 0}}, y;
+      if (p.e.aux) a = load_quad(static_cast<const float *>(p.e.aux) + off);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        y.v[j] = finish2<true>(p.e, sum.v[j], bias.v[j], a.v[j], &z.v[j]);
+      store_quad(o, y);
+      if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + off, z);
+    }
+  }
+  __device__ __forceinline__ void store(void *dst, uint8_t *from, long long row, int col) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      T *d = at(static_cast<T *>(dst), row, col, i);
+      if (d) *reinterpret_cast<uint4 *>(d) = *mine(from, i);
+    }
+  }
+  __device__ __forceinline__ void flush(long long row, int col) const {
+    __syncwarp();
+    store(p.e.out, buf, row, col);
+    if (p.e.keep) store(p.e.keep, buf + kStaging / 2, row, col);
+    __syncwarp();
+  }
+};
+
+template <class Out>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+              const Params p) {
+  constexpr bool kFloat = sizeof(Out) == 4;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *staging = smem + kPairStages * kPairStageBytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kPairWarps * kStaging);
+  uint64_t *empty = full + kPairStages;
+  uint64_t *acc_full = empty + kPairStages, *acc_empty = acc_full + 2;
+  uint64_t *drain = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile uint32_t *abort = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int tiles = p.m_tiles * p.n_tiles, stride = gridDim.x / 2;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tb);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 2 * kPairWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbarrier_init();
+    *abort = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (p.wait) grid_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      long long i = 0;  // stages, over all tiles
+      bool ok = true;
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+        const int m0 = t / p.n_tiles * kPairTile + 128 * rank;
+        const int n0 = t % p.n_tiles * kPairTile + 128 * rank;
+        for (int it = 0; it < p.its; ++it, ++i) {
+          const int s = static_cast<int>(i % kPairStages);
+          ok = mbar_wait_cluster(empty + s, (i / kPairStages & 1) ^ 1, abort, p.wait_ns);
+          if (!ok) {
+            raise_error(p, abort);
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kPairStageBytes);
+          const uint32_t bar = mapa_rank(full + s, 0);
+          uint8_t *a = smem + s * kPairStageBytes;
+          load_stage<128, 128>(&ta, &tb, p, it, m0, n0, a, a + kPairStageBytes / 2,
+                               [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                                 tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+                               });
+        }
+      }
+      // what was asked for lands before the pair leaves (both blocks' copies count on
+      // the leader's barriers, and the other block waits for the leader at the end)
+      if (*abort && rank == 0)
+        for (long long j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
+          drain_wait(full + j % kPairStages, j / kPairStages & 1, p.wait_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      long long i = 0;
+      int c = 0;  // accumulators taken
+      bool ok = true;
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+        for (int it = 0; it < p.its; ++it, ++i) {
+          const bool first = kFloat ? it % kChain == 0 : it == 0;
+          const bool last = it == p.its - 1 || (kFloat && it % kChain == kChain - 1);
+          const int s = static_cast<int>(i % kPairStages);
+          if (first)
+            ok = mbar_wait_cluster(acc_empty + (c & 1), (c >> 1 & 1) ^ 1, abort, p.wait_ns);
+          ok = ok && mbar_wait_cluster(full + s, i / kPairStages & 1, abort, p.wait_ns);
+          if (!ok) {
+            raise_error(p, abort);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * kPairStageBytes);
+          multiply_stage<true>(p, sa, sa + kPairStageBytes / 2, tmem + (c & 1) * kPairTile, first);
+          umma_commit_pair(empty + s, 3);
+          if (last) umma_commit_pair(acc_full + (c++ & 1), 3);
+        }
+      }
+      umma_commit_pair(drain, 1);
+      drain_wait(drain, 0, p.wait_ns);
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t at = tmem + (static_cast<uint32_t>(q) << 21) + 128 * half;
+    const Emitter<Out> out{p, staging + (warp - 2) * kStaging, lane};
+    constexpr int kCols = Emitter<Out>::kCols;
+    int c = 0;  // accumulators taken
+    auto taken = [&](int b) -> bool {
+      bool ok = mbar_wait_cluster(acc_full + (b & 1), b >> 1 & 1, abort, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) raise_error(p, abort);
+      tc_fence_after();
+      return ok;
+    };
+    auto give_back = [&](int b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_rank(acc_empty + (b & 1), 0));
+    };
+    bool ok = true;
+    for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+      const long long row = static_cast<long long>(t / p.n_tiles) * kPairTile + 128 * rank + 32 * q;
+      const int col = t % p.n_tiles * kPairTile + 128 * half;
+      if constexpr (kFloat) {
+        float acc[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+        const int chunks = (p.its + kChain - 1) / kChain;
+        for (int k = 0; k < chunks && ok; ++k, ++c) {
+          ok = taken(c);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 128; j += 16) {
+            float v[16];
+            tmem_ld_16cols(at + (c & 1) * kPairTile + j, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[j + e] += v[e];
+          }
+          give_back(c);
+        }
+        if (!ok) break;
+        // 32 columns at a time: the sums through shared memory, then a lane finishes
+        // four columns of every fourth row, as global memory is read and written
+#pragma unroll
+        for (int j = 0; j < 128; j += kCols) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *piece(out.buf, lane, e) = make_uint4(
+                __float_as_uint(acc[j + 4 * e]), __float_as_uint(acc[j + 4 * e + 1]),
+                __float_as_uint(acc[j + 4 * e + 2]), __float_as_uint(acc[j + 4 * e + 3]));
+          __syncwarp();
+          out.finish_rows(row, col + j);
+          __syncwarp();
+        }
+      } else {
+        uint4 aux[8];
+        auto fetch = [&](int j) {
+          if (p.e.aux) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) aux[i] = out.fetch(row, col + j, i);
+          }
+        };
+        fetch(0);  // on its way while the tile is multiplied
+        ok = taken(c);
+        if (!ok) break;
+#pragma unroll 1
+        for (int j = 0; j < 128; j += kCols) {
+          if (p.e.aux) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *out.mine(out.buf, i) = aux[i];
+            __syncwarp();
+            if (j == 0) fetch(kCols);
+          }
+#pragma unroll 1
+          for (int e = 0; e < kCols; e += 32) {
+            float v[32];
+            tmem_ld_32cols(at + (c & 1) * kPairTile + j + e, v);
+            if (j + e + 32 == 128) give_back(c);
+            out.template finish<4>(v, col + j, e / 8);
+          }
+          out.flush(row, col + j);
+        }
+        ++c;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither block leaves while the pair's products, copies or arrivals touch it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ------------------------------------------------------------------ host
 // A map of `parts` matrices [rows][cols] of 16-bit numbers, in boxes of 64 by box_rows.
 int encode_operand(CUtensorMap *map, const void *p, int parts, long long rows, long long cols,
@@ -413,6 +730,46 @@ cudaLaunchConfig_t launch_config(cudaLaunchAttribute *attr, unsigned grid, int t
   return cfg;
 }
 
+int tile_splits(long long tiles, int its) {
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= num_sms() && its >= 4 * splits) splits *= 2;
+  return splits;
+}
+
+// Whether 256 x 256 tiles on pairs of SMs finish before 128 x 128 ones: rounds of
+// tiles times stages times the clocks of a stage.
+bool takes_pairs(long long m, int n, int its) {
+  const long long small = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
+  const long long large = static_cast<long long>(ceil_div(m, kPairTile)) * ceil_div(n, kPairTile);
+  const int s = tile_splits(small, its), sms = num_sms();
+  if (sms < 2 || large > 0x3fffffff) return false;
+  const long long t_small = (small * s + sms - 1) / sms * (4000 + 512ll * ((its + s - 1) / s));
+  const long long t_large = 3000 + (large + sms / 2 - 1) / (sms / 2) * (1000 + 600ll * its);
+  return t_large < t_small;
+}
+
+int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
+  CUtensorMap ta, tb;
+  VAE_TRY(d.a.k_major ? encode_operand(&ta, d.a.p, d.parts, d.m, d.k, 128)
+                      : encode_operand(&ta, d.a.p, d.parts, d.k, d.m, kBK));
+  VAE_TRY(d.b.k_major ? encode_operand(&tb, d.b.p, d.parts, d.n, d.k, 128)
+                      : encode_operand(&tb, d.b.p, d.parts, d.k, d.n, kBK));
+  p.idesc = idesc_16bit(kPairTile, kPairTile, !d.f16, !d.a.k_major, !d.b.k_major);
+  p.m_tiles = ceil_div(d.m, kPairTile);
+  p.n_tiles = ceil_div(d.n, kPairTile);
+  const unsigned grid = 2 * std::min(p.m_tiles * p.n_tiles, num_sms() / 2);
+  return by_dtype(d.dtype, [&](auto o) -> int {
+    using Out = decltype(o);
+    static std::atomic<uint64_t> done{0};
+    VAE_CUDA_TRY(allow_smem(gemm_pair<Out>, kPairSmem, &done));
+    cudaLaunchAttribute attr[2];
+    const auto cfg = launch_config(attr, grid, kPairThreads, kPairSmem, 2, p.wait, s);
+    VAE_CUDA_TRY(cudaLaunchKernelEx(&cfg, gemm_pair<Out>, ta, tb, p));
+    count_launches(1);
+    return VAE_OK;
+  });
+}
+
 int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
   CUtensorMap ta, tb;
   VAE_TRY(d.a.k_major ? encode_operand(&ta, d.a.p, d.parts, d.m, d.k, kTile)
@@ -423,8 +780,7 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
   p.m_tiles = ceil_div(d.m, kTile);
   p.n_tiles = ceil_div(d.n, kTile);
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= num_sms() && p.its >= 4 * splits) splits *= 2;
+  const int splits = tile_splits(tiles, p.its);
   if (tiles * splits > 0x7fffffff) return VAE_EUNSUPPORTED;
   return by_dtype(d.dtype, [&](auto o) -> int {
     using Out = decltype(o);
@@ -447,7 +803,7 @@ int gemm(const GemmDesc &d, cudaStream_t s) {
   p.n = d.n;
   p.pairs = d.parts > 1 ? 6 : 1;
   const long long its = (d.k + kBK - 1) / kBK * p.pairs;
-  if (its > 0x7fffffff || d.m > 0x7fffffff - kTile) return VAE_EUNSUPPORTED;
+  if (its > 0x7fffffff || d.m > 0x7fffffff - kPairTile) return VAE_EUNSUPPORTED;
   p.its = static_cast<int>(its);
   p.a_k = d.a.k_major;
   p.b_k = d.b.k_major;
@@ -456,7 +812,7 @@ int gemm(const GemmDesc &d, cudaStream_t s) {
   p.err = device_error_word();
   if (!p.err) return VAE_ECUDA;
   p.e = d.epi;
-  return launch_tile(d, p, s);
+  return takes_pairs(d.m, d.n, p.its) ? launch_pair(d, p, s) : launch_tile(d, p, s);
 }
 
 }  // namespace vae

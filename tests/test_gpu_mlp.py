@@ -260,7 +260,8 @@ def test_dropout_state_moves_between_replays(vae):
 # type: the operators have to agree to the last bit at every size.
 LINEAR_SIZES = [(1, 8, 8), (1, 264, 512), (2, 512, 264), (3, 2048, 128), (5, 64, 40), (8, 72, 1000),
                 (9, 520, 72), (127, 128, 128), (128, 136, 64), (129, 264, 200), (257, 120, 520),
-                (1000, 1032, 72), (300, 512, 2056), (4575, 256, 128), (2049, 2048, 520)]
+                (1000, 1032, 72), (300, 512, 2056), (4575, 256, 128), (2049, 2048, 520),
+                (1000, 2056, 2048), (4100, 1032, 2048)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -353,7 +354,7 @@ def test_linear(vae, rows, n, k, act, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("rows,n,k", [(1, 264, 512), (200, 136, 520), (2294, 264, 520),
-                                      (700, 512, 2048)])
+                                      (700, 512, 2048), (4100, 264, 2048)])
 def test_linear_dgrad(vae, rows, n, k, act, dtype):
     t = R.DTYPES[dtype]
     dy, w = rand(1, rows, n, dtype=t, std=0.1), rand(2, n, k, dtype=t, std=k ** -0.5)
@@ -375,7 +376,7 @@ def test_linear_dgrad(vae, rows, n, k, act, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,n,k", [(1, 64, 72), (77, 136, 520), (4575, 256, 128),
-                                      (20000, 512, 264)])
+                                      (20000, 512, 264), (3000, 2048, 2056)])
 def test_linear_wgrad(vae, rows, n, k, dtype):
     t = R.DTYPES[dtype]
     dy, x = rand(1, rows, n, dtype=t, std=0.1), rand(2, rows, k, dtype=t)
