@@ -56,37 +56,72 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
 __device__ __forceinline__ int part_a(int q) { return (0x201100 >> (4 * q)) & 15; }
 __device__ __forceinline__ int part_b(int q) { return (0x021010 >> (4 * q)) & 15; }
 
-// v of act(z) = z sigmoid(v), and dv / dz.
-__device__ __forceinline__ uint64_t gate2(uint64_t z, int act, uint64_t *slope) {
-  if (act == VAE_ACT_SILU) {
-    *slope = pk2(1.f, 1.f);
-    return z;
+// max and min that give a NaN for one.
+__device__ __forceinline__ uint64_t at_least2(uint64_t z, float low) {
+  float a, b;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(lo2(z)), "f"(low));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(hi2(z)), "f"(low));
+  return pk2(a, b);
+}
+__device__ __forceinline__ uint64_t at_most2(uint64_t z, float high) {
+  float a, b;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(lo2(z)), "f"(high));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(hi2(z)), "f"(high));
+  return pk2(a, b);
+}
+
+// The activations are z sigmoid(v), v = z for SiLU and z (a + b z^2) for GELU in its
+// tanh form, a = sqrt(8 / pi), b = 0.044715 a. Beyond kFar both they and their
+// derivatives are, to far below float's resolution, what they are there on the
+// negative side (sigmoid 1e-38), and z and 1 on the positive one; z is held inside,
+// so that no power of it and no exponential overflows. A NaN stays one.
+constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.071354816f;
+__device__ __forceinline__ float far_of(int act) { return act == VAE_ACT_SILU ? 87.f : 10.f; }
+// s = 1 / (1 + e) with e = e^-v, for v >= -87.4. PRECISE: to about 2^-22, with two
+// special-function operations a number (t is the rounded product with log2 e, whose
+// residual w is put back). Else s to 2^-17, where a 16-bit result's rounding is 2^-9
+// or 2^-12, with one: the reciprocal by two Newton steps r <- r (2 - d r) from an
+// integer seed off by at most 5.1 % for d >= 1. The special-function unit takes a warp
+// eight clocks, and two operations a number would be all the 4096 clocks that the
+// tensor core spends on a 256 x 256 tile of 512 products.
+template <bool PRECISE>
+__device__ __forceinline__ uint64_t sigmoid_of(uint64_t v, uint64_t *e) {
+  const uint64_t t = mul2(v, pk2(-1.4426950408889634f, -1.4426950408889634f));
+  const uint64_t one = pk2(1.f, 1.f), m1 = pk2(-1.f, -1.f);
+  *e = pk2(ex2_approx(lo2(t)), ex2_approx(hi2(t)));
+  if constexpr (PRECISE) {
+    const uint64_t w = fma2(t, pk2(0.6931471805599453f, 0.6931471805599453f), v);
+    *e = fma2(mul2(*e, w), m1, *e);
+    return rcp2(add2(*e, one));
+  } else {
+    const uint64_t nd = fma2(*e, m1, m1);  // -d
+    uint64_t r = static_cast<uint64_t>(0xfef30000u - static_cast<uint32_t>(nd)) |
+                 static_cast<uint64_t>(0xfef30000u - static_cast<uint32_t>(nd >> 32)) << 32;
+    r = fma2(r, fma2(nd, r, one), r);
+    return fma2(r, fma2(nd, r, one), r);
   }
-  // gelu: sqrt(8 / pi) (z + 0.044715 z^3)
-  const float a = 1.5957691216057308f, b = 0.044715f;
-  const uint64_t q = mul2(z, z);
-  *slope = fma2(q, pk2(3.f * a * b, 3.f * a * b), pk2(a, a));
-  return mul2(z, fma2(q, pk2(a * b, a * b), pk2(a, a)));
 }
 template <bool PRECISE>
 __device__ __forceinline__ uint64_t act2(uint64_t z, int act) {
   if (act == VAE_ACT_NONE) return z;
-  uint64_t slope;
-  const uint64_t v = gate2(z, act, &slope);
-  return mul2(z, PRECISE ? sigmoid2_precise(v) : sigmoid2(v));
+  const uint64_t h = at_least2(z, -far_of(act));
+  uint64_t v = h, e;
+  if (act == VAE_ACT_GELU)
+    v = mul2(h, fma2(mul2(h, h), pk2(kGeluB, kGeluB), pk2(kGeluA, kGeluA)));
+  return mul2(h, sigmoid_of<PRECISE>(v, &e));
 }
-// act'(z) = s + z slope s (1 - s). Beyond +-32 the derivative is 1 or 0 to far below
-// float's resolution, and the products there would overflow: z is held there
-// (comparisons that leave a NaN).
-__device__ __forceinline__ float held(float z) { return z > 32.f ? 32.f : z < -32.f ? -32.f : z; }
+// act'(z) = s + z v' s (1 - s), with 1 - s = e s, which loses nothing where s is near 1.
 template <bool PRECISE>
 __device__ __forceinline__ uint64_t act_slope2(uint64_t z, int act) {
-  z = pk2(held(lo2(z)), held(hi2(z)));
-  uint64_t slope;
-  const uint64_t v = gate2(z, act, &slope);
-  const uint64_t s = PRECISE ? sigmoid2_precise(v) : sigmoid2(v);
-  const uint64_t rest = fma2(s, pk2(-1.f, -1.f), pk2(1.f, 1.f));
-  return fma2(mul2(mul2(z, slope), s), rest, s);
+  const uint64_t h = at_most2(at_least2(z, -far_of(act)), far_of(act));
+  uint64_t v = h, w = h, e;  // w = z v'
+  if (act == VAE_ACT_GELU) {
+    const uint64_t q = mul2(h, h), a = pk2(kGeluA, kGeluA);
+    v = mul2(h, fma2(q, pk2(kGeluB, kGeluB), a));
+    w = mul2(h, fma2(q, pk2(3.f * kGeluB, 3.f * kGeluB), a));
+  }
+  const uint64_t s = sigmoid_of<PRECISE>(v, &e);
+  return mul2(s, fma2(w, mul2(e, s), pk2(1.f, 1.f)));
 }
 
 // Two neighbouring sums of a row -> out, and z where it is kept.
@@ -379,131 +414,94 @@ constexpr int kPairStages = 5;
 constexpr int kPairThreads = 320;
 constexpr int kPairStageBytes = 2 * 128 * kBK * 2;
 constexpr int kPairWarps = 8;
-constexpr int kStaging = 2 * 32 * 128;  // a warp's two buffers of 32 rows of 128 bytes
+constexpr int kChunk = 32;              // columns that a warp finishes at a time
+constexpr int kChunkBytes = 32 * 64;    // of 16-bit numbers
+constexpr int kStaging = 4 * kChunkBytes;  // a warp's
 constexpr size_t kPairSmem =
-    kPairStages * kPairStageBytes + kPairWarps * kStaging + 1024 + 256;
+    kPairStages * kPairStageBytes + kPairWarps * (kStaging + kChunk * 4) + 1024 + 512;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
 
-// 16-byte piece `c` of row `r` of a staging buffer: rows shift by a piece, so that
-// neither a thread's walk along its row nor a warp's along rows meets in a bank.
-__device__ __forceinline__ uint4 *piece(uint8_t *buf, int r, int c) {
+// 16-byte piece `c` of row `r` in a buffer of 64-byte rows with TMA's 64-byte swizzle:
+// eight threads' pieces of eight rows lie in different banks.
+__device__ __forceinline__ uint4 *piece64(uint8_t *buf, int r, int c) {
+  return reinterpret_cast<uint4 *>(buf + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+}
+// The same for rows of 128 bytes.
+__device__ __forceinline__ uint4 *piece128(uint8_t *buf, int r, int c) {
   return reinterpret_cast<uint4 *>(buf + r * 128 + ((c ^ (r & 7)) << 4));
 }
-// Numbers in 16 bytes, as pairs of floats.
-template <class T>
-struct Piece {
-  uint64_t v[8 / sizeof(T)];
-};
-template <class T>
-__device__ __forceinline__ Piece<T> piece_of(uint4 u) {
-  if constexpr (sizeof(T) == 4)
-    return {{u.x | static_cast<uint64_t>(u.y) << 32, u.z | static_cast<uint64_t>(u.w) << 32}};
-  else
-    return {{unpack2(u.x, T{}), unpack2(u.y, T{}), unpack2(u.z, T{}), unpack2(u.w, T{})}};
-}
-template <class T>
-__device__ __forceinline__ uint4 bits_of(const Piece<T> &p) {
-  if constexpr (sizeof(T) == 4)
-    return make_uint4(static_cast<uint32_t>(p.v[0]), static_cast<uint32_t>(p.v[0] >> 32),
-                      static_cast<uint32_t>(p.v[1]), static_cast<uint32_t>(p.v[1] >> 32));
-  else
-    return make_uint4(pack2(lo2(p.v[0]), hi2(p.v[0]), T{}), pack2(lo2(p.v[1]), hi2(p.v[1]), T{}),
-                      pack2(lo2(p.v[2]), hi2(p.v[2]), T{}), pack2(lo2(p.v[3]), hi2(p.v[3]), T{}));
-}
 
-// A warp's 32 rows x (128 / sizeof(T)) columns of sums at (row, col), a row a thread,
-// finished and stored. Global memory is read and written in whole 128-byte rows.
-template <class T>
-struct Emitter {
-  static constexpr int kCols = 128 / sizeof(T), kPer = 16 / sizeof(T);  // of a row, of a piece
-  const Params &p;
-  uint8_t *buf;  // kStaging bytes: out (aux before it) and z
-  int lane;
-
-  // The piece of a row-major array that this lane carries in step i; NULL outside.
-  template <class P>
-  __device__ __forceinline__ P *at(P *base, long long row, int col, int i) const {
-    const long long r = row + 4 * i + (lane >> 3);
-    const int c = col + (lane & 7) * kPer;
-    return r < p.m && c < p.n ? base + r * p.n + c : nullptr;
-  }
-  __device__ __forceinline__ uint4 *mine(uint8_t *b, int i) const {
-    return piece(b, 4 * i + (lane >> 3), lane & 7);
-  }
-  __device__ __forceinline__ uint4 fetch(long long row, int col, int i) const {
-    const T *a = at(static_cast<const T *>(p.e.aux), row, col, i);
-    return a ? *reinterpret_cast<const uint4 *>(a) : make_uint4(0, 0, 0, 0);
-  }
-  // 16-bit numbers: pieces c0 .. c0 + N - 1 of the thread's row, of sums v.
-  template <int N>
-  __device__ __forceinline__ void finish(const float *v, int col, int c0) const {
+// A warp's 32 rows x 32 columns of floats at (row, col), a row a thread: the sums go
+// through shared memory (`buf`, 4 KB), then a lane finishes four columns of every
+// fourth row, as global memory is read and written.
+__device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int lane,
+                                              const float *sum, long long row, int col) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = c0 + i;
-      Piece<T> a, o, z;
-      if (p.e.aux) a = piece_of<T>(*piece(buf, lane, c));
-#pragma unroll
-      for (int j = 0; j < kPer / 2; ++j) {
-        const int ch = col + c * kPer + 2 * j;
-        uint64_t bias = 0;
-        if (p.e.bias && ch < p.n) bias = __ldg(reinterpret_cast<const unsigned long long *>(p.e.bias + ch));
-        z.v[j] = 0;
-        o.v[j] = finish2<false>(p.e, pk2(v[i * kPer + 2 * j], v[i * kPer + 2 * j + 1]),
-                                         bias, p.e.aux ? a.v[j] : 0, &z.v[j]);
-      }
-      *piece(buf, lane, c) = bits_of<T>(o);
-      if (p.e.keep) *piece(buf + kStaging / 2, lane, c) = bits_of<T>(z);
-    }
-  }
-  // Floats whose sums lie in the buffer.
-  __device__ __forceinline__ void finish_rows(long long row, int col) const {
-    const int ch = col + (lane & 7) * 4;
-    Quad bias = {{0, 0}};
-    if (p.e.bias && ch < p.n) bias = load_quad(p.e.bias + ch);
+  for (int e = 0; e < 8; ++e)
+    *piece128(buf, lane, e) =
+        make_uint4(__float_as_uint(sum[4 * e]), __float_as_uint(sum[4 * e + 1]),
+                   __float_as_uint(sum[4 * e + 2]), __float_as_uint(sum[4 * e + 3]));
+  __syncwarp();
+  const int ch = col + (lane & 7) * 4;
+  Quad bias = {{0, 0}};
+  if (p.e.bias && ch < p.n) bias = load_quad(p.e.bias + ch);
 #pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      float *o = at(static_cast<float *>(p.e.out), row, col, i);
-      if (!o) continue;
-      const size_t off = o - static_cast<float *>(p.e.out);
-      const Piece<float> sum = piece_of<float>(*mine(buf, i));
-      Quad a = {{0, 0}}, z = {{0, 0}}, y;
-      if (p.e.aux) a = load_quad(static_cast<const float *>(p.e.aux) + off);
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (row + r >= p.m || ch >= p.n) continue;
+    const size_t at = static_cast<size_t>(row + r) * p.n + ch;
+    const Quad v = load_quad(reinterpret_cast<const float *>(piece128(buf, r, lane & 7)));
+    Quad a = {{0, 0}}, z = {{0, 0}}, y;
+    if (p.e.aux) a = load_quad(static_cast<const float *>(p.e.aux) + at);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        y.v[j] = finish2<true>(p.e, sum.v[j], bias.v[j], a.v[j], &z.v[j]);
-      store_quad(o, y);
-      if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + off, z);
-    }
+    for (int j = 0; j < 2; ++j) y.v[j] = finish2<true>(p.e, v.v[j], bias.v[j], a.v[j], &z.v[j]);
+    store_quad(static_cast<float *>(p.e.out) + at, y);
+    if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + at, z);
   }
-  __device__ __forceinline__ void store(void *dst, uint8_t *from, long long row, int col) const {
+  __syncwarp();
+}
+
+// 32 columns of a thread's row in 16-bit numbers: aux (read from `buf` where there is
+// one) and the sums make out, in its place, and z in `zbuf` where it is kept. `bias`:
+// the columns', in shared memory.
+template <class T>
+__device__ __forceinline__ void finish_row(const Params &p, uint8_t *buf, uint8_t *zbuf, int lane,
+                                           const float *sum, const float4 *bias_row) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      T *d = at(static_cast<T *>(dst), row, col, i);
-      if (d) *reinterpret_cast<uint4 *>(d) = *mine(from, i);
+  for (int c = 0; c < 4; ++c) {
+    Oct a = {{0, 0, 0, 0}}, bias = a, o, z = a;
+    if (p.e.bias) bias = oct_of(bias_row[2 * c], bias_row[2 * c + 1]);
+    if (p.e.aux) {
+      Raw<T> r;
+      r.v[0] = *piece64(buf, lane, c);
+      a = oct_of(r);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o.v[j] = finish2<false>(p.e, pk2(sum[8 * c + 2 * j], sum[8 * c + 2 * j + 1]), bias.v[j],
+                              a.v[j], &z.v[j]);
+    *piece64(buf, lane, c) = raw_of<T>(o).v[0];
+    if (p.e.keep) *piece64(zbuf, lane, c) = raw_of<T>(z).v[0];
   }
-  __device__ __forceinline__ void flush(long long row, int col) const {
-    __syncwarp();
-    store(p.e.out, buf, row, col);
-    if (p.e.keep) store(p.e.keep, buf + kStaging / 2, row, col);
-    __syncwarp();
-  }
-};
+}
 
 template <class Out>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-              const Params p) {
+              const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tz,
+              const __grid_constant__ CUtensorMap tx, const Params p) {
   constexpr bool kFloat = sizeof(Out) == 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *staging = smem + kPairStages * kPairStageBytes;
-  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kPairWarps * kStaging);
+  float *bias_rows = reinterpret_cast<float *>(staging + kPairWarps * kStaging);
+  uint64_t *full = reinterpret_cast<uint64_t *>(bias_rows + kPairWarps * kChunk);
   uint64_t *empty = full + kPairStages;
   uint64_t *acc_full = empty + kPairStages, *acc_empty = acc_full + 2;
   uint64_t *drain = acc_empty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *aux_full = drain + 1;  // four of each finishing warp's
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(aux_full + 4 * kPairWarps);
   volatile uint32_t *abort = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -520,6 +518,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(acc_empty + i, 2 * kPairWarps);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 4 * kPairWarps; ++i) mbar_init(aux_full + i, 1);
     fence_mbarrier_init();
     *abort = 0;
   }
@@ -593,8 +592,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t at = tmem + (static_cast<uint32_t>(q) << 21) + 128 * half;
-    const Emitter<Out> out{p, staging + (warp - 2) * kStaging, lane};
-    constexpr int kCols = Emitter<Out>::kCols;
     int c = 0;  // accumulators taken
     auto taken = [&](int b) -> bool {
       bool ok = mbar_wait_cluster(acc_full + (b & 1), b >> 1 & 1, abort, p.wait_ns);
@@ -608,6 +605,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_rank(acc_empty + (b & 1), 0));
     };
+    uint8_t *buf = staging + (warp - 2) * kStaging;
+    // 16-bit results: chunk g of the warp's (four a tile) uses buffer g % ring for aux
+    // and out; where z is kept, two of the four buffers are z's. aux is asked for
+    // ring - 1 chunks ahead, over the tiles' ends.
+    uint64_t *aux = aux_full + 4 * (warp - 2);
+    const int ring = p.e.keep ? 2 : 4;
+    int g = 0, asked = 0;
+    auto ask = [&](int k) {
+      const int t = blockIdx.x / 2 + (k >> 2) * stride;
+      if (t >= tiles) return;
+      uint64_t *bar = aux + k % ring;
+      mbar_arrive_expect_tx(bar, kChunkBytes);
+      tma_load_2d(buf + k % ring * kChunkBytes, &tx, bar,
+                  t % p.n_tiles * kPairTile + 128 * half + (k & 3) * kChunk,
+                  t / p.n_tiles * kPairTile + 128 * static_cast<int>(rank) + 32 * q);
+      asked = k + 1;
+    };
+    float *bias_row = bias_rows + kChunk * (warp - 2);
+    auto bias_at = [&](int col) -> float {
+      return p.e.bias && col + lane < p.n ? __ldg(p.e.bias + col + lane) : 0.f;
+    };
+    if (!kFloat && p.e.aux && lane == 0)
+      for (int k = 0; k < ring - 1; ++k) ask(k);
     bool ok = true;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
       const long long row = static_cast<long long>(t / p.n_tiles) * kPairTile + 128 * rank + 32 * q;
@@ -630,49 +650,62 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           give_back(c);
         }
         if (!ok) break;
-        // 32 columns at a time: the sums through shared memory, then a lane finishes
-        // four columns of every fourth row, as global memory is read and written
 #pragma unroll
-        for (int j = 0; j < 128; j += kCols) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *piece(out.buf, lane, e) = make_uint4(
-                __float_as_uint(acc[j + 4 * e]), __float_as_uint(acc[j + 4 * e + 1]),
-                __float_as_uint(acc[j + 4 * e + 2]), __float_as_uint(acc[j + 4 * e + 3]));
-          __syncwarp();
-          out.finish_rows(row, col + j);
-          __syncwarp();
-        }
+        for (int j = 0; j < 128; j += kChunk)
+          finish_floats(p, buf, lane, acc + j, row, col + j);
       } else {
-        uint4 aux[8];
-        auto fetch = [&](int j) {
-          if (p.e.aux) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) aux[i] = out.fetch(row, col + j, i);
-          }
-        };
-        fetch(0);  // on its way while the tile is multiplied
+        // a chunk's bias is asked for a chunk ahead: from L2 it takes longer than the rest
+        float bias = bias_at(col);
         ok = taken(c);
         if (!ok) break;
 #pragma unroll 1
-        for (int j = 0; j < 128; j += kCols) {
+        for (int j = 0; j < 4; ++j, ++g) {
+          uint8_t *mine = buf + g % ring * kChunkBytes;
+          uint8_t *zbuf = buf + (2 + (g & 1)) * kChunkBytes;
+          float v[kChunk];
+          tmem_ld_32cols(at + (c & 1) * kPairTile + j * kChunk, v);
+          if (j == 3) give_back(c);
           if (p.e.aux) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) *out.mine(out.buf, i) = aux[i];
-            __syncwarp();
-            if (j == 0) fetch(kCols);
+            ok = mbar_wait(aux + g % ring, g / ring & 1, abort, p.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+              if (lane == 0) raise_error(p, abort);
+              break;
+            }
           }
-#pragma unroll 1
-          for (int e = 0; e < kCols; e += 32) {
-            float v[32];
-            tmem_ld_32cols(at + (c & 1) * kPairTile + j + e, v);
-            if (j + e + 32 == 128) give_back(c);
-            out.template finish<4>(v, col + j, e / 8);
+          if (p.e.bias) {
+            bias_row[lane] = bias;
+            bias = bias_at(j < 3 ? col + (j + 1) * kChunk : 0);
           }
-          out.flush(row, col + j);
+          if (lane == 0) {  // what was stored from these buffers before has left them
+            if (p.e.keep)
+              bulk_wait_read<1>();
+            else
+              bulk_wait_read<3>();
+          }
+          __syncwarp();
+          finish_row<Out>(p, mine, zbuf, lane, v, reinterpret_cast<const float4 *>(bias_row));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row < p.m && col + j * kChunk < p.n) {
+              tma_store_2d(&to, mine, col + j * kChunk, static_cast<int>(row));
+              if (p.e.keep) tma_store_2d(&tz, zbuf, col + j * kChunk, static_cast<int>(row));
+            }
+            bulk_commit();
+            if (p.e.aux) {
+              bulk_wait_read<1>();
+              ask(g + ring - 1);
+            }
+          }
         }
         ++c;
       }
+    }
+    if (!kFloat && lane == 0) {
+      if (p.e.aux && *abort)  // what was asked for lands before the block leaves
+        for (int k = g; k < asked; ++k) drain_wait(aux + k % ring, k / ring & 1, p.wait_ns);
+      bulk_wait_all();
     }
   }
   __syncwarp();
@@ -693,7 +726,16 @@ int encode_operand(CUtensorMap *map, const void *p, int parts, long long rows, l
   const uint64_t row = static_cast<uint64_t>(cols) * 2;
   const uint64_t strides[2] = {row, parts > 1 ? row * static_cast<uint64_t>(rows) : row};
   const uint32_t box[3] = {64, static_cast<uint32_t>(box_rows), 1};
-  return encode_tiled(map, p, 3, dims, strides, box, true, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+  return encode_tiled(map, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+// A map of a result [rows][cols] of 16-bit numbers in boxes of 32 by 32.
+int encode_result(CUtensorMap *map, const void *p, long long rows, long long cols) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+  const uint64_t stride = static_cast<uint64_t>(cols) * 2;
+  const uint32_t box[2] = {kChunk, 32};
+  return encode_tiled(map, p, 2, dims, &stride, box, CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
 // Kernels' dynamic shared memory is allowed once a device.
@@ -754,6 +796,12 @@ int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
                       : encode_operand(&ta, d.a.p, d.parts, d.k, d.m, kBK));
   VAE_TRY(d.b.k_major ? encode_operand(&tb, d.b.p, d.parts, d.n, d.k, 128)
                       : encode_operand(&tb, d.b.p, d.parts, d.k, d.n, kBK));
+  CUtensorMap to{}, tz{}, tx{};  // 32 x 32 pieces of 16-bit results
+  if (d.dtype != VAE_F32) {
+    VAE_TRY(encode_result(&to, p.e.out, d.m, d.n));
+    if (p.e.keep) VAE_TRY(encode_result(&tz, p.e.keep, d.m, d.n));
+    if (p.e.aux) VAE_TRY(encode_result(&tx, p.e.aux, d.m, d.n));
+  }
   p.idesc = idesc_16bit(kPairTile, kPairTile, !d.f16, !d.a.k_major, !d.b.k_major);
   p.m_tiles = ceil_div(d.m, kPairTile);
   p.n_tiles = ceil_div(d.n, kPairTile);
@@ -764,7 +812,7 @@ int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
     VAE_CUDA_TRY(allow_smem(gemm_pair<Out>, kPairSmem, &done));
     cudaLaunchAttribute attr[2];
     const auto cfg = launch_config(attr, grid, kPairThreads, kPairSmem, 2, p.wait, s);
-    VAE_CUDA_TRY(cudaLaunchKernelEx(&cfg, gemm_pair<Out>, ta, tb, p));
+    VAE_CUDA_TRY(cudaLaunchKernelEx(&cfg, gemm_pair<Out>, ta, tb, to, tz, tx, p));
     count_launches(1);
     return VAE_OK;
   });

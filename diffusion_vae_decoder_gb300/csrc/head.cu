@@ -223,7 +223,7 @@ int head_gn_silu_conv(const float *x, int n, int h, int w, int c, const float *s
   const uint64_t str[3] = {static_cast<uint64_t>(c) * 4, static_cast<uint64_t>(w) * c * 4,
                            static_cast<uint64_t>(h) * w * c * 4};
   const uint32_t box[4] = {kCC, kHW, kHH, 1};
-  VAE_TRY(encode_tiled(&tm, x, 4, dims, str, box, false));
+  VAE_TRY(encode_tiled(&tm, x, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE));
   int rc;
   switch (cout) {
     case 1: rc = launch_head<1>(tm, n, h, w, c, scale, shift, wv, bias, y, err, s); break;

@@ -119,7 +119,7 @@ void count_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed);
 long long launch_count() { return g_launches.load(std::memory_order_relaxed); }
 
 int encode_tiled(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
-                 const uint64_t *strides_bytes, const uint32_t *box, bool swizzle128,
+                 const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle swizzle,
                  CUtensorMapDataType type) {
   auto fn = encode_fn();
   if (!fn) return VAE_ECUDA;
@@ -134,7 +134,7 @@ int encode_tiled(CUtensorMap *map, const void *base, int rank, const uint64_t *d
   const CUresult r =
       fn(map, type, static_cast<cuuint32_t>(rank),
          const_cast<void *>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+         swizzle,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? VAE_OK : VAE_EUNSUPPORTED;
