@@ -38,6 +38,7 @@ struct Params {
   uint32_t idesc;
   uint64_t wait_ns;
   int *err;
+  int kind;
   GemmEpilogue e;
 };
 
@@ -55,6 +56,26 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
 // The parts that product q takes: hh, hm, mh, mm, hl, lh.
 __device__ __forceinline__ int part_a(int q) { return (0x201100 >> (4 * q)) & 15; }
 __device__ __forceinline__ int part_b(int q) { return (0x021010 >> (4 * q)) & 15; }
+
+// What becomes of a sum: KIND of an activation, or of its derivative at aux.
+enum Kind { kNone, kSilu, kGelu, kSiluSlope, kGeluSlope };
+int kind_of(const GemmEpilogue &e) {
+  if (e.act == VAE_ACT_NONE) return kNone;
+  const bool silu = e.act == VAE_ACT_SILU;
+  return e.derivative ? (silu ? kSiluSlope : kGeluSlope) : (silu ? kSilu : kGelu);
+}
+// f(integral_constant) with the launch's kind: one branch around a block of results,
+// where branches in it cost a third of a tile's time.
+template <class F>
+__device__ __forceinline__ void by_kind(int kind, F &&f) {
+  switch (kind) {
+    case kSilu: return f(std::integral_constant<int, kSilu>{});
+    case kGelu: return f(std::integral_constant<int, kGelu>{});
+    case kSiluSlope: return f(std::integral_constant<int, kSiluSlope>{});
+    case kGeluSlope: return f(std::integral_constant<int, kGeluSlope>{});
+    default: return f(std::integral_constant<int, kNone>{});
+  }
+}
 
 // max and min that give a NaN for one.
 __device__ __forceinline__ uint64_t at_least2(uint64_t z, float low) {
@@ -76,7 +97,10 @@ __device__ __forceinline__ uint64_t at_most2(uint64_t z, float high) {
 // negative side (sigmoid 1e-38), and z and 1 on the positive one; z is held inside,
 // so that no power of it and no exponential overflows. A NaN stays one.
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.071354816f;
-__device__ __forceinline__ float far_of(int act) { return act == VAE_ACT_SILU ? 87.f : 10.f; }
+template <int KIND>
+constexpr bool is_gelu = KIND == kGelu || KIND == kGeluSlope;
+template <int KIND>
+constexpr float kFar = is_gelu<KIND> ? 10.f : 87.f;
 // s = 1 / (1 + e) with e = e^-v, for v >= -87.4. PRECISE: to about 2^-22, with two
 // special-function operations a number (t is the rounded product with log2 e, whose
 // residual w is put back). Else s to 2^-17, where a 16-bit result's rounding is 2^-9
@@ -101,21 +125,20 @@ __device__ __forceinline__ uint64_t sigmoid_of(uint64_t v, uint64_t *e) {
     return fma2(r, fma2(nd, r, one), r);
   }
 }
-template <bool PRECISE>
-__device__ __forceinline__ uint64_t act2(uint64_t z, int act) {
-  if (act == VAE_ACT_NONE) return z;
-  const uint64_t h = at_least2(z, -far_of(act));
+template <int KIND, bool PRECISE>
+__device__ __forceinline__ uint64_t act2(uint64_t z) {
+  const uint64_t h = at_least2(z, -kFar<KIND>);
   uint64_t v = h, e;
-  if (act == VAE_ACT_GELU)
+  if (is_gelu<KIND>)
     v = mul2(h, fma2(mul2(h, h), pk2(kGeluB, kGeluB), pk2(kGeluA, kGeluA)));
   return mul2(h, sigmoid_of<PRECISE>(v, &e));
 }
 // act'(z) = s + z v' s (1 - s), with 1 - s = e s, which loses nothing where s is near 1.
-template <bool PRECISE>
-__device__ __forceinline__ uint64_t act_slope2(uint64_t z, int act) {
-  const uint64_t h = at_most2(at_least2(z, -far_of(act)), far_of(act));
+template <int KIND, bool PRECISE>
+__device__ __forceinline__ uint64_t act_slope2(uint64_t z) {
+  const uint64_t h = at_most2(at_least2(z, -kFar<KIND>), kFar<KIND>);
   uint64_t v = h, w = h, e;  // w = z v'
-  if (act == VAE_ACT_GELU) {
+  if (is_gelu<KIND>) {
     const uint64_t q = mul2(h, h), a = pk2(kGeluA, kGeluA);
     v = mul2(h, fma2(q, pk2(kGeluB, kGeluB), a));
     w = mul2(h, fma2(q, pk2(3.f * kGeluB, 3.f * kGeluB), a));
@@ -124,13 +147,17 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t z, int act) {
   return mul2(s, fma2(w, mul2(e, s), pk2(1.f, 1.f)));
 }
 
-// Two neighbouring sums of a row -> out, and z where it is kept.
-template <bool PRECISE>
-__device__ __forceinline__ uint64_t finish2(const GemmEpilogue &e, uint64_t sum, uint64_t bias,
-                                            uint64_t aux, uint64_t *z) {
-  if (e.derivative) return e.aux ? mul2(sum, act_slope2<PRECISE>(aux, e.act)) : sum;
-  *z = add2(sum, bias);
-  return add2(act2<PRECISE>(*z, e.act), aux);
+// Two neighbouring sums of a row -> out, and z.
+template <int KIND, bool PRECISE>
+__device__ __forceinline__ uint64_t finish2(uint64_t sum, uint64_t bias, uint64_t aux,
+                                            uint64_t *z) {
+  if constexpr (KIND == kSiluSlope || KIND == kGeluSlope) {
+    return mul2(sum, act_slope2<KIND, PRECISE>(aux));
+  } else {
+    *z = add2(sum, bias);
+    if constexpr (KIND == kNone) return add2(*z, aux);
+    else return add2(act2<KIND, PRECISE>(*z), aux);
+  }
 }
 
 // Stage `it` of the tile at (m0, n0): `rows_a` and `rows_b` rows of the operands.
@@ -159,16 +186,52 @@ __device__ __forceinline__ void load_stage(const CUtensorMap *ta, const CUtensor
     for (int i = 0; i < ROWS_B / 64; ++i) load(db + i * kBK * 128, tb, n0 + 64 * i, k0, pb);
   }
 }
-// The four steps of a staged pair of operands.
+// What the tensor core is told of the stages: descriptors of stage 0's operands, and
+// how far a step of 16 reduction indexes and a stage move them (in units of 16 bytes;
+// the address is their low word's).
+struct Operands {
+  uint64_t a, b;
+  uint32_t step_a, step_b;
+};
+__device__ __forceinline__ Operands operands_at(const Params &p, uint32_t sa, uint32_t sb) {
+  return {p.a_k ? sw128_kmajor_desc(sa) : sw128_mnmajor_desc(sa, kBK * 128),
+          p.b_k ? sw128_kmajor_desc(sb) : sw128_mnmajor_desc(sb, kBK * 128),
+          (p.a_k ? 32u : 2048u) >> 4, (p.b_k ? 32u : 2048u) >> 4};
+}
+// The four steps of stage `s`, of `bytes` a stage.
 template <bool PAIR>
-__device__ __forceinline__ void multiply_stage(const Params &p, uint32_t sa, uint32_t sb,
-                                               uint32_t acc, bool first) {
-  const uint64_t da = p.a_k ? sw128_kmajor_desc(sa) : sw128_mnmajor_desc(sa, kBK * 128);
-  const uint64_t db = p.b_k ? sw128_kmajor_desc(sb) : sw128_mnmajor_desc(sb, kBK * 128);
-  const uint32_t step_a = (p.a_k ? 32 : 2048) >> 4, step_b = (p.b_k ? 32 : 2048) >> 4;
+__device__ __forceinline__ void multiply_stage(const Operands &o, uint32_t idesc, int s,
+                                               uint32_t bytes, uint32_t acc, bool first) {
+  const uint64_t a = o.a + s * (bytes >> 4), b = o.b + s * (bytes >> 4);
 #pragma unroll
   for (int k = 0; k < kBK / 16; ++k)
-    umma_16bit<PAIR>(acc, da + k * step_a, db + k * step_b, p.idesc, !(first && k == 0));
+    umma_16bit<PAIR>(acc, a + k * o.step_a, b + k * o.step_b, idesc, !(first && k == 0));
+}
+
+// A place in a ring of N stages and the parity of its round; a thread alone goes
+// through it, so that a division a step would be most of its time.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      round ^= 1;
+    }
+  }
+};
+// After an abort: what was asked for in the last stages before `r` lands.
+template <int N>
+__device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long long asked,
+                                             uint64_t limit_ns) {
+  for (int j = 0; j < N && j < asked; ++j) {
+    if (r.s-- == 0) {
+      r.s = N - 1;
+      r.round ^= 1;
+    }
+    drain_wait(full + r.s, r.round, limit_ns);
+  }
 }
 
 // ------------------------------------------------------------------ small tiles
@@ -262,45 +325,55 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (p.wait) grid_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int i = 0;
-      for (; i < its; ++i) {
-        const int s = i % kTileStages;
-        if (!mbar_wait(empty + s, (i / kTileStages & 1) ^ 1, abort, p.wait_ns)) {
-          raise_error(p, abort);
-          break;
-        }
-        mbar_arrive_expect_tx(full + s, kTileStageBytes);
-        uint8_t *a = smem + s * kTileStageBytes;
+    Ring<kTileStages> r;
+    int i = 0;
+    for (; i < its; ++i, r.next()) {
+      bool ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) raise_error(p, abort);
+        break;
+      }
+      uint64_t *bar = full + r.s;
+      uint8_t *a = smem + r.s * kTileStageBytes;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, kTileStageBytes);
         load_stage<kTile, kTile>(&ta, &tb, p, it0 + i, m0, n0, a, a + kTileStageBytes / 2,
                                  [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
-                                   tma_load_3d(dst, m, full + s, c0, c1, c2);
+                                   tma_load_3d(dst, m, bar, c0, c1, c2);
                                  });
       }
-      if (*abort)  // what was asked for lands before the block leaves
-        for (int j = max(0, i - kTileStages); j < i; ++j)
-          drain_wait(full + j % kTileStages, j / kTileStages & 1, p.wait_ns);
+      __syncwarp();
     }
+    if (*abort && lane == 0) drain_stages(full, r, i, p.wait_ns);  // before the block leaves
   } else if (warp == 1) {
-    if (lane == 0) {
+    // The whole warp goes through the loop, so that descriptors stay in registers that
+    // all lanes share, and one lane issues (the same one every time).
+    const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kTileStageBytes / 2);
+    const uint32_t idesc = p.idesc;
+    Ring<kTileStages> r;
+    for (int i = 0; i < its; ++i, r.next()) {
+      const int chunk = kFloat ? i / kChain : 0;
+      const bool first = kFloat ? i % kChain == 0 : i == 0;
       bool ok = true;
-      for (int i = 0; i < its && ok; ++i) {
-        const int chunk = kFloat ? i / kChain : 0, s = i % kTileStages;
-        const bool first = kFloat ? i % kChain == 0 : i == 0;
-        if (kFloat && first)
-          ok = mbar_wait(acc_empty + (chunk & 1), (chunk >> 1 & 1) ^ 1, abort, p.wait_ns);
-        ok = ok && mbar_wait(full + s, i / kTileStages & 1, abort, p.wait_ns);
-        if (!ok) {
-          raise_error(p, abort);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sa = smem_u32(smem + s * kTileStageBytes);
-        multiply_stage<false>(p, sa, sa + kTileStageBytes / 2, tmem + (chunk & 1) * kTile, first);
-        umma_commit(empty + s);
+      if (kFloat && first)
+        ok = mbar_wait(acc_empty + (chunk & 1), (chunk >> 1 & 1) ^ 1, abort, p.wait_ns);
+      ok = ok && mbar_wait(full + r.s, r.round, abort, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) raise_error(p, abort);
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        multiply_stage<false>(o, idesc, r.s, kTileStageBytes, tmem + (chunk & 1) * kTile, first);
+        umma_commit(empty + r.s);
         if (i == its - 1 || (kFloat && i % kChain == kChain - 1)) umma_commit(acc_full + (chunk & 1));
       }
-      // whatever became of the sums, no product is left when tensor memory is freed
+      __syncwarp();
+    }
+    // whatever became of the sums, no product is left when tensor memory is freed
+    if (elect_one()) {
       umma_commit(drain);
       drain_wait(drain, 0, p.wait_ns);
     }
@@ -364,6 +437,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     Quad bias = {{0, 0}};
     if (p.e.bias && in) bias = load_quad(p.e.bias + col);
     constexpr int W = kTileThreads / 32, U = 4;
+    by_kind(p.kind, [&](auto kind) {
     for (int r = warp; r < share; r += W * U) {
       Quad a[U];
 #pragma unroll
@@ -393,11 +467,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         Quad z = {{0, 0}}, o;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          o.v[j] = finish2<kFloat>(p.e, sum.v[j], bias.v[j], a[u].v[j], &z.v[j]);
+          o.v[j] = finish2<decltype(kind)::value, kFloat>(sum.v[j], bias.v[j], a[u].v[j], &z.v[j]);
         store_quad(out + row * p.n + col, o);
         if (keep) store_quad(keep + row * p.n + col, z);
       }
     }
+    });
   }
   if (splits > 1) cluster_sync();  // the others read this block's sums until here
 }
@@ -420,6 +495,19 @@ constexpr int kStaging = 4 * kChunkBytes;  // a warp's
 constexpr size_t kPairSmem =
     kPairStages * kPairStageBytes + kPairWarps * (kStaging + kChunk * 4) + 1024 + 512;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
+
+// The place of tile t in the result: bands of 8 rows of tiles, column by column, so
+// that the tiles under way at a time form a block as wide as it is high, whose
+// operands L2 holds.
+struct Place {
+  int m, n;
+};
+__device__ __forceinline__ Place place_of(const Params &p, int t) {
+  constexpr int kBand = 8;
+  const int band = t / (kBand * p.n_tiles), rest = t - band * kBand * p.n_tiles;
+  const int rows = min(kBand, p.m_tiles - band * kBand);
+  return {(band * kBand + rest % rows) * kPairTile, rest / rows * kPairTile};
+}
 
 // 16-byte piece `c` of row `r` in a buffer of 64-byte rows with TMA's 64-byte swizzle:
 // eight threads' pieces of eight rows lie in different banks.
@@ -445,6 +533,7 @@ __device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int
   const int ch = col + (lane & 7) * 4;
   Quad bias = {{0, 0}};
   if (p.e.bias && ch < p.n) bias = load_quad(p.e.bias + ch);
+  by_kind(p.kind, [&](auto kind) {
 #pragma unroll 2
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3);
@@ -454,10 +543,12 @@ __device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int
     Quad a = {{0, 0}}, z = {{0, 0}}, y;
     if (p.e.aux) a = load_quad(static_cast<const float *>(p.e.aux) + at);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) y.v[j] = finish2<true>(p.e, v.v[j], bias.v[j], a.v[j], &z.v[j]);
+    for (int j = 0; j < 2; ++j)
+      y.v[j] = finish2<decltype(kind)::value, true>(v.v[j], bias.v[j], a.v[j], &z.v[j]);
     store_quad(static_cast<float *>(p.e.out) + at, y);
     if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + at, z);
   }
+  });
   __syncwarp();
 }
 
@@ -467,22 +558,29 @@ __device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int
 template <class T>
 __device__ __forceinline__ void finish_row(const Params &p, uint8_t *buf, uint8_t *zbuf, int lane,
                                            const float *sum, const float4 *bias_row) {
+by_kind(p.kind, [&](auto kind) {
+    constexpr int K = decltype(kind)::value;
+    constexpr bool kSlope = K == kSiluSlope || K == kGeluSlope;
+    Raw<T> aux[4];
+    const bool has_aux = kSlope || p.e.aux;
+    if (has_aux) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    Oct a = {{0, 0, 0, 0}}, bias = a, o, z = a;
-    if (p.e.bias) bias = oct_of(bias_row[2 * c], bias_row[2 * c + 1]);
-    if (p.e.aux) {
-      Raw<T> r;
-      r.v[0] = *piece64(buf, lane, c);
-      a = oct_of(r);
+      for (int c = 0; c < 4; ++c) aux[c].v[0] = *piece64(buf, lane, c);
     }
+    const bool has_bias = !kSlope && p.e.bias, keep = !kSlope && p.e.keep;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o.v[j] = finish2<false>(p.e, pk2(sum[8 * c + 2 * j], sum[8 * c + 2 * j + 1]), bias.v[j],
-                              a.v[j], &z.v[j]);
-    *piece64(buf, lane, c) = raw_of<T>(o).v[0];
-    if (p.e.keep) *piece64(zbuf, lane, c) = raw_of<T>(z).v[0];
-  }
+    for (int c = 0; c < 4; ++c) {
+      Oct a = {{0, 0, 0, 0}}, bias = a, o, z = a;
+      if (has_bias) bias = oct_of(bias_row[2 * c], bias_row[2 * c + 1]);
+      if (has_aux) a = oct_of(aux[c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o.v[j] = finish2<K, false>(pk2(sum[8 * c + 2 * j], sum[8 * c + 2 * j + 1]), bias.v[j],
+                                   a.v[j], &z.v[j]);
+      *piece64(buf, lane, c) = raw_of<T>(o).v[0];
+      if (keep) *piece64(zbuf, lane, c) = raw_of<T>(z).v[0];
+    }
+  });
 }
 
 template <class Out>
@@ -534,60 +632,73 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (p.wait) grid_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      long long i = 0;  // stages, over all tiles
-      bool ok = true;
-      for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-        const int m0 = t / p.n_tiles * kPairTile + 128 * rank;
-        const int n0 = t % p.n_tiles * kPairTile + 128 * rank;
-        for (int it = 0; it < p.its; ++it, ++i) {
-          const int s = static_cast<int>(i % kPairStages);
-          ok = mbar_wait_cluster(empty + s, (i / kPairStages & 1) ^ 1, abort, p.wait_ns);
-          if (!ok) {
-            raise_error(p, abort);
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kPairStageBytes);
-          const uint32_t bar = mapa_rank(full + s, 0);
-          uint8_t *a = smem + s * kPairStageBytes;
+    Ring<kPairStages> r;
+    long long asked = 0;
+    bool ok = true;
+    for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+      const Place at = place_of(p, t);
+      const int m0 = at.m + 128 * rank, n0 = at.n + 128 * rank;
+      for (int it = 0; it < p.its; ++it, ++asked, r.next()) {
+        ok = mbar_wait_cluster(empty + r.s, r.round ^ 1, abort, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) raise_error(p, abort);
+          break;
+        }
+        const uint32_t bar = mapa_rank(full + r.s, 0);
+        uint8_t *a = smem + r.s * kPairStageBytes;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + r.s, 2 * kPairStageBytes);
           load_stage<128, 128>(&ta, &tb, p, it, m0, n0, a, a + kPairStageBytes / 2,
                                [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
                                  tma_load_3d_pair(dst, m, bar, c0, c1, c2);
                                });
         }
+        __syncwarp();
       }
-      // what was asked for lands before the pair leaves (both blocks' copies count on
-      // the leader's barriers, and the other block waits for the leader at the end)
-      if (*abort && rank == 0)
-        for (long long j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
-          drain_wait(full + j % kPairStages, j / kPairStages & 1, p.wait_ns);
     }
+    // what was asked for lands before the pair leaves (both blocks' copies count on
+    // the leader's barriers, and the other block waits for the leader at the end)
+    __syncwarp();
+    if (*abort && rank == 0 && lane == 0) drain_stages(full, r, asked, p.wait_ns);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      long long i = 0;
+    // The whole warp goes through the loop, so that descriptors stay in registers that
+    // all lanes share, and one lane issues: the tensor core takes a stage 512 clocks,
+    // and this loop has to be shorter.
+    if (rank == 0) {
+      const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kPairStageBytes / 2);
+      const uint32_t idesc = p.idesc;
+      const int its = p.its;
+      Ring<kPairStages> r;
       int c = 0;  // accumulators taken
       bool ok = true;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-        for (int it = 0; it < p.its; ++it, ++i) {
+        for (int it = 0; it < its; ++it, r.next()) {
           const bool first = kFloat ? it % kChain == 0 : it == 0;
-          const bool last = it == p.its - 1 || (kFloat && it % kChain == kChain - 1);
-          const int s = static_cast<int>(i % kPairStages);
+          const bool last = it == its - 1 || (kFloat && it % kChain == kChain - 1);
           if (first)
             ok = mbar_wait_cluster(acc_empty + (c & 1), (c >> 1 & 1) ^ 1, abort, p.wait_ns);
-          ok = ok && mbar_wait_cluster(full + s, i / kPairStages & 1, abort, p.wait_ns);
+          ok = ok && mbar_wait_cluster(full + r.s, r.round, abort, p.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
-            raise_error(p, abort);
+            if (lane == 0) raise_error(p, abort);
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kPairStageBytes);
-          multiply_stage<true>(p, sa, sa + kPairStageBytes / 2, tmem + (c & 1) * kPairTile, first);
-          umma_commit_pair(empty + s, 3);
-          if (last) umma_commit_pair(acc_full + (c++ & 1), 3);
+          if (elect_one()) {
+            multiply_stage<true>(o, idesc, r.s, kPairStageBytes, tmem + (c & 1) * kPairTile, first);
+            umma_commit_pair(empty + r.s, 3);
+            if (last) umma_commit_pair(acc_full + (c & 1), 3);
+          }
+          __syncwarp();
+          c += last;
         }
       }
-      umma_commit_pair(drain, 1);
-      drain_wait(drain, 0, p.wait_ns);
+      // (elect_one names the same lane every time: it has issued all of the products)
+      if (elect_one()) {
+        umma_commit_pair(drain, 1);
+        drain_wait(drain, 0, p.wait_ns);
+      }
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -617,9 +728,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (t >= tiles) return;
       uint64_t *bar = aux + k % ring;
       mbar_arrive_expect_tx(bar, kChunkBytes);
-      tma_load_2d(buf + k % ring * kChunkBytes, &tx, bar,
-                  t % p.n_tiles * kPairTile + 128 * half + (k & 3) * kChunk,
-                  t / p.n_tiles * kPairTile + 128 * static_cast<int>(rank) + 32 * q);
+      const Place at = place_of(p, t);
+      tma_load_2d(buf + k % ring * kChunkBytes, &tx, bar, at.n + 128 * half + (k & 3) * kChunk,
+                  at.m + 128 * static_cast<int>(rank) + 32 * q);
       asked = k + 1;
     };
     float *bias_row = bias_rows + kChunk * (warp - 2);
@@ -630,8 +741,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int k = 0; k < ring - 1; ++k) ask(k);
     bool ok = true;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-      const long long row = static_cast<long long>(t / p.n_tiles) * kPairTile + 128 * rank + 32 * q;
-      const int col = t % p.n_tiles * kPairTile + 128 * half;
+      const Place place = place_of(p, t);
+      const long long row = place.m + 128ll * rank + 32 * q;
+      const int col = place.n + 128 * half;
       if constexpr (kFloat) {
         float acc[128];
 #pragma unroll
@@ -784,7 +896,7 @@ bool takes_pairs(long long m, int n, int its) {
   const long long small = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
   const long long large = static_cast<long long>(ceil_div(m, kPairTile)) * ceil_div(n, kPairTile);
   const int s = tile_splits(small, its), sms = num_sms();
-  if (sms < 2 || large > 0x3fffffff) return false;
+  if (sms < 2 || large > 0x0fffffff) return false;
   const long long t_small = (small * s + sms - 1) / sms * (4000 + 512ll * ((its + s - 1) / s));
   const long long t_large = 3000 + (large + sms / 2 - 1) / (sms / 2) * (1000 + 600ll * its);
   return t_large < t_small;
@@ -860,6 +972,7 @@ int gemm(const GemmDesc &d, cudaStream_t s) {
   p.err = device_error_word();
   if (!p.err) return VAE_ECUDA;
   p.e = d.epi;
+  p.kind = kind_of(d.epi);
   return takes_pairs(d.m, d.n, p.its) ? launch_pair(d, p, s) : launch_tile(d, p, s);
 }
 
