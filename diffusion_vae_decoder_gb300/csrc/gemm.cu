@@ -481,19 +481,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // Two blocks on paired SMs share a 256 x 256 tile: each stages 128 rows of either
 // operand and holds 128 rows of sums, so that a stage brings 32 KB into an SM for 512
 // clocks of its tensor core (a tile of one SM's own would bring 48 KB for 128 x 256).
-// Persistent: a pair takes every (grid / 2)-th tile, and while eight warps of either
+// Persistent: a pair takes every (grid / 2)-th tile, and while sixteen warps of either
 // block finish a tile from one half of tensor memory, the next one's products go to
-// the other half.
+// the other half. (Eight warps, two to a scheduler, did not hide each other's waits:
+// for 512 products a sum 38 us instead of TODO.)
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
-constexpr int kPairThreads = 320;
+constexpr int kPairThreads = 576;
 constexpr int kPairStageBytes = 2 * 128 * kBK * 2;
-constexpr int kPairWarps = 8;
+constexpr int kPairWarps = 16;            // that finish tiles, 64 columns each
+constexpr int kWarpCols = 4 * kPairTile / kPairWarps;
 constexpr int kChunk = 32;              // columns that a warp finishes at a time
 constexpr int kChunkBytes = 32 * 64;    // of 16-bit numbers
-constexpr int kStaging = 4 * kChunkBytes;  // a warp's
-constexpr size_t kPairSmem =
-    kPairStages * kPairStageBytes + kPairWarps * (kStaging + kChunk * 4) + 1024 + 512;
+constexpr int kStaging = 2 * kChunkBytes;  // a warp's
+constexpr int kPairHead = 3072;            // barriers and rows of the bias
+constexpr size_t kPairSmem = kPairHead + kPairStages * kPairStageBytes + kPairWarps * kStaging;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
 
 // The place of tile t in the result: bands of 8 rows of tiles, column by column, so
@@ -561,18 +563,17 @@ __device__ __forceinline__ void finish_row(const Params &p, uint8_t *buf, uint8_
 by_kind(p.kind, [&](auto kind) {
     constexpr int K = decltype(kind)::value;
     constexpr bool kSlope = K == kSiluSlope || K == kGeluSlope;
-    Raw<T> aux[4];
     const bool has_aux = kSlope || p.e.aux;
-    if (has_aux) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) aux[c].v[0] = *piece64(buf, lane, c);
-    }
     const bool has_bias = !kSlope && p.e.bias, keep = !kSlope && p.e.keep;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       Oct a = {{0, 0, 0, 0}}, bias = a, o, z = a;
       if (has_bias) bias = oct_of(bias_row[2 * c], bias_row[2 * c + 1]);
-      if (has_aux) a = oct_of(aux[c]);
+      if (has_aux) {
+        Raw<T> r;
+        r.v[0] = *piece64(buf, lane, c);
+        a = oct_of(r);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         o.v[j] = finish2<K, false>(pk2(sum[8 * c + 2 * j], sum[8 * c + 2 * j + 1]), bias.v[j],
@@ -589,17 +590,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tz,
               const __grid_constant__ CUtensorMap tx, const Params p) {
   constexpr bool kFloat = sizeof(Out) == 4;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_aligned[];
+  float *bias_rows = reinterpret_cast<float *>(smem_aligned);
+  uint8_t *smem = smem_aligned + kPairHead;
   uint8_t *staging = smem + kPairStages * kPairStageBytes;
-  float *bias_rows = reinterpret_cast<float *>(staging + kPairWarps * kStaging);
   uint64_t *full = reinterpret_cast<uint64_t *>(bias_rows + kPairWarps * kChunk);
   uint64_t *empty = full + kPairStages;
   uint64_t *acc_full = empty + kPairStages, *acc_empty = acc_full + 2;
   uint64_t *drain = acc_empty + 2;
-  uint64_t *aux_full = drain + 1;  // four of each finishing warp's
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(aux_full + 4 * kPairWarps);
+  uint64_t *aux_full = drain + 1;  // two of each finishing warp's
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(aux_full + 2 * kPairWarps);
   volatile uint32_t *abort = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(acc_empty + i, 2 * kPairWarps);
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < 4 * kPairWarps; ++i) mbar_init(aux_full + i, 1);
+    for (int i = 0; i < 2 * kPairWarps; ++i) mbar_init(aux_full + i, 1);
     fence_mbarrier_init();
     *abort = 0;
   }
@@ -701,8 +701,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t at = tmem + (static_cast<uint32_t>(q) << 21) + 128 * half;
+    const int q = warp & 3, first_col = (warp - 2) / 4 * kWarpCols;
+    const uint32_t at = tmem + (static_cast<uint32_t>(q) << 21) + first_col;
     int c = 0;  // accumulators taken
     auto taken = [&](int b) -> bool {
       bool ok = mbar_wait_cluster(acc_full + (b & 1), b >> 1 & 1, abort, p.wait_ns);
@@ -717,19 +717,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (lane == 0) mbar_arrive_cluster(mapa_rank(acc_empty + (b & 1), 0));
     };
     uint8_t *buf = staging + (warp - 2) * kStaging;
-    // 16-bit results: chunk g of the warp's (four a tile) uses buffer g % ring for aux
-    // and out; where z is kept, two of the four buffers are z's. aux is asked for
-    // ring - 1 chunks ahead, over the tiles' ends.
-    uint64_t *aux = aux_full + 4 * (warp - 2);
-    const int ring = p.e.keep ? 2 : 4;
+    // 16-bit results: chunk g of the warp's (two a tile) uses buffer g % 2 for aux and
+    // out, or the first one where the second is z's. aux is asked for a chunk ahead,
+    // over the tiles' ends, where it has a buffer to go to.
+    uint64_t *aux = aux_full + 2 * (warp - 2);
+    const int other = p.e.keep ? 0 : 1;
     int g = 0, asked = 0;
     auto ask = [&](int k) {
-      const int t = blockIdx.x / 2 + (k >> 2) * stride;
+      const int t = blockIdx.x / 2 + (k >> 1) * stride;
       if (t >= tiles) return;
-      uint64_t *bar = aux + k % ring;
+      uint64_t *bar = aux + (k & other);
       mbar_arrive_expect_tx(bar, kChunkBytes);
       const Place at = place_of(p, t);
-      tma_load_2d(buf + k % ring * kChunkBytes, &tx, bar, at.n + 128 * half + (k & 3) * kChunk,
+      tma_load_2d(buf + (k & other) * kChunkBytes, &tx, bar, at.n + first_col + (k & 1) * kChunk,
                   at.m + 128 * static_cast<int>(rank) + 32 * q);
       asked = k + 1;
     };
@@ -737,23 +737,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto bias_at = [&](int col) -> float {
       return p.e.bias && col + lane < p.n ? __ldg(p.e.bias + col + lane) : 0.f;
     };
-    if (!kFloat && p.e.aux && lane == 0)
-      for (int k = 0; k < ring - 1; ++k) ask(k);
+    if (!kFloat && p.e.aux && !p.e.keep && lane == 0) ask(0);
     bool ok = true;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
       const Place place = place_of(p, t);
       const long long row = place.m + 128ll * rank + 32 * q;
-      const int col = place.n + 128 * half;
+      const int col = place.n + first_col;
       if constexpr (kFloat) {
-        float acc[128];
+        float acc[kWarpCols];
 #pragma unroll
-        for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+        for (int j = 0; j < kWarpCols; ++j) acc[j] = 0.f;
         const int chunks = (p.its + kChain - 1) / kChain;
         for (int k = 0; k < chunks && ok; ++k, ++c) {
           ok = taken(c);
           if (!ok) break;
 #pragma unroll
-          for (int j = 0; j < 128; j += 16) {
+          for (int j = 0; j < kWarpCols; j += 16) {
             float v[16];
             tmem_ld_16cols(at + (c & 1) * kPairTile + j, v);
 #pragma unroll
@@ -763,7 +762,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 128; j += kChunk)
+        for (int j = 0; j < kWarpCols; j += kChunk)
           finish_floats(p, buf, lane, acc + j, row, col + j);
       } else {
         // a chunk's bias is asked for a chunk ahead: from L2 it takes longer than the rest
@@ -771,31 +770,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         ok = taken(c);
         if (!ok) break;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j, ++g) {
-          uint8_t *mine = buf + g % ring * kChunkBytes;
-          uint8_t *zbuf = buf + (2 + (g & 1)) * kChunkBytes;
+        for (int j = 0; j < 2; ++j, ++g) {
+          uint8_t *mine = buf + (g & other) * kChunkBytes, *zbuf = buf + kChunkBytes;
           float v[kChunk];
           tmem_ld_32cols(at + (c & 1) * kPairTile + j * kChunk, v);
-          if (j == 3) give_back(c);
+          if (j == 1) give_back(c);
+          if (lane == 0) {
+            if (p.e.aux || p.e.keep) {
+              bulk_wait_read<0>();  // what was stored has left its buffer
+              if (p.e.aux) ask(p.e.keep ? g : g + 1);
+            } else {
+              bulk_wait_read<1>();
+            }
+          }
+          if (p.e.bias) {
+            bias_row[lane] = bias;
+            bias = bias_at(j == 0 ? col + kChunk : p.n);
+          }
+          __syncwarp();
           if (p.e.aux) {
-            ok = mbar_wait(aux + g % ring, g / ring & 1, abort, p.wait_ns);
+            ok = mbar_wait(aux + (g & other), (p.e.keep ? g : g >> 1) & 1, abort, p.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
               if (lane == 0) raise_error(p, abort);
               break;
             }
           }
-          if (p.e.bias) {
-            bias_row[lane] = bias;
-            bias = bias_at(j < 3 ? col + (j + 1) * kChunk : 0);
-          }
-          if (lane == 0) {  // what was stored from these buffers before has left them
-            if (p.e.keep)
-              bulk_wait_read<1>();
-            else
-              bulk_wait_read<3>();
-          }
-          __syncwarp();
           finish_row<Out>(p, mine, zbuf, lane, v, reinterpret_cast<const float4 *>(bias_row));
           fence_proxy_async_smem();
           __syncwarp();
@@ -805,10 +805,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               if (p.e.keep) tma_store_2d(&tz, zbuf, col + j * kChunk, static_cast<int>(row));
             }
             bulk_commit();
-            if (p.e.aux) {
-              bulk_wait_read<1>();
-              ask(g + ring - 1);
-            }
           }
         }
         ++c;
@@ -816,7 +812,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     if (!kFloat && lane == 0) {
       if (p.e.aux && *abort)  // what was asked for lands before the block leaves
-        for (int k = g; k < asked; ++k) drain_wait(aux + k % ring, k / ring & 1, p.wait_ns);
+        for (int k = g; k < asked; ++k)
+          drain_wait(aux + (k & other), (other ? k >> 1 : k) & 1, p.wait_ns);
       bulk_wait_all();
     }
   }
