@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const Place at = place_of(p, t);
       const int m0 = at.m + 128 * rank, n0 = at.n + 128 * rank;
       for (int it = 0; it < p.its; ++it, ++asked, r.next()) {
-        ok = mbar_wait_cluster(empty + r.s, r.round ^ 1, abort, p.wait_ns);
+        ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) raise_error(p, abort);
@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const bool first = kFloat ? it % kChain == 0 : it == 0;
           const bool last = it == its - 1 || (kFloat && it % kChain == kChain - 1);
           if (first)
-            ok = mbar_wait_cluster(acc_empty + (c & 1), (c >> 1 & 1) ^ 1, abort, p.wait_ns);
-          ok = ok && mbar_wait_cluster(full + r.s, r.round, abort, p.wait_ns);
+            ok = mbar_wait(acc_empty + (c & 1), (c >> 1 & 1) ^ 1, abort, p.wait_ns);
+          ok = ok && mbar_wait(full + r.s, r.round, abort, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
             if (lane == 0) raise_error(p, abort);
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t at = tmem + (static_cast<uint32_t>(q) << 21) + first_col;
     int c = 0;  // accumulators taken
     auto taken = [&](int b) -> bool {
-      bool ok = mbar_wait_cluster(acc_full + (b & 1), b >> 1 & 1, abort, p.wait_ns);
+      bool ok = mbar_wait(acc_full + (b & 1), b >> 1 & 1, abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) raise_error(p, abort);
       tc_fence_after();
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto give_back = [&](int b) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_rank(acc_empty + (b & 1), 0));
+      if (lane == 0) mbar_arrive_remote(mapa_rank(acc_empty + (b & 1), 0));
     };
     uint8_t *buf = staging + (warp - 2) * kStaging;
     // 16-bit results: chunk g of the warp's (two a tile) uses buffer g % 2 for aux and
