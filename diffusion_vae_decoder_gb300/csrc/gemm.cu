@@ -40,6 +40,7 @@ struct Params {
   int *err;
   int kind;
   GemmEpilogue e;
+  GemmColumnSums cols;
 };
 
 __device__ __forceinline__ void raise_error(const Params &p, volatile uint32_t *abort) {
@@ -101,29 +102,19 @@ template <int KIND>
 constexpr bool is_gelu = KIND == kGelu || KIND == kGeluSlope;
 template <int KIND>
 constexpr float kFar = is_gelu<KIND> ? 10.f : 87.f;
-// s = 1 / (1 + e) with e = e^-v, for v >= -87.4. PRECISE: to about 2^-22, with two
-// special-function operations a number (t is the rounded product with log2 e, whose
-// residual w is put back). Else s to 2^-17, where a 16-bit result's rounding is 2^-9
-// or 2^-12, with one: the reciprocal by two Newton steps r <- r (2 - d r) from an
-// integer seed off by at most 5.1 % for d >= 1. The special-function unit takes a warp
-// eight clocks, and two operations a number would be all the 4096 clocks that the
-// tensor core spends on a 256 x 256 tile of 512 products.
+// s = 1 / (1 + e) with e = e^-v, for v >= -87.4, by the exp2 and reciprocal units, to
+// 2^-21 and the rounding of v log2 e (2^-23 |v|), which PRECISE puts back for results
+// that are floats. (The reciprocal by Newton steps from an integer seed instead, for a
+// unit that takes a warp eight clocks: 33 us instead of 31 for 16384 x 512 -> 2048.)
 template <bool PRECISE>
 __device__ __forceinline__ uint64_t sigmoid_of(uint64_t v, uint64_t *e) {
   const uint64_t t = mul2(v, pk2(-1.4426950408889634f, -1.4426950408889634f));
-  const uint64_t one = pk2(1.f, 1.f), m1 = pk2(-1.f, -1.f);
   *e = pk2(ex2_approx(lo2(t)), ex2_approx(hi2(t)));
   if constexpr (PRECISE) {
     const uint64_t w = fma2(t, pk2(0.6931471805599453f, 0.6931471805599453f), v);
-    *e = fma2(mul2(*e, w), m1, *e);
-    return rcp2(add2(*e, one));
-  } else {
-    const uint64_t nd = fma2(*e, m1, m1);  // -d
-    uint64_t r = static_cast<uint64_t>(0xfef30000u - static_cast<uint32_t>(nd)) |
-                 static_cast<uint64_t>(0xfef30000u - static_cast<uint32_t>(nd >> 32)) << 32;
-    r = fma2(r, fma2(nd, r, one), r);
-    return fma2(r, fma2(nd, r, one), r);
+    *e = fma2(mul2(*e, w), pk2(-1.f, -1.f), *e);
   }
+  return rcp2(add2(*e, pk2(1.f, 1.f)));
 }
 template <int KIND, bool PRECISE>
 __device__ __forceinline__ uint64_t act2(uint64_t z) {
@@ -234,17 +225,110 @@ __device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long lon
   }
 }
 
+// Sums of A's columns (the result's rows), by warps that wait for the tensor core: the
+// rows that the copies bring in at the same time are read once more, from L2, by one of
+// the tiles that share them: tile column j takes blocks j, j + n_tiles, ... of 64 rows.
+// Warp w of W takes every W-th pair of a block's rows of 128 numbers, a lane eight of
+// them, which it copies into its own places of the warp's buffer (kColumnBytes) and
+// adds up a chain of products later. (Through registers, whose loads the warp would
+// have to wait for, the call took 124 us instead of 89.)
+constexpr int kColumnBytes = 4096;
+struct Columns {
+  Oct sum = {{0, 0, 0, 0}};
+  int next = 0;     // block of 64 rows
+  int waiting = 0;  // blocks in the buffer
+};
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+// Adds up what is in the buffer, then asks for more blocks before `end`.
+template <int W, class D>
+__device__ __forceinline__ void turn_blocks(const Params &p, uint8_t *buf, int end, long long m0,
+                                            int w, int lane, Columns *c) {
+  constexpr int R = kBK / (2 * W), kLane = 8 * sizeof(D);  // rows of a lane's; bytes of a row
+  constexpr int kSlots = kColumnBytes / (R * 32 * kLane);
+  const long long ch = m0 + 8 * (lane & 15);
+  const uint32_t mine = smem_u32(buf) + 16 * lane;
+  do {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+    for (int i = 0; i < c->waiting * R; ++i) {
+      Raw<D> v;
+#pragma unroll
+      for (int h = 0; h < kLane / 16; ++h)
+        v.v[h] = *reinterpret_cast<const uint4 *>(buf + (i * kLane / 16 + h) * 512 + 16 * lane);
+      const Oct o = oct_of(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c->sum.v[j] = add2(c->sum.v[j], o.v[j]);
+    }
+    c->waiting = 0;
+#pragma unroll 1
+    for (; c->waiting < kSlots && c->next < end; ++c->waiting, c->next += p.n_tiles) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const long long r = static_cast<long long>(c->next) * kBK + 2 * (w + W * i) + (lane >> 4);
+        const bool in = r < p.cols.rows && ch < p.m;
+        const D *src = static_cast<const D *>(p.cols.src) + (in ? r * p.m + ch : 0);
+#pragma unroll
+        for (int h = 0; h < kLane / 16; ++h)
+          copy16(mine + ((c->waiting * R + i) * kLane / 16 + h) * 512, src + 8 / (kLane / 16) * h,
+                 in);
+      }
+    }
+  } while (c->next < end);
+}
+// The blocks that stages before `it` belong to; asks for what lies before `it`, adds up
+// what came before.
+template <int W>
+__device__ __forceinline__ void add_columns(const Params &p, uint8_t *buf, int it, long long m0,
+                                            int w, int lane, Columns *c) {
+  if (!p.cols.part) return;
+  const int end = p.pairs > 1 ? (it + p.pairs - 1) / p.pairs : it;
+  if (p.cols.dtype == VAE_F32)
+    turn_blocks<W, float>(p, buf, end, m0, w, lane, c);
+  else if (p.cols.dtype == VAE_BF16)
+    turn_blocks<W, bf16>(p, buf, end, m0, w, lane, c);
+  else
+    turn_blocks<W, __half>(p, buf, end, m0, w, lane, c);
+}
+// The first block of tile column `col` among those of stages from `it` on.
+__device__ __forceinline__ int first_block(const Params &p, int it, int col) {
+  if (!p.cols.part) return 0;
+  const int from = p.pairs > 1 ? (it + p.pairs - 1) / p.pairs : it;
+  return from + (col + p.n_tiles - from % p.n_tiles) % p.n_tiles;
+}
+// A warp's sums become row `part` of the partial ones.
+template <int W>
+__device__ __forceinline__ void put_columns(const Params &p, uint8_t *buf, int part, long long m0,
+                                            int w, int lane, Columns *c) {
+  if (!p.cols.part) return;
+  add_columns<W>(p, buf, 0, m0, w, lane, c);
+  __syncwarp();  // (the buffer is the warp's again)
+  Oct sum = c->sum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    sum.v[j] = add2(sum.v[j], __shfl_xor_sync(0xffffffffu, sum.v[j], 16));
+  const long long ch = m0 + 8 * lane;
+  if (lane < 16 && ch < p.m)
+    store_raw<float, false>(p.cols.part + part * p.m + ch, 8, raw_of<float>(sum));
+}
+
 // ------------------------------------------------------------------ small tiles
 // A 128 x 128 tile by a cluster of blocks that split the reduction: each adds up its
 // share of the stages, puts its sums into shared memory, and finishes 128 / S rows of
 // the tile from all of them, in the order of the blocks. Warp 0 copies, warp 1
-// multiplies, warps 2 to 5 take the sums out.
+// multiplies, the others take the sums out.
 constexpr int kTile = 128;
 constexpr int kTileStages = 6;
-constexpr int kTileThreads = 192;
+constexpr int kTileWarps = 8;  // that take sums out, 64 columns each
+constexpr int kTileCols = 4 * kTile / kTileWarps;
+constexpr int kTileThreads = 64 + 32 * kTileWarps;
 constexpr int kTileStageBytes = 2 * kTile * kBK * 2;
 constexpr int kSumLd = kTile + 4;  // floats of a row of sums: 16 bytes shift the banks
-constexpr size_t kTileSmem = kTileStages * kTileStageBytes + 1024 + 256;
+constexpr size_t kTileSmem =
+    kTileStages * kTileStageBytes + kTileWarps * kColumnBytes + 1024 + 256;
 static_assert(kTile * kSumLd * 4 <= kTileStages * kTileStageBytes, "sums lie over the stages");
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -288,7 +372,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kTileStages * kTileStageBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kTileStages * kTileStageBytes +
+                                                kTileWarps * kColumnBytes);
   uint64_t *empty = full + kTileStages;
   uint64_t *acc_full = empty + kTileStages, *acc_empty = acc_full + 2;
   uint64_t *drain = acc_empty + 2;
@@ -308,7 +393,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 4);
+      mbar_init(acc_empty + i, kTileWarps);
     }
     mbar_init(drain, 1);
     fence_mbarrier_init();
@@ -378,15 +463,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       drain_wait(drain, 0, p.wait_ns);
     }
   } else {
-    const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const int col = (warp - 2) / 4 * kTileCols;
+    uint8_t *buf = smem + kTileStages * kTileStageBytes + (warp - 2) * kColumnBytes;
+    const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + col;
     const int chunks = kFloat ? (its + kChain - 1) / kChain : its > 0;
-    float acc[kTile];
+    float acc[kTileCols];
     if (kFloat || chunks == 0) {
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) acc[j] = 0.f;
+      for (int j = 0; j < kTileCols; ++j) acc[j] = 0.f;
     }
     bool ok = true;
+    Columns cols;
+    if (kFloat) cols.next = first_block(p, it0, tile % p.n_tiles);
     for (int c = 0; c < chunks; ++c) {
+      if (kFloat)
+        add_columns<kTileWarps>(p, buf, it0 + min(its, (c + 1) * kChain), m0, warp - 2, lane, &cols);
       ok = mbar_wait(acc_full + (c & 1), c >> 1 & 1, abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
@@ -395,7 +486,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc_fence_after();
 #pragma unroll
-      for (int j = 0; j < kTile; j += 32) {
+      for (int j = 0; j < kTileCols; j += 32) {
         if constexpr (kFloat) {
           float v[32];
           tmem_ld_32cols(at + (c & 1) * kTile + j, v);
@@ -409,11 +500,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + (c & 1));
     }
+    if (kFloat)
+      put_columns<kTileWarps>(p, buf, (tile % p.n_tiles * splits + rank) * kTileWarps + warp - 2,
+                              m0, warp - 2, lane, &cols);
     if (ok) {
       // every stage has been read: the last sums came after it
-      float *sums = reinterpret_cast<float *>(smem) + (32 * (warp & 3) + lane) * kSumLd;
+      float *sums = reinterpret_cast<float *>(smem) + (32 * (warp & 3) + lane) * kSumLd + col;
 #pragma unroll
-      for (int j = 0; j < kTile; j += 4)
+      for (int j = 0; j < kTileCols; j += 4)
         *reinterpret_cast<float4 *>(sums + j) =
             make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
     }
@@ -484,7 +578,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // Persistent: a pair takes every (grid / 2)-th tile, and while sixteen warps of either
 // block finish a tile from one half of tensor memory, the next one's products go to
 // the other half. (Eight warps, two to a scheduler, did not hide each other's waits:
-// for 512 products a sum 38 us instead of TODO.)
+// for 16384 x 512 -> 2048 38 us instead of 32.)
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
 constexpr int kPairThreads = 576;
@@ -497,6 +591,8 @@ constexpr int kStaging = 2 * kChunkBytes;  // a warp's
 constexpr int kPairHead = 3072;            // barriers and rows of the bias
 constexpr size_t kPairSmem = kPairHead + kPairStages * kPairStageBytes + kPairWarps * kStaging;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
+
+static_assert(kStaging == kColumnBytes, "columns go through a warp's staging buffer");
 
 // The place of tile t in the result: bands of 8 rows of tiles, column by column, so
 // that the tiles under way at a time form a block as wide as it is high, whose
@@ -748,7 +844,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int j = 0; j < kWarpCols; ++j) acc[j] = 0.f;
         const int chunks = (p.its + kChain - 1) / kChain;
+        const long long first_row = place.m + 128ll * rank;
+        Columns cols;
+        cols.next = first_block(p, 0, place.n / kPairTile);
         for (int k = 0; k < chunks && ok; ++k, ++c) {
+          add_columns<kPairWarps>(p, buf, min(p.its, (k + 1) * kChain), first_row, warp - 2, lane,
+                                  &cols);
           ok = taken(c);
           if (!ok) break;
 #pragma unroll
@@ -761,6 +862,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           give_back(c);
         }
         if (!ok) break;
+        put_columns<kPairWarps>(p, buf, place.n / kPairTile * kPairWarps + warp - 2, first_row,
+                                warp - 2, lane, &cols);
 #pragma unroll
         for (int j = 0; j < kWarpCols; j += kChunk)
           finish_floats(p, buf, lane, acc + j, row, col + j);
@@ -881,7 +984,7 @@ cudaLaunchConfig_t launch_config(cudaLaunchAttribute *attr, unsigned grid, int t
   return cfg;
 }
 
-int tile_splits(long long tiles, int its) {
+int tile_splits(long long tiles, long long its) {
   int splits = 1;
   while (splits < 8 && tiles * splits * 2 <= num_sms() && its >= 4 * splits) splits *= 2;
   return splits;
@@ -889,7 +992,7 @@ int tile_splits(long long tiles, int its) {
 
 // Whether 256 x 256 tiles on pairs of SMs finish before 128 x 128 ones: rounds of
 // tiles times stages times the clocks of a stage.
-bool takes_pairs(long long m, int n, int its) {
+bool takes_pairs(long long m, int n, long long its) {
   const long long small = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
   const long long large = static_cast<long long>(ceil_div(m, kPairTile)) * ceil_div(n, kPairTile);
   const int s = tile_splits(small, its), sms = num_sms();
@@ -954,6 +1057,13 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
 
 }  // namespace
 
+int gemm_column_parts(long long m, int n, long long k, int parts) {
+  const long long its = (k + kBK - 1) / kBK * (parts > 1 ? 6 : 1);
+  if (takes_pairs(m, n, its)) return ceil_div(n, kPairTile) * kPairWarps;
+  const long long tiles = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
+  return ceil_div(n, kTile) * tile_splits(tiles, its) * kTileWarps;
+}
+
 int gemm(const GemmDesc &d, cudaStream_t s) {
   Params p{};
   p.m = d.m;
@@ -970,6 +1080,7 @@ int gemm(const GemmDesc &d, cudaStream_t s) {
   if (!p.err) return VAE_ECUDA;
   p.e = d.epi;
   p.kind = kind_of(d.epi);
+  p.cols = d.cols;
   return takes_pairs(d.m, d.n, p.its) ? launch_pair(d, p, s) : launch_tile(d, p, s);
 }
 

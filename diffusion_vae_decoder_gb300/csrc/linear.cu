@@ -85,37 +85,7 @@ int operands(GemmDesc *d, int dtype, const void *a, long long na, const void *b,
   return VAE_OK;
 }
 
-// ------------------------------------------------------------------ column sums
-// part [slabs][n]: sums of dy's columns over a slab's rows. A block has 256 columns,
-// eight to a thread, and eight rows at a time.
-template <class D, bool WIDE>
-__global__ void __launch_bounds__(256)
-    column_sums(const D *__restrict__ dy, long long rows, int n, float *part) {
-  __shared__ float4 red[8][32][2];
-  grid_release();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ch = 256 * blockIdx.x + 8 * lane;
-  Oct sum = {{0, 0, 0, 0}};
-#pragma unroll 4
-  for (long long r = 8ll * blockIdx.y + warp; r < rows; r += 8ll * gridDim.y) {
-    const Oct v = oct_of(load_raw<D, WIDE>(dy + r * n + ch, n - ch));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum.v[j] = add2(sum.v[j], v.v[j]);
-  }
-  red[warp][lane][0] = oct_lo(sum);
-  red[warp][lane][1] = oct_hi(sum);
-  __syncthreads();
-  if (warp == 0 && ch < n) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) {
-      const Oct o = oct_of(red[w][lane][0], red[w][lane][1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum.v[j] = add2(sum.v[j], o.v[j]);
-    }
-    store_raw<float, false>(part + static_cast<size_t>(blockIdx.y) * n + ch, n - ch,
-                            raw_of<float>(sum));
-  }
-}
+// out [n]: the sums of part [slabs][n], in a fixed order.
 __global__ void __launch_bounds__(256)
     merge_sums(const float *part, int slabs, int n, float *__restrict__ out) {
   __shared__ float red[8][32];
@@ -133,12 +103,6 @@ __global__ void __launch_bounds__(256)
     out[ch] = t;
   }
 }
-int sum_slabs(long long rows, int n) {
-  const int cols = ceil_div(n, 256);
-  return static_cast<int>(
-      std::max<long long>(1, std::min<long long>((rows + 31) / 32, 608 / cols)));
-}
-
 }  // namespace
 
 // ------------------------------------------------------------------ operators
@@ -176,7 +140,7 @@ int linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w
 size_t linear_wgrad_ws_bytes(int dtype, long long rows, int n, int k) {
   Carver cv(nullptr, 0);
   cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
-  cv.take<float>(static_cast<size_t>(sum_slabs(rows, n)) * n);
+  cv.take<float>(static_cast<size_t>(gemm_column_parts(n, k, rows, dtype == VAE_F32 ? 3 : 1)) * n);
   return cv.used;
 }
 
@@ -184,32 +148,22 @@ int linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n
                  float *dbias, void *ws, cudaStream_t s) {
   Carver cv(ws, ~size_t(0));
   void *parts = cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
-  const int slabs = sum_slabs(rows, n);
-  float *part = cv.take<float>(static_cast<size_t>(slabs) * n);
-  if (dbias) {
-    VAE_TRY(by_dtype(dtype, [&](auto t) -> int {
-      using D = decltype(t);
-      auto kernel = raw_wide<D>(n, dy) ? column_sums<D, true> : column_sums<D, false>;
-      kernel<<<dim3(ceil_div(n, 256), slabs), 256, 0, s>>>(static_cast<const D *>(dy), rows, n,
-                                                          slabs > 1 ? part : dbias);
-      VAE_LAUNCH_CHECK();
-      return VAE_OK;
-    }));
-    count_launches(1);
-    if (slabs > 1) {
-      VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, slabs, n, dbias));
-      count_launches(1);
-    }
-  }
   GemmDesc d;
   VAE_TRY(operands(&d, dtype, dy, rows * n, x, rows * k, parts, s));
+  const int slabs = gemm_column_parts(n, k, rows, d.parts);
+  float *part = cv.take<float>(static_cast<size_t>(slabs) * n);
   d.dtype = VAE_F32;
   d.a.k_major = d.b.k_major = false;
   d.m = n;
   d.n = k;
   d.k = rows;
   d.epi = {nullptr, nullptr, dw, nullptr, VAE_ACT_NONE, true};
-  return gemm(d, s);
+  if (dbias) d.cols = {dy, dtype, rows, part};
+  VAE_TRY(gemm(d, s));
+  if (!dbias) return VAE_OK;
+  VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, slabs, n, dbias));
+  count_launches(1);
+  return VAE_OK;
 }
 
 }  // namespace vae

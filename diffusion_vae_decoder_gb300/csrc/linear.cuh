@@ -38,6 +38,16 @@ struct GemmEpilogue {
   bool derivative = false;
 };
 
+// Sums over the reduction of A's columns, taken on the way: src [rows][m], the numbers
+// A's parts come from, of `dtype`. part [gemm_column_parts][m] receives partial sums
+// (NULL: none), whose sum in order is theirs. For float results.
+struct GemmColumnSums {
+  const void *src = nullptr;
+  int dtype = 0;
+  long long rows = 0;
+  float *part = nullptr;
+};
+
 // out[m][n] = sum over k of A[m][k] B[n][k], A and B of bf16 or f16 numbers, or, with
 // parts == 3, each the sum of three bf16 matrices (a float's 24 bits), of whose
 // products the six largest are added up. out, aux and keep are of `dtype`; a
@@ -53,7 +63,9 @@ struct GemmDesc {
   long long k = 0;
   bool wait = false;  // an operand is made by the launch before this one
   GemmEpilogue epi;
+  GemmColumnSums cols;
 };
+int gemm_column_parts(long long m, int n, long long k, int parts);
 int gemm(const GemmDesc &d, cudaStream_t s);
 
 }  // namespace vae
