@@ -18,7 +18,7 @@ SOURCES = ["igemm.cu", "igemm_split.cu", "igemm_xf.cu", "groupnorm.cu", "softmax
            "runtime.cu", "noalloc.cu", "head.cu", "head_tc.cu", "flash.cu", "splitk.cu", "peak.cu", "tiled.cu",
            "ckpt.cu", "gn_train.cu", "gn_resident.cu",
            "block_norm.cu", "wgrad.cu", "train.cu",
-           "layer_norm.cu", "dropout.cu", "gemm.cu", "linear.cu", "mlp.cu"]
+           "layer_norm.cu", "dropout.cu", "gemm.cu", "gemv.cu", "linear.cu", "mlp.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",

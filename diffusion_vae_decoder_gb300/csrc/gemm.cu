@@ -15,10 +15,8 @@
 // leave as 16-bit numbers do not need it.
 #include <atomic>
 
-#include "gn_train.cuh"
-#include "linear.cuh"
+#include "linear_epilogue.cuh"
 #include "ptx.cuh"
-#include "tokens.cuh"
 
 namespace vae {
 
@@ -57,99 +55,6 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
 // The parts that product q takes: hh, hm, mh, mm, hl, lh.
 __device__ __forceinline__ int part_a(int q) { return (0x201100 >> (4 * q)) & 15; }
 __device__ __forceinline__ int part_b(int q) { return (0x021010 >> (4 * q)) & 15; }
-
-// What becomes of a sum: KIND of an activation, or of its derivative at aux.
-enum Kind { kNone, kSilu, kGelu, kSiluSlope, kGeluSlope };
-int kind_of(const GemmEpilogue &e) {
-  if (e.act == VAE_ACT_NONE) return kNone;
-  const bool silu = e.act == VAE_ACT_SILU;
-  return e.derivative ? (silu ? kSiluSlope : kGeluSlope) : (silu ? kSilu : kGelu);
-}
-// f(integral_constant) with the launch's kind: one branch around a block of results,
-// where branches in it cost a third of a tile's time.
-template <class F>
-__device__ __forceinline__ void by_kind(int kind, F &&f) {
-  switch (kind) {
-    case kSilu: return f(std::integral_constant<int, kSilu>{});
-    case kGelu: return f(std::integral_constant<int, kGelu>{});
-    case kSiluSlope: return f(std::integral_constant<int, kSiluSlope>{});
-    case kGeluSlope: return f(std::integral_constant<int, kGeluSlope>{});
-    default: return f(std::integral_constant<int, kNone>{});
-  }
-}
-
-// max and min that give a NaN for one.
-__device__ __forceinline__ uint64_t at_least2(uint64_t z, float low) {
-  float a, b;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(lo2(z)), "f"(low));
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(hi2(z)), "f"(low));
-  return pk2(a, b);
-}
-__device__ __forceinline__ uint64_t at_most2(uint64_t z, float high) {
-  float a, b;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(lo2(z)), "f"(high));
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(hi2(z)), "f"(high));
-  return pk2(a, b);
-}
-
-// The activations are z sigmoid(v), v = z for SiLU and z (a + b z^2) for GELU in its
-// tanh form, a = sqrt(8 / pi), b = 0.044715 a. Beyond kFar both they and their
-// derivatives are, to far below float's resolution, what they are there on the
-// negative side (sigmoid 1e-38), and z and 1 on the positive one; z is held inside,
-// so that no power of it and no exponential overflows. A NaN stays one.
-constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.071354816f;
-template <int KIND>
-constexpr bool is_gelu = KIND == kGelu || KIND == kGeluSlope;
-template <int KIND>
-constexpr float kFar = is_gelu<KIND> ? 10.f : 87.f;
-// s = 1 / (1 + e) with e = e^-v, for v >= -87.4, by the exp2 and reciprocal units, to
-// 2^-21 and the rounding of v log2 e (2^-23 |v|), which PRECISE puts back for results
-// that are floats. (The reciprocal by Newton steps from an integer seed instead, for a
-// unit that takes a warp eight clocks: 33 us instead of 31 for 16384 x 512 -> 2048.)
-template <bool PRECISE>
-__device__ __forceinline__ uint64_t sigmoid_of(uint64_t v, uint64_t *e) {
-  const uint64_t t = mul2(v, pk2(-1.4426950408889634f, -1.4426950408889634f));
-  *e = pk2(ex2_approx(lo2(t)), ex2_approx(hi2(t)));
-  if constexpr (PRECISE) {
-    const uint64_t w = fma2(t, pk2(0.6931471805599453f, 0.6931471805599453f), v);
-    *e = fma2(mul2(*e, w), pk2(-1.f, -1.f), *e);
-  }
-  return rcp2(add2(*e, pk2(1.f, 1.f)));
-}
-template <int KIND, bool PRECISE>
-__device__ __forceinline__ uint64_t act2(uint64_t z) {
-  const uint64_t h = at_least2(z, -kFar<KIND>);
-  uint64_t v = h, e;
-  if (is_gelu<KIND>)
-    v = mul2(h, fma2(mul2(h, h), pk2(kGeluB, kGeluB), pk2(kGeluA, kGeluA)));
-  return mul2(h, sigmoid_of<PRECISE>(v, &e));
-}
-// act'(z) = s + z v' s (1 - s), with 1 - s = e s, which loses nothing where s is near 1.
-template <int KIND, bool PRECISE>
-__device__ __forceinline__ uint64_t act_slope2(uint64_t z) {
-  const uint64_t h = at_most2(at_least2(z, -kFar<KIND>), kFar<KIND>);
-  uint64_t v = h, w = h, e;  // w = z v'
-  if (is_gelu<KIND>) {
-    const uint64_t q = mul2(h, h), a = pk2(kGeluA, kGeluA);
-    v = mul2(h, fma2(q, pk2(kGeluB, kGeluB), a));
-    w = mul2(h, fma2(q, pk2(3.f * kGeluB, 3.f * kGeluB), a));
-  }
-  const uint64_t s = sigmoid_of<PRECISE>(v, &e);
-  return mul2(s, fma2(w, mul2(e, s), pk2(1.f, 1.f)));
-}
-
-// Two neighbouring sums of a row -> out, and z.
-template <int KIND, bool PRECISE>
-__device__ __forceinline__ uint64_t finish2(uint64_t sum, uint64_t bias, uint64_t aux,
-                                            uint64_t *z) {
-  if constexpr (KIND == kSiluSlope || KIND == kGeluSlope) {
-    return mul2(sum, act_slope2<KIND, PRECISE>(aux));
-  } else {
-    *z = add2(sum, bias);
-    if constexpr (KIND == kNone) return add2(*z, aux);
-    else return add2(act2<KIND, PRECISE>(*z), aux);
-  }
-}
 
 // Stage `it` of the tile at (m0, n0): `rows_a` and `rows_b` rows of the operands.
 // `load(dst, map, c0, c1, c2)` issues one copy.
@@ -227,7 +132,8 @@ __device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long lon
 
 // Sums of A's columns (the result's rows), by warps that wait for the tensor core: the
 // rows that the copies bring in at the same time are read once more, from L2, by one of
-// the tiles that share them: tile column j takes blocks j, j + n_tiles, ... of 64 rows.
+// the tiles that share them: on pairs of SMs tile column j takes blocks j, j + n_tiles,
+// ... of 64 rows (small tiles: the first column all of them).
 // Warp w of W takes every W-th pair of a block's rows of 128 numbers, a lane eight of
 // them, which it copies into its own places of the warp's buffer (kColumnBytes) and
 // adds up a chain of products later. (Through registers, whose loads the warp would
@@ -265,7 +171,7 @@ __device__ __forceinline__ void turn_blocks(const Params &p, uint8_t *buf, int e
     }
     c->waiting = 0;
 #pragma unroll 1
-    for (; c->waiting < kSlots && c->next < end; ++c->waiting, c->next += p.n_tiles) {
+    for (; c->waiting < kSlots && c->next < end; ++c->waiting, c->next += p.cols.step) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const long long r = static_cast<long long>(c->next) * kBK + 2 * (w + W * i) + (lane >> 4);
@@ -293,26 +199,17 @@ __device__ __forceinline__ void add_columns(const Params &p, uint8_t *buf, int i
   else
     turn_blocks<W, __half>(p, buf, end, m0, w, lane, c);
 }
-// The first block of tile column `col` among those of stages from `it` on.
-__device__ __forceinline__ int first_block(const Params &p, int it, int col) {
-  if (!p.cols.part) return 0;
-  const int from = p.pairs > 1 ? (it + p.pairs - 1) / p.pairs : it;
-  return from + (col + p.n_tiles - from % p.n_tiles) % p.n_tiles;
-}
-// A warp's sums become row `part` of the partial ones.
+// A warp's sums, eight columns each in lanes 0 to 15.
 template <int W>
-__device__ __forceinline__ void put_columns(const Params &p, uint8_t *buf, int part, long long m0,
-                                            int w, int lane, Columns *c) {
-  if (!p.cols.part) return;
+__device__ __forceinline__ Oct end_columns(const Params &p, uint8_t *buf, long long m0, int w,
+                                           int lane, Columns *c) {
   add_columns<W>(p, buf, 0, m0, w, lane, c);
   __syncwarp();  // (the buffer is the warp's again)
   Oct sum = c->sum;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     sum.v[j] = add2(sum.v[j], __shfl_xor_sync(0xffffffffu, sum.v[j], 16));
-  const long long ch = m0 + 8 * lane;
-  if (lane < 16 && ch < p.m)
-    store_raw<float, false>(p.cols.part + part * p.m + ch, 8, raw_of<float>(sum));
+  return sum;
 }
 
 // ------------------------------------------------------------------ small tiles
@@ -331,6 +228,11 @@ constexpr size_t kTileSmem =
     kTileStages * kTileStageBytes + kTileWarps * kColumnBytes + 1024 + 256;
 static_assert(kTile * kSumLd * 4 <= kTileStages * kTileStageBytes, "sums lie over the stages");
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -339,30 +241,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "memory");
   return v;
 }
-// Four numbers of type T, as two pairs.
-struct Quad {
-  uint64_t v[2];
-};
-template <class T>
-__device__ __forceinline__ Quad load_quad(const T *p) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
-    return {{pk2(f.x, f.y), pk2(f.z, f.w)}};
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return {{unpack2(u.x, T{}), unpack2(u.y, T{})}};
-  }
-}
-template <class T>
-__device__ __forceinline__ void store_quad(T *p, const Quad &q) {
-  if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<float4 *>(p) =
-        make_float4(lo2(q.v[0]), hi2(q.v[0]), lo2(q.v[1]), hi2(q.v[1]));
-  else
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(pack2(lo2(q.v[0]), hi2(q.v[0]), T{}), pack2(lo2(q.v[1]), hi2(q.v[1]), T{}));
-}
-
 template <class Out>
 __global__ void __launch_bounds__(kTileThreads, 1)
     gemm_tile(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -384,6 +262,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int m0 = tile / p.n_tiles * kTile, n0 = tile % p.n_tiles * kTile;
   const int it0 = static_cast<int>(static_cast<long long>(p.its) * rank / splits);
   const int its = static_cast<int>(static_cast<long long>(p.its) * (rank + 1) / splits) - it0;
+  // the tiles of the first column take the sums of A's columns
+  const bool columns = kFloat && p.cols.part && n0 == 0;
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
@@ -474,9 +354,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     bool ok = true;
     Columns cols;
-    if (kFloat) cols.next = first_block(p, it0, tile % p.n_tiles);
+    cols.next = p.pairs > 1 ? (it0 + p.pairs - 1) / p.pairs : it0;
     for (int c = 0; c < chunks; ++c) {
-      if (kFloat)
+      if (kFloat && columns)
         add_columns<kTileWarps>(p, buf, it0 + min(its, (c + 1) * kChain), m0, warp - 2, lane, &cols);
       ok = mbar_wait(acc_full + (c & 1), c >> 1 & 1, abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
@@ -500,9 +380,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + (c & 1));
     }
-    if (kFloat)
-      put_columns<kTileWarps>(p, buf, (tile % p.n_tiles * splits + rank) * kTileWarps + warp - 2,
-                              m0, warp - 2, lane, &cols);
+    if (kFloat && columns) {  // into the warp's buffer, for all blocks of the cluster
+      const Oct sum = end_columns<kTileWarps>(p, buf, m0, warp - 2, lane, &cols);
+      if (lane < 16) {
+        float4 *to = reinterpret_cast<float4 *>(buf) + 2 * lane;
+        to[0] = oct_lo(sum);
+        to[1] = oct_hi(sum);
+      }
+    }
     if (ok) {
       // every stage has been read: the last sums came after it
       float *sums = reinterpret_cast<float *>(smem) + (32 * (warp & 3) + lane) * kSumLd + col;
@@ -524,6 +409,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (!*abort) {
     const int share = kTile / splits, r0 = rank * share;
+    if (columns && static_cast<int>(threadIdx.x) < share) {
+      const int c = r0 + threadIdx.x;
+      const float *mine =
+          reinterpret_cast<const float *>(smem + kTileStages * kTileStageBytes) + c;
+      float sum = 0.f;
+      for (int b = 0; b < splits; ++b) {
+        const uint32_t from = splits > 1 ? mapa_rank(mine, b) : smem_u32(mine);
+#pragma unroll
+        for (int w = 0; w < kTileWarps; ++w) sum += ld_cluster_f32(from + w * kColumnBytes);
+      }
+      if (m0 + c < p.m) p.cols.part[m0 + c] = sum;
+    }
     const int col = n0 + 4 * lane;
     const bool in = col < p.n;
     Out *out = static_cast<Out *>(p.e.out), *keep = static_cast<Out *>(p.e.keep);
@@ -846,7 +743,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int chunks = (p.its + kChain - 1) / kChain;
         const long long first_row = place.m + 128ll * rank;
         Columns cols;
-        cols.next = first_block(p, 0, place.n / kPairTile);
+        cols.next = place.n / kPairTile;
         for (int k = 0; k < chunks && ok; ++k, ++c) {
           add_columns<kPairWarps>(p, buf, min(p.its, (k + 1) * kChain), first_row, warp - 2, lane,
                                   &cols);
@@ -862,8 +759,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           give_back(c);
         }
         if (!ok) break;
-        put_columns<kPairWarps>(p, buf, place.n / kPairTile * kPairWarps + warp - 2, first_row,
-                                warp - 2, lane, &cols);
+        if (p.cols.part) {
+          const Oct sum = end_columns<kPairWarps>(p, buf, first_row, warp - 2, lane, &cols);
+          const long long ch = first_row + 8 * lane, part = place.n / kPairTile * kPairWarps + warp - 2;
+          if (lane < 16 && ch < p.m)
+            store_raw<float, false>(p.cols.part + part * p.m + ch, 8, raw_of<float>(sum));
+        }
 #pragma unroll
         for (int j = 0; j < kWarpCols; j += kChunk)
           finish_floats(p, buf, lane, acc + j, row, col + j);
@@ -1017,6 +918,7 @@ int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
   p.idesc = idesc_16bit(kPairTile, kPairTile, !d.f16, !d.a.k_major, !d.b.k_major);
   p.m_tiles = ceil_div(d.m, kPairTile);
   p.n_tiles = ceil_div(d.n, kPairTile);
+  p.cols.step = p.n_tiles;
   const unsigned grid = 2 * std::min(p.m_tiles * p.n_tiles, num_sms() / 2);
   return by_dtype(d.dtype, [&](auto o) -> int {
     using Out = decltype(o);
@@ -1039,6 +941,7 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
   p.idesc = idesc_16bit(kTile, kTile, !d.f16, !d.a.k_major, !d.b.k_major);
   p.m_tiles = ceil_div(d.m, kTile);
   p.n_tiles = ceil_div(d.n, kTile);
+  p.cols.step = 1;
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
   const int splits = tile_splits(tiles, p.its);
   if (tiles * splits > 0x7fffffff) return VAE_EUNSUPPORTED;
@@ -1059,9 +962,7 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
 
 int gemm_column_parts(long long m, int n, long long k, int parts) {
   const long long its = (k + kBK - 1) / kBK * (parts > 1 ? 6 : 1);
-  if (takes_pairs(m, n, its)) return ceil_div(n, kPairTile) * kPairWarps;
-  const long long tiles = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
-  return ceil_div(n, kTile) * tile_splits(tiles, its) * kTileWarps;
+  return takes_pairs(m, n, its) ? ceil_div(n, kPairTile) * kPairWarps : 1;
 }
 
 int gemm(const GemmDesc &d, cudaStream_t s) {

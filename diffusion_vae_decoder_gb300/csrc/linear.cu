@@ -107,11 +107,14 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ operators
 size_t linear_ws_bytes(int dtype, long long rows, int n, int k) {
-  return parts_bytes(dtype, rows * k, static_cast<long long>(n) * k);
+  return rows <= kFewRows ? 0 : parts_bytes(dtype, rows * k, static_cast<long long>(n) * k);
 }
 
 int linear(const void *x, int dtype, long long rows, int k, const void *w, const float *bias,
            int n, int act, const void *residual, void *y, void *z, void *ws, cudaStream_t s) {
+  if (rows <= kFewRows)
+    return linear_few(x, dtype, static_cast<int>(rows), k, w, n, {bias, residual, y, z, act, false},
+                      s);
   GemmDesc d;
   VAE_TRY(operands(&d, dtype, x, rows * k, w, static_cast<long long>(n) * k, ws, s));
   d.m = rows;
@@ -140,7 +143,8 @@ int linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w
 size_t linear_wgrad_ws_bytes(int dtype, long long rows, int n, int k) {
   Carver cv(nullptr, 0);
   cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
-  cv.take<float>(static_cast<size_t>(gemm_column_parts(n, k, rows, dtype == VAE_F32 ? 3 : 1)) * n);
+  const int slabs = gemm_column_parts(n, k, rows, dtype == VAE_F32 ? 3 : 1);
+  if (slabs > 1) cv.take<float>(static_cast<size_t>(slabs) * n);
   return cv.used;
 }
 
@@ -151,7 +155,7 @@ int linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n
   GemmDesc d;
   VAE_TRY(operands(&d, dtype, dy, rows * n, x, rows * k, parts, s));
   const int slabs = gemm_column_parts(n, k, rows, d.parts);
-  float *part = cv.take<float>(static_cast<size_t>(slabs) * n);
+  float *part = slabs > 1 ? cv.take<float>(static_cast<size_t>(slabs) * n) : dbias;
   d.dtype = VAE_F32;
   d.a.k_major = d.b.k_major = false;
   d.m = n;
@@ -160,7 +164,7 @@ int linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n
   d.epi = {nullptr, nullptr, dw, nullptr, VAE_ACT_NONE, true};
   if (dbias) d.cols = {dy, dtype, rows, part};
   VAE_TRY(gemm(d, s));
-  if (!dbias) return VAE_OK;
+  if (!dbias || slabs == 1) return VAE_OK;
   VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, slabs, n, dbias));
   count_launches(1);
   return VAE_OK;

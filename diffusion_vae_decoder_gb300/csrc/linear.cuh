@@ -40,12 +40,14 @@ struct GemmEpilogue {
 
 // Sums over the reduction of A's columns, taken on the way: src [rows][m], the numbers
 // A's parts come from, of `dtype`. part [gemm_column_parts][m] receives partial sums
-// (NULL: none), whose sum in order is theirs. For float results.
+// (NULL: none), whose sum in order is theirs; the sums themselves where there is one.
+// For float results.
 struct GemmColumnSums {
   const void *src = nullptr;
   int dtype = 0;
   long long rows = 0;
   float *part = nullptr;
+  int step = 1;  // (the launch's: blocks of 64 rows from one to the next)
 };
 
 // out[m][n] = sum over k of A[m][k] B[n][k], A and B of bf16 or f16 numbers, or, with
@@ -67,5 +69,10 @@ struct GemmDesc {
 };
 int gemm_column_parts(long long m, int n, long long k, int parts);
 int gemm(const GemmDesc &d, cudaStream_t s);
+
+// The same as linear() for few rows, on the FP32 cores (gemv.cu).
+constexpr int kFewRows = 8;
+int linear_few(const void *x, int dtype, int rows, int k, const void *w, int n,
+               const GemmEpilogue &e, cudaStream_t s);
 
 }  // namespace vae

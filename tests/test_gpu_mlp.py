@@ -118,7 +118,7 @@ def test_layer_norm_keeps_bad_rows_apart(vae):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,c", NORM_SIZES + [(5000, 32), (2500, 1024)])
+@pytest.mark.parametrize("rows,c", NORM_SIZES + [(2048, 512), (2049, 512), (5000, 32), (2500, 1024)])
 def test_layer_norm_backward(vae, rows, c, dtype):
     t = R.DTYPES[dtype]
     x = rand(rows + c, rows, c, dtype=t, std=2.0, mean=0.7)
@@ -140,8 +140,9 @@ def test_layer_norm_backward(vae, rows, c, dtype):
            (6 * tt.abs() + (SUM + 6) * m1 + xh.abs() * (SUM + 12) * m2) +
            U * (2 * ref.abs() + (0 if dres is None else dres.double().abs())))
     close(dx, ref, tol, "dx")
-    # a column: rows / blocks numbers in a thread, then at most 32 + 10 + 5 sums
-    chain = rows / 304 * max(1, 256 * 8 / c) + 64
+    # a column: rows / blocks numbers in a thread, then at most 32 + 10 + 5 sums; few
+    # rows: rows / 32 in a thread, then 64 threads
+    chain = max(rows / 304 * max(1, 256 * 8 / c) + 64, rows / 32 + 64)
     close(dgamma, rg, U * (chain + 4) * (dy64 * xh).abs().sum(0), "dgamma")
     close(dbeta, rb, U * chain * dy64.abs().sum(0), "dbeta")
     # dx over dy, and over dres

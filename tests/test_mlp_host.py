@@ -65,7 +65,7 @@ A = ctypes.c_void_p(4096)   # aligned; never read: every call is refused first
 ODD = ctypes.c_void_p(4100)
 OK = {
     "vae_layer_norm": [A, 1, 8, 64, 1e-6, A, A, A, A, None],
-    "vae_layer_norm_backward": [A, A, 1, A, 8, 64, A, A, A, A, A, A, 1 << 30, None],
+    "vae_layer_norm_backward": [A, A, 1, A, 100000, 64, A, A, A, A, A, A, 1 << 30, None],
     "vae_dropout": [A, 1, 64, 0.1, 1, 2, None, A, A, None],
     "vae_linear": [A, 1, 8, 64, A, A, 64, 1, A, A, A, A, 1 << 30, None],
     "vae_linear_dgrad": [A, 1, 8, 64, A, 64, 1, A, A, A, 1 << 30, None],
@@ -137,7 +137,9 @@ def test_workspace_sizes(lib):
     assert lib.vae_linear_workspace_size(0, 1000, 64, 128) >= 6 * (1000 * 128 + 64 * 128)
     assert lib.vae_linear_dgrad_workspace_size(0, 1000, 64, 128) >= 6 * (1000 * 64 + 64 * 128)
     assert lib.vae_linear_wgrad_workspace_size(0, 1000, 64, 128) >= 6 * 1000 * (64 + 128)
-    assert lib.vae_layer_norm_backward_workspace_size(1000, 64) > 0
+    assert lib.vae_layer_norm_backward_workspace_size(100000, 64) > 0
+    assert lib.vae_layer_norm_backward_workspace_size(1000, 64) == 0  # (one launch)
+    assert lib.vae_linear_workspace_size(0, 8, 64, 64) == 0
     for bad in ((7, 10, 64, 64), (1, 0, 64, 64), (1, 10, 63, 64), (1, 10, 64, 63)):
         assert lib.vae_linear_workspace_size(*bad) == 0
         assert lib.vae_linear_dgrad_workspace_size(*bad) == 0
