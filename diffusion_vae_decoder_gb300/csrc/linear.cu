@@ -103,6 +103,27 @@ __global__ void __launch_bounds__(256)
     out[ch] = t;
   }
 }
+// dw [count] and dbias [n]: the sums of `slices` arrays [count + n], in order.
+__global__ void __launch_bounds__(256)
+    merge_slices(const float *part, int slices, long long count, int n, float *__restrict__ dw,
+                 float *__restrict__ dbias) {
+  grid_wait();
+  const long long stride = count + n, step = 4ll * gridDim.x * 256;
+  for (long long i = 4 * (blockIdx.x * 256ll + threadIdx.x); i < (dbias ? stride : count);
+       i += step) {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) {
+      const float4 v = *reinterpret_cast<const float4 *>(part + s * stride + i);
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
+    }
+    *reinterpret_cast<float4 *>(i < count ? dw + i : dbias + i - count) = t;
+  }
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ operators
@@ -140,11 +161,19 @@ int linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w
   return gemm(d, s);
 }
 
+namespace {
+// Numbers of the workspace that the sums go through.
+size_t sums_of(const GemmPlan &p, int n, int k) {
+  if (p.slices > 1) return static_cast<size_t>(p.slices) * n * (k + 1ll);
+  return p.columns > 1 ? static_cast<size_t>(p.columns) * n : 0;
+}
+}  // namespace
+
 size_t linear_wgrad_ws_bytes(int dtype, long long rows, int n, int k) {
   Carver cv(nullptr, 0);
   cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
-  const int slabs = gemm_column_parts(n, k, rows, dtype == VAE_F32 ? 3 : 1);
-  if (slabs > 1) cv.take<float>(static_cast<size_t>(slabs) * n);
+  const size_t sums = sums_of(gemm_plan(n, k, rows, dtype == VAE_F32 ? 3 : 1), n, k);
+  if (sums) cv.take<float>(sums);
   return cv.used;
 }
 
@@ -154,19 +183,31 @@ int linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n
   void *parts = cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
   GemmDesc d;
   VAE_TRY(operands(&d, dtype, dy, rows * n, x, rows * k, parts, s));
-  const int slabs = gemm_column_parts(n, k, rows, d.parts);
-  float *part = slabs > 1 ? cv.take<float>(static_cast<size_t>(slabs) * n) : dbias;
+  const GemmPlan plan = gemm_plan(n, k, rows, d.parts);
+  const size_t sums = sums_of(plan, n, k);
+  float *part = sums ? cv.take<float>(sums) : nullptr;
+  const long long count = static_cast<long long>(n) * k;
   d.dtype = VAE_F32;
   d.a.k_major = d.b.k_major = false;
   d.m = n;
   d.n = k;
   d.k = rows;
-  d.epi = {nullptr, nullptr, dw, nullptr, VAE_ACT_NONE, true};
-  if (dbias) d.cols = {dy, dtype, rows, part};
+  d.slices = plan.slices;
+  d.epi = {nullptr, nullptr, plan.slices > 1 ? part : dw, nullptr, VAE_ACT_NONE, true};
+  if (dbias)
+    d.cols = {dy, dtype, rows, plan.slices > 1 ? part + count : sums ? part : dbias};
   VAE_TRY(gemm(d, s));
-  if (!dbias || slabs == 1) return VAE_OK;
-  VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, slabs, n, dbias));
-  count_launches(1);
+  if (plan.slices > 1) {
+    const unsigned grid = static_cast<unsigned>(
+        std::min<long long>((count + n + 1023) / 1024, 4ll * num_sms()));
+    VAE_CUDA_TRY(launch_after(merge_slices, grid, 256, 0, s, part, plan.slices, count, n, dw,
+                              dbias));
+    count_launches(1);
+  } else if (dbias && sums) {
+    VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, plan.columns, n,
+                              dbias));
+    count_launches(1);
+  }
   return VAE_OK;
 }
 

@@ -38,10 +38,14 @@ struct GemmEpilogue {
   bool derivative = false;
 };
 
+// How the sums of a long reduction come: those of the result in `slices` arrays, to be
+// added up in order, and those of A's columns in `columns` of them (slices > 1: in as
+// many, each behind its slice's m n sums).
+struct GemmPlan {
+  int slices, columns;
+};
 // Sums over the reduction of A's columns, taken on the way: src [rows][m], the numbers
-// A's parts come from, of `dtype`. part [gemm_column_parts][m] receives partial sums
-// (NULL: none), whose sum in order is theirs; the sums themselves where there is one.
-// For float results.
+// A's parts come from, of `dtype`; part [columns][m] (NULL: none). For float results.
 struct GemmColumnSums {
   const void *src = nullptr;
   int dtype = 0;
@@ -66,8 +70,9 @@ struct GemmDesc {
   bool wait = false;  // an operand is made by the launch before this one
   GemmEpilogue epi;
   GemmColumnSums cols;
+  int slices = 1;  // gemm_plan's: epi.out [slices][m n + m] (float sums alone)
 };
-int gemm_column_parts(long long m, int n, long long k, int parts);
+GemmPlan gemm_plan(long long m, int n, long long k, int parts);
 int gemm(const GemmDesc &d, cudaStream_t s);
 
 // The same as linear() for few rows, on the FP32 cores (gemv.cu).
