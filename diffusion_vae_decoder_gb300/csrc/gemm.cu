@@ -221,6 +221,7 @@ __device__ __forceinline__ Oct end_columns(const Params &p, uint8_t *buf, long l
 // multiplies, the others take the sums out.
 constexpr int kTile = 128;
 constexpr int kTileStages = 6;
+constexpr int kMaxSplits = 8;  // blocks of a cluster
 constexpr int kTileWarps = 8;  // that take sums out, 64 columns each
 constexpr int kTileCols = 4 * kTile / kTileWarps;
 constexpr int kTileThreads = 64 + 32 * kTileWarps;
@@ -451,11 +452,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (splits == 1) {
           sum = load_quad(mine);
         } else {
-          sum = {{0, 0}};
-          for (int s = 0; s < splits; ++s) {
-            const float4 f = ld_cluster_f4(mapa_rank(mine, s));
-            sum.v[0] = add2(sum.v[0], pk2(f.x, f.y));
-            sum.v[1] = add2(sum.v[1], pk2(f.z, f.w));
+          // (all in flight: one after another, eight blocks' take 5 us)
+          float4 f[kMaxSplits];
+#pragma unroll
+          for (int s = 0; s < kMaxSplits; ++s)
+            if (s < splits) f[s] = ld_cluster_f4(mapa_rank(mine, s));
+          sum = {{pk2(f[0].x, f[0].y), pk2(f[0].z, f[0].w)}};
+#pragma unroll
+          for (int s = 1; s < kMaxSplits; ++s) {
+            if (s >= splits) break;
+            sum.v[0] = add2(sum.v[0], pk2(f[s].x, f[s].y));
+            sum.v[1] = add2(sum.v[1], pk2(f[s].z, f[s].w));
           }
         }
         if (!in) continue;
@@ -889,22 +896,54 @@ cudaLaunchConfig_t launch_config(cudaLaunchAttribute *attr, unsigned grid, int t
   return cfg;
 }
 
-int tile_splits(long long tiles, long long its) {
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= num_sms() && its >= 4 * splits) splits *= 2;
-  return splits;
+// Clusters of `splits` blocks that run at a time (76, 36 and 15 of 2, 4 and 8 on a
+// GB300, whose SMs are not grouped in multiples of eight), asked once a device.
+int clusters_at_once(int splits) {
+  static std::atomic<int> known[64][kMaxSplits + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return std::max(1, num_sms() / splits);
+  }
+  int n = known[dev][splits].load(std::memory_order_relaxed);
+  if (n) return n;
+  static std::atomic<uint64_t> done{0};
+  cudaLaunchAttribute attr[2];
+  const auto cfg = launch_config(attr, splits, kTileThreads, kTileSmem, splits, false, nullptr);
+  if (splits == 1 || allow_smem(gemm_tile<float>, kTileSmem, &done) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, gemm_tile<float>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = std::max(1, num_sms() / splits);
+  }
+  known[dev][splits].store(n, std::memory_order_relaxed);
+  return n;
 }
 
-// Whether 256 x 256 tiles on pairs of SMs finish before 128 x 128 ones: rounds of
-// tiles times stages times the clocks of a stage.
+// How many blocks share a 128 x 128 tile's reduction, and the clocks it takes: rounds of
+// clusters times what a block does besides and its stages.
+struct Tiling {
+  int splits;
+  long long clocks;
+};
+Tiling small_tiling(long long tiles, long long its) {
+  Tiling best{1, 0};
+  for (int s = 1; s <= kMaxSplits; s *= 2) {
+    if (s > 1 && its < 2 * s) break;
+    const long long at_once = clusters_at_once(s);
+    const long long t =
+        (tiles + at_once - 1) / at_once * (4000 + 300 * s + 512 * ((its + s - 1) / s));
+    if (s == 1 || t < best.clocks) best = {s, t};
+  }
+  return best;
+}
+
+// Whether 256 x 256 tiles on pairs of SMs finish before 128 x 128 ones.
 bool takes_pairs(long long m, int n, long long its) {
   const long long small = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
   const long long large = static_cast<long long>(ceil_div(m, kPairTile)) * ceil_div(n, kPairTile);
-  const int s = tile_splits(small, its), sms = num_sms();
-  if (sms < 2 || large > 0x0fffffff) return false;
-  const long long t_small = (small * s + sms - 1) / sms * (4000 + 512ll * ((its + s - 1) / s));
-  const long long t_large = 3000 + (large + sms / 2 - 1) / (sms / 2) * (1000 + 600ll * its);
-  return t_large < t_small;
+  const int pairs = num_sms() / 2;
+  if (!pairs || large > 0x0fffffff) return false;
+  return 3000 + (large + pairs - 1) / pairs * (1000 + 600 * its) < small_tiling(small, its).clocks;
 }
 
 int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
@@ -947,7 +986,7 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
   p.n_tiles = ceil_div(d.n, kTile);
   p.cols.step = 1;
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
-  const int splits = tile_splits(tiles, p.its);
+  const int splits = small_tiling(tiles, p.its).splits;
   p.slices = d.slices;
   p.stride = d.slices > 1 ? d.m * d.n + d.m : 0;
   if (tiles * splits * p.slices > 0x7fffffff) return VAE_EUNSUPPORTED;
@@ -972,9 +1011,9 @@ GemmPlan gemm_plan(long long m, int n, long long k, int parts) {
   // a block's 24 stages and more are shared by idle SMs, eight stages at least to each:
   // 4575 x 256 x 128 floats 15.8 us, 30.2 in one slice; 24576 x 128 x 128 bf16 12.1.
   const long long tiles = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
-  const long long splits = tile_splits(tiles, its);
+  const int splits = small_tiling(tiles, its).splits;
   if (its < 24 * splits) return {1, 1};
-  const long long most = std::min(num_sms() / (tiles * splits), its / (8 * splits));
+  const long long most = std::min(clusters_at_once(splits) / tiles, its / (8 * splits));
   return {static_cast<int>(std::max(1ll, most)), 1};
 }
 
