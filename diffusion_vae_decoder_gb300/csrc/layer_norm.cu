@@ -9,11 +9,16 @@
 // A row stays in the registers of T threads, eight numbers each in packed pairs of
 // floats, whatever the type in memory: x is read once and the squares are of
 // deviations from the mean, so that a mean far from zero costs nothing. The next
-// row's loads are issued before a row is worked on. The column sums of the backward
+// rows' loads are issued before a row is worked on (kAhead). The column sums of the backward
 // pass run in registers over the rows of a block (a thread adds up rows / blocks
 // numbers) and meet in a second, short kernel in a fixed order. Few rows take one
 // launch and no workspace: further blocks of it read the rows once more, column by
 // column, from L2 (small_columns).
+//
+// HBM bounds both, latency and the launch small calls. Measured, forward: 65536 x 1024
+// bf16 52 us (5.1 TB/s), 16384 x 512 8.1 us (from L2), one float row of 512 2.1 us.
+// Backward with dres: 16384 x 1024 bf16 28 us (4.7 TB/s; 33 us with one row's loads
+// under way), float 45 us (5.9 TB/s); three blocks an SM instead of two 35 and 52 us.
 #include <cmath>
 
 #include "layer_norm.cuh"
@@ -25,6 +30,11 @@ namespace vae {
 namespace {
 
 constexpr int kBwdBlocks = 2 * 152;
+
+// Rows whose loads are under way while one is worked on: two of 16-bit numbers, as
+// many bytes as one of floats (one where the registers hold two octs a thread).
+template <class D, int NV>
+constexpr int kAhead = sizeof(D) == 4 || NV > 1 ? 1 : 2;
 
 template <int T>
 constexpr int block_threads() { return T > 256 ? T : 256; }
@@ -70,15 +80,17 @@ __global__ void __launch_bounds__(block_threads<T>())
   const int tid = threadIdx.x % T;
   const unsigned step = gridDim.x * R;
   unsigned row = blockIdx.x * R + threadIdx.x / T;
-  Raw<D> next[NV];
-  auto fetch = [&](unsigned r) {
+  constexpr int P = kAhead<D, NV>;
+  Raw<D> next[P][NV];
+  auto fetch = [&](unsigned r, int slot) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ch = 8 * (i * T + tid);
-      next[i] = load_raw<D, WIDE>(x + static_cast<size_t>(r) * c + ch, r < rows ? c - ch : 0);
+      next[slot][i] = load_raw<D, WIDE>(x + static_cast<size_t>(r) * c + ch, r < rows ? c - ch : 0);
     }
   };
-  fetch(row);
+#pragma unroll
+  for (int q = 0; q < P; ++q) fetch(row + q * step, q);
   Oct g[NV], b[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -87,17 +99,20 @@ __global__ void __launch_bounds__(block_threads<T>())
   }
   const float inv_c = 1.f / c;
   // whole blocks leave the loop together: every lane takes part in the shuffles
-  for (unsigned r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step) {
+  for (unsigned long long r0 = blockIdx.x * R; r0 < rows; r0 += P * step) {
+#pragma unroll
+   for (int q = 0; q < P; ++q, row += step) {
+    if (q && r0 + q * step >= rows) break;
     const bool live = row < rows;
     Oct v[NV];
     uint64_t sum = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      v[i] = oct_of(next[i]);
+      v[i] = oct_of(next[q][i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum = add2(sum, v[i].v[j]);
     }
-    if (r0 + step < rows) fetch(row + step);
+    if (r0 + (q + P) * step < rows) fetch(row + P * step, q);
     const float mean = row_sum<T>(total(sum), buf[0]) * inv_c;
     uint64_t ss = 0;
 #pragma unroll
@@ -120,6 +135,7 @@ __global__ void __launch_bounds__(block_threads<T>())
     }
     if (stats && live && tid == 0)
       *reinterpret_cast<float2 *>(stats + 2 * static_cast<size_t>(row)) = make_float2(mean, rstd);
+   }
   }
 }
 
@@ -192,21 +208,23 @@ __global__ void __launch_bounds__(block_threads<T>())
   const int tid = threadIdx.x % T, grp = threadIdx.x / T;
   const unsigned step = row_blocks * R;
   unsigned row = blockIdx.x * R + grp;
-  Raw<D> xn[NV], dn[NV], rn[NV];
-  float2 sn;
-  auto fetch = [&](unsigned r) {
+  constexpr int P = kAhead<D, NV>;
+  Raw<D> xn[P][NV], dn[P][NV], rn[P][NV];
+  float2 sn[P];
+  auto fetch = [&](unsigned r, int slot) {
     const bool live = r < rows;
-    sn = live ? __ldg(reinterpret_cast<const float2 *>(stats) + r) : make_float2(0.f, 0.f);
+    sn[slot] = live ? __ldg(reinterpret_cast<const float2 *>(stats) + r) : make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ch = 8 * (i * T + tid), left = live ? c - ch : 0;
       const size_t at = static_cast<size_t>(r) * c + ch;
-      xn[i] = load_raw<D, WIDE>(x + at, left);
-      dn[i] = load_raw<D, WIDE>(dy + at, left);
-      if (dres) rn[i] = load_raw<D, WIDE>(dres + at, left);
+      xn[slot][i] = load_raw<D, WIDE>(x + at, left);
+      dn[slot][i] = load_raw<D, WIDE>(dy + at, left);
+      if (dres) rn[slot][i] = load_raw<D, WIDE>(dres + at, left);
     }
   };
-  fetch(row);
+#pragma unroll
+  for (int q = 0; q < P; ++q) fetch(row + q * step, q);
   Oct g[NV], sg[NV], sb[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -215,16 +233,19 @@ __global__ void __launch_bounds__(block_threads<T>())
   }
   const float inv_c = 1.f / c;
   int turn = 0;
-  for (unsigned r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step) {
+  for (unsigned long long r0 = blockIdx.x * R; r0 < rows; r0 += P * step) {
+#pragma unroll
+   for (int q = 0; q < P; ++q, row += step) {
+    if (q && r0 + q * step >= rows) break;
     const bool live = row < rows;
     Oct xh[NV], t[NV], res[NV];
-    const float mean = sn.x, rstd = sn.y;
+    const float mean = sn[q].x, rstd = sn[q].y;
     uint64_t st = 0, sx = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      xh[i] = oct_of(xn[i]);
-      t[i] = oct_of(dn[i]);
-      if (dres) res[i] = oct_of(rn[i]);
+      xh[i] = oct_of(xn[q][i]);
+      t[i] = oct_of(dn[q][i]);
+      if (dres) res[i] = oct_of(rn[q][i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         xh[i].v[j] = mul2(add2(xh[i].v[j], both(-mean)), both(rstd));
@@ -237,7 +258,7 @@ __global__ void __launch_bounds__(block_threads<T>())
         sx = fma2(t[i].v[j], xh[i].v[j], sx);
       }
     }
-    if (r0 + step < rows) fetch(row + step);
+    if (r0 + (q + P) * step < rows) fetch(row + P * step, q);
     const float2 s = row_sum2<T>(make_float2(total(st), total(sx)), buf[turn]);
     turn ^= 1;
     const uint64_t m1 = both(-s.x * inv_c), m2 = both(-s.y * inv_c), r2 = both(rstd);
@@ -252,6 +273,7 @@ __global__ void __launch_bounds__(block_threads<T>())
       }
       store_raw<D, WIDE>(dx + static_cast<size_t>(row) * c + ch, live ? c - ch : 0, raw_of<D>(o));
     }
+   }
   }
   if (SMALL) return;
   if (R > 1) {
@@ -338,7 +360,9 @@ int by_width(int c, F &&f) {
 int bwd_blocks(long long rows, int c) {
   const int octs = ceil_div(c, 8);
   const int r = octs <= 8 ? 32 : octs <= 32 ? 8 : octs <= 64 ? 4 : octs <= 128 ? 2 : 1;
-  return static_cast<int>(std::min<long long>(kBwdBlocks, (rows + r - 1) / r));
+  // (two octs a thread: one block an SM; a second round of them costs 5 %)
+  return static_cast<int>(std::min<long long>(octs > 256 ? kBwdBlocks / 2 : kBwdBlocks,
+                                              (rows + r - 1) / r));
 }
 
 }  // namespace
