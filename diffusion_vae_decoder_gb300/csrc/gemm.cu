@@ -47,11 +47,13 @@ __device__ __forceinline__ void raise_error(const Params &p, volatile uint32_t *
   *abort = 1u;
   atomicCAS(p.err, 0, static_cast<int>(VAE_EDEVICE_TIMEOUT));
 }
-// Used only while draining after an abort.
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+// Waits for products or copies that are under way before a block leaves: 10 ms at
+// most, whatever limit the other waits have, where they take microseconds.
+constexpr uint64_t kDrainNs = 10000000;
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity))
-    if (global_timer_ns() - t0 > limit_ns) return;
+    if (global_timer_ns() - t0 > kDrainNs) return;
 }
 
 // The parts that product q takes: hh, hm, mh, mm, hl, lh.
@@ -121,14 +123,13 @@ struct Ring {
 };
 // After an abort: what was asked for in the last stages before `r` lands.
 template <int N>
-__device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long long asked,
-                                             uint64_t limit_ns) {
+__device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long long asked) {
   for (int j = 0; j < N && j < asked; ++j) {
     if (r.s-- == 0) {
       r.s = N - 1;
       r.round ^= 1;
     }
-    drain_wait(full + r.s, r.round, limit_ns);
+    drain_wait(full + r.s, r.round);
   }
 }
 
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     }
-    if (*abort && lane == 0) drain_stages(full, r, i, p.wait_ns);  // before the block leaves
+    if (*abort && lane == 0) drain_stages(full, r, i);  // before the block leaves
   } else if (warp == 1) {
     // The whole warp goes through the loop, so that descriptors stay in registers that
     // all lanes share, and one lane issues (the same one every time).
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // whatever became of the sums, no product is left when tensor memory is freed
     if (elect_one()) {
       umma_commit(drain);
-      drain_wait(drain, 0, p.wait_ns);
+      drain_wait(drain, 0);
     }
   } else {
     const int col = (warp - 2) / 4 * kTileCols;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (p.e.bias && in) bias = load_quad(p.e.bias + col);
     constexpr int W = kTileThreads / 32, U = 4;
     by_kind(p.kind, [&](auto kind) {
-    for (int r = warp; r < share; r += W * U) {
+     for (int r = warp; r < share; r += W * U) {
       Quad a[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -564,7 +565,7 @@ __device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int
 template <class T>
 __device__ __forceinline__ void finish_row(const Params &p, uint8_t *buf, uint8_t *zbuf, int lane,
                                            const float *sum, const float4 *bias_row) {
-by_kind(p.kind, [&](auto kind) {
+  by_kind(p.kind, [&](auto kind) {
     constexpr int K = decltype(kind)::value;
     constexpr bool kSlope = K == kSiluSlope || K == kGeluSlope;
     const bool has_aux = kSlope || p.e.aux;
@@ -592,9 +593,14 @@ template <class Out>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
               const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tz,
-              const __grid_constant__ CUtensorMap tx, const Params p) {
+              const __grid_constant__ CUtensorMap tx, const __grid_constant__ Params p) {
   constexpr bool kFloat = sizeof(Out) == 4;
+  // (no room is left to align within: should the base not be, nothing is done)
   extern __shared__ __align__(1024) uint8_t smem_aligned[];
+  if (smem_u32(smem_aligned) & 1023) {
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, static_cast<int>(VAE_EUNSUPPORTED));
+    return;
+  }
   float *bias_rows = reinterpret_cast<float *>(smem_aligned);
   uint8_t *smem = smem_aligned + kPairHead;
   uint8_t *staging = smem + kPairStages * kPairStageBytes;
@@ -661,10 +667,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
       }
     }
-    // what was asked for lands before the pair leaves (both blocks' copies count on
-    // the leader's barriers, and the other block waits for the leader at the end)
+    // What was asked for lands before the pair leaves: both blocks' copies count on the
+    // leader's barriers, so that the other block, whose last copies the leader may not
+    // have expected, gives them time.
     __syncwarp();
-    if (*abort && rank == 0 && lane == 0) drain_stages(full, r, asked, p.wait_ns);
+    if (*abort && lane == 0) {
+      if (rank == 0) {
+        drain_stages(full, r, asked);
+      } else {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < kDrainNs / 10) {
+        }
+      }
+    }
   } else if (warp == 1) {
     // The whole warp goes through the loop, so that descriptors stay in registers that
     // all lanes share, and one lane issues: the tensor core takes a stage 512 clocks,
@@ -701,7 +716,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // (elect_one names the same lane every time: it has issued all of the products)
       if (elect_one()) {
         umma_commit_pair(drain, 1);
-        drain_wait(drain, 0, p.wait_ns);
+        drain_wait(drain, 0);
       }
     }
   } else {
@@ -825,10 +840,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         ++c;
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!kFloat && lane == 0) {
       if (p.e.aux && *abort)  // what was asked for lands before the block leaves
         for (int k = g; k < asked; ++k)
-          drain_wait(aux + (k & other), (other ? k >> 1 : k) & 1, p.wait_ns);
+          drain_wait(aux + (k & other), (other ? k >> 1 : k) & 1);
       bulk_wait_all();
     }
   }

@@ -11,7 +11,7 @@ using namespace vae;
 
 namespace {
 
-constexpr long long kMaxRows = 0x7fffff00ll;  // tokens of one call
+constexpr long long kMaxRows = 0x7ffffe00ll;  // tokens of one call
 
 template <class... T>
 bool all_aligned(T... p) {

@@ -554,7 +554,7 @@ VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void
  * and kept activations are of one vae_dtype a call; norm weights, biases and the
  * gradients of every parameter are float32. Everything is computed in FP32 and
  * rounded once, when it is stored. Sums have a fixed order: the same inputs give
- * the same bits. Limits: rows <= 2^31 - 256. */
+ * the same bits. Limits: rows <= 2^31 - 512. */
 typedef enum { VAE_F32 = 0, VAE_BF16 = 1, VAE_F16 = 2 } vae_dtype;
 /* z; z / (1 + e^-z); and z / (1 + e^-v), v = sqrt(8 / pi) (z + 0.044715 z^3), which
  * is GELU in its tanh form */

@@ -566,6 +566,37 @@ def test_beyond_32_bit_offsets(vae):
     close(dw, d1.double() + d2.double(), 3 * sum_tolerance(rows, mag, True, True), "dw")
 
 
+@pytest.mark.parametrize("op", ["linear", "linear_large", "dgrad_large", "wgrad", "wgrad_large"])
+def test_waits_that_run_out(vae, op):
+    """With a limit of a nanosecond some of the products' waits may give up: the call
+    then reports it, and leaves a device on which the next one is right."""
+    t = torch.bfloat16
+    rows, n, k = (2500, 2048, 512) if "large" in op else (300, 264, 520)
+    x, w, dy = rand(1, rows, k, dtype=t), rand(2, n, k, dtype=t), rand(3, rows, n, dtype=t)
+    z = rand(4, rows, k, dtype=t)
+
+    def call():
+        if op.startswith("linear"):
+            return vae.vae_linear(x, w)[0]
+        if op.startswith("dgrad"):
+            return vae.vae_linear_dgrad(dy, w, z=z, act=vae.VAE_ACT_GELU)
+        return torch.cat([v.flatten() for v in vae.vae_linear_wgrad(dy, x)])
+
+    want = call()
+    assert vae.vae_device_error() == 0
+    vae.vae_debug_set_wait_limit(1)
+    try:
+        got = call()
+        code = vae.vae_device_error()
+    finally:
+        vae.vae_debug_set_wait_limit(0)
+    assert code in (0, -6)
+    if code == 0:
+        assert torch.equal(got, want)
+    assert torch.equal(call(), want)
+    assert vae.vae_device_error() == 0
+
+
 def test_python_refusals(vae):
     t = torch.bfloat16
     x, w, g = rand(1, 8, 64, dtype=t), rand(2, 72, 64, dtype=t), rand(3, 64)
