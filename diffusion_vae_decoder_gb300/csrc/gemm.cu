@@ -56,34 +56,17 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kDrainNs) return;
 }
 
-// The parts that product q takes: hh, hm, mh, mm, hl, lh.
-__device__ __forceinline__ int part_a(int q) { return (0x201100 >> (4 * q)) & 15; }
-__device__ __forceinline__ int part_b(int q) { return (0x021010 >> (4 * q)) & 15; }
-
-// Stage `it` of the tile at (m0, n0): `rows_a` and `rows_b` rows of the operands.
-// `load(dst, map, c0, c1, c2)` issues one copy.
-template <int ROWS_A, int ROWS_B, class L>
-__device__ __forceinline__ void load_stage(const CUtensorMap *ta, const CUtensorMap *tb,
-                                           const Params &p, int it, int m0, int n0, uint8_t *da,
-                                           uint8_t *db, L &&load) {
-  int k0 = it * kBK, pa = 0, pb = 0;
-  if (p.pairs > 1) {
-    const int q = it % p.pairs;
-    k0 = it / p.pairs * kBK;
-    pa = part_a(q);
-    pb = part_b(q);
-  }
-  if (p.a_k) {
-    load(da, ta, k0, m0, pa);
+// 64 reduction indexes from k0 on of 128 rows of an operand, 16 KB; `load(dst, map, c0,
+// c1, c2)` issues one copy.
+constexpr int kOperandBytes = 128 * kBK * 2;
+template <class L>
+__device__ __forceinline__ void load_operand(const CUtensorMap *map, bool k_major, int k0, int row,
+                                             int part, uint8_t *dst, L &&load) {
+  if (k_major) {
+    load(dst, map, k0, row, part);
   } else {
-#pragma unroll
-    for (int i = 0; i < ROWS_A / 64; ++i) load(da + i * kBK * 128, ta, m0 + 64 * i, k0, pa);
-  }
-  if (p.b_k) {
-    load(db, tb, k0, n0, pb);
-  } else {
-#pragma unroll
-    for (int i = 0; i < ROWS_B / 64; ++i) load(db + i * kBK * 128, tb, n0 + 64 * i, k0, pb);
+    load(dst, map, row, k0, part);
+    load(dst + kBK * 128, map, row + 64, k0, part);
   }
 }
 // What the tensor core is told of the stages: descriptors of stage 0's operands, and
@@ -131,6 +114,104 @@ __device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long lon
     }
     drain_wait(full + r.s, r.round);
   }
+}
+
+// Floats: 64 reduction indexes are six stages of one operand's 16 KB, in the order
+// A's h, B's h, m, l, A's m, l, and six products, hh, hm, hl, mh, mm, lh, so that each
+// part is copied once and leaves when its last product has been issued.
+template <bool PAIR, int N, class L>
+__device__ __forceinline__ bool copy_parts(const Params &p, const CUtensorMap *ta,
+                                           const CUtensorMap *tb, uint8_t *smem, uint64_t *full,
+                                           uint64_t *empty, int block, int blocks, int m0, int n0,
+                                           bool leader, volatile uint32_t *abort, int lane,
+                                           Ring<N> *r, long long *asked, L &&load) {
+  for (int i = 0; i < 6 * blocks; ++i, ++*asked, r->next()) {
+    bool ok = mbar_wait(empty + r->s, r->round ^ 1, abort, p.wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      if (lane == 0) raise_error(p, abort);
+      return false;
+    }
+    const int tile = i % 6, k0 = (block + i / 6) * kBK;
+    const bool is_a = tile == 0 || tile > 3;
+    const int part = is_a ? max(tile - 3, 0) : tile - 1;
+    if (elect_one()) {
+      if (leader) mbar_arrive_expect_tx(full + r->s, (PAIR ? 2 : 1) * kOperandBytes);
+      load_operand(is_a ? ta : tb, is_a ? p.a_k : p.b_k, k0, is_a ? m0 : n0, part,
+                   smem + r->s * kOperandBytes,
+                   [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+                     load(dst, m, full + r->s, c0, c1, c2);
+                   });
+    }
+    __syncwarp();
+  }
+  return true;
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if constexpr (PAIR)
+    umma_commit_pair(bar, 3);
+  else
+    umma_commit(bar);
+}
+// The products of `blocks` of them, into accumulators c, c + 1, ... of kAccCols columns.
+template <bool PAIR, int N, int ACC_COLS>
+__device__ __forceinline__ bool multiply_parts(const Params &p, const Operands &o, uint64_t *full,
+                                               uint64_t *empty, uint64_t *acc_full,
+                                               uint64_t *acc_empty, uint32_t tmem, int blocks,
+                                               volatile uint32_t *abort, int lane, Ring<N> *r,
+                                               int *c) {
+  const uint32_t idesc = p.idesc;
+  int step = 0;
+  for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+    for (int q = 0; q < 6; ++q, ++step) {
+      // places of the operands among the six stages, and what is new with this product
+      const int ia = q < 3 ? 0 : q < 5 ? 4 : 5, ib = q < 3 ? 1 + q : q == 4 ? 2 : 1;
+      const int fresh = q == 0 ? 2 : q == 4 ? 0 : 1;
+      const bool first = step % kChain == 0;
+      const bool last = step % kChain == kChain - 1 || (b == blocks - 1 && q == 5);
+      auto stage = [&](int i) { return r->s + i < N ? r->s + i : r->s + i - N; };
+      auto round = [&](int i) { return r->s + i < N ? r->round : r->round ^ 1; };
+      bool ok = true;
+      if (first)
+        ok = mbar_wait(acc_empty + (*c & 1), (*c >> 1 & 1) ^ 1, abort, p.wait_ns);
+      if (fresh == 2) ok = ok && mbar_wait(full + stage(0), round(0), abort, p.wait_ns);
+      const int last_in = q < 3 ? ib : ia;
+      if (fresh) ok = ok && mbar_wait(full + stage(last_in), round(last_in), abort, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) raise_error(p, abort);
+        return false;
+      }
+      tc_fence_after();
+      const uint64_t a = o.a + stage(ia) * (kOperandBytes >> 4);
+      const uint64_t bd = o.b + stage(ib) * (kOperandBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          umma_16bit<PAIR>(tmem + (*c & 1) * ACC_COLS, a + k * o.step_a, bd + k * o.step_b, idesc,
+                           !(first && k == 0));
+        if (q == 2) {
+          commit<PAIR>(empty + stage(0));
+          commit<PAIR>(empty + stage(3));
+        }
+        if (q == 4) {
+          commit<PAIR>(empty + stage(2));
+          commit<PAIR>(empty + stage(4));
+        }
+        if (q == 5) {
+          commit<PAIR>(empty + stage(1));
+          commit<PAIR>(empty + stage(5));
+        }
+        if (last) commit<PAIR>(acc_full + (*c & 1));
+      }
+      __syncwarp();
+      *c += last;
+    }
+    for (int i = 0; i < 6; ++i) r->next();
+  }
+  return true;
 }
 
 // Sums of A's columns (the result's rows), by warps that wait for the tensor core: the
@@ -222,11 +303,12 @@ __device__ __forceinline__ Oct end_columns(const Params &p, uint8_t *buf, long l
 // multiplies, the others take the sums out.
 constexpr int kTile = 128;
 constexpr int kTileStages = 6;
+constexpr int kTileSlots = 2 * kTileStages;  // of one operand
 constexpr int kMaxSplits = 8;  // blocks of a cluster
 constexpr int kTileWarps = 8;  // that take sums out, 64 columns each
 constexpr int kTileCols = 4 * kTile / kTileWarps;
 constexpr int kTileThreads = 64 + 32 * kTileWarps;
-constexpr int kTileStageBytes = 2 * kTile * kBK * 2;
+constexpr int kTileStageBytes = 2 * kOperandBytes;
 constexpr int kSumLd = kTile + 4;  // floats of a row of sums: 16 bytes shift the banks
 constexpr size_t kTileSmem =
     kTileStages * kTileStageBytes + kTileWarps * kColumnBytes + 1024 + 256;
@@ -256,8 +338,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + kTileStages * kTileStageBytes +
                                                 kTileWarps * kColumnBytes);
-  uint64_t *empty = full + kTileStages;
-  uint64_t *acc_full = empty + kTileStages, *acc_empty = acc_full + 2;
+  uint64_t *empty = full + kTileSlots;
+  uint64_t *acc_full = empty + kTileSlots, *acc_empty = acc_full + 2;
   uint64_t *drain = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile uint32_t *abort = tmem_slot + 1;
@@ -266,14 +348,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tiles = p.m_tiles * p.n_tiles, slice = unit / tiles, tile = unit - slice * tiles;
   const int m0 = tile / p.n_tiles * kTile, n0 = tile % p.n_tiles * kTile;
   const int share_of = slice * splits + rank, shares = p.slices * splits;
-  const int it0 = static_cast<int>(static_cast<long long>(p.its) * share_of / shares);
-  const int its = static_cast<int>(static_cast<long long>(p.its) * (share_of + 1) / shares) - it0;
+  const long long all = p.its / p.pairs;  // blocks of 64 reduction indexes
+  const int block0 = static_cast<int>(all * share_of / shares);
+  const int blocks = static_cast<int>(all * (share_of + 1) / shares) - block0;
+  const int it0 = block0 * p.pairs, its = blocks * p.pairs;
   // the tiles of the first column take the sums of A's columns
   const bool columns = kFloat && p.cols.part && n0 == 0;
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
-    for (int i = 0; i < kTileStages; ++i) {
+    for (int i = 0; i < kTileSlots; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
     }
@@ -296,52 +380,71 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (p.wait) grid_wait();
 
   if (warp == 0) {
-    Ring<kTileStages> r;
-    int i = 0;
-    for (; i < its; ++i, r.next()) {
-      bool ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        if (lane == 0) raise_error(p, abort);
-        break;
+    if (kFloat && p.pairs > 1) {
+      Ring<kTileSlots> r;
+      long long asked = 0;
+      copy_parts<false>(p, &ta, &tb, smem, full, empty, block0, blocks, m0, n0, true, abort, lane,
+                        &r, &asked,
+                        [](uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
+                           int c2) { tma_load_3d(dst, m, bar, c0, c1, c2); });
+      if (*abort && lane == 0) drain_stages(full, r, asked);
+    } else {
+      Ring<kTileStages> r;
+      int i = 0;
+      for (; i < its; ++i, r.next()) {
+        bool ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) raise_error(p, abort);
+          break;
+        }
+        uint64_t *bar = full + r.s;
+        uint8_t *a = smem + r.s * kTileStageBytes;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, kTileStageBytes);
+          auto load = [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+            tma_load_3d(dst, m, bar, c0, c1, c2);
+          };
+          load_operand(&ta, p.a_k, (it0 + i) * kBK, m0, 0, a, load);
+          load_operand(&tb, p.b_k, (it0 + i) * kBK, n0, 0, a + kOperandBytes, load);
+        }
+        __syncwarp();
       }
-      uint64_t *bar = full + r.s;
-      uint8_t *a = smem + r.s * kTileStageBytes;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar, kTileStageBytes);
-        load_stage<kTile, kTile>(&ta, &tb, p, it0 + i, m0, n0, a, a + kTileStageBytes / 2,
-                                 [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
-                                   tma_load_3d(dst, m, bar, c0, c1, c2);
-                                 });
-      }
-      __syncwarp();
+      if (*abort && lane == 0) drain_stages(full, r, i);  // before the block leaves
     }
-    if (*abort && lane == 0) drain_stages(full, r, i);  // before the block leaves
   } else if (warp == 1) {
     // The whole warp goes through the loop, so that descriptors stay in registers that
     // all lanes share, and one lane issues (the same one every time).
-    const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kTileStageBytes / 2);
-    const uint32_t idesc = p.idesc;
-    Ring<kTileStages> r;
-    for (int i = 0; i < its; ++i, r.next()) {
-      const int chunk = kFloat ? i / kChain : 0;
-      const bool first = kFloat ? i % kChain == 0 : i == 0;
-      bool ok = true;
-      if (kFloat && first)
-        ok = mbar_wait(acc_empty + (chunk & 1), (chunk >> 1 & 1) ^ 1, abort, p.wait_ns);
-      ok = ok && mbar_wait(full + r.s, r.round, abort, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        if (lane == 0) raise_error(p, abort);
-        break;
+    if (kFloat && p.pairs > 1) {
+      const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem));
+      Ring<kTileSlots> r;
+      int c = 0;
+      multiply_parts<false, kTileSlots, kTile>(p, o, full, empty, acc_full, acc_empty, tmem, blocks,
+                                               abort, lane, &r, &c);
+    } else {
+      const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kOperandBytes);
+      const uint32_t idesc = p.idesc;
+      Ring<kTileStages> r;
+      for (int i = 0; i < its; ++i, r.next()) {
+        const int chunk = kFloat ? i / kChain : 0;
+        const bool first = kFloat ? i % kChain == 0 : i == 0;
+        bool ok = true;
+        if (kFloat && first)
+          ok = mbar_wait(acc_empty + (chunk & 1), (chunk >> 1 & 1) ^ 1, abort, p.wait_ns);
+        ok = ok && mbar_wait(full + r.s, r.round, abort, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) raise_error(p, abort);
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          multiply_stage<false>(o, idesc, r.s, kTileStageBytes, tmem + (chunk & 1) * kTile, first);
+          umma_commit(empty + r.s);
+          if (i == its - 1 || (kFloat && i % kChain == kChain - 1)) umma_commit(acc_full + (chunk & 1));
+        }
+        __syncwarp();
       }
-      tc_fence_after();
-      if (elect_one()) {
-        multiply_stage<false>(o, idesc, r.s, kTileStageBytes, tmem + (chunk & 1) * kTile, first);
-        umma_commit(empty + r.s);
-        if (i == its - 1 || (kFloat && i % kChain == kChain - 1)) umma_commit(acc_full + (chunk & 1));
-      }
-      __syncwarp();
     }
     // whatever became of the sums, no product is left when tensor memory is freed
     if (elect_one()) {
@@ -490,8 +593,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // for 16384 x 512 -> 2048 38 us instead of 32.)
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
+constexpr int kPairSlots = 2 * kPairStages;  // of one operand
 constexpr int kPairThreads = 576;
-constexpr int kPairStageBytes = 2 * 128 * kBK * 2;
+constexpr int kPairStageBytes = 2 * kOperandBytes;
 constexpr int kPairWarps = 16;            // that finish tiles, 64 columns each
 constexpr int kWarpCols = 4 * kPairTile / kPairWarps;
 constexpr int kChunk = 32;              // columns that a warp finishes at a time
@@ -605,8 +709,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint8_t *smem = smem_aligned + kPairHead;
   uint8_t *staging = smem + kPairStages * kPairStageBytes;
   uint64_t *full = reinterpret_cast<uint64_t *>(bias_rows + kPairWarps * kChunk);
-  uint64_t *empty = full + kPairStages;
-  uint64_t *acc_full = empty + kPairStages, *acc_empty = acc_full + 2;
+  uint64_t *empty = full + kPairSlots;
+  uint64_t *acc_full = empty + kPairSlots, *acc_empty = acc_full + 2;
   uint64_t *drain = acc_empty + 2;
   uint64_t *aux_full = drain + 1;  // two of each finishing warp's
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(aux_full + 2 * kPairWarps);
@@ -617,7 +721,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
-    for (int i = 0; i < kPairStages; ++i) {
+    for (int i = 0; i < kPairSlots; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
     }
@@ -643,28 +747,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   if (warp == 0) {
     Ring<kPairStages> r;
+    Ring<kPairSlots> slots;
     long long asked = 0;
     bool ok = true;
-    for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-      const Place at = place_of(p, t);
-      const int m0 = at.m + 128 * rank, n0 = at.n + 128 * rank;
-      for (int it = 0; it < p.its; ++it, ++asked, r.next()) {
-        ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) raise_error(p, abort);
-          break;
+    if (kFloat && p.pairs > 1) {
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+        const Place at = place_of(p, t);
+        ok = copy_parts<true>(p, &ta, &tb, smem, full, empty, 0, p.its / p.pairs,
+                              at.m + 128 * rank, at.n + 128 * rank, rank == 0, abort, lane, &slots,
+                              &asked,
+                              [](uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
+                                 int c2) { tma_load_3d_pair(dst, m, mapa_rank(bar, 0), c0, c1, c2); });
+      }
+    } else {
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+        const Place at = place_of(p, t);
+        const int m0 = at.m + 128 * rank, n0 = at.n + 128 * rank;
+        for (int it = 0; it < p.its; ++it, ++asked, r.next()) {
+          ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0) raise_error(p, abort);
+            break;
+          }
+          const uint32_t bar = mapa_rank(full + r.s, 0);
+          uint8_t *a = smem + r.s * kPairStageBytes;
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(full + r.s, 2 * kPairStageBytes);
+            auto load = [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
+              tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+            };
+            load_operand(&ta, p.a_k, it * kBK, m0, 0, a, load);
+            load_operand(&tb, p.b_k, it * kBK, n0, 0, a + kOperandBytes, load);
+          }
+          __syncwarp();
         }
-        const uint32_t bar = mapa_rank(full + r.s, 0);
-        uint8_t *a = smem + r.s * kPairStageBytes;
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full + r.s, 2 * kPairStageBytes);
-          load_stage<128, 128>(&ta, &tb, p, it, m0, n0, a, a + kPairStageBytes / 2,
-                               [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1, int c2) {
-                                 tma_load_3d_pair(dst, m, bar, c0, c1, c2);
-                               });
-        }
-        __syncwarp();
       }
     }
     // What was asked for lands before the pair leaves: both blocks' copies count on the
@@ -673,7 +790,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncwarp();
     if (*abort && lane == 0) {
       if (rank == 0) {
-        drain_stages(full, r, asked);
+        if (kFloat && p.pairs > 1)
+          drain_stages(full, slots, asked);
+        else
+          drain_stages(full, r, asked);
       } else {
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < kDrainNs / 10) {
@@ -685,12 +805,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // all lanes share, and one lane issues: the tensor core takes a stage 512 clocks,
     // and this loop has to be shorter.
     if (rank == 0) {
-      const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kPairStageBytes / 2);
+      const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kOperandBytes);
       const uint32_t idesc = p.idesc;
       const int its = p.its;
       Ring<kPairStages> r;
       int c = 0;  // accumulators taken
       bool ok = true;
+      if (kFloat && p.pairs > 1) {
+        const Operands same = operands_at(p, smem_u32(smem), smem_u32(smem));
+        Ring<kPairSlots> slots;
+        for (int t = blockIdx.x / 2; t < tiles && ok; t += stride)
+          ok = multiply_parts<true, kPairSlots, kPairTile>(p, same, full, empty, acc_full, acc_empty,
+                                                           tmem, its / p.pairs, abort, lane, &slots,
+                                                           &c);
+        ok = false;  // (the tiles are done)
+      }
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
         for (int it = 0; it < its; ++it, r.next()) {
           const bool first = kFloat ? it % kChain == 0 : it == 0;
