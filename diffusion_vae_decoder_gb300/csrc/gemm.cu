@@ -31,8 +31,7 @@ struct Params {
   int its;    // stages of a tile: 64-index blocks of k times `pairs`
   int pairs;  // products of parts: 1 or 6
   int m_tiles, n_tiles;
-  int slices;         // of the reduction, whose sums a later launch adds up; small tiles
-  long long stride;   // numbers from a slice's sums to the next
+  int slices;         // of the reduction, whose sums a later launch adds up
   bool a_k, b_k;
   bool wait;
   uint32_t idesc;
@@ -528,11 +527,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int w = 0; w < kTileWarps; ++w) sum += ld_cluster_f32(from + w * kColumnBytes);
       }
-      if (m0 + c < p.m) p.cols.part[slice * p.stride + m0 + c] = sum;
+      if (m0 + c < p.m) p.cols.part[slice * p.m + m0 + c] = sum;
     }
     const int col = n0 + 4 * lane;
     const bool in = col < p.n;
-    Out *out = static_cast<Out *>(p.e.out) + slice * p.stride, *keep = static_cast<Out *>(p.e.keep);
+    Out *out = static_cast<Out *>(p.e.out) + slice * p.m * p.n, *keep = static_cast<Out *>(p.e.keep);
     const Out *aux = static_cast<const Out *>(p.e.aux);
     Quad bias = {{0, 0}};
     if (p.e.bias && in) bias = load_quad(p.e.bias + col);
@@ -607,6 +606,17 @@ static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
 
 static_assert(kStaging == kColumnBytes, "columns go through a warp's staging buffer");
 
+// A slice's blocks of 64 reduction indexes.
+struct Range {
+  int block0, blocks;
+};
+__device__ __forceinline__ Range range_of(const Params &p, int slice) {
+  const int all = p.pairs > 1 ? p.its / p.pairs : p.its;
+  if (p.slices == 1) return {0, all};
+  const int block0 = static_cast<int>(static_cast<long long>(all) * slice / p.slices);
+  return {block0, static_cast<int>(static_cast<long long>(all) * (slice + 1) / p.slices) - block0};
+}
+
 // The place of tile t in the result: bands of 8 rows of tiles, column by column, so
 // that the tiles under way at a time form a block as wide as it is high, whose
 // operands L2 holds.
@@ -633,7 +643,7 @@ __device__ __forceinline__ uint4 *piece128(uint8_t *buf, int r, int c) {
 // A warp's 32 rows x 32 columns of floats at (row, col), a row a thread: the sums go
 // through shared memory (`buf`, 4 KB), then a lane finishes four columns of every
 // fourth row, as global memory is read and written.
-__device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int lane,
+__device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int lane, int slice,
                                               const float *sum, long long row, int col) {
 #pragma unroll
   for (int e = 0; e < 8; ++e)
@@ -656,7 +666,7 @@ __device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       y.v[j] = finish2<decltype(kind)::value, true>(v.v[j], bias.v[j], a.v[j], &z.v[j]);
-    store_quad(static_cast<float *>(p.e.out) + at, y);
+    store_quad(static_cast<float *>(p.e.out) + slice * p.m * p.n + at, y);
     if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + at, z);
   }
   });
@@ -717,7 +727,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   volatile uint32_t *abort = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int tiles = p.m_tiles * p.n_tiles, stride = gridDim.x / 2;
+  const int per = p.m_tiles * p.n_tiles, tiles = per * p.slices, stride = gridDim.x / 2;
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
@@ -752,8 +762,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     if (kFloat && p.pairs > 1) {
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-        const Place at = place_of(p, t);
-        ok = copy_parts<true>(p, &ta, &tb, smem, full, empty, 0, p.its / p.pairs,
+        const Place at = place_of(p, t % per);
+        const Range its = range_of(p, t / per);
+        ok = copy_parts<true>(p, &ta, &tb, smem, full, empty, its.block0, its.blocks,
                               at.m + 128 * rank, at.n + 128 * rank, rank == 0, abort, lane, &slots,
                               &asked,
                               [](uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
@@ -761,9 +772,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     } else {
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-        const Place at = place_of(p, t);
+        const Place at = place_of(p, t % per);
+        const Range its = range_of(p, t / per);
         const int m0 = at.m + 128 * rank, n0 = at.n + 128 * rank;
-        for (int it = 0; it < p.its; ++it, ++asked, r.next()) {
+        for (int it = its.block0; it < its.block0 + its.blocks; ++it, ++asked, r.next()) {
           ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
@@ -807,7 +819,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (rank == 0) {
       const Operands o = operands_at(p, smem_u32(smem), smem_u32(smem) + kOperandBytes);
       const uint32_t idesc = p.idesc;
-      const int its = p.its;
       Ring<kPairStages> r;
       int c = 0;  // accumulators taken
       bool ok = true;
@@ -816,11 +827,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         Ring<kPairSlots> slots;
         for (int t = blockIdx.x / 2; t < tiles && ok; t += stride)
           ok = multiply_parts<true, kPairSlots, kPairTile>(p, same, full, empty, acc_full, acc_empty,
-                                                           tmem, its / p.pairs, abort, lane, &slots,
-                                                           &c);
+                                                           tmem, range_of(p, t / per).blocks,
+                                                           abort, lane, &slots, &c);
         ok = false;  // (the tiles are done)
       }
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
+        const int its = range_of(p, t / per).blocks;
         for (int it = 0; it < its; ++it, r.next()) {
           const bool first = kFloat ? it % kChain == 0 : it == 0;
           const bool last = it == its - 1 || (kFloat && it % kChain == kChain - 1);
@@ -888,19 +900,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (!kFloat && p.e.aux && !p.e.keep && lane == 0) ask(0);
     bool ok = true;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
-      const Place place = place_of(p, t);
+      const Place place = place_of(p, t % per);
       const long long row = place.m + 128ll * rank + 32 * q;
       const int col = place.n + first_col;
       if constexpr (kFloat) {
         float acc[kWarpCols];
 #pragma unroll
         for (int j = 0; j < kWarpCols; ++j) acc[j] = 0.f;
-        const int chunks = (p.its + kChain - 1) / kChain;
+        const int slice = t / per;
+        const Range its = range_of(p, slice);
+        const int chunks = (its.blocks * p.pairs + kChain - 1) / kChain;
+        const int it0 = its.block0 * p.pairs, it1 = it0 + its.blocks * p.pairs;
         const long long first_row = place.m + 128ll * rank;
         Columns cols;
-        cols.next = place.n / kPairTile;
+        cols.next = its.block0 + (place.n / kPairTile + p.n_tiles - its.block0 % p.n_tiles) % p.n_tiles;
         for (int k = 0; k < chunks && ok; ++k, ++c) {
-          add_columns<kPairWarps>(p, buf, min(p.its, (k + 1) * kChain), first_row, warp - 2, lane,
+          add_columns<kPairWarps>(p, buf, min(it1, it0 + (k + 1) * kChain), first_row, warp - 2, lane,
                                   &cols);
           ok = taken(c);
           if (!ok) break;
@@ -916,13 +931,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
         if (p.cols.part) {
           const Oct sum = end_columns<kPairWarps>(p, buf, first_row, warp - 2, lane, &cols);
-          const long long ch = first_row + 8 * lane, part = place.n / kPairTile * kPairWarps + warp - 2;
+          const long long ch = first_row + 8 * lane;
+          const long long part =
+              (static_cast<long long>(slice) * p.n_tiles + place.n / kPairTile) * kPairWarps + warp - 2;
           if (lane < 16 && ch < p.m)
             store_raw<float, false>(p.cols.part + part * p.m + ch, 8, raw_of<float>(sum));
         }
 #pragma unroll
         for (int j = 0; j < kWarpCols; j += kChunk)
-          finish_floats(p, buf, lane, acc + j, row, col + j);
+          finish_floats(p, buf, lane, slice, acc + j, row, col + j);
       } else {
         // a chunk's bias is asked for a chunk ahead: from L2 it takes longer than the rest
         float bias = bias_at(col);
@@ -1070,25 +1087,16 @@ struct Tiling {
   int splits;
   long long clocks;
 };
-Tiling small_tiling(long long tiles, long long its) {
+Tiling small_tiling(long long tiles, long long its, long long blocks) {
   Tiling best{1, 0};
   for (int s = 1; s <= kMaxSplits; s *= 2) {
-    if (s > 1 && its < 2 * s) break;
+    if (s > 1 && (its < 2 * s || blocks < s)) break;
     const long long at_once = clusters_at_once(s);
     const long long t =
         (tiles + at_once - 1) / at_once * (4000 + 300 * s + 512 * ((its + s - 1) / s));
     if (s == 1 || t < best.clocks) best = {s, t};
   }
   return best;
-}
-
-// Whether 256 x 256 tiles on pairs of SMs finish before 128 x 128 ones.
-bool takes_pairs(long long m, int n, long long its) {
-  const long long small = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
-  const long long large = static_cast<long long>(ceil_div(m, kPairTile)) * ceil_div(n, kPairTile);
-  const int pairs = num_sms() / 2;
-  if (!pairs || large > 0x0fffffff) return false;
-  return 3000 + (large + pairs - 1) / pairs * (1000 + 600 * its) < small_tiling(small, its).clocks;
 }
 
 int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
@@ -1107,7 +1115,7 @@ int launch_pair(const GemmDesc &d, Params p, cudaStream_t s) {
   p.m_tiles = ceil_div(d.m, kPairTile);
   p.n_tiles = ceil_div(d.n, kPairTile);
   p.cols.step = p.n_tiles;
-  const unsigned grid = 2 * std::min(p.m_tiles * p.n_tiles, num_sms() / 2);
+  const unsigned grid = 2 * std::min(p.m_tiles * p.n_tiles * p.slices, num_sms() / 2);
   return by_dtype(d.dtype, [&](auto o) -> int {
     using Out = decltype(o);
     static std::atomic<uint64_t> done{0};
@@ -1131,9 +1139,7 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
   p.n_tiles = ceil_div(d.n, kTile);
   p.cols.step = 1;
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
-  const int splits = small_tiling(tiles, p.its).splits;
-  p.slices = d.slices;
-  p.stride = d.slices > 1 ? d.m * d.n + d.m : 0;
+  const int splits = small_tiling(tiles, p.its, p.its / p.pairs).splits;
   if (tiles * splits * p.slices > 0x7fffffff) return VAE_EUNSUPPORTED;
   return by_dtype(d.dtype, [&](auto o) -> int {
     using Out = decltype(o);
@@ -1150,16 +1156,37 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
 
 }  // namespace
 
-GemmPlan gemm_plan(long long m, int n, long long k, int parts) {
-  const long long its = (k + kBK - 1) / kBK * (parts > 1 ? 6 : 1);
-  if (takes_pairs(m, n, its)) return {1, ceil_div(n, kPairTile) * kPairWarps};
-  // a block's 24 stages and more are shared by idle SMs, eight stages at least to each:
-  // 4575 x 256 x 128 floats 15.8 us, 30.2 in one slice; 24576 x 128 x 128 bf16 12.1.
-  const long long tiles = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
-  const int splits = small_tiling(tiles, its).splits;
-  if (its < 24 * splits) return {1, 1};
-  const long long most = std::min(clusters_at_once(splits) / tiles, its / (8 * splits));
-  return {static_cast<int>(std::max(1ll, most)), 1};
+// The plan that the clocks speak for: rounds of tiles times what one takes besides its
+// stages, and its stages; adding up slices takes a launch and the reading of their sums.
+GemmPlan gemm_plan(long long m, int n, long long k, int parts, bool sliced) {
+  const long long blocks = (k + kBK - 1) / kBK, pairs = parts > 1 ? 6 : 1, its = blocks * pairs;
+  const long long small = static_cast<long long>(ceil_div(m, kTile)) * ceil_div(n, kTile);
+  const long long large = static_cast<long long>(ceil_div(m, kPairTile)) * ceil_div(n, kPairTile);
+  auto merge = [&](long long slices) { return slices > 1 ? 6000 + slices * m * n / 600 : 0; };
+  GemmPlan best;
+  const Tiling t = small_tiling(small, its, blocks);
+  long long clocks = t.clocks;
+  const long long idle = clusters_at_once(t.splits) / small;  // (whole clusters)
+  if (sliced && idle > 1) {
+    const long long s = std::min(idle, blocks * pairs / (8 * t.splits));
+    const long long c = 4000 + 300 * t.splits + 512 * its / (t.splits * std::max(1ll, s)) + merge(s);
+    if (s > 1 && c < clocks) {
+      best.slices = best.columns = static_cast<int>(s);
+      clocks = c;
+    }
+  }
+  const long long units = num_sms() / 2;
+  if (!units || large > 0x0fffffff) return best;
+  for (long long s = 1; s == 1 || (sliced && s <= units / large && s * 16 <= its); ++s) {
+    const long long c =
+        3000 + (large * s + units - 1) / units * (1000 + 600 * ((its + s - 1) / s)) + merge(s);
+    if (c >= clocks) continue;
+    best.pairs = true;
+    best.slices = static_cast<int>(s);
+    best.columns = static_cast<int>(s) * ceil_div(n, kPairTile) * kPairWarps;
+    clocks = c;
+  }
+  return best;
 }
 
 int gemm(const GemmDesc &d, cudaStream_t s) {
@@ -1179,7 +1206,8 @@ int gemm(const GemmDesc &d, cudaStream_t s) {
   p.e = d.epi;
   p.kind = kind_of(d.epi);
   p.cols = d.cols;
-  return takes_pairs(d.m, d.n, p.its) ? launch_pair(d, p, s) : launch_tile(d, p, s);
+  p.slices = d.plan.slices;
+  return d.plan.pairs ? launch_pair(d, p, s) : launch_tile(d, p, s);
 }
 
 }  // namespace vae

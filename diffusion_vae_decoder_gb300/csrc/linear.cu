@@ -85,42 +85,42 @@ int operands(GemmDesc *d, int dtype, const void *a, long long na, const void *b,
   return VAE_OK;
 }
 
-// out [n]: the sums of part [slabs][n], in a fixed order.
+// dw [count], the sums of `slices` arrays (blocks before `sum_blocks`, 1024 numbers
+// each), and dbias [n], of `columns` rows (32 numbers a block, the others); both in a
+// fixed order.
 __global__ void __launch_bounds__(256)
-    merge_sums(const float *part, int slabs, int n, float *__restrict__ out) {
+    merge_sums(const float *part, int slices, long long count, float *__restrict__ dw,
+               unsigned sum_blocks, const float *cols, int columns, int n,
+               float *__restrict__ dbias) {
   __shared__ float red[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = 32 * blockIdx.x + lane;
-  float t = 0.f;
   grid_wait();
-  if (ch < n)
-#pragma unroll 8
-    for (int s = warp; s < slabs; s += 8) t += part[static_cast<size_t>(s) * n + ch];
-  red[warp][lane] = t;
-  __syncthreads();
-  if (warp == 0 && ch < n) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) t += red[w][lane];
-    out[ch] = t;
-  }
-}
-// dw [count] and dbias [n]: the sums of `slices` arrays [count + n], in order.
-__global__ void __launch_bounds__(256)
-    merge_slices(const float *part, int slices, long long count, int n, float *__restrict__ dw,
-                 float *__restrict__ dbias) {
-  grid_wait();
-  const long long stride = count + n, step = 4ll * gridDim.x * 256;
-  for (long long i = 4 * (blockIdx.x * 256ll + threadIdx.x); i < (dbias ? stride : count);
-       i += step) {
+  if (blockIdx.x < sum_blocks) {
+    const long long i = 4 * (blockIdx.x * 256ll + threadIdx.x);
+    if (i >= count) return;
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = 0; s < slices; ++s) {
-      const float4 v = *reinterpret_cast<const float4 *>(part + s * stride + i);
+      const float4 v = *reinterpret_cast<const float4 *>(part + s * count + i);
       t.x += v.x;
       t.y += v.y;
       t.z += v.z;
       t.w += v.w;
     }
-    *reinterpret_cast<float4 *>(i < count ? dw + i : dbias + i - count) = t;
+    *reinterpret_cast<float4 *>(dw + i) = t;
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ch = 32 * (blockIdx.x - sum_blocks) + lane;
+  float t = 0.f;
+  if (ch < n)
+#pragma unroll 8
+    for (int s = warp; s < columns; s += 8) t += cols[static_cast<size_t>(s) * n + ch];
+  red[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && ch < n) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t += red[w][lane];
+    dbias[ch] = t;
   }
 }
 
@@ -142,6 +142,7 @@ int linear(const void *x, int dtype, long long rows, int k, const void *w, const
   d.n = n;
   d.k = k;
   d.epi = {bias, residual, y, z, act, false};
+  d.plan = gemm_plan(d.m, d.n, d.k, d.parts, false);
   return gemm(d, s);
 }
 
@@ -158,22 +159,16 @@ int linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w
   d.n = k;
   d.k = n;
   d.epi = {nullptr, z, dx, nullptr, act, true};
+  d.plan = gemm_plan(d.m, d.n, d.k, d.parts, false);
   return gemm(d, s);
 }
 
-namespace {
-// Numbers of the workspace that the sums go through.
-size_t sums_of(const GemmPlan &p, int n, int k) {
-  if (p.slices > 1) return static_cast<size_t>(p.slices) * n * (k + 1ll);
-  return p.columns > 1 ? static_cast<size_t>(p.columns) * n : 0;
-}
-}  // namespace
-
 size_t linear_wgrad_ws_bytes(int dtype, long long rows, int n, int k) {
+  const GemmPlan plan = gemm_plan(n, k, rows, dtype == VAE_F32 ? 3 : 1, true);
   Carver cv(nullptr, 0);
   cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
-  const size_t sums = sums_of(gemm_plan(n, k, rows, dtype == VAE_F32 ? 3 : 1), n, k);
-  if (sums) cv.take<float>(sums);
+  if (plan.slices > 1) cv.take<float>(static_cast<size_t>(plan.slices) * n * k);
+  if (plan.columns > 1) cv.take<float>(static_cast<size_t>(plan.columns) * n);
   return cv.used;
 }
 
@@ -183,31 +178,25 @@ int linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n
   void *parts = cv.take<char>(parts_bytes(dtype, rows * n, rows * k));
   GemmDesc d;
   VAE_TRY(operands(&d, dtype, dy, rows * n, x, rows * k, parts, s));
-  const GemmPlan plan = gemm_plan(n, k, rows, d.parts);
-  const size_t sums = sums_of(plan, n, k);
-  float *part = sums ? cv.take<float>(sums) : nullptr;
+  d.plan = gemm_plan(n, k, rows, d.parts, true);
   const long long count = static_cast<long long>(n) * k;
+  const int slices = d.plan.slices, columns = d.plan.columns;
+  float *sums = slices > 1 ? cv.take<float>(static_cast<size_t>(slices) * count) : dw;
+  float *cols = columns > 1 ? cv.take<float>(static_cast<size_t>(columns) * n) : dbias;
   d.dtype = VAE_F32;
   d.a.k_major = d.b.k_major = false;
   d.m = n;
   d.n = k;
   d.k = rows;
-  d.slices = plan.slices;
-  d.epi = {nullptr, nullptr, plan.slices > 1 ? part : dw, nullptr, VAE_ACT_NONE, true};
-  if (dbias)
-    d.cols = {dy, dtype, rows, plan.slices > 1 ? part + count : sums ? part : dbias};
+  d.epi = {nullptr, nullptr, sums, nullptr, VAE_ACT_NONE, true};
+  if (dbias) d.cols = {dy, dtype, rows, cols};
   VAE_TRY(gemm(d, s));
-  if (plan.slices > 1) {
-    const unsigned grid = static_cast<unsigned>(
-        std::min<long long>((count + n + 1023) / 1024, 4ll * num_sms()));
-    VAE_CUDA_TRY(launch_after(merge_slices, grid, 256, 0, s, part, plan.slices, count, n, dw,
-                              dbias));
-    count_launches(1);
-  } else if (dbias && sums) {
-    VAE_CUDA_TRY(launch_after(merge_sums, ceil_div(n, 32), 256, 0, s, part, plan.columns, n,
-                              dbias));
-    count_launches(1);
-  }
+  const unsigned sum_blocks = slices > 1 ? ceil_div(count, 1024) : 0;
+  const unsigned col_blocks = dbias && columns > 1 ? ceil_div(n, 32) : 0;
+  if (sum_blocks + col_blocks == 0) return VAE_OK;
+  VAE_CUDA_TRY(launch_after(merge_sums, sum_blocks + col_blocks, 256, 0, s, sums, slices, count, dw,
+                            sum_blocks, cols, columns, n, dbias));
+  count_launches(1);
   return VAE_OK;
 }
 

@@ -38,12 +38,15 @@ struct GemmEpilogue {
   bool derivative = false;
 };
 
-// How the sums of a long reduction come: those of the result in `slices` arrays, to be
-// added up in order, and those of A's columns in `columns` of them (slices > 1: in as
-// many, each behind its slice's m n sums).
+// How a product is made: on pairs of SMs or in small tiles, and, where `sliced` sums
+// are asked for, its long reduction in how many slices, whose sums [slices][m][n] are
+// added up in order afterwards. `columns`: partial sums of A's columns (1: the sums).
 struct GemmPlan {
-  int slices, columns;
+  bool pairs = false;
+  int slices = 1, columns = 1;
 };
+GemmPlan gemm_plan(long long m, int n, long long k, int parts, bool sliced);
+
 // Sums over the reduction of A's columns, taken on the way: src [rows][m], the numbers
 // A's parts come from, of `dtype`; part [columns][m] (NULL: none). For float results.
 struct GemmColumnSums {
@@ -70,9 +73,8 @@ struct GemmDesc {
   bool wait = false;  // an operand is made by the launch before this one
   GemmEpilogue epi;
   GemmColumnSums cols;
-  int slices = 1;  // gemm_plan's: epi.out [slices][m n + m] (float sums alone)
+  GemmPlan plan;
 };
-GemmPlan gemm_plan(long long m, int n, long long k, int parts);
 int gemm(const GemmDesc &d, cudaStream_t s);
 
 // The same as linear() for few rows, on the FP32 cores (gemv.cu).

@@ -382,7 +382,8 @@ def test_linear_dgrad(vae, rows, n, k, act, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,n,k", [(1, 64, 72), (77, 136, 520), (4575, 256, 128),
-                                      (20000, 512, 264), (3000, 2048, 2056)])
+                                      (20000, 512, 264), (3000, 2048, 2056), (20011, 520, 1032),
+                                      (30000, 64, 40)])
 def test_linear_wgrad(vae, rows, n, k, dtype):
     t = R.DTYPES[dtype]
     dy, x = rand(1, rows, n, dtype=t, std=0.1), rand(2, rows, k, dtype=t)
