@@ -224,69 +224,80 @@ __device__ __forceinline__ bool multiply_parts(const Params &p, const Operands &
 constexpr int kColumnBytes = 4096;
 struct Columns {
   Oct sum = {{0, 0, 0, 0}};
-  int next = 0;     // block of 64 rows
-  int waiting = 0;  // blocks in the buffer
+  int next = 0;                // block of 64 rows
+  int oldest = 0, waiting = 0;  // place and number of the blocks in the buffer
 };
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(in ? 16 : 0)
                : "memory");
 }
-// Adds up what is in the buffer, then asks for more blocks before `end`.
+// Asks for the blocks before `end`, adding up the oldest one whenever the buffer is
+// full; `rest`: what is in it as well.
 template <int W, class D>
-__device__ __forceinline__ void turn_blocks(const Params &p, uint8_t *buf, int end, long long m0,
-                                            int w, int lane, Columns *c) {
+__device__ __forceinline__ void turn_blocks(const Params &p, uint8_t *buf, int end, bool rest,
+                                            long long m0, int w, int lane, Columns *c) {
   constexpr int R = kBK / (2 * W), kLane = 8 * sizeof(D);  // rows of a lane's; bytes of a row
-  constexpr int kSlots = kColumnBytes / (R * 32 * kLane);
+  constexpr int kBlock = R * 32 * kLane, kSlots = kColumnBytes / kBlock;
   const long long ch = m0 + 8 * (lane & 15);
-  const uint32_t mine = smem_u32(buf) + 16 * lane;
-  do {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-    for (int i = 0; i < c->waiting * R; ++i) {
+  buf += 16 * lane;
+  auto add_oldest = [&] {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
       Raw<D> v;
 #pragma unroll
       for (int h = 0; h < kLane / 16; ++h)
-        v.v[h] = *reinterpret_cast<const uint4 *>(buf + (i * kLane / 16 + h) * 512 + 16 * lane);
+        v.v[h] = *reinterpret_cast<const uint4 *>(buf + c->oldest * kBlock +
+                                                  (i * kLane / 16 + h) * 512);
       const Oct o = oct_of(v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) c->sum.v[j] = add2(c->sum.v[j], o.v[j]);
     }
-    c->waiting = 0;
+    c->oldest = c->oldest + 1 == kSlots ? 0 : c->oldest + 1;
+    --c->waiting;
+  };
 #pragma unroll 1
-    for (; c->waiting < kSlots && c->next < end; ++c->waiting, c->next += p.cols.step) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const long long r = static_cast<long long>(c->next) * kBK + 2 * (w + W * i) + (lane >> 4);
-        const bool in = r < p.cols.rows && ch < p.m;
-        const D *src = static_cast<const D *>(p.cols.src) + (in ? r * p.m + ch : 0);
-#pragma unroll
-        for (int h = 0; h < kLane / 16; ++h)
-          copy16(mine + ((c->waiting * R + i) * kLane / 16 + h) * 512, src + 8 / (kLane / 16) * h,
-                 in);
-      }
+  for (; c->next < end; c->next += p.cols.step) {
+    if (c->waiting == kSlots) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+      add_oldest();
     }
-  } while (c->next < end);
+    const int slot = c->oldest + c->waiting;
+    const uint32_t to = smem_u32(buf) + (slot < kSlots ? slot : slot - kSlots) * kBlock;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const long long r = static_cast<long long>(c->next) * kBK + 2 * (w + W * i) + (lane >> 4);
+      const bool in = r < p.cols.rows && ch < p.m;
+      const D *src = static_cast<const D *>(p.cols.src) + (in ? r * p.m + ch : 0);
+#pragma unroll
+      for (int h = 0; h < kLane / 16; ++h)
+        copy16(to + (i * kLane / 16 + h) * 512, src + 8 / (kLane / 16) * h, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++c->waiting;
+  }
+  if (!rest) return;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  while (c->waiting) add_oldest();
 }
-// The blocks that stages before `it` belong to; asks for what lies before `it`, adds up
-// what came before.
+// The blocks that stages before `it` belong to.
 template <int W>
-__device__ __forceinline__ void add_columns(const Params &p, uint8_t *buf, int it, long long m0,
-                                            int w, int lane, Columns *c) {
+__device__ __forceinline__ void add_columns(const Params &p, uint8_t *buf, int it, bool rest,
+                                            long long m0, int w, int lane, Columns *c) {
   if (!p.cols.part) return;
   const int end = p.pairs > 1 ? (it + p.pairs - 1) / p.pairs : it;
   if (p.cols.dtype == VAE_F32)
-    turn_blocks<W, float>(p, buf, end, m0, w, lane, c);
+    turn_blocks<W, float>(p, buf, end, rest, m0, w, lane, c);
   else if (p.cols.dtype == VAE_BF16)
-    turn_blocks<W, bf16>(p, buf, end, m0, w, lane, c);
+    turn_blocks<W, bf16>(p, buf, end, rest, m0, w, lane, c);
   else
-    turn_blocks<W, __half>(p, buf, end, m0, w, lane, c);
+    turn_blocks<W, __half>(p, buf, end, rest, m0, w, lane, c);
 }
 // A warp's sums, eight columns each in lanes 0 to 15.
 template <int W>
 __device__ __forceinline__ Oct end_columns(const Params &p, uint8_t *buf, long long m0, int w,
                                            int lane, Columns *c) {
-  add_columns<W>(p, buf, 0, m0, w, lane, c);
+  add_columns<W>(p, buf, 0, true, m0, w, lane, c);
   __syncwarp();  // (the buffer is the warp's again)
   Oct sum = c->sum;
 #pragma unroll
@@ -465,7 +476,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     cols.next = p.pairs > 1 ? (it0 + p.pairs - 1) / p.pairs : it0;
     for (int c = 0; c < chunks; ++c) {
       if (kFloat && columns)
-        add_columns<kTileWarps>(p, buf, it0 + min(its, (c + 1) * kChain), m0, warp - 2, lane, &cols);
+        add_columns<kTileWarps>(p, buf, it0 + min(its, (c + 1) * kChain), false, m0, warp - 2, lane,
+                                &cols);
       ok = mbar_wait(acc_full + (c & 1), c >> 1 & 1, abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
@@ -915,8 +927,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         Columns cols;
         cols.next = its.block0 + (place.n / kPairTile + p.n_tiles - its.block0 % p.n_tiles) % p.n_tiles;
         for (int k = 0; k < chunks && ok; ++k, ++c) {
-          add_columns<kPairWarps>(p, buf, min(it1, it0 + (k + 1) * kChain), first_row, warp - 2, lane,
-                                  &cols);
+          add_columns<kPairWarps>(p, buf, min(it1, it0 + (k + 1) * kChain), false, first_row, warp - 2,
+                                  lane, &cols);
           ok = taken(c);
           if (!ok) break;
 #pragma unroll
@@ -1081,6 +1093,10 @@ int clusters_at_once(int splits) {
   return n;
 }
 
+// Clocks of a stage, measured: small tiles are bound by shared memory, which takes in
+// every operand for 128 rows and columns alone; floats' parts are copied once for six.
+int small_stage(bool parts) { return parts ? 400 : 700; }
+int pair_stage(bool parts) { return parts ? 520 : 600; }
 // How many blocks share a 128 x 128 tile's reduction, and the clocks it takes: rounds of
 // clusters times what a block does besides and its stages.
 struct Tiling {
@@ -1093,7 +1109,7 @@ Tiling small_tiling(long long tiles, long long its, long long blocks) {
     if (s > 1 && (its < 2 * s || blocks < s)) break;
     const long long at_once = clusters_at_once(s);
     const long long t =
-        (tiles + at_once - 1) / at_once * (4000 + 300 * s + 512 * ((its + s - 1) / s));
+        (tiles + at_once - 1) / at_once * (4000 + 300 * s + small_stage(its > blocks) * ((its + s - 1) / s));
     if (s == 1 || t < best.clocks) best = {s, t};
   }
   return best;
@@ -1169,7 +1185,8 @@ GemmPlan gemm_plan(long long m, int n, long long k, int parts, bool sliced) {
   const long long idle = clusters_at_once(t.splits) / small;  // (whole clusters)
   if (sliced && idle > 1) {
     const long long s = std::min(idle, blocks * pairs / (8 * t.splits));
-    const long long c = 4000 + 300 * t.splits + 512 * its / (t.splits * std::max(1ll, s)) + merge(s);
+    const long long c = 4000 + 300 * t.splits +
+                        small_stage(parts > 1) * its / (t.splits * std::max(1ll, s)) + merge(s);
     if (s > 1 && c < clocks) {
       best.slices = best.columns = static_cast<int>(s);
       clocks = c;
@@ -1179,7 +1196,8 @@ GemmPlan gemm_plan(long long m, int n, long long k, int parts, bool sliced) {
   if (!units || large > 0x0fffffff) return best;
   for (long long s = 1; s == 1 || (sliced && s <= units / large && s * 16 <= its); ++s) {
     const long long c =
-        3000 + (large * s + units - 1) / units * (1000 + 600 * ((its + s - 1) / s)) + merge(s);
+        5000 + merge(s) +
+        (large * s + units - 1) / units * (1000 + pair_stage(parts > 1) * ((its + s - 1) / s));
     if (c >= clocks) continue;
     best.pairs = true;
     best.slices = static_cast<int>(s);
