@@ -16,7 +16,7 @@
 // column, from L2 (small_columns).
 //
 // HBM bounds both, latency and the launch small calls. Measured, forward: 65536 x 1024
-// bf16 52 us (5.1 TB/s), 16384 x 512 8.1 us (from L2), one float row of 512 2.1 us.
+// bf16 50 us (5.3 TB/s), 16384 x 512 7.6 us (from L2), one float row of 512 2.1 us.
 // Backward with dres: 16384 x 1024 bf16 28 us (4.7 TB/s; 33 us with one row's loads
 // under way), float 45 us (5.9 TB/s); three blocks an SM instead of two 35 and 52 us.
 #include <cmath>
@@ -31,10 +31,11 @@ namespace {
 
 constexpr int kBwdBlocks = 2 * 152;
 
-// Rows whose loads are under way while one is worked on: two of 16-bit numbers, as
-// many bytes as one of floats (one where the registers hold two octs a thread).
-template <class D, int NV>
-constexpr int kAhead = sizeof(D) == 4 || NV > 1 ? 1 : 2;
+// Rows whose loads are under way while one is worked on: of 16-bit numbers two, as many
+// bytes as one of floats, and forward three (65536 x 1024 50 us instead of 52); one
+// where the registers hold two octs a thread.
+template <class D, int NV, int MOST>
+constexpr int kAhead = sizeof(D) == 4 || NV > 1 ? 1 : MOST;
 
 template <int T>
 constexpr int block_threads() { return T > 256 ? T : 256; }
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(block_threads<T>())
   const int tid = threadIdx.x % T;
   const unsigned step = gridDim.x * R;
   unsigned row = blockIdx.x * R + threadIdx.x / T;
-  constexpr int P = kAhead<D, NV>;
+  constexpr int P = kAhead<D, NV, 3>;
   Raw<D> next[P][NV];
   auto fetch = [&](unsigned r, int slot) {
 #pragma unroll
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(block_threads<T>())
   const int tid = threadIdx.x % T, grp = threadIdx.x / T;
   const unsigned step = row_blocks * R;
   unsigned row = blockIdx.x * R + grp;
-  constexpr int P = kAhead<D, NV>;
+  constexpr int P = kAhead<D, NV, 2>;
   Raw<D> xn[P][NV], dn[P][NV], rn[P][NV];
   float2 sn[P];
   auto fetch = [&](unsigned r, int slot) {
@@ -350,6 +351,7 @@ int by_width(int c, F &&f) {
   using std::integral_constant;
   const int octs = ceil_div(c, 8);
   if (octs <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (octs <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if (octs <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   if (octs <= 64) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   if (octs <= 128) return f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
@@ -359,7 +361,7 @@ int by_width(int c, F &&f) {
 }
 int bwd_blocks(long long rows, int c) {
   const int octs = ceil_div(c, 8);
-  const int r = octs <= 8 ? 32 : octs <= 32 ? 8 : octs <= 64 ? 4 : octs <= 128 ? 2 : 1;
+  const int r = octs <= 8 ? 32 : octs <= 16 ? 16 : octs <= 32 ? 8 : octs <= 64 ? 4 : octs <= 128 ? 2 : 1;
   // (two octs a thread: one block an SM; a second round of them costs 5 %)
   return static_cast<int>(std::min<long long>(octs > 256 ? kBwdBlocks / 2 : kBwdBlocks,
                                               (rows + r - 1) / r));

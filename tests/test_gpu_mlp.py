@@ -54,7 +54,7 @@ def close(got, ref, tol, what=""):
 
 
 # ---------------------------------------------------------------- layer norm
-NORM_SIZES = [(1, 4), (1, 512), (3, 36), (7, 64), (129, 256), (1221, 700), (300, 1024),
+NORM_SIZES = [(1, 4), (1, 512), (3, 36), (7, 64), (500, 68), (61, 128), (129, 256), (1221, 700), (300, 1024),
               (65, 2048), (33, 4096), (2, 4100), (9, 8192)]
 # A row's sum passes at most 8 x 2 additions in a thread, 1 of a pair, 5 of a warp and
 # 16 of a block: 38 roundings of partial sums, each below the sum of the magnitudes.
