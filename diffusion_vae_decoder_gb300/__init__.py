@@ -863,56 +863,79 @@ def vae_block_norm_backward(dy, dh, u_ckpt, h_ckpt, rstd, w_post, gate=None, sca
 
 
 # ---------------------------------------------------------------- a transformer block's MLP
-@functools.lru_cache(maxsize=None)
-def _dtypes():
+# (Small calls are bound by this code: it asks a tensor for as little as it can.)
+_DTYPES = {}  # torch dtype -> vae_dtype, once torch is loaded
+
+
+def _load_dtypes():
     import torch
-    return {torch.float32: VAE_F32, torch.bfloat16: VAE_BF16, torch.float16: VAE_F16}
+    global _F32
+    _F32 = torch.float32
+    _DTYPES.update({torch.float32: VAE_F32, torch.bfloat16: VAE_BF16, torch.float16: VAE_F16})
 
 
 def _tokens(x, name):
-    """(vae_dtype, dtype, shape, rows, c, device) of token rows x [..., c]."""
-    global _F32
+    """(vae_dtype, dtype, shape, rows, c, device index) of token rows x [..., c]."""
+    if not _DTYPES:
+        _load_dtypes()
+        load_library()
     try:
         dtype = x.dtype
-        code = _dtypes()[dtype]
-        if not (x.is_cuda and x.is_contiguous()):
+        code = _DTYPES[dtype]
+        index = x.get_device()
+        if index < 0 or not x.is_contiguous():
             raise KeyError
     except (AttributeError, KeyError):
         raise TypeError(f"{name} must be a contiguous float32, bfloat16 or float16 CUDA "
                         "tensor") from None
-    if _F32 is None:
-        import torch
-        _F32 = torch.float32
     shape = x.shape
     if len(shape) < 2:
         raise ValueError(f"{name} must be [..., c]")
     c = shape[-1]
     if c > 65536:  # (beyond every operator's limit, and C's int)
         raise VaeError(name, -2)
-    return code, dtype, shape, x.numel() // c if c else 0, c, x.device
+    return code, dtype, shape, x.numel() // c if c else 0, c, index
 
 
-def _like(t, dtype, shape, device, name):
-    """The address of a contiguous tensor of `dtype` and `shape` on `device`."""
+def _like(t, dtype, shape, index, name):
+    """The address of a contiguous tensor of `dtype` and `shape` on a CUDA device."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.device == device
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == index
                 and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
-    if dtype is _F32:
-        _refuse(t, shape, device, name)
     import torch
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
             and t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    raise ValueError(f"{name} is on {t.device}, not {device}")
+    raise ValueError(f"{name} is on {t.device}, not cuda:{index}")
 
 
-def _like_opt(t, dtype, shape, device, name):
-    return None if t is None else _like(t, dtype, shape, device, name)
+def _launch(name, index, *args):
+    """Calls entry point `name` with `args` and the current stream of a device."""
+    import torch
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        status = getattr(_lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(_lib, name)(*args, raw)
+    if status != 0:
+        raise VaeError(name, status)
+
+
+def _scratch(like, name, *args):
+    """(tensor, address, bytes) of an operator's workspace on `like`'s device; Nones when
+    it takes none."""
+    nbytes = _ws_bytes(name, *args)
+    if not nbytes:
+        return None, None, 0
+    import torch
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr(), nbytes
 
 
 def vae_layer_norm(x, gamma, beta=None, eps=1e-6, keep=True, out=None, stream=None):
@@ -921,16 +944,19 @@ def vae_layer_norm(x, gamma, beta=None, eps=1e-6, keep=True, out=None, stream=No
     import torch
     if stream is not None:
         return _on(stream, vae_layer_norm, x, gamma, beta, eps, keep, out)
-    load_library()
     code, dtype, shape, rows, c, dev = _tokens(x, "x")
-    pg, pb = _like(gamma, _F32, (c,), dev, "gamma"), _like_opt(beta, _F32, (c,), dev, "beta")
-    y = torch.empty_like(x) if out is None else out
-    py = y.data_ptr() if out is None else _like(out, dtype, shape, dev, "out")
+    pg = _like(gamma, _F32, (c,), dev, "gamma")
+    pb = None if beta is None else _like(beta, _F32, (c,), dev, "beta")
+    if out is None:
+        y = torch.empty_like(x)
+        py = y.data_ptr()
+    else:
+        y, py = out, _like(out, dtype, shape, dev, "out")
     stats = pst = None
     if keep:
-        stats = torch.empty((*shape[:-1], 2), dtype=_F32, device=dev)
+        stats = torch.empty((*shape[:-1], 2), dtype=_F32, device=x.device)
         pst = stats.data_ptr()
-    _call("vae_layer_norm", dev, x.data_ptr(), code, rows, c, eps, pg, pb, py, pst)
+    _launch("vae_layer_norm", dev, x.data_ptr(), code, rows, c, eps, pg, pb, py, pst)
     return y, stats
 
 
@@ -940,18 +966,20 @@ def vae_layer_norm_backward(dy, x, stats, gamma, dres=None, out=None, stream=Non
     import torch
     if stream is not None:
         return _on(stream, vae_layer_norm_backward, dy, x, stats, gamma, dres, out)
-    load_library()
     code, dtype, shape, rows, c, dev = _tokens(dy, "dy")
     px = _like(x, dtype, shape, dev, "x")
     pst = _like(stats, _F32, (*shape[:-1], 2), dev, "stats")
     pg = _like(gamma, _F32, (c,), dev, "gamma")
-    pr = _like_opt(dres, dtype, shape, dev, "dres")
-    dx = torch.empty_like(dy) if out is None else out
-    pdx = dx.data_ptr() if out is None else _like(out, dtype, shape, dev, "out")
-    ws, pw, nw = _workspace(dev, "vae_layer_norm_backward_workspace_size", rows, c)
+    pr = None if dres is None else _like(dres, dtype, shape, dev, "dres")
+    if out is None:
+        dx = torch.empty_like(dy)
+        pdx = dx.data_ptr()
+    else:
+        dx, pdx = out, _like(out, dtype, shape, dev, "out")
+    ws, pw, nw = _scratch(gamma, "vae_layer_norm_backward_workspace_size", rows, c)
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
-    _call("vae_layer_norm_backward", dev, dy.data_ptr(), px, code, pst, rows, c, pg, pr, pdx,
-          dgamma.data_ptr(), dbeta.data_ptr(), pw, nw)
+    _launch("vae_layer_norm_backward", dev, dy.data_ptr(), px, code, pst, rows, c, pg, pr, pdx,
+            dgamma.data_ptr(), dbeta.data_ptr(), pw, nw)
     return dx, dgamma, dbeta
 
 
@@ -965,34 +993,41 @@ def vae_dropout(x, p, seed=None, offset=0, state=None, residual=None, out=None, 
     import torch
     if stream is not None:
         return _on(stream, vae_dropout, x, p, seed, offset, state, residual, out)
-    load_library()
-    code = _dtypes().get(getattr(x, "dtype", None))
-    if code is None or not (x.is_cuda and x.is_contiguous()):
+    if not _DTYPES:
+        _load_dtypes()
+        load_library()
+    code = _DTYPES.get(getattr(x, "dtype", None))
+    dev = -1 if code is None else x.get_device()
+    if dev < 0 or not x.is_contiguous():
         raise TypeError("x must be a contiguous float32, bfloat16 or float16 CUDA tensor")
-    dtype, shape, dev = x.dtype, x.shape, x.device
+    dtype, shape = x.dtype, x.shape
     if (seed is None) == (state is None):
         raise ValueError("one of seed and state must be given")
-    for v, name in ((seed or 0, "seed"), (offset, "offset")):
-        if not 0 <= v < 2 ** 64:
-            raise ValueError(f"{name} must lie in [0, 2^64)")
+    ps = None
+    if state is not None:
+        seed, ps = 0, _like(state, torch.int64, (2,), dev, "state")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must lie in [0, 2^64)")
     if not 0 <= p <= 1:
         raise ValueError("p must lie in [0, 1]")
-    ps = None if state is None else _like(state, torch.int64, (2,), dev, "state")
-    pr = _like_opt(residual, dtype, shape, dev, "residual")
-    y = torch.empty_like(x) if out is None else out
-    py = y.data_ptr() if out is None else _like(out, dtype, shape, dev, "out")
-    _call("vae_dropout", dev, x.data_ptr(), code, x.numel(), p, seed or 0, offset, ps, pr, py)
+    pr = None if residual is None else _like(residual, dtype, shape, dev, "residual")
+    if out is None:
+        y = torch.empty_like(x)
+        py = y.data_ptr()
+    else:
+        y, py = out, _like(out, dtype, shape, dev, "out")
+    _launch("vae_dropout", dev, x.data_ptr(), code, x.numel(), p, seed, offset, ps, pr, py)
     return y
 
 
-def _weights(w, dtype, c, axis, device):
-    """(address, n, k) of a linear layer's weights [n, k] with c along `axis`."""
+def _weights(w):
+    """(n, k) of a linear layer's weights."""
     if getattr(w, "ndim", None) != 2:
         raise ValueError("w must be [n, k]")
     n, k = w.shape
     if n > 65536 or k > 65536:
         raise VaeError("w", -2)
-    return _like(w, dtype, (n, c) if axis else (c, k), device, "w"), n, k
+    return n, k
 
 
 def vae_linear(x, w, bias=None, act=VAE_ACT_NONE, residual=None, keep=False, out=None,
@@ -1003,20 +1038,23 @@ def vae_linear(x, w, bias=None, act=VAE_ACT_NONE, residual=None, keep=False, out
     import torch
     if stream is not None:
         return _on(stream, vae_linear, x, w, bias, act, residual, keep, out)
-    load_library()
     code, dtype, shape, rows, k, dev = _tokens(x, "x")
-    pw, n, _ = _weights(w, dtype, k, 1, dev)
-    pb = _like_opt(bias, _F32, (n,), dev, "bias")
+    n, _ = _weights(w)
+    pw = _like(w, dtype, (n, k), dev, "w")
+    pb = None if bias is None else _like(bias, _F32, (n,), dev, "bias")
     to = (*shape[:-1], n)
-    pr = _like_opt(residual, dtype, to, dev, "residual")
-    y = torch.empty(to, dtype=dtype, device=dev) if out is None else out
-    py = y.data_ptr() if out is None else _like(out, dtype, to, dev, "out")
+    pr = None if residual is None else _like(residual, dtype, to, dev, "residual")
+    if out is None:
+        y = torch.empty(to, dtype=dtype, device=x.device)
+        py = y.data_ptr()
+    else:
+        y, py = out, _like(out, dtype, to, dev, "out")
     z = pz = None
     if keep:
-        z = torch.empty(to, dtype=dtype, device=dev)
+        z = torch.empty(to, dtype=dtype, device=x.device)
         pz = z.data_ptr()
-    ws, pws, nws = _workspace(dev, "vae_linear_workspace_size", code, rows, n, k)
-    _call("vae_linear", dev, x.data_ptr(), code, rows, k, pw, pb, n, act, pr, py, pz, pws, nws)
+    ws, pws, nws = _scratch(x, "vae_linear_workspace_size", code, rows, n, k)
+    _launch("vae_linear", dev, x.data_ptr(), code, rows, k, pw, pb, n, act, pr, py, pz, pws, nws)
     return y, z
 
 
@@ -1027,17 +1065,20 @@ def vae_linear_dgrad(dy, w, z=None, act=VAE_ACT_NONE, out=None, stream=None):
     import torch
     if stream is not None:
         return _on(stream, vae_linear_dgrad, dy, w, z, act, out)
-    load_library()
     code, dtype, shape, rows, n, dev = _tokens(dy, "dy")
-    pw, _, k = _weights(w, dtype, n, 0, dev)
+    _, k = _weights(w)
+    pw = _like(w, dtype, (n, k), dev, "w")
     to = (*shape[:-1], k)
     if (z is None) != (act == VAE_ACT_NONE):
         raise ValueError("z goes with an activation")
-    pz = _like_opt(z, dtype, to, dev, "z")
-    dx = torch.empty(to, dtype=dtype, device=dev) if out is None else out
-    pdx = dx.data_ptr() if out is None else _like(out, dtype, to, dev, "out")
-    ws, pws, nws = _workspace(dev, "vae_linear_dgrad_workspace_size", code, rows, n, k)
-    _call("vae_linear_dgrad", dev, dy.data_ptr(), code, rows, n, pw, k, act, pz, pdx, pws, nws)
+    pz = None if z is None else _like(z, dtype, to, dev, "z")
+    if out is None:
+        dx = torch.empty(to, dtype=dtype, device=dy.device)
+        pdx = dx.data_ptr()
+    else:
+        dx, pdx = out, _like(out, dtype, to, dev, "out")
+    ws, pws, nws = _scratch(dy, "vae_linear_dgrad_workspace_size", code, rows, n, k)
+    _launch("vae_linear_dgrad", dev, dy.data_ptr(), code, rows, n, pw, k, act, pz, pdx, pws, nws)
     return dx
 
 
@@ -1047,18 +1088,17 @@ def vae_linear_wgrad(dy, x, bias=True, stream=None):
     import torch
     if stream is not None:
         return _on(stream, vae_linear_wgrad, dy, x, bias)
-    load_library()
     code, dtype, shape, rows, n, dev = _tokens(dy, "dy")
     _, _, _, _, k, _ = _tokens(x, "x")
     px = _like(x, dtype, (*shape[:-1], k), dev, "x")
-    ws, pws, nws = _workspace(dev, "vae_linear_wgrad_workspace_size", code, rows, n, k)
-    dw = torch.empty((n, k), dtype=_F32, device=dev)
+    ws, pws, nws = _scratch(dy, "vae_linear_wgrad_workspace_size", code, rows, n, k)
+    dw = torch.empty((n, k), dtype=_F32, device=dy.device)
     dbias = pb = None
     if bias:
-        dbias = torch.empty(n, dtype=_F32, device=dev)
+        dbias = torch.empty(n, dtype=_F32, device=dy.device)
         pb = dbias.data_ptr()
-    _call("vae_linear_wgrad", dev, dy.data_ptr(), px, code, rows, n, k, dw.data_ptr(), pb, pws,
-          nws)
+    _launch("vae_linear_wgrad", dev, dy.data_ptr(), px, code, rows, n, k, dw.data_ptr(), pb, pws,
+            nws)
     return dw, dbias
 
 
