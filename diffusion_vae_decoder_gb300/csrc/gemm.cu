@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (elect_one()) {
           multiply_stage<false>(o, idesc, r.s, kTileStageBytes, tmem + (chunk & 1) * kTile, first);
           umma_commit(empty + r.s);
-          if (i == its - 1 || (kFloat && i % kChain == kChain - 1)) umma_commit(acc_full + (chunk & 1));
+          if (i == its - 1 || (kFloat && i % kChain == kChain - 1))
+            umma_commit(acc_full + (chunk & 1));
         }
         __syncwarp();
       }
@@ -543,52 +544,53 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     const int col = n0 + 4 * lane;
     const bool in = col < p.n;
-    Out *out = static_cast<Out *>(p.e.out) + slice * p.m * p.n, *keep = static_cast<Out *>(p.e.keep);
+    Out *out = static_cast<Out *>(p.e.out) + slice * p.m * p.n;
+    Out *keep = static_cast<Out *>(p.e.keep);
     const Out *aux = static_cast<const Out *>(p.e.aux);
     Quad bias = {{0, 0}};
     if (p.e.bias && in) bias = load_quad(p.e.bias + col);
     constexpr int W = kTileThreads / 32, U = 4;
     by_kind(p.kind, [&](auto kind) {
-     for (int r = warp; r < share; r += W * U) {
-      Quad a[U];
+      for (int r = warp; r < share; r += W * U) {
+        Quad a[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long row = m0 + r0 + r + u * W;
-        a[u] = {{0, 0}};
-        if (aux && in && r + u * W < share && row < p.m) a[u] = load_quad(aux + row * p.n + col);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int rr = r0 + r + u * W;
-        const long long row = m0 + rr;
-        if (r + u * W >= share || row >= p.m) continue;
-        const float *mine = reinterpret_cast<const float *>(smem) + rr * kSumLd + 4 * lane;
-        Quad sum;
-        if (splits == 1) {
-          sum = load_quad(mine);
-        } else {
-          // (all in flight: one after another, eight blocks' take 5 us)
-          float4 f[kMaxSplits];
-#pragma unroll
-          for (int s = 0; s < kMaxSplits; ++s)
-            if (s < splits) f[s] = ld_cluster_f4(mapa_rank(mine, s));
-          sum = {{pk2(f[0].x, f[0].y), pk2(f[0].z, f[0].w)}};
-#pragma unroll
-          for (int s = 1; s < kMaxSplits; ++s) {
-            if (s >= splits) break;
-            sum.v[0] = add2(sum.v[0], pk2(f[s].x, f[s].y));
-            sum.v[1] = add2(sum.v[1], pk2(f[s].z, f[s].w));
-          }
+        for (int u = 0; u < U; ++u) {
+          const long long row = m0 + r0 + r + u * W;
+          a[u] = {{0, 0}};
+          if (aux && in && r + u * W < share && row < p.m) a[u] = load_quad(aux + row * p.n + col);
         }
-        if (!in) continue;
-        Quad z = {{0, 0}}, o;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          o.v[j] = finish2<decltype(kind)::value, kFloat>(sum.v[j], bias.v[j], a[u].v[j], &z.v[j]);
-        store_quad(out + row * p.n + col, o);
-        if (keep) store_quad(keep + row * p.n + col, z);
+        for (int u = 0; u < U; ++u) {
+          const int rr = r0 + r + u * W;
+          const long long row = m0 + rr;
+          if (r + u * W >= share || row >= p.m) continue;
+          const float *mine = reinterpret_cast<const float *>(smem) + rr * kSumLd + 4 * lane;
+          Quad sum;
+          if (splits == 1) {
+            sum = load_quad(mine);
+          } else {
+            // (all in flight: one after another, eight blocks' take 5 us)
+            float4 f[kMaxSplits];
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+              if (s < splits) f[s] = ld_cluster_f4(mapa_rank(mine, s));
+            sum = {{pk2(f[0].x, f[0].y), pk2(f[0].z, f[0].w)}};
+#pragma unroll
+            for (int s = 1; s < kMaxSplits; ++s) {
+              if (s >= splits) break;
+              sum.v[0] = add2(sum.v[0], pk2(f[s].x, f[s].y));
+              sum.v[1] = add2(sum.v[1], pk2(f[s].z, f[s].w));
+            }
+          }
+          if (!in) continue;
+          Quad z = {{0, 0}}, o;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            o.v[j] = finish2<decltype(kind)::value, kFloat>(sum.v[j], bias.v[j], a[u].v[j], &z.v[j]);
+          store_quad(out + row * p.n + col, o);
+          if (keep) store_quad(keep + row * p.n + col, z);
+        }
       }
-    }
     });
   }
   if (splits > 1) cluster_sync();  // the others read this block's sums until here
@@ -668,19 +670,19 @@ __device__ __forceinline__ void finish_floats(const Params &p, uint8_t *buf, int
   if (p.e.bias && ch < p.n) bias = load_quad(p.e.bias + ch);
   by_kind(p.kind, [&](auto kind) {
 #pragma unroll 2
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    if (row + r >= p.m || ch >= p.n) continue;
-    const size_t at = static_cast<size_t>(row + r) * p.n + ch;
-    const Quad v = load_quad(reinterpret_cast<const float *>(piece128(buf, r, lane & 7)));
-    Quad a = {{0, 0}}, z = {{0, 0}}, y;
-    if (p.e.aux) a = load_quad(static_cast<const float *>(p.e.aux) + at);
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (row + r >= p.m || ch >= p.n) continue;
+      const size_t at = static_cast<size_t>(row + r) * p.n + ch;
+      const Quad v = load_quad(reinterpret_cast<const float *>(piece128(buf, r, lane & 7)));
+      Quad a = {{0, 0}}, z = {{0, 0}}, y;
+      if (p.e.aux) a = load_quad(static_cast<const float *>(p.e.aux) + at);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      y.v[j] = finish2<decltype(kind)::value, true>(v.v[j], bias.v[j], a.v[j], &z.v[j]);
-    store_quad(static_cast<float *>(p.e.out) + slice * p.m * p.n + at, y);
-    if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + at, z);
-  }
+      for (int j = 0; j < 2; ++j)
+        y.v[j] = finish2<decltype(kind)::value, true>(v.v[j], bias.v[j], a.v[j], &z.v[j]);
+      store_quad(static_cast<float *>(p.e.out) + slice * p.m * p.n + at, y);
+      if (p.e.keep) store_quad(static_cast<float *>(p.e.keep) + at, z);
+    }
   });
   __syncwarp();
 }
@@ -780,7 +782,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                               at.m + 128 * rank, at.n + 128 * rank, rank == 0, abort, lane, &slots,
                               &asked,
                               [](uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
-                                 int c2) { tma_load_3d_pair(dst, m, mapa_rank(bar, 0), c0, c1, c2); });
+                                 int c2) {
+                                tma_load_3d_pair(dst, m, mapa_rank(bar, 0), c0, c1, c2);
+                              });
       }
     } else {
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
@@ -838,9 +842,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const Operands same = operands_at(p, smem_u32(smem), smem_u32(smem));
         Ring<kPairSlots> slots;
         for (int t = blockIdx.x / 2; t < tiles && ok; t += stride)
-          ok = multiply_parts<true, kPairSlots, kPairTile>(p, same, full, empty, acc_full, acc_empty,
-                                                           tmem, range_of(p, t / per).blocks,
-                                                           abort, lane, &slots, &c);
+          ok = multiply_parts<true, kPairSlots, kPairTile>(
+              p, same, full, empty, acc_full, acc_empty, tmem, range_of(p, t / per).blocks, abort,
+              lane, &slots, &c);
         ok = false;  // (the tiles are done)
       }
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
@@ -925,10 +929,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int it0 = its.block0 * p.pairs, it1 = it0 + its.blocks * p.pairs;
         const long long first_row = place.m + 128ll * rank;
         Columns cols;
-        cols.next = its.block0 + (place.n / kPairTile + p.n_tiles - its.block0 % p.n_tiles) % p.n_tiles;
+        const int tile_col = place.n / kPairTile;
+        cols.next = its.block0 + (tile_col + p.n_tiles - its.block0 % p.n_tiles) % p.n_tiles;
         for (int k = 0; k < chunks && ok; ++k, ++c) {
-          add_columns<kPairWarps>(p, buf, min(it1, it0 + (k + 1) * kChain), false, first_row, warp - 2,
-                                  lane, &cols);
+          add_columns<kPairWarps>(p, buf, min(it1, it0 + (k + 1) * kChain), false, first_row,
+                                  warp - 2, lane, &cols);
           ok = taken(c);
           if (!ok) break;
 #pragma unroll
@@ -945,7 +950,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const Oct sum = end_columns<kPairWarps>(p, buf, first_row, warp - 2, lane, &cols);
           const long long ch = first_row + 8 * lane;
           const long long part =
-              (static_cast<long long>(slice) * p.n_tiles + place.n / kPairTile) * kPairWarps + warp - 2;
+              (static_cast<long long>(slice) * p.n_tiles + tile_col) * kPairWarps + warp - 2;
           if (lane < 16 && ch < p.m)
             store_raw<float, false>(p.cols.part + part * p.m + ch, 8, raw_of<float>(sum));
         }
@@ -1108,8 +1113,8 @@ Tiling small_tiling(long long tiles, long long its, long long blocks) {
   for (int s = 1; s <= kMaxSplits; s *= 2) {
     if (s > 1 && (its < 2 * s || blocks < s)) break;
     const long long at_once = clusters_at_once(s);
-    const long long t =
-        (tiles + at_once - 1) / at_once * (4000 + 300 * s + small_stage(its > blocks) * ((its + s - 1) / s));
+    const long long stages = (its + s - 1) / s, rounds = (tiles + at_once - 1) / at_once;
+    const long long t = rounds * (4000 + 300 * s + small_stage(its > blocks) * stages);
     if (s == 1 || t < best.clocks) best = {s, t};
   }
   return best;
@@ -1162,7 +1167,8 @@ int launch_tile(const GemmDesc &d, Params p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     VAE_CUDA_TRY(allow_smem(gemm_tile<Out>, kTileSmem, &done));
     cudaLaunchAttribute attr[2];
-    const auto cfg = launch_config(attr, static_cast<unsigned>(tiles * splits * p.slices), kTileThreads,
+    const auto grid = static_cast<unsigned>(tiles * splits * p.slices);
+    const auto cfg = launch_config(attr, grid, kTileThreads,
                                    kTileSmem, splits, p.wait, s);
     VAE_CUDA_TRY(cudaLaunchKernelEx(&cfg, gemm_tile<Out>, ta, tb, p, splits));
     count_launches(1);

@@ -102,41 +102,41 @@ __global__ void __launch_bounds__(block_threads<T>())
   // whole blocks leave the loop together: every lane takes part in the shuffles
   for (unsigned long long r0 = blockIdx.x * R; r0 < rows; r0 += P * step) {
 #pragma unroll
-   for (int q = 0; q < P; ++q, row += step) {
-    if (q && r0 + q * step >= rows) break;
-    const bool live = row < rows;
-    Oct v[NV];
-    uint64_t sum = 0;
+    for (int q = 0; q < P; ++q, row += step) {
+      if (q && r0 + q * step >= rows) break;
+      const bool live = row < rows;
+      Oct v[NV];
+      uint64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      v[i] = oct_of(next[q][i]);
+      for (int i = 0; i < NV; ++i) {
+        v[i] = oct_of(next[q][i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum = add2(sum, v[i].v[j]);
-    }
-    if (r0 + (q + P) * step < rows) fetch(row + P * step, q);
-    const float mean = row_sum<T>(total(sum), buf[0]) * inv_c;
-    uint64_t ss = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int left = c - 8 * (i * T + tid);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[i].v[j] = add2(v[i].v[j], both(-mean));
-        if (2 * j < left) ss = fma2(v[i].v[j], v[i].v[j], ss);  // (c is a multiple of four)
+        for (int j = 0; j < 4; ++j) sum = add2(sum, v[i].v[j]);
       }
-    }
-    const float rstd = 1.f / sqrtf(row_sum<T>(total(ss), buf[1]) * inv_c + eps);
+      if (r0 + (q + P) * step < rows) fetch(row + P * step, q);
+      const float mean = row_sum<T>(total(sum), buf[0]) * inv_c;
+      uint64_t ss = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int ch = 8 * (i * T + tid);
-      Oct o;
+      for (int i = 0; i < NV; ++i) {
+        const int left = c - 8 * (i * T + tid);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o.v[j] = fma2(mul2(v[i].v[j], both(rstd)), g[i].v[j], b[i].v[j]);
-      store_raw<D, WIDE>(y + static_cast<size_t>(row) * c + ch, live ? c - ch : 0, raw_of<D>(o));
+        for (int j = 0; j < 4; ++j) {
+          v[i].v[j] = add2(v[i].v[j], both(-mean));
+          if (2 * j < left) ss = fma2(v[i].v[j], v[i].v[j], ss);  // (c is a multiple of four)
+        }
+      }
+      const float rstd = 1.f / sqrtf(row_sum<T>(total(ss), buf[1]) * inv_c + eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int ch = 8 * (i * T + tid);
+        Oct o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.v[j] = fma2(mul2(v[i].v[j], both(rstd)), g[i].v[j], b[i].v[j]);
+        store_raw<D, WIDE>(y + static_cast<size_t>(row) * c + ch, live ? c - ch : 0, raw_of<D>(o));
+      }
+      if (stats && live && tid == 0)
+        *reinterpret_cast<float2 *>(stats + 2 * static_cast<size_t>(row)) = make_float2(mean, rstd);
     }
-    if (stats && live && tid == 0)
-      *reinterpret_cast<float2 *>(stats + 2 * static_cast<size_t>(row)) = make_float2(mean, rstd);
-   }
   }
 }
 
@@ -236,45 +236,45 @@ __global__ void __launch_bounds__(block_threads<T>())
   int turn = 0;
   for (unsigned long long r0 = blockIdx.x * R; r0 < rows; r0 += P * step) {
 #pragma unroll
-   for (int q = 0; q < P; ++q, row += step) {
-    if (q && r0 + q * step >= rows) break;
-    const bool live = row < rows;
-    Oct xh[NV], t[NV], res[NV];
-    const float mean = sn[q].x, rstd = sn[q].y;
-    uint64_t st = 0, sx = 0;
+    for (int q = 0; q < P; ++q, row += step) {
+      if (q && r0 + q * step >= rows) break;
+      const bool live = row < rows;
+      Oct xh[NV], t[NV], res[NV];
+      const float mean = sn[q].x, rstd = sn[q].y;
+      uint64_t st = 0, sx = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      xh[i] = oct_of(xn[q][i]);
-      t[i] = oct_of(dn[q][i]);
-      if (dres) res[i] = oct_of(rn[q][i]);
+      for (int i = 0; i < NV; ++i) {
+        xh[i] = oct_of(xn[q][i]);
+        t[i] = oct_of(dn[q][i]);
+        if (dres) res[i] = oct_of(rn[q][i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        xh[i].v[j] = mul2(add2(xh[i].v[j], both(-mean)), both(rstd));
-        if (!SMALL) {
-          sg[i].v[j] = fma2(t[i].v[j], xh[i].v[j], sg[i].v[j]);
-          sb[i].v[j] = add2(t[i].v[j], sb[i].v[j]);
+        for (int j = 0; j < 4; ++j) {
+          xh[i].v[j] = mul2(add2(xh[i].v[j], both(-mean)), both(rstd));
+          if (!SMALL) {
+            sg[i].v[j] = fma2(t[i].v[j], xh[i].v[j], sg[i].v[j]);
+            sb[i].v[j] = add2(t[i].v[j], sb[i].v[j]);
+          }
+          t[i].v[j] = mul2(t[i].v[j], g[i].v[j]);  // (zero past c, as dy is)
+          st = add2(st, t[i].v[j]);
+          sx = fma2(t[i].v[j], xh[i].v[j], sx);
         }
-        t[i].v[j] = mul2(t[i].v[j], g[i].v[j]);  // (zero past c, as dy is)
-        st = add2(st, t[i].v[j]);
-        sx = fma2(t[i].v[j], xh[i].v[j], sx);
+      }
+      if (r0 + (q + P) * step < rows) fetch(row + P * step, q);
+      const float2 s = row_sum2<T>(make_float2(total(st), total(sx)), buf[turn]);
+      turn ^= 1;
+      const uint64_t m1 = both(-s.x * inv_c), m2 = both(-s.y * inv_c), r2 = both(rstd);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int ch = 8 * (i * T + tid);
+        Oct o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = fma2(xh[i].v[j], m2, add2(t[i].v[j], m1));
+          o.v[j] = dres ? fma2(d, r2, res[i].v[j]) : mul2(d, r2);
+        }
+        store_raw<D, WIDE>(dx + static_cast<size_t>(row) * c + ch, live ? c - ch : 0, raw_of<D>(o));
       }
     }
-    if (r0 + (q + P) * step < rows) fetch(row + P * step, q);
-    const float2 s = row_sum2<T>(make_float2(total(st), total(sx)), buf[turn]);
-    turn ^= 1;
-    const uint64_t m1 = both(-s.x * inv_c), m2 = both(-s.y * inv_c), r2 = both(rstd);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int ch = 8 * (i * T + tid);
-      Oct o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t d = fma2(xh[i].v[j], m2, add2(t[i].v[j], m1));
-        o.v[j] = dres ? fma2(d, r2, res[i].v[j]) : mul2(d, r2);
-      }
-      store_raw<D, WIDE>(dx + static_cast<size_t>(row) * c + ch, live ? c - ch : 0, raw_of<D>(o));
-    }
-   }
   }
   if (SMALL) return;
   if (R > 1) {
@@ -361,7 +361,12 @@ int by_width(int c, F &&f) {
 }
 int bwd_blocks(long long rows, int c) {
   const int octs = ceil_div(c, 8);
-  const int r = octs <= 8 ? 32 : octs <= 16 ? 16 : octs <= 32 ? 8 : octs <= 64 ? 4 : octs <= 128 ? 2 : 1;
+  const int r = octs <= 8    ? 32
+                : octs <= 16  ? 16
+                : octs <= 32  ? 8
+                : octs <= 64  ? 4
+                : octs <= 128 ? 2
+                              : 1;
   // (two octs a thread: one block an SM; a second round of them costs 5 %)
   return static_cast<int>(std::min<long long>(octs > 256 ? kBwdBlocks / 2 : kBwdBlocks,
                                               (rows + r - 1) / r));
@@ -375,8 +380,8 @@ int layer_norm(const void *x, int dtype, long long rows, int c, float eps, const
     using D = decltype(d);
     return by_width(c, [&](auto t, auto nv) -> int {
       constexpr int T = decltype(t)::value, NV = decltype(nv)::value, R = block_threads<T>() / T;
-      const unsigned grid = static_cast<unsigned>(
-          std::min<long long>((rows + R - 1) / R, (T > 256 ? 1ll : NV > 1 ? 2ll : 4ll) * num_sms()));
+      const long long most = (T > 256 ? 1ll : NV > 1 ? 2ll : 4ll) * num_sms();
+      const unsigned grid = static_cast<unsigned>(std::min<long long>((rows + R - 1) / R, most));
       auto kernel = raw_wide<D>(c, x, y) ? layer_norm_fwd<D, T, NV, true>
                                          : layer_norm_fwd<D, T, NV, false>;
       kernel<<<grid, block_threads<T>(), 0, s>>>(static_cast<const D *>(x),

@@ -44,8 +44,9 @@ __device__ __forceinline__ uint64_t at_most2(uint64_t z, float high) {
 // The activations are z sigmoid(v), v = z for SiLU and z (a + b z^2) for GELU in its
 // tanh form, a = sqrt(8 / pi), b = 0.044715 a. Beyond kFar both they and their
 // derivatives are, to far below float's resolution, what they are there on the
-// negative side (sigmoid 1e-38), and z and 1 on the positive one; z is held inside,
-// so that no power of it and no exponential overflows. A NaN stays one.
+// negative side (sigmoid 1e-38), and z and 1 on the positive one; z is held inside
+// (activations: on the negative side), so that no product of a large and a vanishing
+// number is formed. A NaN stays one.
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.071354816f;
 template <int KIND>
 constexpr bool is_gelu = KIND == kGelu || KIND == kGeluSlope;
@@ -53,13 +54,14 @@ template <int KIND>
 constexpr float kFar = is_gelu<KIND> ? 10.f : 87.f;
 // s = 1 / (1 + e) with e = e^-v, for v >= -87.4, by the exp2 and reciprocal units, to
 // 2^-21 and the rounding of v log2 e (2^-23 |v|), which PRECISE puts back for results
-// that are floats. (The reciprocal by Newton steps from an integer seed instead, for a
+// that are floats (v at most 128 there: the rest of an infinite product is a NaN, and
+// e is 0 long before). (The reciprocal by Newton steps from an integer seed instead, for a
 // unit that takes a warp eight clocks: 33 us instead of 31 for 16384 x 512 -> 2048.)
 template <bool PRECISE>
 __device__ __forceinline__ uint64_t sigmoid_of(uint64_t v, uint64_t *e) {
   const uint64_t t = mul2(v, pk2(-1.4426950408889634f, -1.4426950408889634f));
   *e = pk2(ex2_approx(lo2(t)), ex2_approx(hi2(t)));
-  if constexpr (PRECISE) {
+  if constexpr (PRECISE) {  // e^-v = 2^t (1 - w)
     const uint64_t w = fma2(t, pk2(0.6931471805599453f, 0.6931471805599453f), v);
     *e = fma2(mul2(*e, w), pk2(-1.f, -1.f), *e);
   }
@@ -71,6 +73,7 @@ __device__ __forceinline__ uint64_t act2(uint64_t z) {
   uint64_t v = h, e;
   if (is_gelu<KIND>)
     v = mul2(h, fma2(mul2(h, h), pk2(kGeluB, kGeluB), pk2(kGeluA, kGeluA)));
+  if (PRECISE) v = at_most2(v, 128.f);
   return mul2(h, sigmoid_of<PRECISE>(v, &e));
 }
 // act'(z) = s + z v' s (1 - s), with 1 - s = e s, which loses nothing where s is near 1.

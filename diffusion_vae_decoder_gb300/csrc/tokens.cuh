@@ -64,9 +64,9 @@ __device__ __forceinline__ Raw<T> raw_of(const Oct &o) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      r.v[h] = make_uint4(static_cast<uint32_t>(o.v[2 * h]), static_cast<uint32_t>(o.v[2 * h] >> 32),
-                          static_cast<uint32_t>(o.v[2 * h + 1]),
-                          static_cast<uint32_t>(o.v[2 * h + 1] >> 32));
+      r.v[h] = make_uint4(__float_as_uint(lo2(o.v[2 * h])), __float_as_uint(hi2(o.v[2 * h])),
+                          __float_as_uint(lo2(o.v[2 * h + 1])),
+                          __float_as_uint(hi2(o.v[2 * h + 1])));
   } else {
     r.v[0] = make_uint4(pack2(lo2(o.v[0]), hi2(o.v[0]), T{}), pack2(lo2(o.v[1]), hi2(o.v[1]), T{}),
                         pack2(lo2(o.v[2]), hi2(o.v[2]), T{}), pack2(lo2(o.v[3]), hi2(o.v[3]), T{}));

@@ -557,7 +557,8 @@ VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void
  * the same bits. Limits: rows <= 2^31 - 512. */
 typedef enum { VAE_F32 = 0, VAE_BF16 = 1, VAE_F16 = 2 } vae_dtype;
 /* z; z / (1 + e^-z); and z / (1 + e^-v), v = sqrt(8 / pi) (z + 0.044715 z^3), which
- * is GELU in its tanh form */
+ * is GELU in its tanh form; at an infinite z their limits (below 1e-35 for -infinity),
+ * and their derivatives' */
 typedef enum { VAE_ACT_NONE = 0, VAE_ACT_SILU = 1, VAE_ACT_GELU = 2 } vae_act;
 
 /* vae_layer_norm -- per row of c: y = gamma (x - mean) rstd + beta with
@@ -603,7 +604,7 @@ VAE_API int vae_dropout(const void *x, int dtype, long long count, double p,
  * vae_linear_dgrad -- dx = (dy w) act'(z): the gradient of a layer's input x,
  * carried through the activation that made x out of z.
  *   dy [rows][n], w [n][k], dx [rows][k]; z [rows][k], NULL exactly when act is
- *   VAE_ACT_NONE (dx = dy w). At an infinite z the derivative is its limit.
+ *   VAE_ACT_NONE (dx = dy w).
  * vae_linear_wgrad -- dw[o][c] = sum over rows of dy[o] x[c], dbias[o] = sum of dy[o].
  *   dy [rows][n], x [rows][k], dw [n][k] float32, dbias [n] float32 or NULL.
  * 16-bit products are exact, their sums FP32. Floats enter the tensor cores as three
@@ -685,9 +686,9 @@ VAE_API int vae_measure_tf32_mma(int iters, double *flops, float *ms, vae_stream
  * GPU. Process-wide settings, read when a kernel is launched.
  *
  * vae_debug_set_wait_limit: every device-side wait of the implicit-GEMM conv
- * gives up after `ns` nanoseconds (0 restores the default, 4 s) and records
- * VAE_EDEVICE_TIMEOUT, drains its own copies and MMAs, frees its TMEM and
- * returns.
+ * and of the linear layers' products gives up after `ns` nanoseconds (0 restores
+ * the default, 4 s) and records VAE_EDEVICE_TIMEOUT; the kernel drains its own
+ * copies and MMAs, frees its TMEM and returns.
  * vae_debug_inject: VAE_INJECT_WITHHOLD_STREAMK_FLAG makes the conv's
  * stream-K CTAs skip the flag that hands a tile's tail over to the CTA that
  * finishes it, so that CTA's bounded wait runs out (0 clears).

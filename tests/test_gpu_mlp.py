@@ -411,6 +411,24 @@ def test_derivative_at_the_far_ends(vae):
             assert torch.isnan(bad).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n", [(2, 64), (200, 64), (2500, 2048)])
+def test_activation_at_the_far_ends(vae, rows, n, dtype):
+    t = R.DTYPES[dtype]
+    top = 6e4 if dtype == "f16" else 1e30
+    ends = torch.tensor([top, 3e4, 100.0, -100.0, -3e4, -top, float("inf"), -float("inf")],
+                        device="cuda")
+    bias = ends.repeat(n // 8)
+    x, w = torch.zeros(rows, 64, dtype=t, device="cuda"), rand(1, n, 64, dtype=t)
+    for act in (vae.VAE_ACT_SILU, vae.VAE_ACT_GELU):
+        y, z = vae.vae_linear(x, w, bias=bias, act=act, keep=True)
+        assert torch.equal(z, bias.to(t).expand(rows, n))
+        y = y.view(rows, -1, 8)
+        assert torch.equal(y[..., :3], ends[:3].to(t).expand_as(y[..., :3]))
+        assert torch.isinf(y[..., 6]).all() and (y[..., 6] > 0).all()
+        assert (y[..., [3, 4, 5, 7]].float().abs() < 1e-30).all()
+
+
 @pytest.mark.parametrize("rows", [4, 300])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_bad_numbers_stay_in_their_row_and_column(vae, rows, dtype):
