@@ -322,6 +322,7 @@ constexpr int kTileStageBytes = 2 * kOperandBytes;
 constexpr int kSumLd = kTile + 4;  // floats of a row of sums: 16 bytes shift the banks
 constexpr size_t kTileSmem =
     kTileStages * kTileStageBytes + kTileWarps * kColumnBytes + 1024 + 256;
+static_assert(kTileSmem <= 227 * 1024 && (2 * kTileSlots + 5) * 8 + 8 <= 256, "barriers");
 static_assert(kTile * kSumLd * 4 <= kTileStages * kTileStageBytes, "sums lie over the stages");
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (splits == 1) {
             sum = load_quad(mine);
           } else {
-            // (all in flight: one after another, eight blocks' take 5 us)
+            // all in flight, added up in order
             float4 f[kMaxSplits];
 #pragma unroll
             for (int s = 0; s < kMaxSplits; ++s)
@@ -586,7 +587,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           Quad z = {{0, 0}}, o;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            o.v[j] = finish2<decltype(kind)::value, kFloat>(sum.v[j], bias.v[j], a[u].v[j], &z.v[j]);
+            o.v[j] =
+                finish2<decltype(kind)::value, kFloat>(sum.v[j], bias.v[j], a[u].v[j], &z.v[j]);
           store_quad(out + row * p.n + col, o);
           if (keep) store_quad(keep + row * p.n + col, z);
         }
@@ -609,15 +611,16 @@ constexpr int kPairStages = 5;
 constexpr int kPairSlots = 2 * kPairStages;  // of one operand
 constexpr int kPairThreads = 576;
 constexpr int kPairStageBytes = 2 * kOperandBytes;
-constexpr int kPairWarps = 16;            // that finish tiles, 64 columns each
+constexpr int kPairWarps = 16;  // that finish tiles, 64 columns each
 constexpr int kWarpCols = 4 * kPairTile / kPairWarps;
-constexpr int kChunk = 32;              // columns that a warp finishes at a time
-constexpr int kChunkBytes = 32 * 64;    // of 16-bit numbers
+constexpr int kChunk = 32;                 // columns that a warp finishes at a time
+constexpr int kChunkBytes = 32 * 64;       // of 16-bit numbers
 constexpr int kStaging = 2 * kChunkBytes;  // a warp's
-constexpr int kPairHead = 3072;            // barriers and rows of the bias
+constexpr int kPairHead = 3072;            // rows of the bias, and barriers
 constexpr size_t kPairSmem = kPairHead + kPairStages * kPairStageBytes + kPairWarps * kStaging;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
-
+static_assert(kPairWarps * kChunk * 4 + (2 * kPairSlots + 5 + 2 * kPairWarps) * 8 + 8 <= kPairHead,
+              "the head's parts");
 static_assert(kStaging == kColumnBytes, "columns go through a warp's staging buffer");
 
 // A slice's blocks of 64 reduction indexes.

@@ -28,6 +28,11 @@ int linear_args_ok(int dtype, long long rows, int n, int k) {
   if (rows > kMaxRows || n % 8 || k % 8 || n > 65536 || k > 65536) return VAE_EUNSUPPORTED;
   return VAE_OK;
 }
+// Whether `out` is one of the arrays that a product reads while it writes.
+template <class... T>
+bool one_of(const void *out, T... in) {
+  return out && ((out == static_cast<const void *>(in)) || ...);
+}
 bool act_ok(int act) { return act == VAE_ACT_NONE || act == VAE_ACT_SILU || act == VAE_ACT_GELU; }
 int workspace_ok(const void *ws, size_t ws_bytes, size_t need) {
   if (!need) return VAE_OK;
@@ -83,7 +88,8 @@ size_t vae_linear_workspace_size(int dtype, long long rows, int n, int k) {
 int vae_linear(const void *x, int dtype, long long rows, int k, const void *w, const float *bias,
                int n, int act, const void *residual, void *y, void *z, void *ws, size_t ws_bytes,
                vae_stream_t stream) {
-  if (!x || !w || !y || !act_ok(act)) return VAE_EINVAL;
+  if (!x || !w || !y || !act_ok(act) || one_of(y, x, w) || one_of(z, x, w, y, residual))
+    return VAE_EINVAL;
   VAE_TRY(linear_args_ok(dtype, rows, n, k));
   if (!all_aligned(x, w, bias, residual, y, z, ws)) return VAE_EINVAL;
   VAE_TRY(workspace_ok(ws, ws_bytes, linear_ws_bytes(dtype, rows, n, k)));
@@ -97,7 +103,8 @@ size_t vae_linear_dgrad_workspace_size(int dtype, long long rows, int n, int k) 
 int vae_linear_dgrad(const void *dy, int dtype, long long rows, int n, const void *w, int k,
                      int act, const void *z, void *dx, void *ws, size_t ws_bytes,
                      vae_stream_t stream) {
-  if (!dy || !w || !dx || !act_ok(act) || (act != VAE_ACT_NONE) != (z != nullptr))
+  if (!dy || !w || !dx || !act_ok(act) || (act != VAE_ACT_NONE) != (z != nullptr) ||
+      one_of(dx, dy, w))
     return VAE_EINVAL;
   VAE_TRY(linear_args_ok(dtype, rows, n, k));
   if (!all_aligned(dy, w, z, dx, ws)) return VAE_EINVAL;
@@ -111,7 +118,7 @@ size_t vae_linear_wgrad_workspace_size(int dtype, long long rows, int n, int k) 
 
 int vae_linear_wgrad(const void *dy, const void *x, int dtype, long long rows, int n, int k,
                      float *dw, float *dbias, void *ws, size_t ws_bytes, vae_stream_t stream) {
-  if (!dy || !x || !dw) return VAE_EINVAL;
+  if (!dy || !x || !dw || one_of(dw, dy, x) || one_of(dbias, dy, x, dw)) return VAE_EINVAL;
   VAE_TRY(linear_args_ok(dtype, rows, n, k));
   if (!all_aligned(dy, x, dw, dbias, ws)) return VAE_EINVAL;
   VAE_TRY(workspace_ok(ws, ws_bytes, linear_wgrad_ws_bytes(dtype, rows, n, k)));

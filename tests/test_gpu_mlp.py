@@ -637,6 +637,7 @@ def test_python_refusals(vae):
         lambda: vae.vae_linear(x, w, bias=rand(1, 72).to(t)),
         lambda: vae.vae_linear(x, w, residual=x), lambda: vae.vae_linear(x, w, act=5),
         lambda: vae.vae_linear(x, w[:66]), lambda: vae.vae_linear(x, w, out=x),
+        lambda: vae.vae_linear(x, w[:64], out=x),
         lambda: vae.vae_linear_dgrad(x, w), lambda: vae.vae_linear_dgrad(x[:, :8], w[:8]),
         lambda: vae.vae_linear_dgrad(x, w.t().contiguous(), z=rand(1, 8, 72, dtype=t)),
         lambda: vae.vae_linear_dgrad(x, w.t().contiguous(), act=vae.VAE_ACT_SILU),

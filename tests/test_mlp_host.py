@@ -62,14 +62,15 @@ def test_three_bf16_parts_are_the_float():
 
 
 A = ctypes.c_void_p(4096)   # aligned; never read: every call is refused first
+B, C = ctypes.c_void_p(8192), ctypes.c_void_p(16384)  # others, for what is written
 ODD = ctypes.c_void_p(4100)
 OK = {
     "vae_layer_norm": [A, 1, 8, 64, 1e-6, A, A, A, A, None],
     "vae_layer_norm_backward": [A, A, 1, A, 100000, 64, A, A, A, A, A, A, 1 << 30, None],
     "vae_dropout": [A, 1, 64, 0.1, 1, 2, None, A, A, None],
-    "vae_linear": [A, 1, 8, 64, A, A, 64, 1, A, A, A, A, 1 << 30, None],
-    "vae_linear_dgrad": [A, 1, 8, 64, A, 64, 1, A, A, A, 1 << 30, None],
-    "vae_linear_wgrad": [A, A, 1, 8, 64, 64, A, A, A, 1 << 30, None],
+    "vae_linear": [A, 1, 8, 64, A, A, 64, 1, A, B, C, A, 1 << 30, None],
+    "vae_linear_dgrad": [A, 1, 8, 64, A, 64, 1, A, B, A, 1 << 30, None],
+    "vae_linear_wgrad": [A, A, 1, 8, 64, 64, B, C, A, 1 << 30, None],
 }
 EINVAL, EUNSUPPORTED, EWORKSPACE = -1, -2, -3
 REFUSALS = [
@@ -105,6 +106,9 @@ REFUSALS = [
     ("vae_linear_wgrad", 0, None, EINVAL), ("vae_linear_wgrad", 1, None, EINVAL),
     ("vae_linear_wgrad", 6, None, EINVAL), ("vae_linear_wgrad", 2, 5, EINVAL),
     ("vae_linear_wgrad", 3, 0, EINVAL), ("vae_linear_wgrad", 4, 4, EUNSUPPORTED),
+    ("vae_linear", 9, A, EINVAL), ("vae_linear", 10, A, EINVAL), ("vae_linear", 10, B, EINVAL),
+    ("vae_linear_dgrad", 8, A, EINVAL), ("vae_linear_wgrad", 6, A, EINVAL),
+    ("vae_linear_wgrad", 7, A, EINVAL), ("vae_linear_wgrad", 7, B, EINVAL),
     ("vae_linear_wgrad", 5, 4, EUNSUPPORTED), ("vae_linear_wgrad", 7, ODD, EINVAL),
 ]
 
