@@ -548,6 +548,37 @@ def test_two_streams_at_once(vae):
     assert torch.equal(y, y2) and torch.equal(dw, dw2) and torch.equal(db, db2)
 
 
+def test_next_to_the_decoders_kernels(vae):
+    """Products on one stream while convs and a weight gradient, which take tensor memory
+    as well, run on another."""
+    x, w = rand(1, 3000, 512, dtype=torch.bfloat16), rand(2, 2048, 512, dtype=torch.bfloat16)
+    xf, wf = rand(3, 700, 264), rand(4, 520, 264)
+    img, cw = rand(5, 1, 64, 64, 128), rand(6, 128, 128, 3, 3, std=0.03)
+    dy = rand(7, 1, 64, 64, 128, std=0.01)
+    ckpt = vae.vae_ckpt_pack(img)
+
+    def mine():
+        y, z = vae.vae_linear(x, w, act=vae.VAE_ACT_GELU, keep=True)
+        return y, z, *vae.vae_linear_wgrad(y, x), vae.vae_linear(xf, wf)[0]
+
+    def others():
+        return vae.vae_conv2d(img, cw, layout=vae.VAE_NHWC), *vae.vae_conv2d_wgrad(
+            dy, ckpt, 3, layout=vae.VAE_NHWC)
+
+    want = mine(), others()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a = [mine() for _ in range(3)][-1]
+        with torch.cuda.stream(s2):
+            b = [others() for _ in range(3)][-1]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(a, want[0]))
+        assert all(torch.equal(p, q) for p, q in zip(b, want[1]))
+    assert vae.vae_device_error() == 0
+
+
 def test_beyond_32_bit_offsets(vae):
     """More than 2^31 elements: the last rows are right, and so are the first."""
     t = torch.bfloat16
