@@ -616,7 +616,7 @@ constexpr int kWarpCols = 4 * kPairTile / kPairWarps;
 constexpr int kChunk = 32;                 // columns that a warp finishes at a time
 constexpr int kChunkBytes = 32 * 64;       // of 16-bit numbers
 constexpr int kStaging = 2 * kChunkBytes;  // a warp's
-constexpr int kPairHead = 3072;            // rows of the bias, and barriers
+constexpr int kPairHead = 3 * 1024;        // rows of the bias, and barriers
 constexpr size_t kPairSmem = kPairHead + kPairStages * kPairStageBytes + kPairWarps * kStaging;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
 static_assert(kPairWarps * kChunk * 4 + (2 * kPairSlots + 5 + 2 * kPairWarps) * 8 + 8 <= kPairHead,
