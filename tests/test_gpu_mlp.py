@@ -316,6 +316,30 @@ def test_linear_wgrad_exact(vae, rows, n, k, dtype):
     assert none is None and torch.equal(again, dw)
 
 
+@pytest.mark.parametrize("rows,n,k", [(3, 264, 512), (300, 264, 512), (2500, 2048, 256)])
+def test_linear_of_subnormal_halves(vae, rows, n, k):
+    """f16 numbers below the smallest normal one, as gradients are, lose nothing."""
+    tiny = 2.0 ** -24  # the smallest f16
+    x = (ints(1, rows, k, dtype=torch.float32, top=9) * tiny).half()
+    w = ints(2, n, k, dtype=torch.float16, top=2)
+    z = x.double() @ w.double().t()
+    assert (z.abs() < 2.0 ** -13).all()  # (exact in f16)
+    assert torch.equal(vae.vae_linear(x, w)[0].double(), z)
+    dw, db = vae.vae_linear_wgrad(x, w[:1].expand(rows, k).contiguous())
+    assert torch.equal(dw.double(), x.double().t() @ w[:1].double().expand(rows, k))
+    assert torch.equal(db.double(), x.double().sum(0))
+
+
+@pytest.mark.parametrize("rows,n,k", [(3, 264, 512), (300, 264, 512), (2500, 2048, 256)])
+def test_float_products_scale_with_powers_of_two(vae, rows, n, k):
+    """All three parts of a float keep their numbers over float's range."""
+    x, w = rand(1, rows, k), rand(2, n, k, std=k ** -0.5)
+    want, _ = vae.vae_linear(x, w)
+    for e in (-80, 90):
+        got, _ = vae.vae_linear(x * 2.0 ** e, w)
+        assert torch.equal(got, want * 2.0 ** e)
+
+
 # ---------------------------------------------------------------- linear: numbers
 # The tensor core cuts its running sum once every 16 products, by at most 2^-22 of it
 # (2^-23 where the products are aligned and 2^-23 where they are added); a float's sum
