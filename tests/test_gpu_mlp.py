@@ -262,7 +262,7 @@ def test_dropout_state_moves_between_replays(vae):
 LINEAR_SIZES = [(1, 8, 8), (1, 264, 512), (2, 512, 264), (3, 2048, 128), (5, 64, 40), (8, 72, 1000),
                 (9, 520, 72), (127, 128, 128), (128, 136, 64), (129, 264, 200), (257, 120, 520),
                 (1000, 1032, 72), (300, 512, 2056), (4575, 256, 128), (2049, 2048, 520),
-                (1000, 2056, 2048), (4100, 1032, 2048)]
+                (1000, 2056, 2048), (4100, 1032, 2048), (8, 4096, 2048), (7, 4104, 2048)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
