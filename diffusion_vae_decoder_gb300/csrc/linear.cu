@@ -128,20 +128,22 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ operators
 // Few rows are multiplied on the FP32 cores: up to four, whose weights' bytes bound both
-// ways (one row 512 -> 2048 2.3 us, in a tile 5.9; four rows 4096 -> 4096 7.9, 9.4), and
-// up to eight of smaller weights (eight rows 512 -> 2048 3.7 us, in a tile 5.6; 4096 ->
-// 4096 13.3, 9.4).
-static bool takes_few(long long rows, int n, int k) {
-  return rows <= 4 || (rows <= kFewRows && static_cast<long long>(n) * k <= 8 << 20);
+// ways (one row 512 -> 2048 2.3 us, in a tile 5.5; four rows 4096 -> 4096 7.9, 9.1), and
+// up to eight of smaller weights (eight rows 2048 -> 1024 4.3 us, in a tile 6.2; 2048 ->
+// 4096 9.1, 6.9) or of floats, whose weights a tile would need split (2048 -> 4096 16.2,
+// 25.6).
+static bool takes_few(int dtype, long long rows, int n, int k) {
+  if (rows > kFewRows) return false;
+  return rows <= 4 || dtype == VAE_F32 || static_cast<long long>(n) * k < 4 << 20;
 }
 
 size_t linear_ws_bytes(int dtype, long long rows, int n, int k) {
-  return takes_few(rows, n, k) ? 0 : parts_bytes(dtype, rows * k, static_cast<long long>(n) * k);
+  return takes_few(dtype, rows, n, k) ? 0 : parts_bytes(dtype, rows * k, static_cast<long long>(n) * k);
 }
 
 int linear(const void *x, int dtype, long long rows, int k, const void *w, const float *bias,
            int n, int act, const void *residual, void *y, void *z, void *ws, cudaStream_t s) {
-  if (takes_few(rows, n, k))
+  if (takes_few(dtype, rows, n, k))
     return linear_few(x, dtype, static_cast<int>(rows), k, w, n, {bias, residual, y, z, act, false},
                       s);
   GemmDesc d;
