@@ -101,6 +101,7 @@ class TracePoint(ctypes.Structure):
 TRACE_KINDS = {0: "latent", 1: "conv", 2: "groupnorm", 3: "resnet", 4: "attention",
                5: "upsample", 6: "rgb"}
 INJECT_WITHHOLD_STREAMK_FLAG = 1
+INJECT_WITHHOLD_COPY, INJECT_WITHHOLD_PAIR_COPY, INJECT_WITHHOLD_ACCUMULATOR = 4, 8, 16
 
 _I, _LL, _F, _SZ = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
 _ULL = ctypes.c_ulonglong

@@ -38,13 +38,18 @@ struct Params {
   uint32_t stage_bytes;  // that the copies of a small tile's stage bring
   uint64_t wait_ns;
   int *err;
+  int inject;  // test hook: VAE_INJECT_* bits (0 in normal operation)
   int kind;
   GemmEpilogue e;
   GemmColumnSums cols;
 };
 
+// A wait ran out: the block's other waits give up as well, and a pair's other block's.
+template <bool PAIR>
 __device__ __forceinline__ void raise_error(const Params &p, volatile uint32_t *abort) {
   *abort = 1u;
+  if constexpr (PAIR)
+    st_cluster(mapa_rank(const_cast<const uint32_t *>(abort), cluster_ctarank() ^ 1), 1u);
   atomicCAS(p.err, 0, static_cast<int>(VAE_EDEVICE_TIMEOUT));
 }
 // Waits for products or copies that are under way before a block leaves: 10 ms at
@@ -104,16 +109,23 @@ struct Ring {
     }
   }
 };
-// After an abort: what was asked for in the last stages before `r` lands.
+// After an abort, which may come when a block has asked for its last copies already, and
+// a barrier of all threads: the last of the `asked` stages of a ring of N land. (Those
+// before them were multiplied, or their places would not have been asked for again.)
 template <int N>
-__device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long long asked) {
-  for (int j = 0; j < N && j < asked; ++j) {
-    if (r.s-- == 0) {
-      r.s = N - 1;
-      r.round ^= 1;
-    }
-    drain_wait(full + r.s, r.round);
-  }
+__device__ __forceinline__ void drain_stages(uint64_t *full, uint64_t asked) {
+  for (uint64_t i = asked > N ? asked - N : 0; i < asked; ++i)
+    drain_wait(full + i % N, i / N & 1);
+}
+// The same on a pair's leader, whose barriers count both blocks' copies, `bytes` of each
+// a stage: the stages that one block alone has asked for are put right first.
+template <int N>
+__device__ __forceinline__ void drain_pair(uint64_t *full, const volatile uint64_t *asked,
+                                           uint32_t bytes) {
+  const uint64_t mine = asked[0], theirs = asked[1];
+  for (uint64_t i = mine; i < theirs; ++i) mbar_arrive_expect_tx(full + i % N, bytes);
+  for (uint64_t i = theirs; i < mine; ++i) mbar_complete_tx(full + i % N, bytes);
+  drain_stages<N>(full, max(mine, theirs));
 }
 
 // Floats: 64 reduction indexes are six stages of one operand's 16 KB, in the order
@@ -122,14 +134,14 @@ __device__ __forceinline__ void drain_stages(uint64_t *full, Ring<N> r, long lon
 template <bool PAIR, int N, class L>
 __device__ __forceinline__ bool copy_parts(const Params &p, const CUtensorMap *ta,
                                            const CUtensorMap *tb, uint8_t *smem, uint64_t *full,
-                                           uint64_t *empty, int block, int blocks, int m0, int n0,
-                                           bool leader, volatile uint32_t *abort, int lane,
-                                           Ring<N> *r, long long *asked, L &&load) {
-  for (int i = 0; i < 6 * blocks; ++i, ++*asked, r->next()) {
+                                           uint64_t *empty, int block, int blocks, int withheld,
+                                           int m0, int n0, bool leader, volatile uint32_t *abort,
+                                           int lane, Ring<N> *r, uint64_t *asked, L &&load) {
+  for (int i = 0; i < 6 * blocks - withheld; ++i, ++*asked, r->next()) {
     bool ok = mbar_wait(empty + r->s, r->round ^ 1, abort, p.wait_ns);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
-      if (lane == 0) raise_error(p, abort);
+      if (lane == 0) raise_error<PAIR>(p, abort);
       return false;
     }
     const int tile = i % 6, k0 = (block + i / 6) * kBK;
@@ -181,7 +193,7 @@ __device__ __forceinline__ bool multiply_parts(const Params &p, const Operands &
       if (fresh) ok = ok && mbar_wait(full + stage(last_in), round(last_in), abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
-        if (lane == 0) raise_error(p, abort);
+        if (lane == 0) raise_error<PAIR>(p, abort);
         return false;
       }
       tc_fence_after();
@@ -323,7 +335,7 @@ constexpr int kTileStageBytes = 2 * kOperandBytes;
 constexpr int kSumLd = kTile + 4;  // floats of a row of sums: 16 bytes shift the banks
 constexpr size_t kTileSmem =
     kTileStages * kTileStageBytes + kTileWarps * kColumnBytes + 1024 + 256;
-static_assert(kTileSmem <= 227 * 1024 && (2 * kTileSlots + 5) * 8 + 8 <= 256, "barriers");
+static_assert(kTileSmem <= 227 * 1024 && (2 * kTileSlots + 5) * 8 + 16 <= 256, "barriers");
 static_assert(kTile * kSumLd * 4 <= kTileStages * kTileStageBytes, "sums lie over the stages");
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -355,6 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t *drain = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile uint32_t *abort = tmem_slot + 1;
+  volatile uint64_t *asked_of = reinterpret_cast<uint64_t *>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / splits, rank = blockIdx.x % splits;
   const int tiles = p.m_tiles * p.n_tiles, slice = unit / tiles, tile = unit - slice * tiles;
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kTileWarps);
+      mbar_init(acc_empty + i, kTileWarps + !!(p.inject & VAE_INJECT_WITHHOLD_ACCUMULATOR));
     }
     mbar_init(drain, 1);
     fence_mbarrier_init();
@@ -392,22 +405,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (p.wait) grid_wait();
 
   if (warp == 0) {
+    const int withheld = !!(p.inject & VAE_INJECT_WITHHOLD_COPY);
+    uint64_t asked = 0;
     if (kFloat && p.pairs > 1) {
       Ring<kTileSlots> r;
-      long long asked = 0;
-      copy_parts<false>(p, &ta, &tb, smem, full, empty, block0, blocks, m0, n0, true, abort, lane,
-                        &r, &asked,
+      copy_parts<false>(p, &ta, &tb, smem, full, empty, block0, blocks, withheld, m0, n0, true,
+                        abort, lane, &r, &asked,
                         [](uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
                            int c2) { tma_load_3d(dst, m, bar, c0, c1, c2); });
-      if (*abort && lane == 0) drain_stages(full, r, asked);
     } else {
       Ring<kTileStages> r;
       int i = 0;
-      for (; i < its; ++i, r.next()) {
+      for (; i < its - withheld; ++i, r.next()) {
         bool ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
-          if (lane == 0) raise_error(p, abort);
+          if (lane == 0) raise_error<false>(p, abort);
           break;
         }
         uint64_t *bar = full + r.s;
@@ -422,8 +435,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
       }
-      if (*abort && lane == 0) drain_stages(full, r, i);  // before the block leaves
+      asked = i;
     }
+    if (lane == 0) *asked_of = asked;
   } else if (warp == 1) {
     // The whole warp goes through the loop, so that descriptors stay in registers that
     // all lanes share, and one lane issues (the same one every time).
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = ok && mbar_wait(full + r.s, r.round, abort, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
-          if (lane == 0) raise_error(p, abort);
+          if (lane == 0) raise_error<false>(p, abort);
           break;
         }
         tc_fence_after();
@@ -484,7 +498,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = mbar_wait(acc_full + (c & 1), c >> 1 & 1, abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
-        if (lane == 0) raise_error(p, abort);
+        if (lane == 0) raise_error<false>(p, abort);
         break;
       }
       tc_fence_after();
@@ -530,7 +544,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmem);
   }
-  if (!*abort) {
+  if (*abort) {  // what was asked for lands before the block leaves
+    if (threadIdx.x == 0) {
+      if (kFloat && p.pairs > 1)
+        drain_stages<kTileSlots>(full, *asked_of);
+      else
+        drain_stages<kTileStages>(full, *asked_of);
+    }
+    __syncwarp();
+  } else {
     const int share = kTile / splits, r0 = rank * share;
     if (columns && static_cast<int>(threadIdx.x) < share) {
       const int c = r0 + threadIdx.x;
@@ -620,7 +642,7 @@ constexpr int kStaging = 2 * kChunkBytes;  // a warp's
 constexpr int kPairHead = 3 * 1024;        // rows of the bias, and barriers
 constexpr size_t kPairSmem = kPairHead + kPairStages * kPairStageBytes + kPairWarps * kStaging;
 static_assert(kPairSmem <= 227 * 1024, "shared memory of a block");
-static_assert(kPairWarps * kChunk * 4 + (2 * kPairSlots + 5 + 2 * kPairWarps) * 8 + 8 <= kPairHead,
+static_assert(kPairWarps * kChunk * 4 + (2 * kPairSlots + 5 + 2 * kPairWarps) * 8 + 24 <= kPairHead,
               "the head's parts");
 static_assert(kStaging == kColumnBytes, "columns go through a warp's staging buffer");
 
@@ -743,6 +765,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t *aux_full = drain + 1;  // two of each finishing warp's
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(aux_full + 2 * kPairWarps);
   volatile uint32_t *abort = tmem_slot + 1;
+  uint64_t *asked_of = reinterpret_cast<uint64_t *>(tmem_slot + 2);  // the leader's, of both
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int per = p.m_tiles * p.n_tiles, tiles = per * p.slices, stride = gridDim.x / 2;
@@ -755,7 +778,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 2 * kPairWarps);
+      mbar_init(acc_empty + i, 2 * kPairWarps + !!(p.inject & VAE_INJECT_WITHHOLD_ACCUMULATOR));
     }
     mbar_init(drain, 1);
     for (int i = 0; i < 2 * kPairWarps; ++i) mbar_init(aux_full + i, 1);
@@ -776,13 +799,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     Ring<kPairStages> r;
     Ring<kPairSlots> slots;
-    long long asked = 0;
+    const int withheld =
+        !!(p.inject & (rank == 0 ? VAE_INJECT_WITHHOLD_COPY : VAE_INJECT_WITHHOLD_PAIR_COPY));
+    uint64_t asked = 0;
     bool ok = true;
     if (kFloat && p.pairs > 1) {
       for (int t = blockIdx.x / 2; t < tiles && ok; t += stride) {
         const Place at = place_of(p, t % per);
         const Range its = range_of(p, t / per);
-        ok = copy_parts<true>(p, &ta, &tb, smem, full, empty, its.block0, its.blocks,
+        ok = copy_parts<true>(p, &ta, &tb, smem, full, empty, its.block0, its.blocks, withheld,
                               at.m + 128 * rank, at.n + 128 * rank, rank == 0, abort, lane, &slots,
                               &asked,
                               [](uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
@@ -795,11 +820,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const Place at = place_of(p, t % per);
         const Range its = range_of(p, t / per);
         const int m0 = at.m + 128 * rank, n0 = at.n + 128 * rank;
-        for (int it = its.block0; it < its.block0 + its.blocks; ++it, ++asked, r.next()) {
+        const int end = its.block0 + its.blocks - withheld;
+        for (int it = its.block0; it < end; ++it, ++asked, r.next()) {
           ok = mbar_wait(empty + r.s, r.round ^ 1, abort, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
-            if (lane == 0) raise_error(p, abort);
+            if (lane == 0) raise_error<true>(p, abort);
             break;
           }
           const uint32_t bar = mapa_rank(full + r.s, 0);
@@ -816,22 +842,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-    // What was asked for lands before the pair leaves: both blocks' copies count on the
-    // leader's barriers, so that the other block, whose last copies the leader may not
-    // have expected, gives them time.
-    __syncwarp();
-    if (*abort && lane == 0) {
-      if (rank == 0) {
-        if (kFloat && p.pairs > 1)
-          drain_stages(full, slots, asked);
-        else
-          drain_stages(full, r, asked);
-      } else {
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < kDrainNs / 10) {
-        }
-      }
-    }
+    if (lane == 0) st_cluster(mapa_rank(asked_of + rank, 0), asked);
   } else if (warp == 1) {
     // The whole warp goes through the loop, so that descriptors stay in registers that
     // all lanes share, and one lane issues: the tensor core takes a stage 512 clocks,
@@ -861,7 +872,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           ok = ok && mbar_wait(full + r.s, r.round, abort, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
-            if (lane == 0) raise_error(p, abort);
+            if (lane == 0) raise_error<true>(p, abort);
             break;
           }
           tc_fence_after();
@@ -887,7 +898,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto taken = [&](int b) -> bool {
       bool ok = mbar_wait(acc_full + (b & 1), b >> 1 & 1, abort, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok && lane == 0) raise_error(p, abort);
+      if (!ok && lane == 0) raise_error<true>(p, abort);
       tc_fence_after();
       return ok;
     };
@@ -989,7 +1000,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             ok = mbar_wait(aux + (g & other), (p.e.keep ? g : g >> 1) & 1, abort, p.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
-              if (lane == 0) raise_error(p, abort);
+              if (lane == 0) raise_error<true>(p, abort);
               break;
             }
           }
@@ -1018,6 +1029,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // neither block leaves while the pair's products, copies or arrivals touch it
+  if (*abort) {    // (in both, raise_error's) what either asked for lands first
+    if (rank == 0 && threadIdx.x == 0) {
+      if (kFloat && p.pairs > 1)
+        drain_pair<kPairSlots>(full, asked_of, kOperandBytes);
+      else
+        drain_pair<kPairStages>(full, asked_of, kPairStageBytes);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -1241,6 +1262,7 @@ int gemm(const GemmDesc &d, cudaStream_t s) {
   p.wait = d.wait;
   p.wait_ns = wait_limit_ns();
   p.err = device_error_word();
+  p.inject = injected_faults();
   if (!p.err) return VAE_ECUDA;
   p.e = d.epi;
   p.kind = kind_of(d.epi);

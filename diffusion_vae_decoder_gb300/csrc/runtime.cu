@@ -180,7 +180,9 @@ int vae_debug_set_wait_limit(unsigned long long ns) {
 }
 
 int vae_debug_inject(int bits) {
-  if (bits & ~VAE_INJECT_WITHHOLD_STREAMK_FLAG) return VAE_EINVAL;
+  constexpr int known = VAE_INJECT_WITHHOLD_STREAMK_FLAG | VAE_INJECT_WITHHOLD_COPY |
+                        VAE_INJECT_WITHHOLD_PAIR_COPY | VAE_INJECT_WITHHOLD_ACCUMULATOR;
+  if (bits & ~known) return VAE_EINVAL;
   vae::g_inject.store(bits);
   return VAE_OK;
 }

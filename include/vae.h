@@ -691,11 +691,20 @@ VAE_API int vae_measure_tf32_mma(int iters, double *flops, float *ms, vae_stream
  * copies and MMAs, frees its TMEM and returns.
  * vae_debug_inject: VAE_INJECT_WITHHOLD_STREAMK_FLAG makes the conv's
  * stream-K CTAs skip the flag that hands a tile's tail over to the CTA that
- * finishes it, so that CTA's bounded wait runs out (0 clears).
+ * finishes it, so that CTA's bounded wait runs out (0 clears). In the linear layers'
+ * products, VAE_INJECT_WITHHOLD_COPY leaves out the last copies of every tile's
+ * operands, VAE_INJECT_WITHHOLD_PAIR_COPY those of the second block of a pair
+ * alone (with the first bit, of both), and VAE_INJECT_WITHHOLD_ACCUMULATOR lets no
+ * accumulator be used a second time.
  * vae_debug_fail_allocation: the nth device allocation vae_chain_prepare
  * makes from now on (1 = the next) fails as if the device were out of
  * memory: prepare frees what it allocated and returns VAE_ENOMEM (0 clears). */
-typedef enum { VAE_INJECT_WITHHOLD_STREAMK_FLAG = 1 } vae_inject_bits;
+typedef enum {
+  VAE_INJECT_WITHHOLD_STREAMK_FLAG = 1,
+  VAE_INJECT_WITHHOLD_COPY = 4,
+  VAE_INJECT_WITHHOLD_PAIR_COPY = 8,
+  VAE_INJECT_WITHHOLD_ACCUMULATOR = 16
+} vae_inject_bits;
 VAE_API int vae_debug_set_wait_limit(unsigned long long ns);
 VAE_API int vae_debug_inject(int bits);
 VAE_API int vae_debug_fail_allocation(int nth);
