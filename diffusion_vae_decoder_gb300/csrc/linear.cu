@@ -14,18 +14,25 @@ namespace {
 
 // x = h + m + l exactly, each the nearest bf16 of what is left: 8 significant bits
 // and a sign, so that |m| <= 2^-8 |x| and |l| <= 2^-17 |x| (what lies below the
-// smallest bf16 is dropped). An infinite or NaN x is h; a finite one that would round
-// to infinity is cut.
+// smallest bf16 is dropped). A finite x that would round to infinity is cut, and no h
+// but zero's is zero (m takes it back). A NaN is h. An infinity is l, beside h = 1 of its
+// sign: of the products that are added up l enters the one with the other number's h
+// alone, so that each of them is infinite with the right sign, finite, or NaN where
+// infinity times x is (an infinite h would meet zeros and other signs in m and l).
 __device__ __forceinline__ uint32_t nearest_bf16(float x) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 __device__ __forceinline__ void split3(float x, uint32_t *h, uint32_t *m, uint32_t *l) {
   const uint32_t bits = __float_as_uint(x), mag = bits & 0x7fffffffu;
-  *h = mag >= 0x7f7f8000u && mag < 0x7f800000u ? bits >> 16 : nearest_bf16(x);
   if (mag >= 0x7f800000u) {
-    *m = *l = 0;
+    const bool infinite = mag == 0x7f800000u;
+    *h = infinite ? (bits >> 16 & 0x8000u) | 0x3f80u : nearest_bf16(x);
+    *m = 0;
+    *l = infinite ? bits >> 16 : 0;
     return;
   }
+  *h = mag >= 0x7f7f8000u ? bits >> 16 : nearest_bf16(x);
+  if (mag && !(*h & 0x7fffu)) *h |= 1u;
   const float r = x - __uint_as_float(*h << 16);
   *m = nearest_bf16(r);
   *l = nearest_bf16(r - __uint_as_float(*m << 16));

@@ -608,8 +608,10 @@ VAE_API int vae_dropout(const void *x, int dtype, long long count, double p,
  * vae_linear_wgrad -- dw[o][c] = sum over rows of dy[o] x[c], dbias[o] = sum of dy[o].
  *   dy [rows][n], x [rows][k], dw [n][k] float32, dbias [n] float32 or NULL.
  * 16-bit products are exact, their sums FP32. Floats enter the tensor cores as three
- * bf16 parts each (all 24 bits), of whose products those below 2^-24 are left out;
- * an infinity or a NaN among them makes the sums it enters NaN. A workspace size of
+ * bf16 parts each (all 24 bits), of whose products those below 2^-24 are left out.
+ * Infinities and NaN among the numbers make sums infinite or NaN as in FP32
+ * arithmetic, however many the rows; where finite floats' products pass float's range
+ * (or come within 1 % of its end), the sum may be infinite or NaN. A workspace size of
  * 0 for valid sizes means that ws is not used and may be NULL.
  * Limits: n % 8 == 0, k % 8 == 0, n, k <= 65536. */
 VAE_API size_t vae_linear_workspace_size(int dtype, long long rows, int n, int k);

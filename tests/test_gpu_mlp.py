@@ -468,6 +468,57 @@ def test_bad_numbers_stay_in_their_row_and_column(vae, rows, dtype):
     assert torch.equal(got, want)
 
 
+def same_bad_numbers(got, ref, want, rows=(), cols=()):
+    """Infinities and NaN are float64's; everything outside the rows and columns that they
+    reach is `want`, and so is what they leave finite in them."""
+    bad = ~torch.isfinite(ref)
+    assert torch.equal(~torch.isfinite(got), bad)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    inf = torch.isinf(ref)
+    assert torch.equal(got[inf].double(), ref[inf])
+    clean = torch.ones_like(bad)
+    clean[list(rows)] = False
+    clean[:, list(cols)] = False
+    assert not bad[clean].any() and torch.equal(got[clean], want[clean])
+
+
+def spoil(a, b):
+    """Infinities of either sign in a row of a, alone, together and on b's zero, infinity
+    and smallest numbers; infinities and a NaN in rows of b. (rows of a, of b) reached."""
+    inf = float("inf")
+    a[1, 5], a[2, 5], a[3, 7], a[3, 8] = inf, -inf, inf, inf
+    b[17, 9], b[7, 5], b[33, 11] = -inf, inf, float("nan")
+    b[20, 5], b[21, 5], b[22, 5] = 0.0, 1e-45, -1e-42
+    return (1, 2, 3), (17, 7, 33, 20, 21, 22)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n,k", [(4, 264, 136), (8, 264, 136), (9, 264, 136), (300, 264, 136),
+                                      (2500, 2048, 512)])
+def test_bad_numbers_are_those_of_float(vae, rows, n, k, dtype):
+    """The same infinities and NaN whichever kernel the number of rows takes."""
+    t = R.DTYPES[dtype]
+    x, w = rand(1, rows, k, dtype=t), rand(2, n, k, dtype=t)
+    dy, wt = rand(3, rows, k, dtype=t), rand(4, k, n, dtype=t)
+    want, back = vae.vae_linear(x, w)[0], vae.vae_linear_dgrad(dy, wt)
+    ra, rb = spoil(x, w)
+    same_bad_numbers(vae.vae_linear(x, w)[0], x.double() @ w.double().t(), want, ra, rb)
+    ra, rb = spoil(dy, wt.t())
+    same_bad_numbers(vae.vae_linear_dgrad(dy, wt), dy.double() @ wt.double(), back, ra, rb)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n,k", [(40, 64, 72), (4575, 256, 128), (8192, 2048, 512)])
+def test_bad_numbers_of_the_weights_gradient(vae, rows, n, k, dtype):
+    t = R.DTYPES[dtype]
+    dy, x = rand(1, rows, n, dtype=t), rand(2, rows, k, dtype=t)
+    want, sums = vae.vae_linear_wgrad(dy, x)
+    ra, rb = spoil(dy.t(), x.t())
+    dw, db = vae.vae_linear_wgrad(dy, x)
+    same_bad_numbers(dw, dy.double().t() @ x.double(), want, ra, rb)
+    same_bad_numbers(db.view(-1, 1), dy.double().sum(0).view(-1, 1), sums.view(-1, 1), ra)
+
+
 # ---------------------------------------------------------------- all of them
 def mlp_ref(x, gamma, beta, w1, b1, w2, b2, keep, scale):
     """float64 MLP block with autograd."""
