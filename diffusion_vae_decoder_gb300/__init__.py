@@ -660,14 +660,20 @@ def _on(stream, fn, *args):
 
 
 @functools.lru_cache(maxsize=4096)
-def _ws_bytes(name, *args):
-    return getattr(load_library(), name)(*args)
+def _ws_bytes(index, name, *args):
+    """A workspace's size on CUDA device `index` (how work is split depends on its SMs)."""
+    import torch
+    fn = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _workspace(device, name, *args):
     """(tensor, address, bytes) of an operator's workspace; Nones when it takes none."""
     import torch
-    nbytes = _ws_bytes(name, *args)
+    nbytes = _ws_bytes(device.index, name, *args)
     if not nbytes:
         return None, None, 0
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -931,7 +937,7 @@ def _launch(name, index, *args):
 def _scratch(like, name, *args):
     """(tensor, address, bytes) of an operator's workspace on `like`'s device; Nones when
     it takes none."""
-    nbytes = _ws_bytes(name, *args)
+    nbytes = _ws_bytes(like.get_device(), name, *args)
     if not nbytes:
         return None, None, 0
     import torch

@@ -612,7 +612,8 @@ VAE_API int vae_dropout(const void *x, int dtype, long long count, double p,
  * Infinities and NaN among the numbers make sums infinite or NaN as in FP32
  * arithmetic, however many the rows; where finite floats' products pass float's range
  * (or come within 1 % of its end), the sum may be infinite or NaN. A workspace size of
- * 0 for valid sizes means that ws is not used and may be NULL.
+ * 0 for valid sizes means that ws is not used and may be NULL; a size is the current
+ * device's, the one that the call is made on.
  * Limits: n % 8 == 0, k % 8 == 0, n, k <= 65536. */
 VAE_API size_t vae_linear_workspace_size(int dtype, long long rows, int n, int k);
 VAE_API int vae_linear(const void *x, int dtype, long long rows, int k, const void *w,

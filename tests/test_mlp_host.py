@@ -162,3 +162,51 @@ def test_python_checks_refuse_host_tensors(lib):
                  lambda: vae.vae_linear_wgrad(x, x)):
         with pytest.raises(TypeError):
             call()
+
+
+class _Devices:
+    """Two devices of different SM counts, and a library whose sizes depend on the current
+    one's."""
+
+    def __init__(self, monkeypatch, vae):
+        self.current, self.asked = 0, []
+        devices = self
+
+        class Guard:
+            def __init__(self, device):
+                self.index = getattr(device, "index", device)
+
+            def __enter__(self):
+                self.before, devices.current = devices.current, self.index
+
+            def __exit__(self, *_):
+                devices.current = self.before
+
+        class Lib:
+            def sizes(self, rows, n):
+                return rows * n * (devices.current + 1)
+        monkeypatch.setattr(torch.cuda, "device", Guard)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.current, raising=False)
+        monkeypatch.setattr(torch, "empty", lambda n, **kw: torch.zeros(n, dtype=torch.uint8))
+        monkeypatch.setattr(vae, "_lib", Lib())
+        vae._ws_bytes.cache_clear()
+
+
+class _On:
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+
+def test_workspaces_are_of_the_tensors_device(monkeypatch):
+    import diffusion_vae_decoder_gb300 as vae
+    devices = _Devices(monkeypatch, vae)
+    try:
+        for index in (0, 1, 0, 1):
+            assert vae._scratch(_On(index), "sizes", 3, 5)[2] == 15 * (index + 1)
+            assert vae._workspace(torch.device("cuda", index), "sizes", 7, 5)[2] == 35 * (index + 1)
+            assert devices.current == 0
+    finally:
+        vae._ws_bytes.cache_clear()
