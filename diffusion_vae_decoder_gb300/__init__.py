@@ -877,6 +877,7 @@ _DTYPES = {}  # torch dtype -> vae_dtype, once torch is loaded
 def _load_dtypes():
     import torch
     global _F32
+    load_library()  # (first: another thread takes a full table for a loaded library)
     _F32 = torch.float32
     _DTYPES.update({torch.float32: VAE_F32, torch.bfloat16: VAE_BF16, torch.float16: VAE_F16})
 
@@ -885,7 +886,6 @@ def _tokens(x, name):
     """(vae_dtype, dtype, shape, rows, c, device index) of token rows x [..., c]."""
     if not _DTYPES:
         _load_dtypes()
-        load_library()
     try:
         dtype = x.dtype
         code = _DTYPES[dtype]
@@ -1002,7 +1002,6 @@ def vae_dropout(x, p, seed=None, offset=0, state=None, residual=None, out=None, 
         return _on(stream, vae_dropout, x, p, seed, offset, state, residual, out)
     if not _DTYPES:
         _load_dtypes()
-        load_library()
     code = _DTYPES.get(getattr(x, "dtype", None))
     dev = -1 if code is None else x.get_device()
     if dev < 0 or not x.is_contiguous():

@@ -210,3 +210,22 @@ def test_workspaces_are_of_the_tensors_device(monkeypatch):
             assert devices.current == 0
     finally:
         vae._ws_bytes.cache_clear()
+
+
+@pytest.mark.parametrize("call", ["tokens", "dropout"])
+def test_the_library_is_loaded_before_a_call_goes_on(monkeypatch, call):
+    """A first call whose library does not load fails, and so does the next one; another
+    thread's call meanwhile does not take the library for loaded."""
+    import diffusion_vae_decoder_gb300 as vae
+    loads = []
+
+    def load(path=None):
+        loads.append(dict(vae._DTYPES))
+        raise RuntimeError("no library")
+    monkeypatch.setattr(vae, "_DTYPES", {})
+    monkeypatch.setattr(vae, "load_library", load)
+    x = torch.zeros(4, 8)
+    for i in range(2):
+        with pytest.raises(RuntimeError, match="no library"):
+            vae._tokens(x, "x") if call == "tokens" else vae.vae_dropout(x, 0.1, seed=1)
+    assert loads == [{}, {}]
