@@ -554,7 +554,9 @@ VAE_API int vae_block_norm_backward(const float *dy, const float *dh, const void
  * and kept activations are of one vae_dtype a call; norm weights, biases and the
  * gradients of every parameter are float32. Everything is computed in FP32 and
  * rounded once, when it is stored. Sums have a fixed order: the same inputs give
- * the same bits. Limits: rows <= 2^31 - 512. */
+ * the same bits. Where an output may be an input it is that array as a whole; tokens,
+ * weights and their gradients that are written and begin or end inside another of the
+ * call's are refused. Limits: rows <= 2^31 - 512. */
 typedef enum { VAE_F32 = 0, VAE_BF16 = 1, VAE_F16 = 2 } vae_dtype;
 /* z; z / (1 + e^-z); and z / (1 + e^-v), v = sqrt(8 / pi) (z + 0.044715 z^3), which
  * is GELU in its tanh form; at an infinite z their limits (below 1e-35 for -infinity),
@@ -604,7 +606,7 @@ VAE_API int vae_dropout(const void *x, int dtype, long long count, double p,
  * vae_linear_dgrad -- dx = (dy w) act'(z): the gradient of a layer's input x,
  * carried through the activation that made x out of z.
  *   dy [rows][n], w [n][k], dx [rows][k]; z [rows][k], NULL exactly when act is
- *   VAE_ACT_NONE (dx = dy w).
+ *   VAE_ACT_NONE (dx = dy w). dx == z is allowed.
  * vae_linear_wgrad -- dw[o][c] = sum over rows of dy[o] x[c], dbias[o] = sum of dy[o].
  *   dy [rows][n], x [rows][k], dw [n][k] float32, dbias [n] float32 or NULL.
  * 16-bit products are exact, their sums FP32. Floats enter the tensor cores as three

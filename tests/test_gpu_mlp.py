@@ -519,6 +519,37 @@ def test_bad_numbers_of_the_weights_gradient(vae, rows, n, k, dtype):
     same_bad_numbers(db.view(-1, 1), dy.double().sum(0).view(-1, 1), sums.view(-1, 1), ra)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_arrays_next_to_one_another(vae, dtype):
+    """Inputs and outputs cut from one buffer without a gap are taken; shifted ones not."""
+    t = R.DTYPES[dtype]
+    rows, c = 40, 64
+    buf = rand(1, 5 * rows, c, dtype=t)
+    x, w, r, y, more = buf.split(rows)
+    w = rand(2, c, c, dtype=t)
+    gamma = rand(3, c, std=0.2, mean=1.0)
+    want = vae.vae_linear(x.clone(), w, residual=r.clone())[0]
+    assert torch.equal(vae.vae_linear(x, w, residual=r, out=y)[0], want)
+    stats = vae.vae_layer_norm(x.clone(), gamma)[1]
+    want = vae.vae_layer_norm_backward(y.clone(), x.clone(), stats, gamma, dres=r.clone())[0]
+    assert torch.equal(vae.vae_layer_norm_backward(y, x, stats, gamma, dres=r, out=more)[0], want)
+    want = vae.vae_linear_dgrad(x.clone(), w, z=r.clone(), act=vae.VAE_ACT_SILU)
+    assert torch.equal(vae.vae_linear_dgrad(x, w, z=r, act=vae.VAE_ACT_SILU, out=y), want)
+    want = vae.vae_linear_dgrad(x, w, z=r.clone(), act=vae.VAE_ACT_SILU)
+    over = r.clone()  # the derivative's numbers, written over
+    assert torch.equal(vae.vae_linear_dgrad(x, w, z=over, act=vae.VAE_ACT_SILU, out=over), want)
+    before, shifted = buf.clone(), buf[8:8 + rows]
+    for call in (lambda: vae.vae_linear(x, w, out=shifted),
+                 lambda: vae.vae_linear(y, w, residual=x, out=shifted),
+                 lambda: vae.vae_layer_norm(x, gamma, out=shifted),
+                 lambda: vae.vae_layer_norm_backward(y, more, stats, gamma, dres=x, out=shifted),
+                 lambda: vae.vae_dropout(x, 0.1, seed=1, out=shifted),
+                 lambda: vae.vae_linear_dgrad(y, w, z=x, act=vae.VAE_ACT_SILU, out=shifted)):
+        with pytest.raises(vae.VaeError):
+            call()
+    assert torch.equal(buf, before)
+
+
 # ---------------------------------------------------------------- all of them
 def mlp_ref(x, gamma, beta, w1, b1, w2, b2, keep, scale):
     """float64 MLP block with autograd."""

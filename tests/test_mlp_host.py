@@ -229,3 +229,44 @@ def test_the_library_is_loaded_before_a_call_goes_on(monkeypatch, call):
         with pytest.raises(RuntimeError, match="no library"):
             vae._tokens(x, "x") if call == "tokens" else vae.vae_dropout(x, 0.1, seed=1)
     assert loads == [{}, {}]
+
+
+# Addresses of arrays that lie apart, and of one that begins inside another: 8 rows of 64
+# numbers of 16 bits are 1024 bytes, 64 x 64 weights 8192, a float gradient of them 16384.
+P = [ctypes.c_void_p(1 << 20 | i << 16) for i in range(1, 8)]
+APART = {
+    "vae_layer_norm": [P[0], 1, 8, 64, 1e-6, P[1], P[2], P[3], P[4], None],
+    "vae_layer_norm_backward": [P[0], P[1], 1, P[2], 8, 64, P[3], P[4], P[5], P[6], None, None, 0,
+                                None],
+    "vae_dropout": [P[0], 1, 512, 0.1, 1, 2, None, P[1], P[2], None],
+    "vae_linear": [P[0], 1, 8, 64, P[1], None, 64, 1, P[2], P[3], P[4], None, 0, None],
+    "vae_linear_dgrad": [P[0], 1, 8, 64, P[1], 64, 1, P[2], P[3], None, 0, None],
+    "vae_linear_wgrad": [P[0], P[1], 1, 8, 64, 64, P[2], P[3], P[4], 1 << 30, None],
+}
+
+
+def inside(p, offset):
+    return ctypes.c_void_p(p.value + offset)
+
+
+@pytest.mark.parametrize("fn,at,value", [
+    ("vae_layer_norm", 7, inside(P[0], 128)), ("vae_layer_norm", 7, inside(P[0], -1008)),
+    ("vae_layer_norm_backward", 8, inside(P[0], 16)), ("vae_layer_norm_backward", 8, inside(P[1], 16)),
+    ("vae_layer_norm_backward", 8, inside(P[4], -16)),
+    ("vae_dropout", 8, inside(P[0], 1008)), ("vae_dropout", 8, inside(P[1], -16)),
+    ("vae_linear", 9, inside(P[0], 128)), ("vae_linear", 9, inside(P[1], 8176)),
+    ("vae_linear", 9, inside(P[2], 128)), ("vae_linear", 10, inside(P[3], -128)),
+    ("vae_linear", 10, inside(P[2], 16)), ("vae_linear", 10, inside(P[1], 4096)),
+    ("vae_linear_dgrad", 8, inside(P[0], 1008)), ("vae_linear_dgrad", 8, inside(P[1], -1008)),
+    ("vae_linear_dgrad", 8, inside(P[2], 16)),
+    ("vae_linear_wgrad", 6, inside(P[0], 1008)), ("vae_linear_wgrad", 6, inside(P[1], -16368)),
+    ("vae_linear_wgrad", 7, inside(P[2], 16368)), ("vae_linear_wgrad", 7, inside(P[0], 16)),
+])
+def test_outputs_that_begin_inside_another_array_are_refused(lib, fn, at, value):
+    """(Before any launch. That arrays next to one another, and outputs that are an input
+    as a whole, are taken is the GPU tests' matter.)"""
+    args = list(APART[fn])
+    args[at] = value
+    before = lib.vae_kernel_launch_count()
+    assert getattr(lib, fn)(*args) == EINVAL
+    assert lib.vae_kernel_launch_count() == before
