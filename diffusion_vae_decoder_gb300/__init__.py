@@ -1040,7 +1040,8 @@ def vae_linear(x, w, bias=None, act=VAE_ACT_NONE, residual=None, keep=False, out
                stream=None):
     """(y, z) of a linear layer on token rows x [..., k] with weights w [n, k]:
     z = x w^T + bias, y = act(z) + residual. z is None with keep=False; act's
-    gradient (vae_linear_dgrad of the layer that follows) needs it."""
+    gradient (vae_linear_dgrad of the layer that follows) needs it. VAE_ACT_GELU is
+    GELU in its tanh form."""
     import torch
     if stream is not None:
         return _on(stream, vae_linear, x, w, bias, act, residual, keep, out)

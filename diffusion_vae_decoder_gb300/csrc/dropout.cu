@@ -9,7 +9,7 @@
 // expectation is x's. 16 bits and not 32: a block of ten rounds (20 wide products
 // and 20 three-input operations) is shared by eight elements instead of four, which
 // keeps the kernel below HBM's time in the 16-bit types (4 bytes an element). HBM
-// bounds it: 16384 x 2048 bf16 with a residual 30 us (6.7 TB/s), without 25 us.
+// bounds it: 16384 x 2048 bf16 with a residual 30 us (6.7 TB/s), without 26 us.
 #include "dropout.cuh"
 #include "tokens.cuh"
 

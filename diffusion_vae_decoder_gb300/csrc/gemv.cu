@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 
 int linear_few(const void *x, int dtype, int rows, int k, const void *w, int n,
                const GemmEpilogue &e, cudaStream_t s) {
-  // a warp's share of the reduction is 512 numbers at least, two loads of each row
+  // a warp's share of the reduction is 512 numbers, two loads of each row, where k has them
   const int along = k >= 2048 ? 4 : k >= 1024 ? 2 : 1;
   const unsigned grid = static_cast<unsigned>(ceil_div(n, kCols * (kWarps / along)));
   const int kind = kind_of(e);

@@ -16,7 +16,8 @@
 // column, from L2 (small_columns).
 //
 // HBM bounds both, latency and the launch small calls. Measured, forward: 65536 x 1024
-// bf16 50 us (5.3 TB/s), 16384 x 512 7.6 us (from L2), one float row of 512 2.1 us.
+// bf16 50 us (5.4 TB/s), float 81 us (6.7 TB/s), 16384 x 512 bf16 7.4 us (from L2), one
+// float row of 512 1.7 us.
 // Backward with dres: 16384 x 1024 bf16 28 us (4.7 TB/s; 33 us with one row's loads
 // under way), float 45 us (5.9 TB/s); three blocks an SM instead of two 35 and 52 us.
 #include <cmath>
@@ -29,6 +30,8 @@ namespace vae {
 
 namespace {
 
+// Blocks of the backward pass: two on each SM of a GB300, and as many elsewhere, so that
+// the size of the workspace and the order of the sums do not depend on the device.
 constexpr int kBwdBlocks = 2 * 152;
 
 // Rows whose loads are under way while one is worked on: of 16-bit numbers two, as many

@@ -609,8 +609,11 @@ VAE_API int vae_dropout(const void *x, int dtype, long long count, double p,
  *   VAE_ACT_NONE (dx = dy w). dx == z is allowed.
  * vae_linear_wgrad -- dw[o][c] = sum over rows of dy[o] x[c], dbias[o] = sum of dy[o].
  *   dy [rows][n], x [rows][k], dw [n][k] float32, dbias [n] float32 or NULL.
- * 16-bit products are exact, their sums FP32. Floats enter the tensor cores as three
- * bf16 parts each (all 24 bits), of whose products those below 2^-24 are left out.
+ * 16-bit products are exact, their sums FP32; the tensor cores' accumulator, which
+ * sums of more than 8 rows pass through, cuts where it adds (about 1e-8 of the sum for
+ * every 16 products). Floats enter the tensor cores as three bf16 parts each (24 bits
+ * of numbers above 2^-110, fewer below), of whose products those below 2^-24 are left
+ * out, and their sums move to FP32 registers every 32 steps of 16.
  * Infinities and NaN among the numbers make sums infinite or NaN as in FP32
  * arithmetic, however many the rows; where finite floats' products pass float's range
  * (or come within 1 % of its end), the sum may be infinite or NaN. A workspace size of
